@@ -22,11 +22,15 @@ STATUS_NAMES = {
     4: "NF4_ERR_WORKSPACE", 5: "NF4_ERR_CUDA", 6: "NF4_ERR_TIMEOUT", 7: "NF4_ERR_UNSUPPORTED",
     8: "NF4_ERR_BAD_OFFSETS", 9: "NF4_ERR_BOUNDS",
 }
-DTYPE_F32, DTYPE_BF16 = 0, 1
-OP_QUANTIZE, OP_LINEAR_FWD, OP_LINEAR_DGRAD, OP_GROUPED_FWD, OP_GROUPED_DGRAD, OP_GROUPED_SWIGLU_BWD = range(6)
+DTYPE_F32, DTYPE_BF16, DTYPE_F16 = 0, 1, 2
+(OP_QUANTIZE, OP_LINEAR_FWD, OP_LINEAR_DGRAD, OP_GROUPED_FWD, OP_GROUPED_DGRAD, OP_GROUPED_SWIGLU_BWD,
+ OP_NORM_RESIDUAL_BWD, OP_ATTENTION_BWD) = range(8)
+GATE_NONE, GATE_CHANNEL, GATE_TOKEN = range(3)
+ADAMW_BLOCK = 256  # NF4_ADAMW_BLOCK of include/nf4.h
 PATHS = ["linear_fwd", "linear_dgrad", "splitk_reduce", "grouped_fwd", "grouped_dgrad",
          "dequantize", "quantize", "total", "gemv_fwd", "gemv_dgrad", "skinny_fwd",
-         "skinny_dgrad", "stream_k", "cluster_split", "multi", "moe_combine"]
+         "skinny_dgrad", "stream_k", "cluster_split", "multi", "moe_combine", "attention", "attention_any",
+         "norm_residual", "adamw"]
 
 
 class NF4Error(RuntimeError):
@@ -58,6 +62,37 @@ class nf4_epilogue(ctypes.Structure):
         ("bias", ctypes.c_void_p),
         ("row_scale", ctypes.c_void_p),
         ("swiglu", ctypes.c_int32),
+    ]
+
+
+class nf4_norm_residual(ctypes.Structure):
+    _fields_ = [
+        ("y", ctypes.c_void_p), ("ld_y", ctypes.c_int64),
+        ("residual", ctypes.c_void_p), ("ld_residual", ctypes.c_int64),
+        ("gate", ctypes.c_void_p), ("ld_gate", ctypes.c_int64),
+        ("w_post", ctypes.c_void_p), ("w_pre", ctypes.c_void_p),
+        ("T", ctypes.c_int64), ("H", ctypes.c_int64),
+        ("gate_kind", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("scale", ctypes.c_float), ("eps", ctypes.c_float),
+    ]
+
+
+class nf4_attention(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("q_token", ctypes.c_int64), ("q_head", ctypes.c_int64),
+        ("k_token", ctypes.c_int64), ("k_head", ctypes.c_int64),
+        ("v_token", ctypes.c_int64), ("v_head", ctypes.c_int64),
+        ("cu_seqlens", ctypes.c_void_p), ("nseq", ctypes.c_int64), ("T", ctypes.c_int64),
+        ("Hq", ctypes.c_int32), ("Hk", ctypes.c_int32), ("D", ctypes.c_int32),
+        ("dtype", ctypes.c_int32), ("scale", ctypes.c_float),
+    ]
+
+
+class nf4_adamw_tensor(ctypes.Structure):
+    _fields_ = [
+        ("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("m_absmax", ctypes.c_void_p), ("v_absmax", ctypes.c_void_p), ("n", ctypes.c_int64),
     ]
 
 
@@ -102,6 +137,7 @@ def lib() -> ctypes.CDLL:
         L = ctypes.CDLL(LIB_PATH)
         P, I64, I32, SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
         W = ctypes.POINTER(nf4_weight)
+        NR, AT, F64 = ctypes.POINTER(nf4_norm_residual), ctypes.POINTER(nf4_attention), ctypes.c_double
         sig = {
             "nf4_quantize": [P, I32, I64, I64, I32, I32, I32, P, P, P, P, P, P, P, P, SZ, P],
             "nf4_quantize_8bit": [P, I32, I64, I64, I32, I32, I32, P, P, P, P, P, P, P, P, SZ, P],
@@ -119,6 +155,12 @@ def lib() -> ctypes.CDLL:
             "nf4_grouped_fwd_ep": [P, P, I32, I64, I64, W, I64, ctypes.POINTER(nf4_epilogue), P, I64, P],
             "nf4_grouped_swiglu_bwd": [P, P, I32, I64, I64, W, I64, ctypes.POINTER(nf4_epilogue), P, I64,
                                        P, I64, P, P, SZ, P],
+            "nf4_norm_residual_fwd": [NR, P, I64, P, I64, P, P],
+            "nf4_norm_residual_bwd": [NR, P, P, I64, P, I64, P, I64, P, I64, P, P, I64, P, P, SZ, P],
+            "nf4_attention_fwd": [AT, P, I64, I64, P, P],
+            "nf4_attention_bwd": [AT, P, I64, I64, P, P, I64, I64, P, I64, I64, P, I64, I64, P, I64, I64, P, SZ, P],
+            "nf4_adamw_step": [P, I32, I32, I32, P, P, F64, F64, F64, F64, F64, I64, P, P],
+            "nf4_adamw_state_values": [P, P, P, P, P, P, I64, P, P, P],
             "nf4_workspace_size": [I32, I64, I64, I64, I32],
             "nf4_status_string": [I32],
             "nf4_checked_build": [],

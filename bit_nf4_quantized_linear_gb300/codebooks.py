@@ -104,3 +104,14 @@ def dynamic_code8() -> torch.Tensor:
     levels = torch.cat([mags, -mags, torch.tensor([0.0, 1.0], dtype=torch.float64)])
     levels, _ = torch.sort(levels)
     return levels.to(torch.float32)
+
+
+def dynamic_code8_unsigned() -> torch.Tensor:
+    """The unsigned 8-bit dynamic map (second moments of the optimiser, which have no
+    sign): 2**(e+1) fractions in decade e instead of 2**e of either sign, plus 0 and 1."""
+    parts = []
+    for e in range(7):
+        edges = torch.linspace(0.1, 1.0, 2 ** (e + 1) + 1, dtype=torch.float64)
+        parts.append((edges[:-1] + edges[1:]) / 2.0 * (10.0 ** (e - 6)))
+    levels, _ = torch.sort(torch.cat([*parts, torch.tensor([0.0, 1.0], dtype=torch.float64)]))
+    return levels.to(torch.float32)

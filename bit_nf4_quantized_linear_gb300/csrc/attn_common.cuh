@@ -1,0 +1,88 @@
+// attn_common.cuh -- what the attention kernels share: which sequence and tile a CTA
+// works on, and the rows that belong to no sequence.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "internal.h"
+
+namespace nf4 {
+
+struct AttnTile {
+  int64_t row0;  // first row of the sequence in the packed tensors
+  int len;       // rows of the sequence
+  int tile;      // tile within the sequence; -1: the id is past the last tile
+};
+
+// Bounds of sequence b, forced into 0 <= start <= end <= T: bad offsets cannot lead
+// outside the tensors, and are recorded.
+__device__ __forceinline__ void seq_bounds(const AttnArgs& a, int64_t b, int64_t* start, int64_t* end) {
+  if (!a.cu_seqlens) {
+    *start = 0;
+    *end = a.T;
+    return;
+  }
+  const int64_t s = a.cu_seqlens[b], e = a.cu_seqlens[b + 1];
+  if ((s < 0 || e < s || e > a.T) && a.status) atomicCAS(a.status, 0, kStatusBadOffsets);
+  *start = s < 0 ? 0 : (s > a.T ? a.T : s);
+  *end = e < *start ? *start : (e > a.T ? a.T : e);
+}
+
+// The sequence and tile of tile number `id`, counting ceil(len / rows) tiles for
+// each sequence in turn, the last tile of a sequence first: under the causal mask it
+// is the longest, and a grid deals its CTAs in order.  Called by one full warp; all
+// lanes get the answer.
+__device__ __forceinline__ AttnTile find_tile(const AttnArgs& a, int64_t id, int rows) {
+  const int lane = threadIdx.x & 31;
+  AttnTile r{0, 0, -1};
+  int64_t base = 0;
+  for (int64_t b0 = 0; b0 < a.nseq; b0 += 32) {
+    int64_t s = 0, e = 0;
+    if (b0 + lane < a.nseq) seq_bounds(a, b0 + lane, &s, &e);
+    const int64_t tiles = (e - s + rows - 1) / rows;
+    int64_t incl = tiles;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += up;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, base + incl > id);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      const int64_t before = base + incl - tiles;
+      r.row0 = __shfl_sync(0xffffffffu, s, src);
+      r.len = static_cast<int>(__shfl_sync(0xffffffffu, e - s, src));
+      r.tile = static_cast<int>(__shfl_sync(0xffffffffu, tiles - 1 - (id - before), src));
+      return r;
+    }
+    base += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return r;
+}
+
+// Rows before the first sequence and after the last.
+__device__ __forceinline__ void gap_rows(const AttnArgs& a, int64_t* head_end, int64_t* tail_start) {
+  *head_end = 0;
+  *tail_start = a.T;
+  if (a.cu_seqlens) {
+    const int64_t h = a.cu_seqlens[0], t = a.cu_seqlens[a.nseq];
+    *head_end = h < 0 ? 0 : (h > a.T ? a.T : h);
+    *tail_start = t < *head_end ? *head_end : (t > a.T ? a.T : t);
+  }
+}
+
+// Zeros in rows [lo, hi) of every head of `p`, spread over the whole grid.
+template <typename T>
+__device__ __forceinline__ void zero_rows(T* p, int64_t ld_t, int64_t ld_h, int heads, int D, int64_t lo, int64_t hi) {
+  const int64_t n = (hi - lo) * heads * D;
+  const int64_t cta = blockIdx.x + static_cast<int64_t>(gridDim.x) * blockIdx.y;
+  const int64_t nthr = static_cast<int64_t>(gridDim.x) * gridDim.y * blockDim.x;
+  for (int64_t i = cta * blockDim.x + threadIdx.x; i < n; i += nthr) {
+    const int64_t d = i % D, h = (i / D) % heads, t = lo + i / (static_cast<int64_t>(D) * heads);
+    p[t * ld_t + h * ld_h + d] = T(0.0f);
+  }
+}
+
+}  // namespace nf4

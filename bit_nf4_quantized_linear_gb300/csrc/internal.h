@@ -61,6 +61,78 @@ struct MoeArgs {
 };
 cudaError_t launch_moe(bool backward, const MoeArgs& a, cudaStream_t s);
 
+// The gated residual norm and its backward (nf4_norm_residual_fwd / _bwd).  Rows of
+// width H with their own pitches in elements; a null pointer leaves that input or
+// output out.
+struct NormArgs {
+  const void *y, *residual, *gate, *gz, *gh;
+  void *z, *h, *gy, *gr, *ggate;
+  int64_t ld_y, ld_r, ld_gate, ld_gz, ld_gh, ld_z, ld_h, ld_gy, ld_gr, ld_ggate;
+  const float *w_post, *w_pre;
+  float *gw_post, *gw_pre;
+  float* stats;  // [2][T]: rstd of y, rstd of z
+  float* part;   // backward: partial sums over tokens [CTAs][3][H] (gw_pre, gw_post, ggate)
+  int64_t T, H;
+  int gate_kind;
+  float scale, eps;
+};
+// CTAs of the backward, each with its own partial sums.
+int norm_bwd_ctas(int64_t T, int sms);
+cudaError_t launch_norm(bool backward, int dtype, const NormArgs& a, int sms, cudaStream_t s);
+
+// AdamW over many tensors.  The table travels in the kernel's parameters (no copy to
+// the device): tensor i holds blocks blk0[i] .. blk0[i + 1] - 1 of kAdamBlock values.
+constexpr int kAdamBlock = NF4_ADAMW_BLOCK;
+constexpr int kAdamMaxTensors = 400;  // of one launch
+struct AdamTensor {
+  void* param;
+  const void* grad;
+  void *m, *v;
+  float *m_absmax, *v_absmax;
+  int64_t n;
+};
+struct AdamTable {
+  AdamTensor t[kAdamMaxTensors];
+  int64_t blk0[kAdamMaxTensors + 1];
+  int count;
+};
+static_assert(sizeof(AdamTable) < 30000, "kernel parameters hold 32764 bytes");
+struct AdamArgs {
+  float beta1, one_minus_beta1, beta2, one_minus_beta2, eps, decay, step_size, inv_sqrt_c2;
+  const float* grad_scale;
+  const float *levels_m, *levels_v;
+};
+cudaError_t launch_adamw(int dtype, int bits, const AdamTable& tab, const AdamArgs& a, int sms, cudaStream_t s);
+struct AdamValuesArgs {
+  const uint8_t *m, *v;
+  const float *m_absmax, *v_absmax, *levels_m, *levels_v;
+  float *out_m, *out_v;
+  int64_t n;
+};
+cudaError_t launch_adamw_values(const AdamValuesArgs& a, int sms, cudaStream_t s);
+
+// Causal attention over packed sequences and its backward (nf4_attention_fwd / _bwd):
+// tensors [T, heads, D] with token and head strides in elements, unit stride within
+// a head.
+struct AttnArgs {
+  const void *q, *k, *v, *go;
+  void *o, *gq, *gk, *gv;
+  int64_t q_t, q_h, k_t, k_h, v_t, v_h, o_t, o_h, go_t, go_h, gq_t, gq_h, gk_t, gk_h, gv_t, gv_h;
+  float* lse;    // [Hq][T]
+  float* delta;  // [Hq][T], backward
+  const int32_t* cu_seqlens;  // [nseq + 1], or null: one sequence of T rows
+  int64_t T, nseq;
+  int Hq, Hk, D;
+  float scale;
+  int* status;
+};
+// Most tiles of `rows` rows that any offsets within [0, T] give.
+inline int64_t attn_tiles(const AttnArgs& a, int rows) {
+  const int64_t most = a.nseq < a.T ? a.nseq : a.T;  // sequences that can hold a row
+  return a.T / rows + most;
+}
+cudaError_t launch_attn_any(bool backward, int dtype, const AttnArgs& a, int sms, cudaStream_t s);
+
 // Multi-product launches (nf4_linear_fwd_multi / nf4_linear_dgrad_multi): up to
 // kMaxProds independent products with the same M and in-features K, each with its
 // own weight, activation and output, whose work items share one grid.

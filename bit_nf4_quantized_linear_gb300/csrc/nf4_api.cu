@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <cstdio>
 #include <cstring>
@@ -897,9 +898,283 @@ nf4_status run_moe(bool backward, const void* src, int64_t src_rows, int64_t ld_
   return NF4_OK;
 }
 
+bool known_dtype(int32_t dt) { return dt == NF4_DTYPE_F32 || dt == NF4_DTYPE_BF16 || dt == NF4_DTYPE_F16; }
+
+size_t dtype_bytes(int32_t dt) { return dt == NF4_DTYPE_F32 ? 4 : 2; }
+
+bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// Checks and arguments common to the norm's two directions.
+nf4_status norm_args(const nf4_norm_residual* d, nf4::NormArgs* a) {
+  if (!d || !known_dtype(d->dtype)) return NF4_ERR_INVALID_ARG;
+  if (d->T < 0 || d->H < 1 || d->gate_kind < NF4_GATE_NONE || d->gate_kind > NF4_GATE_TOKEN) return NF4_ERR_INVALID_ARG;
+  if (d->T > INT32_MAX || d->H > INT32_MAX) return NF4_ERR_UNSUPPORTED_SHAPE;
+  if (!(d->eps >= 0.0f)) return NF4_ERR_INVALID_ARG;
+  if (d->T > 0) {
+    if (!d->y || d->ld_y < d->H || (d->residual && d->ld_residual < d->H)) return NF4_ERR_INVALID_ARG;
+    if (d->gate_kind != NF4_GATE_NONE && !d->gate) return NF4_ERR_INVALID_ARG;
+    if (d->gate_kind == NF4_GATE_TOKEN && d->ld_gate < d->H) return NF4_ERR_INVALID_ARG;
+    const size_t e = dtype_bytes(d->dtype);
+    if (!aligned_to(d->y, e) || !aligned_to(d->residual, e) || !aligned_to(d->w_post, 4) || !aligned_to(d->w_pre, 4) ||
+        !aligned_to(d->gate, d->gate_kind == NF4_GATE_CHANNEL ? 4 : e))
+      return NF4_ERR_ALIGNMENT;
+  }
+  *a = {};
+  a->y = d->y;
+  a->ld_y = d->ld_y;
+  a->residual = d->residual;
+  a->ld_r = d->ld_residual;
+  a->gate = d->gate;
+  a->ld_gate = d->ld_gate;
+  a->w_post = d->w_post;
+  a->w_pre = d->w_pre;
+  a->T = d->T;
+  a->H = d->H;
+  a->gate_kind = d->gate_kind;
+  a->scale = d->scale;
+  a->eps = d->eps;
+  return NF4_OK;
+}
+
+// Checks and arguments common to the attention's two directions.
+nf4_status attn_args(const nf4_attention* d, nf4::AttnArgs* a) {
+  if (!d || !known_dtype(d->dtype)) return NF4_ERR_INVALID_ARG;
+  if (d->T < 0 || d->Hk < 1 || d->Hq < 1 || d->Hq % d->Hk != 0 || d->D < 1) return NF4_ERR_INVALID_ARG;
+  if (d->cu_seqlens && d->nseq < 1) return NF4_ERR_INVALID_ARG;
+  if (d->D > 256 || d->T > INT32_MAX || d->nseq > INT32_MAX || d->Hq > 65535) return NF4_ERR_UNSUPPORTED_SHAPE;
+  if (d->T > 0) {
+    const size_t e = dtype_bytes(d->dtype);
+    if (!d->q || !d->k || !d->v) return NF4_ERR_INVALID_ARG;
+    if (!aligned_to(d->q, e) || !aligned_to(d->k, e) || !aligned_to(d->v, e) || !aligned_to(d->cu_seqlens, 4))
+      return NF4_ERR_ALIGNMENT;
+  }
+  *a = {};
+  a->q = d->q;
+  a->k = d->k;
+  a->v = d->v;
+  a->q_t = d->q_token;
+  a->q_h = d->q_head;
+  a->k_t = d->k_token;
+  a->k_h = d->k_head;
+  a->v_t = d->v_token;
+  a->v_h = d->v_head;
+  a->cu_seqlens = d->cu_seqlens;
+  a->nseq = d->cu_seqlens ? d->nseq : 1;
+  a->T = d->T;
+  a->Hq = d->Hq;
+  a->Hk = d->Hk;
+  a->D = d->D;
+  a->scale = d->scale;
+  return NF4_OK;
+}
+
 }  // namespace
 
 extern "C" {
+
+nf4_status nf4_norm_residual_fwd(const nf4_norm_residual* d, void* z, int64_t ld_z, void* h, int64_t ld_h,
+                                 float* stats, void* stream) {
+  nf4::NormArgs a;
+  if (nf4_status s = norm_args(d, &a)) return s;
+  if ((z && ld_z < a.H) || (h && ld_h < a.H) || (h && !a.w_pre)) return NF4_ERR_INVALID_ARG;
+  if (a.T == 0) return NF4_OK;
+  const size_t e = dtype_bytes(d->dtype);
+  if (!aligned_to(z, e) || !aligned_to(h, e) || !aligned_to(stats, 4)) return NF4_ERR_ALIGNMENT;
+  a.z = z;
+  a.ld_z = ld_z;
+  a.h = h;
+  a.ld_h = ld_h;
+  a.stats = stats;
+  DevInfo dev;
+  if (!current_device(&dev)) return cuda_fail(cudaGetLastError(), "device query");
+  cudaError_t le = nf4::launch_norm(false, d->dtype, a, dev.sms, static_cast<cudaStream_t>(stream));
+  if (le != cudaSuccess) return cuda_fail(le, "kernel launch");
+  count(NF4_PATH_NORM_RESIDUAL);
+  return NF4_OK;
+}
+
+nf4_status nf4_norm_residual_bwd(const nf4_norm_residual* d, const float* stats, const void* gz, int64_t ld_gz,
+                                 const void* gh, int64_t ld_gh, void* gy, int64_t ld_gy, void* gr, int64_t ld_gr,
+                                 float* gw_post, void* ggate, int64_t ld_ggate, float* gw_pre, void* ws,
+                                 size_t ws_bytes, void* stream) {
+  nf4::NormArgs a;
+  if (nf4_status s = norm_args(d, &a)) return s;
+  const bool token = a.gate_kind == NF4_GATE_TOKEN;
+  if ((gz && ld_gz < a.H) || (gh && ld_gh < a.H) || (gy && ld_gy < a.H) || (gr && ld_gr < a.H) ||
+      (token && ggate && ld_ggate < a.H))
+    return NF4_ERR_INVALID_ARG;
+  if ((gh && !a.w_pre) || (gw_pre && !a.w_pre) || (gw_post && !a.w_post) || (ggate && a.gate_kind == NF4_GATE_NONE) ||
+      (gr && !a.residual && a.T > 0))
+    return NF4_ERR_INVALID_ARG;
+  const size_t e = dtype_bytes(d->dtype);
+  if (!aligned_to(gz, e) || !aligned_to(gh, e) || !aligned_to(gy, e) || !aligned_to(gr, e) || !aligned_to(gw_post, 4) ||
+      !aligned_to(gw_pre, 4) || !aligned_to(ggate, token ? e : 4) || !aligned_to(stats, 4))
+    return NF4_ERR_ALIGNMENT;
+  DevInfo dev;
+  if (!current_device(&dev)) return cuda_fail(cudaGetLastError(), "device query");
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  float* vecs[3] = {gw_post, gw_pre, token ? nullptr : static_cast<float*>(ggate)};
+  if (a.T == 0) {
+    for (float* v : vecs)
+      if (v)
+        if (cudaError_t ce = cudaMemsetAsync(v, 0, static_cast<size_t>(a.H) * 4, st)) return cuda_fail(ce, "memset");
+    return NF4_OK;
+  }
+  if (!stats) return NF4_ERR_INVALID_ARG;
+  if (vecs[0] || vecs[1] || vecs[2]) {
+    const size_t need = nf4_workspace_size(NF4_OP_NORM_RESIDUAL_BWD, a.T, a.H, 0, 0);
+    if (!ws || ws_bytes < need) return NF4_ERR_WORKSPACE;
+    if (!aligned_to(ws, 16)) return NF4_ERR_ALIGNMENT;
+    a.part = static_cast<float*>(ws);
+  }
+  a.stats = const_cast<float*>(stats);
+  a.gz = gz;
+  a.ld_gz = ld_gz;
+  a.gh = gh;
+  a.ld_gh = ld_gh;
+  a.gy = gy;
+  a.ld_gy = ld_gy;
+  a.gr = gr;
+  a.ld_gr = ld_gr;
+  a.ggate = ggate;
+  a.ld_ggate = ld_ggate;
+  a.gw_post = gw_post;
+  a.gw_pre = gw_pre;
+  cudaError_t le = nf4::launch_norm(true, d->dtype, a, dev.sms, st);
+  if (le != cudaSuccess) return cuda_fail(le, "kernel launch");
+  count(NF4_PATH_NORM_RESIDUAL);
+  return NF4_OK;
+}
+
+nf4_status nf4_attention_fwd(const nf4_attention* d, void* o, int64_t o_token, int64_t o_head, float* lse,
+                             void* stream) {
+  nf4::AttnArgs a;
+  if (nf4_status s = attn_args(d, &a)) return s;
+  if (a.T == 0) return NF4_OK;
+  if (!o || !lse) return NF4_ERR_INVALID_ARG;
+  if (!aligned_to(o, dtype_bytes(d->dtype)) || !aligned_to(lse, 4)) return NF4_ERR_ALIGNMENT;
+  a.o = o;
+  a.o_t = o_token;
+  a.o_h = o_head;
+  a.lse = lse;
+  DevInfo dev;
+  if (!current_device(&dev)) return cuda_fail(cudaGetLastError(), "device query");
+  a.status = dev.status;
+  cudaError_t le = nf4::launch_attn_any(false, d->dtype, a, dev.sms, static_cast<cudaStream_t>(stream));
+  if (le != cudaSuccess) return cuda_fail(le, "kernel launch");
+  count(NF4_PATH_ATTENTION_ANY);
+  return NF4_OK;
+}
+
+nf4_status nf4_attention_bwd(const nf4_attention* d, const void* o, int64_t o_token, int64_t o_head, const float* lse,
+                             const void* go, int64_t go_token, int64_t go_head, void* gq, int64_t gq_token,
+                             int64_t gq_head, void* gk, int64_t gk_token, int64_t gk_head, void* gv, int64_t gv_token,
+                             int64_t gv_head, void* ws, size_t ws_bytes, void* stream) {
+  nf4::AttnArgs a;
+  if (nf4_status s = attn_args(d, &a)) return s;
+  if (a.T == 0) return NF4_OK;
+  if (!o || !lse || !go || !gq || !gk || !gv) return NF4_ERR_INVALID_ARG;
+  const size_t e = dtype_bytes(d->dtype);
+  if (!aligned_to(o, e) || !aligned_to(go, e) || !aligned_to(gq, e) || !aligned_to(gk, e) || !aligned_to(gv, e) ||
+      !aligned_to(lse, 4))
+    return NF4_ERR_ALIGNMENT;
+  if (!ws || ws_bytes < nf4_workspace_size(NF4_OP_ATTENTION_BWD, a.T, a.Hq, 0, 0)) return NF4_ERR_WORKSPACE;
+  if (!aligned_to(ws, 16)) return NF4_ERR_ALIGNMENT;
+  a.o = const_cast<void*>(o);
+  a.o_t = o_token;
+  a.o_h = o_head;
+  a.lse = const_cast<float*>(lse);
+  a.delta = static_cast<float*>(ws);
+  a.go = go;
+  a.go_t = go_token;
+  a.go_h = go_head;
+  a.gq = gq;
+  a.gq_t = gq_token;
+  a.gq_h = gq_head;
+  a.gk = gk;
+  a.gk_t = gk_token;
+  a.gk_h = gk_head;
+  a.gv = gv;
+  a.gv_t = gv_token;
+  a.gv_h = gv_head;
+  DevInfo dev;
+  if (!current_device(&dev)) return cuda_fail(cudaGetLastError(), "device query");
+  a.status = dev.status;
+  cudaError_t le = nf4::launch_attn_any(true, d->dtype, a, dev.sms, static_cast<cudaStream_t>(stream));
+  if (le != cudaSuccess) return cuda_fail(le, "kernel launch");
+  count(NF4_PATH_ATTENTION_ANY);
+  return NF4_OK;
+}
+
+nf4_status nf4_adamw_step(const nf4_adamw_tensor* tensors, int32_t count_, int32_t dtype, int32_t bits,
+                          const float* levels_m, const float* levels_v, double lr, double beta1, double beta2,
+                          double eps, double weight_decay, int64_t step, const float* grad_scale, void* stream) {
+  if (count_ < 0 || (count_ > 0 && !tensors) || !known_dtype(dtype) || (bits != 8 && bits != 32) || step < 1)
+    return NF4_ERR_INVALID_ARG;
+  if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || !(eps >= 0.0) || !(lr >= 0.0) ||
+      !(weight_decay >= 0.0))
+    return NF4_ERR_INVALID_ARG;
+  if (bits == 8 && (!levels_m || !levels_v)) return NF4_ERR_INVALID_ARG;
+  const size_t e = dtype_bytes(dtype), se = bits == 8 ? 1 : 4;
+  for (int32_t i = 0; i < count_; ++i) {
+    const nf4_adamw_tensor& t = tensors[i];
+    if (t.n < 0) return NF4_ERR_INVALID_ARG;
+    if (t.n == 0) continue;
+    if (!t.param || !t.grad || !t.m || !t.v) return NF4_ERR_INVALID_ARG;
+    if (bits == 8 && (!t.m_absmax || !t.v_absmax)) return NF4_ERR_INVALID_ARG;
+    if (!aligned_to(t.param, e) || !aligned_to(t.grad, e) || !aligned_to(t.m, se) || !aligned_to(t.v, se) ||
+        !aligned_to(t.m_absmax, 4) || !aligned_to(t.v_absmax, 4))
+      return NF4_ERR_ALIGNMENT;
+  }
+  DevInfo dev;
+  if (!current_device(&dev)) return cuda_fail(cudaGetLastError(), "device query");
+  const double c1 = 1.0 - std::pow(beta1, static_cast<double>(step)), c2 = 1.0 - std::pow(beta2, static_cast<double>(step));
+  nf4::AdamArgs a{};
+  a.beta1 = static_cast<float>(beta1);
+  a.one_minus_beta1 = static_cast<float>(1.0 - beta1);
+  a.beta2 = static_cast<float>(beta2);
+  a.one_minus_beta2 = static_cast<float>(1.0 - beta2);
+  a.eps = static_cast<float>(eps);
+  a.decay = static_cast<float>(lr * weight_decay);
+  a.step_size = static_cast<float>(lr / c1);
+  a.inv_sqrt_c2 = static_cast<float>(1.0 / std::sqrt(c2));
+  a.grad_scale = grad_scale;
+  a.levels_m = levels_m;
+  a.levels_v = levels_v;
+  static thread_local nf4::AdamTable tab;  // 25 KB: not on the caller's stack
+  for (int32_t i0 = 0; i0 < count_;) {
+    tab.count = 0;
+    tab.blk0[0] = 0;
+    for (; i0 < count_ && tab.count < nf4::kAdamMaxTensors; ++i0) {
+      const nf4_adamw_tensor& t = tensors[i0];
+      if (t.n == 0) continue;
+      tab.t[tab.count] = {t.param, t.grad, t.m, t.v, t.m_absmax, t.v_absmax, t.n};
+      tab.blk0[tab.count + 1] = tab.blk0[tab.count] + (t.n + NF4_ADAMW_BLOCK - 1) / NF4_ADAMW_BLOCK;
+      ++tab.count;
+    }
+    if (tab.count == 0) break;
+    cudaError_t le = nf4::launch_adamw(dtype, bits, tab, a, dev.sms, static_cast<cudaStream_t>(stream));
+    if (le != cudaSuccess) return cuda_fail(le, "kernel launch");
+    count(NF4_PATH_ADAMW);
+  }
+  return NF4_OK;
+}
+
+nf4_status nf4_adamw_state_values(const uint8_t* m, const uint8_t* v, const float* m_absmax, const float* v_absmax,
+                                  const float* levels_m, const float* levels_v, int64_t n, float* out_m, float* out_v,
+                                  void* stream) {
+  if (n < 0) return NF4_ERR_INVALID_ARG;
+  if (n == 0) return NF4_OK;
+  if (!m || !v || !m_absmax || !v_absmax || !levels_m || !levels_v || !out_m || !out_v) return NF4_ERR_INVALID_ARG;
+  if (!aligned_to(out_m, 4) || !aligned_to(out_v, 4)) return NF4_ERR_ALIGNMENT;
+  DevInfo dev;
+  if (!current_device(&dev)) return cuda_fail(cudaGetLastError(), "device query");
+  const nf4::AdamValuesArgs a{m, v, m_absmax, v_absmax, levels_m, levels_v, out_m, out_v, n};
+  cudaError_t le = nf4::launch_adamw_values(a, dev.sms, static_cast<cudaStream_t>(stream));
+  if (le != cudaSuccess) return cuda_fail(le, "kernel launch");
+  count(NF4_PATH_ADAMW);
+  return NF4_OK;
+}
 
 nf4_status nf4_quantize(const void* W, int32_t w_dtype, int64_t N, int64_t K, int32_t blocksize,
                         int32_t double_quant, int32_t nested_blocksize, const float* code4,
@@ -1053,6 +1328,15 @@ size_t nf4_workspace_size(int32_t op, int64_t M, int64_t N, int64_t K, int32_t E
     if (M <= 0 || N <= 0) return 0;
     return swiglu_bwd_dgu_bytes(M, N) + static_cast<size_t>(N / 64) * M * sizeof(float);
   }
+  if (op == NF4_OP_NORM_RESIDUAL_BWD) {
+    DevInfo dev;
+    if (M <= 0 || N <= 0 || !current_device(&dev)) return 0;
+    return static_cast<size_t>(nf4::norm_bwd_ctas(M, dev.sms)) * 3 * N * sizeof(float);
+  }
+  if (op == NF4_OP_ATTENTION_BWD) {
+    if (M <= 0 || N <= 0) return 0;
+    return static_cast<size_t>(M) * N * sizeof(float);  // delta [Hq][T]
+  }
   if (op == NF4_OP_QUANTIZE) {
     const int64_t nblocks = (N * K + 63) / 64;
     return static_cast<size_t>((nblocks + nf4::kMeanChunk - 1) / nf4::kMeanChunk) * 8;
@@ -1084,7 +1368,7 @@ const char* nf4_status_string(nf4_status s) {
     case NF4_ERR_CUDA: return "CUDA error";
     case NF4_ERR_TIMEOUT: return "device wait timed out";
     case NF4_ERR_UNSUPPORTED: return "unsupported device or parameter";
-    case NF4_ERR_BAD_OFFSETS: return "expert offsets out of contract";
+    case NF4_ERR_BAD_OFFSETS: return "expert or sequence offsets out of contract";
     case NF4_ERR_BOUNDS: return "an in-kernel index check failed (checked build)";
   }
   return "unknown status";

@@ -61,7 +61,7 @@ typedef enum {
   NF4_ERR_BOUNDS = 9             /* checked build: an in-kernel index check failed   */
 } nf4_status;
 
-enum { NF4_DTYPE_F32 = 0, NF4_DTYPE_BF16 = 1 };
+enum { NF4_DTYPE_F32 = 0, NF4_DTYPE_BF16 = 1, NF4_DTYPE_F16 = 2 /* attention, norms, optimiser */ };
 
 enum {
   NF4_OP_QUANTIZE = 0,
@@ -69,7 +69,9 @@ enum {
   NF4_OP_LINEAR_DGRAD = 2,
   NF4_OP_GROUPED_FWD = 3,
   NF4_OP_GROUPED_DGRAD = 4,
-  NF4_OP_GROUPED_SWIGLU_BWD = 5  /* M = T rows, N = N_e, K; E experts */
+  NF4_OP_GROUPED_SWIGLU_BWD = 5, /* M = T rows, N = N_e, K; E experts */
+  NF4_OP_NORM_RESIDUAL_BWD = 6,  /* M = T rows, N = H; K and E unused */
+  NF4_OP_ATTENTION_BWD = 7       /* M = T rows, N = Hq query heads; K and E unused */
 };
 
 /* Path counters (nf4_get_path_counters): how many launches each kernel got.
@@ -92,7 +94,11 @@ enum {
   NF4_PATH_CLUSTER_SPLIT = 13,/* fused launch with the cluster split         */
   NF4_PATH_MULTI = 14,       /* multi-product fused launch                  */
   NF4_PATH_MOE_COMBINE = 15, /* top-k combine of the experts, or its backward */
-  NF4_NUM_PATHS = 16
+  NF4_PATH_ATTENTION = 16,   /* attention forward or backward, tensor-core kernels */
+  NF4_PATH_ATTENTION_ANY = 17,/* the same for layouts the tensor-core kernels do not take */
+  NF4_PATH_NORM_RESIDUAL = 18,/* gated residual norm, or its backward       */
+  NF4_PATH_ADAMW = 19,       /* AdamW step, or the read-out of 8-bit states */
+  NF4_NUM_PATHS = 20
 };
 
 /* A quantised weight: the tensors of the pages' QuantState as plain device
@@ -331,6 +337,132 @@ nf4_status nf4_grouped_swiglu_bwd(const void* x, const int32_t* offsets, int32_t
                                   int64_t ldx, const nf4_weight* w, int64_t N_e,
                                   const nf4_epilogue* ep, const void* gh, int64_t ldgh, void* gx,
                                   int64_t ldgx, float* grad_row_scale, void* ws, size_t ws_bytes,
+                                  void* stream);
+
+/* nf4_norm_residual_fwd / nf4_norm_residual_bwd -- the norms before and after a
+ * block of a transformer, fused with the block's gate, the residual scale and the
+ * residual sum (the parts of a training step over frozen projections that the pages
+ * leave in native ops).  Per row of width H, in fp32, each output rounded once:
+ *   n = y rstd(y) w_post         (w_post NULL: n = y)
+ *   z = residual + scale g n     (residual NULL: no sum)
+ *   h = z rstd(z) w_pre          (from the unrounded z)
+ * with rstd(x) = 1 / sqrt(mean(x^2) + eps).  A plain norm before the first block is
+ * y with w_pre alone.
+ *   y, residual, z, h   [T, H] of `dtype` (NF4_DTYPE_*), row pitches in elements;
+ *                       residual may be NULL; z and h may each be NULL (not wanted).
+ *   w_post, w_pre       fp32 [H]; w_post may be NULL, w_pre NULL means no h.
+ *   gate                by gate_kind: NF4_GATE_NONE (g = 1, gate NULL),
+ *                       NF4_GATE_CHANNEL (fp32 [H]), NF4_GATE_TOKEN ([T, H] of
+ *                       `dtype`, pitch ld_gate).
+ *   stats               fp32 [2][T]: rstd(y) (1 without w_post), then rstd(z); NULL
+ *                       in the forward when no backward follows.
+ * Backward, from gz = dL/dz (NULL: zero) and gh = dL/dh (NULL: zero):
+ *   gy, gr [T, H]       gradients of y and residual;
+ *   gw_post, gw_pre     fp32 [H], sums over the tokens;
+ *   ggate               of the gate's own shape and type (channel: fp32 [H]).
+ * Each may be NULL (not wanted).  z is recomputed from y and residual, so the
+ * gradients are those of the unrounded function.  ws: nf4_workspace_size(
+ * NF4_OP_NORM_RESIDUAL_BWD, T, H, 0, 0) bytes, needed for gw_post, gw_pre or a
+ * channel gate's gradient.  Any width, pitch and alignment; T == 0 launches nothing
+ * but the zero gradients of the vectors.  Deterministic: no atomics. */
+enum { NF4_GATE_NONE = 0, NF4_GATE_CHANNEL = 1, NF4_GATE_TOKEN = 2 };
+typedef struct {
+  const void* y;
+  int64_t ld_y;
+  const void* residual;
+  int64_t ld_residual;
+  const void* gate;
+  int64_t ld_gate;
+  const float* w_post;
+  const float* w_pre;
+  int64_t T;
+  int64_t H;
+  int32_t gate_kind;
+  int32_t dtype;
+  float scale;
+  float eps;
+} nf4_norm_residual;
+nf4_status nf4_norm_residual_fwd(const nf4_norm_residual* d, void* z, int64_t ld_z, void* h, int64_t ld_h,
+                                 float* stats, void* stream);
+nf4_status nf4_norm_residual_bwd(const nf4_norm_residual* d, const float* stats, const void* gz, int64_t ld_gz,
+                                 const void* gh, int64_t ld_gh, void* gy, int64_t ld_gy, void* gr, int64_t ld_gr,
+                                 float* gw_post, void* ggate, int64_t ld_ggate, float* gw_pre, void* ws,
+                                 size_t ws_bytes, void* stream);
+
+/* nf4_attention_fwd / nf4_attention_bwd -- causal softmax attention of a whole
+ * prompt, over sequences packed one after another, with grouped heads: query head h
+ * reads key and value head h / (Hq / Hk).
+ *   o_i = sum_j p_ij v_j,  p_ij = exp(scale q_i . k_j - lse_i),  j <= i in i's sequence.
+ *   q, o [T, Hq, D], k, v [T, Hk, D] of `dtype`, each with a token and a head stride
+ *   in elements and unit stride within a head (views of one fused projection output
+ *   will do).  Hq a multiple of Hk, 1 <= D <= 256.
+ *   cu_seqlens  DEVICE int32 [nseq + 1], ascending row offsets; NULL: one sequence
+ *               of T rows (nseq ignored).  Sequences of zero rows are fine; rows
+ *               before cu_seqlens[0] or from cu_seqlens[nseq] on belong to none:
+ *               their outputs and gradients are zero and their lse is -inf.
+ *               Offsets that descend or leave [0, T] are clamped and recorded as
+ *               NF4_ERR_BAD_OFFSETS in the device status word.
+ *   lse         fp32 [Hq][T], natural log of each row's sum of exponentials; written
+ *               by the forward, read by the backward.
+ * The backward takes o, lse and go = dL/do and writes gq, gk, gv (each with its own
+ * strides); ws: nf4_workspace_size(NF4_OP_ATTENTION_BWD, T, Hq, 0, 0) bytes.  A value
+ * of a masked pair reaches no output, not even as 0 x NaN.  Deterministic.
+ * fp16 and bf16 with D a multiple of 8 up to 128, 16-byte aligned pointers and
+ * strides of a multiple of 8 elements run on the tensor cores (scores and softmax in
+ * fp32, the probabilities rounded to the inputs' type for the second product); every
+ * other layout, and fp32, runs fp32 arithmetic throughout. */
+typedef struct {
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t q_token, q_head, k_token, k_head, v_token, v_head;
+  const int32_t* cu_seqlens;
+  int64_t nseq;
+  int64_t T;
+  int32_t Hq, Hk, D;
+  int32_t dtype;
+  float scale;
+} nf4_attention;
+nf4_status nf4_attention_fwd(const nf4_attention* d, void* o, int64_t o_token, int64_t o_head, float* lse,
+                             void* stream);
+nf4_status nf4_attention_bwd(const nf4_attention* d, const void* o, int64_t o_token, int64_t o_head, const float* lse,
+                             const void* go, int64_t go_token, int64_t go_head, void* gq, int64_t gq_token,
+                             int64_t gq_head, void* gk, int64_t gk_token, int64_t gk_head, void* gv, int64_t gv_token,
+                             int64_t gv_head, void* ws, size_t ws_bytes, void* stream);
+
+/* nf4_adamw_step -- one AdamW step over `count` tensors at once (the trained tensors
+ * beside the frozen weights: adapters, gains).  Per value, in fp32 (the moments by
+ * separately rounded operations), the parameter rounded once to its own type:
+ *   m = m b1 + g (1 - b1),  v = v b2 + g g (1 - b2),  g = grad * grad_scale
+ *   p = p (1 - lr weight_decay) - lr / (1 - b1^step) * m / (sqrt(v) / sqrt(1 - b2^step) + eps)
+ *   tensors     HOST array; the pointers in it are device pointers.  Nothing of it is
+ *               kept after the call.  param and grad have `dtype`; bits 32: m, v fp32
+ *               [n]; bits 8: m, v uint8 [n] with one fp32 scale per NF4_ADAMW_BLOCK
+ *               values (m_absmax, v_absmax [ceil(n / 256)]), a value standing for
+ *               levels[code] * scale.
+ *   levels_m, levels_v  DEVICE fp32 [256], ascending: the signed and the unsigned
+ *               dynamic map (bits 8; NULL otherwise).  New codes are the nearest level
+ *               of x / max|x| of the block, ties to the lower index.
+ *   step        the number of this step, from 1.
+ *   grad_scale  DEVICE fp32 [1] or NULL (1): for instance a clipping factor.
+ * A block of a tensor is 256 consecutive values from its start; the last may be
+ * short.  nf4_adamw_state_values writes levels[code] * scale of both states (n
+ * values, fp32). */
+#define NF4_ADAMW_BLOCK 256
+typedef struct {
+  void* param;
+  const void* grad;
+  void* m;
+  void* v;
+  float* m_absmax;
+  float* v_absmax;
+  int64_t n;
+} nf4_adamw_tensor;
+nf4_status nf4_adamw_step(const nf4_adamw_tensor* tensors, int32_t count, int32_t dtype, int32_t bits,
+                          const float* levels_m, const float* levels_v, double lr, double beta1, double beta2,
+                          double eps, double weight_decay, int64_t step, const float* grad_scale, void* stream);
+nf4_status nf4_adamw_state_values(const uint8_t* m, const uint8_t* v, const float* m_absmax, const float* v_absmax,
+                                  const float* levels_m, const float* levels_v, int64_t n, float* out_m, float* out_v,
                                   void* stream);
 
 /* nf4_linear_fwd_noalloc -- the forward of nf4_linear_fwd without a workspace
