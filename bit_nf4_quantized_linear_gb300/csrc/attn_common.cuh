@@ -31,10 +31,10 @@ __device__ __forceinline__ void seq_bounds(const AttnArgs& a, int64_t b, int64_t
 }
 
 // The sequence and tile of tile number `id`, counting ceil(len / rows) tiles for
-// each sequence in turn, the last tile of a sequence first: under the causal mask it
-// is the longest, and a grid deals its CTAs in order.  Called by one full warp; all
-// lanes get the answer.
-__device__ __forceinline__ AttnTile find_tile(const AttnArgs& a, int64_t id, int rows) {
+// each sequence in turn, its last tile first (or its first): under the causal mask the
+// last query tile, or the first key tile, has the most work, and a grid deals its CTAs
+// in order.  Called by one full warp; all lanes get the answer.
+__device__ __forceinline__ AttnTile find_tile(const AttnArgs& a, int64_t id, int rows, bool last_first = true) {
   const int lane = threadIdx.x & 31;
   AttnTile r{0, 0, -1};
   int64_t base = 0;
@@ -54,7 +54,7 @@ __device__ __forceinline__ AttnTile find_tile(const AttnArgs& a, int64_t id, int
       const int64_t before = base + incl - tiles;
       r.row0 = __shfl_sync(0xffffffffu, s, src);
       r.len = static_cast<int>(__shfl_sync(0xffffffffu, e - s, src));
-      r.tile = static_cast<int>(__shfl_sync(0xffffffffu, tiles - 1 - (id - before), src));
+      r.tile = static_cast<int>(__shfl_sync(0xffffffffu, last_first ? tiles - 1 - (id - before) : id - before, src));
       return r;
     }
     base += __shfl_sync(0xffffffffu, incl, 31);

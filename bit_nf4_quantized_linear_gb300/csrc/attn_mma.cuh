@@ -1,0 +1,224 @@
+// attn_mma.cuh -- tcgen05 / TMA pieces of the attention kernels: operands from tensor
+// memory, wide tensor-memory loads and stores, packed fp32 arithmetic, bounded waits.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "attn_common.cuh"
+#include "sm100_ptx.cuh"
+
+namespace nf4 {
+
+using namespace nf4ptx;
+
+constexpr int kAttnTile = 128;                  // rows of a tile (MMA M, and N of the scores)
+constexpr int kPanelBytes = kAttnTile * 128;    // a [128 rows][64 columns] 16-bit panel, 128-byte swizzled
+constexpr uint64_t kAttnTimeoutNs = 2000000000; // bound of every wait
+
+// What the roles of a CTA share about giving up.
+struct AttnGuard {
+  volatile int* abort_flag;
+  int* status;
+};
+
+static __device__ __noinline__ bool attn_wait_slow(uint32_t bar, uint32_t parity, const AttnGuard& g) {
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+    if (mbar_try_wait_sleep(bar, parity, 20000)) return true;
+    if (*g.abort_flag) return false;
+    if (globaltimer_ns() - t0 > kAttnTimeoutNs) {
+      *g.abort_flag = 1;
+      if (g.status) atomicCAS(g.status, 0, kStatusTimeout);
+      return false;
+    }
+  }
+}
+
+// Bounded wait for a barrier phase; false: this role gives up (a timeout is recorded).
+__device__ __forceinline__ bool attn_wait(uint32_t bar, uint32_t parity, const AttnGuard& g) {
+  if (mbar_test_wait(bar, parity)) return true;
+  return attn_wait_slow(bar, parity, g);
+}
+
+// The same for copies and MMAs in flight that must land before the CTA may exit.
+static __device__ __noinline__ void attn_drain(uint32_t bar, uint32_t parity, const AttnGuard& g) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait_sleep(bar, parity, 20000)) {
+    if (globaltimer_ns() - t0 > kAttnTimeoutNs) {
+      if (g.status) atomicCAS(g.status, 0, kStatusTimeout);
+      return;
+    }
+  }
+}
+
+// Tile of 128 rows x 64 columns of one head of a [T][heads][D] tensor.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t c0, int32_t c1,
+                                            int32_t c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
+// D(tmem) (+)= A(tmem) * B(smem): A's row is the lane, two 16-bit values a column.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Operand tile [128 rows][64-column panels], 128-byte swizzled rows.  Rows are M / N
+// and columns the contraction (K-major): 16 columns further is 32 bytes, the next
+// panel kPanelBytes.
+__device__ __forceinline__ uint64_t desc_k_major(uint32_t saddr, int step) {
+  return smem_desc_sw128(saddr + (step >> 2) * kPanelBytes + (step & 3) * 32, 16, 1024);
+}
+// Columns are M / N and rows the contraction (MN-major): 16 rows further is 2 KB.
+__device__ __forceinline__ uint64_t desc_mn_major(uint32_t saddr, int step) {
+  return smem_desc_sw128(saddr + step * 2048, kPanelBytes, 1024);
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t* r);
+template <>
+__device__ __forceinline__ void tmem_ld<32>(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32"
+      " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23,"
+      " %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0],"
+      " {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0],"
+      " {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24,"
+      " %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Two fp32 operations in one instruction, each rounded as alone.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t x, y, z, r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(z) : "f"(c.x), "f"(c.y));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+  float2 o;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(r));
+  return o;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t x, y, r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  float2 o;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(r));
+  return o;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t x, y, r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  float2 o;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(r));
+  return o;
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Two values rounded to 16 bits, the first in the low half.
+template <bool F16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  if (F16) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+template <bool F16>
+__device__ __forceinline__ float lo16(uint32_t w) {
+  return F16 ? __half2float(__ushort_as_half(static_cast<unsigned short>(w))) : __uint_as_float(w << 16);
+}
+template <bool F16>
+__device__ __forceinline__ float hi16(uint32_t w) {
+  return F16 ? __half2float(__ushort_as_half(static_cast<unsigned short>(w >> 16))) : __uint_as_float(w & 0xffff0000u);
+}
+
+// Whether either half of w is an infinity or a NaN (its exponent bits all ones).
+template <bool F16>
+__device__ __forceinline__ bool nonfinite16(uint32_t w) {
+  constexpr uint32_t e = F16 ? 0x7c00u : 0x7f80u;
+  return (w & e) == e || ((w >> 16) & e) == e;
+}
+
+// One warp clears rows >= `rows` of an operand tile in shared memory and, with
+// `values`, replaces the infinities and NaNs of the others by zero; true (in every
+// lane) when there were any.  Ends with the fence that lets the tensor cores see the
+// stores.
+template <bool F16, int PANELS>
+__device__ __forceinline__ bool clean_tile(uint8_t* tile, int rows, bool values) {
+  const int lane = threadIdx.x & 31;
+  constexpr uint32_t e = F16 ? 0x7c00u : 0x7f80u;
+  bool any = false, wrote = false;
+  for (int i = lane; i < PANELS * kAttnTile * 8; i += 32) {  // 16-byte pieces; a row is 8 pieces of a panel
+    uint4* p = reinterpret_cast<uint4*>(tile) + i;
+    if (((i >> 3) & (kAttnTile - 1)) >= rows) {
+      *p = make_uint4(0u, 0u, 0u, 0u);
+      wrote = true;
+      continue;
+    }
+    if (!values) continue;
+    uint4 v = *p;
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if (nonfinite16<F16>(w[0]) || nonfinite16<F16>(w[1]) || nonfinite16<F16>(w[2]) || nonfinite16<F16>(w[3])) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if ((w[k] & e) == e) w[k] &= 0xffff0000u;
+        if (((w[k] >> 16) & e) == e) w[k] &= 0x0000ffffu;
+      }
+      *p = make_uint4(w[0], w[1], w[2], w[3]);
+      any = wrote = true;
+    }
+  }
+  if (wrote) fence_proxy_async_smem();
+  return __any_sync(0xffffffffu, any);
+}
+
+}  // namespace nf4

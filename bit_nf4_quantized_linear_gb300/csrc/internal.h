@@ -131,6 +131,13 @@ inline int64_t attn_tiles(const AttnArgs& a, int rows) {
   const int64_t most = a.nseq < a.T ? a.nseq : a.T;  // sequences that can hold a row
   return a.T / rows + most;
 }
+// Tensor-core kernels: [T][heads][D] tensors as 3-D maps with a box of 64 columns x 1
+// head x 128 rows, 128-byte swizzle.
+struct AttnMaps {
+  CUtensorMap q, k, v, go;
+};
+cudaError_t launch_attn_fwd(bool f16, const AttnMaps& m, const AttnArgs& a, cudaStream_t s);
+cudaError_t launch_attn_bwd(bool f16, const AttnMaps& m, const AttnArgs& a, int sms, cudaStream_t s);
 cudaError_t launch_attn_any(bool backward, int dtype, const AttnArgs& a, int sms, cudaStream_t s);
 
 // Multi-product launches (nf4_linear_fwd_multi / nf4_linear_dgrad_multi): up to

@@ -117,6 +117,30 @@ bool encode_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_
   return r == CUDA_SUCCESS;
 }
 
+// A 16-bit [T][heads][D] tensor with token and head strides in elements, boxes of 64
+// columns x 1 head x 128 rows.
+bool encode_heads(CUtensorMap* m, bool f16, const void* base, int64_t T, int64_t heads, int64_t D, int64_t token,
+                  int64_t head) {
+  auto fn = tensor_map_encoder();
+  if (!fn) {
+    std::snprintf(g_last_error, sizeof(g_last_error), "cuTensorMapEncodeTiled entry point not found");
+    return false;
+  }
+  // the stride of a dimension of one is never used; any valid value does
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(T)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(heads > 1 ? head : D) * 2,
+                                 static_cast<cuuint64_t>(T > 1 ? token : D) * 2};
+  const cuuint32_t box[3] = {64, 1, 128}, estr[3] = {1, 1, 1};
+  const CUresult r = fn(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                        const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    std::snprintf(g_last_error, sizeof(g_last_error), "cuTensorMapEncodeTiled failed (CUresult %d) for heads",
+                  static_cast<int>(r));
+  return r == CUDA_SUCCESS;
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Tensor map of the codes for one contraction step: the forward reads 128 weight
@@ -968,6 +992,34 @@ nf4_status attn_args(const nf4_attention* d, nf4::AttnArgs* a) {
   return NF4_OK;
 }
 
+// Whether a tensor can be a TMA operand of the tensor-core attention kernels: 16-byte
+// aligned base, positive strides of whole 16-byte pieces below 2^40 bytes.
+bool tma_heads(const void* p, int64_t T, int64_t heads, int64_t token, int64_t head) {
+  auto ok = [](int64_t s) { return s > 0 && s % 8 == 0 && s < (int64_t{1} << 39); };
+  return aligned16(p) && (T == 1 || ok(token)) && (heads == 1 || ok(head));
+}
+
+// Rows that 16-byte stores can write.
+bool vec_heads(const void* p, int64_t token, int64_t head) {
+  return aligned16(p) && token % 8 == 0 && head % 8 == 0;
+}
+
+// The tensor cores take 16-bit types, whole 16-byte rows of at most 128 values, and a
+// positive scale (the running maximum is that of the unscaled scores, and a hidden
+// score is -inf before it is scaled).
+bool attn_on_tensor_cores(const nf4_attention* d) {
+  return d->dtype != NF4_DTYPE_F32 && d->D % 8 == 0 && d->D <= 128 && d->scale > 0.0f &&
+         tma_heads(d->q, d->T, d->Hq, d->q_token, d->q_head) && tma_heads(d->k, d->T, d->Hk, d->k_token, d->k_head) &&
+         tma_heads(d->v, d->T, d->Hk, d->v_token, d->v_head);
+}
+
+bool attn_maps(const nf4_attention* d, nf4::AttnMaps* m) {  // go, of the backward, apart
+  const bool f16 = d->dtype == NF4_DTYPE_F16;
+  return encode_heads(&m->q, f16, d->q, d->T, d->Hq, d->D, d->q_token, d->q_head) &&
+         encode_heads(&m->k, f16, d->k, d->T, d->Hk, d->D, d->k_token, d->k_head) &&
+         encode_heads(&m->v, f16, d->v, d->T, d->Hk, d->D, d->v_token, d->v_head);
+}
+
 }  // namespace
 
 extern "C" {
@@ -1060,7 +1112,16 @@ nf4_status nf4_attention_fwd(const nf4_attention* d, void* o, int64_t o_token, i
   DevInfo dev;
   if (!current_device(&dev)) return cuda_fail(cudaGetLastError(), "device query");
   a.status = dev.status;
-  cudaError_t le = nf4::launch_attn_any(false, d->dtype, a, dev.sms, static_cast<cudaStream_t>(stream));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (dev.supported && attn_on_tensor_cores(d) && vec_heads(o, o_token, o_head)) {
+    nf4::AttnMaps m;
+    if (!attn_maps(d, &m)) return NF4_ERR_CUDA;
+    cudaError_t le = nf4::launch_attn_fwd(d->dtype == NF4_DTYPE_F16, m, a, st);
+    if (le != cudaSuccess) return cuda_fail(le, "kernel launch");
+    count(NF4_PATH_ATTENTION);
+    return NF4_OK;
+  }
+  cudaError_t le = nf4::launch_attn_any(false, d->dtype, a, dev.sms, st);
   if (le != cudaSuccess) return cuda_fail(le, "kernel launch");
   count(NF4_PATH_ATTENTION_ANY);
   return NF4_OK;
@@ -1100,7 +1161,19 @@ nf4_status nf4_attention_bwd(const nf4_attention* d, const void* o, int64_t o_to
   DevInfo dev;
   if (!current_device(&dev)) return cuda_fail(cudaGetLastError(), "device query");
   a.status = dev.status;
-  cudaError_t le = nf4::launch_attn_any(true, d->dtype, a, dev.sms, static_cast<cudaStream_t>(stream));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (dev.supported && attn_on_tensor_cores(d) && tma_heads(go, a.T, a.Hq, go_token, go_head) &&
+      vec_heads(o, o_token, o_head) && vec_heads(go, go_token, go_head) && vec_heads(gq, gq_token, gq_head) &&
+      vec_heads(gk, gk_token, gk_head) && vec_heads(gv, gv_token, gv_head)) {
+    nf4::AttnMaps m;
+    const bool f16 = d->dtype == NF4_DTYPE_F16;
+    if (!attn_maps(d, &m) || !encode_heads(&m.go, f16, go, a.T, a.Hq, a.D, go_token, go_head)) return NF4_ERR_CUDA;
+    cudaError_t le = nf4::launch_attn_bwd(f16, m, a, dev.sms, st);
+    if (le != cudaSuccess) return cuda_fail(le, "kernel launch");
+    count(NF4_PATH_ATTENTION);
+    return NF4_OK;
+  }
+  cudaError_t le = nf4::launch_attn_any(true, d->dtype, a, dev.sms, st);
   if (le != cudaSuccess) return cuda_fail(le, "kernel launch");
   count(NF4_PATH_ATTENTION_ANY);
   return NF4_OK;

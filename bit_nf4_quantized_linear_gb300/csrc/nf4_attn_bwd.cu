@@ -1,0 +1,596 @@
+// nf4_attn_bwd.cu -- backward of causal attention over packed sequences on the tensor
+// cores (fp16 or bf16, head width a multiple of 8 up to 128).
+//
+// A first kernel forms delta_i = do_i . o_i.  A second launch holds two kinds of CTAs,
+// the longer ones first:
+//  - keys: 128 keys of one key head, over every query tile that sees them and every
+//    query head of the group.  Transposed, so that P and dS stay in tensor memory as the
+//    left operands:
+//      S' = K Q^T,  dP' = V dO^T,  P' = exp2(S' c - lse log2 e),  dV += P' dO,
+//      dS' = P' (dP' - delta),  dK += dS' Q
+//  - queries: 128 queries of one head, over the key tiles they see:
+//      S = Q K^T,  dP = dO V^T,  dS = P (dP - delta),  dQ += dS K
+// Seven products against the five that the definition needs: the scores and their
+// gradient are formed twice so that each sum stays with one CTA in one order, without
+// atomics on dQ or partial sums through memory.  P and dS are rounded to the operands'
+// type for their products; sums are fp32.
+//
+// The MMA warp keeps the tensor cores on one of a step's products while the two
+// compute groups (each half of a tile's columns, one thread a row) work on the other:
+// in the keys' CTAs dV and the next S' run during dS, dK and the next dP' during P; in
+// the queries' CTAs dQ and the scores after next run while dS is formed.
+//
+// Masked pairs: P and dS are set to 0 by index.  Where that 0 would still meet an
+// infinity or a NaN as a factor -- rows of another sequence in a ragged tile, and rows
+// of the diagonal tile -- the tile is cleaned in shared memory first.  A row whose lse
+// is not finite has P = NaN wherever it is seen, and non-finite values of dO taken out
+// of a diagonal tile are added to dV at the end.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <type_traits>
+
+#include "attn_mma.cuh"
+#include "elem.cuh"
+
+namespace nf4 {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kWarpMma = 8, kWarpLoad = 9, kWarpPrep = 10;
+constexpr int kCompute = 256;  // threads of the two compute groups
+constexpr float kLog2e = 1.4426950408889634f;
+// fp16 keeps 11 bits down to 2^-14 only: the keys' CTAs hold P' times 2^14 (P' <= 1), and
+// divide dV by it at the end.
+constexpr float kShift = 14.0f, kUnshift = 1.0f / 16384.0f;
+
+template <int PANELS>
+struct Geo {
+  static constexpr int kTileBytes = PANELS * kPanelBytes;
+  // keys: K, V, then two stages of (Q, dO).  queries: Q, dO, three K, two V.
+  static constexpr int kTiles = 7;
+  static constexpr int kSmem = kTiles * kTileBytes + 1024;
+};
+
+struct Shared {
+  AttnTile tile;
+  uint32_t tmem;
+  int abort_flag;
+  int dirty;
+  uint64_t own_full, full[3], vfull[2], empty[3], vempty[2], ready[2], diag, clean;
+  uint64_t s_full[2], dp_full, p_full, ds_full, out_full, drain;
+};
+
+// Row statistics of the keys' CTAs, in the tile of shared memory that they leave free.
+struct Rows {
+  float lse2[2][kAttnTile];
+  float delta[2][kAttnTile];
+};
+
+// delta[h][t] = do . o: 16 bytes a lane, rows of a head side by side.
+template <typename T>
+__global__ void __launch_bounds__(256) attn_delta_kernel(const __grid_constant__ AttnArgs a) {
+  const int per = a.D / 8;                          // lanes with work in a row
+  const int width = per <= 8 ? 8 : 16;              // lanes of a row
+  const int lane = threadIdx.x & (width - 1);
+  const int64_t n = a.T * a.Hq, rows = static_cast<int64_t>(gridDim.x) * 256 / width;
+  const int64_t first = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / width;
+  for (int64_t i0 = 0; i0 < n; i0 += rows) {  // the same trips for all lanes of a warp
+    const int64_t i = i0 + first;
+    float s = 0.0f;
+    if (i < n && lane < per) {
+      const int64_t t = i / a.Hq;
+      const int h = static_cast<int>(i - t * a.Hq);
+      const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.o) + t * a.o_t + h * a.o_h + lane * 8);
+      const uint4 y = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.go) + t * a.go_t + h * a.go_h + lane * 8);
+      const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+      constexpr bool f16 = std::is_same<T, __half>::value;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s = fmaf(lo16<f16>(xs[e]), lo16<f16>(ys[e]), s);
+        s = fmaf(hi16<f16>(xs[e]), hi16<f16>(ys[e]), s);
+      }
+    }
+    for (int o = width / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (i < n && lane == 0) {
+      const int64_t t = i / a.Hq;
+      a.delta[(i - t * a.Hq) * a.T + t] = s;
+    }
+  }
+}
+
+// lse in units of log2, as the weights need it: +inf (weight 0) past the sequence, NaN
+// for a row of it whose sum of exponentials is not a positive number.
+__device__ __forceinline__ float lse2_of(const AttnArgs& a, int64_t at, bool in) {
+  if (!in) return INFINITY;
+  const float l = a.lse[at];
+  return fabsf(l) < INFINITY ? l * kLog2e : __int_as_float(0x7fffffff);
+}
+
+// Writes 32 columns of a row that this thread holds.
+template <bool F16, typename T>
+__device__ __forceinline__ void store32(T* out, const uint32_t* r, float f, int from, int D) {
+#pragma unroll
+  for (int e = 0; e < 32; e += 8)
+    if (from + e < D)
+      *reinterpret_cast<uint4*>(out + from + e) =
+          make_uint4(pack16<F16>(__uint_as_float(r[e]) * f, __uint_as_float(r[e + 1]) * f),
+                     pack16<F16>(__uint_as_float(r[e + 2]) * f, __uint_as_float(r[e + 3]) * f),
+                     pack16<F16>(__uint_as_float(r[e + 4]) * f, __uint_as_float(r[e + 5]) * f),
+                     pack16<F16>(__uint_as_float(r[e + 6]) * f, __uint_as_float(r[e + 7]) * f));
+}
+
+template <bool F16, int PANELS>
+struct Ctx {
+  using G = Geo<PANELS>;
+  const AttnArgs& a;
+  Shared& sh;
+  AttnGuard guard;
+  uint8_t* smem;
+  uint32_t sbase, tmem;
+  int warp, lane;
+  AttnTile w;
+  int ksteps, boxes;
+
+  __device__ __forceinline__ uint32_t bar(const uint64_t& b) const { return smem_addr(&b); }
+  __device__ __forceinline__ uint32_t tile(int i) const { return sbase + i * G::kTileBytes; }
+  __device__ __forceinline__ bool wait(const uint64_t& b, uint32_t parity) const { return attn_wait(bar(b), parity, guard); }
+  __device__ __forceinline__ bool wait_warp(const uint64_t& b, uint32_t parity) const {
+    return __all_sync(0xffffffffu, attn_wait(bar(b), parity, guard));
+  }
+  __device__ __forceinline__ void load(const CUtensorMap* m, int to, const uint64_t& b, int head, int row) const {
+    for (int x = 0; x < boxes; ++x) tma_load_3d(tile(to) + x * kPanelBytes, m, bar(b), x * 64, head, row);
+  }
+  __device__ __forceinline__ uint32_t bytes() const { return boxes * kPanelBytes; }
+  // D = A B^T over the head's columns, both operands in shared memory.
+  __device__ __forceinline__ void over_columns(uint32_t d, int ta, int tb, uint32_t idesc) const {
+    for (int k = 0; k < ksteps; ++k)
+      mma_bf16_ss(d, desc_k_major(tile(ta), k), desc_k_major(tile(tb), k), idesc, k > 0);
+  }
+  // D += A B over the tile's 128 rows, A in tensor memory in two halves 64 columns apart.
+  __device__ __forceinline__ void over_rows(uint32_t d, uint32_t at, int tb, uint32_t idesc, bool more) const {
+    for (int k = 0; k < kAttnTile / 16; ++k)
+      mma_f16_ts(d, at + (k >> 2) * 64 + (k & 3) * 8, desc_mn_major(tile(tb), k), idesc, more || k > 0);
+  }
+};
+
+// ------------------------------------------------------------------------- keys --
+// Tiles in shared memory: 0 K, 1 V, 2 + 2 st Q, 3 + 2 st dO, 6 Rows.  Tensor memory: S' and P'
+// from 0, dP' and dS' from 128, dV from 256, dK from 384.
+template <bool F16, int PANELS, typename T>
+__device__ __forceinline__ void keys_cta(const Ctx<F16, PANELS>& x, const CUtensorMap* mq, const CUtensorMap* mk,
+                                         const CUtensorMap* mv, const CUtensorMap* mg, int hk) {
+  const AttnArgs& a = x.a;
+  Shared& sh = x.sh;
+  const AttnTile& w = x.w;
+  Rows& rs = *reinterpret_cast<Rows*>(x.smem + 6 * Geo<PANELS>::kTileBytes);
+  const int jt = w.tile, nt = (w.len + kAttnTile - 1) / kAttnTile, nq = nt - jt;
+  const int group = a.Hq / a.Hk, n = group * nq;
+  const int row0 = static_cast<int>(w.row0), lane = x.lane, warp = x.warp;
+  if (warp == kWarpLoad) {
+    if (lane == 0) {
+      mbar_arrive_expect_tx(x.bar(sh.own_full), 2 * x.bytes());
+      x.load(mk, 0, sh.own_full, hk, row0 + jt * kAttnTile);
+      x.load(mv, 1, sh.own_full, hk, row0 + jt * kAttnTile);
+      int done = 0, g = 0, i = jt;
+      for (int it = 0; it < n; ++it) {
+        const int st = it & 1;
+        if (!x.wait(sh.empty[st], ((it >> 1) & 1) ^ 1)) break;
+        mbar_arrive_expect_tx(x.bar(sh.full[st]), 2 * x.bytes());
+        x.load(mq, 2 + 2 * st, sh.full[st], hk * group + g, row0 + i * kAttnTile);
+        x.load(mg, 3 + 2 * st, sh.full[st], hk * group + g, row0 + i * kAttnTile);
+        done = it + 1;
+        if (++i == nt) {
+          i = jt;
+          ++g;
+        }
+      }
+      attn_drain(x.bar(sh.own_full), 0, x.guard);
+      for (int it = done < 2 ? 0 : done - 2; it < done; ++it) attn_drain(x.bar(sh.full[it & 1]), (it >> 1) & 1, x.guard);
+    }
+  } else if (warp == kWarpPrep) {
+    int g = 0, i = jt;
+    for (int it = 0; it < n; ++it) {
+      const int st = it & 1, rows = min(kAttnTile, w.len - i * kAttnTile);
+      const int64_t at = static_cast<int64_t>(hk * group + g) * a.T + w.row0 + i * kAttnTile;
+      float l[4], d[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = lane * 4 + e;
+        l[e] = lse2_of(a, at + r, r < rows) - (F16 ? kShift : 0.0f);
+        d[e] = r < rows ? a.delta[at + r] * (F16 ? kUnshift : 1.0f) : 0.0f;
+      }
+      if (!x.wait_warp(sh.empty[st], ((it >> 1) & 1) ^ 1)) break;
+      *reinterpret_cast<float4*>(&rs.lse2[st][lane * 4]) = make_float4(l[0], l[1], l[2], l[3]);
+      *reinterpret_cast<float4*>(&rs.delta[st][lane * 4]) = make_float4(d[0], d[1], d[2], d[3]);
+      if (!x.wait_warp(sh.full[st], (it >> 1) & 1)) break;
+      if (i == jt || rows < kAttnTile) {
+        clean_tile<F16, PANELS>(x.smem + (2 + 2 * st) * Geo<PANELS>::kTileBytes, rows, i == jt);
+        if (clean_tile<F16, PANELS>(x.smem + (3 + 2 * st) * Geo<PANELS>::kTileBytes, rows, i == jt) && lane == 0) sh.dirty = 1;
+      }
+      mbar_arrive(x.bar(sh.ready[st]));
+      if (++i == nt) {
+        i = jt;
+        ++g;
+      }
+    }
+  } else if (warp == kWarpMma) {
+    if (lane == 0) {
+      const uint32_t id_s = F16 ? idesc_f16_f32(128, 128, false, false) : idesc_bf16_f32(128, 128, false, false);
+      const uint32_t id_o = F16 ? idesc_f16_f32(128, x.ksteps * 16, false, true) : idesc_bf16_f32(128, x.ksteps * 16, false, true);
+      const uint32_t S = x.tmem, P = x.tmem + 128, DV = x.tmem + 256, DK = x.tmem + 384;
+      bool ok = x.wait(sh.own_full, 0) && x.wait(sh.ready[0], 0);
+      if (ok) {
+        x.over_columns(S, 0, 2, id_s);
+        mma_commit(x.bar(sh.s_full[0]));
+        x.over_columns(P, 1, 3, id_s);
+        mma_commit(x.bar(sh.dp_full));
+      }
+      for (int it = 0; ok && it < n; ++it) {
+        const int st = it & 1, st1 = st ^ 1;
+        const bool more = it + 1 < n;
+        if (!(ok = x.wait(sh.p_full, it & 1))) break;
+        tc_fence_after();
+        x.over_rows(DV, S, 3 + 2 * st, id_o, it > 0);
+        if (more) {
+          if (!(ok = x.wait(sh.ready[st1], ((it + 1) >> 1) & 1))) break;
+          x.over_columns(S, 0, 2 + 2 * st1, id_s);
+          mma_commit(x.bar(sh.s_full[0]));
+        }
+        if (!(ok = x.wait(sh.ds_full, it & 1))) break;
+        tc_fence_after();
+        x.over_rows(DK, P, 2 + 2 * st, id_o, it > 0);
+        mma_commit(x.bar(sh.empty[st]));
+        if (more) {
+          x.over_columns(P, 1, 3 + 2 * st1, id_s);
+          mma_commit(x.bar(sh.dp_full));
+        } else {
+          mma_commit(x.bar(sh.out_full));
+        }
+      }
+      if (!ok) {
+        mma_commit(x.bar(sh.drain));
+        attn_drain(x.bar(sh.drain), 0, x.guard);
+      }
+    }
+  } else if (warp < 8) {
+    const int wg = warp >> 2, kv = (warp & 3) * 32 + lane;  // this thread's key within the tile
+    const uint32_t lanes = ((warp & 3) * 32u) << 16;
+    const uint32_t ts = x.tmem + lanes + wg * 64, tp = ts + 128;
+    const float c = a.scale * kLog2e;
+    const float2 c2 = make_float2(c, c);
+    bool ok = true;
+    int i = jt;
+    for (int it = 0; it < n; ++it) {
+      const int st = it & 1;
+      const bool diag = i == jt;
+      if (!(ok = x.wait_warp(sh.ready[st], (it >> 1) & 1) && x.wait_warp(sh.s_full[0], it & 1))) break;
+      tc_fence_after();
+      uint32_t s[64];
+      tmem_ld<32>(ts, s);
+      tmem_ld<32>(ts + 32, s + 32);
+      tmem_wait_ld();
+#pragma unroll
+      for (int q = 0; q < 64; q += 4) {
+        const float4 l = *reinterpret_cast<const float4*>(&rs.lse2[st][wg * 64 + q]);
+        const float2 u = fma2(make_float2(__uint_as_float(s[q]), __uint_as_float(s[q + 1])), c2, make_float2(-l.x, -l.y));
+        const float2 v = fma2(make_float2(__uint_as_float(s[q + 2]), __uint_as_float(s[q + 3])), c2, make_float2(-l.z, -l.w));
+        s[q] = __float_as_uint(exp2_approx(u.x));
+        s[q + 1] = __float_as_uint(exp2_approx(u.y));
+        s[q + 2] = __float_as_uint(exp2_approx(v.x));
+        s[q + 3] = __float_as_uint(exp2_approx(v.y));
+      }
+      if (diag) {
+#pragma unroll
+        for (int q = 0; q < 64; ++q)
+          if (wg * 64 + q < kv) s[q] = 0u;  // queries before this key
+      }
+#pragma unroll
+      for (int q = 0; q < 64; q += 32) {
+        uint32_t p[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) p[e] = pack16<F16>(__uint_as_float(s[q + 2 * e]), __uint_as_float(s[q + 2 * e + 1]));
+        tmem_st16(ts + q / 2, p);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(x.bar(sh.p_full));
+      if (!(ok = x.wait_warp(sh.dp_full, it & 1))) break;
+      tc_fence_after();
+#pragma unroll
+      for (int q = 0; q < 64; q += 32) {
+        uint32_t d[32], p[16];
+        tmem_ld<32>(tp + q, d);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+          const float4 dl = *reinterpret_cast<const float4*>(&rs.delta[st][wg * 64 + q + e]);
+          float2 u = make_float2(__uint_as_float(d[e]), __uint_as_float(d[e + 1]));
+          float2 v = make_float2(__uint_as_float(d[e + 2]), __uint_as_float(d[e + 3]));
+          const float2 one = make_float2(kUnshift, kUnshift);
+          u = F16 ? fma2(u, one, make_float2(-dl.x, -dl.y)) : add2(u, make_float2(-dl.x, -dl.y));
+          v = F16 ? fma2(v, one, make_float2(-dl.z, -dl.w)) : add2(v, make_float2(-dl.z, -dl.w));
+          u = mul2(u, make_float2(__uint_as_float(s[q + e]), __uint_as_float(s[q + e + 1])));
+          v = mul2(v, make_float2(__uint_as_float(s[q + e + 2]), __uint_as_float(s[q + e + 3])));
+          if (diag) {
+            u.x = wg * 64 + q + e < kv ? 0.0f : u.x;
+            u.y = wg * 64 + q + e + 1 < kv ? 0.0f : u.y;
+            v.x = wg * 64 + q + e + 2 < kv ? 0.0f : v.x;
+            v.y = wg * 64 + q + e + 3 < kv ? 0.0f : v.y;
+          }
+          p[e / 2] = pack16<F16>(u.x, u.y);
+          p[e / 2 + 1] = pack16<F16>(v.x, v.y);
+        }
+        // dS' of columns q .. q + 31 goes to q / 2 ..: columns already read
+        tmem_st16(tp + q / 2, p);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(x.bar(sh.ds_full));
+      if (++i == nt) i = jt;
+    }
+    if (ok && x.wait_warp(sh.out_full, 0)) {
+      tc_fence_after();
+      // the first group writes dV, the second dK
+      const bool live = jt * kAttnTile + kv < w.len;
+      const int64_t r = w.row0 + jt * kAttnTile + kv;
+      const uint32_t from = x.tmem + lanes + 256 + wg * 128;
+      T* out = wg == 0 ? static_cast<T*>(a.gv) + r * a.gv_t + hk * a.gv_h : static_cast<T*>(a.gk) + r * a.gk_t + hk * a.gk_h;
+      const float f = wg == 0 ? (F16 ? kUnshift : 1.0f) : a.scale;
+      const bool dirty = wg == 0 && sh.dirty;
+      for (int q = 0; q < a.D; q += 32) {
+        uint32_t o[32];
+        tmem_ld<32>(from + q, o);
+        tmem_wait_ld();
+        if (dirty && live) {
+          // the non-finite values taken out of dO's diagonal tiles, for the keys that they see
+          const int end = min(w.len, (jt + 1) * kAttnTile);
+#pragma unroll 1
+          for (int g = 0; g < group; ++g)
+#pragma unroll 1
+            for (int t = jt * kAttnTile + kv; t < end; ++t) {
+              const T* go = static_cast<const T*>(a.go) + (w.row0 + t) * a.go_t + (hk * group + g) * a.go_h;
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                if (q + e >= a.D) continue;
+                const float y = to_f32(go[q + e]);
+                if (!(fabsf(y) < INFINITY)) o[e] = __float_as_uint(__uint_as_float(o[e]) + y);
+              }
+            }
+        }
+        if (live) store32<F16>(out, o, f, q, a.D);
+        __syncwarp();
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------- queries --
+// Tiles in shared memory: 0 Q, 1 dO, 2 + j % 3 K, 5 + j % 2 V.  Tensor memory: S and dS
+// of even steps from 0, of odd steps from 128, dP from 256, dQ from 384.
+template <bool F16, int PANELS, typename T>
+__device__ __forceinline__ void queries_cta(const Ctx<F16, PANELS>& x, const CUtensorMap* mq, const CUtensorMap* mk,
+                                            const CUtensorMap* mv, const CUtensorMap* mg, int h) {
+  const AttnArgs& a = x.a;
+  Shared& sh = x.sh;
+  const AttnTile& w = x.w;
+  const int it = w.tile, n = it + 1, hk = h / (a.Hq / a.Hk);
+  const int row0 = static_cast<int>(w.row0), lane = x.lane, warp = x.warp;
+  if (warp == kWarpLoad) {
+    if (lane == 0) {
+      mbar_arrive_expect_tx(x.bar(sh.own_full), 2 * x.bytes());
+      x.load(mq, 0, sh.own_full, h, row0 + it * kAttnTile);
+      x.load(mg, 1, sh.own_full, h, row0 + it * kAttnTile);
+      int nk = 0, nv = 0;
+      bool diag = false;
+      for (int j = 0; j < n; ++j) {
+        if (!x.wait(sh.empty[j % 3], ((j / 3) & 1) ^ 1)) break;
+        const uint64_t& b = j + 1 == n ? sh.diag : sh.full[j % 3];  // the last one is cleaned first
+        mbar_arrive_expect_tx(x.bar(b), x.bytes());
+        x.load(mk, 2 + j % 3, b, hk, row0 + j * kAttnTile);
+        if (j + 1 == n) diag = true; else nk = j + 1;
+        if (!x.wait(sh.vempty[j & 1], ((j >> 1) & 1) ^ 1)) break;
+        mbar_arrive_expect_tx(x.bar(sh.vfull[j & 1]), x.bytes());
+        x.load(mv, 5 + (j & 1), sh.vfull[j & 1], hk, row0 + j * kAttnTile);
+        nv = j + 1;
+      }
+      attn_drain(x.bar(sh.own_full), 0, x.guard);
+      if (diag) attn_drain(x.bar(sh.diag), 0, x.guard);
+      for (int j = nk < 3 ? 0 : nk - 3; j < nk; ++j) attn_drain(x.bar(sh.full[j % 3]), (j / 3) & 1, x.guard);
+      for (int j = nv < 2 ? 0 : nv - 2; j < nv; ++j) attn_drain(x.bar(sh.vfull[j & 1]), (j >> 1) & 1, x.guard);
+    }
+  } else if (warp == kWarpPrep) {
+    if (x.wait_warp(sh.diag, 0)) {
+      clean_tile<F16, PANELS>(x.smem + (2 + it % 3) * Geo<PANELS>::kTileBytes, min(kAttnTile, w.len - it * kAttnTile), true);
+      mbar_arrive(x.bar(sh.clean));
+    }
+  } else if (warp == kWarpMma) {
+    if (lane == 0) {
+      const uint32_t id_s = F16 ? idesc_f16_f32(128, 128, false, false) : idesc_bf16_f32(128, 128, false, false);
+      const uint32_t id_o = F16 ? idesc_f16_f32(128, x.ksteps * 16, false, true) : idesc_bf16_f32(128, x.ksteps * 16, false, true);
+      const uint32_t S = x.tmem, P = x.tmem + 256, DQ = x.tmem + 384;
+      auto key = [&](int j) { return j + 1 == n ? x.wait(sh.clean, 0) : x.wait(sh.full[j % 3], (j / 3) & 1); };
+      auto scores = [&](int j) {
+        x.over_columns(S + (j & 1) * 128, 0, 2 + j % 3, id_s);
+        mma_commit(x.bar(sh.s_full[j & 1]));
+      };
+      auto grads = [&](int j) {
+        x.over_columns(P, 1, 5 + (j & 1), id_s);
+        mma_commit(x.bar(sh.dp_full));
+        mma_commit(x.bar(sh.vempty[j & 1]));
+      };
+      bool ok = x.wait(sh.own_full, 0) && key(0);
+      if (ok) {
+        scores(0);
+        if ((ok = x.wait(sh.vfull[0], 0))) grads(0);
+        if (ok && n > 1 && (ok = key(1))) scores(1);
+      }
+      for (int j = 0; ok && j < n; ++j) {
+        if (!(ok = x.wait(sh.ds_full, j & 1))) break;
+        tc_fence_after();
+        if (j + 1 < n) {
+          if (!(ok = x.wait(sh.vfull[(j + 1) & 1], ((j + 1) >> 1) & 1))) break;
+          grads(j + 1);
+        }
+        x.over_rows(DQ, S + (j & 1) * 128, 2 + j % 3, id_o, j > 0);
+        mma_commit(x.bar(sh.empty[j % 3]));
+        if (j + 2 < n) {
+          if (!(ok = key(j + 2))) break;
+          scores(j + 2);
+        }
+      }
+      if (ok) {
+        mma_commit(x.bar(sh.out_full));
+      } else {
+        mma_commit(x.bar(sh.drain));
+        attn_drain(x.bar(sh.drain), 0, x.guard);
+      }
+    }
+  } else if (warp < 8) {
+    const int wg = warp >> 2, row = (warp & 3) * 32 + lane, i = it * kAttnTile + row;
+    const uint32_t lanes = ((warp & 3) * 32u) << 16;
+    const uint32_t tp = x.tmem + lanes + 256 + wg * 64;
+    const float c = a.scale * kLog2e;
+    const bool live = i < w.len;
+    const int64_t at = static_cast<int64_t>(h) * a.T + w.row0 + i;
+    const float l = lse2_of(a, at, live), dl = live ? a.delta[at] : 0.0f;
+    const float2 c2 = make_float2(c, c), l2 = make_float2(-l, -l), d2 = make_float2(-dl, -dl);
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+      const uint32_t ts = x.tmem + lanes + (j & 1) * 128 + wg * 64;
+      const bool diag = j + 1 == n;
+      if (!(ok = x.wait_warp(sh.s_full[j & 1], (j >> 1) & 1) && x.wait_warp(sh.dp_full, j & 1))) break;
+      tc_fence_after();
+      uint32_t s[64], d[64];
+      tmem_ld<32>(ts, s);
+      tmem_ld<32>(ts + 32, s + 32);
+      tmem_ld<32>(tp, d);
+      tmem_ld<32>(tp + 32, d + 32);
+      tmem_wait_ld();
+#pragma unroll
+      for (int q = 0; q < 64; q += 32) {
+        uint32_t p[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          float2 u = fma2(make_float2(__uint_as_float(s[q + 2 * e]), __uint_as_float(s[q + 2 * e + 1])), c2, l2);
+          u.x = exp2_approx(u.x);
+          u.y = exp2_approx(u.y);
+          u = mul2(u, add2(make_float2(__uint_as_float(d[q + 2 * e]), __uint_as_float(d[q + 2 * e + 1])), d2));
+          if (diag) {
+            u.x = wg * 64 + q + 2 * e > row ? 0.0f : u.x;  // keys after this query
+            u.y = wg * 64 + q + 2 * e + 1 > row ? 0.0f : u.y;
+          }
+          p[e] = pack16<F16>(u.x, u.y);
+        }
+        tmem_st16(ts + q / 2, p);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(x.bar(sh.ds_full));
+    }
+    if (ok && x.wait_warp(sh.out_full, 0)) {
+      tc_fence_after();
+      T* out = static_cast<T*>(a.gq) + (w.row0 + i) * a.gq_t + h * a.gq_h;
+      for (int q = wg * 32; q < a.D; q += 64) {  // the groups take 32 columns in turn
+        uint32_t o[32];
+        tmem_ld<32>(x.tmem + lanes + 384 + q, o);
+        tmem_wait_ld();
+        if (live) store32<F16>(out, o, a.scale, q, a.D);
+        __syncwarp();
+      }
+    }
+  }
+}
+
+template <bool F16, int PANELS>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                    const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mg,
+                    const __grid_constant__ AttnArgs a, const int64_t key_ctas) {
+  using T = typename std::conditional<F16, __half, __nv_bfloat16>::type;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Shared sh;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint8_t* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+  const bool keys = blockIdx.x < key_ctas;
+  const int64_t id = keys ? blockIdx.x : blockIdx.x - key_ctas;
+  const int heads = keys ? a.Hk : a.Hq, h = static_cast<int>(id % heads);
+
+  int64_t g0, g1;
+  gap_rows(a, &g0, &g1);
+  if (g0 > 0 || g1 < a.T) {
+    zero_rows(static_cast<T*>(a.gq), a.gq_t, a.gq_h, a.Hq, a.D, 0, g0);
+    zero_rows(static_cast<T*>(a.gq), a.gq_t, a.gq_h, a.Hq, a.D, g1, a.T);
+    zero_rows(static_cast<T*>(a.gk), a.gk_t, a.gk_h, a.Hk, a.D, 0, g0);
+    zero_rows(static_cast<T*>(a.gk), a.gk_t, a.gk_h, a.Hk, a.D, g1, a.T);
+    zero_rows(static_cast<T*>(a.gv), a.gv_t, a.gv_h, a.Hk, a.D, 0, g0);
+    zero_rows(static_cast<T*>(a.gv), a.gv_t, a.gv_h, a.Hk, a.D, g1, a.T);
+  }
+  if (warp == 0) {
+    const AttnTile w = find_tile(a, id / heads, kAttnTile, !keys);
+    if (lane == 0) sh.tile = w;
+  } else if (warp == kWarpMma) {
+    tmem_alloc(smem_addr(&sh.tmem), 512);
+    tmem_relinquish();
+  } else if (warp == kWarpLoad && lane == 0) {
+    sh.abort_flag = 0;
+    sh.dirty = 0;
+    uint64_t* one[] = {&sh.own_full, &sh.full[0], &sh.full[1], &sh.full[2], &sh.vfull[0], &sh.vfull[1], &sh.empty[0],
+                       &sh.empty[1], &sh.empty[2], &sh.vempty[0], &sh.vempty[1], &sh.diag, &sh.s_full[0], &sh.s_full[1],
+                       &sh.dp_full, &sh.out_full, &sh.drain};
+    for (uint64_t* b : one) mbar_init(smem_addr(b), 1);
+    mbar_init(smem_addr(&sh.ready[0]), 32);
+    mbar_init(smem_addr(&sh.ready[1]), 32);
+    mbar_init(smem_addr(&sh.clean), 32);
+    mbar_init(smem_addr(&sh.p_full), kCompute);
+    mbar_init(smem_addr(&sh.ds_full), kCompute);
+    fence_mbar_init();
+    prefetch_tensormap(&mq);
+    prefetch_tensormap(&mk);
+    prefetch_tensormap(&mv);
+    prefetch_tensormap(&mg);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (sh.tile.tile >= 0) {
+    const Ctx<F16, PANELS> x{a, sh, AttnGuard{&sh.abort_flag, a.status}, smem, smem_addr(smem), sh.tmem, warp, lane,
+                             sh.tile, (a.D + 15) / 16, (a.D + 63) / 64};
+    if (keys)
+      keys_cta<F16, PANELS, T>(x, &mq, &mk, &mv, &mg, h);
+    else
+      queries_cta<F16, PANELS, T>(x, &mq, &mk, &mv, &mg, h);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpMma) tmem_dealloc(sh.tmem, 512);
+}
+
+template <bool F16, int PANELS>
+cudaError_t launch_one(const AttnMaps& m, const AttnArgs& a, int sms, cudaStream_t s) {
+  static bool configured = false;
+  using T = typename std::conditional<F16, __half, __nv_bfloat16>::type;
+  auto kern = attn_bwd_kernel<F16, PANELS>;
+  if (!configured) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<PANELS>::kSmem);
+    if (e != cudaSuccess) return e;
+    configured = true;
+  }
+  const int width = a.D <= 64 ? 8 : 16;
+  const int64_t want = (a.T * a.Hq * width + 255) / 256, most = 32 * static_cast<int64_t>(sms);
+  attn_delta_kernel<T><<<static_cast<unsigned>(want < most ? want : most), 256, 0, s>>>(a);
+  if (cudaError_t e = cudaGetLastError()) return e;
+  const int64_t tiles = attn_tiles(a, kAttnTile), key_ctas = tiles * a.Hk;
+  kern<<<static_cast<unsigned>(key_ctas + tiles * a.Hq), kThreads, Geo<PANELS>::kSmem, s>>>(m.q, m.k, m.v, m.go, a, key_ctas);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attn_bwd(bool f16, const AttnMaps& m, const AttnArgs& a, int sms, cudaStream_t s) {
+  if (a.D <= 64) return f16 ? launch_one<true, 1>(m, a, sms, s) : launch_one<false, 1>(m, a, sms, s);
+  return f16 ? launch_one<true, 2>(m, a, sms, s) : launch_one<false, 2>(m, a, sms, s);
+}
+
+}  // namespace nf4
