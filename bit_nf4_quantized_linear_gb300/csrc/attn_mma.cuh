@@ -188,36 +188,60 @@ __device__ __forceinline__ bool nonfinite16(uint32_t w) {
   return (w & e) == e || ((w >> 16) & e) == e;
 }
 
-// One warp clears rows >= `rows` of an operand tile in shared memory and, with
-// `values`, replaces the infinities and NaNs of the others by zero; true (in every
-// lane) when there were any.  Ends with the fence that lets the tensor cores see the
-// stores.
+// `warps` warps (this one the `me`-th) clear rows >= `rows` of an operand tile in shared
+// memory and, with `values`, replace the infinities and NaNs of the others by zero; true
+// (in every lane of the warp) when it met any.  Ends with the fence that lets the tensor
+// cores see the stores.  The scan costs one fused multiply-add a word: x * 0 + acc stays
+// 0 until an x is not finite.
 template <bool F16, int PANELS>
-__device__ __forceinline__ bool clean_tile(uint8_t* tile, int rows, bool values) {
+__device__ __forceinline__ bool clean_tile(uint8_t* tile, int rows, bool values, int me, int warps) {
   const int lane = threadIdx.x & 31;
-  constexpr uint32_t e = F16 ? 0x7c00u : 0x7f80u;
-  bool any = false, wrote = false;
-  for (int i = lane; i < PANELS * kAttnTile * 8; i += 32) {  // 16-byte pieces; a row is 8 pieces of a panel
-    uint4* p = reinterpret_cast<uint4*>(tile) + i;
-    if (((i >> 3) & (kAttnTile - 1)) >= rows) {
-      *p = make_uint4(0u, 0u, 0u, 0u);
-      wrote = true;
-      continue;
-    }
-    if (!values) continue;
-    uint4 v = *p;
-    uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    if (nonfinite16<F16>(w[0]) || nonfinite16<F16>(w[1]) || nonfinite16<F16>(w[2]) || nonfinite16<F16>(w[3])) {
+  constexpr int kPieces = PANELS * kAttnTile * 8;  // of 16 bytes; a row is 8 of a panel
+  bool any = false;
+  if (rows < kAttnTile) {
+    const int dead = (kAttnTile - rows) * 8;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if ((w[k] & e) == e) w[k] &= 0xffff0000u;
-        if (((w[k] >> 16) & e) == e) w[k] &= 0x0000ffffu;
+    for (int p = 0; p < PANELS; ++p)
+      for (int i = me * 32 + lane; i < dead; i += warps * 32)
+        *reinterpret_cast<uint4*>(tile + p * kPanelBytes + rows * 128 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+  }
+  if (values) {
+    // the cleared rows may be read before or after: what they held does not matter
+    for (int i0 = me * 256 + lane; i0 < kPieces; i0 += warps * 256) {
+      uint4 v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = reinterpret_cast<const uint4*>(tile)[i0 + k * 32];
+      uint32_t acc = 0u;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (F16)
+            asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(w[e]), "r"(0u));
+          else
+            asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(w[e]), "r"(0u));
+        }
       }
-      *p = make_uint4(w[0], w[1], w[2], w[3]);
-      any = wrote = true;
+      if ((acc & 0x7fff7fffu) == 0u) continue;
+      for (int k = 0; k < 8; ++k) {
+        const int i = i0 + k * 32;
+        if (((i >> 3) & (kAttnTile - 1)) >= rows) continue;
+        uint32_t* w = reinterpret_cast<uint32_t*>(tile) + i * 4;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          constexpr uint32_t x = F16 ? 0x7c00u : 0x7f80u;
+          uint32_t u = w[e];
+          if (!nonfinite16<F16>(u)) continue;
+          if ((u & x) == x) u &= 0xffff0000u;
+          if (((u >> 16) & x) == x) u &= 0x0000ffffu;
+          w[e] = u;
+          any = true;
+        }
+      }
     }
   }
-  if (wrote) fence_proxy_async_smem();
+  fence_proxy_async_smem();
   return __any_sync(0xffffffffu, any);
 }
 

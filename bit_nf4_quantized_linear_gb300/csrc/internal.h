@@ -77,7 +77,7 @@ struct NormArgs {
   float scale, eps;
 };
 // CTAs of the backward, each with its own partial sums.
-int norm_bwd_ctas(int64_t T, int sms);
+int norm_bwd_ctas(int64_t T, int64_t H, int sms);
 cudaError_t launch_norm(bool backward, int dtype, const NormArgs& a, int sms, cudaStream_t s);
 
 // AdamW over many tensors.  The table travels in the kernel's parameters (no copy to

@@ -1404,7 +1404,7 @@ size_t nf4_workspace_size(int32_t op, int64_t M, int64_t N, int64_t K, int32_t E
   if (op == NF4_OP_NORM_RESIDUAL_BWD) {
     DevInfo dev;
     if (M <= 0 || N <= 0 || !current_device(&dev)) return 0;
-    return static_cast<size_t>(nf4::norm_bwd_ctas(M, dev.sms)) * 3 * N * sizeof(float);
+    return static_cast<size_t>(nf4::norm_bwd_ctas(M, N, dev.sms)) * 3 * N * sizeof(float);
   }
   if (op == NF4_OP_ATTENTION_BWD) {
     if (M <= 0 || N <= 0) return 0;

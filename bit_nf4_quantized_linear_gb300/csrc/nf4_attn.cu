@@ -14,7 +14,7 @@
 // operands' type; l sums the unrounded values.
 //
 // Roles: warps 0-3 and 4-7 the softmax of the two tiles, warp 8 issues every MMA, warp
-// 9 every TMA load, warp 10 cleans the value tiles that the causal mask cuts.  The MMA
+// 9 every TMA load, warps 10 and 11 clean the value tiles that the causal mask cuts.  The MMA
 // warp alternates between the tiles (P V of one, then its next S), so the tensor cores
 // work on one tile while the other's softmax runs.
 //
@@ -35,8 +35,8 @@
 namespace nf4 {
 namespace {
 
-constexpr int kThreads = 352;
-constexpr int kWarpMma = 8, kWarpLoad = 9, kWarpClean = 10;
+constexpr int kThreads = 384;
+constexpr int kWarpMma = 8, kWarpLoad = 9, kWarpClean = 10;  // the last one and the next
 constexpr float kRaise = 8.0f;  // log2 of the growth that makes the maximum move
 // fp16 keeps 11 bits down to 2^-14 only: P is held times 2^7, which with the growth above
 // still ends below 2^15.  The factor divides out of O and l.
@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_addr(&sh.p_full[i]), 128);
       mbar_init(smem_addr(&sh.o_full[i]), 1);
       mbar_init(smem_addr(&sh.diag[i]), 1);
-      mbar_init(smem_addr(&sh.clean[i]), 32);
+      mbar_init(smem_addr(&sh.clean[i]), 64);
     }
     mbar_init(smem_addr(&sh.drain), 1);
     for (int i = 0; i < G::kStages; ++i) {
@@ -165,13 +165,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int q = 0; q < G::kStages; ++q)
         if (issued & (1u << q)) attn_drain(smem_addr(&sh.full[q]), (par >> q) & 1u, guard);
     }
-  } else if (warp == kWarpClean) {
+  } else if (warp >= kWarpClean) {
     // The value tiles at the two diagonals (the last one of each query tile).
     for (int d = 0; d < (nb > 0 ? 2 : 1); ++d) {
       const int jt = i0 + d, st = (2 * jt + 1) % G::kStages;
       if (!__all_sync(0xffffffffu, attn_wait(smem_addr(&sh.diag[d]), 0, guard))) break;
       const int rows = min(kAttnTile, w.len - jt * kAttnTile);
-      if (clean_tile<F16, PANELS>(smem + G::kOffRing + st * G::kTileBytes, rows, true) && lane == 0) sh.dirty[d] = 1;
+      if (clean_tile<F16, PANELS>(smem + G::kOffRing + st * G::kTileBytes, rows, true, warp - kWarpClean, 2) && lane == 0)
+        sh.dirty[d] = 1;
       mbar_arrive(smem_addr(&sh.clean[d]));
     }
   } else if (warp == kWarpMma) {

@@ -38,7 +38,7 @@ namespace nf4 {
 namespace {
 
 constexpr int kThreads = 384;
-constexpr int kWarpMma = 8, kWarpLoad = 9, kWarpPrep = 10;
+constexpr int kWarpMma = 8, kWarpLoad = 9, kWarpPrep = 10;  // the last one and the next
 constexpr int kCompute = 256;  // threads of the two compute groups
 constexpr float kLog2e = 1.4426950408889634f;
 // fp16 keeps 11 bits down to 2^-14 only: the keys' CTAs hold P' times 2^14 (P' <= 1), and
@@ -189,25 +189,26 @@ __device__ __forceinline__ void keys_cta(const Ctx<F16, PANELS>& x, const CUtens
       attn_drain(x.bar(sh.own_full), 0, x.guard);
       for (int it = done < 2 ? 0 : done - 2; it < done; ++it) attn_drain(x.bar(sh.full[it & 1]), (it >> 1) & 1, x.guard);
     }
-  } else if (warp == kWarpPrep) {
+  } else if (warp >= kWarpPrep) {
     int g = 0, i = jt;
     for (int it = 0; it < n; ++it) {
       const int st = it & 1, rows = min(kAttnTile, w.len - i * kAttnTile);
       const int64_t at = static_cast<int64_t>(hk * group + g) * a.T + w.row0 + i * kAttnTile;
-      float l[4], d[4];
+      float l[2], d[2];  // two rows a lane, the second warp the upper half
+      const int r0 = (warp - kWarpPrep) * 64 + lane * 2;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int r = lane * 4 + e;
-        l[e] = lse2_of(a, at + r, r < rows) - (F16 ? kShift : 0.0f);
-        d[e] = r < rows ? a.delta[at + r] * (F16 ? kUnshift : 1.0f) : 0.0f;
+      for (int e = 0; e < 2; ++e) {
+        l[e] = lse2_of(a, at + r0 + e, r0 + e < rows) - (F16 ? kShift : 0.0f);
+        d[e] = r0 + e < rows ? a.delta[at + r0 + e] * (F16 ? kUnshift : 1.0f) : 0.0f;
       }
       if (!x.wait_warp(sh.empty[st], ((it >> 1) & 1) ^ 1)) break;
-      *reinterpret_cast<float4*>(&rs.lse2[st][lane * 4]) = make_float4(l[0], l[1], l[2], l[3]);
-      *reinterpret_cast<float4*>(&rs.delta[st][lane * 4]) = make_float4(d[0], d[1], d[2], d[3]);
+      *reinterpret_cast<float2*>(&rs.lse2[st][r0]) = make_float2(l[0], l[1]);
+      *reinterpret_cast<float2*>(&rs.delta[st][r0]) = make_float2(d[0], d[1]);
       if (!x.wait_warp(sh.full[st], (it >> 1) & 1)) break;
       if (i == jt || rows < kAttnTile) {
-        clean_tile<F16, PANELS>(x.smem + (2 + 2 * st) * Geo<PANELS>::kTileBytes, rows, i == jt);
-        if (clean_tile<F16, PANELS>(x.smem + (3 + 2 * st) * Geo<PANELS>::kTileBytes, rows, i == jt) && lane == 0) sh.dirty = 1;
+        clean_tile<F16, PANELS>(x.smem + (2 + 2 * st) * Geo<PANELS>::kTileBytes, rows, i == jt, warp - kWarpPrep, 2);
+        if (clean_tile<F16, PANELS>(x.smem + (3 + 2 * st) * Geo<PANELS>::kTileBytes, rows, i == jt, warp - kWarpPrep, 2) && lane == 0)
+          sh.dirty = 1;
       }
       mbar_arrive(x.bar(sh.ready[st]));
       if (++i == nt) {
@@ -400,9 +401,10 @@ __device__ __forceinline__ void queries_cta(const Ctx<F16, PANELS>& x, const CUt
       for (int j = nk < 3 ? 0 : nk - 3; j < nk; ++j) attn_drain(x.bar(sh.full[j % 3]), (j / 3) & 1, x.guard);
       for (int j = nv < 2 ? 0 : nv - 2; j < nv; ++j) attn_drain(x.bar(sh.vfull[j & 1]), (j >> 1) & 1, x.guard);
     }
-  } else if (warp == kWarpPrep) {
+  } else if (warp >= kWarpPrep) {
     if (x.wait_warp(sh.diag, 0)) {
-      clean_tile<F16, PANELS>(x.smem + (2 + it % 3) * Geo<PANELS>::kTileBytes, min(kAttnTile, w.len - it * kAttnTile), true);
+      clean_tile<F16, PANELS>(x.smem + (2 + it % 3) * Geo<PANELS>::kTileBytes, min(kAttnTile, w.len - it * kAttnTile), true,
+                              warp - kWarpPrep, 2);
       mbar_arrive(x.bar(sh.clean));
     }
   } else if (warp == kWarpMma) {
@@ -540,9 +542,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                        &sh.empty[1], &sh.empty[2], &sh.vempty[0], &sh.vempty[1], &sh.diag, &sh.s_full[0], &sh.s_full[1],
                        &sh.dp_full, &sh.out_full, &sh.drain};
     for (uint64_t* b : one) mbar_init(smem_addr(b), 1);
-    mbar_init(smem_addr(&sh.ready[0]), 32);
-    mbar_init(smem_addr(&sh.ready[1]), 32);
-    mbar_init(smem_addr(&sh.clean), 32);
+    mbar_init(smem_addr(&sh.ready[0]), 64);
+    mbar_init(smem_addr(&sh.ready[1]), 64);
+    mbar_init(smem_addr(&sh.clean), 64);
     mbar_init(smem_addr(&sh.p_full), kCompute);
     mbar_init(smem_addr(&sh.ds_full), kCompute);
     fence_mbar_init();

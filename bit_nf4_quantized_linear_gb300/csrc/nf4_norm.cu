@@ -20,6 +20,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "elem.cuh"
 #include "internal.h"
@@ -46,7 +47,8 @@ __device__ __forceinline__ float z_at(const NormArgs& a, int64_t t, int64_t c, f
   return r + a.scale * gate_at<T>(a, t, c) * n;
 }
 
-// Any width, stride and alignment: one CTA per row, one element per thread and step.
+// Any width: one CTA per row, one element per thread and step, each pass over the row from
+// memory.  For rows too wide for the registers of a CTA.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) norm_fwd_any_kernel(NormArgs a) {
   __shared__ float red[64];
@@ -78,7 +80,7 @@ __global__ void __launch_bounds__(kThreads) norm_fwd_any_kernel(NormArgs a) {
   }
 }
 
-// The backward for any width, stride and alignment.  part [CTAs][3][H].
+// The backward for any width.  part [CTAs][3][H].
 template <typename T>
 __global__ void __launch_bounds__(kThreads) norm_bwd_any_kernel(NormArgs a) {
   __shared__ float red[64];
@@ -137,37 +139,316 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_any_kernel(NormArgs a) {
   }
 }
 
-// out[v][c] = sum over p = 0 .. P-1 in order of part[p][v][c], v = gw_pre, gw_post, ggate.
-__global__ void __launch_bounds__(kThreads) norm_partials_kernel(NormArgs a, int P) {
-  float* outs[3] = {a.gw_pre, a.gw_post, a.gate_kind == NF4_GATE_CHANNEL ? static_cast<float*>(a.ggate) : nullptr};
-  float* out = outs[blockIdx.y];
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  if (!out || c >= a.H) return;
-  const float* p = a.part + blockIdx.y * a.H + c;
-  float s = 0.0f;
-  for (int i = 0; i < P; ++i) s += p[static_cast<int64_t>(i) * 3 * a.H];
-  out[c] = s;
+// ------------------------------------------------------- a row in registers --
+// Both directions are bound by HBM (about 12 fp32 operations a value forward, 40
+// backward), so the kernels below read each value once: a CTA holds a whole row, eight
+// values a thread, and every load of a row is in flight before its first sum.
+//   VEC values are one load: 16 bytes where the width, pitches and pointers allow, else
+//   single values, neighbours in neighbouring threads (thread i holds columns i, i + n, ...),
+//   which costs more instructions but the same memory traffic.
+
+constexpr int kHold = 8;                 // values of a row per thread
+constexpr int kMaxThreadsFwd = 1024;     // rows up to 8192 wide
+constexpr int kMaxThreadsBwd = 640;      // rows up to 5120 wide: 24 sums a thread in registers
+
+template <typename T, int VEC>
+struct Frag {
+  static constexpr int kVecs = kHold / VEC;
+  using Raw = typename std::conditional<VEC == 1, T, uint4>::type;
+  Raw v[kVecs];
+
+  // column of value i, for a CTA of n threads
+  static __device__ __forceinline__ int64_t column(int i, int n) {
+    return (static_cast<int64_t>(i / VEC) * n + threadIdx.x) * VEC + i % VEC;
+  }
+  __device__ __forceinline__ void load(const void* row, int64_t H, int n) {
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) {
+      const int64_t c = column(k * VEC, n);
+      if (c < H)
+        v[k] = *reinterpret_cast<const Raw*>(static_cast<const T*>(row) + c);
+      else
+        v[k] = Raw{};
+    }
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) v[k] = Raw{};
+  }
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (VEC == 1)
+      return to_f32(v[i]);
+    else
+      return to_f32(reinterpret_cast<const T*>(&v[i / VEC])[i % VEC]);
+  }
+  __device__ __forceinline__ void set(int i, float x) {
+    if constexpr (VEC == 1)
+      v[i] = from_f32<T>(x);
+    else
+      reinterpret_cast<T*>(&v[i / VEC])[i % VEC] = from_f32<T>(x);
+  }
+  __device__ __forceinline__ void store(void* row, int64_t H, int n) const {
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) {
+      const int64_t c = column(k * VEC, n);
+      if (c < H) *reinterpret_cast<Raw*>(static_cast<T*>(row) + c) = v[k];
+    }
+  }
+};
+
+// fp32 values (gains, channel gate) at the columns of Frag<T, VEC>.
+template <typename T, int VEC>
+__device__ __forceinline__ void load_gain(float (&g)[kHold], const float* p, int64_t H, int n, float none) {
+#pragma unroll
+  for (int k = 0; k < kHold / VEC; ++k) {
+    const int64_t c = Frag<T, VEC>::column(k * VEC, n);
+    if (!p || c >= H) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) g[k * VEC + e] = none;
+    } else if constexpr (VEC == 1) {
+      g[k] = p[c];
+    } else {
+#pragma unroll
+      for (int e = 0; e < VEC; e += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(p + c + e);
+        g[k * VEC + e] = f.x;
+        g[k * VEC + e + 1] = f.y;
+        g[k * VEC + e + 2] = f.z;
+        g[k * VEC + e + 3] = f.w;
+      }
+    }
+  }
 }
 
 template <typename T>
+__device__ __forceinline__ const void* row_of(const void* p, int64_t t, int64_t ld) {
+  return static_cast<const T*>(p) + t * ld;
+}
+template <typename T>
+__device__ __forceinline__ void* row_of(void* p, int64_t t, int64_t ld) {
+  return static_cast<T*>(p) + t * ld;
+}
+
+// One CTA per row.
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kMaxThreadsFwd) norm_fwd_kernel(const __grid_constant__ NormArgs a) {
+  __shared__ float red[64];
+  const int n = blockDim.x;
+  const int64_t t = blockIdx.x;
+  using F = Frag<T, VEC>;
+  F y, r, gt;
+  float wp[kHold], wn[kHold], gc[kHold];
+  y.load(row_of<T>(a.y, t, a.ld_y), a.H, n);
+  if (a.residual) r.load(row_of<T>(a.residual, t, a.ld_r), a.H, n); else r.clear();
+  if (a.gate_kind == NF4_GATE_TOKEN) gt.load(row_of<T>(a.gate, t, a.ld_gate), a.H, n);
+  load_gain<T, VEC>(wp, a.w_post, a.H, n, 1.0f);
+  load_gain<T, VEC>(gc, a.gate_kind == NF4_GATE_CHANNEL ? static_cast<const float*>(a.gate) : nullptr, a.H, n, 1.0f);
+  load_gain<T, VEC>(wn, a.w_pre, a.H, n, 1.0f);
+  const float inv_h = 1.0f / static_cast<float>(a.H);
+  float rstd_y = 1.0f;
+  if (a.w_post) {
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kHold; ++i) s = fmaf(y.at(i), y.at(i), s);
+    rstd_y = rsqrtf(block_sum(s, red) * inv_h + a.eps);
+  }
+  float z[kHold], s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kHold; ++i) {
+    const float g = a.gate_kind == NF4_GATE_TOKEN ? gt.at(i) : gc[i];
+    z[i] = r.at(i) + a.scale * g * (y.at(i) * rstd_y * wp[i]);
+    s = fmaf(z[i], z[i], s);
+  }
+  if (a.z) {
+    F o;
+#pragma unroll
+    for (int i = 0; i < kHold; ++i) o.set(i, z[i]);
+    o.store(row_of<T>(a.z, t, a.ld_z), a.H, n);
+  }
+  float rstd_z = 1.0f;
+  if (a.h || a.stats) rstd_z = rsqrtf(block_sum(s, red + 32) * inv_h + a.eps);
+  if (a.h) {
+    F o;
+#pragma unroll
+    for (int i = 0; i < kHold; ++i) o.set(i, z[i] * rstd_z * wn[i]);
+    o.store(row_of<T>(a.h, t, a.ld_h), a.H, n);
+  }
+  if (a.stats && threadIdx.x == 0) {
+    a.stats[t] = rstd_y;
+    a.stats[a.T + t] = rstd_z;
+  }
+}
+
+// The inputs of a row of the backward.
+template <typename T, int VEC>
+struct BwdRow {
+  Frag<T, VEC> y, r, gz, gh, gt;
+  float rstd_y, rstd_z;
+  __device__ __forceinline__ void load(const NormArgs& a, int64_t t, int n) {
+    y.load(row_of<T>(a.y, t, a.ld_y), a.H, n);
+    if (a.residual) r.load(row_of<T>(a.residual, t, a.ld_r), a.H, n); else r.clear();
+    if (a.gz) gz.load(row_of<T>(a.gz, t, a.ld_gz), a.H, n); else gz.clear();
+    if (a.gh) gh.load(row_of<T>(a.gh, t, a.ld_gh), a.H, n); else gh.clear();
+    if (a.gate_kind == NF4_GATE_TOKEN) gt.load(row_of<T>(a.gate, t, a.ld_gate), a.H, n); else gt.clear();
+    rstd_y = a.stats[t];
+    rstd_z = a.stats[a.T + t];
+  }
+};
+
+// CTAs walk the rows with the grid's stride, the next row's loads in flight while a row
+// is worked on; the sums over tokens stay in registers until the end.
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kMaxThreadsBwd) norm_bwd_kernel(const __grid_constant__ NormArgs a) {
+  __shared__ float red[64];
+  const int n = blockDim.x;
+  const bool token = a.gate_kind == NF4_GATE_TOKEN;
+  const float* gate = a.gate_kind == NF4_GATE_CHANNEL ? static_cast<const float*>(a.gate) : nullptr;
+  const float inv_h = 1.0f / static_cast<float>(a.H);
+  using F = Frag<T, VEC>;
+  float sum_pre[kHold], sum_post[kHold], sum_gate[kHold];
+#pragma unroll
+  for (int i = 0; i < kHold; ++i) sum_pre[i] = sum_post[i] = sum_gate[i] = 0.0f;
+  BwdRow<T, VEC> x;
+  x.load(a, blockIdx.x, n);
+  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+    BwdRow<T, VEC> next = x;
+    if (t + gridDim.x < a.T) next.load(a, t + gridDim.x, n);
+    float wn[kHold], wp[kHold], g[kHold];
+    load_gain<T, VEC>(wp, a.w_post, a.H, n, 1.0f);
+    load_gain<T, VEC>(g, gate, a.H, n, 1.0f);
+    load_gain<T, VEC>(wn, a.w_pre, a.H, n, 0.0f);
+    float zhat[kHold], s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kHold; ++i) {
+      if (token) g[i] = x.gt.at(i);
+      const float nn = x.y.at(i) * x.rstd_y * wp[i];
+      zhat[i] = (x.r.at(i) + a.scale * g[i] * nn) * x.rstd_z;
+      s = fmaf(zhat[i], x.gh.at(i) * wn[i], s);
+    }
+    const float mz = block_sum(s, red) * inv_h;
+    float b[kHold];
+    F gr, gg;
+    s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kHold; ++i) {
+      const float gh = x.gh.at(i);
+      const float dz = x.gz.at(i) + x.rstd_z * (gh * wn[i] - zhat[i] * mz);
+      const float yhat = x.y.at(i) * x.rstd_y;
+      const float u = a.scale * g[i] * dz, gate_grad = a.scale * dz * (yhat * wp[i]);
+      gr.set(i, dz);
+      gg.set(i, gate_grad);
+      sum_pre[i] = fmaf(gh, zhat[i], sum_pre[i]);
+      sum_post[i] = fmaf(u, yhat, sum_post[i]);
+      if (!token) sum_gate[i] += gate_grad;
+      b[i] = u * wp[i];
+      s = fmaf(yhat, b[i], s);
+    }
+    if (a.gr) gr.store(row_of<T>(a.gr, t, a.ld_gr), a.H, n);
+    if (token && a.ggate) gg.store(row_of<T>(a.ggate, t, a.ld_ggate), a.H, n);
+    // without w_post, n is y itself: no norm to go back through
+    const float my = a.w_post ? block_sum(s, red + 32) * inv_h : 0.0f;
+    if (!a.w_post) __syncthreads();
+    if (a.gy) {
+      F gy;
+#pragma unroll
+      for (int i = 0; i < kHold; ++i) gy.set(i, x.rstd_y * (b[i] - x.y.at(i) * x.rstd_y * my));
+      gy.store(row_of<T>(a.gy, t, a.ld_gy), a.H, n);
+    }
+    x = next;
+  }
+  if (!a.part) return;
+  float* part = a.part + static_cast<int64_t>(blockIdx.x) * 3 * a.H;
+#pragma unroll
+  for (int i = 0; i < kHold; ++i) {
+    const int64_t c = F::column(i, n);
+    if (c >= a.H) continue;
+    part[c] = sum_pre[i];
+    part[a.H + c] = sum_post[i];
+    part[2 * a.H + c] = sum_gate[i];
+  }
+}
+
+// out[v][c] = sum over p of part[p][v][c], v = gw_pre, gw_post, ggate.  A CTA takes 32
+// columns; its eight warps each add every eighth partial in order, then the warps' sums
+// are added in order.
+__global__ void __launch_bounds__(kThreads) norm_partials_kernel(const __grid_constant__ NormArgs a, int P) {
+  __shared__ float sums[kThreads / 32][32];
+  float* outs[3] = {a.gw_pre, a.gw_post, a.gate_kind == NF4_GATE_CHANNEL ? static_cast<float*>(a.ggate) : nullptr};
+  float* out = outs[blockIdx.y];
+  if (!out) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+  const float* p = a.part + blockIdx.y * a.H + c;
+  float s = 0.0f;
+  if (c < a.H) {
+#pragma unroll 8
+    for (int i = warp; i < P; i += kThreads / 32) s += p[static_cast<int64_t>(i) * 3 * a.H];
+  }
+  sums[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && c < a.H) {
+    for (int k = 1; k < kThreads / 32; ++k) s += sums[k][lane];
+    out[c] = s;
+  }
+}
+
+// Whether every row of the tensors in use can be read and written 16 bytes at a time.
+bool vectors(const NormArgs& a, size_t elem) {
+  const int64_t vec = static_cast<int64_t>(16 / elem);
+  if (a.H % vec != 0) return false;
+  const struct { const void* p; int64_t ld; } rows[] = {
+      {a.y, a.ld_y}, {a.residual, a.ld_r}, {a.gz, a.ld_gz}, {a.gh, a.ld_gh}, {a.z, a.ld_z}, {a.h, a.ld_h},
+      {a.gy, a.ld_gy}, {a.gr, a.ld_gr}, {a.gate_kind == NF4_GATE_TOKEN ? a.gate : nullptr, a.ld_gate},
+      {a.gate_kind == NF4_GATE_TOKEN ? a.ggate : nullptr, a.ld_ggate}};
+  for (const auto& r : rows)
+    if (r.p && (reinterpret_cast<uintptr_t>(r.p) % 16 != 0 || r.ld % vec != 0)) return false;
+  const void* gains[] = {a.w_post, a.w_pre, a.gate_kind == NF4_GATE_CHANNEL ? a.gate : nullptr};
+  for (const void* g : gains)
+    if (reinterpret_cast<uintptr_t>(g) % 16 != 0) return false;
+  return true;
+}
+
+int threads_of(int64_t H) { return static_cast<int>((H + kHold * 32 - 1) / (kHold * 32)) * 32; }
+
+template <typename T>
 cudaError_t launch_typed(bool backward, const NormArgs& a, int sms, cudaStream_t s) {
+  constexpr int kVec = 16 / sizeof(T);
+  const bool vec = vectors(a, sizeof(T));
   if (!backward) {
-    const int64_t grid = a.T < 8 * static_cast<int64_t>(sms) ? a.T : 8 * static_cast<int64_t>(sms);
-    norm_fwd_any_kernel<T><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(a);
+    if (a.H <= kMaxThreadsFwd * kHold) {
+      const unsigned grid = static_cast<unsigned>(a.T), n = threads_of(a.H);
+      if (vec)
+        norm_fwd_kernel<T, kVec><<<grid, n, 0, s>>>(a);
+      else
+        norm_fwd_kernel<T, 1><<<grid, n, 0, s>>>(a);
+    } else {
+      const int64_t grid = a.T < 8 * static_cast<int64_t>(sms) ? a.T : 8 * static_cast<int64_t>(sms);
+      norm_fwd_any_kernel<T><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(a);
+    }
     return cudaGetLastError();
   }
-  const int P = norm_bwd_ctas(a.T, sms);
-  norm_bwd_any_kernel<T><<<P, kThreads, 0, s>>>(a);
+  const int P = norm_bwd_ctas(a.T, a.H, sms);
+  if (a.H <= kMaxThreadsBwd * kHold) {
+    if (vec)
+      norm_bwd_kernel<T, kVec><<<P, threads_of(a.H), 0, s>>>(a);
+    else
+      norm_bwd_kernel<T, 1><<<P, threads_of(a.H), 0, s>>>(a);
+  } else {
+    norm_bwd_any_kernel<T><<<P, kThreads, 0, s>>>(a);
+  }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !a.part) return e;
-  norm_partials_kernel<<<dim3(static_cast<unsigned>((a.H + kThreads - 1) / kThreads), 3, 1), kThreads, 0, s>>>(a, P);
+  norm_partials_kernel<<<dim3(static_cast<unsigned>((a.H + 31) / 32), 3, 1), kThreads, 0, s>>>(a, P);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-int norm_bwd_ctas(int64_t T, int sms) {
-  return static_cast<int>(T < 2 * static_cast<int64_t>(sms) ? T : 2 * static_cast<int64_t>(sms));
+// Enough CTAs to fill the SMs' registers: one of 640 threads, or up to four narrow ones.
+int norm_bwd_ctas(int64_t T, int64_t H, int sms) {
+  const int n = threads_of(H), k = n >= 512 ? 1 : n >= 256 ? 2 : 4;
+  const int64_t most = static_cast<int64_t>(H > kMaxThreadsBwd * kHold ? 2 : k) * sms;
+  return static_cast<int>(T < most ? T : most);
 }
 
 cudaError_t launch_norm(bool backward, int dtype, const NormArgs& a, int sms, cudaStream_t s) {
