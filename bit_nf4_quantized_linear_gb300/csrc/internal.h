@@ -75,6 +75,7 @@ struct NormArgs {
   int64_t T, H;
   int gate_kind;
   float scale, eps;
+  int* status;
 };
 // CTAs of the backward, each with its own partial sums.
 int norm_bwd_ctas(int64_t T, int64_t H, int sms);
@@ -90,6 +91,7 @@ struct AdamTensor {
   void *m, *v;
   float *m_absmax, *v_absmax;
   int64_t n;
+  int64_t vec;  // set by the launcher: 16-byte accesses to every array
 };
 struct AdamTable {
   AdamTensor t[kAdamMaxTensors];
@@ -102,14 +104,15 @@ struct AdamArgs {
   const float* grad_scale;
   const float *levels_m, *levels_v;
 };
-cudaError_t launch_adamw(int dtype, int bits, const AdamTable& tab, const AdamArgs& a, int sms, cudaStream_t s);
+cudaError_t launch_adamw(int dtype, int bits, AdamTable& tab, const AdamArgs& a, int sms, cudaStream_t s);
 struct AdamValuesArgs {
   const uint8_t *m, *v;
   const float *m_absmax, *v_absmax, *levels_m, *levels_v;
   float *out_m, *out_v;
   int64_t n;
+  int vec;  // set by the launcher
 };
-cudaError_t launch_adamw_values(const AdamValuesArgs& a, int sms, cudaStream_t s);
+cudaError_t launch_adamw_values(AdamValuesArgs a, int sms, cudaStream_t s);
 
 // Causal attention over packed sequences and its backward (nf4_attention_fwd / _bwd):
 // tensors [T, heads, D] with token and head strides in elements, unit stride within

@@ -1039,6 +1039,7 @@ nf4_status nf4_norm_residual_fwd(const nf4_norm_residual* d, void* z, int64_t ld
   a.stats = stats;
   DevInfo dev;
   if (!current_device(&dev)) return cuda_fail(cudaGetLastError(), "device query");
+  a.status = dev.status;
   cudaError_t le = nf4::launch_norm(false, d->dtype, a, dev.sms, static_cast<cudaStream_t>(stream));
   if (le != cudaSuccess) return cuda_fail(le, "kernel launch");
   count(NF4_PATH_NORM_RESIDUAL);
@@ -1092,6 +1093,7 @@ nf4_status nf4_norm_residual_bwd(const nf4_norm_residual* d, const float* stats,
   a.ld_ggate = ld_ggate;
   a.gw_post = gw_post;
   a.gw_pre = gw_pre;
+  a.status = dev.status;
   cudaError_t le = nf4::launch_norm(true, d->dtype, a, dev.sms, st);
   if (le != cudaSuccess) return cuda_fail(le, "kernel launch");
   count(NF4_PATH_NORM_RESIDUAL);
@@ -1221,7 +1223,7 @@ nf4_status nf4_adamw_step(const nf4_adamw_tensor* tensors, int32_t count_, int32
     for (; i0 < count_ && tab.count < nf4::kAdamMaxTensors; ++i0) {
       const nf4_adamw_tensor& t = tensors[i0];
       if (t.n == 0) continue;
-      tab.t[tab.count] = {t.param, t.grad, t.m, t.v, t.m_absmax, t.v_absmax, t.n};
+      tab.t[tab.count] = {t.param, t.grad, t.m, t.v, t.m_absmax, t.v_absmax, t.n, 0};
       tab.blk0[tab.count + 1] = tab.blk0[tab.count] + (t.n + NF4_ADAMW_BLOCK - 1) / NF4_ADAMW_BLOCK;
       ++tab.count;
     }
@@ -1242,7 +1244,7 @@ nf4_status nf4_adamw_state_values(const uint8_t* m, const uint8_t* v, const floa
   if (!aligned_to(out_m, 4) || !aligned_to(out_v, 4)) return NF4_ERR_ALIGNMENT;
   DevInfo dev;
   if (!current_device(&dev)) return cuda_fail(cudaGetLastError(), "device query");
-  const nf4::AdamValuesArgs a{m, v, m_absmax, v_absmax, levels_m, levels_v, out_m, out_v, n};
+  const nf4::AdamValuesArgs a{m, v, m_absmax, v_absmax, levels_m, levels_v, out_m, out_v, n, 0};
   cudaError_t le = nf4::launch_adamw_values(a, dev.sms, static_cast<cudaStream_t>(stream));
   if (le != cudaSuccess) return cuda_fail(le, "kernel launch");
   count(NF4_PATH_ADAMW);

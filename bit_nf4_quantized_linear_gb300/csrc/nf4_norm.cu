@@ -24,6 +24,7 @@
 
 #include "elem.cuh"
 #include "internal.h"
+#include "sm100_ptx.cuh"
 
 namespace nf4 {
 namespace {
@@ -295,28 +296,29 @@ struct BwdRow {
   }
 };
 
-// CTAs walk the rows with the grid's stride, the next row's loads in flight while a row
-// is worked on; the sums over tokens stay in registers until the end.
-template <typename T, int VEC>
-__global__ void __launch_bounds__(kMaxThreadsBwd) norm_bwd_kernel(const __grid_constant__ NormArgs a) {
-  __shared__ float red[64];
-  const int n = blockDim.x;
-  const bool token = a.gate_kind == NF4_GATE_TOKEN;
-  const float* gate = a.gate_kind == NF4_GATE_CHANNEL ? static_cast<const float*>(a.gate) : nullptr;
-  const float inv_h = 1.0f / static_cast<float>(a.H);
-  using F = Frag<T, VEC>;
-  float sum_pre[kHold], sum_post[kHold], sum_gate[kHold];
+// The sums over tokens of a CTA's rows, at the thread's columns.
+struct Sums {
+  float pre[kHold], post[kHold], gate[kHold];
+  __device__ __forceinline__ void clear() {
 #pragma unroll
-  for (int i = 0; i < kHold; ++i) sum_pre[i] = sum_post[i] = sum_gate[i] = 0.0f;
-  BwdRow<T, VEC> x;
-  x.load(a, blockIdx.x, n);
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-    BwdRow<T, VEC> next = x;
-    if (t + gridDim.x < a.T) next.load(a, t + gridDim.x, n);
-    float wn[kHold], wp[kHold], g[kHold];
-    load_gain<T, VEC>(wp, a.w_post, a.H, n, 1.0f);
-    load_gain<T, VEC>(g, gate, a.H, n, 1.0f);
-    load_gain<T, VEC>(wn, a.w_pre, a.H, n, 0.0f);
+    for (int i = 0; i < kHold; ++i) pre[i] = post[i] = gate[i] = 0.0f;
+  }
+};
+
+// One row of the backward.  gains(k, g) fetches w_post, the channel gate or w_pre (k = 0,
+// 1, 2) at this thread's columns; it is asked twice, to leave the registers to the sums.
+// `red` [64]: CTA barriers separate its reads from the next call's writes.  Every thread
+// has its inputs in registers when after_first() runs.
+template <typename T, int VEC, typename Gains, typename AfterFirst>
+__device__ __forceinline__ void bwd_row(const NormArgs& a, const BwdRow<T, VEC>& x, int64_t t, int n, float inv_h,
+                                        Gains gains, float* red, Sums& sum, AfterFirst after_first) {
+  using F = Frag<T, VEC>;
+  const bool token = a.gate_kind == NF4_GATE_TOKEN;
+  {
+    float g[kHold], wp[kHold], wn[kHold];
+    gains(0, wp);
+    gains(1, g);
+    gains(2, wn);
     float zhat[kHold], s = 0.0f;
 #pragma unroll
     for (int i = 0; i < kHold; ++i) {
@@ -326,6 +328,10 @@ __global__ void __launch_bounds__(kMaxThreadsBwd) norm_bwd_kernel(const __grid_c
       s = fmaf(zhat[i], x.gh.at(i) * wn[i], s);
     }
     const float mz = block_sum(s, red) * inv_h;
+    after_first();
+    gains(0, wp);
+    gains(1, g);
+    gains(2, wn);
     float b[kHold];
     F gr, gg;
     s = 0.0f;
@@ -334,12 +340,13 @@ __global__ void __launch_bounds__(kMaxThreadsBwd) norm_bwd_kernel(const __grid_c
       const float gh = x.gh.at(i);
       const float dz = x.gz.at(i) + x.rstd_z * (gh * wn[i] - zhat[i] * mz);
       const float yhat = x.y.at(i) * x.rstd_y;
+      if (token) g[i] = x.gt.at(i);
       const float u = a.scale * g[i] * dz, gate_grad = a.scale * dz * (yhat * wp[i]);
       gr.set(i, dz);
       gg.set(i, gate_grad);
-      sum_pre[i] = fmaf(gh, zhat[i], sum_pre[i]);
-      sum_post[i] = fmaf(u, yhat, sum_post[i]);
-      if (!token) sum_gate[i] += gate_grad;
+      sum.pre[i] = fmaf(gh, zhat[i], sum.pre[i]);
+      sum.post[i] = fmaf(u, yhat, sum.post[i]);
+      if (!token) sum.gate[i] += gate_grad;
       b[i] = u * wp[i];
       s = fmaf(yhat, b[i], s);
     }
@@ -354,18 +361,252 @@ __global__ void __launch_bounds__(kMaxThreadsBwd) norm_bwd_kernel(const __grid_c
       for (int i = 0; i < kHold; ++i) gy.set(i, x.rstd_y * (b[i] - x.y.at(i) * x.rstd_y * my));
       gy.store(row_of<T>(a.gy, t, a.ld_gy), a.H, n);
     }
-    x = next;
   }
+}
+
+template <typename T, int VEC>
+__device__ __forceinline__ void store_sums(const NormArgs& a, const Sums& sum, int n) {
   if (!a.part) return;
   float* part = a.part + static_cast<int64_t>(blockIdx.x) * 3 * a.H;
 #pragma unroll
   for (int i = 0; i < kHold; ++i) {
-    const int64_t c = F::column(i, n);
+    const int64_t c = Frag<T, VEC>::column(i, n);
     if (c >= a.H) continue;
-    part[c] = sum_pre[i];
-    part[a.H + c] = sum_post[i];
-    part[2 * a.H + c] = sum_gate[i];
+    part[c] = sum.pre[i];
+    part[a.H + c] = sum.post[i];
+    part[2 * a.H + c] = sum.gate[i];
   }
+}
+
+// CTAs walk the rows with the grid's stride; single-value loads.
+template <typename T>
+__global__ void __launch_bounds__(kMaxThreadsBwd) norm_bwd_kernel(const __grid_constant__ NormArgs a) {
+  __shared__ float red[64];
+  const int n = blockDim.x;
+  const float inv_h = 1.0f / static_cast<float>(a.H);
+  Sums sum;
+  sum.clear();
+  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+    BwdRow<T, 1> x;
+    x.load(a, t, n);
+    auto gains = [&](int k, float (&g)[kHold]) {
+      const float* p = k == 0 ? a.w_post : k == 2 ? a.w_pre
+                       : a.gate_kind == NF4_GATE_CHANNEL ? static_cast<const float*>(a.gate) : nullptr;
+      load_gain<T, 1>(g, p, a.H, n, k == 2 ? 0.0f : 1.0f);
+    };
+    bwd_row<T, 1>(a, x, t, n, inv_h, gains, red, sum, [] {});
+  }
+  store_sums<T, 1>(a, sum, n);
+}
+
+// ------------------------------------------------------------ rows by bulk copy --
+// Where rows are whole 16-byte pieces, one thread streams the CTA's rows into a ring in
+// shared memory by bulk copies, several rows ahead of the arithmetic, so that the loads
+// never wait for a row's two sums; the gains stay in shared memory for all rows.
+
+constexpr int kMaxStages = 4;
+constexpr uint64_t kTimeoutNs = 2000000000;
+
+struct Ring {
+  uint64_t full[kMaxStages];
+  int gave_up;
+};
+
+// Bounded: after a timeout (recorded) every later wait returns at once, and the kernel
+// runs out on whatever the buffers hold.
+static __device__ __noinline__ void ring_wait_slow(Ring& r, uint32_t bar, uint32_t parity, int* status) {
+  volatile int* gave_up = &r.gave_up;
+  const uint64_t t0 = nf4ptx::globaltimer_ns();
+  while (!nf4ptx::mbar_try_wait_sleep(bar, parity, 20000)) {
+    if (*gave_up) return;
+    if (nf4ptx::globaltimer_ns() - t0 > kTimeoutNs) {
+      *gave_up = 1;
+      if (status) atomicCAS(status, 0, kStatusTimeout);
+      return;
+    }
+  }
+}
+
+// The shared memory of a ring CTA: gains [3][H] fp32, then the stages.
+template <typename T, bool BWD>
+struct RowRing {
+  const NormArgs& a;
+  Ring& ring;
+  uint8_t* gains;
+  uint8_t* stage0;
+  uint32_t row_bytes, stage_bytes;
+  int stages, arrays;
+
+  __device__ __forceinline__ RowRing(const NormArgs& a_, Ring& r, uint8_t* smem, int stages_)
+      : a(a_), ring(r), gains(smem), stages(stages_) {
+    row_bytes = static_cast<uint32_t>(a.H * sizeof(T));
+    arrays = 1 + (a.residual != nullptr) + (a.gate_kind == NF4_GATE_TOKEN) + (BWD && a.gz) + (BWD && a.gh);
+    stage_bytes = arrays * row_bytes;
+    stage0 = smem + 3 * a.H * sizeof(float);
+  }
+  // Thread 0: the copies of row t into a stage.
+  __device__ __forceinline__ void issue(int st, int64_t t) const {
+    const uint32_t bar = nf4ptx::smem_addr(&ring.full[st]);
+    nf4ptx::mbar_arrive_expect_tx(bar, stage_bytes);
+    uint32_t to = nf4ptx::smem_addr(stage0) + st * stage_bytes;
+    auto copy = [&](const void* p, int64_t ld) {
+      nf4ptx::bulk_load_g2s(to, row_of<T>(p, t, ld), row_bytes, bar);
+      to += row_bytes;
+    };
+    copy(a.y, a.ld_y);
+    if (a.residual) copy(a.residual, a.ld_r);
+    if (a.gate_kind == NF4_GATE_TOKEN) copy(a.gate, a.ld_gate);
+    if (BWD && a.gz) copy(a.gz, a.ld_gz);
+    if (BWD && a.gh) copy(a.gh, a.ld_gh);
+  }
+  __device__ __forceinline__ void wait(int st, uint32_t parity, int* status) const {
+    const uint32_t bar = nf4ptx::smem_addr(&ring.full[st]);
+    if (!nf4ptx::mbar_test_wait(bar, parity)) ring_wait_slow(ring, bar, parity, status);
+  }
+  template <int VEC>
+  __device__ __forceinline__ void gain(float (&g)[kHold], int which, bool have, float none, int n) const {
+    load_gain<T, VEC>(g, have ? reinterpret_cast<const float*>(gains) + which * a.H : nullptr, a.H, n, none);
+  }
+};
+
+// Set-up common to both directions; returns after the CTA barrier.
+template <typename T, bool BWD>
+__device__ __forceinline__ void ring_start(const RowRing<T, BWD>& rr, int n) {
+  const NormArgs& a = rr.a;
+  if (threadIdx.x == 0) {
+    rr.ring.gave_up = 0;
+    for (int i = 0; i < rr.stages; ++i) nf4ptx::mbar_init(nf4ptx::smem_addr(&rr.ring.full[i]), 1);
+    nf4ptx::fence_mbar_init();
+    for (int i = 0; i < rr.stages; ++i) {
+      const int64_t t = blockIdx.x + static_cast<int64_t>(i) * gridDim.x;
+      if (t < a.T) rr.issue(i, t);
+    }
+  }
+  float* g = reinterpret_cast<float*>(rr.gains);
+  const float* src[3] = {a.w_post, a.gate_kind == NF4_GATE_CHANNEL ? static_cast<const float*>(a.gate) : nullptr, a.w_pre};
+#pragma unroll
+  for (int k = 0; k < 3; ++k)
+    if (src[k])
+      for (int64_t c = threadIdx.x * 4; c < a.H; c += n * 4)
+        *reinterpret_cast<float4*>(g + k * a.H + c) = *reinterpret_cast<const float4*>(src[k] + c);
+  __syncthreads();
+}
+
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kMaxThreadsFwd) norm_fwd_ring_kernel(const __grid_constant__ NormArgs a, int stages) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float red[64];
+  __shared__ Ring ring;
+  const int n = blockDim.x;
+  const RowRing<T, false> rr(a, ring, smem, stages);
+  ring_start(rr, n);
+  using F = Frag<T, VEC>;
+  const float inv_h = 1.0f / static_cast<float>(a.H);
+  int st = 0;
+  uint32_t ph = 0;
+  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+    rr.wait(st, ph, a.status);
+    const uint8_t* p = rr.stage0 + st * rr.stage_bytes;
+    F y, r, gt;
+    y.load(p, a.H, n);
+    p += rr.row_bytes;
+    if (a.residual) {
+      r.load(p, a.H, n);
+      p += rr.row_bytes;
+    } else {
+      r.clear();
+    }
+    if (a.gate_kind == NF4_GATE_TOKEN) gt.load(p, a.H, n);
+    float rstd_y = 1.0f;
+    if (a.w_post) {
+      float s = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kHold; ++i) s = fmaf(y.at(i), y.at(i), s);
+      rstd_y = rsqrtf(block_sum(s, red) * inv_h + a.eps);
+    }
+    float g[kHold], z[kHold], s = 0.0f;
+    rr.template gain<VEC>(z, 0, a.w_post != nullptr, 1.0f, n);
+    rr.template gain<VEC>(g, 1, a.gate_kind == NF4_GATE_CHANNEL, 1.0f, n);
+#pragma unroll
+    for (int i = 0; i < kHold; ++i) {
+      z[i] = r.at(i) + a.scale * (a.gate_kind == NF4_GATE_TOKEN ? gt.at(i) : g[i]) * (y.at(i) * rstd_y * z[i]);
+      s = fmaf(z[i], z[i], s);
+    }
+    if (a.z) {
+      F o;
+#pragma unroll
+      for (int i = 0; i < kHold; ++i) o.set(i, z[i]);
+      o.store(row_of<T>(a.z, t, a.ld_z), a.H, n);
+    }
+    const float rstd_z = rsqrtf(block_sum(s, red + 32) * inv_h + a.eps);
+    // every thread has read its part of the stage
+    if (threadIdx.x == 0 && t + static_cast<int64_t>(stages) * gridDim.x < a.T)
+      rr.issue(st, t + static_cast<int64_t>(stages) * gridDim.x);
+    if (a.h) {
+      F o;
+      rr.template gain<VEC>(g, 2, true, 1.0f, n);
+#pragma unroll
+      for (int i = 0; i < kHold; ++i) o.set(i, z[i] * rstd_z * g[i]);
+      o.store(row_of<T>(a.h, t, a.ld_h), a.H, n);
+    }
+    if (a.stats && threadIdx.x == 0) {
+      a.stats[t] = rstd_y;
+      a.stats[a.T + t] = rstd_z;
+    }
+    if (!a.w_post) __syncthreads();  // red is read before the next row's sum writes it
+    if (++st == stages) {
+      st = 0;
+      ph ^= 1u;
+    }
+  }
+}
+
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kMaxThreadsBwd) norm_bwd_ring_kernel(const __grid_constant__ NormArgs a, int stages) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float red[64];
+  __shared__ Ring ring;
+  const int n = blockDim.x;
+  const RowRing<T, true> rr(a, ring, smem, stages);
+  ring_start(rr, n);
+  const float inv_h = 1.0f / static_cast<float>(a.H);
+  Sums sum;
+  sum.clear();
+  int st = 0;
+  uint32_t ph = 0;
+  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+    BwdRow<T, VEC> x;
+    x.rstd_y = a.stats[t];
+    x.rstd_z = a.stats[a.T + t];
+    rr.wait(st, ph, a.status);
+    const uint8_t* p = rr.stage0 + st * rr.stage_bytes;
+    auto take = [&](Frag<T, VEC>& f, bool have) {
+      if (have) {
+        f.load(p, a.H, n);
+        p += rr.row_bytes;
+      } else {
+        f.clear();
+      }
+    };
+    take(x.y, true);
+    take(x.r, a.residual != nullptr);
+    take(x.gt, a.gate_kind == NF4_GATE_TOKEN);
+    take(x.gz, a.gz != nullptr);
+    take(x.gh, a.gh != nullptr);
+    auto gains = [&](int k, float (&g)[kHold]) {
+      const bool have = k == 0 ? a.w_post != nullptr : k == 2 ? a.w_pre != nullptr : a.gate_kind == NF4_GATE_CHANNEL;
+      rr.template gain<VEC>(g, k, have, k == 2 ? 0.0f : 1.0f, n);
+    };
+    bwd_row<T, VEC>(a, x, t, n, inv_h, gains, red, sum, [&] {
+      if (threadIdx.x == 0 && t + static_cast<int64_t>(stages) * gridDim.x < a.T)
+        rr.issue(st, t + static_cast<int64_t>(stages) * gridDim.x);
+    });
+    if (++st == stages) {
+      st = 0;
+      ph ^= 1u;
+    }
+  }
+  store_sums<T, VEC>(a, sum, n);
 }
 
 // out[v][c] = sum over p of part[p][v][c], v = gw_pre, gw_post, ggate.  A CTA takes 32
@@ -410,33 +651,67 @@ bool vectors(const NormArgs& a, size_t elem) {
 
 int threads_of(int64_t H) { return static_cast<int>((H + kHold * 32 - 1) / (kHold * 32)) * 32; }
 
+// Ring CTAs on an SM: narrow rows want several, whose sums overlap.
+int ring_ctas(int64_t H, bool backward) {
+  const int n = threads_of(H), k = (backward ? kMaxThreadsBwd : kMaxThreadsFwd) / n;
+  return k > 8 ? 8 : k;
+}
+
+// Shared memory of one: gains and as many stages as its share of the SM holds.
+int ring_smem(const NormArgs& a, size_t elem, bool backward, int* stages) {
+  const int arrays = 1 + (a.residual != nullptr) + (a.gate_kind == NF4_GATE_TOKEN) + (backward && a.gz) + (backward && a.gh);
+  const int64_t gains = 12 * a.H, stage = static_cast<int64_t>(arrays) * a.H * static_cast<int64_t>(elem);
+  const int64_t share = 220 * 1024 / ring_ctas(a.H, backward) - 2048;
+  int64_t k = (share - gains) / stage;
+  *stages = static_cast<int>(k > kMaxStages ? kMaxStages : k);
+  return static_cast<int>(gains + *stages * stage);
+}
+
+template <typename K>
+cudaError_t ring_launch(K kern, unsigned grid, int n, int smem, const NormArgs& a, int stages, cudaStream_t s) {
+  if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) return e;
+  kern<<<grid, n, smem, s>>>(a, stages);
+  return cudaGetLastError();
+}
+
 template <typename T>
 cudaError_t launch_typed(bool backward, const NormArgs& a, int sms, cudaStream_t s) {
   constexpr int kVec = 16 / sizeof(T);
   const bool vec = vectors(a, sizeof(T));
+  const int n = threads_of(a.H);
+  int stages = 0;
   if (!backward) {
-    if (a.H <= kMaxThreadsFwd * kHold) {
-      const unsigned grid = static_cast<unsigned>(a.T), n = threads_of(a.H);
-      if (vec)
-        norm_fwd_kernel<T, kVec><<<grid, n, 0, s>>>(a);
-      else
-        norm_fwd_kernel<T, 1><<<grid, n, 0, s>>>(a);
-    } else {
-      const int64_t grid = a.T < 8 * static_cast<int64_t>(sms) ? a.T : 8 * static_cast<int64_t>(sms);
-      norm_fwd_any_kernel<T><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(a);
+    const int64_t most = static_cast<int64_t>(sms) * (a.H <= kMaxThreadsFwd * kHold ? ring_ctas(a.H, false) : 8);
+    if (a.H > kMaxThreadsFwd * kHold) {
+      norm_fwd_any_kernel<T><<<static_cast<unsigned>(a.T < most ? a.T : most), kThreads, 0, s>>>(a);
+      return cudaGetLastError();
     }
-    return cudaGetLastError();
+    if (!vec) {
+      norm_fwd_kernel<T, 1><<<static_cast<unsigned>(a.T), n, 0, s>>>(a);
+      return cudaGetLastError();
+    }
+    // a row for each CTA at most, or rows too wide for two stages: no ring to fill
+    const int smem = ring_smem(a, sizeof(T), false, &stages);
+    if (a.T <= most || stages < 2) {
+      norm_fwd_kernel<T, kVec><<<static_cast<unsigned>(a.T), n, 0, s>>>(a);
+      return cudaGetLastError();
+    }
+    return ring_launch(norm_fwd_ring_kernel<T, kVec>, static_cast<unsigned>(most), n, smem, a, stages, s);
   }
   const int P = norm_bwd_ctas(a.T, a.H, sms);
-  if (a.H <= kMaxThreadsBwd * kHold) {
-    if (vec)
-      norm_bwd_kernel<T, kVec><<<P, threads_of(a.H), 0, s>>>(a);
-    else
-      norm_bwd_kernel<T, 1><<<P, threads_of(a.H), 0, s>>>(a);
-  } else {
+  cudaError_t e = cudaSuccess;
+  if (a.H > kMaxThreadsBwd * kHold) {
     norm_bwd_any_kernel<T><<<P, kThreads, 0, s>>>(a);
+    e = cudaGetLastError();
+  } else {
+    const int smem = vec ? ring_smem(a, sizeof(T), true, &stages) : 0;
+    if (stages >= 1) {
+      e = ring_launch(norm_bwd_ring_kernel<T, kVec>, static_cast<unsigned>(P), n, smem, a, stages, s);
+    } else {
+      norm_bwd_kernel<T><<<P, n, 0, s>>>(a);
+      e = cudaGetLastError();
+    }
   }
-  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !a.part) return e;
   norm_partials_kernel<<<dim3(static_cast<unsigned>((a.H + 31) / 32), 3, 1), kThreads, 0, s>>>(a, P);
   return cudaGetLastError();
@@ -444,10 +719,9 @@ cudaError_t launch_typed(bool backward, const NormArgs& a, int sms, cudaStream_t
 
 }  // namespace
 
-// Enough CTAs to fill the SMs' registers: one of 640 threads, or up to four narrow ones.
+// CTAs of the backward, each with partial sums of its own.
 int norm_bwd_ctas(int64_t T, int64_t H, int sms) {
-  const int n = threads_of(H), k = n >= 512 ? 1 : n >= 256 ? 2 : 4;
-  const int64_t most = static_cast<int64_t>(H > kMaxThreadsBwd * kHold ? 2 : k) * sms;
+  const int64_t most = static_cast<int64_t>(H > kMaxThreadsBwd * kHold ? 2 : ring_ctas(H, true)) * sms;
   return static_cast<int>(T < most ? T : most);
 }
 
