@@ -9,6 +9,7 @@
 #include <cstdint>
 
 #include "attn_common.cuh"
+#include "elem.cuh"
 #include "sm100_ptx.cuh"
 
 namespace nf4 {
@@ -26,9 +27,10 @@ struct AttnGuard {
 };
 
 static __device__ __noinline__ bool attn_wait_slow(uint32_t bar, uint32_t parity, const AttnGuard& g) {
+  if (mbar_try_wait_sleep(bar, parity, 100000)) return true;
   const uint64_t t0 = globaltimer_ns();
   while (true) {
-    if (mbar_try_wait_sleep(bar, parity, 20000)) return true;
+    if (mbar_try_wait_sleep(bar, parity, 100000)) return true;
     if (*g.abort_flag) return false;
     if (globaltimer_ns() - t0 > kAttnTimeoutNs) {
       *g.abort_flag = 1;
@@ -78,13 +80,42 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
 
 // Operand tile [128 rows][64-column panels], 128-byte swizzled rows.  Rows are M / N
 // and columns the contraction (K-major): 16 columns further is 32 bytes, the next
-// panel kPanelBytes.
-__device__ __forceinline__ uint64_t desc_k_major(uint32_t saddr, int step) {
-  return smem_desc_sw128(saddr + (step >> 2) * kPanelBytes + (step & 3) * 32, 16, 1024);
+// panel kPanelBytes.  Or columns are M / N and rows the contraction (MN-major): 16 rows
+// further is 2 KB.  Steps only change the descriptor's address field (in 16-byte units),
+// so one thread issues an MMA every few instructions.
+__device__ __forceinline__ uint64_t desc_k_major(uint32_t saddr) { return smem_desc_sw128(saddr, 16, 1024); }
+__device__ __forceinline__ uint64_t desc_mn_major(uint32_t saddr) { return smem_desc_sw128(saddr, kPanelBytes, 1024); }
+
+// D = A B^T over the head's columns in steps of 16, both operands in shared memory.  With
+// FULL the panels are full: a fixed number of steps, unrolled.  Else `ksteps` steps in a
+// rolled loop; no MMA stands under a condition of its own (unrolled MMAs guarded by
+// `k < ksteps` came out wrong).
+template <bool FULL, int PANELS>
+__device__ __forceinline__ void mma_over_columns(uint32_t d, uint32_t a_tile, uint32_t b_tile, uint32_t idesc, int ksteps) {
+  uint64_t da = desc_k_major(a_tile), db = desc_k_major(b_tile);
+  if constexpr (FULL) {
+#pragma unroll
+    for (int k = 0; k < 4 * PANELS; ++k) {
+      const uint64_t off = (k >> 2) * (kPanelBytes >> 4) + (k & 3) * 2;
+      mma_bf16_ss(d, da + off, db + off, idesc, k > 0);
+    }
+  } else {
+#pragma unroll 1
+    for (int k = 0; k < ksteps; ++k) {
+      const uint64_t off = (k >> 2) * (kPanelBytes >> 4) + (k & 3) * 2;
+      mma_bf16_ss(d, da + off, db + off, idesc, k > 0);
+    }
+  }
 }
-// Columns are M / N and rows the contraction (MN-major): 16 rows further is 2 KB.
-__device__ __forceinline__ uint64_t desc_mn_major(uint32_t saddr, int step) {
-  return smem_desc_sw128(saddr + step * 2048, kPanelBytes, 1024);
+
+// D (+)= A B over a tile's 128 rows: A in tensor memory, 16 rows to 8 columns, its second
+// half `half` columns after the first; B in shared memory.
+__device__ __forceinline__ void mma_over_rows(uint32_t d, uint32_t a_tmem, int half, uint32_t b_tile, uint32_t idesc,
+                                              bool more) {
+  const uint64_t db = desc_mn_major(b_tile);
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    mma_f16_ts(d, a_tmem + (k >> 2) * half + (k & 3) * 8, db + k * 128, idesc, more || k > 0);
 }
 
 template <int N>
@@ -100,6 +131,18 @@ __device__ __forceinline__ void tmem_ld<32>(uint32_t taddr, uint32_t* r) {
         "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
+}
+
+// Waits for this thread's tensor-memory loads, into `r` among others.  The loads write
+// their registers asynchronously, and nothing but this ties the registers to the wait: the
+// empty statements keep the compiler from using them before it.
+template <int N>
+__device__ __forceinline__ void tmem_wait_ld(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; i += 8)
+    asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                      "+r"(r[i + 6]), "+r"(r[i + 7])::"memory");
 }
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
@@ -125,34 +168,19 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
 
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Two fp32 operations in one instruction, each rounded as alone.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  uint64_t x, y, z, r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
-  asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
-  asm("mov.b64 %0, {%1, %2};" : "=l"(z) : "f"(c.x), "f"(c.y));
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
-  float2 o;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(r));
-  return o;
+// This warp's tensor-memory accesses are done: one arrival for all its lanes.
+__device__ __forceinline__ void arrive_warp(uint32_t bar) {
+  tc_fence_before();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+  __syncwarp();
 }
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  uint64_t x, y, r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
-  asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
-  float2 o;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(r));
-  return o;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  uint64_t x, y, r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
-  asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
-  float2 o;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(r));
-  return o;
+
+// Bounded wait of a converged warp: one answer for all lanes.
+__device__ __forceinline__ bool attn_wait_warp(uint32_t bar, uint32_t parity, const AttnGuard& g) {
+  const bool ok = __all_sync(0xffffffffu, attn_wait(bar, parity, g));
+  __syncwarp();
+  return ok;
 }
 
 __device__ __forceinline__ float exp2_approx(float x) {

@@ -61,7 +61,7 @@ struct Shared {
   uint64_t s_full[2], p_full[2], o_full[2], diag[2], clean[2], drain;
 };
 
-template <bool F16, int PANELS>
+template <bool F16, int PANELS, bool FULL>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                     const __grid_constant__ CUtensorMap mv, const __grid_constant__ AttnArgs a) {
@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       sh.dirty[i] = 0;
       mbar_init(smem_addr(&sh.q_full[i]), 1);
       mbar_init(smem_addr(&sh.s_full[i]), 1);
-      mbar_init(smem_addr(&sh.p_full[i]), 128);
+      mbar_init(smem_addr(&sh.p_full[i]), 4);
       mbar_init(smem_addr(&sh.o_full[i]), 1);
       mbar_init(smem_addr(&sh.diag[i]), 1);
       mbar_init(smem_addr(&sh.clean[i]), 64);
@@ -124,22 +124,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int row0 = static_cast<int>(w.row0);
   const int ksteps = (a.D + 15) / 16;
 
-  if (na == 0) {
-    // no tile: nothing but the deallocation below
-  } else if (warp == kWarpLoad) {
-    if (lane == 0) {
+  if (warp >= 8) {
+    if (na == 0) {
+      // no tile: nothing but the deallocation below
+    } else if (warp == kWarpLoad) {
+      // The load and MMA warps stay converged: all lanes walk the loop, one lane issues.
       const int boxes = (a.D + 63) / 64;
       const uint32_t bytes = boxes * kPanelBytes;
       auto load = [&](const CUtensorMap* m, uint32_t dst, uint32_t bar, int head, int r) {
-        mbar_arrive_expect_tx(bar, bytes);
-        for (int b = 0; b < boxes; ++b) tma_load_3d(dst + b * kPanelBytes, m, bar, b * 64, head, r);
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar, bytes);
+          for (int b = 0; b < boxes; ++b) tma_load_3d(dst + b * kPanelBytes, m, bar, b * 64, head, r);
+        }
+        __syncwarp();
       };
       load(&mq, sbase + G::kOffQ, smem_addr(&sh.q_full[0]), h, row0 + i0 * kAttnTile);
       uint32_t st = 0, ph = 0, issued = 0, par = 0, diag = 0;
       bool any = false;
       for (int j = 0; j < 2 * nkv; ++j) {  // K0 V0 K1 V1 ...
-        if (!attn_wait(smem_addr(&sh.empty[st]), ph ^ 1u, guard)) break;
-        // the value tiles at the diagonals, the last ones, go to the cleaning warp first
+        if (!attn_wait_warp(smem_addr(&sh.empty[st]), ph ^ 1u, guard)) break;
+        // the value tiles at the diagonals, the last ones, go to the cleaning warps first
         const int d = (j & 1) ? (j >> 1) - i0 : -1;
         load((j & 1) ? &mv : &mk, sbase + G::kOffRing + st * G::kTileBytes,
              d >= 0 ? smem_addr(&sh.diag[d]) : smem_addr(&sh.full[st]), hk, row0 + (j >> 1) * kAttnTile);
@@ -164,70 +168,72 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (diag & (1u << d)) attn_drain(smem_addr(&sh.diag[d]), 0, guard);
       for (int q = 0; q < G::kStages; ++q)
         if (issued & (1u << q)) attn_drain(smem_addr(&sh.full[q]), (par >> q) & 1u, guard);
-    }
-  } else if (warp >= kWarpClean) {
-    // The value tiles at the two diagonals (the last one of each query tile).
-    for (int d = 0; d < (nb > 0 ? 2 : 1); ++d) {
-      const int jt = i0 + d, st = (2 * jt + 1) % G::kStages;
-      if (!__all_sync(0xffffffffu, attn_wait(smem_addr(&sh.diag[d]), 0, guard))) break;
-      const int rows = min(kAttnTile, w.len - jt * kAttnTile);
-      if (clean_tile<F16, PANELS>(smem + G::kOffRing + st * G::kTileBytes, rows, true, warp - kWarpClean, 2) && lane == 0)
-        sh.dirty[d] = 1;
-      mbar_arrive(smem_addr(&sh.clean[d]));
-    }
-  } else if (warp == kWarpMma) {
-    if (lane == 0) {
+      __syncwarp();
+    } else if (warp >= kWarpClean) {
+      // The value tiles at the two diagonals (the last one of each query tile).
+      for (int d = 0; d < (nb > 0 ? 2 : 1); ++d) {
+        const int jt = i0 + d, st = (2 * jt + 1) % G::kStages;
+        if (!attn_wait_warp(smem_addr(&sh.diag[d]), 0, guard)) break;
+        const int rows = min(kAttnTile, w.len - jt * kAttnTile);
+        if (clean_tile<F16, PANELS>(smem + G::kOffRing + st * G::kTileBytes, rows, true, warp - kWarpClean, 2) && lane == 0)
+          sh.dirty[d] = 1;
+        mbar_arrive(smem_addr(&sh.clean[d]));
+      }
+    } else if (warp == kWarpMma) {
       const uint32_t id_s = F16 ? idesc_f16_f32(128, 128, false, false) : idesc_bf16_f32(128, 128, false, false);
       const uint32_t id_o = F16 ? idesc_f16_f32(128, ksteps * 16, false, true) : idesc_bf16_f32(128, ksteps * 16, false, true);
-      auto scores = [&](int t, uint32_t kaddr) {
-        const uint32_t qaddr = sbase + G::kOffQ + t * G::kTileBytes;
-        for (int k = 0; k < ksteps; ++k)
-          mma_bf16_ss(tmem + t * 128, desc_k_major(qaddr, k), desc_k_major(kaddr, k), id_s, k > 0);
-        mma_commit(smem_addr(&sh.s_full[t]));
+      auto wait = [&](uint64_t& b, uint32_t parity) { return attn_wait_warp(smem_addr(&b), parity, guard); };
+      auto commit = [&](uint64_t& b) {
+        if (lane == 0) mma_commit(smem_addr(&b));
+        __syncwarp();
       };
-      const int n[2] = {na, nb};
-      bool ok = attn_wait(smem_addr(&sh.q_full[0]), 0, guard) && attn_wait(smem_addr(&sh.full[0]), 0, guard);
+      auto scores = [&](int t, uint32_t kaddr) {
+        if (lane == 0) {
+          mma_over_columns<FULL, PANELS>(tmem + t * 128, sbase + G::kOffQ + t * G::kTileBytes, kaddr, id_s, ksteps);
+          mma_commit(smem_addr(&sh.s_full[t]));
+        }
+        __syncwarp();
+      };
+      bool ok = wait(sh.q_full[0], 0) && wait(sh.full[0], 0);
       if (ok) {
         scores(0, sbase + G::kOffRing);
         if (nb > 0) {
-          ok = attn_wait(smem_addr(&sh.q_full[1]), 0, guard);
+          ok = wait(sh.q_full[1], 0);
           if (ok) scores(1, sbase + G::kOffRing);
         }
-        mma_commit(smem_addr(&sh.empty[0]));
+        commit(sh.empty[0]);
       }
       for (int j = 0; ok && j < nkv; ++j) {
         const int lv = 2 * j + 1, lk = 2 * j + 2;  // loads of V_j and K_{j+1}
         const int sv = lv % G::kStages, sk = lk % G::kStages;
         const uint32_t vaddr = sbase + G::kOffRing + sv * G::kTileBytes, kaddr = sbase + G::kOffRing + sk * G::kTileBytes;
-        ok = j >= i0 ? attn_wait(smem_addr(&sh.clean[j - i0]), 0, guard)
-                     : attn_wait(smem_addr(&sh.full[sv]), (lv / G::kStages) & 1, guard);
+        ok = j >= i0 ? wait(sh.clean[j - i0], 0) : wait(sh.full[sv], (lv / G::kStages) & 1);
         if (!ok) break;
         bool have_k = false;
         for (int t = 0; t < 2; ++t) {
-          if (j >= n[t]) continue;
-          if (!(ok = attn_wait(smem_addr(&sh.p_full[t]), j & 1, guard))) break;
+          const int n = t ? nb : na;
+          if (j >= n) continue;
+          if (!(ok = wait(sh.p_full[t], j & 1))) break;
           tc_fence_after();
-          for (int k = 0; k < kAttnTile / 16; ++k)
-            mma_f16_ts(tmem + 256 + t * 128, tmem + t * 128 + k * 8, desc_mn_major(vaddr, k), id_o, j > 0 || k > 0);
-          if (j + 1 == n[t]) {
-            mma_commit(smem_addr(&sh.o_full[t]));
-          } else {
-            if (!have_k) {
-              if (!(ok = attn_wait(smem_addr(&sh.full[sk]), (lk / G::kStages) & 1, guard))) break;
-              have_k = true;
-            }
+          if (lane == 0) {
+            mma_over_rows(tmem + 256 + t * 128, tmem + t * 128, 32, vaddr, id_o, j > 0);
+            if (j + 1 == n) mma_commit(smem_addr(&sh.o_full[t]));
+          }
+          __syncwarp();
+          if (j + 1 < n) {
+            if (!have_k && !(ok = wait(sh.full[sk], (lk / G::kStages) & 1))) break;
+            have_k = true;
             scores(t, kaddr);
           }
         }
         if (!ok) break;
-        mma_commit(smem_addr(&sh.empty[sv]));
-        if (have_k) mma_commit(smem_addr(&sh.empty[sk]));
+        commit(sh.empty[sv]);
+        if (have_k) commit(sh.empty[sk]);
       }
-      // on the way out after an abort, MMAs may still be in flight
-      if (!ok) {
-        mma_commit(smem_addr(&sh.drain));
-        attn_drain(smem_addr(&sh.drain), 0, guard);
-      }
+      // no MMA and no arrival of a commit may be in flight when the CTA exits
+      commit(sh.drain);
+      attn_drain(smem_addr(&sh.drain), 0, guard);
+      __syncwarp();
     }
   } else {
     // ------------------------------------------------------------- softmax --
@@ -239,24 +245,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     float m = -INFINITY, mc = 0.0f, l = 0.0f;  // mc: m c (less the shift), or 0 while m is -inf
     bool ok = n > 0;
     for (int j = 0; ok && j < n; ++j) {
-      ok = __all_sync(0xffffffffu, attn_wait(smem_addr(&sh.s_full[t]), j & 1, guard));
-      if (!ok) break;
+      if (!(ok = attn_wait_warp(smem_addr(&sh.s_full[t]), j & 1, guard))) break;
       tc_fence_after();
-      uint32_t s[128];
+      // The maximum first, over the upper half of the columns, then over the lower half,
+      // which stays in registers; the upper half is read again for its exponentials.
+      const int last = j + 1 == n ? i - j * kAttnTile : kAttnTile;  // keys past row i are hidden
+      uint32_t s[64];
+      auto fetch = [&](int from) {
+        tmem_ld<32>(ts + from, s);
+        tmem_ld<32>(ts + from + 32, s + 32);
+        tmem_wait_ld<64>(s);
+        if (j + 1 == n) {  // the diagonal
 #pragma unroll
-      for (int q = 0; q < 4; ++q) tmem_ld<32>(ts + q * 32, s + q * 32);
-      tmem_wait_ld();
-      if (j + 1 == n) {  // the diagonal: keys past row i (and so past the sequence) are hidden
-        const int last = i - j * kAttnTile;
+          for (int q = 0; q < 64; ++q)
+            if (from + q > last) s[q] = 0xff800000u;
+        }
+      };
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      auto raise_to = [&] {
 #pragma unroll
-        for (int q = 0; q < 128; ++q)
-          if (q > last) s[q] = 0xff800000u;
-      }
-      float mx[4];
+        for (int q = 0; q < 64; q += 8)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) mx[q] = __uint_as_float(s[q]);
-#pragma unroll
-      for (int q = 4; q < 128; ++q) mx[q & 3] = fmaxf(mx[q & 3], __uint_as_float(s[q]));
+          for (int e = 0; e < 4; ++e)
+            mx[e] = fmaxf(mx[e], fmaxf(__uint_as_float(s[q + e]), __uint_as_float(s[q + e + 4])));
+      };
+      fetch(64);
+      raise_to();
+      fetch(0);
+      raise_to();
       const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
       if (j == 0) {
         m = top;
@@ -273,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int q = 0; q < ksteps; q += 2) {
           uint32_t o[32];
           tmem_ld<32>(to + q * 16, o);
-          tmem_wait_ld();
+          tmem_wait_ld<32>(o);
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
           tmem_st32(to + q * 16, o);
@@ -281,26 +297,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const float2 c2 = make_float2(c, c), m2 = make_float2(-mc, -mc);
       float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+      auto weigh = [&](int from) {  // P of 64 columns goes to 32, behind the scores still to be read
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t p[16];
+        for (int q = 0; q < 64; q += 32) {
+          uint32_t p[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          float2 x = make_float2(__uint_as_float(s[q * 32 + 2 * e]), __uint_as_float(s[q * 32 + 2 * e + 1]));
-          x = fma2(x, c2, m2);
-          x.x = exp2_approx(x.x);
-          x.y = exp2_approx(x.y);
-          sum[e & 1] = add2(sum[e & 1], x);
-          p[e] = pack16<F16>(x.x, x.y);
+          for (int e = 0; e < 16; ++e) {
+            float2 x = make_float2(__uint_as_float(s[q + 2 * e]), __uint_as_float(s[q + 2 * e + 1]));
+            x = fma2(x, c2, m2);
+            x.x = exp2_approx(x.x);
+            x.y = exp2_approx(x.y);
+            sum[e & 1] = add2(sum[e & 1], x);
+            p[e] = pack16<F16>(x.x, x.y);
+          }
+          tmem_st16(ts + (from + q) / 2, p);
         }
-        tmem_st16(ts + q * 16, p);
-      }
+      };
+      weigh(0);
+      fetch(64);
+      weigh(64);
       l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(smem_addr(&sh.p_full[t]));
+      arrive_warp(smem_addr(&sh.p_full[t]));
     }
-    if (ok && __all_sync(0xffffffffu, attn_wait(smem_addr(&sh.o_full[t]), 0, guard))) {
+    if (ok && attn_wait_warp(smem_addr(&sh.o_full[t]), 0, guard)) {
       tc_fence_after();
       const bool live = i < w.len;
       const float inv = 1.0f / l;
@@ -310,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int q = 0; q < ksteps; q += 2) {
         uint32_t o[32];
         tmem_ld<32>(to + q * 16, o);
-        tmem_wait_ld();
+        tmem_wait_ld<32>(o);
         float f[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(o[e]) * inv;
@@ -345,10 +365,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kWarpMma) tmem_dealloc(tmem, 512);
 }
 
-template <bool F16, int PANELS>
+template <bool F16, int PANELS, bool FULL>
 cudaError_t launch_one(const AttnMaps& m, const AttnArgs& a, cudaStream_t s) {
   static bool configured = false;
-  auto kern = attn_fwd_kernel<F16, PANELS>;
+  auto kern = attn_fwd_kernel<F16, PANELS, FULL>;
   if (!configured) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<PANELS>::kSmem);
     if (e != cudaSuccess) return e;
@@ -362,8 +382,10 @@ cudaError_t launch_one(const AttnMaps& m, const AttnArgs& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_attn_fwd(bool f16, const AttnMaps& m, const AttnArgs& a, cudaStream_t s) {
-  if (a.D <= 64) return f16 ? launch_one<true, 1>(m, a, s) : launch_one<false, 1>(m, a, s);
-  return f16 ? launch_one<true, 2>(m, a, s) : launch_one<false, 2>(m, a, s);
+  if (a.D == 128) return f16 ? launch_one<true, 2, true>(m, a, s) : launch_one<false, 2, true>(m, a, s);
+  if (a.D == 64) return f16 ? launch_one<true, 1, true>(m, a, s) : launch_one<false, 1, true>(m, a, s);
+  if (a.D > 64) return f16 ? launch_one<true, 2, false>(m, a, s) : launch_one<false, 2, false>(m, a, s);
+  return f16 ? launch_one<true, 1, false>(m, a, s) : launch_one<false, 1, false>(m, a, s);
 }
 
 }  // namespace nf4

@@ -39,7 +39,7 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kWarpMma = 8, kWarpLoad = 9, kWarpPrep = 10;  // the last one and the next
-constexpr int kCompute = 256;  // threads of the two compute groups
+constexpr int kCompute = 8;  // warps of the two compute groups
 constexpr float kLog2e = 1.4426950408889634f;
 // fp16 keeps 11 bits down to 2^-14 only: the keys' CTAs hold P' times 2^14 (P' <= 1), and
 // divide dV by it at the end.
@@ -121,7 +121,7 @@ __device__ __forceinline__ void store32(T* out, const uint32_t* r, float f, int 
                      pack16<F16>(__uint_as_float(r[e + 6]) * f, __uint_as_float(r[e + 7]) * f));
 }
 
-template <bool F16, int PANELS>
+template <bool F16, int PANELS, bool FULL>
 struct Ctx {
   using G = Geo<PANELS>;
   const AttnArgs& a;
@@ -135,31 +135,41 @@ struct Ctx {
 
   __device__ __forceinline__ uint32_t bar(const uint64_t& b) const { return smem_addr(&b); }
   __device__ __forceinline__ uint32_t tile(int i) const { return sbase + i * G::kTileBytes; }
-  __device__ __forceinline__ bool wait(const uint64_t& b, uint32_t parity) const { return attn_wait(bar(b), parity, guard); }
-  __device__ __forceinline__ bool wait_warp(const uint64_t& b, uint32_t parity) const {
-    return __all_sync(0xffffffffu, attn_wait(bar(b), parity, guard));
+  // Every role's warp stays converged: all lanes walk its loop, one lane issues.
+  __device__ __forceinline__ bool wait(const uint64_t& b, uint32_t parity) const {
+    return attn_wait_warp(bar(b), parity, guard);
+  }
+  __device__ __forceinline__ void expect(const uint64_t& b, uint32_t n) const {
+    if (lane == 0) mbar_arrive_expect_tx(bar(b), n);
+    __syncwarp();
+  }
+  __device__ __forceinline__ void commit(const uint64_t& b) const {
+    if (lane == 0) mma_commit(bar(b));
+    __syncwarp();
   }
   __device__ __forceinline__ void load(const CUtensorMap* m, int to, const uint64_t& b, int head, int row) const {
-    for (int x = 0; x < boxes; ++x) tma_load_3d(tile(to) + x * kPanelBytes, m, bar(b), x * 64, head, row);
+    if (lane == 0)
+      for (int x = 0; x < boxes; ++x) tma_load_3d(tile(to) + x * kPanelBytes, m, bar(b), x * 64, head, row);
+    __syncwarp();
   }
   __device__ __forceinline__ uint32_t bytes() const { return boxes * kPanelBytes; }
   // D = A B^T over the head's columns, both operands in shared memory.
   __device__ __forceinline__ void over_columns(uint32_t d, int ta, int tb, uint32_t idesc) const {
-    for (int k = 0; k < ksteps; ++k)
-      mma_bf16_ss(d, desc_k_major(tile(ta), k), desc_k_major(tile(tb), k), idesc, k > 0);
+    if (lane == 0) mma_over_columns<FULL, PANELS>(d, tile(ta), tile(tb), idesc, ksteps);
+    __syncwarp();
   }
   // D += A B over the tile's 128 rows, A in tensor memory in two halves 64 columns apart.
   __device__ __forceinline__ void over_rows(uint32_t d, uint32_t at, int tb, uint32_t idesc, bool more) const {
-    for (int k = 0; k < kAttnTile / 16; ++k)
-      mma_f16_ts(d, at + (k >> 2) * 64 + (k & 3) * 8, desc_mn_major(tile(tb), k), idesc, more || k > 0);
+    if (lane == 0) mma_over_rows(d, at, 64, tile(tb), idesc, more);
+    __syncwarp();
   }
 };
 
 // ------------------------------------------------------------------------- keys --
 // Tiles in shared memory: 0 K, 1 V, 2 + 2 st Q, 3 + 2 st dO, 6 Rows.  Tensor memory: S' and P'
 // from 0, dP' and dS' from 128, dV from 256, dK from 384.
-template <bool F16, int PANELS, typename T>
-__device__ __forceinline__ void keys_cta(const Ctx<F16, PANELS>& x, const CUtensorMap* mq, const CUtensorMap* mk,
+template <bool COMPUTE, bool F16, int PANELS, bool FULL, typename T>
+__device__ __forceinline__ void keys_cta(const Ctx<F16, PANELS, FULL>& x, const CUtensorMap* mq, const CUtensorMap* mk,
                                          const CUtensorMap* mv, const CUtensorMap* mg, int hk) {
   const AttnArgs& a = x.a;
   Shared& sh = x.sh;
@@ -168,27 +178,27 @@ __device__ __forceinline__ void keys_cta(const Ctx<F16, PANELS>& x, const CUtens
   const int jt = w.tile, nt = (w.len + kAttnTile - 1) / kAttnTile, nq = nt - jt;
   const int group = a.Hq / a.Hk, n = group * nq;
   const int row0 = static_cast<int>(w.row0), lane = x.lane, warp = x.warp;
+  if constexpr (!COMPUTE) {
   if (warp == kWarpLoad) {
-    if (lane == 0) {
-      mbar_arrive_expect_tx(x.bar(sh.own_full), 2 * x.bytes());
-      x.load(mk, 0, sh.own_full, hk, row0 + jt * kAttnTile);
-      x.load(mv, 1, sh.own_full, hk, row0 + jt * kAttnTile);
-      int done = 0, g = 0, i = jt;
-      for (int it = 0; it < n; ++it) {
-        const int st = it & 1;
-        if (!x.wait(sh.empty[st], ((it >> 1) & 1) ^ 1)) break;
-        mbar_arrive_expect_tx(x.bar(sh.full[st]), 2 * x.bytes());
-        x.load(mq, 2 + 2 * st, sh.full[st], hk * group + g, row0 + i * kAttnTile);
-        x.load(mg, 3 + 2 * st, sh.full[st], hk * group + g, row0 + i * kAttnTile);
-        done = it + 1;
-        if (++i == nt) {
-          i = jt;
-          ++g;
-        }
+    x.expect(sh.own_full, 2 * x.bytes());
+    x.load(mk, 0, sh.own_full, hk, row0 + jt * kAttnTile);
+    x.load(mv, 1, sh.own_full, hk, row0 + jt * kAttnTile);
+    int done = 0, g = 0, i = jt;
+    for (int it = 0; it < n; ++it) {
+      const int st = it & 1;
+      if (!x.wait(sh.empty[st], ((it >> 1) & 1) ^ 1)) break;
+      x.expect(sh.full[st], 2 * x.bytes());
+      x.load(mq, 2 + 2 * st, sh.full[st], hk * group + g, row0 + i * kAttnTile);
+      x.load(mg, 3 + 2 * st, sh.full[st], hk * group + g, row0 + i * kAttnTile);
+      done = it + 1;
+      if (++i == nt) {
+        i = jt;
+        ++g;
       }
-      attn_drain(x.bar(sh.own_full), 0, x.guard);
-      for (int it = done < 2 ? 0 : done - 2; it < done; ++it) attn_drain(x.bar(sh.full[it & 1]), (it >> 1) & 1, x.guard);
     }
+    attn_drain(x.bar(sh.own_full), 0, x.guard);
+    for (int it = done < 2 ? 0 : done - 2; it < done; ++it) attn_drain(x.bar(sh.full[it & 1]), (it >> 1) & 1, x.guard);
+    __syncwarp();
   } else if (warp >= kWarpPrep) {
     int g = 0, i = jt;
     for (int it = 0; it < n; ++it) {
@@ -201,10 +211,10 @@ __device__ __forceinline__ void keys_cta(const Ctx<F16, PANELS>& x, const CUtens
         l[e] = lse2_of(a, at + r0 + e, r0 + e < rows) - (F16 ? kShift : 0.0f);
         d[e] = r0 + e < rows ? a.delta[at + r0 + e] * (F16 ? kUnshift : 1.0f) : 0.0f;
       }
-      if (!x.wait_warp(sh.empty[st], ((it >> 1) & 1) ^ 1)) break;
+      if (!x.wait(sh.empty[st], ((it >> 1) & 1) ^ 1)) break;
       *reinterpret_cast<float2*>(&rs.lse2[st][r0]) = make_float2(l[0], l[1]);
       *reinterpret_cast<float2*>(&rs.delta[st][r0]) = make_float2(d[0], d[1]);
-      if (!x.wait_warp(sh.full[st], (it >> 1) & 1)) break;
+      if (!x.wait(sh.full[st], (it >> 1) & 1)) break;
       if (i == jt || rows < kAttnTile) {
         clean_tile<F16, PANELS>(x.smem + (2 + 2 * st) * Geo<PANELS>::kTileBytes, rows, i == jt, warp - kWarpPrep, 2);
         if (clean_tile<F16, PANELS>(x.smem + (3 + 2 * st) * Geo<PANELS>::kTileBytes, rows, i == jt, warp - kWarpPrep, 2) && lane == 0)
@@ -217,45 +227,44 @@ __device__ __forceinline__ void keys_cta(const Ctx<F16, PANELS>& x, const CUtens
       }
     }
   } else if (warp == kWarpMma) {
-    if (lane == 0) {
-      const uint32_t id_s = F16 ? idesc_f16_f32(128, 128, false, false) : idesc_bf16_f32(128, 128, false, false);
-      const uint32_t id_o = F16 ? idesc_f16_f32(128, x.ksteps * 16, false, true) : idesc_bf16_f32(128, x.ksteps * 16, false, true);
-      const uint32_t S = x.tmem, P = x.tmem + 128, DV = x.tmem + 256, DK = x.tmem + 384;
-      bool ok = x.wait(sh.own_full, 0) && x.wait(sh.ready[0], 0);
-      if (ok) {
-        x.over_columns(S, 0, 2, id_s);
-        mma_commit(x.bar(sh.s_full[0]));
-        x.over_columns(P, 1, 3, id_s);
-        mma_commit(x.bar(sh.dp_full));
+    const uint32_t id_s = F16 ? idesc_f16_f32(128, 128, false, false) : idesc_bf16_f32(128, 128, false, false);
+    const uint32_t id_o = F16 ? idesc_f16_f32(128, x.ksteps * 16, false, true) : idesc_bf16_f32(128, x.ksteps * 16, false, true);
+    const uint32_t S = x.tmem, P = x.tmem + 128, DV = x.tmem + 256, DK = x.tmem + 384;
+    bool ok = x.wait(sh.own_full, 0) && x.wait(sh.ready[0], 0);
+    if (ok) {
+      x.over_columns(S, 0, 2, id_s);
+      x.commit(sh.s_full[0]);
+      x.over_columns(P, 1, 3, id_s);
+      x.commit(sh.dp_full);
+    }
+    for (int it = 0; ok && it < n; ++it) {
+      const int st = it & 1, st1 = st ^ 1;
+      const bool more = it + 1 < n;
+      if (!(ok = x.wait(sh.p_full, it & 1))) break;
+      tc_fence_after();
+      x.over_rows(DV, S, 3 + 2 * st, id_o, it > 0);
+      if (more) {
+        if (!(ok = x.wait(sh.ready[st1], ((it + 1) >> 1) & 1))) break;
+        x.over_columns(S, 0, 2 + 2 * st1, id_s);
+        x.commit(sh.s_full[0]);
       }
-      for (int it = 0; ok && it < n; ++it) {
-        const int st = it & 1, st1 = st ^ 1;
-        const bool more = it + 1 < n;
-        if (!(ok = x.wait(sh.p_full, it & 1))) break;
-        tc_fence_after();
-        x.over_rows(DV, S, 3 + 2 * st, id_o, it > 0);
-        if (more) {
-          if (!(ok = x.wait(sh.ready[st1], ((it + 1) >> 1) & 1))) break;
-          x.over_columns(S, 0, 2 + 2 * st1, id_s);
-          mma_commit(x.bar(sh.s_full[0]));
-        }
-        if (!(ok = x.wait(sh.ds_full, it & 1))) break;
-        tc_fence_after();
-        x.over_rows(DK, P, 2 + 2 * st, id_o, it > 0);
-        mma_commit(x.bar(sh.empty[st]));
-        if (more) {
-          x.over_columns(P, 1, 3 + 2 * st1, id_s);
-          mma_commit(x.bar(sh.dp_full));
-        } else {
-          mma_commit(x.bar(sh.out_full));
-        }
-      }
-      if (!ok) {
-        mma_commit(x.bar(sh.drain));
-        attn_drain(x.bar(sh.drain), 0, x.guard);
+      if (!(ok = x.wait(sh.ds_full, it & 1))) break;
+      tc_fence_after();
+      x.over_rows(DK, P, 2 + 2 * st, id_o, it > 0);
+      x.commit(sh.empty[st]);
+      if (more) {
+        x.over_columns(P, 1, 3 + 2 * st1, id_s);
+        x.commit(sh.dp_full);
+      } else {
+        x.commit(sh.out_full);
       }
     }
-  } else if (warp < 8) {
+    // no MMA and no arrival of a commit may be in flight when the CTA exits
+    x.commit(sh.drain);
+    attn_drain(x.bar(sh.drain), 0, x.guard);
+    __syncwarp();
+  }
+  } else {
     const int wg = warp >> 2, kv = (warp & 3) * 32 + lane;  // this thread's key within the tile
     const uint32_t lanes = ((warp & 3) * 32u) << 16;
     const uint32_t ts = x.tmem + lanes + wg * 64, tp = ts + 128;
@@ -266,12 +275,12 @@ __device__ __forceinline__ void keys_cta(const Ctx<F16, PANELS>& x, const CUtens
     for (int it = 0; it < n; ++it) {
       const int st = it & 1;
       const bool diag = i == jt;
-      if (!(ok = x.wait_warp(sh.ready[st], (it >> 1) & 1) && x.wait_warp(sh.s_full[0], it & 1))) break;
+      if (!(ok = x.wait(sh.ready[st], (it >> 1) & 1) && x.wait(sh.s_full[0], it & 1))) break;
       tc_fence_after();
       uint32_t s[64];
       tmem_ld<32>(ts, s);
       tmem_ld<32>(ts + 32, s + 32);
-      tmem_wait_ld();
+      tmem_wait_ld<64>(s);
 #pragma unroll
       for (int q = 0; q < 64; q += 4) {
         const float4 l = *reinterpret_cast<const float4*>(&rs.lse2[st][wg * 64 + q]);
@@ -295,15 +304,14 @@ __device__ __forceinline__ void keys_cta(const Ctx<F16, PANELS>& x, const CUtens
         tmem_st16(ts + q / 2, p);
       }
       tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(x.bar(sh.p_full));
-      if (!(ok = x.wait_warp(sh.dp_full, it & 1))) break;
+      arrive_warp(x.bar(sh.p_full));
+      if (!(ok = x.wait(sh.dp_full, it & 1))) break;
       tc_fence_after();
 #pragma unroll
       for (int q = 0; q < 64; q += 32) {
         uint32_t d[32], p[16];
         tmem_ld<32>(tp + q, d);
-        tmem_wait_ld();
+        tmem_wait_ld<32>(d);
 #pragma unroll
         for (int e = 0; e < 32; e += 4) {
           const float4 dl = *reinterpret_cast<const float4*>(&rs.delta[st][wg * 64 + q + e]);
@@ -327,11 +335,10 @@ __device__ __forceinline__ void keys_cta(const Ctx<F16, PANELS>& x, const CUtens
         tmem_st16(tp + q / 2, p);
       }
       tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(x.bar(sh.ds_full));
+      arrive_warp(x.bar(sh.ds_full));
       if (++i == nt) i = jt;
     }
-    if (ok && x.wait_warp(sh.out_full, 0)) {
+    if (ok && x.wait(sh.out_full, 0)) {
       tc_fence_after();
       // the first group writes dV, the second dK
       const bool live = jt * kAttnTile + kv < w.len;
@@ -343,7 +350,7 @@ __device__ __forceinline__ void keys_cta(const Ctx<F16, PANELS>& x, const CUtens
       for (int q = 0; q < a.D; q += 32) {
         uint32_t o[32];
         tmem_ld<32>(from + q, o);
-        tmem_wait_ld();
+        tmem_wait_ld<32>(o);
         if (dirty && live) {
           // the non-finite values taken out of dO's diagonal tiles, for the keys that they see
           const int end = min(w.len, (jt + 1) * kAttnTile);
@@ -370,86 +377,84 @@ __device__ __forceinline__ void keys_cta(const Ctx<F16, PANELS>& x, const CUtens
 // ---------------------------------------------------------------------- queries --
 // Tiles in shared memory: 0 Q, 1 dO, 2 + j % 3 K, 5 + j % 2 V.  Tensor memory: S and dS
 // of even steps from 0, of odd steps from 128, dP from 256, dQ from 384.
-template <bool F16, int PANELS, typename T>
-__device__ __forceinline__ void queries_cta(const Ctx<F16, PANELS>& x, const CUtensorMap* mq, const CUtensorMap* mk,
+template <bool COMPUTE, bool F16, int PANELS, bool FULL, typename T>
+__device__ __forceinline__ void queries_cta(const Ctx<F16, PANELS, FULL>& x, const CUtensorMap* mq, const CUtensorMap* mk,
                                             const CUtensorMap* mv, const CUtensorMap* mg, int h) {
   const AttnArgs& a = x.a;
   Shared& sh = x.sh;
   const AttnTile& w = x.w;
   const int it = w.tile, n = it + 1, hk = h / (a.Hq / a.Hk);
   const int row0 = static_cast<int>(w.row0), lane = x.lane, warp = x.warp;
+  if constexpr (!COMPUTE) {
   if (warp == kWarpLoad) {
-    if (lane == 0) {
-      mbar_arrive_expect_tx(x.bar(sh.own_full), 2 * x.bytes());
-      x.load(mq, 0, sh.own_full, h, row0 + it * kAttnTile);
-      x.load(mg, 1, sh.own_full, h, row0 + it * kAttnTile);
-      int nk = 0, nv = 0;
-      bool diag = false;
-      for (int j = 0; j < n; ++j) {
-        if (!x.wait(sh.empty[j % 3], ((j / 3) & 1) ^ 1)) break;
-        const uint64_t& b = j + 1 == n ? sh.diag : sh.full[j % 3];  // the last one is cleaned first
-        mbar_arrive_expect_tx(x.bar(b), x.bytes());
-        x.load(mk, 2 + j % 3, b, hk, row0 + j * kAttnTile);
-        if (j + 1 == n) diag = true; else nk = j + 1;
-        if (!x.wait(sh.vempty[j & 1], ((j >> 1) & 1) ^ 1)) break;
-        mbar_arrive_expect_tx(x.bar(sh.vfull[j & 1]), x.bytes());
-        x.load(mv, 5 + (j & 1), sh.vfull[j & 1], hk, row0 + j * kAttnTile);
-        nv = j + 1;
-      }
-      attn_drain(x.bar(sh.own_full), 0, x.guard);
-      if (diag) attn_drain(x.bar(sh.diag), 0, x.guard);
-      for (int j = nk < 3 ? 0 : nk - 3; j < nk; ++j) attn_drain(x.bar(sh.full[j % 3]), (j / 3) & 1, x.guard);
-      for (int j = nv < 2 ? 0 : nv - 2; j < nv; ++j) attn_drain(x.bar(sh.vfull[j & 1]), (j >> 1) & 1, x.guard);
+    x.expect(sh.own_full, 2 * x.bytes());
+    x.load(mq, 0, sh.own_full, h, row0 + it * kAttnTile);
+    x.load(mg, 1, sh.own_full, h, row0 + it * kAttnTile);
+    int nk = 0, nv = 0;
+    bool diag = false;
+    for (int j = 0; j < n; ++j) {
+      if (!x.wait(sh.empty[j % 3], ((j / 3) & 1) ^ 1)) break;
+      const uint64_t& b = j + 1 == n ? sh.diag : sh.full[j % 3];  // the last one is cleaned first
+      x.expect(b, x.bytes());
+      x.load(mk, 2 + j % 3, b, hk, row0 + j * kAttnTile);
+      if (j + 1 == n) diag = true; else nk = j + 1;
+      if (!x.wait(sh.vempty[j & 1], ((j >> 1) & 1) ^ 1)) break;
+      x.expect(sh.vfull[j & 1], x.bytes());
+      x.load(mv, 5 + (j & 1), sh.vfull[j & 1], hk, row0 + j * kAttnTile);
+      nv = j + 1;
     }
+    attn_drain(x.bar(sh.own_full), 0, x.guard);
+    if (diag) attn_drain(x.bar(sh.diag), 0, x.guard);
+    for (int j = nk < 3 ? 0 : nk - 3; j < nk; ++j) attn_drain(x.bar(sh.full[j % 3]), (j / 3) & 1, x.guard);
+    for (int j = nv < 2 ? 0 : nv - 2; j < nv; ++j) attn_drain(x.bar(sh.vfull[j & 1]), (j >> 1) & 1, x.guard);
+    __syncwarp();
   } else if (warp >= kWarpPrep) {
-    if (x.wait_warp(sh.diag, 0)) {
+    if (x.wait(sh.diag, 0)) {
       clean_tile<F16, PANELS>(x.smem + (2 + it % 3) * Geo<PANELS>::kTileBytes, min(kAttnTile, w.len - it * kAttnTile), true,
                               warp - kWarpPrep, 2);
       mbar_arrive(x.bar(sh.clean));
     }
   } else if (warp == kWarpMma) {
-    if (lane == 0) {
-      const uint32_t id_s = F16 ? idesc_f16_f32(128, 128, false, false) : idesc_bf16_f32(128, 128, false, false);
-      const uint32_t id_o = F16 ? idesc_f16_f32(128, x.ksteps * 16, false, true) : idesc_bf16_f32(128, x.ksteps * 16, false, true);
-      const uint32_t S = x.tmem, P = x.tmem + 256, DQ = x.tmem + 384;
-      auto key = [&](int j) { return j + 1 == n ? x.wait(sh.clean, 0) : x.wait(sh.full[j % 3], (j / 3) & 1); };
-      auto scores = [&](int j) {
-        x.over_columns(S + (j & 1) * 128, 0, 2 + j % 3, id_s);
-        mma_commit(x.bar(sh.s_full[j & 1]));
-      };
-      auto grads = [&](int j) {
-        x.over_columns(P, 1, 5 + (j & 1), id_s);
-        mma_commit(x.bar(sh.dp_full));
-        mma_commit(x.bar(sh.vempty[j & 1]));
-      };
-      bool ok = x.wait(sh.own_full, 0) && key(0);
-      if (ok) {
-        scores(0);
-        if ((ok = x.wait(sh.vfull[0], 0))) grads(0);
-        if (ok && n > 1 && (ok = key(1))) scores(1);
+    const uint32_t id_s = F16 ? idesc_f16_f32(128, 128, false, false) : idesc_bf16_f32(128, 128, false, false);
+    const uint32_t id_o = F16 ? idesc_f16_f32(128, x.ksteps * 16, false, true) : idesc_bf16_f32(128, x.ksteps * 16, false, true);
+    const uint32_t S = x.tmem, P = x.tmem + 256, DQ = x.tmem + 384;
+    auto key = [&](int j) { return j + 1 == n ? x.wait(sh.clean, 0) : x.wait(sh.full[j % 3], (j / 3) & 1); };
+    auto scores = [&](int j) {
+      x.over_columns(S + (j & 1) * 128, 0, 2 + j % 3, id_s);
+      x.commit(sh.s_full[j & 1]);
+    };
+    auto grads = [&](int j) {
+      x.over_columns(P, 1, 5 + (j & 1), id_s);
+      x.commit(sh.dp_full);
+      x.commit(sh.vempty[j & 1]);
+    };
+    bool ok = x.wait(sh.own_full, 0) && key(0);
+    if (ok) {
+      scores(0);
+      if ((ok = x.wait(sh.vfull[0], 0))) grads(0);
+      if (ok && n > 1 && (ok = key(1))) scores(1);
+    }
+    for (int j = 0; ok && j < n; ++j) {
+      if (!(ok = x.wait(sh.ds_full, j & 1))) break;
+      tc_fence_after();
+      if (j + 1 < n) {
+        if (!(ok = x.wait(sh.vfull[(j + 1) & 1], ((j + 1) >> 1) & 1))) break;
+        grads(j + 1);
       }
-      for (int j = 0; ok && j < n; ++j) {
-        if (!(ok = x.wait(sh.ds_full, j & 1))) break;
-        tc_fence_after();
-        if (j + 1 < n) {
-          if (!(ok = x.wait(sh.vfull[(j + 1) & 1], ((j + 1) >> 1) & 1))) break;
-          grads(j + 1);
-        }
-        x.over_rows(DQ, S + (j & 1) * 128, 2 + j % 3, id_o, j > 0);
-        mma_commit(x.bar(sh.empty[j % 3]));
-        if (j + 2 < n) {
-          if (!(ok = key(j + 2))) break;
-          scores(j + 2);
-        }
-      }
-      if (ok) {
-        mma_commit(x.bar(sh.out_full));
-      } else {
-        mma_commit(x.bar(sh.drain));
-        attn_drain(x.bar(sh.drain), 0, x.guard);
+      x.over_rows(DQ, S + (j & 1) * 128, 2 + j % 3, id_o, j > 0);
+      x.commit(sh.empty[j % 3]);
+      if (j + 2 < n) {
+        if (!(ok = key(j + 2))) break;
+        scores(j + 2);
       }
     }
-  } else if (warp < 8) {
+    if (ok) x.commit(sh.out_full);
+    // no MMA and no arrival of a commit may be in flight when the CTA exits
+    x.commit(sh.drain);
+    attn_drain(x.bar(sh.drain), 0, x.guard);
+    __syncwarp();
+  }
+  } else {
     const int wg = warp >> 2, row = (warp & 3) * 32 + lane, i = it * kAttnTile + row;
     const uint32_t lanes = ((warp & 3) * 32u) << 16;
     const uint32_t tp = x.tmem + lanes + 256 + wg * 64;
@@ -462,14 +467,15 @@ __device__ __forceinline__ void queries_cta(const Ctx<F16, PANELS>& x, const CUt
     for (int j = 0; j < n; ++j) {
       const uint32_t ts = x.tmem + lanes + (j & 1) * 128 + wg * 64;
       const bool diag = j + 1 == n;
-      if (!(ok = x.wait_warp(sh.s_full[j & 1], (j >> 1) & 1) && x.wait_warp(sh.dp_full, j & 1))) break;
+      if (!(ok = x.wait(sh.s_full[j & 1], (j >> 1) & 1) && x.wait(sh.dp_full, j & 1))) break;
       tc_fence_after();
       uint32_t s[64], d[64];
       tmem_ld<32>(ts, s);
       tmem_ld<32>(ts + 32, s + 32);
       tmem_ld<32>(tp, d);
       tmem_ld<32>(tp + 32, d + 32);
-      tmem_wait_ld();
+      tmem_wait_ld<64>(s);
+      tmem_wait_ld<64>(d);
 #pragma unroll
       for (int q = 0; q < 64; q += 32) {
         uint32_t p[16];
@@ -488,16 +494,15 @@ __device__ __forceinline__ void queries_cta(const Ctx<F16, PANELS>& x, const CUt
         tmem_st16(ts + q / 2, p);
       }
       tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(x.bar(sh.ds_full));
+      arrive_warp(x.bar(sh.ds_full));
     }
-    if (ok && x.wait_warp(sh.out_full, 0)) {
+    if (ok && x.wait(sh.out_full, 0)) {
       tc_fence_after();
       T* out = static_cast<T*>(a.gq) + (w.row0 + i) * a.gq_t + h * a.gq_h;
       for (int q = wg * 32; q < a.D; q += 64) {  // the groups take 32 columns in turn
         uint32_t o[32];
         tmem_ld<32>(x.tmem + lanes + 384 + q, o);
-        tmem_wait_ld();
+        tmem_wait_ld<32>(o);
         if (live) store32<F16>(out, o, a.scale, q, a.D);
         __syncwarp();
       }
@@ -505,7 +510,7 @@ __device__ __forceinline__ void queries_cta(const Ctx<F16, PANELS>& x, const CUt
   }
 }
 
-template <bool F16, int PANELS>
+template <bool F16, int PANELS, bool FULL>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                     const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mg,
@@ -556,24 +561,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (sh.tile.tile >= 0) {
-    const Ctx<F16, PANELS> x{a, sh, AttnGuard{&sh.abort_flag, a.status}, smem, smem_addr(smem), sh.tmem, warp, lane,
+  {
+    const Ctx<F16, PANELS, FULL> x{a, sh, AttnGuard{&sh.abort_flag, a.status}, smem, smem_addr(smem), sh.tmem, warp, lane,
                              sh.tile, (a.D + 15) / 16, (a.D + 63) / 64};
-    if (keys)
-      keys_cta<F16, PANELS, T>(x, &mq, &mk, &mv, &mg, h);
-    else
-      queries_cta<F16, PANELS, T>(x, &mq, &mk, &mv, &mg, h);
+    const bool work = x.w.tile >= 0;
+    if (warp < 8) {
+      if (work && keys) keys_cta<true, F16, PANELS, FULL, T>(x, &mq, &mk, &mv, &mg, h);
+      if (work && !keys) queries_cta<true, F16, PANELS, FULL, T>(x, &mq, &mk, &mv, &mg, h);
+    } else {
+      if (work && keys) keys_cta<false, F16, PANELS, FULL, T>(x, &mq, &mk, &mv, &mg, h);
+      if (work && !keys) queries_cta<false, F16, PANELS, FULL, T>(x, &mq, &mk, &mv, &mg, h);
+    }
   }
   tc_fence_before();
   __syncthreads();
   if (warp == kWarpMma) tmem_dealloc(sh.tmem, 512);
 }
 
-template <bool F16, int PANELS>
+template <bool F16, int PANELS, bool FULL>
 cudaError_t launch_one(const AttnMaps& m, const AttnArgs& a, int sms, cudaStream_t s) {
   static bool configured = false;
   using T = typename std::conditional<F16, __half, __nv_bfloat16>::type;
-  auto kern = attn_bwd_kernel<F16, PANELS>;
+  auto kern = attn_bwd_kernel<F16, PANELS, FULL>;
   if (!configured) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<PANELS>::kSmem);
     if (e != cudaSuccess) return e;
@@ -591,8 +600,10 @@ cudaError_t launch_one(const AttnMaps& m, const AttnArgs& a, int sms, cudaStream
 }  // namespace
 
 cudaError_t launch_attn_bwd(bool f16, const AttnMaps& m, const AttnArgs& a, int sms, cudaStream_t s) {
-  if (a.D <= 64) return f16 ? launch_one<true, 1>(m, a, sms, s) : launch_one<false, 1>(m, a, sms, s);
-  return f16 ? launch_one<true, 2>(m, a, sms, s) : launch_one<false, 2>(m, a, sms, s);
+  if (a.D == 128) return f16 ? launch_one<true, 2, true>(m, a, sms, s) : launch_one<false, 2, true>(m, a, sms, s);
+  if (a.D == 64) return f16 ? launch_one<true, 1, true>(m, a, sms, s) : launch_one<false, 1, true>(m, a, sms, s);
+  if (a.D > 64) return f16 ? launch_one<true, 2, false>(m, a, sms, s) : launch_one<false, 2, false>(m, a, sms, s);
+  return f16 ? launch_one<true, 1, false>(m, a, sms, s) : launch_one<false, 1, false>(m, a, sms, s);
 }
 
 }  // namespace nf4
