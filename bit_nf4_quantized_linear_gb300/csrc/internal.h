@@ -91,7 +91,7 @@ struct AdamTensor {
   void *m, *v;
   float *m_absmax, *v_absmax;
   int64_t n;
-  int64_t vec;  // set by the launcher: 16-byte accesses to every array
+  int64_t vec;  // set by the launcher: vector accesses to every array
 };
 struct AdamTable {
   AdamTensor t[kAdamMaxTensors];

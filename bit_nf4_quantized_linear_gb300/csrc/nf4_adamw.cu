@@ -14,6 +14,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "elem.cuh"
 #include "internal.h"
@@ -42,13 +43,10 @@ __device__ __forceinline__ float warp_absmax_nan(float v) {
 // ---------------------------------------------------------- nearest level --
 // The code of r is the count of midpoints below it.  Each midpoint is rounded down to
 // fp32 first: r > mid is the same as r > floor32(mid) for an fp32 r.  A binary search
-// takes eight dependent loads; instead the top 16 bits of |r| (sign apart, exponent and
-// seven bits) select a bucket that holds one midpoint at most, as the dynamic maps do
-// everywhere from 2^-23 up, and one comparison of the low 16 bits decides.  An entry is
-//   bits 31..16  low half of the bucket's midpoint (0xffff: none, nothing is above it)
-//   bits 15..0   code below the midpoint (r >= 0), or, in the second half of the table,
-//                code of an |r| below it (r < 0, where the code falls as |r| grows)
-// Levels that do not fit the scheme are searched.
+// takes eight dependent loads; instead the sign, exponent and seven bits of r select a
+// bucket that holds one midpoint at most, as the dynamic maps do everywhere from 2^-23
+// up, and one comparison with it picks one of two codes.  Levels that do not fit the
+// scheme are searched.
 constexpr int kBucket0 = 104 << 7;                        // of 2^-23
 constexpr int kBuckets = (127 << 7) - kBucket0 + 1;       // up to that of 1.0
 
@@ -56,7 +54,8 @@ struct Map {
   float level[256];
   float mid[255];
   int searched;
-  uint32_t entry[2 * kBuckets];
+  // .x: the bucket's threshold on |r| (fp32); .y: codes at or below it (bits 0-7) and above (8-15)
+  uint2 entry[2 * kBuckets];
 };
 
 __device__ __forceinline__ int search(const Map& mp, float r) {
@@ -93,61 +92,60 @@ __device__ void build_maps(Map* maps, const float* levels_m, const float* levels
       const int from = i == zero ? 0 : bucket_of(mp.mid[i - 1]) + 1;
       const int own = i == 255 ? kBuckets : bucket_of(mp.mid[i]);
       if (i < 255 && (own <= 0 || own >= kBuckets || own < from)) mp.searched = 1;
-      for (int b = max(from, 0) + lane; b < min(own, kBuckets); b += 32) mp.entry[b] = 0xffff0000u | i;
+      for (int b = max(from, 0) + lane; b < min(own, kBuckets); b += 32)
+        mp.entry[b] = make_uint2(__float_as_uint(INFINITY), i * 0x101u);
       if (lane == 0 && i < 255 && own >= 0 && own < kBuckets)
-        mp.entry[own] = (__float_as_uint(mp.mid[i]) << 16) | i;
+        mp.entry[own] = make_uint2(__float_as_uint(mp.mid[i]), i | (i + 1) << 8);
     }
-    // the negative ones by |mid|, i falling: code i + 1 below |mid[i]|, i from it on.  The
-    // comparison is |r| >= |mid|, so the entry holds the low half of the fp32 before it.
+    // the negative ones by |mid|, i falling: code i + 1 below |mid[i]|, i from it on; the
+    // comparison is |r| >= |mid|, so the threshold is the fp32 before it
     for (int i = zero - 1 - warp; i >= -1; i -= kWarps) {
       const int from = i == zero - 1 ? 0 : bucket_of(mp.mid[i + 1]) + 1;
       const int own = i < 0 ? kBuckets : bucket_of(mp.mid[i]);
       if (i >= 0 && (own <= 0 || own >= kBuckets || own < from)) mp.searched = 1;
-      uint32_t* e = mp.entry + kBuckets;
-      for (int b = max(from, 0) + lane; b < min(own, kBuckets); b += 32) e[b] = 0xffff0000u | (i + 1);
-      if (lane == 0 && i >= 0 && own >= 0 && own < kBuckets) {
-        const uint32_t low = __float_as_uint(mp.mid[i]) & 0xffffu;
-        e[own] = low == 0u ? 0xffff0000u | i : ((low - 1) << 16) | (i + 1);
-      }
+      uint2* e = mp.entry + kBuckets;
+      for (int b = max(from, 0) + lane; b < min(own, kBuckets); b += 32)
+        e[b] = make_uint2(__float_as_uint(INFINITY), (i + 1) * 0x101u);
+      if (lane == 0 && i >= 0 && own >= 0 && own < kBuckets)
+        e[own] = make_uint2((__float_as_uint(mp.mid[i]) & 0x7fffffffu) - 1u, (i + 1) | i << 8);
     }
     // no negative midpoints: codes of r < 0 do not occur, entries stay readable
     if (zero == 0)
-      for (int b = threadIdx.x; b < kBuckets; b += kThreads) mp.entry[kBuckets + b] = 0xffff0000u;
+      for (int b = threadIdx.x; b < kBuckets; b += kThreads) mp.entry[kBuckets + b] = make_uint2(__float_as_uint(INFINITY), 0u);
   }
   __syncthreads();
 }
 
+// The code in bits 0-7; the bits above are not cleared.  |r| <= 1.
 template <bool SIGNED>
 __device__ __forceinline__ uint32_t code_of(const Map& mp, float r) {
-  const uint32_t u = __float_as_uint(r);
-  int b = static_cast<int>((u >> 16) & 0x7fffu) - kBucket0;
-  b = min(max(b, 0), kBuckets - 1);
-  const bool neg = SIGNED && (u >> 31);
-  const uint32_t e = mp.entry[neg ? b + kBuckets : b];
-  const uint32_t above = (u & 0xffffu) > (e >> 16) ? 1u : 0u;
-  return (neg ? e - above : e + above) & 0xffu;
+  // values below the first bucket have no midpoint above zero beneath them: they read it
+  const float mag = fmaxf(SIGNED ? fabsf(r) : r, 1.1920928955078125e-7f);
+  const uint32_t at = (__float_as_uint(mag) >> 13) & ~7u;  // eight bytes an entry
+  const char* base = reinterpret_cast<const char*>(mp.entry) - static_cast<ptrdiff_t>(kBucket0) * 8;
+  if (SIGNED) base += (__float_as_uint(r) >> 31) * (kBuckets * 8);
+  const uint2 e = *reinterpret_cast<const uint2*>(base + at);
+  return mag > __uint_as_float(e.x) ? e.y >> 8 : e.y;
 }
 
 // Exact quotients x / top of |x| <= top by multiplication: with y the correctly rounded
 // reciprocal and q within an ulp of the quotient, q + (x - q top) y rounded once is the
-// correctly rounded quotient (Markstein 1990); a first step of the same form brings q
-// that near.  Both sides are scaled by the power of two that makes top lie in [1, 2), so
-// that the residual x - q top is exact.  Only for a normal top below 2^126.
+// correctly rounded quotient (Markstein 1990).  q comes from the reciprocal in two words,
+// y + rest.  The residual x - q top is exact while top is neither tiny nor huge; outside
+// [2^-75, 2^100] the values are divided.
 struct Quotient {
-  float scale, top, y;
-  bool plain;  // outside that range: divide
+  float2 top, y, rest;
+  bool plain;
   __device__ __forceinline__ explicit Quotient(float t) {
-    const int e = static_cast<int>(__float_as_uint(t) >> 23);
-    plain = e < 1 || e > 252;
-    scale = __uint_as_float(static_cast<uint32_t>(254 - (plain ? 127 : e)) << 23);
-    top = t * scale;
-    y = __frcp_rn(top);
+    plain = !(t >= 2.6469779601696886e-23f && t <= 1.2676506002282294e30f);
+    const float d = plain ? 1.0f : t, r = __frcp_rn(d), w = __fmaf_rn(-d, r, 1.0f) * r;
+    top = make_float2(-d, -d);
+    y = make_float2(r, r);
+    rest = make_float2(w, w);
   }
-  __device__ __forceinline__ float of(float x) const {
-    x *= scale;
-    float q = x * y;
-    q = __fmaf_rn(__fmaf_rn(-q, top, x), y, q);
-    return __fmaf_rn(__fmaf_rn(-q, top, x), y, q);
+  __device__ __forceinline__ float2 of(float2 x) const {
+    const float2 q = fma2(x, y, mul2(x, rest));  // contracted or not
+    return fma2(fma2(q, top, x), y, q);
   }
 };
 
@@ -161,7 +159,8 @@ __device__ __forceinline__ int find_tensor(const AdamTable& tab, int64_t b) {
   return lo;
 }
 
-// Eight neighbouring values of a lane.
+// Eight neighbouring values of a lane: one access of 16 or 32 bytes, so that a lane always
+// covers whole 32-byte sectors of fp32 data.
 template <typename T>
 __device__ __forceinline__ void load8(const T* p, float (&x)[kPer]) {
   if constexpr (sizeof(T) == 2) {
@@ -170,9 +169,10 @@ __device__ __forceinline__ void load8(const T* p, float (&x)[kPer]) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) x[k] = to_f32(e[k]);
   } else {
-    const float4 u = reinterpret_cast<const float4*>(p)[0], v = reinterpret_cast<const float4*>(p)[1];
-    x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
-    x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
+    asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
+                 : "l"(p)
+                 : "memory");
   }
 }
 template <typename T>
@@ -184,8 +184,9 @@ __device__ __forceinline__ void store8(T* p, const float (&x)[kPer]) {
     for (int k = 0; k < 8; ++k) e[k] = from_f32<T>(x[k]);
     *reinterpret_cast<uint4*>(p) = v;
   } else {
-    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(x[0]), "f"(x[1]), "f"(x[2]),
+                 "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+                 : "memory");
   }
 }
 
@@ -194,20 +195,173 @@ __device__ __forceinline__ float sqrt_approx(float x) {
   asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-
-// New moments and parameter of one value; the square root and the quotient, which only
-// the parameter sees, are the hardware's approximations (errors near 2^-23).
-__device__ __forceinline__ void update(const AdamArgs& a, float g, float& m, float& v, float& p) {
-  m = __fadd_rn(__fmul_rn(m, a.beta1), __fmul_rn(g, a.one_minus_beta1));
-  v = __fadd_rn(__fmul_rn(v, a.beta2), __fmul_rn(__fmul_rn(g, g), a.one_minus_beta2));
-  const float den = __fadd_rn(__fmul_rn(sqrt_approx(v), a.inv_sqrt_c2), a.eps);
-  // p - (lr wd p + step q): the rounding of the small bracket does not show in p
-  p = __fsub_rn(p, __fmaf_rn(a.decay, p, __fmul_rn(a.step_size, __fdividef(m, den))));
+__device__ __forceinline__ float sqrt_approx_ftz(float x) {
+  float r;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_approx_ftz(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
-// One warp per block of 256 values; a lane owns eight neighbours.  Bound by HBM (10 bytes
-// a value in and out for 16-bit parameters with 8-bit states) with the integer pipe close
-// behind: the codes cost about 20 of its instructions a value.
+// New moments and parameters of two values; the square root and the quotient, which only
+// the parameter sees, are the hardware's approximations (errors near 2^-23).  With an eps
+// from 1e-12 up (EPS), subnormal second moments may count as zero (their root is below
+// 1.1e-19) and the denominator is normal: two plain approximations do.
+template <bool EPS>
+__device__ __forceinline__ void update(const AdamArgs& a, float2 g, float2& m, float2& v, float2& p) {
+  auto both = [](float x) { return make_float2(x, x); };
+  // single operations: the packed ones may be contracted into one rounding
+  m.x = __fadd_rn(__fmul_rn(m.x, a.beta1), __fmul_rn(g.x, a.one_minus_beta1));
+  m.y = __fadd_rn(__fmul_rn(m.y, a.beta1), __fmul_rn(g.y, a.one_minus_beta1));
+  v.x = __fadd_rn(__fmul_rn(v.x, a.beta2), __fmul_rn(__fmul_rn(g.x, g.x), a.one_minus_beta2));
+  v.y = __fadd_rn(__fmul_rn(v.y, a.beta2), __fmul_rn(__fmul_rn(g.y, g.y), a.one_minus_beta2));
+  float2 q;
+  if (EPS) {
+    const float2 den = fma2(make_float2(sqrt_approx_ftz(v.x), sqrt_approx_ftz(v.y)), both(a.inv_sqrt_c2), both(a.eps));
+    q = mul2(m, make_float2(rcp_approx_ftz(den.x), rcp_approx_ftz(den.y)));
+  } else {
+    q.x = __fdividef(m.x, fmaf(sqrt_approx(v.x), a.inv_sqrt_c2, a.eps));
+    q.y = __fdividef(m.y, fmaf(sqrt_approx(v.y), a.inv_sqrt_c2, a.eps));
+  }
+  // p - (lr wd p + step q): the rounding of the small bracket does not show in p
+  const float2 d = fma2(both(a.decay), p, mul2(both(a.step_size), q));
+  p = fma2(d, both(-1.0f), p);
+}
+
+// Codes of eight values of a block with the scale `top`.
+template <bool SIGNED, bool WIDE>
+__device__ __forceinline__ void store_codes(const Map& mp, float (&x)[kPer], float top, uint8_t* to, int have) {
+  const Quotient q(top);
+  uint32_t w[2] = {0u, 0u};
+  if (q.plain || mp.searched) {
+    const float d = top > 0.0f ? top : 1.0f;
+#pragma unroll 1
+    for (int k = 0; k < kPer; ++k) {  // no indexing of registers: values and codes rotate
+      const uint32_t c = search(mp, __fdiv_rn(x[0], d));
+#pragma unroll
+      for (int e = 0; e + 1 < kPer; ++e) x[e] = x[e + 1];
+      w[0] = __funnelshift_r(w[0], w[1], 8);
+      w[1] = w[1] >> 8 | c << 24;
+    }
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float2 a = q.of(make_float2(x[4 * h], x[4 * h + 1])), b = q.of(make_float2(x[4 * h + 2], x[4 * h + 3]));
+      const uint32_t lo = __byte_perm(code_of<SIGNED>(mp, a.x), code_of<SIGNED>(mp, a.y), 0x0040);
+      const uint32_t hi = __byte_perm(code_of<SIGNED>(mp, b.x), code_of<SIGNED>(mp, b.y), 0x0040);
+      w[h] = __byte_perm(lo, hi, 0x5410);
+    }
+  }
+  if (WIDE) {
+    *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+      if (k < have) to[k] = static_cast<uint8_t>(w[k >> 2] >> (8 * (k & 3)));
+  }
+}
+
+// A block of 256 values by one warp, a lane owning eight neighbours; WIDE: all of them
+// inside the tensor and every array fit for vector accesses.
+template <typename T, int BITS, bool WIDE>
+__device__ __forceinline__ void block_step(const AdamArgs& a, const Map* maps, const AdamTensor& t, int64_t blk, int lane,
+                                           float gs) {
+  const int64_t base = blk * kAdamBlock + lane * kPer;
+  T* p = static_cast<T*>(t.param) + base;
+  const T* g = static_cast<const T*>(t.grad) + base;
+  const int have = WIDE ? kPer : t.n - base >= kPer ? kPer : t.n > base ? static_cast<int>(t.n - base) : 0;
+  uint8_t *mc = static_cast<uint8_t*>(t.m) + base, *vc = static_cast<uint8_t*>(t.v) + base;
+  float *mf = static_cast<float*>(t.m) + base, *vf = static_cast<float*>(t.v) + base;
+  float pv[kPer], gv[kPer], m[kPer], v[kPer];
+  if (WIDE) {
+    load8(g, gv);
+    load8(p, pv);
+    if (BITS == 8) {
+      const uint2 cm = *reinterpret_cast<const uint2*>(mc), cv = *reinterpret_cast<const uint2*>(vc);
+      const float sm = t.m_absmax[blk], sv = t.v_absmax[blk];
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        m[k] = __fmul_rn(maps[0].level[((k < 4 ? cm.x : cm.y) >> (8 * (k & 3))) & 255u], sm);
+        v[k] = __fmul_rn(maps[1].level[((k < 4 ? cv.x : cv.y) >> (8 * (k & 3))) & 255u], sv);
+      }
+    } else {
+      load8(mf, m);
+      load8(vf, v);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const bool in = k < have;
+      gv[k] = in ? to_f32(g[k]) : 0.0f;
+      pv[k] = in ? to_f32(p[k]) : 0.0f;
+      if (BITS == 8) {
+        m[k] = in ? __fmul_rn(maps[0].level[mc[k]], t.m_absmax[blk]) : 0.0f;
+        v[k] = in ? __fmul_rn(maps[1].level[vc[k]], t.v_absmax[blk]) : 0.0f;
+      } else {
+        m[k] = in ? mf[k] : 0.0f;
+        v[k] = in ? vf[k] : 0.0f;
+      }
+    }
+  }
+  if (a.grad_scale)
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) gv[k] = __fmul_rn(gv[k], gs);
+  auto all = [&](auto eps) {
+#pragma unroll
+    for (int k = 0; k < kPer; k += 2) {
+      float2 m2 = make_float2(m[k], m[k + 1]), v2 = make_float2(v[k], v[k + 1]), p2 = make_float2(pv[k], pv[k + 1]);
+      update<decltype(eps)::value>(a, make_float2(gv[k], gv[k + 1]), m2, v2, p2);
+      m[k] = m2.x;
+      m[k + 1] = m2.y;
+      v[k] = v2.x;
+      v[k + 1] = v2.y;
+      pv[k] = p2.x;
+      pv[k + 1] = p2.y;
+    }
+  };
+  if (a.eps >= 1e-12f) all(std::true_type{}); else all(std::false_type{});
+  if (WIDE) {
+    store8(p, pv);
+  } else {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+      if (k < have) p[k] = from_f32<T>(pv[k]);
+  }
+  if (BITS == 32) {
+    if (WIDE) {
+      store8(mf, m);
+      store8(vf, v);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        if (k >= have) continue;
+        mf[k] = m[k];
+        vf[k] = v[k];
+      }
+    }
+    return;
+  }
+  float top_m = 0.0f, top_v = 0.0f;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    if (!WIDE && k >= have) continue;  // past the tensor: no part of the scale
+    top_m = max_nan(top_m, fabsf(m[k]));
+    top_v = max_nan(top_v, fabsf(v[k]));
+  }
+  top_m = warp_absmax_nan(top_m);
+  top_v = warp_absmax_nan(top_v);
+  if (lane == 0) {
+    t.m_absmax[blk] = top_m;
+    t.v_absmax[blk] = top_v;
+  }
+  store_codes<true, WIDE>(maps[0], m, top_m, mc, have);
+  store_codes<false, WIDE>(maps[1], v, top_v, vc, have);
+}
+
+// Warps walk the blocks of all tensors with the grid's stride.
 template <typename T, int BITS>
 __global__ void __launch_bounds__(kThreads, 2) adamw_kernel(const __grid_constant__ AdamTable tab,
                                                             const __grid_constant__ AdamArgs a) {
@@ -226,118 +380,11 @@ __global__ void __launch_bounds__(kThreads, 2) adamw_kernel(const __grid_constan
       last = tab.blk0[ti + 1];
     }
     const AdamTensor& t = tab.t[ti];
-    const int64_t blk = b - first, base = blk * kAdamBlock + lane * kPer;
-    T* p = static_cast<T*>(t.param) + base;
-    const T* g = static_cast<const T*>(t.grad) + base;
-    const int have = t.n - base >= kPer ? kPer : t.n > base ? static_cast<int>(t.n - base) : 0;
-    // the same for a whole warp but in a tensor's last block
-    const bool wide = t.vec && have == kPer;
-    float pv[kPer], gv[kPer], m[kPer], v[kPer];
-    uint8_t *mc = static_cast<uint8_t*>(t.m) + base, *vc = static_cast<uint8_t*>(t.v) + base;
-    float *mf = static_cast<float*>(t.m) + base, *vf = static_cast<float*>(t.v) + base;
-    uint8_t cm[kPer], cv[kPer];
-    if (wide) {
-      load8(g, gv);
-      load8(p, pv);
-      if (BITS == 8) {
-        *reinterpret_cast<uint2*>(cm) = *reinterpret_cast<const uint2*>(mc);
-        *reinterpret_cast<uint2*>(cv) = *reinterpret_cast<const uint2*>(vc);
-      } else {
-        load8(mf, m);
-        load8(vf, v);
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        const bool in = k < have;
-        gv[k] = in ? to_f32(g[k]) : 0.0f;
-        pv[k] = in ? to_f32(p[k]) : 0.0f;
-        if (BITS == 8) {
-          cm[k] = in ? mc[k] : 0;
-          cv[k] = in ? vc[k] : 0;
-        } else {
-          m[k] = in ? mf[k] : 0.0f;
-          v[k] = in ? vf[k] : 0.0f;
-        }
-      }
-    }
-    if (BITS == 8) {
-      const float sm = t.m_absmax[blk], sv = t.v_absmax[blk];
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        m[k] = __fmul_rn(maps[0].level[cm[k]], sm);
-        v[k] = __fmul_rn(maps[1].level[cv[k]], sv);
-      }
-    }
-    if (a.grad_scale)
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) gv[k] = __fmul_rn(gv[k], gs);
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      update(a, gv[k], m[k], v[k], pv[k]);
-      if (BITS == 8 && k >= have) m[k] = v[k] = 0.0f;  // past the tensor: no part of the scale
-    }
-    if (BITS == 8) {
-      float top_m = fabsf(m[0]), top_v = fabsf(v[0]);
-#pragma unroll
-      for (int k = 1; k < kPer; ++k) {
-        top_m = max_nan(top_m, fabsf(m[k]));
-        top_v = max_nan(top_v, fabsf(v[k]));
-      }
-      top_m = warp_absmax_nan(top_m);
-      top_v = warp_absmax_nan(top_v);
-      const Quotient qm(top_m), qv(top_v);
-      if (qm.plain || qv.plain || maps[0].searched || maps[1].searched) {
-        const float dm = top_m > 0.0f ? top_m : 1.0f, dv = top_v > 0.0f ? top_v : 1.0f;
-#pragma unroll 1
-        for (int k = 0; k < kPer; ++k) {
-          // no indexing of registers: rotate the values through the first place
-          const uint32_t x = search(maps[0], __fdiv_rn(m[0], dm)), y = search(maps[1], __fdiv_rn(v[0], dv));
-#pragma unroll
-          for (int e = 0; e + 1 < kPer; ++e) {
-            m[e] = m[e + 1];
-            v[e] = v[e + 1];
-            cm[e] = cm[e + 1];
-            cv[e] = cv[e + 1];
-          }
-          cm[kPer - 1] = static_cast<uint8_t>(x);
-          cv[kPer - 1] = static_cast<uint8_t>(y);
-        }
-      } else {
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-          cm[k] = static_cast<uint8_t>(code_of<true>(maps[0], qm.of(m[k])));
-          cv[k] = static_cast<uint8_t>(code_of<false>(maps[1], qv.of(v[k])));
-        }
-      }
-      if (lane == 0) {
-        t.m_absmax[blk] = top_m;
-        t.v_absmax[blk] = top_v;
-      }
-    }
-    if (wide) {
-      store8(p, pv);
-      if (BITS == 8) {
-        *reinterpret_cast<uint2*>(mc) = *reinterpret_cast<const uint2*>(cm);
-        *reinterpret_cast<uint2*>(vc) = *reinterpret_cast<const uint2*>(cv);
-      } else {
-        store8(mf, m);
-        store8(vf, v);
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        if (k >= have) continue;
-        p[k] = from_f32<T>(pv[k]);
-        if (BITS == 8) {
-          mc[k] = cm[k];
-          vc[k] = cv[k];
-        } else {
-          mf[k] = m[k];
-          vf[k] = v[k];
-        }
-      }
-    }
+    const int64_t blk = b - first;
+    if (t.vec && (blk + 1) * kAdamBlock <= t.n)
+      block_step<T, BITS, true>(a, maps, t, blk, lane, gs);
+    else
+      block_step<T, BITS, false>(a, maps, t, blk, lane, gs);
   }
 }
 
@@ -391,8 +438,8 @@ template <typename T>
 cudaError_t launch_typed(int bits, AdamTable& tab, const AdamArgs& a, int sms, cudaStream_t s) {
   for (int i = 0; i < tab.count; ++i) {
     AdamTensor& t = tab.t[i];
-    const size_t state = bits == 8 ? 8 : 16;
-    t.vec = aligned(t.param, 16) && aligned(t.grad, 16) && aligned(t.m, state) && aligned(t.v, state);
+    const size_t state = bits == 8 ? 8 : 32;
+    t.vec = aligned(t.param, 8 * sizeof(T)) && aligned(t.grad, 8 * sizeof(T)) && aligned(t.m, state) && aligned(t.v, state);
   }
   return bits == 8 ? launch_one<T, 8>(tab, a, sms, s) : launch_one<T, 32>(tab, a, sms, s);
 }
@@ -407,7 +454,7 @@ cudaError_t launch_adamw(int dtype, int bits, AdamTable& tab, const AdamArgs& a,
 }
 
 cudaError_t launch_adamw_values(AdamValuesArgs a, int sms, cudaStream_t s) {
-  a.vec = aligned(a.m, 8) && aligned(a.v, 8) && aligned(a.out_m, 16) && aligned(a.out_v, 16);
+  a.vec = aligned(a.m, 8) && aligned(a.v, 8) && aligned(a.out_m, 32) && aligned(a.out_v, 32);
   const int64_t want = (a.n + kThreads * 8 - 1) / (kThreads * 8), most = 4 * static_cast<int64_t>(sms);
   adamw_values_kernel<<<static_cast<unsigned>(want < most ? want : most), kThreads, 0, s>>>(a);
   return cudaGetLastError();

@@ -307,11 +307,10 @@ struct Sums {
 
 // One row of the backward.  gains(k, g) fetches w_post, the channel gate or w_pre (k = 0,
 // 1, 2) at this thread's columns; it is asked twice, to leave the registers to the sums.
-// `red` [64]: CTA barriers separate its reads from the next call's writes.  Every thread
-// has its inputs in registers when after_first() runs.
-template <typename T, int VEC, typename Gains, typename AfterFirst>
+// `red` [64]: CTA barriers separate its reads from the next call's writes.
+template <typename T, int VEC, typename Gains>
 __device__ __forceinline__ void bwd_row(const NormArgs& a, const BwdRow<T, VEC>& x, int64_t t, int n, float inv_h,
-                                        Gains gains, float* red, Sums& sum, AfterFirst after_first) {
+                                        Gains gains, float* red, Sums& sum) {
   using F = Frag<T, VEC>;
   const bool token = a.gate_kind == NF4_GATE_TOKEN;
   {
@@ -328,7 +327,6 @@ __device__ __forceinline__ void bwd_row(const NormArgs& a, const BwdRow<T, VEC>&
       s = fmaf(zhat[i], x.gh.at(i) * wn[i], s);
     }
     const float mz = block_sum(s, red) * inv_h;
-    after_first();
     gains(0, wp);
     gains(1, g);
     gains(2, wn);
@@ -394,7 +392,7 @@ __global__ void __launch_bounds__(kMaxThreadsBwd) norm_bwd_kernel(const __grid_c
                        : a.gate_kind == NF4_GATE_CHANNEL ? static_cast<const float*>(a.gate) : nullptr;
       load_gain<T, 1>(g, p, a.H, n, k == 2 ? 0.0f : 1.0f);
     };
-    bwd_row<T, 1>(a, x, t, n, inv_h, gains, red, sum, [] {});
+    bwd_row<T, 1>(a, x, t, n, inv_h, gains, red, sum);
   }
   store_sums<T, 1>(a, sum, n);
 }
@@ -492,20 +490,34 @@ __device__ __forceinline__ void ring_start(const RowRing<T, BWD>& rr, int n) {
   __syncthreads();
 }
 
+// The rows' sums overlap: while row t's second sum is formed, so is row t + 1's first, and
+// one CTA barrier serves both.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kMaxThreadsFwd) norm_fwd_ring_kernel(const __grid_constant__ NormArgs a, int stages) {
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float red[64];
+  __shared__ float2 red[2][32];
   __shared__ Ring ring;
   const int n = blockDim.x;
   const RowRing<T, false> rr(a, ring, smem, stages);
   ring_start(rr, n);
   using F = Frag<T, VEC>;
   const float inv_h = 1.0f / static_cast<float>(a.H);
-  int st = 0;
+  int st = 0, buf = 0;
   uint32_t ph = 0;
+  auto squares = [&](int stage) {  // of this thread's part of y
+    float s = 0.0f;
+    if (a.w_post) {
+      F y;
+      y.load(rr.stage0 + stage * rr.stage_bytes, a.H, n);
+#pragma unroll
+      for (int i = 0; i < kHold; ++i) s = fmaf(y.at(i), y.at(i), s);
+    }
+    return s;
+  };
+  rr.wait(0, 0, a.status);
+  float ss_y = block_sum2(make_float2(squares(0), 0.0f), red[1]).x;
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-    rr.wait(st, ph, a.status);
+    const float rstd_y = a.w_post ? rsqrtf(ss_y * inv_h + a.eps) : 1.0f;
     const uint8_t* p = rr.stage0 + st * rr.stage_bytes;
     F y, r, gt;
     y.load(p, a.H, n);
@@ -517,13 +529,6 @@ __global__ void __launch_bounds__(kMaxThreadsFwd) norm_fwd_ring_kernel(const __g
       r.clear();
     }
     if (a.gate_kind == NF4_GATE_TOKEN) gt.load(p, a.H, n);
-    float rstd_y = 1.0f;
-    if (a.w_post) {
-      float s = 0.0f;
-#pragma unroll
-      for (int i = 0; i < kHold; ++i) s = fmaf(y.at(i), y.at(i), s);
-      rstd_y = rsqrtf(block_sum(s, red) * inv_h + a.eps);
-    }
     float g[kHold], z[kHold], s = 0.0f;
     rr.template gain<VEC>(z, 0, a.w_post != nullptr, 1.0f, n);
     rr.template gain<VEC>(g, 1, a.gate_kind == NF4_GATE_CHANNEL, 1.0f, n);
@@ -538,8 +543,18 @@ __global__ void __launch_bounds__(kMaxThreadsFwd) norm_fwd_ring_kernel(const __g
       for (int i = 0; i < kHold; ++i) o.set(i, z[i]);
       o.store(row_of<T>(a.z, t, a.ld_z), a.H, n);
     }
-    const float rstd_z = rsqrtf(block_sum(s, red + 32) * inv_h + a.eps);
-    // every thread has read its part of the stage
+    const int st1 = st + 1 == stages ? 0 : st + 1;
+    const uint32_t ph1 = st1 == 0 ? ph ^ 1u : ph;
+    float s1 = 0.0f;
+    if (t + gridDim.x < a.T) {
+      rr.wait(st1, ph1, a.status);
+      s1 = squares(st1);
+    }
+    const float2 sums = block_sum2(make_float2(s, s1), red[buf]);
+    buf ^= 1;
+    ss_y = sums.y;
+    const float rstd_z = rsqrtf(sums.x * inv_h + a.eps);
+    // every thread has read its part of row t
     if (threadIdx.x == 0 && t + static_cast<int64_t>(stages) * gridDim.x < a.T)
       rr.issue(st, t + static_cast<int64_t>(stages) * gridDim.x);
     if (a.h) {
@@ -553,59 +568,133 @@ __global__ void __launch_bounds__(kMaxThreadsFwd) norm_fwd_ring_kernel(const __g
       a.stats[t] = rstd_y;
       a.stats[a.T + t] = rstd_z;
     }
-    if (!a.w_post) __syncthreads();  // red is read before the next row's sum writes it
-    if (++st == stages) {
-      st = 0;
-      ph ^= 1u;
-    }
+    st = st1;
+    ph = ph1;
   }
 }
 
+// As in the forward, row t's second sum and row t + 1's first share a barrier.  What a row
+// needs after its first sum is read from shared memory again, which leaves the registers
+// to the sums over tokens.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kMaxThreadsBwd) norm_bwd_ring_kernel(const __grid_constant__ NormArgs a, int stages) {
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float red[64];
+  __shared__ float2 red[2][32];
   __shared__ Ring ring;
   const int n = blockDim.x;
   const RowRing<T, true> rr(a, ring, smem, stages);
   ring_start(rr, n);
+  using F = Frag<T, VEC>;
+  const bool token = a.gate_kind == NF4_GATE_TOKEN;
   const float inv_h = 1.0f / static_cast<float>(a.H);
+  // places of the arrays in a stage
+  const uint32_t at_r = rr.row_bytes, at_t = at_r + (a.residual ? rr.row_bytes : 0), at_z = at_t + (token ? rr.row_bytes : 0),
+                 at_h = at_z + (a.gz ? rr.row_bytes : 0);
+  auto take = [&](F& f, bool have, int stage, uint32_t at) {
+    if (have) f.load(rr.stage0 + stage * rr.stage_bytes + at, a.H, n); else f.clear();
+  };
+  auto gains = [&](int k, float (&g)[kHold]) {
+    const bool have = k == 0 ? a.w_post != nullptr : k == 2 ? a.w_pre != nullptr : a.gate_kind == NF4_GATE_CHANNEL;
+    rr.template gain<VEC>(g, k, have, k == 2 ? 0.0f : 1.0f, n);
+  };
+  // z of this thread's columns, with y and n = y rstd_y w_post
+  auto forward = [&](int stage, float rstd_y, F& y, float (&nn)[kHold], float (&sg)[kHold], float (&z)[kHold]) {
+    F r, gt;
+    take(y, true, stage, 0);
+    take(r, a.residual != nullptr, stage, at_r);
+    take(gt, token, stage, at_t);
+    gains(0, nn);
+    gains(1, sg);
+#pragma unroll
+    for (int i = 0; i < kHold; ++i) {
+      nn[i] *= y.at(i) * rstd_y;
+      sg[i] = a.scale * (token ? gt.at(i) : sg[i]);
+      z[i] = fmaf(sg[i], nn[i], r.at(i));
+    }
+  };
+  auto first_sum = [&](int stage, float rstd_y) {  // of z gh w_pre
+    float s = 0.0f;
+    if (a.gh) {
+      F y, gh;
+      float nn[kHold], sg[kHold], z[kHold];
+      forward(stage, rstd_y, y, nn, sg, z);
+      take(gh, true, stage, at_h);
+      gains(2, nn);
+#pragma unroll
+      for (int i = 0; i < kHold; ++i) s = fmaf(z[i], gh.at(i) * nn[i], s);
+    }
+    return s;
+  };
   Sums sum;
   sum.clear();
-  int st = 0;
+  int st = 0, buf = 0;
   uint32_t ph = 0;
+  float rstd_y = a.stats[blockIdx.x], rstd_z = a.stats[a.T + blockIdx.x];
+  rr.wait(0, 0, a.status);
+  float dot = block_sum2(make_float2(first_sum(0, rstd_y), 0.0f), red[1]).x;
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-    BwdRow<T, VEC> x;
-    x.rstd_y = a.stats[t];
-    x.rstd_z = a.stats[a.T + t];
-    rr.wait(st, ph, a.status);
-    const uint8_t* p = rr.stage0 + st * rr.stage_bytes;
-    auto take = [&](Frag<T, VEC>& f, bool have) {
-      if (have) {
-        f.load(p, a.H, n);
-        p += rr.row_bytes;
-      } else {
-        f.clear();
+    const bool more = t + gridDim.x < a.T;
+    const float rstd_y1 = more ? a.stats[t + gridDim.x] : 0.0f, rstd_z1 = more ? a.stats[a.T + t + gridDim.x] : 0.0f;
+    // dz = gz + rstd_z gh w_pre - z rstd_z^3 mean(z gh w_pre)
+    const float pull = rstd_z * rstd_z * rstd_z * dot * inv_h;
+    F y;
+    float b[kHold], s = 0.0f;
+    {
+      F gz, gh, gr, gg;
+      float nn[kHold], sg[kHold], z[kHold], w[kHold];
+      forward(st, rstd_y, y, nn, sg, z);
+      take(gz, a.gz != nullptr, st, at_z);
+      take(gh, a.gh != nullptr, st, at_h);
+      gains(2, w);
+#pragma unroll
+      for (int i = 0; i < kHold; ++i) {
+        const float ghz = gh.at(i) * rstd_z;
+        const float dz = fmaf(-pull, z[i], fmaf(ghz, w[i], gz.at(i)));
+        gr.set(i, dz);
+        gg.set(i, a.scale * dz * nn[i]);
+        b[i] = sg[i] * dz;
+        sum.pre[i] = fmaf(ghz, z[i], sum.pre[i]);
+        sum.gate[i] = fmaf(dz, nn[i], sum.gate[i]);
       }
-    };
-    take(x.y, true);
-    take(x.r, a.residual != nullptr);
-    take(x.gt, a.gate_kind == NF4_GATE_TOKEN);
-    take(x.gz, a.gz != nullptr);
-    take(x.gh, a.gh != nullptr);
-    auto gains = [&](int k, float (&g)[kHold]) {
-      const bool have = k == 0 ? a.w_post != nullptr : k == 2 ? a.w_pre != nullptr : a.gate_kind == NF4_GATE_CHANNEL;
-      rr.template gain<VEC>(g, k, have, k == 2 ? 0.0f : 1.0f, n);
-    };
-    bwd_row<T, VEC>(a, x, t, n, inv_h, gains, red, sum, [&] {
-      if (threadIdx.x == 0 && t + static_cast<int64_t>(stages) * gridDim.x < a.T)
-        rr.issue(st, t + static_cast<int64_t>(stages) * gridDim.x);
-    });
-    if (++st == stages) {
-      st = 0;
-      ph ^= 1u;
+      if (a.gr) gr.store(row_of<T>(a.gr, t, a.ld_gr), a.H, n);
+      if (token && a.ggate) gg.store(row_of<T>(a.ggate, t, a.ld_ggate), a.H, n);
+      gains(0, w);
+#pragma unroll
+      for (int i = 0; i < kHold; ++i) {
+        const float yhat = y.at(i) * rstd_y;
+        sum.post[i] = fmaf(b[i], yhat, sum.post[i]);
+        b[i] *= w[i];
+        s = fmaf(yhat, b[i], s);
+      }
     }
+    const int st1 = st + 1 == stages ? 0 : st + 1;
+    const uint32_t ph1 = st1 == 0 ? ph ^ 1u : ph;
+    float s1 = 0.0f;
+    if (more) {
+      rr.wait(st1, ph1, a.status);
+      s1 = first_sum(st1, rstd_y1);
+    }
+    const float2 sums = block_sum2(make_float2(s, s1), red[buf]);
+    buf ^= 1;
+    // every thread has read its part of row t
+    if (threadIdx.x == 0 && t + static_cast<int64_t>(stages) * gridDim.x < a.T)
+      rr.issue(st, t + static_cast<int64_t>(stages) * gridDim.x);
+    if (a.gy) {
+      // without w_post, n is y itself: no norm to go back through
+      const float back = a.w_post ? rstd_y * rstd_y * sums.x * inv_h : 0.0f;
+      F gy;
+#pragma unroll
+      for (int i = 0; i < kHold; ++i) gy.set(i, fmaf(-back, y.at(i), rstd_y * b[i]));
+      gy.store(row_of<T>(a.gy, t, a.ld_gy), a.H, n);
+    }
+    dot = sums.y;
+    rstd_y = rstd_y1;
+    rstd_z = rstd_z1;
+    st = st1;
+    ph = ph1;
   }
+#pragma unroll
+  for (int i = 0; i < kHold; ++i) sum.gate[i] *= a.scale;
   store_sums<T, VEC>(a, sum, n);
 }
 
@@ -705,7 +794,7 @@ cudaError_t launch_typed(bool backward, const NormArgs& a, int sms, cudaStream_t
     e = cudaGetLastError();
   } else {
     const int smem = vec ? ring_smem(a, sizeof(T), true, &stages) : 0;
-    if (stages >= 1) {
+    if (stages >= 2) {
       e = ring_launch(norm_bwd_ring_kernel<T, kVec>, static_cast<unsigned>(P), n, smem, a, stages, s);
     } else {
       norm_bwd_kernel<T><<<P, n, 0, s>>>(a);
