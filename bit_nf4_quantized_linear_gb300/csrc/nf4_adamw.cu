@@ -45,20 +45,31 @@ __device__ __forceinline__ float warp_absmax_nan(float v) {
 // fp32 first: r > mid is the same as r > floor32(mid) for an fp32 r.  A binary search
 // takes eight dependent loads; instead the sign, exponent and seven bits of r select a
 // bucket that holds one midpoint at most, as the dynamic maps do everywhere from 2^-23
-// up, and one comparison with it picks one of two codes.  Levels that do not fit the
-// scheme are searched.
+// up, and one comparison of the low halves picks one of two codes.  Levels that do not
+// fit the scheme are searched.
 constexpr int kBucket0 = 104 << 7;                        // of 2^-23
 constexpr int kBuckets = (127 << 7) - kBucket0 + 1;       // up to that of 1.0
+constexpr uint32_t kNoMid = 0xffff0000u;
 
+// Levels are held 32 times over, one copy a bank, so that the lanes' look-ups do not
+// collide; bucket entries once (neighbouring values mostly share a few buckets).
+//   entry: low half of the bucket's threshold on |r| (bits 16-31; 0xffff: nothing is above
+//   it), code above it (8-15), code at or below it (0-7); r >= 0, then r < 0
+template <bool SIGNED>
 struct Map {
-  float level[256];
+  float level[256 * 32];
+  float once[256];
   float mid[255];
   int searched;
-  // .x: the bucket's threshold on |r| (fp32); .y: codes at or below it (bits 0-7) and above (8-15)
-  uint2 entry[2 * kBuckets];
+  uint32_t entry[(SIGNED ? 2 : 1) * kBuckets];
+};
+struct Maps {
+  Map<true> m;
+  Map<false> v;
 };
 
-__device__ __forceinline__ int search(const Map& mp, float r) {
+template <bool SIGNED>
+__device__ __forceinline__ int search(const Map<SIGNED>& mp, float r) {
   int lo = 0, hi = 255;
   while (lo < hi) {
     const int m = (lo + hi) >> 1;
@@ -69,63 +80,63 @@ __device__ __forceinline__ int search(const Map& mp, float r) {
 
 __device__ __forceinline__ int bucket_of(float x) { return static_cast<int>((__float_as_uint(x) >> 16) & 0x7fffu) - kBucket0; }
 
-// Levels, midpoints and buckets of both maps, by the whole CTA.
-__device__ void build_maps(Map* maps, const float* levels_m, const float* levels_v) {
-  for (int i = threadIdx.x; i < 512; i += kThreads) {
-    const float* L = i < 256 ? levels_m : levels_v;
-    Map& mp = maps[i >> 8];
-    const int k = i & 255;
-    mp.level[k] = L[k];
-    if (k < 255) mp.mid[k] = __double2float_rd((static_cast<double>(L[k]) + static_cast<double>(L[k + 1])) * 0.5);
-    if (k == 255) mp.searched = 0;
-  }
-  __syncthreads();
+// Levels, midpoints and buckets of a map, by the whole CTA.
+template <bool SIGNED>
+__device__ void build_map(Map<SIGNED>& mp, const float* L) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int k = 0; k < 2; ++k) {
-    Map& mp = maps[k];
-    int zero = 0;  // midpoints below zero: 0 .. zero - 1
-    for (int i = lane; i < 255; i += 32) zero += mp.mid[i] < 0.0f;
-    zero = __reduce_add_sync(0xffffffffu, zero);
-    // midpoint i of the positive ones fills the buckets after its predecessor's, up to its
-    // own; the last stretch, past the last midpoint, is item 255
-    for (int i = zero + warp; i <= 255; i += kWarps) {
-      const int from = i == zero ? 0 : bucket_of(mp.mid[i - 1]) + 1;
-      const int own = i == 255 ? kBuckets : bucket_of(mp.mid[i]);
-      if (i < 255 && (own <= 0 || own >= kBuckets || own < from)) mp.searched = 1;
-      for (int b = max(from, 0) + lane; b < min(own, kBuckets); b += 32)
-        mp.entry[b] = make_uint2(__float_as_uint(INFINITY), i * 0x101u);
-      if (lane == 0 && i < 255 && own >= 0 && own < kBuckets)
-        mp.entry[own] = make_uint2(__float_as_uint(mp.mid[i]), i | (i + 1) << 8);
-    }
+  if (threadIdx.x < 256) mp.once[threadIdx.x] = L[threadIdx.x];
+  if (threadIdx.x == 0) mp.searched = 0;
+  __syncthreads();
+  for (int i = warp; i < 256; i += kWarps) mp.level[i * 32 + lane] = mp.once[i];
+  // half the sum rounded down: the halving is exact
+  if (threadIdx.x < 255) mp.mid[threadIdx.x] = 0.5f * __fadd_rd(mp.once[threadIdx.x], mp.once[threadIdx.x + 1]);
+  __syncthreads();
+  int zero = 0;  // midpoints below zero: 0 .. zero - 1
+  for (int i = lane; i < 255; i += 32) zero += mp.mid[i] < 0.0f;
+  zero = __reduce_add_sync(0xffffffffu, zero);
+  if (!SIGNED && zero > 0) mp.searched = 1;
+  // midpoint i of the positive ones fills the buckets after its predecessor's, up to its
+  // own; the last stretch, past the last midpoint, is item 255
+  for (int i = zero + warp; i <= 255; i += kWarps) {
+    const int from = i == zero ? 0 : bucket_of(mp.mid[i - 1]) + 1;
+    const int own = i == 255 ? kBuckets : bucket_of(mp.mid[i]);
+    if (i < 255 && (own <= 0 || own >= kBuckets || own < from)) mp.searched = 1;
+    for (int b = max(from, 0) + lane; b < min(own, kBuckets); b += 32) mp.entry[b] = kNoMid | i * 0x101u;
+    if (lane == 0 && i < 255 && own >= 0 && own < kBuckets)
+      mp.entry[own] = __float_as_uint(mp.mid[i]) << 16 | (i + 1) << 8 | i;
+  }
+  if (SIGNED) {
     // the negative ones by |mid|, i falling: code i + 1 below |mid[i]|, i from it on; the
-    // comparison is |r| >= |mid|, so the threshold is the fp32 before it
+    // comparison is |r| >= |mid|, so the threshold is the fp32 before it (where that lies
+    // in the bucket before, every value here is above it)
+    uint32_t* e = mp.entry + kBuckets;
     for (int i = zero - 1 - warp; i >= -1; i -= kWarps) {
       const int from = i == zero - 1 ? 0 : bucket_of(mp.mid[i + 1]) + 1;
       const int own = i < 0 ? kBuckets : bucket_of(mp.mid[i]);
       if (i >= 0 && (own <= 0 || own >= kBuckets || own < from)) mp.searched = 1;
-      uint2* e = mp.entry + kBuckets;
-      for (int b = max(from, 0) + lane; b < min(own, kBuckets); b += 32)
-        e[b] = make_uint2(__float_as_uint(INFINITY), (i + 1) * 0x101u);
-      if (lane == 0 && i >= 0 && own >= 0 && own < kBuckets)
-        e[own] = make_uint2((__float_as_uint(mp.mid[i]) & 0x7fffffffu) - 1u, (i + 1) | i << 8);
+      for (int b = max(from, 0) + lane; b < min(own, kBuckets); b += 32) e[b] = kNoMid | (i + 1) * 0x101u;
+      if (lane == 0 && i >= 0 && own >= 0 && own < kBuckets) {
+        const uint32_t low = __float_as_uint(mp.mid[i]) & 0xffffu;
+        e[own] = low == 0u ? kNoMid | i * 0x101u : (low - 1u) << 16 | i << 8 | (i + 1);
+      }
     }
-    // no negative midpoints: codes of r < 0 do not occur, entries stay readable
     if (zero == 0)
-      for (int b = threadIdx.x; b < kBuckets; b += kThreads) mp.entry[kBuckets + b] = make_uint2(__float_as_uint(INFINITY), 0u);
+      for (int b = threadIdx.x; b < kBuckets; b += kThreads) e[b] = kNoMid;
   }
   __syncthreads();
 }
 
 // The code in bits 0-7; the bits above are not cleared.  |r| <= 1.
 template <bool SIGNED>
-__device__ __forceinline__ uint32_t code_of(const Map& mp, float r) {
-  // values below the first bucket have no midpoint above zero beneath them: they read it
-  const float mag = fmaxf(SIGNED ? fabsf(r) : r, 1.1920928955078125e-7f);
-  const uint32_t at = (__float_as_uint(mag) >> 13) & ~7u;  // eight bytes an entry
-  const char* base = reinterpret_cast<const char*>(mp.entry) - static_cast<ptrdiff_t>(kBucket0) * 8;
-  if (SIGNED) base += (__float_as_uint(r) >> 31) * (kBuckets * 8);
-  const uint2 e = *reinterpret_cast<const uint2*>(base + at);
-  return mag > __uint_as_float(e.x) ? e.y >> 8 : e.y;
+__device__ __forceinline__ uint32_t code_of(const Map<SIGNED>& mp, float r) {
+  // values below the first bucket have no midpoint between zero and them: they read it
+  const uint32_t mag = __float_as_uint(fmaxf(SIGNED ? fabsf(r) : r, 1.1920928955078125e-7f));
+  const uint32_t at = (mag >> 14) & ~3u;  // four bytes an entry
+  const char* base = reinterpret_cast<const char*>(mp.entry) - static_cast<ptrdiff_t>(kBucket0) * 4;
+  if (SIGNED) base += (__float_as_uint(r) >> 31) * (kBuckets * 4);
+  const uint32_t e = *reinterpret_cast<const uint32_t*>(base + at);
+  // equal low halves give mag << 16 <= e: not above
+  return mag << 16 > e ? e >> 8 : e;
 }
 
 // Exact quotients x / top of |x| <= top by multiplication: with y the correctly rounded
@@ -161,20 +172,6 @@ __device__ __forceinline__ int find_tensor(const AdamTable& tab, int64_t b) {
 
 // Eight neighbouring values of a lane: one access of 16 or 32 bytes, so that a lane always
 // covers whole 32-byte sectors of fp32 data.
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&x)[kPer]) {
-  if constexpr (sizeof(T) == 2) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
-    const T* e = reinterpret_cast<const T*>(&v);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = to_f32(e[k]);
-  } else {
-    asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
-                 : "l"(p)
-                 : "memory");
-  }
-}
 template <typename T>
 __device__ __forceinline__ void store8(T* p, const float (&x)[kPer]) {
   if constexpr (sizeof(T) == 2) {
@@ -233,7 +230,7 @@ __device__ __forceinline__ void update(const AdamArgs& a, float2 g, float2& m, f
 
 // Codes of eight values of a block with the scale `top`.
 template <bool SIGNED, bool WIDE>
-__device__ __forceinline__ void store_codes(const Map& mp, float (&x)[kPer], float top, uint8_t* to, int have) {
+__device__ __forceinline__ void store_codes(const Map<SIGNED>& mp, float (&x)[kPer], float top, uint8_t* to, int have) {
   const Quotient q(top);
   uint32_t w[2] = {0u, 0u};
   if (q.plain || mp.searched) {
@@ -264,12 +261,65 @@ __device__ __forceinline__ void store_codes(const Map& mp, float (&x)[kPer], flo
   }
 }
 
-// A block of 256 values by one warp, a lane owning eight neighbours; WIDE: all of them
-// inside the tensor and every array fit for vector accesses.
+// The level of byte `k` of w, from this lane's copy.
+template <bool SIGNED>
+__device__ __forceinline__ float level(const Map<SIGNED>& mp, uint32_t w, int k) {
+  const uint32_t at = (k == 0 ? w << 7 : w >> (8 * k - 7)) & (255u << 7);
+  return *reinterpret_cast<const float*>(reinterpret_cast<const char*>(mp.level + (threadIdx.x & 31)) + at);
+}
+
+// Where a warp's block lies: its tensor and its number in it.
+struct Place {
+  const AdamTensor* t;
+  int64_t blk;
+};
+
+// A lane's eight values of a block as they lie in memory.
+template <typename T, int BITS>
+struct Raw {
+  uint32_t g[2 * sizeof(T)], p[2 * sizeof(T)];
+  uint32_t m[BITS == 8 ? 2 : 8], v[BITS == 8 ? 2 : 8];
+  float sm, sv;
+  template <int N>
+  static __device__ __forceinline__ void get(const void* from, uint32_t (&to)[N]) {
+    if constexpr (N == 8) {
+      asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=r"(to[0]), "=r"(to[1]), "=r"(to[2]), "=r"(to[3]), "=r"(to[4]), "=r"(to[5]), "=r"(to[6]), "=r"(to[7])
+                   : "l"(from)
+                   : "memory");
+    } else if constexpr (N == 4) {
+      const uint4 x = *static_cast<const uint4*>(from);
+      to[0] = x.x; to[1] = x.y; to[2] = x.z; to[3] = x.w;
+    } else {
+      const uint2 x = *static_cast<const uint2*>(from);
+      to[0] = x.x; to[1] = x.y;
+    }
+  }
+  __device__ __forceinline__ void load(const Place& at, int lane) {
+    const int64_t base = at.blk * kAdamBlock + lane * kPer;
+    get(static_cast<const T*>(at.t->grad) + base, g);
+    get(static_cast<const T*>(at.t->param) + base, p);
+    constexpr int64_t size = BITS == 8 ? 1 : 4;
+    get(static_cast<const char*>(at.t->m) + base * size, m);
+    get(static_cast<const char*>(at.t->v) + base * size, v);
+    if (BITS == 8) {
+      sm = at.t->m_absmax[at.blk];
+      sv = at.t->v_absmax[at.blk];
+    }
+  }
+  static __device__ __forceinline__ void widen(const uint32_t (&w)[2 * sizeof(T)], float (&x)[kPer]) {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) x[k] = to_f32(reinterpret_cast<const T*>(w)[k]);
+  }
+};
+
+// A block of 256 values by one warp, a lane owning eight neighbours: from `raw` (WIDE), or
+// value by value.
 template <typename T, int BITS, bool WIDE>
-__device__ __forceinline__ void block_step(const AdamArgs& a, const Map* maps, const AdamTensor& t, int64_t blk, int lane,
-                                           float gs) {
-  const int64_t base = blk * kAdamBlock + lane * kPer;
+__device__ __forceinline__ void block_step(const AdamArgs& a, const Maps& maps, const Place& at, const Raw<T, BITS>& raw,
+                                           int lane, float gs) {
+  const AdamTensor& t = *at.t;
+  const int64_t blk = at.blk, base = blk * kAdamBlock + lane * kPer;
   T* p = static_cast<T*>(t.param) + base;
   const T* g = static_cast<const T*>(t.grad) + base;
   const int have = WIDE ? kPer : t.n - base >= kPer ? kPer : t.n > base ? static_cast<int>(t.n - base) : 0;
@@ -277,19 +327,17 @@ __device__ __forceinline__ void block_step(const AdamArgs& a, const Map* maps, c
   float *mf = static_cast<float*>(t.m) + base, *vf = static_cast<float*>(t.v) + base;
   float pv[kPer], gv[kPer], m[kPer], v[kPer];
   if (WIDE) {
-    load8(g, gv);
-    load8(p, pv);
-    if (BITS == 8) {
-      const uint2 cm = *reinterpret_cast<const uint2*>(mc), cv = *reinterpret_cast<const uint2*>(vc);
-      const float sm = t.m_absmax[blk], sv = t.v_absmax[blk];
+    raw.widen(raw.g, gv);
+    raw.widen(raw.p, pv);
 #pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        m[k] = __fmul_rn(maps[0].level[((k < 4 ? cm.x : cm.y) >> (8 * (k & 3))) & 255u], sm);
-        v[k] = __fmul_rn(maps[1].level[((k < 4 ? cv.x : cv.y) >> (8 * (k & 3))) & 255u], sv);
+    for (int k = 0; k < kPer; ++k) {
+      if (BITS == 8) {
+        m[k] = __fmul_rn(level(maps.m, raw.m[k >> 2], k & 3), raw.sm);
+        v[k] = __fmul_rn(level(maps.v, raw.v[k >> 2], k & 3), raw.sv);
+      } else {
+        m[k] = __uint_as_float(raw.m[k]);
+        v[k] = __uint_as_float(raw.v[k]);
       }
-    } else {
-      load8(mf, m);
-      load8(vf, v);
     }
   } else {
 #pragma unroll
@@ -298,8 +346,8 @@ __device__ __forceinline__ void block_step(const AdamArgs& a, const Map* maps, c
       gv[k] = in ? to_f32(g[k]) : 0.0f;
       pv[k] = in ? to_f32(p[k]) : 0.0f;
       if (BITS == 8) {
-        m[k] = in ? __fmul_rn(maps[0].level[mc[k]], t.m_absmax[blk]) : 0.0f;
-        v[k] = in ? __fmul_rn(maps[1].level[vc[k]], t.v_absmax[blk]) : 0.0f;
+        m[k] = in ? __fmul_rn(level(maps.m, mc[k], 0), t.m_absmax[blk]) : 0.0f;
+        v[k] = in ? __fmul_rn(level(maps.v, vc[k], 0), t.v_absmax[blk]) : 0.0f;
       } else {
         m[k] = in ? mf[k] : 0.0f;
         v[k] = in ? vf[k] : 0.0f;
@@ -357,34 +405,41 @@ __device__ __forceinline__ void block_step(const AdamArgs& a, const Map* maps, c
     t.m_absmax[blk] = top_m;
     t.v_absmax[blk] = top_v;
   }
-  store_codes<true, WIDE>(maps[0], m, top_m, mc, have);
-  store_codes<false, WIDE>(maps[1], v, top_v, vc, have);
+  store_codes<true, WIDE>(maps.m, m, top_m, mc, have);
+  store_codes<false, WIDE>(maps.v, v, top_v, vc, have);
 }
 
-// Warps walk the blocks of all tensors with the grid's stride.
 template <typename T, int BITS>
 __global__ void __launch_bounds__(kThreads, 2) adamw_kernel(const __grid_constant__ AdamTable tab,
                                                             const __grid_constant__ AdamArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
-  Map* maps = reinterpret_cast<Map*>(smem);
-  if (BITS == 8) build_maps(maps, a.levels_m, a.levels_v);
+  Maps& maps = *reinterpret_cast<Maps*>(smem);
+  if (BITS == 8) {
+    build_map(maps.m, a.levels_m);
+    build_map(maps.v, a.levels_v);
+  }
   const float gs = a.grad_scale ? *a.grad_scale : 1.0f;
   const int lane = threadIdx.x & 31;
-  const int64_t nw = static_cast<int64_t>(gridDim.x) * kWarps, blocks = tab.blk0[tab.count];
+  const int64_t blocks = tab.blk0[tab.count];
+  // A CTA takes one stretch of blocks, its warps in turn: a stretch lies in few tensors.
+  const int64_t per = (blocks + gridDim.x - 1) / gridDim.x, end = min(blocks, (blockIdx.x + 1) * per);
   int ti = -1;
   int64_t first = 0, last = 0;
-  for (int64_t b = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); b < blocks; b += nw) {
+  for (int64_t b = blockIdx.x * per + (threadIdx.x >> 5); b < end; b += kWarps) {
     if (b >= last) {
       ti = find_tensor(tab, b);
       first = tab.blk0[ti];
       last = tab.blk0[ti + 1];
     }
     const AdamTensor& t = tab.t[ti];
-    const int64_t blk = b - first;
-    if (t.vec && (blk + 1) * kAdamBlock <= t.n)
-      block_step<T, BITS, true>(a, maps, t, blk, lane, gs);
-    else
-      block_step<T, BITS, false>(a, maps, t, blk, lane, gs);
+    const Place at{&t, b - first};
+    Raw<T, BITS> raw;
+    if (t.vec && (at.blk + 1) * kAdamBlock <= t.n) {  // all of the block inside, every array fit for vectors
+      raw.load(at, lane);
+      block_step<T, BITS, true>(a, maps, at, raw, lane, gs);
+    } else {
+      block_step<T, BITS, false>(a, maps, at, raw, lane, gs);
+    }
   }
 }
 
@@ -422,7 +477,7 @@ bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % 
 
 template <typename T, int BITS>
 cudaError_t launch_one(const AdamTable& tab, const AdamArgs& a, int sms, cudaStream_t s) {
-  constexpr int kSmem = BITS == 8 ? 2 * static_cast<int>(sizeof(Map)) : 0;
+  constexpr int kSmem = BITS == 8 ? static_cast<int>(sizeof(Maps)) : 0;
   static bool configured = false;
   if (!configured && kSmem > 0) {
     if (cudaError_t e = cudaFuncSetAttribute(adamw_kernel<T, BITS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem))

@@ -182,6 +182,27 @@ struct Frag {
     else
       return to_f32(reinterpret_cast<const T*>(&v[i / VEC])[i % VEC]);
   }
+  // values 2 i and 2 i + 1
+  __device__ __forceinline__ float2 pair(int i) const {
+    if constexpr (VEC > 1 && std::is_same<T, __nv_bfloat16>::value) {
+      const uint32_t w = reinterpret_cast<const uint32_t*>(&v[0])[i];
+      return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    } else if constexpr (VEC > 1 && std::is_same<T, __half>::value) {
+      return __half22float2(reinterpret_cast<const __half2*>(&v[0])[i]);
+    } else {
+      return make_float2(at(2 * i), at(2 * i + 1));
+    }
+  }
+  __device__ __forceinline__ void set_pair(int i, float2 x) {
+    if constexpr (VEC > 1 && std::is_same<T, __nv_bfloat16>::value) {
+      reinterpret_cast<__nv_bfloat162*>(&v[0])[i] = __floats2bfloat162_rn(x.x, x.y);
+    } else if constexpr (VEC > 1 && std::is_same<T, __half>::value) {
+      reinterpret_cast<__half2*>(&v[0])[i] = __floats2half2_rn(x.x, x.y);
+    } else {
+      set(2 * i, x.x);
+      set(2 * i + 1, x.y);
+    }
+  }
   __device__ __forceinline__ void set(int i, float x) {
     if constexpr (VEC == 1)
       v[i] = from_f32<T>(x);
@@ -425,21 +446,40 @@ static __device__ __noinline__ void ring_wait_slow(Ring& r, uint32_t bar, uint32
   }
 }
 
-// The shared memory of a ring CTA: gains [3][H] fp32, then the stages.
-template <typename T, bool BWD>
+constexpr int kPairs = kHold / 2;
+
+// This thread's vectors of a row: their first columns, and whether they lie in the row.
+template <int VEC>
+struct Cols {
+  static constexpr int kVecs = kHold / VEC;
+  uint32_t col[kVecs];
+  bool in[kVecs];
+  __device__ __forceinline__ explicit Cols(const NormArgs& a, int n) {
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) {
+      col[k] = (k * n + threadIdx.x) * VEC;
+      in[k] = col[k] < a.H;
+    }
+  }
+};
+
+// The shared memory of a ring CTA: gains [3][H] fp32 (w_post, scale times the channel
+// gate, w_pre; 1, scale and 0 where there is none), then the stages.
+template <typename T, int VEC, bool BWD>
 struct RowRing {
+  using F = Frag<T, VEC>;
   const NormArgs& a;
   Ring& ring;
-  uint8_t* gains;
+  const Cols<VEC> cols;
+  float* gains;
   uint8_t* stage0;
   uint32_t row_bytes, stage_bytes;
-  int stages, arrays;
+  int stages;
 
-  __device__ __forceinline__ RowRing(const NormArgs& a_, Ring& r, uint8_t* smem, int stages_)
-      : a(a_), ring(r), gains(smem), stages(stages_) {
+  __device__ __forceinline__ RowRing(const NormArgs& a_, Ring& r, uint8_t* smem, int stages_, int n)
+      : a(a_), ring(r), cols(a_, n), gains(reinterpret_cast<float*>(smem)), stages(stages_) {
     row_bytes = static_cast<uint32_t>(a.H * sizeof(T));
-    arrays = 1 + (a.residual != nullptr) + (a.gate_kind == NF4_GATE_TOKEN) + (BWD && a.gz) + (BWD && a.gh);
-    stage_bytes = arrays * row_bytes;
+    stage_bytes = row_bytes * (1 + (a.residual != nullptr) + (a.gate_kind == NF4_GATE_TOKEN) + (BWD && a.gz) + (BWD && a.gh));
     stage0 = smem + 3 * a.H * sizeof(float);
   }
   // Thread 0: the copies of row t into a stage.
@@ -461,34 +501,56 @@ struct RowRing {
     const uint32_t bar = nf4ptx::smem_addr(&ring.full[st]);
     if (!nf4ptx::mbar_test_wait(bar, parity)) ring_wait_slow(ring, bar, parity, status);
   }
-  template <int VEC>
-  __device__ __forceinline__ void gain(float (&g)[kHold], int which, bool have, float none, int n) const {
-    load_gain<T, VEC>(g, have ? reinterpret_cast<const float*>(gains) + which * a.H : nullptr, a.H, n, none);
+  __device__ __forceinline__ void take(F& f, bool have, const uint8_t* row) const {
+    f.clear();
+    if (!have) return;
+#pragma unroll
+    for (int k = 0; k < F::kVecs; ++k)
+      if (cols.in[k]) f.v[k] = *reinterpret_cast<const typename F::Raw*>(row + cols.col[k] * sizeof(T));
+  }
+  __device__ __forceinline__ void put(const F& f, void* row) const {
+#pragma unroll
+    for (int k = 0; k < F::kVecs; ++k)
+      if (cols.in[k]) *reinterpret_cast<typename F::Raw*>(static_cast<T*>(row) + cols.col[k]) = f.v[k];
+  }
+  __device__ __forceinline__ void gain(float2 (&g)[kPairs], int which) const {
+    const float* p = gains + which * a.H;
+#pragma unroll
+    for (int k = 0; k < F::kVecs; ++k)
+#pragma unroll
+      for (int e = 0; e < VEC; e += 4) {
+        float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (cols.in[k]) f = *reinterpret_cast<const float4*>(p + cols.col[k] + e);
+        g[(k * VEC + e) / 2] = make_float2(f.x, f.y);
+        g[(k * VEC + e) / 2 + 1] = make_float2(f.z, f.w);
+      }
+  }
+  // Barriers, the first copies and the gains; ends with a CTA barrier.
+  __device__ __forceinline__ void start(int n) const {
+    if (threadIdx.x == 0) {
+      ring.gave_up = 0;
+      for (int i = 0; i < stages; ++i) nf4ptx::mbar_init(nf4ptx::smem_addr(&ring.full[i]), 1);
+      nf4ptx::fence_mbar_init();
+      for (int i = 0; i < stages; ++i) {
+        const int64_t t = blockIdx.x + static_cast<int64_t>(i) * gridDim.x;
+        if (t < a.T) issue(i, t);
+      }
+    }
+    const float* src[3] = {a.w_post, a.gate_kind == NF4_GATE_CHANNEL ? static_cast<const float*>(a.gate) : nullptr, a.w_pre};
+    const float none[3] = {1.0f, a.scale, 0.0f};
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+      for (int64_t c = threadIdx.x * 4; c < a.H; c += n * 4) {
+        float4 f = make_float4(none[k], none[k], none[k], none[k]);
+        if (src[k]) f = *reinterpret_cast<const float4*>(src[k] + c);
+        if (k == 1 && src[k]) f = make_float4(f.x * a.scale, f.y * a.scale, f.z * a.scale, f.w * a.scale);
+        *reinterpret_cast<float4*>(gains + k * a.H + c) = f;
+      }
+    __syncthreads();
   }
 };
 
-// Set-up common to both directions; returns after the CTA barrier.
-template <typename T, bool BWD>
-__device__ __forceinline__ void ring_start(const RowRing<T, BWD>& rr, int n) {
-  const NormArgs& a = rr.a;
-  if (threadIdx.x == 0) {
-    rr.ring.gave_up = 0;
-    for (int i = 0; i < rr.stages; ++i) nf4ptx::mbar_init(nf4ptx::smem_addr(&rr.ring.full[i]), 1);
-    nf4ptx::fence_mbar_init();
-    for (int i = 0; i < rr.stages; ++i) {
-      const int64_t t = blockIdx.x + static_cast<int64_t>(i) * gridDim.x;
-      if (t < a.T) rr.issue(i, t);
-    }
-  }
-  float* g = reinterpret_cast<float*>(rr.gains);
-  const float* src[3] = {a.w_post, a.gate_kind == NF4_GATE_CHANNEL ? static_cast<const float*>(a.gate) : nullptr, a.w_pre};
-#pragma unroll
-  for (int k = 0; k < 3; ++k)
-    if (src[k])
-      for (int64_t c = threadIdx.x * 4; c < a.H; c += n * 4)
-        *reinterpret_cast<float4*>(g + k * a.H + c) = *reinterpret_cast<const float4*>(src[k] + c);
-  __syncthreads();
-}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 // The rows' sums overlap: while row t's second sum is formed, so is row t + 1's first, and
 // one CTA barrier serves both.
@@ -498,51 +560,43 @@ __global__ void __launch_bounds__(kMaxThreadsFwd) norm_fwd_ring_kernel(const __g
   __shared__ float2 red[2][32];
   __shared__ Ring ring;
   const int n = blockDim.x;
-  const RowRing<T, false> rr(a, ring, smem, stages);
-  ring_start(rr, n);
+  const RowRing<T, VEC, false> rr(a, ring, smem, stages, n);
+  rr.start(n);
   using F = Frag<T, VEC>;
+  const bool token = a.gate_kind == NF4_GATE_TOKEN;
   const float inv_h = 1.0f / static_cast<float>(a.H);
   int st = 0, buf = 0;
   uint32_t ph = 0;
   auto squares = [&](int stage) {  // of this thread's part of y
-    float s = 0.0f;
+    float2 s = both(0.0f);
     if (a.w_post) {
       F y;
-      y.load(rr.stage0 + stage * rr.stage_bytes, a.H, n);
+      rr.take(y, true, rr.stage0 + stage * rr.stage_bytes);
 #pragma unroll
-      for (int i = 0; i < kHold; ++i) s = fmaf(y.at(i), y.at(i), s);
+      for (int i = 0; i < kPairs; ++i) s = fma2(y.pair(i), y.pair(i), s);
     }
-    return s;
+    return s.x + s.y;
   };
   rr.wait(0, 0, a.status);
   float ss_y = block_sum2(make_float2(squares(0), 0.0f), red[1]).x;
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
     const float rstd_y = a.w_post ? rsqrtf(ss_y * inv_h + a.eps) : 1.0f;
     const uint8_t* p = rr.stage0 + st * rr.stage_bytes;
-    F y, r, gt;
-    y.load(p, a.H, n);
-    p += rr.row_bytes;
-    if (a.residual) {
-      r.load(p, a.H, n);
-      p += rr.row_bytes;
-    } else {
-      r.clear();
-    }
-    if (a.gate_kind == NF4_GATE_TOKEN) gt.load(p, a.H, n);
-    float g[kHold], z[kHold], s = 0.0f;
-    rr.template gain<VEC>(z, 0, a.w_post != nullptr, 1.0f, n);
-    rr.template gain<VEC>(g, 1, a.gate_kind == NF4_GATE_CHANNEL, 1.0f, n);
+    F y, r, gt, o;
+    rr.take(y, true, p);
+    rr.take(r, a.residual != nullptr, p + rr.row_bytes);
+    rr.take(gt, token, p + (a.residual ? 2 : 1) * rr.row_bytes);
+    float2 g[kPairs], z[kPairs], s = both(0.0f);
+    rr.gain(z, 0);
+    rr.gain(g, 1);
 #pragma unroll
-    for (int i = 0; i < kHold; ++i) {
-      z[i] = r.at(i) + a.scale * (a.gate_kind == NF4_GATE_TOKEN ? gt.at(i) : g[i]) * (y.at(i) * rstd_y * z[i]);
-      s = fmaf(z[i], z[i], s);
+    for (int i = 0; i < kPairs; ++i) {
+      const float2 nn = mul2(mul2(y.pair(i), both(rstd_y)), z[i]);
+      z[i] = fma2(token ? mul2(gt.pair(i), both(a.scale)) : g[i], nn, r.pair(i));
+      s = fma2(z[i], z[i], s);
+      o.set_pair(i, z[i]);
     }
-    if (a.z) {
-      F o;
-#pragma unroll
-      for (int i = 0; i < kHold; ++i) o.set(i, z[i]);
-      o.store(row_of<T>(a.z, t, a.ld_z), a.H, n);
-    }
+    if (a.z) rr.put(o, row_of<T>(a.z, t, a.ld_z));
     const int st1 = st + 1 == stages ? 0 : st + 1;
     const uint32_t ph1 = st1 == 0 ? ph ^ 1u : ph;
     float s1 = 0.0f;
@@ -550,7 +604,7 @@ __global__ void __launch_bounds__(kMaxThreadsFwd) norm_fwd_ring_kernel(const __g
       rr.wait(st1, ph1, a.status);
       s1 = squares(st1);
     }
-    const float2 sums = block_sum2(make_float2(s, s1), red[buf]);
+    const float2 sums = block_sum2(make_float2(s.x + s.y, s1), red[buf]);
     buf ^= 1;
     ss_y = sums.y;
     const float rstd_z = rsqrtf(sums.x * inv_h + a.eps);
@@ -558,11 +612,10 @@ __global__ void __launch_bounds__(kMaxThreadsFwd) norm_fwd_ring_kernel(const __g
     if (threadIdx.x == 0 && t + static_cast<int64_t>(stages) * gridDim.x < a.T)
       rr.issue(st, t + static_cast<int64_t>(stages) * gridDim.x);
     if (a.h) {
-      F o;
-      rr.template gain<VEC>(g, 2, true, 1.0f, n);
+      rr.gain(g, 2);
 #pragma unroll
-      for (int i = 0; i < kHold; ++i) o.set(i, z[i] * rstd_z * g[i]);
-      o.store(row_of<T>(a.h, t, a.ld_h), a.H, n);
+      for (int i = 0; i < kPairs; ++i) o.set_pair(i, mul2(mul2(z[i], both(rstd_z)), g[i]));
+      rr.put(o, row_of<T>(a.h, t, a.ld_h));
     }
     if (a.stats && threadIdx.x == 0) {
       a.stats[t] = rstd_y;
@@ -582,51 +635,46 @@ __global__ void __launch_bounds__(kMaxThreadsBwd) norm_bwd_ring_kernel(const __g
   __shared__ float2 red[2][32];
   __shared__ Ring ring;
   const int n = blockDim.x;
-  const RowRing<T, true> rr(a, ring, smem, stages);
-  ring_start(rr, n);
+  const RowRing<T, VEC, true> rr(a, ring, smem, stages, n);
+  rr.start(n);
   using F = Frag<T, VEC>;
   const bool token = a.gate_kind == NF4_GATE_TOKEN;
   const float inv_h = 1.0f / static_cast<float>(a.H);
   // places of the arrays in a stage
   const uint32_t at_r = rr.row_bytes, at_t = at_r + (a.residual ? rr.row_bytes : 0), at_z = at_t + (token ? rr.row_bytes : 0),
                  at_h = at_z + (a.gz ? rr.row_bytes : 0);
-  auto take = [&](F& f, bool have, int stage, uint32_t at) {
-    if (have) f.load(rr.stage0 + stage * rr.stage_bytes + at, a.H, n); else f.clear();
-  };
-  auto gains = [&](int k, float (&g)[kHold]) {
-    const bool have = k == 0 ? a.w_post != nullptr : k == 2 ? a.w_pre != nullptr : a.gate_kind == NF4_GATE_CHANNEL;
-    rr.template gain<VEC>(g, k, have, k == 2 ? 0.0f : 1.0f, n);
-  };
-  // z of this thread's columns, with y and n = y rstd_y w_post
-  auto forward = [&](int stage, float rstd_y, F& y, float (&nn)[kHold], float (&sg)[kHold], float (&z)[kHold]) {
+  // z of this thread's columns, with y, n = y rstd_y w_post and scale times the gate
+  auto forward = [&](const uint8_t* row, float rstd_y, F& y, float2 (&nn)[kPairs], float2 (&sg)[kPairs], float2 (&z)[kPairs]) {
     F r, gt;
-    take(y, true, stage, 0);
-    take(r, a.residual != nullptr, stage, at_r);
-    take(gt, token, stage, at_t);
-    gains(0, nn);
-    gains(1, sg);
+    rr.take(y, true, row);
+    rr.take(r, a.residual != nullptr, row + at_r);
+    rr.take(gt, token, row + at_t);
+    rr.gain(nn, 0);
+    rr.gain(sg, 1);
 #pragma unroll
-    for (int i = 0; i < kHold; ++i) {
-      nn[i] *= y.at(i) * rstd_y;
-      sg[i] = a.scale * (token ? gt.at(i) : sg[i]);
-      z[i] = fmaf(sg[i], nn[i], r.at(i));
+    for (int i = 0; i < kPairs; ++i) {
+      nn[i] = mul2(nn[i], mul2(y.pair(i), both(rstd_y)));
+      if (token) sg[i] = mul2(gt.pair(i), both(a.scale));
+      z[i] = fma2(sg[i], nn[i], r.pair(i));
     }
   };
   auto first_sum = [&](int stage, float rstd_y) {  // of z gh w_pre
-    float s = 0.0f;
+    float2 s = both(0.0f);
     if (a.gh) {
+      const uint8_t* row = rr.stage0 + stage * rr.stage_bytes;
       F y, gh;
-      float nn[kHold], sg[kHold], z[kHold];
-      forward(stage, rstd_y, y, nn, sg, z);
-      take(gh, true, stage, at_h);
-      gains(2, nn);
+      float2 nn[kPairs], sg[kPairs], z[kPairs];
+      forward(row, rstd_y, y, nn, sg, z);
+      rr.take(gh, true, row + at_h);
+      rr.gain(nn, 2);
 #pragma unroll
-      for (int i = 0; i < kHold; ++i) s = fmaf(z[i], gh.at(i) * nn[i], s);
+      for (int i = 0; i < kPairs; ++i) s = fma2(z[i], mul2(gh.pair(i), nn[i]), s);
     }
-    return s;
+    return s.x + s.y;
   };
-  Sums sum;
-  sum.clear();
+  float2 sum_pre[kPairs], sum_post[kPairs], sum_gate[kPairs];
+#pragma unroll
+  for (int i = 0; i < kPairs; ++i) sum_pre[i] = sum_post[i] = sum_gate[i] = both(0.0f);
   int st = 0, buf = 0;
   uint32_t ph = 0;
   float rstd_y = a.stats[blockIdx.x], rstd_z = a.stats[a.T + blockIdx.x];
@@ -638,33 +686,34 @@ __global__ void __launch_bounds__(kMaxThreadsBwd) norm_bwd_ring_kernel(const __g
     // dz = gz + rstd_z gh w_pre - z rstd_z^3 mean(z gh w_pre)
     const float pull = rstd_z * rstd_z * rstd_z * dot * inv_h;
     F y;
-    float b[kHold], s = 0.0f;
+    float2 b[kPairs], s = both(0.0f);
     {
+      const uint8_t* row = rr.stage0 + st * rr.stage_bytes;
       F gz, gh, gr, gg;
-      float nn[kHold], sg[kHold], z[kHold], w[kHold];
-      forward(st, rstd_y, y, nn, sg, z);
-      take(gz, a.gz != nullptr, st, at_z);
-      take(gh, a.gh != nullptr, st, at_h);
-      gains(2, w);
+      float2 nn[kPairs], z[kPairs], w[kPairs];
+      forward(row, rstd_y, y, nn, b, z);
+      rr.take(gz, a.gz != nullptr, row + at_z);
+      rr.take(gh, a.gh != nullptr, row + at_h);
+      rr.gain(w, 2);
 #pragma unroll
-      for (int i = 0; i < kHold; ++i) {
-        const float ghz = gh.at(i) * rstd_z;
-        const float dz = fmaf(-pull, z[i], fmaf(ghz, w[i], gz.at(i)));
-        gr.set(i, dz);
-        gg.set(i, a.scale * dz * nn[i]);
-        b[i] = sg[i] * dz;
-        sum.pre[i] = fmaf(ghz, z[i], sum.pre[i]);
-        sum.gate[i] = fmaf(dz, nn[i], sum.gate[i]);
+      for (int i = 0; i < kPairs; ++i) {
+        const float2 ghz = mul2(gh.pair(i), both(rstd_z));
+        const float2 dz = fma2(both(-pull), z[i], fma2(ghz, w[i], gz.pair(i)));
+        gr.set_pair(i, dz);
+        if (token) gg.set_pair(i, mul2(mul2(dz, both(a.scale)), nn[i]));
+        b[i] = mul2(b[i], dz);
+        sum_pre[i] = fma2(ghz, z[i], sum_pre[i]);
+        if (!token) sum_gate[i] = fma2(dz, nn[i], sum_gate[i]);
       }
-      if (a.gr) gr.store(row_of<T>(a.gr, t, a.ld_gr), a.H, n);
-      if (token && a.ggate) gg.store(row_of<T>(a.ggate, t, a.ld_ggate), a.H, n);
-      gains(0, w);
+      if (a.gr) rr.put(gr, row_of<T>(a.gr, t, a.ld_gr));
+      if (token && a.ggate) rr.put(gg, row_of<T>(a.ggate, t, a.ld_ggate));
+      rr.gain(w, 0);
 #pragma unroll
-      for (int i = 0; i < kHold; ++i) {
-        const float yhat = y.at(i) * rstd_y;
-        sum.post[i] = fmaf(b[i], yhat, sum.post[i]);
-        b[i] *= w[i];
-        s = fmaf(yhat, b[i], s);
+      for (int i = 0; i < kPairs; ++i) {
+        const float2 yhat = mul2(y.pair(i), both(rstd_y));
+        sum_post[i] = fma2(b[i], yhat, sum_post[i]);
+        b[i] = mul2(b[i], w[i]);
+        s = fma2(yhat, b[i], s);
       }
     }
     const int st1 = st + 1 == stages ? 0 : st + 1;
@@ -674,7 +723,7 @@ __global__ void __launch_bounds__(kMaxThreadsBwd) norm_bwd_ring_kernel(const __g
       rr.wait(st1, ph1, a.status);
       s1 = first_sum(st1, rstd_y1);
     }
-    const float2 sums = block_sum2(make_float2(s, s1), red[buf]);
+    const float2 sums = block_sum2(make_float2(s.x + s.y, s1), red[buf]);
     buf ^= 1;
     // every thread has read its part of row t
     if (threadIdx.x == 0 && t + static_cast<int64_t>(stages) * gridDim.x < a.T)
@@ -684,8 +733,8 @@ __global__ void __launch_bounds__(kMaxThreadsBwd) norm_bwd_ring_kernel(const __g
       const float back = a.w_post ? rstd_y * rstd_y * sums.x * inv_h : 0.0f;
       F gy;
 #pragma unroll
-      for (int i = 0; i < kHold; ++i) gy.set(i, fmaf(-back, y.at(i), rstd_y * b[i]));
-      gy.store(row_of<T>(a.gy, t, a.ld_gy), a.H, n);
+      for (int i = 0; i < kPairs; ++i) gy.set_pair(i, fma2(both(-back), y.pair(i), mul2(both(rstd_y), b[i])));
+      rr.put(gy, row_of<T>(a.gy, t, a.ld_gy));
     }
     dot = sums.y;
     rstd_y = rstd_y1;
@@ -693,8 +742,16 @@ __global__ void __launch_bounds__(kMaxThreadsBwd) norm_bwd_ring_kernel(const __g
     st = st1;
     ph = ph1;
   }
+  Sums sum;
 #pragma unroll
-  for (int i = 0; i < kHold; ++i) sum.gate[i] *= a.scale;
+  for (int i = 0; i < kPairs; ++i) {
+    sum.pre[2 * i] = sum_pre[i].x;
+    sum.pre[2 * i + 1] = sum_pre[i].y;
+    sum.post[2 * i] = sum_post[i].x;
+    sum.post[2 * i + 1] = sum_post[i].y;
+    sum.gate[2 * i] = sum_gate[i].x * a.scale;
+    sum.gate[2 * i + 1] = sum_gate[i].y * a.scale;
+  }
   store_sums<T, VEC>(a, sum, n);
 }
 
