@@ -4,9 +4,9 @@ The compute lives in ``libnf4.so`` (hand-written CUDA, C ABI in ``include/nf4.h`
 this package is its thin binding plus the autograd Functions.  Importing it does
 not load the library; the first call does, and fails loudly if it is not built.
 """
-from .autograd import (NF4GroupedFn, NF4GroupedSwiGLUFn, NF4Linear, NF4LinearFn, NF4MoECombineFn,
-                       NF4MultiLinearFn, nf4_combine, nf4_grouped, nf4_grouped_swiglu, nf4_linear,
-                       nf4_linear_multi)
+from .autograd import (NF4AttentionFn, NF4GroupedFn, NF4GroupedSwiGLUFn, NF4Linear, NF4LinearFn, NF4MoECombineFn,
+                       NF4MultiLinearFn, NF4NormResidualFn, nf4_attention, nf4_combine, nf4_grouped, nf4_grouped_swiglu,
+                       nf4_linear, nf4_linear_multi, nf4_norm_residual)
 from .block_ops import (AdamWState, adamw_state, adamw_state_values, adamw_step, attention_bwd, attention_fwd,
                         norm_residual_bwd, norm_residual_fwd)
 from .codebooks import (code4_for, code_for, dynamic_code8, dynamic_code8_unsigned, e4m3_code8, fp4_code4,
@@ -16,6 +16,7 @@ from .ops import (NF4Weight, dequantize, device_check, device_status, grouped_dg
                   linear_dgrad, linear_dgrad_multi, linear_fwd, linear_fwd_multi, moe_combine,
                   moe_combine_bwd, path_counters, quantize, reset_path_counters, route_rows,
                   workspace_size)
+from .optim import NF4AdamW
 
 # The C-ABI names.
 nf4_quantize = quantize
@@ -53,4 +54,5 @@ __all__ = [
     "AdamWState", "adamw_state", "adamw_state_values", "adamw_step", "attention_bwd", "attention_fwd",
     "norm_residual_bwd", "norm_residual_fwd", "dynamic_code8_unsigned", "nf4_attention_fwd", "nf4_attention_bwd",
     "nf4_norm_residual_fwd", "nf4_norm_residual_bwd", "nf4_adamw_step", "nf4_adamw_state_values",
+    "NF4AttentionFn", "NF4NormResidualFn", "nf4_attention", "nf4_norm_residual", "NF4AdamW",
 ]

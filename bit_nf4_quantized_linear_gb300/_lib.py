@@ -137,7 +137,7 @@ def lib() -> ctypes.CDLL:
         L = ctypes.CDLL(LIB_PATH)
         P, I64, I32, SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
         W = ctypes.POINTER(nf4_weight)
-        NR, AT, F64 = ctypes.POINTER(nf4_norm_residual), ctypes.POINTER(nf4_attention), ctypes.c_double
+        NR, AT, F64 = P, P, ctypes.c_double  # structs by reference or as packed bytes
         sig = {
             "nf4_quantize": [P, I32, I64, I64, I32, I32, I32, P, P, P, P, P, P, P, P, SZ, P],
             "nf4_quantize_8bit": [P, I32, I64, I64, I32, I32, I32, P, P, P, P, P, P, P, P, SZ, P],

@@ -17,7 +17,7 @@ from __future__ import annotations
 
 import torch
 
-from . import ops
+from . import block_ops, ops
 
 
 class NF4LinearFn(torch.autograd.Function):
@@ -183,6 +183,70 @@ class NF4MoECombineFn(torch.autograd.Function):
 def nf4_combine(rows: torch.Tensor, token_rows: torch.Tensor) -> torch.Tensor:
     """Sum each token's routed expert rows (bf16; see ops.route_rows for the table)."""
     return NF4MoECombineFn.apply(rows, token_rows)
+
+
+class NF4AttentionFn(torch.autograd.Function):
+    """Causal attention over packed sequences (nf4_attention_fwd) and its gradients
+    (nf4_attention_bwd).  Inputs, output and row statistics go through
+    save_for_backward; ctx holds the scale."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, cu_seqlens, scale):
+        o, lse = block_ops.attention_fwd(q, k, v, cu_seqlens, scale)
+        ctx.save_for_backward(q, k, v, o, lse, cu_seqlens)
+        ctx.scale = scale
+        return o
+
+    @staticmethod
+    def backward(ctx, go):
+        q, k, v, o, lse, cu_seqlens = ctx.saved_tensors
+        if go.stride(2) != 1:
+            go = go.contiguous()
+        gq, gk, gv = block_ops.attention_bwd(go, q, k, v, o, lse, cu_seqlens, ctx.scale)
+        return gq, gk, gv, None, None
+
+
+def nf4_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor = None,
+                  scale: float = None) -> torch.Tensor:
+    """Causal softmax attention of packed sequences: q [T, Hq, D] over k, v [T, Hk, D] (query head h reads
+    key head h // (Hq // Hk)), bf16, fp16 or fp32.  `cu_seqlens` int32 [sequences + 1] on the device holds
+    the row offsets (None: one sequence); rows outside them give zeros.  `scale` defaults to D ** -0.5."""
+    return NF4AttentionFn.apply(q, k, v, cu_seqlens, scale)
+
+
+class NF4NormResidualFn(torch.autograd.Function):
+    """The gated residual norm (nf4_norm_residual_fwd / _bwd).  The inputs and the rows' statistics are
+    saved; z is recomputed from them in the backward."""
+
+    @staticmethod
+    def forward(ctx, y, residual, w_post, gate, w_pre, scale, eps):
+        z, h, stats = block_ops.norm_residual_fwd(y, residual, w_post=w_post, gate=gate, scale=scale, w_pre=w_pre, eps=eps)
+        ctx.save_for_backward(y, residual, w_post, gate, w_pre, stats)
+        ctx.scale, ctx.eps = scale, eps
+        ctx.set_materialize_grads(False)
+        return (y.view_as(y) if z is y else z), h
+
+    @staticmethod
+    def backward(ctx, gz, gh):
+        y, residual, w_post, gate, w_pre, stats = ctx.saved_tensors
+        if gz is None and gh is None:
+            return (None,) * 7
+        gz, gh = (g if g is None or g.stride(1) == 1 and g.stride(0) >= g.shape[1] else g.contiguous() for g in (gz, gh))
+        need = ctx.needs_input_grad
+        gy, gr, gw_post, ggate, gw_pre = block_ops.norm_residual_bwd(
+            gz, gh, y, residual, stats, w_post=w_post, gate=gate, scale=ctx.scale, w_pre=w_pre, eps=ctx.eps, need_y=need[0],
+            need_residual=need[1], need_vectors=need[2] or need[3] or need[4])
+        return tuple(g if n else None for g, n in zip((gy, gr, gw_post, ggate, gw_pre), need)) + (None, None)
+
+
+def nf4_norm_residual(y: torch.Tensor, residual: torch.Tensor = None, *, w_post: torch.Tensor = None,
+                      gate: torch.Tensor = None, scale: float = 1.0, w_pre: torch.Tensor = None, eps: float = 1e-6) -> tuple:
+    """The norms around a block with its gate, residual scale and sum in one pass:
+    z = residual + scale * gate * norm(y; w_post) and h = norm(z; w_pre).  y is the block's output and
+    residual the stream it joins ([T, H]); z is the new stream and h the next block's input.  Gains are
+    fp32 [H]; the gate is fp32 [H] or [T, H] in y's dtype.  Every part but y may be left out (w_pre None:
+    h is None; y with w_pre alone is a plain norm before the first block).  Returns (z, h)."""
+    return NF4NormResidualFn.apply(y, residual, w_post, gate, w_pre, float(scale), float(eps))
 
 
 def nf4_linear(x: torch.Tensor, w: ops.NF4Weight) -> torch.Tensor:

@@ -6,15 +6,41 @@ the computation runs in the library's kernels, and there is no CPU path.
 """
 from __future__ import annotations
 
-import ctypes
+import functools
+import itertools
+import struct
 from typing import Optional, Sequence
 
 import torch
 
 from . import _lib, codebooks
-from .ops import _device_codebook, _need_cuda, _ptr, _stream, workspace_size
+from .ops import _device_codebook, _need_cuda, _ptr, workspace_size
+
+# The calls of a training step are short next to what the host spends on them, so the
+# wrappers check their arguments in single expressions (a failed one is then explained by a
+# slower function), pass structs as packed bytes and look the library's functions up once.
 
 _DTYPES = {torch.float32: _lib.DTYPE_F32, torch.bfloat16: _lib.DTYPE_BF16, torch.float16: _lib.DTYPE_F16}
+_ATTENTION = struct.Struct("@3P6qP2q4if4x")     # nf4_attention
+_NORM = struct.Struct("@PqPqPqPP2q2i2f")        # nf4_norm_residual
+_FNS = {}
+
+
+def _fn(name: str):
+    f = _FNS.get(name)
+    if f is None:
+        f = _FNS[name] = getattr(_lib.lib(), name)
+    return f
+
+
+def _raw_stream(device: torch.device) -> int:
+    """The current stream of `device` (which has to be the current device, as for every launch)."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+@functools.lru_cache(maxsize=4096)
+def _workspace(op: int, M: int, N: int, device: torch.device) -> int:
+    return workspace_size(op, M, N, 0)
 
 
 def _one_device(name: str, *ts):
@@ -32,35 +58,50 @@ def _dtype(name: str, t: torch.Tensor) -> int:
 
 # ------------------------------------------------------------------- attention --
 
-def _heads(name: str, what: str, t: torch.Tensor, like: torch.Tensor, shape: tuple) -> torch.Tensor:
-    """t as a [T, heads, D] operand with unit stride within a head; `shape` may hold None for a free size."""
+def _heads(name: str, what: str, t: torch.Tensor, like: torch.Tensor, shape: tuple):
+    """Explains why t is no [T, heads, D] operand; `shape` may hold None for a free size."""
     if t.dim() != 3 or any(n is not None and n != s for n, s in zip(shape, t.shape)):
         raise ValueError(f"{name}: {what} must have shape {shape}, got {tuple(t.shape)}")
     if t.dtype != like.dtype:
         raise ValueError(f"{name}: {what} must have q's dtype")
     if t.shape[2] > 1 and t.stride(2) != 1:
         raise ValueError(f"{name}: {what} must have unit stride within a head")
-    return t
 
 
-def _attention(name, q, k, v, cu_seqlens, scale, more=()):
-    _one_device(name, q, k, v, cu_seqlens, *more)
-    dt = _dtype(name, q)
+def _explain_attention(name, q, k, v, cu_seqlens, like_q):
+    _one_device(name, q, k, v, cu_seqlens, *(t for _, t in like_q))
+    _dtype(name, q)
     _heads(name, "q", q, q, (None, None, None))
     T, Hq, D = q.shape
     _heads(name, "k", k, q, (T, None, D))
     _heads(name, "v", v, q, tuple(k.shape))
+    for what, t in like_q:
+        _heads(name, what, t, q, (T, Hq, D))
     Hk = k.shape[1]
     if Hk == 0 or Hq == 0 or Hq % Hk != 0:
         raise ValueError(f"{name}: {Hq} query heads do not divide into groups over {Hk} key heads")
-    nseq = 0
+    raise ValueError(f"{name}: cu_seqlens must be a contiguous int32 [sequences + 1] tensor")
+
+
+def _attention(name, q, k, v, cu_seqlens, scale, like_q=()):
+    """The packed nf4_attention of checked arguments; like_q: (what, tensor) of q's shape and dtype."""
+    dt, dev, qs, ks, qt, kt, vt = q.dtype, q.device, q.shape, k.shape, q.stride(), k.stride(), v.stride()
+    ok = (dt in _DTYPES and dev.type == "cuda" and k.dtype is dt and v.dtype is dt and k.device == dev and v.device == dev
+          and len(qs) == 3 and len(ks) == 3 and ks == v.shape and ks[0] == qs[0] and ks[2] == qs[2] and ks[1] > 0
+          and qs[1] > 0 and qs[1] % ks[1] == 0 and (qs[2] == 1 or qt[2] == kt[2] == vt[2] == 1))
+    for _, t in like_q if ok else ():
+        ok = ok and t.dtype is dt and t.device == dev and t.shape == qs and (qs[2] == 1 or t.stride(2) == 1)
+    nseq = cu = 0
     if cu_seqlens is not None:
-        if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or not cu_seqlens.is_contiguous() or cu_seqlens.numel() < 2:
-            raise ValueError(f"{name}: cu_seqlens must be a contiguous int32 [sequences + 1] tensor")
         nseq = cu_seqlens.numel() - 1
-    return _lib.nf4_attention(q.data_ptr(), k.data_ptr(), v.data_ptr(), q.stride(0), q.stride(1), k.stride(0), k.stride(1),
-                              v.stride(0), v.stride(1), _ptr(cu_seqlens), nseq, T, Hq, Hk, D, dt,
-                              D ** -0.5 if scale is None else float(scale))
+        cu = cu_seqlens.data_ptr()
+        ok = (ok and cu_seqlens.dtype is torch.int32 and cu_seqlens.dim() == 1 and nseq > 0 and cu_seqlens.stride(0) == 1
+              and cu_seqlens.device == dev)
+    if not ok:
+        _explain_attention(name, q, k, v, cu_seqlens, like_q)
+    T, Hq, D = qs
+    return _ATTENTION.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), qt[0], qt[1], kt[0], kt[1], vt[0], vt[1], cu, nseq, T,
+                           Hq, ks[1], D, _DTYPES[dt], D ** -0.5 if scale is None else scale)
 
 
 def attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None,
@@ -68,70 +109,95 @@ def attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens:
     """nf4_attention_fwd: causal attention of packed sequences, q [T, Hq, D] over k, v [T, Hk, D]
     (any token and head strides).  `cu_seqlens` int32 [sequences + 1] holds the row offsets (None:
     one sequence); rows outside them give zeros.  Returns (o [T, Hq, D], lse fp32 [Hq, T])."""
-    d = _attention("attention_fwd", q, k, v, cu_seqlens, scale, (out,))
-    o = torch.empty(q.shape, dtype=q.dtype, device=q.device) if out is None else _heads(
-        "attention_fwd", "out", out, q, tuple(q.shape))
-    lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
-    _lib.check(_lib.lib().nf4_attention_fwd(ctypes.byref(d), o.data_ptr(), o.stride(0), o.stride(1), lse.data_ptr(),
-                                            _stream()), "nf4_attention_fwd")
+    d = _attention("attention_fwd", q, k, v, cu_seqlens, scale, () if out is None else (("out", out),))
+    T, Hq, D = q.shape
+    o = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device) if out is None else out
+    lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
+    ot, oh, _ = o.stride()
+    rc = _fn("nf4_attention_fwd")(d, o.data_ptr(), ot, oh, lse.data_ptr(), _raw_stream(q.device))
+    if rc:
+        _lib.check(rc, "nf4_attention_fwd")
     return o, lse
 
 
 def attention_bwd(go: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
                   lse: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None, scale: Optional[float] = None):
     """nf4_attention_bwd: the gradients (gq, gk, gv) of attention_fwd from its o, lse and go = dL/do."""
-    name = "attention_bwd"
-    d = _attention(name, q, k, v, cu_seqlens, scale, (go, o, lse))
-    _heads(name, "go", go, q, tuple(q.shape))
-    _heads(name, "o", o, q, tuple(q.shape))
-    T, Hq, _ = q.shape
-    if lse.dtype != torch.float32 or tuple(lse.shape) != (Hq, T) or not lse.is_contiguous():
-        raise ValueError(f"{name}: lse must be the contiguous fp32 [Hq, T] of the forward")
-    gq, gk, gv = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))
-    need = workspace_size(_lib.OP_ATTENTION_BWD, T, Hq, 0)
-    ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-    _lib.check(_lib.lib().nf4_attention_bwd(
-        ctypes.byref(d), o.data_ptr(), o.stride(0), o.stride(1), lse.data_ptr(), go.data_ptr(), go.stride(0), go.stride(1),
-        gq.data_ptr(), gq.stride(0), gq.stride(1), gk.data_ptr(), gk.stride(0), gk.stride(1),
-        gv.data_ptr(), gv.stride(0), gv.stride(1), ws.data_ptr(), need, _stream()), name)
+    d = _attention("attention_bwd", q, k, v, cu_seqlens, scale, (("go", go), ("o", o)))
+    T, Hq, D = q.shape
+    dev, dt = q.device, q.dtype
+    if lse.dtype is not torch.float32 or lse.shape != (Hq, T) or not lse.is_contiguous() or lse.device != dev:
+        raise ValueError("attention_bwd: lse must be the contiguous fp32 [Hq, T] of the forward")
+    Hk = k.shape[1]
+    gq = torch.empty((T, Hq, D), dtype=dt, device=dev)
+    gk = torch.empty((T, Hk, D), dtype=dt, device=dev)
+    gv = torch.empty((T, Hk, D), dtype=dt, device=dev)
+    need = _workspace(_lib.OP_ATTENTION_BWD, T, Hq, dev)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    ot, oh, _ = o.stride()
+    gt, gh, _ = go.stride()
+    rc = _fn("nf4_attention_bwd")(d, o.data_ptr(), ot, oh, lse.data_ptr(), go.data_ptr(), gt, gh, gq.data_ptr(), Hq * D, D,
+                                  gk.data_ptr(), Hk * D, D, gv.data_ptr(), Hk * D, D, ws.data_ptr(), need, _raw_stream(dev))
+    if rc:
+        _lib.check(rc, "nf4_attention_bwd")
     return gq, gk, gv
 
 
 # --------------------------------------------------------- gated residual norm --
 
-def _rows(name: str, what: str, t: Optional[torch.Tensor], like: torch.Tensor):
-    if t is None:
-        return
-    if t.shape != like.shape or t.dtype != like.dtype or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name}: {what} must be a {like.dtype} {tuple(like.shape)} tensor with unit column stride")
-
-
-def _pitch(t: Optional[torch.Tensor]) -> int:
-    return 0 if t is None else max(t.stride(0), t.shape[1])
-
-
-def _norm(name, y, residual, w_post, gate, scale, w_pre, eps, more=()):
-    _one_device(name, y, residual, w_post, gate, w_pre, *more)
-    dt = _dtype(name, y)
+def _explain_norm(name, y, w_post, gate, w_pre, rows):
+    _one_device(name, y, w_post, gate, w_pre, *(t for _, t in rows))
+    _dtype(name, y)
     if y.dim() != 2 or y.shape[1] < 1:
         raise ValueError(f"{name}: y must be [tokens, width]")
-    _rows(name, "y", y, y)
-    _rows(name, "residual", residual, y)
-    T, H = y.shape
-    for what, w in (("w_post", w_post), ("w_pre", w_pre)):
-        if w is not None and (w.dtype != torch.float32 or tuple(w.shape) != (H,) or not w.is_contiguous()):
+    H = y.shape[1]
+    for what, t in (("y", y), ("a token gate", gate if gate is not None and gate.dim() != 1 else None), *rows):
+        if t is not None and (t.shape != y.shape or t.dtype != y.dtype or (H > 1 and t.stride(1) != 1)):
+            raise ValueError(f"{name}: {what} must be a {y.dtype} {tuple(y.shape)} tensor with unit column stride")
+    for what, w in (("w_post", w_post), ("w_pre", w_pre), ("a channel gate", gate)):
+        if w is not None and w.dim() == 1 and (w.dtype != torch.float32 or tuple(w.shape) != (H,) or not w.is_contiguous()):
             raise ValueError(f"{name}: {what} must be a contiguous fp32 [{H}] tensor")
-    kind = _lib.GATE_NONE
-    if gate is not None and gate.dim() == 1:
-        kind = _lib.GATE_CHANNEL
-        if gate.dtype != torch.float32 or tuple(gate.shape) != (H,) or not gate.is_contiguous():
-            raise ValueError(f"{name}: a channel gate must be a contiguous fp32 [{H}] tensor")
-    elif gate is not None:
-        kind = _lib.GATE_TOKEN
-        _rows(name, "a token gate", gate, y)
-    return _lib.nf4_norm_residual(y.data_ptr(), _pitch(y), _ptr(residual), _pitch(residual), _ptr(gate),
-                                  _pitch(gate) if kind == _lib.GATE_TOKEN else 0, _ptr(w_post), _ptr(w_pre), T, H, kind,
-                                  dt, float(scale), float(eps))
+    raise ValueError(f"{name}: the gains must be contiguous fp32 [{H}] tensors")
+
+
+def _norm(name, y, w_post, gate, scale, w_pre, eps, rows):
+    """The packed nf4_norm_residual of checked arguments, the gate's kind, and the row pitches of `rows`, which
+    starts with the residual: (what, tensor or None) of y's shape and dtype."""
+    dt, dev, ys = y.dtype, y.device, y.shape
+    H = ys[-1] if len(ys) == 2 else 0
+    ok = dt in _DTYPES and dev.type == "cuda" and H > 0 and (H == 1 or y.stride(1) == 1)
+    kind, gp, gl = _lib.GATE_NONE, 0, 0
+    wp = wn = 0
+    pitches = []
+    if ok:
+        for _, t in rows:
+            if t is None:
+                pitches.append(0)
+                continue
+            ok = ok and t.dtype is dt and t.device == dev and t.shape == ys and (H == 1 or t.stride(1) == 1)
+            pitches.append(max(t.stride(0), H) if ok else 0)
+        if w_post is not None:
+            wp = w_post.data_ptr()
+            ok = (ok and w_post.dtype is torch.float32 and w_post.shape == (H,) and w_post.device == dev
+                  and w_post.is_contiguous())
+        if w_pre is not None:
+            wn = w_pre.data_ptr()
+            ok = ok and w_pre.dtype is torch.float32 and w_pre.shape == (H,) and w_pre.device == dev and w_pre.is_contiguous()
+        if gate is not None:
+            gp = gate.data_ptr()
+            if gate.dim() == 1:
+                kind = _lib.GATE_CHANNEL
+                ok = ok and gate.dtype is torch.float32 and gate.shape == (H,) and gate.device == dev and gate.is_contiguous()
+            else:
+                kind = _lib.GATE_TOKEN
+                ok = ok and gate.dtype is dt and gate.device == dev and gate.shape == ys and (H == 1 or gate.stride(1) == 1)
+                gl = max(gate.stride(0), H) if ok else 0
+    if not ok:
+        _explain_norm(name, y, w_post, gate, w_pre, rows)
+    residual = rows[0][1]
+    d = _NORM.pack(y.data_ptr(), max(y.stride(0), H), 0 if residual is None else residual.data_ptr(), pitches[0], gp, gl, wp,
+                   wn, ys[0], H, kind, _DTYPES[dt], scale, eps)
+    return d, kind, pitches
 
 
 def norm_residual_fwd(y: torch.Tensor, residual: Optional[torch.Tensor] = None, *, w_post: Optional[torch.Tensor] = None,
@@ -141,15 +207,15 @@ def norm_residual_fwd(y: torch.Tensor, residual: Optional[torch.Tensor] = None, 
     norms being x / sqrt(mean(x^2) + eps) * w.  y, residual [T, H]; w_post, w_pre fp32 [H] (w_post None:
     y itself; w_pre None: no h); gate fp32 [H], or [T, H] in y's dtype, or None.  Returns (z, h, stats);
     z is y itself where nothing changes it, and stats (fp32 [2, T]) is what the backward needs."""
-    name = "norm_residual_fwd"
-    d = _norm(name, y, residual, w_post, gate, scale, w_pre, eps)
-    same = residual is None and w_post is None and gate is None and float(scale) == 1.0
-    T, H = y.shape
-    z = y if same else torch.empty((T, H), dtype=y.dtype, device=y.device)
-    h = None if w_pre is None else torch.empty((T, H), dtype=y.dtype, device=y.device)
-    stats = torch.empty((2, T), dtype=torch.float32, device=y.device)
-    _lib.check(_lib.lib().nf4_norm_residual_fwd(ctypes.byref(d), None if same else z.data_ptr(), H, _ptr(h), H,
-                                                stats.data_ptr(), _stream()), "nf4_norm_residual_fwd")
+    d, _, _ = _norm("norm_residual_fwd", y, w_post, gate, scale, w_pre, eps, (("residual", residual),))
+    same = residual is None and w_post is None and gate is None and scale == 1.0
+    (T, H), dt, dev = y.shape, y.dtype, y.device
+    z = y if same else torch.empty((T, H), dtype=dt, device=dev)
+    h = None if w_pre is None else torch.empty((T, H), dtype=dt, device=dev)
+    stats = torch.empty((2, T), dtype=torch.float32, device=dev)
+    rc = _fn("nf4_norm_residual_fwd")(d, None if same else z.data_ptr(), H, _ptr(h), H, stats.data_ptr(), _raw_stream(dev))
+    if rc:
+        _lib.check(rc, "nf4_norm_residual_fwd")
     return z, h, stats
 
 
@@ -162,31 +228,29 @@ def norm_residual_bwd(gz: Optional[torch.Tensor], gh: Optional[torch.Tensor], y:
     ones (`need_vectors` covers the two gains and the gate).  gw_* and a channel gate's gradient are
     fp32 [H]; a token gate's has the gate's shape and dtype."""
     name = "norm_residual_bwd"
-    d = _norm(name, y, residual, w_post, gate, scale, w_pre, eps, (gz, gh, stats))
-    _rows(name, "gz", gz, y)
-    _rows(name, "gh", gh, y)
-    T, H = y.shape
-    if stats.dtype != torch.float32 or tuple(stats.shape) != (2, T) or not stats.is_contiguous():
+    d, kind, (_, pitch_z, pitch_h) = _norm(name, y, w_post, gate, scale, w_pre, eps,
+                                           (("residual", residual), ("gz", gz), ("gh", gh)))
+    (T, H), dt, dev = y.shape, y.dtype, y.device
+    if stats.dtype is not torch.float32 or stats.shape != (2, T) or not stats.is_contiguous() or stats.device != dev:
         raise ValueError(f"{name}: stats must be the contiguous fp32 [2, T] of the forward")
     if gh is not None and w_pre is None:
         raise ValueError(f"{name}: gh without w_pre")
-
-    def rows(want):
-        return torch.empty((T, H), dtype=y.dtype, device=y.device) if want else None
-
-    def vector(want):
-        return torch.empty(H, dtype=torch.float32, device=y.device) if want and need_vectors else None
-
-    gy, gr = rows(need_y), rows(need_residual and residual is not None)
-    gw_post, gw_pre = vector(w_post is not None), vector(w_pre is not None)
-    ggate = rows(need_vectors) if d.gate_kind == _lib.GATE_TOKEN else vector(gate is not None)
+    f32 = torch.float32
+    gy = torch.empty((T, H), dtype=dt, device=dev) if need_y else None
+    gr = torch.empty((T, H), dtype=dt, device=dev) if need_residual and residual is not None else None
+    gw_post = torch.empty(H, dtype=f32, device=dev) if need_vectors and w_post is not None else None
+    gw_pre = torch.empty(H, dtype=f32, device=dev) if need_vectors and w_pre is not None else None
+    ggate = None
+    if need_vectors and kind != _lib.GATE_NONE:
+        ggate = torch.empty((T, H), dtype=dt, device=dev) if kind == _lib.GATE_TOKEN else torch.empty(H, dtype=f32, device=dev)
     ws, need = None, 0
-    if gw_post is not None or gw_pre is not None or (ggate is not None and d.gate_kind == _lib.GATE_CHANNEL):
-        need = workspace_size(_lib.OP_NORM_RESIDUAL_BWD, T, H, 0)
-        ws = torch.empty(need, dtype=torch.uint8, device=y.device)
-    _lib.check(_lib.lib().nf4_norm_residual_bwd(
-        ctypes.byref(d), stats.data_ptr(), _ptr(gz), _pitch(gz), _ptr(gh), _pitch(gh), _ptr(gy), H, _ptr(gr), H,
-        _ptr(gw_post), _ptr(ggate), H, _ptr(gw_pre), _ptr(ws), need, _stream()), "nf4_norm_residual_bwd")
+    if gw_post is not None or gw_pre is not None or (ggate is not None and kind == _lib.GATE_CHANNEL):
+        need = _workspace(_lib.OP_NORM_RESIDUAL_BWD, T, H, dev)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    rc = _fn("nf4_norm_residual_bwd")(d, stats.data_ptr(), _ptr(gz), pitch_z, _ptr(gh), pitch_h, _ptr(gy), H, _ptr(gr), H,
+                                      _ptr(gw_post), _ptr(ggate), H, _ptr(gw_pre), _ptr(ws), need, _raw_stream(dev))
+    if rc:
+        _lib.check(rc, "nf4_norm_residual_bwd")
     return gy, gr, gw_post, ggate, gw_pre
 
 
@@ -208,6 +272,8 @@ class AdamWState:
             raise ValueError(f"{name}: no tensors")
         _one_device(name, *params)
         self.bits, self.step, self.device = bits, 0, params[0].device
+        self.shapes = [p.size() for p in params]
+        self._rows, self._held = struct.Struct("@" + "6Pq" * len(params)), None  # nf4_adamw_tensor
         self.numels = [p.numel() for p in params]
         self.slices, at = [], 0
         for n in self.numels:
@@ -226,21 +292,27 @@ class AdamWState:
                 torch.zeros(at // _lib.ADAMW_BLOCK, dtype=torch.float32, device=self.device) for _ in range(2))
 
     def nbytes(self) -> int:
-        return sum(t.numel() * t.element_size()
-                   for t in (self.exp_avg, self.exp_avg_sq, self.exp_avg_absmax, self.exp_avg_sq_absmax) if t is not None)
+        return sum(t.numel() * t.element_size() for t in self._buffers() if t is not None)
 
-    def _table(self):
-        """The C table with the states' pointers; param and grad are filled in by each call."""
-        tab = (_lib.nf4_adamw_tensor * len(self.numels))()
-        size = self.exp_avg.element_size()
-        for row, n, sl in zip(tab, self.numels, self.slices):
-            row.m = self.exp_avg.data_ptr() + sl.start * size
-            row.v = self.exp_avg_sq.data_ptr() + sl.start * size
-            if self.bits == 8:
-                row.m_absmax = self.exp_avg_absmax.data_ptr() + sl.start // _lib.ADAMW_BLOCK * 4
-                row.v_absmax = self.exp_avg_sq_absmax.data_ptr() + sl.start // _lib.ADAMW_BLOCK * 4
-            row.n = n
-        return tab
+    def _buffers(self):
+        return self.exp_avg, self.exp_avg_sq, self.exp_avg_absmax, self.exp_avg_sq_absmax
+
+    def _columns(self):
+        """The C table's columns that lie in the state's own buffers: a pointer to each moment and scale of every
+        tensor, and its size."""
+        m, v, ma, va = base = tuple(0 if t is None else t.data_ptr() for t in self._buffers())
+        if self._held is None or self._held[0] != base:  # the buffers were replaced
+            size, per = self.exp_avg.element_size(), 4 if self.bits == 8 else 0
+            at = [s.start for s in self.slices]
+            block = [a // _lib.ADAMW_BLOCK * per for a in at]
+            self._held = (base, [m + a * size for a in at], [v + a * size for a in at], [ma + b for b in block],
+                          [va + b for b in block])
+        return self._held[1:]
+
+    def _table(self, params, grads) -> bytes:
+        """The packed nf4_adamw_tensor rows from the tensors' addresses; a gradient of 0 makes an empty row."""
+        n = self.numels if 0 not in grads else [n if g else 0 for n, g in zip(self.numels, grads)]
+        return self._rows.pack(*itertools.chain.from_iterable(zip(params, grads, *self._columns(), n)))
 
 
 def adamw_state(params: Sequence[torch.Tensor], bits: int = 8) -> AdamWState:
@@ -255,27 +327,40 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[Optional[torch.Te
     Parameters and gradients are contiguous and of one dtype; a gradient of None leaves its tensor and
     states alone.  `grad_scale`, a device fp32 scalar, multiplies the gradients (a clipping factor)."""
     name = "adamw_step"
-    if len(params) != len(state.numels) or len(grads) != len(params):
-        raise ValueError(f"{name}: {len(params)} tensors and {len(grads)} gradients for a state of {len(state.numels)}")
-    dtype = params[0].dtype
-    dt = _dtype(name, params[0])
-    tab = state._table()
-    for i, (p, g) in enumerate(zip(params, grads)):
-        row = tab[i]
-        if p.dtype != dtype or p.device != state.device or not p.is_contiguous() or p.numel() != row.n:
-            raise ValueError(f"{name}: tensor {i} must be contiguous, {dtype}, on {state.device} and of {row.n} values")
-        if g is None:
-            row.n = 0
-            continue
-        if g.dtype != dtype or g.device != p.device or not g.is_contiguous() or g.shape != p.shape:
-            raise ValueError(f"{name}: gradient {i} must be contiguous and of its tensor's shape, dtype and device")
-        row.param, row.grad = p.data_ptr(), g.data_ptr()
-    if grad_scale is not None and (grad_scale.dtype != torch.float32 or grad_scale.numel() != 1 or grad_scale.device != state.device):
-        raise ValueError(f"{name}: grad_scale must be one fp32 value on {state.device}")
-    _lib.check(_lib.lib().nf4_adamw_step(tab, len(params), dt, state.bits, _ptr(state.levels[0]), _ptr(state.levels[1]),
-                                         float(lr), float(betas[0]), float(betas[1]), float(eps), float(weight_decay),
-                                         state.step + 1, _ptr(grad_scale), _stream()), "nf4_adamw_step")
+    n = len(state.numels)
+    if len(params) != n or len(grads) != n:
+        raise ValueError(f"{name}: {len(params)} tensors and {len(grads)} gradients for a state of {n}")
+    T, dtype, dev = torch.Tensor, params[0].dtype, state.device
+    some = [g for g in grads if g is not None]
+    full = len(some) == n
+    every = [*params, *some]
+    shapes = state.shapes if full else [s for s, g in zip(state.shapes, grads) if g is not None]
+    if not (dtype in _DTYPES and all(map(T.is_contiguous, every)) and list(map(T.size, params)) == state.shapes
+            and list(map(T.size, some)) == shapes and {t.dtype for t in every} == {dtype} and set(map(T.get_device, every)) == {dev.index}):
+        _explain_adamw(name, params, grads, state)
+    if grad_scale is not None and (grad_scale.dtype != torch.float32 or grad_scale.numel() != 1 or grad_scale.device != dev):
+        raise ValueError(f"{name}: grad_scale must be one fp32 value on {dev}")
+    ptrs = list(map(T.data_ptr, some))
+    if not full:
+        it = iter(ptrs)
+        ptrs = [0 if g is None else next(it) for g in grads]
+    tab = state._table(map(T.data_ptr, params), ptrs)
+    rc = _fn("nf4_adamw_step")(tab, n, _DTYPES[dtype], state.bits, _ptr(state.levels[0]), _ptr(state.levels[1]), lr, betas[0],
+                               betas[1], eps, weight_decay, state.step + 1, _ptr(grad_scale), _raw_stream(dev))
+    if rc:
+        _lib.check(rc, "nf4_adamw_step")
     state.step += 1
+
+
+def _explain_adamw(name, params, grads, state):
+    dtype = params[0].dtype
+    _dtype(name, params[0])
+    for i, (p, g, shape) in enumerate(zip(params, grads, state.shapes)):
+        if p.dtype != dtype or p.device != state.device or not p.is_contiguous() or p.shape != shape:
+            raise ValueError(f"{name}: tensor {i} must be contiguous, {dtype}, on {state.device} and of shape {tuple(shape)}")
+        if g is not None and (g.dtype != dtype or g.device != p.device or not g.is_contiguous() or g.shape != p.shape):
+            raise ValueError(f"{name}: gradient {i} must be contiguous and of its tensor's shape, dtype and device")
+    raise ValueError(f"{name}: tensors and gradients do not fit the state")
 
 
 def adamw_state_values(state: AdamWState):
@@ -284,8 +369,8 @@ def adamw_state_values(state: AdamWState):
     if state.bits == 32:
         return state.exp_avg, state.exp_avg_sq
     m, v = (torch.empty(state.exp_avg.numel(), dtype=torch.float32, device=state.device) for _ in range(2))
-    _lib.check(_lib.lib().nf4_adamw_state_values(
+    _lib.check(_fn("nf4_adamw_state_values")(
         _ptr(state.exp_avg), _ptr(state.exp_avg_sq), _ptr(state.exp_avg_absmax), _ptr(state.exp_avg_sq_absmax),
-        _ptr(state.levels[0]), _ptr(state.levels[1]), m.numel(), m.data_ptr(), v.data_ptr(), _stream()),
+        _ptr(state.levels[0]), _ptr(state.levels[1]), m.numel(), m.data_ptr(), v.data_ptr(), _raw_stream(state.device)),
         "nf4_adamw_state_values")
     return m, v

@@ -19,6 +19,7 @@
 // partials in order.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <type_traits>
 
@@ -813,10 +814,15 @@ int ring_smem(const NormArgs& a, size_t elem, bool backward, int* stages) {
   return static_cast<int>(gains + *stages * stage);
 }
 
-template <typename K>
-cudaError_t ring_launch(K kern, unsigned grid, int n, int smem, const NormArgs& a, int stages, cudaStream_t s) {
-  if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) return e;
-  kern<<<grid, n, smem, s>>>(a, stages);
+// KERN's own, so that the attribute is set once and not with every launch.
+template <auto KERN>
+cudaError_t ring_launch(unsigned grid, int n, int smem, const NormArgs& a, int stages, cudaStream_t s) {
+  static std::atomic<bool> configured{false};
+  if (!configured.load(std::memory_order_relaxed)) {
+    if (cudaError_t e = cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024)) return e;
+    configured.store(true, std::memory_order_relaxed);
+  }
+  KERN<<<grid, n, smem, s>>>(a, stages);
   return cudaGetLastError();
 }
 
@@ -842,7 +848,7 @@ cudaError_t launch_typed(bool backward, const NormArgs& a, int sms, cudaStream_t
       norm_fwd_kernel<T, kVec><<<static_cast<unsigned>(a.T), n, 0, s>>>(a);
       return cudaGetLastError();
     }
-    return ring_launch(norm_fwd_ring_kernel<T, kVec>, static_cast<unsigned>(most), n, smem, a, stages, s);
+    return ring_launch<norm_fwd_ring_kernel<T, kVec>>(static_cast<unsigned>(most), n, smem, a, stages, s);
   }
   const int P = norm_bwd_ctas(a.T, a.H, sms);
   cudaError_t e = cudaSuccess;
@@ -852,7 +858,7 @@ cudaError_t launch_typed(bool backward, const NormArgs& a, int sms, cudaStream_t
   } else {
     const int smem = vec ? ring_smem(a, sizeof(T), true, &stages) : 0;
     if (stages >= 2) {
-      e = ring_launch(norm_bwd_ring_kernel<T, kVec>, static_cast<unsigned>(P), n, smem, a, stages, s);
+      e = ring_launch<norm_bwd_ring_kernel<T, kVec>>(static_cast<unsigned>(P), n, smem, a, stages, s);
     } else {
       norm_bwd_kernel<T><<<P, n, 0, s>>>(a);
       e = cudaGetLastError();

@@ -1,0 +1,79 @@
+"""AdamW for the trained tensors beside the frozen weights, over the library's many-tensor step."""
+from __future__ import annotations
+
+from typing import Optional
+
+import torch
+
+from . import block_ops
+
+
+class NF4AdamW(torch.optim.Optimizer):
+    """AdamW whose step is one launch per parameter group and dtype (nf4_adamw_step), with the two moments
+    in 8 bits (256-value blocks of the dynamic map) or in fp32.
+
+    Options per group as in torch.optim.AdamW: lr, betas, eps, weight_decay; `state_bits` is 8 or 32.  A
+    group's parameters are contiguous CUDA tensors on one device, of fp32, bf16 or fp16.  The state of a group
+    is made at its first step and lies in `group_state` (one AdamWState per group and dtype)."""
+
+    def __init__(self, params, lr: float = 2e-4, betas: tuple = (0.9, 0.999), eps: float = 1e-8,
+                 weight_decay: float = 0.01, state_bits: int = 8):
+        if state_bits not in (8, 32):
+            raise ValueError("NF4AdamW: state_bits must be 8 or 32")
+        super().__init__(params, dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay, state_bits=state_bits))
+        self.group_state = {}
+
+    def _sets(self):
+        """(key, group, parameters) of each group and dtype."""
+        for i, group in enumerate(self.param_groups):
+            by = {}
+            for p in group["params"]:
+                by.setdefault(p.dtype, []).append(p)
+            for dtype, ps in by.items():
+                yield (i, str(dtype)), group, ps
+
+    def _state(self, key, group, ps) -> block_ops.AdamWState:
+        st = self.group_state.get(key)
+        if st is None:
+            st = self.group_state[key] = block_ops.adamw_state([p.detach() for p in ps], bits=group["state_bits"])
+        return st
+
+    @torch.no_grad()
+    def step(self, closure=None, grad_scale: Optional[torch.Tensor] = None):
+        """One step; `grad_scale`, a device fp32 scalar, multiplies every gradient (a clipping factor).  A
+        parameter without a gradient is left alone."""
+        loss = None
+        if closure is not None:
+            with torch.enable_grad():
+                loss = closure()
+        for key, group, ps in self._sets():
+            grads = [None if p.grad is None else p.grad.contiguous() for p in ps]
+            if all(g is None for g in grads):
+                continue
+            block_ops.adamw_step([p.detach() for p in ps], grads, self._state(key, group, ps), lr=group["lr"],
+                                 betas=group["betas"], eps=group["eps"], weight_decay=group["weight_decay"],
+                                 grad_scale=grad_scale)
+        return loss
+
+    def state_dict(self):
+        d = super().state_dict()
+        d["group_state"] = {key: dict(bits=st.bits, step=st.step, buffers=list(st._buffers()))
+                            for key, st in self.group_state.items()}
+        return d
+
+    def load_state_dict(self, state_dict):
+        state_dict = dict(state_dict)
+        held = state_dict.pop("group_state")
+        super().load_state_dict(state_dict)
+        self.group_state = {}
+        for key, group, ps in self._sets():
+            if key not in held:
+                continue
+            rec, st = held[key], self._state(key, group, ps)
+            if rec["bits"] != st.bits or any((a is None) != (b is None) or (a is not None and a.shape != b.shape)
+                                             for a, b in zip(rec["buffers"], st._buffers())):
+                raise ValueError("NF4AdamW: the saved state belongs to other parameters or another state_bits")
+            st.step = int(rec["step"])
+            for saved, own in zip(rec["buffers"], st._buffers()):
+                if own is not None:
+                    own.copy_(saved)
