@@ -74,41 +74,63 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sbase = smem_addr(smem);
   const int h = blockIdx.x % a.Hq, hk = h / (a.Hq / a.Hk);
 
-  int64_t g0, g1;
-  gap_rows(a, &g0, &g1);
-  if (g0 > 0 || g1 < a.T) {
-    zero_rows(static_cast<T*>(a.o), a.o_t, a.o_h, a.Hq, a.D, 0, g0);
-    zero_rows(static_cast<T*>(a.o), a.o_t, a.o_h, a.Hq, a.D, g1, a.T);
-    if (blockIdx.x < a.Hq)
-      for (int64_t t = threadIdx.x; t < a.T; t += kThreads)
-        if (t < g0 || t >= g1) a.lse[h * a.T + t] = -INFINITY;
-  }
-  if (warp == 0) {
+  // The load warp sets the CTA up on its own -- barriers, its tile, the first loads -- while
+  // the MMA warp allocates tensor memory.
+  auto load = [&](const CUtensorMap* m, uint32_t dst, uint32_t bar, int head, int r) {
+    const int boxes = (a.D + 63) / 64;
+    if (lane == 0) {
+      mbar_arrive_expect_tx(bar, boxes * kPanelBytes);
+      for (int b = 0; b < boxes; ++b) tma_load_3d(dst + b * kPanelBytes, m, bar, b * 64, head, r);
+    }
+    __syncwarp();
+  };
+  if (warp == kWarpLoad) {
+    if (lane == 0) {
+      prefetch_tensormap(&mq);
+      prefetch_tensormap(&mk);
+      prefetch_tensormap(&mv);
+      sh.abort_flag = 0;
+      for (int i = 0; i < 2; ++i) {
+        sh.dirty[i] = 0;
+        mbar_init(smem_addr(&sh.q_full[i]), 1);
+        mbar_init(smem_addr(&sh.s_full[i]), 1);
+        mbar_init(smem_addr(&sh.p_full[i]), 4);
+        mbar_init(smem_addr(&sh.o_full[i]), 1);
+        mbar_init(smem_addr(&sh.diag[i]), 1);
+        mbar_init(smem_addr(&sh.clean[i]), 64);
+      }
+      mbar_init(smem_addr(&sh.drain), 1);
+      for (int i = 0; i < G::kStages; ++i) {
+        mbar_init(smem_addr(&sh.full[i]), 1);
+        mbar_init(smem_addr(&sh.empty[i]), 1);
+      }
+      fence_mbar_init();
+    }
+    __syncwarp();
     const AttnTile w = find_tile(a, blockIdx.x / a.Hq, 2 * kAttnTile);
     if (lane == 0) sh.tile = w;
+    if (w.tile >= 0) {
+      const int r = static_cast<int>(w.row0) + 2 * w.tile * kAttnTile;
+      load(&mq, sbase + G::kOffQ, smem_addr(&sh.q_full[0]), h, r);
+      load(&mk, sbase + G::kOffRing, smem_addr(&sh.full[0]), hk, static_cast<int>(w.row0));
+      if ((2 * w.tile + 1) * kAttnTile < w.len)
+        load(&mq, sbase + G::kOffQ + G::kTileBytes, smem_addr(&sh.q_full[1]), h, r + kAttnTile);
+    }
   } else if (warp == kWarpMma) {
     tmem_alloc(smem_addr(&sh.tmem), 512);
     tmem_relinquish();
-  } else if (warp == kWarpLoad && lane == 0) {
-    sh.abort_flag = 0;
-    for (int i = 0; i < 2; ++i) {
-      sh.dirty[i] = 0;
-      mbar_init(smem_addr(&sh.q_full[i]), 1);
-      mbar_init(smem_addr(&sh.s_full[i]), 1);
-      mbar_init(smem_addr(&sh.p_full[i]), 4);
-      mbar_init(smem_addr(&sh.o_full[i]), 1);
-      mbar_init(smem_addr(&sh.diag[i]), 1);
-      mbar_init(smem_addr(&sh.clean[i]), 64);
+  } else if (warp >= kWarpClean) {
+    int64_t g0, g1;
+    gap_rows(a, &g0, &g1);
+    if (g0 > 0 || g1 < a.T) {
+      const int me = threadIdx.x - 32 * kWarpClean;
+      zero_rows(static_cast<T*>(a.o), a.o_t, a.o_h, a.Hq, a.D, 0, g0, me, 64);
+      zero_rows(static_cast<T*>(a.o), a.o_t, a.o_h, a.Hq, a.D, g1, a.T, me, 64);
+      if (blockIdx.x < a.Hq) {
+        for (int64_t t = me; t < g0; t += 64) a.lse[h * a.T + t] = -INFINITY;
+        for (int64_t t = g1 + me; t < a.T; t += 64) a.lse[h * a.T + t] = -INFINITY;
+      }
     }
-    mbar_init(smem_addr(&sh.drain), 1);
-    for (int i = 0; i < G::kStages; ++i) {
-      mbar_init(smem_addr(&sh.full[i]), 1);
-      mbar_init(smem_addr(&sh.empty[i]), 1);
-    }
-    fence_mbar_init();
-    prefetch_tensormap(&mq);
-    prefetch_tensormap(&mk);
-    prefetch_tensormap(&mv);
   }
   tc_fence_before();
   __syncthreads();
@@ -129,27 +151,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       // no tile: nothing but the deallocation below
     } else if (warp == kWarpLoad) {
       // The load and MMA warps stay converged: all lanes walk the loop, one lane issues.
-      const int boxes = (a.D + 63) / 64;
-      const uint32_t bytes = boxes * kPanelBytes;
-      auto load = [&](const CUtensorMap* m, uint32_t dst, uint32_t bar, int head, int r) {
-        if (lane == 0) {
-          mbar_arrive_expect_tx(bar, bytes);
-          for (int b = 0; b < boxes; ++b) tma_load_3d(dst + b * kPanelBytes, m, bar, b * 64, head, r);
-        }
-        __syncwarp();
-      };
-      load(&mq, sbase + G::kOffQ, smem_addr(&sh.q_full[0]), h, row0 + i0 * kAttnTile);
-      uint32_t st = 0, ph = 0, issued = 0, par = 0, diag = 0;
-      bool any = false;
-      for (int j = 0; j < 2 * nkv; ++j) {  // K0 V0 K1 V1 ...
+      // (the first queries and keys are on their way)
+      uint32_t st = 1, ph = 0, issued = 1, par = 0, diag = 0;
+      for (int j = 1; j < 2 * nkv; ++j) {  // K0 V0 K1 V1 ...
         if (!attn_wait_warp(smem_addr(&sh.empty[st]), ph ^ 1u, guard)) break;
         // the value tiles at the diagonals, the last ones, go to the cleaning warps first
         const int d = (j & 1) ? (j >> 1) - i0 : -1;
         load((j & 1) ? &mv : &mk, sbase + G::kOffRing + st * G::kTileBytes,
              d >= 0 ? smem_addr(&sh.diag[d]) : smem_addr(&sh.full[st]), hk, row0 + (j >> 1) * kAttnTile);
-        if (j == 0 && nb > 0)
-          load(&mq, sbase + G::kOffQ + G::kTileBytes, smem_addr(&sh.q_full[1]), h, row0 + (i0 + 1) * kAttnTile);
-        any = true;
         if (d >= 0) {
           diag |= 1u << d;
         } else {
@@ -163,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // every load must have landed before the CTA may exit
       attn_drain(smem_addr(&sh.q_full[0]), 0, guard);
-      if (nb > 0 && any) attn_drain(smem_addr(&sh.q_full[1]), 0, guard);
+      if (nb > 0) attn_drain(smem_addr(&sh.q_full[1]), 0, guard);
       for (int d = 0; d < 2; ++d)
         if (diag & (1u << d)) attn_drain(smem_addr(&sh.diag[d]), 0, guard);
       for (int q = 0; q < G::kStages; ++q)

@@ -85,8 +85,8 @@ __global__ void __launch_bounds__(kThreads) attn_any_fwd_kernel(AttnArgs a) {
   float *qs = smem, *ks = qs + kRows * pitch, *vs = ks + kStep * pitch;
   int64_t g0, g1;
   gap_rows(a, &g0, &g1);
-  zero_rows(static_cast<T*>(a.o), a.o_t, a.o_h, a.Hq, D, 0, g0);
-  zero_rows(static_cast<T*>(a.o), a.o_t, a.o_h, a.Hq, D, g1, a.T);
+  zero_rows(static_cast<T*>(a.o), a.o_t, a.o_h, a.Hq, D, 0, g0, threadIdx.x, kThreads);
+  zero_rows(static_cast<T*>(a.o), a.o_t, a.o_h, a.Hq, D, g1, a.T, threadIdx.x, kThreads);
   if (blockIdx.x == 0)
     for (int64_t t = threadIdx.x; t < a.T; t += kThreads)
       if (t < g0 || t >= g1) a.lse[h * a.T + t] = -INFINITY;
@@ -168,8 +168,8 @@ __global__ void __launch_bounds__(kThreads) attn_any_dq_kernel(AttnArgs a) {
   float *qs = smem, *gs = qs + kRows * pitch, *ks = gs + kRows * pitch, *vs = ks + kStep * pitch;
   int64_t g0, g1;
   gap_rows(a, &g0, &g1);
-  zero_rows(static_cast<T*>(a.gq), a.gq_t, a.gq_h, a.Hq, D, 0, g0);
-  zero_rows(static_cast<T*>(a.gq), a.gq_t, a.gq_h, a.Hq, D, g1, a.T);
+  zero_rows(static_cast<T*>(a.gq), a.gq_t, a.gq_h, a.Hq, D, 0, g0, threadIdx.x, kThreads);
+  zero_rows(static_cast<T*>(a.gq), a.gq_t, a.gq_h, a.Hq, D, g1, a.T, threadIdx.x, kThreads);
   if (warp == 0) {
     const AttnTile w = find_tile(a, blockIdx.x, kRows);
     if (lane == 0) sh.tile = w;
@@ -219,10 +219,10 @@ __global__ void __launch_bounds__(kThreads) attn_any_dkv_kernel(AttnArgs a) {
   float *ks = smem, *vs = ks + kRows * pitch, *qs = vs + kRows * pitch, *gs = qs + kStep * pitch;
   int64_t g0, g1;
   gap_rows(a, &g0, &g1);
-  zero_rows(static_cast<T*>(a.gk), a.gk_t, a.gk_h, a.Hk, D, 0, g0);
-  zero_rows(static_cast<T*>(a.gk), a.gk_t, a.gk_h, a.Hk, D, g1, a.T);
-  zero_rows(static_cast<T*>(a.gv), a.gv_t, a.gv_h, a.Hk, D, 0, g0);
-  zero_rows(static_cast<T*>(a.gv), a.gv_t, a.gv_h, a.Hk, D, g1, a.T);
+  zero_rows(static_cast<T*>(a.gk), a.gk_t, a.gk_h, a.Hk, D, 0, g0, threadIdx.x, kThreads);
+  zero_rows(static_cast<T*>(a.gk), a.gk_t, a.gk_h, a.Hk, D, g1, a.T, threadIdx.x, kThreads);
+  zero_rows(static_cast<T*>(a.gv), a.gv_t, a.gv_h, a.Hk, D, 0, g0, threadIdx.x, kThreads);
+  zero_rows(static_cast<T*>(a.gv), a.gv_t, a.gv_h, a.Hk, D, g1, a.T, threadIdx.x, kThreads);
   if (warp == 0) {
     const AttnTile w = find_tile(a, blockIdx.x, kRows);
     if (lane == 0) sh.tile = w;

@@ -62,7 +62,8 @@ struct Shared {
   uint64_t s_full[2], dp_full, p_full, ds_full, out_full, drain;
 };
 
-// Row statistics of the keys' CTAs, in the tile of shared memory that they leave free.
+// Row statistics of the keys' CTAs, negated (they are only subtracted), in the tile of
+// shared memory that these leave free.
 struct Rows {
   float lse2[2][kAttnTile];
   float delta[2][kAttnTile];
@@ -180,9 +181,6 @@ __device__ __forceinline__ void keys_cta(const Ctx<F16, PANELS, FULL>& x, const 
   const int row0 = static_cast<int>(w.row0), lane = x.lane, warp = x.warp;
   if constexpr (!COMPUTE) {
   if (warp == kWarpLoad) {
-    x.expect(sh.own_full, 2 * x.bytes());
-    x.load(mk, 0, sh.own_full, hk, row0 + jt * kAttnTile);
-    x.load(mv, 1, sh.own_full, hk, row0 + jt * kAttnTile);
     int done = 0, g = 0, i = jt;
     for (int it = 0; it < n; ++it) {
       const int st = it & 1;
@@ -208,8 +206,8 @@ __device__ __forceinline__ void keys_cta(const Ctx<F16, PANELS, FULL>& x, const 
       const int r0 = (warp - kWarpPrep) * 64 + lane * 2;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        l[e] = lse2_of(a, at + r0 + e, r0 + e < rows) - (F16 ? kShift : 0.0f);
-        d[e] = r0 + e < rows ? a.delta[at + r0 + e] * (F16 ? kUnshift : 1.0f) : 0.0f;
+        l[e] = (F16 ? kShift : 0.0f) - lse2_of(a, at + r0 + e, r0 + e < rows);
+        d[e] = r0 + e < rows ? -a.delta[at + r0 + e] * (F16 ? kUnshift : 1.0f) : 0.0f;
       }
       if (!x.wait(sh.empty[st], ((it >> 1) & 1) ^ 1)) break;
       *reinterpret_cast<float2*>(&rs.lse2[st][r0]) = make_float2(l[0], l[1]);
@@ -284,8 +282,8 @@ __device__ __forceinline__ void keys_cta(const Ctx<F16, PANELS, FULL>& x, const 
 #pragma unroll
       for (int q = 0; q < 64; q += 4) {
         const float4 l = *reinterpret_cast<const float4*>(&rs.lse2[st][wg * 64 + q]);
-        const float2 u = fma2(make_float2(__uint_as_float(s[q]), __uint_as_float(s[q + 1])), c2, make_float2(-l.x, -l.y));
-        const float2 v = fma2(make_float2(__uint_as_float(s[q + 2]), __uint_as_float(s[q + 3])), c2, make_float2(-l.z, -l.w));
+        const float2 u = fma2(make_float2(__uint_as_float(s[q]), __uint_as_float(s[q + 1])), c2, make_float2(l.x, l.y));
+        const float2 v = fma2(make_float2(__uint_as_float(s[q + 2]), __uint_as_float(s[q + 3])), c2, make_float2(l.z, l.w));
         s[q] = __float_as_uint(exp2_approx(u.x));
         s[q + 1] = __float_as_uint(exp2_approx(u.y));
         s[q + 2] = __float_as_uint(exp2_approx(v.x));
@@ -318,8 +316,8 @@ __device__ __forceinline__ void keys_cta(const Ctx<F16, PANELS, FULL>& x, const 
           float2 u = make_float2(__uint_as_float(d[e]), __uint_as_float(d[e + 1]));
           float2 v = make_float2(__uint_as_float(d[e + 2]), __uint_as_float(d[e + 3]));
           const float2 one = make_float2(kUnshift, kUnshift);
-          u = F16 ? fma2(u, one, make_float2(-dl.x, -dl.y)) : add2(u, make_float2(-dl.x, -dl.y));
-          v = F16 ? fma2(v, one, make_float2(-dl.z, -dl.w)) : add2(v, make_float2(-dl.z, -dl.w));
+          u = F16 ? fma2(u, one, make_float2(dl.x, dl.y)) : add2(u, make_float2(dl.x, dl.y));
+          v = F16 ? fma2(v, one, make_float2(dl.z, dl.w)) : add2(v, make_float2(dl.z, dl.w));
           u = mul2(u, make_float2(__uint_as_float(s[q + e]), __uint_as_float(s[q + e + 1])));
           v = mul2(v, make_float2(__uint_as_float(s[q + e + 2]), __uint_as_float(s[q + e + 3])));
           if (diag) {
@@ -387,9 +385,6 @@ __device__ __forceinline__ void queries_cta(const Ctx<F16, PANELS, FULL>& x, con
   const int row0 = static_cast<int>(w.row0), lane = x.lane, warp = x.warp;
   if constexpr (!COMPUTE) {
   if (warp == kWarpLoad) {
-    x.expect(sh.own_full, 2 * x.bytes());
-    x.load(mq, 0, sh.own_full, h, row0 + it * kAttnTile);
-    x.load(mg, 1, sh.own_full, h, row0 + it * kAttnTile);
     int nk = 0, nv = 0;
     bool diag = false;
     for (int j = 0; j < n; ++j) {
@@ -524,39 +519,55 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int64_t id = keys ? blockIdx.x : blockIdx.x - key_ctas;
   const int heads = keys ? a.Hk : a.Hq, h = static_cast<int>(id % heads);
 
-  int64_t g0, g1;
-  gap_rows(a, &g0, &g1);
-  if (g0 > 0 || g1 < a.T) {
-    zero_rows(static_cast<T*>(a.gq), a.gq_t, a.gq_h, a.Hq, a.D, 0, g0);
-    zero_rows(static_cast<T*>(a.gq), a.gq_t, a.gq_h, a.Hq, a.D, g1, a.T);
-    zero_rows(static_cast<T*>(a.gk), a.gk_t, a.gk_h, a.Hk, a.D, 0, g0);
-    zero_rows(static_cast<T*>(a.gk), a.gk_t, a.gk_h, a.Hk, a.D, g1, a.T);
-    zero_rows(static_cast<T*>(a.gv), a.gv_t, a.gv_h, a.Hk, a.D, 0, g0);
-    zero_rows(static_cast<T*>(a.gv), a.gv_t, a.gv_h, a.Hk, a.D, g1, a.T);
-  }
-  if (warp == 0) {
+  // The load warp sets the CTA up on its own -- barriers, its tile, the loads of the tiles
+  // that the CTA owns -- while the MMA warp allocates tensor memory.
+  if (warp == kWarpLoad) {
+    if (lane == 0) {
+      prefetch_tensormap(&mq);
+      prefetch_tensormap(&mk);
+      prefetch_tensormap(&mv);
+      prefetch_tensormap(&mg);
+      sh.abort_flag = 0;
+      sh.dirty = 0;
+      uint64_t* one[] = {&sh.own_full, &sh.full[0], &sh.full[1], &sh.full[2], &sh.vfull[0], &sh.vfull[1], &sh.empty[0],
+                         &sh.empty[1], &sh.empty[2], &sh.vempty[0], &sh.vempty[1], &sh.diag, &sh.s_full[0], &sh.s_full[1],
+                         &sh.dp_full, &sh.out_full, &sh.drain};
+      for (uint64_t* b : one) mbar_init(smem_addr(b), 1);
+      mbar_init(smem_addr(&sh.ready[0]), 64);
+      mbar_init(smem_addr(&sh.ready[1]), 64);
+      mbar_init(smem_addr(&sh.clean), 64);
+      mbar_init(smem_addr(&sh.p_full), kCompute);
+      mbar_init(smem_addr(&sh.ds_full), kCompute);
+      fence_mbar_init();
+    }
+    __syncwarp();
     const AttnTile w = find_tile(a, id / heads, kAttnTile, !keys);
     if (lane == 0) sh.tile = w;
+    if (lane == 0 && w.tile >= 0) {
+      const int boxes = (a.D + 63) / 64, r = static_cast<int>(w.row0) + w.tile * kAttnTile;
+      const uint32_t bar = smem_addr(&sh.own_full), to = smem_addr(smem);
+      mbar_arrive_expect_tx(bar, 2 * boxes * kPanelBytes);
+      for (int x = 0; x < boxes; ++x) {
+        tma_load_3d(to + x * kPanelBytes, keys ? &mk : &mq, bar, x * 64, h, r);
+        tma_load_3d(to + Geo<PANELS>::kTileBytes + x * kPanelBytes, keys ? &mv : &mg, bar, x * 64, h, r);
+      }
+    }
+    __syncwarp();
   } else if (warp == kWarpMma) {
     tmem_alloc(smem_addr(&sh.tmem), 512);
     tmem_relinquish();
-  } else if (warp == kWarpLoad && lane == 0) {
-    sh.abort_flag = 0;
-    sh.dirty = 0;
-    uint64_t* one[] = {&sh.own_full, &sh.full[0], &sh.full[1], &sh.full[2], &sh.vfull[0], &sh.vfull[1], &sh.empty[0],
-                       &sh.empty[1], &sh.empty[2], &sh.vempty[0], &sh.vempty[1], &sh.diag, &sh.s_full[0], &sh.s_full[1],
-                       &sh.dp_full, &sh.out_full, &sh.drain};
-    for (uint64_t* b : one) mbar_init(smem_addr(b), 1);
-    mbar_init(smem_addr(&sh.ready[0]), 64);
-    mbar_init(smem_addr(&sh.ready[1]), 64);
-    mbar_init(smem_addr(&sh.clean), 64);
-    mbar_init(smem_addr(&sh.p_full), kCompute);
-    mbar_init(smem_addr(&sh.ds_full), kCompute);
-    fence_mbar_init();
-    prefetch_tensormap(&mq);
-    prefetch_tensormap(&mk);
-    prefetch_tensormap(&mv);
-    prefetch_tensormap(&mg);
+  } else if (warp >= kWarpPrep) {
+    int64_t g0, g1;
+    gap_rows(a, &g0, &g1);
+    if (g0 > 0 || g1 < a.T) {
+      const int me = threadIdx.x - 32 * kWarpPrep;
+      zero_rows(static_cast<T*>(a.gq), a.gq_t, a.gq_h, a.Hq, a.D, 0, g0, me, 64);
+      zero_rows(static_cast<T*>(a.gq), a.gq_t, a.gq_h, a.Hq, a.D, g1, a.T, me, 64);
+      zero_rows(static_cast<T*>(a.gk), a.gk_t, a.gk_h, a.Hk, a.D, 0, g0, me, 64);
+      zero_rows(static_cast<T*>(a.gk), a.gk_t, a.gk_h, a.Hk, a.D, g1, a.T, me, 64);
+      zero_rows(static_cast<T*>(a.gv), a.gv_t, a.gv_h, a.Hk, a.D, 0, g0, me, 64);
+      zero_rows(static_cast<T*>(a.gv), a.gv_t, a.gv_h, a.Hk, a.D, g1, a.T, me, 64);
+    }
   }
   tc_fence_before();
   __syncthreads();
