@@ -85,7 +85,7 @@ class nf4_attention(ctypes.Structure):
         ("v_token", ctypes.c_int64), ("v_head", ctypes.c_int64),
         ("cu_seqlens", ctypes.c_void_p), ("nseq", ctypes.c_int64), ("T", ctypes.c_int64),
         ("Hq", ctypes.c_int32), ("Hk", ctypes.c_int32), ("D", ctypes.c_int32),
-        ("dtype", ctypes.c_int32), ("scale", ctypes.c_float),
+        ("dtype", ctypes.c_int32), ("scale", ctypes.c_float), ("o_rest", ctypes.c_void_p),
     ]
 
 

@@ -192,17 +192,17 @@ class NF4AttentionFn(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, q, k, v, cu_seqlens, scale):
-        o, lse = block_ops.attention_fwd(q, k, v, cu_seqlens, scale)
-        ctx.save_for_backward(q, k, v, o, lse, cu_seqlens)
+        o, lse = block_ops.attention_fwd(q, k, v, cu_seqlens, scale, for_backward=any(ctx.needs_input_grad[:3]))
+        ctx.save_for_backward(q, k, v, o, lse, lse.o_rest, cu_seqlens)
         ctx.scale = scale
         return o
 
     @staticmethod
     def backward(ctx, go):
-        q, k, v, o, lse, cu_seqlens = ctx.saved_tensors
+        q, k, v, o, lse, rest, cu_seqlens = ctx.saved_tensors
         if go.stride(2) != 1:
             go = go.contiguous()
-        gq, gk, gv = block_ops.attention_bwd(go, q, k, v, o, lse, cu_seqlens, ctx.scale)
+        gq, gk, gv = block_ops.attention_bwd(go, q, k, v, o, lse, cu_seqlens, ctx.scale, rest)
         return gq, gk, gv, None, None
 
 

@@ -21,7 +21,7 @@ from .ops import _device_codebook, _need_cuda, _ptr, workspace_size
 # slower function), pass structs as packed bytes and look the library's functions up once.
 
 _DTYPES = {torch.float32: _lib.DTYPE_F32, torch.bfloat16: _lib.DTYPE_BF16, torch.float16: _lib.DTYPE_F16}
-_ATTENTION = struct.Struct("@3P6qP2q4if4x")     # nf4_attention
+_ATTENTION = struct.Struct("@3P6qP2q4if4xP")     # nf4_attention
 _NORM = struct.Struct("@PqPqPqPP2q2i2f")        # nf4_norm_residual
 _FNS = {}
 
@@ -83,7 +83,7 @@ def _explain_attention(name, q, k, v, cu_seqlens, like_q):
     raise ValueError(f"{name}: cu_seqlens must be a contiguous int32 [sequences + 1] tensor")
 
 
-def _attention(name, q, k, v, cu_seqlens, scale, like_q=()):
+def _attention(name, q, k, v, cu_seqlens, scale, rest, like_q=()):
     """The packed nf4_attention of checked arguments; like_q: (what, tensor) of q's shape and dtype."""
     dt, dev, qs, ks, qt, kt, vt = q.dtype, q.device, q.shape, k.shape, q.stride(), k.stride(), v.stride()
     ok = (dt in _DTYPES and dev.type == "cuda" and k.dtype is dt and v.dtype is dt and k.device == dev and v.device == dev
@@ -101,15 +101,21 @@ def _attention(name, q, k, v, cu_seqlens, scale, like_q=()):
         _explain_attention(name, q, k, v, cu_seqlens, like_q)
     T, Hq, D = qs
     return _ATTENTION.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), qt[0], qt[1], kt[0], kt[1], vt[0], vt[1], cu, nseq, T,
-                           Hq, ks[1], D, _DTYPES[dt], D ** -0.5 if scale is None else scale)
+                           Hq, ks[1], D, _DTYPES[dt], D ** -0.5 if scale is None else scale,
+                           0 if rest is None else rest.data_ptr())
 
 
 def attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None,
-                  scale: Optional[float] = None, out: Optional[torch.Tensor] = None):
+                  scale: Optional[float] = None, out: Optional[torch.Tensor] = None, for_backward: bool = True):
     """nf4_attention_fwd: causal attention of packed sequences, q [T, Hq, D] over k, v [T, Hk, D]
     (any token and head strides).  `cu_seqlens` int32 [sequences + 1] holds the row offsets (None:
-    one sequence); rows outside them give zeros.  Returns (o [T, Hq, D], lse fp32 [Hq, T])."""
-    d = _attention("attention_fwd", q, k, v, cu_seqlens, scale, () if out is None else (("out", out),))
+    one sequence); rows outside them give zeros.  Returns (o [T, Hq, D], lse fp32 [Hq, T]).  With
+    `for_backward` and a 16-bit dtype, `lse.o_rest` is a tensor of o's shape with what o's rounding
+    left over, for attention_bwd; a caller that wants no gradients saves its memory with False."""
+    rest = None
+    if for_backward and q.dtype is not torch.float32 and q.dim() == 3 and q.is_cuda:
+        rest = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    d = _attention("attention_fwd", q, k, v, cu_seqlens, scale, rest, () if out is None else (("out", out),))
     T, Hq, D = q.shape
     o = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device) if out is None else out
     lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
@@ -117,13 +123,21 @@ def attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens:
     rc = _fn("nf4_attention_fwd")(d, o.data_ptr(), ot, oh, lse.data_ptr(), _raw_stream(q.device))
     if rc:
         _lib.check(rc, "nf4_attention_fwd")
+    lse.o_rest = rest
     return o, lse
 
 
 def attention_bwd(go: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
-                  lse: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None, scale: Optional[float] = None):
-    """nf4_attention_bwd: the gradients (gq, gk, gv) of attention_fwd from its o, lse and go = dL/do."""
-    d = _attention("attention_bwd", q, k, v, cu_seqlens, scale, (("go", go), ("o", o)))
+                  lse: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                  o_rest: Optional[torch.Tensor] = None):
+    """nf4_attention_bwd: the gradients (gq, gk, gv) of attention_fwd from its o, lse and go = dL/do.  `o_rest`
+    is the forward's `lse.o_rest` (taken from lse where it still carries it); without it the row sums do . o
+    see the rounded o."""
+    rest = getattr(lse, "o_rest", None) if o_rest is None else o_rest
+    if rest is not None and (rest.shape != q.shape or rest.dtype is not q.dtype or not rest.is_contiguous() or rest.device != q.device
+                             or q.dtype is torch.float32):
+        raise ValueError("attention_bwd: o_rest must be the forward's, contiguous and of q's shape and 16-bit dtype")
+    d = _attention("attention_bwd", q, k, v, cu_seqlens, scale, rest, (("go", go), ("o", o)))
     T, Hq, D = q.shape
     dev, dt = q.device, q.dtype
     if lse.dtype is not torch.float32 or lse.shape != (Hq, T) or not lse.is_contiguous() or lse.device != dev:

@@ -121,6 +121,7 @@ struct AttnArgs {
   const void *q, *k, *v, *go;
   void *o, *gq, *gk, *gv;
   int64_t q_t, q_h, k_t, k_h, v_t, v_h, o_t, o_h, go_t, go_h, gq_t, gq_h, gk_t, gk_h, gv_t, gv_h;
+  void* o_rest;  // [T][Hq][D] or null: o before its rounding, less o
   float* lse;    // [Hq][T]
   float* delta;  // [Hq][T], backward
   const int32_t* cu_seqlens;  // [nseq + 1], or null: one sequence of T rows

@@ -968,8 +968,8 @@ nf4_status attn_args(const nf4_attention* d, nf4::AttnArgs* a) {
   if (d->D > 256 || d->T > INT32_MAX || d->nseq > INT32_MAX || d->Hq > 65535) return NF4_ERR_UNSUPPORTED_SHAPE;
   if (d->T > 0) {
     const size_t e = dtype_bytes(d->dtype);
-    if (!d->q || !d->k || !d->v) return NF4_ERR_INVALID_ARG;
-    if (!aligned_to(d->q, e) || !aligned_to(d->k, e) || !aligned_to(d->v, e) || !aligned_to(d->cu_seqlens, 4))
+    if (!d->q || !d->k || !d->v || (d->o_rest && e != 2)) return NF4_ERR_INVALID_ARG;
+    if (!aligned_to(d->o_rest, 16) || !aligned_to(d->q, e) || !aligned_to(d->k, e) || !aligned_to(d->v, e) || !aligned_to(d->cu_seqlens, 4))
       return NF4_ERR_ALIGNMENT;
   }
   *a = {};
@@ -989,6 +989,7 @@ nf4_status attn_args(const nf4_attention* d, nf4::AttnArgs* a) {
   a->Hk = d->Hk;
   a->D = d->D;
   a->scale = d->scale;
+  a->o_rest = d->o_rest;
   return NF4_OK;
 }
 

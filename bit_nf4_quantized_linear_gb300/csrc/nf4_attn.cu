@@ -335,6 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float inv = 1.0f / l;
       const int64_t r = w.row0 + i;
       T* out = static_cast<T*>(a.o) + r * a.o_t + h * a.o_h;
+      T* rest = a.o_rest ? static_cast<T*>(a.o_rest) + (r * a.Hq + h) * a.D : nullptr;
       const bool dirty = sh.dirty[0] || sh.dirty[1];
       for (int q = 0; q < ksteps; q += 2) {
         uint32_t o[32];
@@ -360,10 +361,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int e = 0; e < 32; e += 8)
-          if (live && q * 16 + e < a.D)
-            *reinterpret_cast<uint4*>(out + q * 16 + e) =
-                make_uint4(pack16<F16>(f[e], f[e + 1]), pack16<F16>(f[e + 2], f[e + 3]), pack16<F16>(f[e + 4], f[e + 5]),
-                           pack16<F16>(f[e + 6], f[e + 7]));
+          if (live && q * 16 + e < a.D) {
+            uint32_t x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[k] = pack16<F16>(f[e + 2 * k], f[e + 2 * k + 1]);
+            *reinterpret_cast<uint4*>(out + q * 16 + e) = make_uint4(x[0], x[1], x[2], x[3]);
+            if (rest) {  // what the rounding left over
+#pragma unroll
+              for (int k = 0; k < 4; ++k) x[k] = pack16<F16>(f[e + 2 * k] - lo16<F16>(x[k]), f[e + 2 * k + 1] - hi16<F16>(x[k]));
+              *reinterpret_cast<uint4*>(rest + q * 16 + e) = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+          }
         __syncwarp();
       }
       if (live) a.lse[h * a.T + r] = (mc + log2f(l)) * 0.6931471805599453f;

@@ -138,6 +138,14 @@ __global__ void __launch_bounds__(kThreads) attn_any_fwd_kernel(AttnArgs a) {
     const int i = i0 + warp * kOwn + r;
     if (i >= w.len) continue;
     store_row<T>(a.o, a.o_t, a.o_h, h, w.row0 + i, acc[r], 1.0f / sum[r], D, lane);
+    if (a.o_rest) {  // what the rounding left over
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const float x = acc[r][c] * (1.0f / sum[r]);
+        acc[r][c] = x - to_f32(from_f32<T>(x));
+      }
+      store_row<T>(a.o_rest, static_cast<int64_t>(a.Hq) * D, D, h, w.row0 + i, acc[r], 1.0f, D, lane);
+    }
     if (lane == 0) a.lse[h * a.T + w.row0 + i] = mx[r] + logf(sum[r]);
   }
 }
@@ -153,7 +161,8 @@ __global__ void __launch_bounds__(kThreads) attn_any_delta_kernel(AttnArgs a) {
     const T* o = static_cast<const T*>(a.o) + t * a.o_t + h * a.o_h;
     const T* g = static_cast<const T*>(a.go) + t * a.go_t + h * a.go_h;
     float s = 0.0f;
-    for (int d = lane; d < a.D; d += 32) s = fmaf(to_f32(o[d]), to_f32(g[d]), s);
+    const T* rest = a.o_rest ? static_cast<const T*>(a.o_rest) + i * a.D : nullptr;
+    for (int d = lane; d < a.D; d += 32) s = fmaf(to_f32(o[d]) + (rest ? to_f32(rest[d]) : 0.0f), to_f32(g[d]), s);
     s = warp_sum(s);
     if (lane == 0) a.delta[h * a.T + t] = s;
   }

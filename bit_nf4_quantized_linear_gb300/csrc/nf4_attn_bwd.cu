@@ -1,7 +1,8 @@
 // nf4_attn_bwd.cu -- backward of causal attention over packed sequences on the tensor
 // cores (fp16 or bf16, head width a multiple of 8 up to 128).
 //
-// A first kernel forms delta_i = do_i . o_i.  A second launch holds two kinds of CTAs,
+// A first kernel forms delta_i = do_i . o_i (o with the rest of its rounding, where the
+// forward left it).  A second launch holds two kinds of CTAs,
 // the longer ones first:
 //  - keys: 128 keys of one key head, over every query tile that sees them and every
 //    query head of the group.  Transposed, so that P and dS stay in tensor memory as the
@@ -69,7 +70,8 @@ struct Rows {
   float delta[2][kAttnTile];
 };
 
-// delta[h][t] = do . o: 16 bytes a lane, rows of a head side by side.
+// delta[h][t] = do . (o + what its rounding left over): 16 bytes a lane, rows of a head
+// side by side.  Bound by HBM.
 template <typename T>
 __global__ void __launch_bounds__(256) attn_delta_kernel(const __grid_constant__ AttnArgs a) {
   const int per = a.D / 8;                          // lanes with work in a row
@@ -85,12 +87,14 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(const __grid_constant__
       const int h = static_cast<int>(i - t * a.Hq);
       const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.o) + t * a.o_t + h * a.o_h + lane * 8);
       const uint4 y = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.go) + t * a.go_t + h * a.go_h + lane * 8);
-      const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+      uint4 z = make_uint4(0u, 0u, 0u, 0u);
+      if (a.o_rest) z = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.o_rest) + i * a.D + lane * 8);
+      const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w}, zs[4] = {z.x, z.y, z.z, z.w};
       constexpr bool f16 = std::is_same<T, __half>::value;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        s = fmaf(lo16<f16>(xs[e]), lo16<f16>(ys[e]), s);
-        s = fmaf(hi16<f16>(xs[e]), hi16<f16>(ys[e]), s);
+        s = fmaf(lo16<f16>(xs[e]) + lo16<f16>(zs[e]), lo16<f16>(ys[e]), s);
+        s = fmaf(hi16<f16>(xs[e]) + hi16<f16>(zs[e]), hi16<f16>(ys[e]), s);
       }
     }
     for (int o = width / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);

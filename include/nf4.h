@@ -404,6 +404,10 @@ nf4_status nf4_norm_residual_bwd(const nf4_norm_residual* d, const float* stats,
  *               NF4_ERR_BAD_OFFSETS in the device status word.
  *   lse         fp32 [Hq][T], natural log of each row's sum of exponentials; written
  *               by the forward, read by the backward.
+ *   o_rest      [T][Hq][D] contiguous, of `dtype` (16-bit types), or NULL: what the
+ *               rounding of o left over.  Written by the forward; the backward adds it
+ *               to o in its row sums do . o, whose error would otherwise be the largest
+ *               in gq and gk after the roundings that their products need.
  * The backward takes o, lse and go = dL/do and writes gq, gk, gv (each with its own
  * strides); ws: nf4_workspace_size(NF4_OP_ATTENTION_BWD, T, Hq, 0, 0) bytes.  A value
  * of a masked pair reaches no output, not even as 0 x NaN.  Deterministic.
@@ -422,6 +426,7 @@ typedef struct {
   int32_t Hq, Hk, D;
   int32_t dtype;
   float scale;
+  void* o_rest;
 } nf4_attention;
 nf4_status nf4_attention_fwd(const nf4_attention* d, void* o, int64_t o_token, int64_t o_head, float* lse,
                              void* stream);

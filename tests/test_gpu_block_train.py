@@ -159,3 +159,24 @@ def test_example_learns():
     import train_block
     losses = train_block.train(steps=40, tokens=512, hidden=512)
     assert losses[-1] < 0.5 * losses[0]
+
+
+@pytest.mark.parametrize("D,dtype", [(64, BF16), (128, torch.float16), (40, BF16), (37, BF16)])
+def test_attention_rest_of_the_output(D, dtype):
+    """o plus its rest is the unrounded output (to the rest's own rounding); a forward that no gradient follows makes none,
+    and a backward without it stays within the bounds that count o's rounding."""
+    n = gen(7)
+    q, k, v, go = (n(150, 2, D).to(dtype) for _ in range(4))
+    o, lse = nf4.attention_fwd(q, k, v)
+    want, mag = ref.attention(q, k, v, [0, 150], D ** -0.5, go)
+    u = ref.UNIT[dtype]
+    # the probabilities are rounded once (u of their products), o + rest to u * u
+    bound = (1.1 * u + 2.0 ** -12) * mag["o"] + 1.1 * u * u * want["o"].abs() + ref.TINY[dtype]
+    assert ((o.double() + lse.o_rest.double() - want["o"]).abs() <= bound).all()
+    o2, lse2 = nf4.attention_fwd(q, k, v, for_backward=False)
+    assert torch.equal(o, o2) and lse2.o_rest is None
+    smax = D ** -0.5 * (q.double().norm(dim=2).max() * k.double().norm(dim=2).max()).item()
+    for got, name in zip(nf4.attention_bwd(go, q, k, v, o2, lse2), ("gq", "gk", "gv")):
+        assert ((got.double() - want[name]).abs() <= ref.attention_bound(name, want[name], mag[name], dtype, smax)).all()
+    with pytest.raises(ValueError):
+        nf4.attention_bwd(go, q, k, v, o2, lse2, o_rest=lse.o_rest[:, :1])
