@@ -465,7 +465,9 @@ struct Cols {
 };
 
 // The shared memory of a ring CTA: gains [3][H] fp32 (w_post, scale times the channel
-// gate, w_pre; 1, scale and 0 where there is none), then the stages.
+// gate, w_pre; 1, scale and 0 where there is none), then the stages.  A thread's eight
+// gains lie four and four, half a row apart: neighbouring threads then read neighbouring
+// 16-byte pieces, without bank conflicts.
 template <typename T, int VEC, bool BWD>
 struct RowRing {
   using F = Frag<T, VEC>;
@@ -514,6 +516,9 @@ struct RowRing {
     for (int k = 0; k < F::kVecs; ++k)
       if (cols.in[k]) *reinterpret_cast<typename F::Raw*>(static_cast<T*>(row) + cols.col[k]) = f.v[k];
   }
+  __device__ __forceinline__ uint32_t gain_at(uint32_t c) const {  // c a multiple of 4
+    return VEC == 8 ? (c >> 3) * 4 + (c & 4 ? static_cast<uint32_t>(a.H) / 2 : 0u) : c;
+  }
   __device__ __forceinline__ void gain(float2 (&g)[kPairs], int which) const {
     const float* p = gains + which * a.H;
 #pragma unroll
@@ -521,7 +526,7 @@ struct RowRing {
 #pragma unroll
       for (int e = 0; e < VEC; e += 4) {
         float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (cols.in[k]) f = *reinterpret_cast<const float4*>(p + cols.col[k] + e);
+        if (cols.in[k]) f = *reinterpret_cast<const float4*>(p + gain_at(cols.col[k] + e));
         g[(k * VEC + e) / 2] = make_float2(f.x, f.y);
         g[(k * VEC + e) / 2 + 1] = make_float2(f.z, f.w);
       }
@@ -545,7 +550,7 @@ struct RowRing {
         float4 f = make_float4(none[k], none[k], none[k], none[k]);
         if (src[k]) f = *reinterpret_cast<const float4*>(src[k] + c);
         if (k == 1 && src[k]) f = make_float4(f.x * a.scale, f.y * a.scale, f.z * a.scale, f.w * a.scale);
-        *reinterpret_cast<float4*>(gains + k * a.H + c) = f;
+        *reinterpret_cast<float4*>(gains + k * a.H + gain_at(static_cast<uint32_t>(c))) = f;
       }
     __syncthreads();
   }
