@@ -11,6 +11,15 @@
 // m, unsigned for v), ties to the lower index; the update of p uses the m and v
 // from before they are rounded.  A block whose values are all zero gets scale 0.  A
 // NaN in a block makes its scale NaN, so the whole block reads as NaN.
+//
+// A warp takes a block, a lane eight neighbours, all tensors of a launch in one grid (the
+// table of tensors travels in the kernel's parameters).  fp32 states are bound by HBM (67 M
+// bf16 values: 222 us, 6.6 TB/s of 6.8 measured by a copy).  8-bit states move 10 bytes a
+// value instead of 22 but cost about 70 instructions, most of them for the codes (134 M
+// bf16 values: 385 us, 3.5 TB/s; issue slots at 60%, the rest latencies of the look-ups);
+// the set-up of the look-up tables adds about 8 us a launch.  Loading the next block ahead
+// was slower each way it was tried (435 us with fewer warps, 450 us with spills).  The
+// read-out of 8-bit states is bound by HBM (224 us, 6.0 TB/s).
 #include <cuda_runtime.h>
 
 #include <cstdint>

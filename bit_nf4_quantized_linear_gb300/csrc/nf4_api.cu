@@ -990,6 +990,8 @@ nf4_status attn_args(const nf4_attention* d, nf4::AttnArgs* a) {
   a->D = d->D;
   a->scale = d->scale;
   a->o_rest = d->o_rest;
+  // the launches' grids: a CTA per tile and head at most (the general kernels' tiles are the smallest)
+  if (nf4::attn_tiles(*a, 16) > INT32_MAX / (int64_t{2} * d->Hq)) return NF4_ERR_UNSUPPORTED_SHAPE;
   return NF4_OK;
 }
 
