@@ -15,11 +15,11 @@
 // A warp takes a block, a lane eight neighbours, all tensors of a launch in one grid (the
 // table of tensors travels in the kernel's parameters).  fp32 states are bound by HBM (67 M
 // bf16 values: 222 us, 6.6 TB/s of 6.8 measured by a copy).  8-bit states move 10 bytes a
-// value instead of 22 but cost about 70 instructions, most of them for the codes (134 M
-// bf16 values: 385 us, 3.5 TB/s; issue slots at 60%, the rest latencies of the look-ups);
-// the set-up of the look-up tables adds about 8 us a launch.  Loading the next block ahead
-// was slower each way it was tried (435 us with fewer warps, 450 us with spills).  The
-// read-out of 8-bit states is bound by HBM (224 us, 6.0 TB/s).
+// value instead of 22 but cost about 70 instructions, most of them for the codes: a warp's
+// next block is copied to shared memory while it codes the present one, with one CTA of 32
+// warps an SM, so that the look-up tables leave room for it (134 M bf16 values: 322 us, 4.2
+// TB/s; 385 us with two CTAs of 16 warps and loads as they are needed; 425 us with 24 warps
+// of more registers).  The read-out of 8-bit states is bound by HBM (224 us, 6.0 TB/s).
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -31,8 +31,10 @@
 namespace nf4 {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
+constexpr int kThreads = 512;  // of the read-out
+// 8-bit states: one CTA an SM, so that its look-up tables are there once and leave room for
+// the next blocks' data.
+constexpr int threads(int bits) { return bits == 8 ? 1024 : 512; }
 constexpr int kPer = kAdamBlock / 32;  // values of a block per lane
 
 // max that keeps a NaN of either side.
@@ -89,24 +91,17 @@ __device__ __forceinline__ int search(const Map<SIGNED>& mp, float r) {
 
 __device__ __forceinline__ int bucket_of(float x) { return static_cast<int>((__float_as_uint(x) >> 16) & 0x7fffu) - kBucket0; }
 
-// Levels, midpoints and buckets of a map, by the whole CTA.
+// Buckets of a map by `warps` warps, this one being number `warp` of them.
 template <bool SIGNED>
-__device__ void build_map(Map<SIGNED>& mp, const float* L) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (threadIdx.x < 256) mp.once[threadIdx.x] = L[threadIdx.x];
-  if (threadIdx.x == 0) mp.searched = 0;
-  __syncthreads();
-  for (int i = warp; i < 256; i += kWarps) mp.level[i * 32 + lane] = mp.once[i];
-  // half the sum rounded down: the halving is exact
-  if (threadIdx.x < 255) mp.mid[threadIdx.x] = 0.5f * __fadd_rd(mp.once[threadIdx.x], mp.once[threadIdx.x + 1]);
-  __syncthreads();
+__device__ __forceinline__ void build_buckets(Map<SIGNED>& mp, int warp, int warps) {
+  const int lane = threadIdx.x & 31;
   int zero = 0;  // midpoints below zero: 0 .. zero - 1
   for (int i = lane; i < 255; i += 32) zero += mp.mid[i] < 0.0f;
   zero = __reduce_add_sync(0xffffffffu, zero);
   if (!SIGNED && zero > 0) mp.searched = 1;
   // midpoint i of the positive ones fills the buckets after its predecessor's, up to its
   // own; the last stretch, past the last midpoint, is item 255
-  for (int i = zero + warp; i <= 255; i += kWarps) {
+  for (int i = zero + warp; i <= 255; i += warps) {
     const int from = i == zero ? 0 : bucket_of(mp.mid[i - 1]) + 1;
     const int own = i == 255 ? kBuckets : bucket_of(mp.mid[i]);
     if (i < 255 && (own <= 0 || own >= kBuckets || own < from)) mp.searched = 1;
@@ -119,7 +114,7 @@ __device__ void build_map(Map<SIGNED>& mp, const float* L) {
     // comparison is |r| >= |mid|, so the threshold is the fp32 before it (where that lies
     // in the bucket before, every value here is above it)
     uint32_t* e = mp.entry + kBuckets;
-    for (int i = zero - 1 - warp; i >= -1; i -= kWarps) {
+    for (int i = zero - 1 - warp; i >= -1; i -= warps) {
       const int from = i == zero - 1 ? 0 : bucket_of(mp.mid[i + 1]) + 1;
       const int own = i < 0 ? kBuckets : bucket_of(mp.mid[i]);
       if (i >= 0 && (own <= 0 || own >= kBuckets || own < from)) mp.searched = 1;
@@ -130,8 +125,24 @@ __device__ void build_map(Map<SIGNED>& mp, const float* L) {
       }
     }
     if (zero == 0)
-      for (int b = threadIdx.x; b < kBuckets; b += kThreads) e[b] = kNoMid;
+      for (int b = warp * 32 + lane; b < kBuckets; b += warps * 32) e[b] = kNoMid;
   }
+}
+
+// Levels, midpoints and buckets of both maps, by the whole CTA, each by a half of it.
+__device__ __forceinline__ void build_maps(Maps& maps, const float* levels_m, const float* levels_v) {
+  constexpr int kHalf = threads(8) / 2, kWarps = kHalf / 32;
+  const int lane = threadIdx.x & 31, half = threadIdx.x / kHalf, at = threadIdx.x % kHalf, warp = at / 32;
+  float* once = half ? maps.v.once : maps.m.once;
+  float* copies = half ? maps.v.level : maps.m.level;
+  if (at < 256) once[at] = (half ? levels_v : levels_m)[at];
+  if (at == 0) (half ? maps.v.searched : maps.m.searched) = 0;
+  __syncthreads();
+  for (int i = warp; i < 256; i += kWarps) copies[i * 32 + lane] = once[i];
+  // half the sum rounded down: the halving is exact
+  if (at < 255) (half ? maps.v.mid : maps.m.mid)[at] = 0.5f * __fadd_rd(once[at], once[at + 1]);
+  __syncthreads();
+  if (half) build_buckets(maps.v, warp, kWarps); else build_buckets(maps.m, warp, kWarps);
   __syncthreads();
 }
 
@@ -283,6 +294,35 @@ struct Place {
   int64_t blk;
 };
 
+// A warp's next block on its way through shared memory: a lane copies and later reads only
+// its own eight values of each array, in pieces of 16 bytes (8 of the codes), so that its own
+// wait suffices.
+template <typename T>
+struct Slot {
+  uint4 g[sizeof(T) / 2][32], p[sizeof(T) / 2][32];
+  uint2 m[32], v[32];
+  template <int N>
+  static __device__ __forceinline__ void copy(void* to, const void* from) {
+    const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(to));
+    if (N == 16)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
+    else
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(at), "l"(from) : "memory");
+  }
+  __device__ __forceinline__ void fetch(const Place& at, int lane) {
+    const int64_t base = at.blk * kAdamBlock + lane * kPer;
+    const T *gr = static_cast<const T*>(at.t->grad) + base, *pa = static_cast<const T*>(at.t->param) + base;
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) {
+      copy<16>(&g[i][lane], gr + 4 * i);
+      copy<16>(&p[i][lane], pa + 4 * i);
+    }
+    copy<8>(&m[lane], static_cast<const uint8_t*>(at.t->m) + base);
+    copy<8>(&v[lane], static_cast<const uint8_t*>(at.t->v) + base);
+  }
+};
+__device__ __forceinline__ void wait_copies() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // A lane's eight values of a block as they lie in memory.
 template <typename T, int BITS>
 struct Raw {
@@ -296,25 +336,28 @@ struct Raw {
                    : "=r"(to[0]), "=r"(to[1]), "=r"(to[2]), "=r"(to[3]), "=r"(to[4]), "=r"(to[5]), "=r"(to[6]), "=r"(to[7])
                    : "l"(from)
                    : "memory");
-    } else if constexpr (N == 4) {
+    } else {
       const uint4 x = *static_cast<const uint4*>(from);
       to[0] = x.x; to[1] = x.y; to[2] = x.z; to[3] = x.w;
-    } else {
-      const uint2 x = *static_cast<const uint2*>(from);
-      to[0] = x.x; to[1] = x.y;
     }
   }
   __device__ __forceinline__ void load(const Place& at, int lane) {
     const int64_t base = at.blk * kAdamBlock + lane * kPer;
     get(static_cast<const T*>(at.t->grad) + base, g);
     get(static_cast<const T*>(at.t->param) + base, p);
-    constexpr int64_t size = BITS == 8 ? 1 : 4;
-    get(static_cast<const char*>(at.t->m) + base * size, m);
-    get(static_cast<const char*>(at.t->v) + base * size, v);
-    if (BITS == 8) {
-      sm = at.t->m_absmax[at.blk];
-      sv = at.t->v_absmax[at.blk];
+    get(static_cast<const float*>(at.t->m) + base, m);
+    get(static_cast<const float*>(at.t->v) + base, v);
+  }
+  __device__ __forceinline__ void take(const Slot<T>& s, int lane) {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) {
+      const uint4 a = s.g[i][lane], b = s.p[i][lane];
+      g[4 * i] = a.x; g[4 * i + 1] = a.y; g[4 * i + 2] = a.z; g[4 * i + 3] = a.w;
+      p[4 * i] = b.x; p[4 * i + 1] = b.y; p[4 * i + 2] = b.z; p[4 * i + 3] = b.w;
     }
+    const uint2 a = s.m[lane], b = s.v[lane];
+    m[0] = a.x; m[1] = a.y;
+    v[0] = b.x; v[1] = b.y;
   }
   static __device__ __forceinline__ void widen(const uint32_t (&w)[2 * sizeof(T)], float (&x)[kPer]) {
 #pragma unroll
@@ -323,10 +366,10 @@ struct Raw {
 };
 
 // A block of 256 values by one warp, a lane owning eight neighbours: from `raw` (WIDE), or
-// value by value.
-template <typename T, int BITS, bool WIDE>
+// value by value.  `used()` runs once nothing of `raw` is needed any more.
+template <typename T, int BITS, bool WIDE, typename F>
 __device__ __forceinline__ void block_step(const AdamArgs& a, const Maps& maps, const Place& at, const Raw<T, BITS>& raw,
-                                           int lane, float gs) {
+                                           int lane, float gs, F used) {
   const AdamTensor& t = *at.t;
   const int64_t blk = at.blk, base = blk * kAdamBlock + lane * kPer;
   T* p = static_cast<T*>(t.param) + base;
@@ -410,6 +453,7 @@ __device__ __forceinline__ void block_step(const AdamArgs& a, const Maps& maps, 
   }
   top_m = warp_absmax_nan(top_m);
   top_v = warp_absmax_nan(top_v);
+  used();
   if (lane == 0) {
     t.m_absmax[blk] = top_m;
     t.v_absmax[blk] = top_v;
@@ -418,36 +462,79 @@ __device__ __forceinline__ void block_step(const AdamArgs& a, const Maps& maps, 
   store_codes<false, WIDE>(maps.v, v, top_v, vc, have);
 }
 
-template <typename T, int BITS>
-__global__ void __launch_bounds__(kThreads, 2) adamw_kernel(const __grid_constant__ AdamTable tab,
-                                                            const __grid_constant__ AdamArgs a) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  Maps& maps = *reinterpret_cast<Maps*>(smem);
-  if (BITS == 8) {
-    build_map(maps.m, a.levels_m);
-    build_map(maps.v, a.levels_v);
-  }
-  const float gs = a.grad_scale ? *a.grad_scale : 1.0f;
-  const int lane = threadIdx.x & 31;
-  const int64_t blocks = tab.blk0[tab.count];
-  // A CTA takes one stretch of blocks, its warps in turn: a stretch lies in few tensors.
-  const int64_t per = (blocks + gridDim.x - 1) / gridDim.x, end = min(blocks, (blockIdx.x + 1) * per);
-  int ti = -1;
+// Finds the places of rising blocks: the tensor is searched for where the last one ends.
+struct Finder {
+  int ti = 0;
   int64_t first = 0, last = 0;
-  for (int64_t b = blockIdx.x * per + (threadIdx.x >> 5); b < end; b += kWarps) {
+  __device__ __forceinline__ Place at(const AdamTable& tab, int64_t b) {
     if (b >= last) {
       ti = find_tensor(tab, b);
       first = tab.blk0[ti];
       last = tab.blk0[ti + 1];
     }
-    const AdamTensor& t = tab.t[ti];
-    const Place at{&t, b - first};
-    Raw<T, BITS> raw;
-    if (t.vec && (at.blk + 1) * kAdamBlock <= t.n) {  // all of the block inside, every array fit for vectors
-      raw.load(at, lane);
-      block_step<T, BITS, true>(a, maps, at, raw, lane, gs);
-    } else {
-      block_step<T, BITS, false>(a, maps, at, raw, lane, gs);
+    return Place{&tab.t[ti], b - first};
+  }
+};
+
+// All of the block inside, every array fit for vectors.
+__device__ __forceinline__ bool wide(const Place& at) { return at.t->vec && (at.blk + 1) * kAdamBlock <= at.t->n; }
+
+template <typename T, int BITS>
+constexpr int smem_bytes() { return BITS == 8 ? sizeof(Maps) + threads(8) / 32 * sizeof(Slot<T>) : 0; }
+
+template <typename T, int BITS>
+__global__ void __launch_bounds__(threads(BITS), BITS == 8 ? 1 : 2) adamw_kernel(const __grid_constant__ AdamTable tab,
+                                                                                 const __grid_constant__ AdamArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  constexpr int kWarps = threads(BITS) / 32;
+  Slot<T>& slot = reinterpret_cast<Slot<T>*>(smem)[BITS == 8 ? threadIdx.x / 32 : 0];
+  Maps& maps = *reinterpret_cast<Maps*>(smem + (BITS == 8 ? kWarps * sizeof(Slot<T>) : 0));
+  const int lane = threadIdx.x & 31;
+  const int64_t blocks = tab.blk0[tab.count];
+  // A CTA takes one stretch of blocks, its warps in turn: a stretch lies in few tensors.
+  const int64_t per = (blocks + gridDim.x - 1) / gridDim.x, end = min(blocks, (blockIdx.x + 1) * per);
+  int64_t b = blockIdx.x * per + threadIdx.x / 32;
+  Finder find;
+  Raw<T, BITS> raw;
+  if constexpr (BITS == 32) {
+    const float gs = a.grad_scale ? *a.grad_scale : 1.0f;
+    for (; b < end; b += kWarps) {
+      const Place at = find.at(tab, b);
+      if (wide(at)) {
+        raw.load(at, lane);
+        block_step<T, BITS, true>(a, maps, at, raw, lane, gs, [] {});
+      } else {
+        block_step<T, BITS, false>(a, maps, at, raw, lane, gs, [] {});
+      }
+    }
+  } else {
+    Place at{}, next{};
+    bool full = false;
+    float sm = 0.0f, sv = 0.0f;  // scales of the block on its way
+    auto fetch = [&](int64_t i) {
+      full = false;
+      if (i >= end) return;
+      next = find.at(tab, i);
+      full = wide(next);
+      if (!full) return;
+      slot.fetch(next, lane);
+      sm = next.t->m_absmax[next.blk];
+      sv = next.t->v_absmax[next.blk];
+    };
+    fetch(b);
+    build_maps(maps, a.levels_m, a.levels_v);
+    const float gs = a.grad_scale ? *a.grad_scale : 1.0f;
+    for (; b < end; b += kWarps) {
+      at = next;
+      if (full) {
+        wait_copies();
+        raw.take(slot, lane);
+        raw.sm = sm;
+        raw.sv = sv;
+        block_step<T, BITS, true>(a, maps, at, raw, lane, gs, [&] { fetch(b + kWarps); });
+      } else {
+        block_step<T, BITS, false>(a, maps, at, raw, lane, gs, [&] { fetch(b + kWarps); });
+      }
     }
   }
 }
@@ -486,15 +573,15 @@ bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % 
 
 template <typename T, int BITS>
 cudaError_t launch_one(const AdamTable& tab, const AdamArgs& a, int sms, cudaStream_t s) {
-  constexpr int kSmem = BITS == 8 ? static_cast<int>(sizeof(Maps)) : 0;
+  constexpr int kSmem = smem_bytes<T, BITS>(), kWarps = threads(BITS) / 32;
   static bool configured = false;
   if (!configured && kSmem > 0) {
     if (cudaError_t e = cudaFuncSetAttribute(adamw_kernel<T, BITS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem))
       return e;
     configured = true;
   }
-  const int64_t want = (tab.blk0[tab.count] + kWarps - 1) / kWarps, most = 2 * static_cast<int64_t>(sms);
-  adamw_kernel<T, BITS><<<static_cast<unsigned>(want < most ? want : most), kThreads, kSmem, s>>>(tab, a);
+  const int64_t want = (tab.blk0[tab.count] + kWarps - 1) / kWarps, most = (BITS == 8 ? 1 : 2) * static_cast<int64_t>(sms);
+  adamw_kernel<T, BITS><<<static_cast<unsigned>(want < most ? want : most), threads(BITS), kSmem, s>>>(tab, a);
   return cudaGetLastError();
 }
 
