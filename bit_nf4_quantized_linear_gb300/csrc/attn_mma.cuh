@@ -57,6 +57,20 @@ static __device__ __noinline__ void attn_drain(uint32_t bar, uint32_t parity, co
   }
 }
 
+// True in one lane of a converged warp, the same each time.  Asynchronous operations (MMAs,
+// commits, copies) are issued under it and not under `lane == 0`: their operands lie in
+// registers of the warp, and only here does the compiler know that one lane is active (an
+// MMA took about 100 cycles to issue under the other).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+
 // Tile of 128 rows x 64 columns of one head of a [T][heads][D] tensor.
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t c0, int32_t c1,
                                             int32_t c2) {

@@ -203,11 +203,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t id_o = F16 ? idesc_f16_f32(128, ksteps * 16, false, true) : idesc_bf16_f32(128, ksteps * 16, false, true);
       auto wait = [&](uint64_t& b, uint32_t parity) { return attn_wait_warp(smem_addr(&b), parity, guard); };
       auto commit = [&](uint64_t& b) {
-        if (lane == 0) mma_commit(smem_addr(&b));
+        if (elect_one()) mma_commit(smem_addr(&b));
         __syncwarp();
       };
       auto scores = [&](int t, uint32_t kaddr) {
-        if (lane == 0) {
+        if (elect_one()) {
           mma_over_columns<FULL, PANELS>(tmem + t * 128, sbase + G::kOffQ + t * G::kTileBytes, kaddr, id_s, ksteps);
           mma_commit(smem_addr(&sh.s_full[t]));
         }
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (j >= n) continue;
           if (!(ok = wait(sh.p_full[t], j & 1))) break;
           tc_fence_after();
-          if (lane == 0) {
+          if (elect_one()) {
             mma_over_rows(tmem + 256 + t * 128, tmem + t * 128, 32, vaddr, id_o, j > 0);
             if (j + 1 == n) mma_commit(smem_addr(&sh.o_full[t]));
           }

@@ -66,7 +66,7 @@ struct Shared {
   int abort_flag;
   int dirty;
   uint64_t own_full, full[3], vfull[2], empty[3], vempty[2], ready[2], diag, clean;
-  uint64_t s_full[2], dp_full, p_full, ds_full, out_full, drain;
+  uint64_t s_full[2], dp_full, dp_free, p_full, ds_full, out_full, drain;
 };
 
 // Row statistics of the keys' CTAs, negated (they are only subtracted), in the tile of
@@ -151,27 +151,27 @@ struct Ctx {
     return attn_wait_warp(bar(b), parity, guard);
   }
   __device__ __forceinline__ void expect(const uint64_t& b, uint32_t n) const {
-    if (lane == 0) mbar_arrive_expect_tx(bar(b), n);
+    if (elect_one()) mbar_arrive_expect_tx(bar(b), n);
     __syncwarp();
   }
   __device__ __forceinline__ void commit(const uint64_t& b) const {
-    if (lane == 0) mma_commit(bar(b));
+    if (elect_one()) mma_commit(bar(b));
     __syncwarp();
   }
   __device__ __forceinline__ void load(const CUtensorMap* m, int to, const uint64_t& b, int head, int row) const {
-    if (lane == 0)
+    if (elect_one())
       for (int x = 0; x < boxes; ++x) tma_load_3d(tile(to) + x * kPanelBytes, m, bar(b), x * 64, head, row);
     __syncwarp();
   }
   __device__ __forceinline__ uint32_t bytes() const { return boxes * kPanelBytes; }
   // D = A B^T over the head's columns, both operands in shared memory.
   __device__ __forceinline__ void over_columns(uint32_t d, int ta, int tb, uint32_t idesc) const {
-    if (lane == 0) mma_over_columns<FULL, PANELS>(d, tile(ta), tile(tb), idesc, ksteps);
+    if (elect_one()) mma_over_columns<FULL, PANELS>(d, tile(ta), tile(tb), idesc, ksteps);
     __syncwarp();
   }
   // D += A B over the tile's 128 rows, A in tensor memory in two halves 64 columns apart.
   __device__ __forceinline__ void over_rows(uint32_t d, uint32_t at, int tb, uint32_t idesc, bool more) const {
-    if (lane == 0) mma_over_rows(d, at, 64, tile(tb), idesc, more);
+    if (elect_one()) mma_over_rows(d, at, 64, tile(tb), idesc, more);
     __syncwarp();
   }
 };
@@ -440,12 +440,13 @@ __device__ __forceinline__ void queries_cta(const Ctx<F16, PANELS, FULL>& x, con
       if (ok && n > 1 && (ok = key(1))) scores(1);
     }
     for (int j = 0; ok && j < n; ++j) {
-      if (!(ok = x.wait(sh.ds_full, j & 1))) break;
-      tc_fence_after();
       if (j + 1 < n) {
-        if (!(ok = x.wait(sh.vfull[(j + 1) & 1], ((j + 1) >> 1) & 1))) break;
+        if (!(ok = x.wait(sh.vfull[(j + 1) & 1], ((j + 1) >> 1) & 1) && x.wait(sh.dp_free, j & 1))) break;
+        tc_fence_after();
         grads(j + 1);
       }
+      if (!(ok = x.wait(sh.ds_full, j & 1))) break;
+      tc_fence_after();
       x.over_rows(DQ, S + (j & 1) * 128, 2 + j % 3, id_o, j > 0);
       x.commit(sh.empty[j % 3]);
       if (j + 2 < n) {
@@ -481,6 +482,7 @@ __device__ __forceinline__ void queries_cta(const Ctx<F16, PANELS, FULL>& x, con
       tmem_ld<32>(tp + 32, d + 32);
       tmem_wait_ld<64>(s);
       tmem_wait_ld<64>(d);
+      arrive_warp(x.bar(sh.dp_free));
 #pragma unroll
       for (int q = 0; q < 64; q += 32) {
         uint32_t p[16];
@@ -548,6 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_addr(&sh.clean), 64);
       mbar_init(smem_addr(&sh.p_full), kCompute);
       mbar_init(smem_addr(&sh.ds_full), kCompute);
+      mbar_init(smem_addr(&sh.dp_free), kCompute);
       fence_mbar_init();
     }
     __syncwarp();
