@@ -55,25 +55,24 @@ constexpr float kShift = 14.0f, kUnshift = 1.0f / 16384.0f;
 template <int PANELS>
 struct Geo {
   static constexpr int kTileBytes = PANELS * kPanelBytes;
-  // keys: K, V, then two stages of (Q, dO).  queries: Q, dO, three K, two V.
-  static constexpr int kTiles = 7;
-  static constexpr int kSmem = kTiles * kTileBytes + 1024;
+  // keys: K, V, three Q, two dO.  queries: Q, dO, three K, two V.
+  static constexpr int kSmem = 7 * kTileBytes;
+};
+
+// Row statistics of the keys' CTAs, negated (they are only subtracted).
+struct alignas(16) Rows {
+  float lse2[2][kAttnTile];
+  float delta[2][kAttnTile];
 };
 
 struct Shared {
+  Rows rows;
   AttnTile tile;
   uint32_t tmem;
   int abort_flag;
   int dirty;
-  uint64_t own_full, full[3], vfull[2], empty[3], vempty[2], ready[2], diag, clean;
+  uint64_t own_full, full[3], vfull[2], empty[3], vempty[2], ready[2], gready[2], diag, clean;
   uint64_t s_full[2], dp_full, dp_free, p_full, ds_full, out_full, drain;
-};
-
-// Row statistics of the keys' CTAs, negated (they are only subtracted), in the tile of
-// shared memory that these leave free.
-struct Rows {
-  float lse2[2][kAttnTile];
-  float delta[2][kAttnTile];
 };
 
 // delta[h][t] = do . (o + what its rounding left over): 16 bytes a lane, rows of a head
@@ -177,35 +176,39 @@ struct Ctx {
 };
 
 // ------------------------------------------------------------------------- keys --
-// Tiles in shared memory: 0 K, 1 V, 2 + 2 st Q, 3 + 2 st dO, 6 Rows.  Tensor memory: S' and P'
-// from 0, dP' and dS' from 128, dV from 256, dK from 384.
+// Tiles in shared memory: 0 K, 1 V, 2 + it % 3 Q, 5 + it % 2 dO (dO of a step is free after
+// dV, Q only after dK).  Tensor memory: S' and P' from 0, dP' and dS' from 128, dV from 256,
+// dK from 384.
 template <bool COMPUTE, bool F16, int PANELS, bool FULL, typename T>
 __device__ __forceinline__ void keys_cta(const Ctx<F16, PANELS, FULL>& x, const CUtensorMap* mq, const CUtensorMap* mk,
                                          const CUtensorMap* mv, const CUtensorMap* mg, int hk) {
   const AttnArgs& a = x.a;
   Shared& sh = x.sh;
   const AttnTile& w = x.w;
-  Rows& rs = *reinterpret_cast<Rows*>(x.smem + 6 * Geo<PANELS>::kTileBytes);
+  Rows& rs = sh.rows;
   const int jt = w.tile, nt = (w.len + kAttnTile - 1) / kAttnTile, nq = nt - jt;
   const int group = a.Hq / a.Hk, n = group * nq;
   const int row0 = static_cast<int>(w.row0), lane = x.lane, warp = x.warp;
   if constexpr (!COMPUTE) {
   if (warp == kWarpLoad) {
-    int done = 0, g = 0, i = jt;
+    int loads_q = 0, loads_g = 0, g = 0, i = jt;
     for (int it = 0; it < n; ++it) {
-      const int st = it & 1;
-      if (!x.wait(sh.empty[st], ((it >> 1) & 1) ^ 1)) break;
-      x.expect(sh.full[st], 2 * x.bytes());
-      x.load(mq, 2 + 2 * st, sh.full[st], hk * group + g, row0 + i * kAttnTile);
-      x.load(mg, 3 + 2 * st, sh.full[st], hk * group + g, row0 + i * kAttnTile);
-      done = it + 1;
+      if (!x.wait(sh.empty[it % 3], ((it / 3) & 1) ^ 1)) break;
+      x.expect(sh.full[it % 3], x.bytes());
+      x.load(mq, 2 + it % 3, sh.full[it % 3], hk * group + g, row0 + i * kAttnTile);
+      loads_q = it + 1;
+      if (!x.wait(sh.vempty[it & 1], ((it >> 1) & 1) ^ 1)) break;
+      x.expect(sh.vfull[it & 1], x.bytes());
+      x.load(mg, 5 + (it & 1), sh.vfull[it & 1], hk * group + g, row0 + i * kAttnTile);
+      loads_g = it + 1;
       if (++i == nt) {
         i = jt;
         ++g;
       }
     }
     attn_drain(x.bar(sh.own_full), 0, x.guard);
-    for (int it = done < 2 ? 0 : done - 2; it < done; ++it) attn_drain(x.bar(sh.full[it & 1]), (it >> 1) & 1, x.guard);
+    for (int it = loads_q < 3 ? 0 : loads_q - 3; it < loads_q; ++it) attn_drain(x.bar(sh.full[it % 3]), (it / 3) & 1, x.guard);
+    for (int it = loads_g < 2 ? 0 : loads_g - 2; it < loads_g; ++it) attn_drain(x.bar(sh.vfull[it & 1]), (it >> 1) & 1, x.guard);
     __syncwarp();
   } else if (warp >= kWarpPrep) {
     int g = 0, i = jt;
@@ -219,16 +222,19 @@ __device__ __forceinline__ void keys_cta(const Ctx<F16, PANELS, FULL>& x, const 
         l[e] = (F16 ? kShift : 0.0f) - lse2_of(a, at + r0 + e, r0 + e < rows);
         d[e] = r0 + e < rows ? -a.delta[at + r0 + e] * (F16 ? kUnshift : 1.0f) : 0.0f;
       }
-      if (!x.wait(sh.empty[st], ((it >> 1) & 1) ^ 1)) break;
+      // the statistics of two steps ago have been read once that step's dK is done
+      if (it >= 2 && !x.wait(sh.empty[(it - 2) % 3], ((it - 2) / 3) & 1)) break;
       *reinterpret_cast<float2*>(&rs.lse2[st][r0]) = make_float2(l[0], l[1]);
       *reinterpret_cast<float2*>(&rs.delta[st][r0]) = make_float2(d[0], d[1]);
-      if (!x.wait(sh.full[st], (it >> 1) & 1)) break;
-      if (i == jt || rows < kAttnTile) {
-        clean_tile<F16, PANELS>(x.smem + (2 + 2 * st) * Geo<PANELS>::kTileBytes, rows, i == jt, warp - kWarpPrep, 2);
-        if (clean_tile<F16, PANELS>(x.smem + (3 + 2 * st) * Geo<PANELS>::kTileBytes, rows, i == jt, warp - kWarpPrep, 2) && lane == 0)
-          sh.dirty = 1;
-      }
+      const bool clean = i == jt || rows < kAttnTile;
+      if (!x.wait(sh.full[it % 3], (it / 3) & 1)) break;
+      if (clean) clean_tile<F16, PANELS>(x.smem + (2 + it % 3) * Geo<PANELS>::kTileBytes, rows, i == jt, warp - kWarpPrep, 2);
       mbar_arrive(x.bar(sh.ready[st]));
+      if (!x.wait(sh.vfull[st], (it >> 1) & 1)) break;
+      if (clean && clean_tile<F16, PANELS>(x.smem + (5 + st) * Geo<PANELS>::kTileBytes, rows, i == jt, warp - kWarpPrep, 2) &&
+          lane == 0)
+        sh.dirty = 1;
+      mbar_arrive(x.bar(sh.gready[st]));
       if (++i == nt) {
         i = jt;
         ++g;
@@ -242,26 +248,30 @@ __device__ __forceinline__ void keys_cta(const Ctx<F16, PANELS, FULL>& x, const 
     if (ok) {
       x.over_columns(S, 0, 2, id_s);
       x.commit(sh.s_full[0]);
-      x.over_columns(P, 1, 3, id_s);
-      x.commit(sh.dp_full);
+      if ((ok = x.wait(sh.gready[0], 0))) {
+        x.over_columns(P, 1, 5, id_s);
+        x.commit(sh.dp_full);
+      }
     }
     for (int it = 0; ok && it < n; ++it) {
-      const int st = it & 1, st1 = st ^ 1;
+      const int st = it & 1, st1 = st ^ 1, next = ((it + 1) >> 1) & 1;
       const bool more = it + 1 < n;
       if (!(ok = x.wait(sh.p_full, it & 1))) break;
       tc_fence_after();
-      x.over_rows(DV, S, 3 + 2 * st, id_o, it > 0);
+      x.over_rows(DV, S, 5 + st, id_o, it > 0);
+      x.commit(sh.vempty[st]);
       if (more) {
-        if (!(ok = x.wait(sh.ready[st1], ((it + 1) >> 1) & 1))) break;
-        x.over_columns(S, 0, 2 + 2 * st1, id_s);
+        if (!(ok = x.wait(sh.ready[st1], next))) break;
+        x.over_columns(S, 0, 2 + (it + 1) % 3, id_s);
         x.commit(sh.s_full[0]);
       }
       if (!(ok = x.wait(sh.ds_full, it & 1))) break;
       tc_fence_after();
-      x.over_rows(DK, P, 2 + 2 * st, id_o, it > 0);
-      x.commit(sh.empty[st]);
+      x.over_rows(DK, P, 2 + it % 3, id_o, it > 0);
+      x.commit(sh.empty[it % 3]);
       if (more) {
-        x.over_columns(P, 1, 3 + 2 * st1, id_s);
+        if (!(ok = x.wait(sh.gready[st1], next))) break;
+        x.over_columns(P, 1, 5 + st1, id_s);
         x.commit(sh.dp_full);
       } else {
         x.commit(sh.out_full);
@@ -523,38 +533,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mg,
                     const __grid_constant__ AttnArgs a, const int64_t key_ctas) {
   using T = typename std::conditional<F16, __half, __nv_bfloat16>::type;
-  extern __shared__ uint8_t smem_raw[];
+  // the tiles' swizzle counts from multiples of 1024 bytes, and nothing is left to round up to one
+  extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ Shared sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint8_t* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
   const bool keys = blockIdx.x < key_ctas;
-  const int64_t id = keys ? blockIdx.x : blockIdx.x - key_ctas;
-  const int heads = keys ? a.Hk : a.Hq, h = static_cast<int>(id % heads);
+  const uint32_t id = keys ? blockIdx.x : blockIdx.x - static_cast<uint32_t>(key_ctas);
+  const uint32_t heads = keys ? a.Hk : a.Hq, tile_id = id / heads;
+  const int h = static_cast<int>(id - tile_id * heads);
 
-  // The load warp sets the CTA up on its own -- barriers, its tile, the loads of the tiles
-  // that the CTA owns -- while the MMA warp allocates tensor memory.
+  // The load warp finds the CTA's tile and issues the loads of the tiles that it owns, the
+  // MMA warp allocates tensor memory, and another sets up the barriers.
   if (warp == kWarpLoad) {
     if (lane == 0) {
       prefetch_tensormap(&mq);
       prefetch_tensormap(&mk);
       prefetch_tensormap(&mv);
       prefetch_tensormap(&mg);
-      sh.abort_flag = 0;
-      sh.dirty = 0;
-      uint64_t* one[] = {&sh.own_full, &sh.full[0], &sh.full[1], &sh.full[2], &sh.vfull[0], &sh.vfull[1], &sh.empty[0],
-                         &sh.empty[1], &sh.empty[2], &sh.vempty[0], &sh.vempty[1], &sh.diag, &sh.s_full[0], &sh.s_full[1],
-                         &sh.dp_full, &sh.out_full, &sh.drain};
-      for (uint64_t* b : one) mbar_init(smem_addr(b), 1);
-      mbar_init(smem_addr(&sh.ready[0]), 64);
-      mbar_init(smem_addr(&sh.ready[1]), 64);
-      mbar_init(smem_addr(&sh.clean), 64);
-      mbar_init(smem_addr(&sh.p_full), kCompute);
-      mbar_init(smem_addr(&sh.ds_full), kCompute);
-      mbar_init(smem_addr(&sh.dp_free), kCompute);
+      mbar_init(smem_addr(&sh.own_full), 1);
       fence_mbar_init();
     }
     __syncwarp();
-    const AttnTile w = find_tile(a, id / heads, kAttnTile, !keys);
+    const AttnTile w = find_tile(a, tile_id, kAttnTile, !keys);
     if (lane == 0) sh.tile = w;
     if (lane == 0 && w.tile >= 0) {
       const int boxes = (a.D + 63) / 64, r = static_cast<int>(w.row0) + w.tile * kAttnTile;
@@ -570,6 +570,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_addr(&sh.tmem), 512);
     tmem_relinquish();
   } else if (warp >= kWarpPrep) {
+    if (warp == kWarpPrep && lane == 0) {
+      sh.abort_flag = 0;
+      sh.dirty = 0;
+      uint64_t* one[] = {&sh.full[0], &sh.full[1], &sh.full[2], &sh.vfull[0], &sh.vfull[1], &sh.empty[0], &sh.empty[1],
+                         &sh.empty[2], &sh.vempty[0], &sh.vempty[1], &sh.diag, &sh.s_full[0], &sh.s_full[1], &sh.dp_full,
+                         &sh.out_full, &sh.drain};
+      for (uint64_t* b : one) mbar_init(smem_addr(b), 1);
+      uint64_t* prep[] = {&sh.ready[0], &sh.ready[1], &sh.gready[0], &sh.gready[1], &sh.clean};
+      for (uint64_t* b : prep) mbar_init(smem_addr(b), 64);
+      uint64_t* groups[] = {&sh.p_full, &sh.ds_full, &sh.dp_free};
+      for (uint64_t* b : groups) mbar_init(smem_addr(b), kCompute);
+      fence_mbar_init();
+    }
+    __syncwarp();
     int64_t g0, g1;
     gap_rows(a, &g0, &g1);
     if (g0 > 0 || g1 < a.T) {
