@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // the MMA warp allocates tensor memory.
   auto load = [&](const CUtensorMap* m, uint32_t dst, uint32_t bar, int head, int r) {
     const int boxes = (a.D + 63) / 64;
-    if (lane == 0) {
+    if (elect_one()) {
       mbar_arrive_expect_tx(bar, boxes * kPanelBytes);
       for (int b = 0; b < boxes; ++b) tma_load_3d(dst + b * kPanelBytes, m, bar, b * 64, head, r);
     }

@@ -556,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     const AttnTile w = find_tile(a, tile_id, kAttnTile, !keys);
     if (lane == 0) sh.tile = w;
-    if (lane == 0 && w.tile >= 0) {
+    if (w.tile >= 0 && elect_one()) {
       const int boxes = (a.D + 63) / 64, r = static_cast<int>(w.row0) + w.tile * kAttnTile;
       const uint32_t bar = smem_addr(&sh.own_full), to = smem_addr(smem);
       mbar_arrive_expect_tx(bar, 2 * boxes * kPanelBytes);
