@@ -231,7 +231,7 @@ class NF4NormResidualFn(torch.autograd.Function):
         y, residual, w_post, gate, w_pre, stats = ctx.saved_tensors
         if gz is None and gh is None:
             return (None,) * 7
-        gz, gh = (g if g is None or g.stride(1) == 1 and g.stride(0) >= g.shape[1] else g.contiguous() for g in (gz, gh))
+        gz, gh = (g if g is None or g.stride(1) == 1 else g.contiguous() for g in (gz, gh))
         need = ctx.needs_input_grad
         gy, gr, gw_post, ggate, gw_pre = block_ops.norm_residual_bwd(
             gz, gh, y, residual, stats, w_post=w_post, gate=gate, scale=ctx.scale, w_pre=w_pre, eps=ctx.eps, need_y=need[0],

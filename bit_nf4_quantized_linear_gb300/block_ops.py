@@ -175,21 +175,27 @@ def _explain_norm(name, y, w_post, gate, w_pre, rows):
 
 
 def _norm(name, y, w_post, gate, scale, w_pre, eps, rows):
-    """The packed nf4_norm_residual of checked arguments, the gate's kind, and the row pitches of `rows`, which
-    starts with the residual: (what, tensor or None) of y's shape and dtype."""
+    """The packed nf4_norm_residual of checked arguments, the gate's kind, the row pitches of `rows`, which starts
+    with the residual ((what, tensor or None) of y's shape and dtype), and the tensors that the pointers lie in: those
+    of `rows`, y and the gate.  A pitch is the row width at least, so rows that share storage (broadcast over the
+    tokens, or overlapping) are copied; the pitch of a single row is never used."""
     dt, dev, ys = y.dtype, y.device, y.shape
     H = ys[-1] if len(ys) == 2 else 0
     ok = dt in _DTYPES and dev.type == "cuda" and H > 0 and (H == 1 or y.stride(1) == 1)
     kind, gp, gl = _lib.GATE_NONE, 0, 0
     wp = wn = 0
-    pitches = []
+    pitches, held = [], []
     if ok:
+        T = ys[0]
+        if T > 1 and y.stride(0) < H:
+            y = y.contiguous()
         for _, t in rows:
-            if t is None:
-                pitches.append(0)
-                continue
-            ok = ok and t.dtype is dt and t.device == dev and t.shape == ys and (H == 1 or t.stride(1) == 1)
-            pitches.append(max(t.stride(0), H) if ok else 0)
+            if t is not None:
+                ok = ok and t.dtype is dt and t.device == dev and t.shape == ys and (H == 1 or t.stride(1) == 1)
+                if ok and T > 1 and t.stride(0) < H:
+                    t = t.contiguous()
+            held.append(t)
+            pitches.append(0 if t is None or not ok else t.stride(0) if T > 1 else H)
         if w_post is not None:
             wp = w_post.data_ptr()
             ok = (ok and w_post.dtype is torch.float32 and w_post.shape == (H,) and w_post.device == dev
@@ -198,20 +204,22 @@ def _norm(name, y, w_post, gate, scale, w_pre, eps, rows):
             wn = w_pre.data_ptr()
             ok = ok and w_pre.dtype is torch.float32 and w_pre.shape == (H,) and w_pre.device == dev and w_pre.is_contiguous()
         if gate is not None:
-            gp = gate.data_ptr()
             if gate.dim() == 1:
                 kind = _lib.GATE_CHANNEL
                 ok = ok and gate.dtype is torch.float32 and gate.shape == (H,) and gate.device == dev and gate.is_contiguous()
             else:
                 kind = _lib.GATE_TOKEN
                 ok = ok and gate.dtype is dt and gate.device == dev and gate.shape == ys and (H == 1 or gate.stride(1) == 1)
-                gl = max(gate.stride(0), H) if ok else 0
+                if ok and T > 1 and gate.stride(0) < H:
+                    gate = gate.contiguous()
+                gl = gate.stride(0) if ok and T > 1 else H
+            gp = gate.data_ptr()
     if not ok:
         _explain_norm(name, y, w_post, gate, w_pre, rows)
-    residual = rows[0][1]
-    d = _NORM.pack(y.data_ptr(), max(y.stride(0), H), 0 if residual is None else residual.data_ptr(), pitches[0], gp, gl, wp,
-                   wn, ys[0], H, kind, _DTYPES[dt], scale, eps)
-    return d, kind, pitches
+    residual = held[0]
+    d = _NORM.pack(y.data_ptr(), y.stride(0) if T > 1 else H, 0 if residual is None else residual.data_ptr(), pitches[0], gp, gl,
+                   wp, wn, T, H, kind, _DTYPES[dt], scale, eps)
+    return d, kind, pitches, (*held, y, gate)
 
 
 def norm_residual_fwd(y: torch.Tensor, residual: Optional[torch.Tensor] = None, *, w_post: Optional[torch.Tensor] = None,
@@ -219,9 +227,10 @@ def norm_residual_fwd(y: torch.Tensor, residual: Optional[torch.Tensor] = None, 
                       eps: float = 1e-6):
     """nf4_norm_residual_fwd: z = residual + scale * gate * norm(y; w_post) and h = norm(z; w_pre), the
     norms being x / sqrt(mean(x^2) + eps) * w.  y, residual [T, H]; w_post, w_pre fp32 [H] (w_post None:
-    y itself; w_pre None: no h); gate fp32 [H], or [T, H] in y's dtype, or None.  Returns (z, h, stats);
+    y itself; w_pre None: no h); gate fp32 [H], or [T, H] in y's dtype, or None.  Rows may lie at any distance;
+    those that share storage (an expanded row) are copied first.  Returns (z, h, stats);
     z is y itself where nothing changes it, and stats (fp32 [2, T]) is what the backward needs."""
-    d, _, _ = _norm("norm_residual_fwd", y, w_post, gate, scale, w_pre, eps, (("residual", residual),))
+    d, _, _, _held = _norm("norm_residual_fwd", y, w_post, gate, scale, w_pre, eps, (("residual", residual),))
     same = residual is None and w_post is None and gate is None and scale == 1.0
     (T, H), dt, dev = y.shape, y.dtype, y.device
     z = y if same else torch.empty((T, H), dtype=dt, device=dev)
@@ -242,8 +251,8 @@ def norm_residual_bwd(gz: Optional[torch.Tensor], gh: Optional[torch.Tensor], y:
     ones (`need_vectors` covers the two gains and the gate).  gw_* and a channel gate's gradient are
     fp32 [H]; a token gate's has the gate's shape and dtype."""
     name = "norm_residual_bwd"
-    d, kind, (_, pitch_z, pitch_h) = _norm(name, y, w_post, gate, scale, w_pre, eps,
-                                           (("residual", residual), ("gz", gz), ("gh", gh)))
+    d, kind, (_, pitch_z, pitch_h), held = _norm(name, y, w_post, gate, scale, w_pre, eps,
+                                                 (("residual", residual), ("gz", gz), ("gh", gh)))
     (T, H), dt, dev = y.shape, y.dtype, y.device
     if stats.dtype is not torch.float32 or stats.shape != (2, T) or not stats.is_contiguous() or stats.device != dev:
         raise ValueError(f"{name}: stats must be the contiguous fp32 [2, T] of the forward")
@@ -261,7 +270,7 @@ def norm_residual_bwd(gz: Optional[torch.Tensor], gh: Optional[torch.Tensor], y:
     if gw_post is not None or gw_pre is not None or (ggate is not None and kind == _lib.GATE_CHANNEL):
         need = _workspace(_lib.OP_NORM_RESIDUAL_BWD, T, H, dev)
         ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    rc = _fn("nf4_norm_residual_bwd")(d, stats.data_ptr(), _ptr(gz), pitch_z, _ptr(gh), pitch_h, _ptr(gy), H, _ptr(gr), H,
+    rc = _fn("nf4_norm_residual_bwd")(d, stats.data_ptr(), _ptr(held[1]), pitch_z, _ptr(held[2]), pitch_h, _ptr(gy), H, _ptr(gr), H,
                                       _ptr(gw_post), _ptr(ggate), H, _ptr(gw_pre), _ptr(ws), need, _raw_stream(dev))
     if rc:
         _lib.check(rc, "nf4_norm_residual_bwd")
