@@ -124,6 +124,9 @@ struct AttnArgs {
   void* o_rest;  // [T][Hq][D] or null: o before its rounding, less o
   float* lse;    // [Hq][T]
   float* delta;  // [Hq][T], backward
+  // Backward in fp16: [Hq][T], [Hk][T], [Hk][T].  shift_q holds the rows' |go| until the
+  // exponents of the queries' scales replace them; |v|; the exponents of the keys' scales.
+  float *shift_q, *v_norm, *shift_k;
   const int32_t* cu_seqlens;  // [nseq + 1], or null: one sequence of T rows
   int64_t T, nseq;
   int Hq, Hk, D;

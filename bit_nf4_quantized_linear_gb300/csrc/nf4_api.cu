@@ -1151,6 +1151,9 @@ nf4_status nf4_attention_bwd(const nf4_attention* d, const void* o, int64_t o_to
   a.o_h = o_head;
   a.lse = const_cast<float*>(lse);
   a.delta = static_cast<float*>(ws);
+  a.shift_q = a.delta + a.T * a.Hq;
+  a.v_norm = a.shift_q + a.T * a.Hq;
+  a.shift_k = a.v_norm + a.T * a.Hk;
   a.go = go;
   a.go_t = go_token;
   a.go_h = go_head;
@@ -1413,7 +1416,8 @@ size_t nf4_workspace_size(int32_t op, int64_t M, int64_t N, int64_t K, int32_t E
   }
   if (op == NF4_OP_ATTENTION_BWD) {
     if (M <= 0 || N <= 0) return 0;
-    return static_cast<size_t>(M) * N * sizeof(float);  // delta [Hq][T]
+    // delta and shift_q [Hq][T], v_norm and shift_k [Hk][T] with Hk <= Hq
+    return static_cast<size_t>(M) * N * 4 * sizeof(float);
   }
   if (op == NF4_OP_QUANTIZE) {
     const int64_t nblocks = (N * K + 63) / 64;

@@ -16,6 +16,13 @@
 // atomics on dQ or partial sums through memory.  P and dS are rounded to the operands'
 // type for their products; sums are fp32.
 //
+// In fp16 each query's (for dK each key's) dS is held times a power of two, divided out of
+// the sum at the end, that brings a bound of the row's |dS| just below 2^15: what the range
+// of fp16 loses then lies 2^-29 below the largest that a row may hold, whatever the size of
+// dO and V.  The bound is (|do_i| |v_j| + |delta_i|) with the largest |v_j| that query i
+// sees, or the largest |do_i| and |delta_i| that see key j: two more passes over the rows'
+// norms (attn_shift_kernel), and nothing of a masked pair.
+//
 // The MMA warp keeps the tensor cores on one of a step's products while the two
 // compute groups (each half of a tile's columns, one thread a row) work on the other:
 // in the keys' CTAs dV and the next S' run during dS, dK and the next dP' during P; in
@@ -54,7 +61,7 @@ constexpr int kWarpMma = 8, kWarpLoad = 9, kWarpPrep = 10;  // the last one and 
 constexpr int kCompute = 8;  // warps of the two compute groups
 constexpr float kLog2e = 1.4426950408889634f;
 // fp16 keeps 11 bits down to 2^-14 only: the keys' CTAs hold P' times 2^14 (P' <= 1), and
-// divide dV by it at the end.
+// divide dV by it at the end.  dS has a scale of its own (attn_shift_kernel).
 constexpr float kShift = 14.0f, kUnshift = 1.0f / 16384.0f;
 
 template <int PANELS>
@@ -81,37 +88,122 @@ struct Shared {
 };
 
 // delta[h][t] = do . (o + what its rounding left over): 16 bytes a lane, rows of a head
-// side by side.  Bound by HBM.
+// side by side.  In fp16 also the rows' |do| and |v|, 0 where they are not finite (every
+// gradient that such a row reaches is not finite either).  Bound by HBM.
 template <typename T>
 __global__ void __launch_bounds__(256) attn_delta_kernel(const __grid_constant__ AttnArgs a) {
+  constexpr bool f16 = std::is_same<T, __half>::value;
   const int per = a.D / 8;                          // lanes with work in a row
   const int width = per <= 8 ? 8 : 16;              // lanes of a row
   const int lane = threadIdx.x & (width - 1);
-  const int64_t n = a.T * a.Hq, rows = static_cast<int64_t>(gridDim.x) * 256 / width;
+  const int64_t nq = a.T * a.Hq, n = f16 ? nq + a.T * a.Hk : nq, rows = static_cast<int64_t>(gridDim.x) * 256 / width;
   const int64_t first = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / width;
   for (int64_t i0 = 0; i0 < n; i0 += rows) {  // the same trips for all lanes of a warp
     const int64_t i = i0 + first;
-    float s = 0.0f;
+    const bool value = f16 && i >= nq;
+    const int64_t row = value ? i - nq : i;
+    const int heads = value ? a.Hk : a.Hq;
+    const int64_t t = row / heads;
+    const int h = static_cast<int>(row - t * heads);
+    float s = 0.0f, sq = 0.0f;
     if (i < n && lane < per) {
-      const int64_t t = i / a.Hq;
-      const int h = static_cast<int>(i - t * a.Hq);
-      const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.o) + t * a.o_t + h * a.o_h + lane * 8);
-      const uint4 y = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.go) + t * a.go_t + h * a.go_h + lane * 8);
-      uint4 z = make_uint4(0u, 0u, 0u, 0u);
-      if (a.o_rest) z = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.o_rest) + i * a.D + lane * 8);
+      const T* yp = value ? static_cast<const T*>(a.v) + t * a.v_t + h * a.v_h : static_cast<const T*>(a.go) + t * a.go_t + h * a.go_h;
+      const uint4 y = *reinterpret_cast<const uint4*>(yp + lane * 8);
+      uint4 x = make_uint4(0u, 0u, 0u, 0u), z = x;
+      if (!value) {
+        x = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.o) + t * a.o_t + h * a.o_h + lane * 8);
+        if (a.o_rest) z = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.o_rest) + i * a.D + lane * 8);
+      }
       const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w}, zs[4] = {z.x, z.y, z.z, z.w};
-      constexpr bool f16 = std::is_same<T, __half>::value;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         s = fmaf(lo16<f16>(xs[e]) + lo16<f16>(zs[e]), lo16<f16>(ys[e]), s);
         s = fmaf(hi16<f16>(xs[e]) + hi16<f16>(zs[e]), hi16<f16>(ys[e]), s);
+        if (f16) {
+          sq = fmaf(lo16<f16>(ys[e]), lo16<f16>(ys[e]), sq);
+          sq = fmaf(hi16<f16>(ys[e]), hi16<f16>(ys[e]), sq);
+        }
       }
     }
-    for (int o = width / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (i < n && lane == 0) {
-      const int64_t t = i / a.Hq;
-      a.delta[(i - t * a.Hq) * a.T + t] = s;
+    for (int o = width / 2; o > 0; o >>= 1) {
+      s += __shfl_xor_sync(0xffffffffu, s, o);
+      if (f16) sq += __shfl_xor_sync(0xffffffffu, sq, o);
     }
+    if (i < n && lane == 0) {
+      const int64_t at = h * a.T + t;
+      if (!value) a.delta[at] = s;
+      if (f16) (value ? a.v_norm : a.shift_q)[at] = sq < INFINITY ? sqrtf(sq) : 0.0f;
+    }
+  }
+}
+
+constexpr int kScanThreads = 1024;
+
+// Running maxima of N rows of values over the threads of a CTA, from thread 0 on, carried
+// from call to call.  Ends with a CTA barrier.
+template <int N>
+__device__ __forceinline__ void scan_max(float (&x)[N], float (&carry)[N], float (&totals)[2][32]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const float up = __shfl_up_sync(0xffffffffu, x[k], o);
+      if (lane >= o) x[k] = fmaxf(x[k], up);
+    }
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+    if (lane == 31) totals[k][warp] = x[k];
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const float all = totals[k][lane];
+    x[k] = fmaxf(x[k], fmaxf(carry[k], warp_max(lane < warp ? all : 0.0f)));
+    carry[k] = fmaxf(carry[k], warp_max(all));
+  }
+  __syncthreads();
+}
+
+// The exponent of the scale for score gradients of at most `bound`: below 2^15 with it.
+__device__ __forceinline__ float shift_of(float bound) {
+  const int e = static_cast<int>(__float_as_uint(bound) >> 23) - 127;
+  return bound > 0.0f ? static_cast<float>(max(-64, min(64, 14 - e))) : 0.0f;
+}
+
+__device__ __forceinline__ float pow2(float e) { return __int_as_float((127 + static_cast<int>(e)) << 23); }
+
+// The exponents of the scales that fp16 score gradients are held at (see the head of the
+// file): one CTA a sequence and key head.  First the keys, from the last row back, then the
+// queries.  A row sum that is not finite bounds nothing: its row's gradients are not finite.
+// Bound by the latency of its loads, a chunk of rows after the other (8192 rows in 9 sequences,
+// 32 heads over 8: 11 us, beside 450 for the products; one sequence of 12289: 54 of 3660).
+__global__ void __launch_bounds__(kScanThreads) attn_shift_kernel(const __grid_constant__ AttnArgs a) {
+  __shared__ float totals[2][32];
+  const int hk = blockIdx.y, group = a.Hq / a.Hk;
+  int64_t first, last;
+  seq_bounds(a, blockIdx.x, &first, &last);
+  auto finite = [](float x) { return fabsf(x) < INFINITY ? fabsf(x) : 0.0f; };
+  float seen[2] = {0.0f, 0.0f}, value[1] = {0.0f};
+  for (int64_t end = last; end > first; end -= kScanThreads) {
+    const int64_t t = end - 1 - threadIdx.x;
+    float m[2] = {0.0f, 0.0f};
+    if (t >= first)
+#pragma unroll 4
+      for (int h = hk * group; h < (hk + 1) * group; ++h) {
+        m[0] = fmaxf(m[0], a.shift_q[h * a.T + t]);
+        m[1] = fmaxf(m[1], finite(a.delta[h * a.T + t]));
+      }
+    scan_max(m, seen, totals);
+    if (t >= first) a.shift_k[hk * a.T + t] = shift_of(fmaf(m[0], a.v_norm[hk * a.T + t], m[1]));
+  }
+  for (int64_t at = first; at < last; at += kScanThreads) {
+    const int64_t t = at + threadIdx.x;
+    float v[1] = {t < last ? a.v_norm[hk * a.T + t] : 0.0f};
+    scan_max(v, value, totals);
+    if (t < last)
+#pragma unroll 4
+      for (int h = hk * group; h < (hk + 1) * group; ++h)
+        a.shift_q[h * a.T + t] = shift_of(fmaf(a.shift_q[h * a.T + t], v[0], finite(a.delta[h * a.T + t])));
   }
 }
 
@@ -225,7 +317,7 @@ __device__ __forceinline__ void keys_cta(const Ctx<F16, PANELS, FULL>& x, const 
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         l[e] = (F16 ? kShift : 0.0f) - lse2_of(a, at + r0 + e, r0 + e < rows);
-        d[e] = r0 + e < rows ? -a.delta[at + r0 + e] * (F16 ? kUnshift : 1.0f) : 0.0f;
+        d[e] = r0 + e < rows ? -a.delta[at + r0 + e] : 0.0f;
       }
       // the statistics of two steps ago have been read once that step's dK is done
       if (it >= 2 && !x.wait(sh.empty[(it - 2) % 3], ((it - 2) / 3) & 1)) break;
@@ -293,6 +385,9 @@ __device__ __forceinline__ void keys_cta(const Ctx<F16, PANELS, FULL>& x, const 
     const uint32_t ts = x.tmem + lanes + wg * 64, tp = ts + 128;
     const float c = a.scale * kLog2e;
     const float2 c2 = make_float2(c, c);
+    // fp16: the exponent of dS' (read again at the end: a register less); P' holds 2^14 already
+    auto shift = [&] { return jt * kAttnTile + kv < w.len ? a.shift_k[hk * a.T + w.row0 + jt * kAttnTile + kv] : 0.0f; };
+    const float more = F16 ? pow2(shift() - kShift) : 1.0f;
     bool ok = true;
     int i = jt;
     for (int it = 0; it < n; ++it) {
@@ -328,6 +423,14 @@ __device__ __forceinline__ void keys_cta(const Ctx<F16, PANELS, FULL>& x, const 
       }
       tmem_wait_st();
       arrive_warp(x.bar(sh.p_full));
+      if (F16) {
+#pragma unroll
+        for (int q = 0; q < 64; q += 2) {
+          const float2 u = mul2(make_float2(__uint_as_float(s[q]), __uint_as_float(s[q + 1])), make_float2(more, more));
+          s[q] = __float_as_uint(u.x);
+          s[q + 1] = __float_as_uint(u.y);
+        }
+      }
       if (!(ok = x.wait(sh.dp_full, it & 1))) break;
       tc_fence_after();
 #pragma unroll
@@ -340,9 +443,8 @@ __device__ __forceinline__ void keys_cta(const Ctx<F16, PANELS, FULL>& x, const 
           const float4 dl = *reinterpret_cast<const float4*>(&rs.delta[st][wg * 64 + q + e]);
           float2 u = make_float2(__uint_as_float(d[e]), __uint_as_float(d[e + 1]));
           float2 v = make_float2(__uint_as_float(d[e + 2]), __uint_as_float(d[e + 3]));
-          const float2 one = make_float2(kUnshift, kUnshift);
-          u = F16 ? fma2(u, one, make_float2(dl.x, dl.y)) : add2(u, make_float2(dl.x, dl.y));
-          v = F16 ? fma2(v, one, make_float2(dl.z, dl.w)) : add2(v, make_float2(dl.z, dl.w));
+          u = add2(u, make_float2(dl.x, dl.y));
+          v = add2(v, make_float2(dl.z, dl.w));
           u = mul2(u, make_float2(__uint_as_float(s[q + e]), __uint_as_float(s[q + e + 1])));
           v = mul2(v, make_float2(__uint_as_float(s[q + e + 2]), __uint_as_float(s[q + e + 3])));
           if (diag) {
@@ -368,7 +470,7 @@ __device__ __forceinline__ void keys_cta(const Ctx<F16, PANELS, FULL>& x, const 
       const int64_t r = w.row0 + jt * kAttnTile + kv;
       const uint32_t from = x.tmem + lanes + 256 + wg * 128;
       T* out = wg == 0 ? static_cast<T*>(a.gv) + r * a.gv_t + hk * a.gv_h : static_cast<T*>(a.gk) + r * a.gk_t + hk * a.gk_h;
-      const float f = wg == 0 ? (F16 ? kUnshift : 1.0f) : a.scale;
+      const float f = wg == 0 ? (F16 ? kUnshift : 1.0f) : a.scale * (F16 ? pow2(-shift()) : 1.0f);
       const bool dirty = wg == 0 && sh.dirty;
       for (int q = 0; q < a.D; q += 32) {
         uint32_t o[32];
@@ -482,7 +584,8 @@ __device__ __forceinline__ void queries_cta(const Ctx<F16, PANELS, FULL>& x, con
     const float c = a.scale * kLog2e;
     const bool live = i < w.len;
     const int64_t at = static_cast<int64_t>(h) * a.T + w.row0 + i;
-    const float l = lse2_of(a, at, live), dl = live ? a.delta[at] : 0.0f;
+    auto shift = [&] { return F16 && live ? a.shift_q[at] : 0.0f; };  // P comes times 2^shift
+    const float l = lse2_of(a, at, live) - shift(), dl = live ? a.delta[at] : 0.0f;
     const float2 c2 = make_float2(c, c), l2 = make_float2(-l, -l), d2 = make_float2(-dl, -dl);
     bool ok = true;
     for (int j = 0; j < n; ++j) {
@@ -525,7 +628,7 @@ __device__ __forceinline__ void queries_cta(const Ctx<F16, PANELS, FULL>& x, con
         uint32_t o[32];
         tmem_ld<32>(x.tmem + lanes + 384 + q, o);
         tmem_wait_ld<32>(o);
-        if (live) store32<F16>(out, o, a.scale, q, a.D);
+        if (live) store32<F16>(out, o, a.scale * pow2(-shift()), q, a.D);
         __syncwarp();
       }
     }
@@ -632,9 +735,13 @@ cudaError_t launch_one(const AttnMaps& m, const AttnArgs& a, int sms, cudaStream
     configured = true;
   }
   const int width = a.D <= 64 ? 8 : 16;
-  const int64_t want = (a.T * a.Hq * width + 255) / 256, most = 32 * static_cast<int64_t>(sms);
+  const int64_t want = (a.T * (a.Hq + (F16 ? a.Hk : 0)) * width + 255) / 256, most = 32 * static_cast<int64_t>(sms);
   attn_delta_kernel<T><<<static_cast<unsigned>(want < most ? want : most), 256, 0, s>>>(a);
   if (cudaError_t e = cudaGetLastError()) return e;
+  if (F16) {
+    attn_shift_kernel<<<dim3(static_cast<unsigned>(a.nseq), a.Hk, 1), kScanThreads, 0, s>>>(a);
+    if (cudaError_t e = cudaGetLastError()) return e;
+  }
   const int64_t tiles = attn_tiles(a, kAttnTile), key_ctas = tiles * a.Hk;
   kern<<<static_cast<unsigned>(key_ctas + tiles * a.Hq), kThreads, Geo<PANELS>::kSmem, s>>>(m.q, m.k, m.v, m.go, a, key_ctas);
   return cudaGetLastError();

@@ -413,8 +413,10 @@ nf4_status nf4_norm_residual_bwd(const nf4_norm_residual* d, const float* stats,
  * of a masked pair reaches no output, not even as 0 x NaN.  Deterministic.
  * fp16 and bf16 with D a multiple of 8 up to 128, 16-byte aligned pointers and
  * strides of a multiple of 8 elements run on the tensor cores (scores and softmax in
- * fp32, the probabilities rounded to the inputs' type for the second product); every
- * other layout, and fp32, runs fp32 arithmetic throughout. */
+ * fp32, the probabilities and score gradients rounded to the inputs' type for their
+ * second products, in fp16 times a power of two that keeps a row's score gradients
+ * inside the type's range whatever the size of go and v); every other layout, and fp32,
+ * runs fp32 arithmetic throughout. */
 typedef struct {
   const void* q;
   const void* k;

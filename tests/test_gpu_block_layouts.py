@@ -79,3 +79,113 @@ def test_norm_plain_norm_of_a_broadcast_row():
     z, h, _ = nf4.norm_residual_fwd(y, w_pre=w)
     one = nf4.norm_residual_fwd(row[None], w_pre=w)[1]
     assert z is y and torch.equal(h, one.expand(50, 256))
+
+
+# -------------------------------------------------------------------- attention --
+
+def qkv(T, Hq, Hk, D, dtype, seed=0):
+    n = gen(seed)
+    q, k = 1.3 * n(T, Hq, D), 1.3 * n(T, Hk, D)
+    return [x.to(dtype) for x in (q, k, n(T, Hk, D) + 0.3, n(T, Hq, D))]
+
+
+def offsets(lens):
+    b = ref.bounds_of(lens)
+    return b, torch.tensor(b, dtype=torch.int32, device=DEV)
+
+
+# Relative rms error of one rounding to fp16: 2^-11 / sqrt(3) of the binade's start, over mantissas spread evenly in
+# their logarithm a factor sqrt(3 / (8 ln 2)).
+ROUND16 = 2.0 ** -11 / math.sqrt(3) * math.sqrt(3 / (8 * math.log(2)))
+
+
+def relative(got, want):
+    return ((got.double() - want).norm() / want.norm()).item()
+
+
+def check_relative(grads, want):
+    """Relative error of each whole gradient: one rounding of the result (subnormal where it is), one of the weights or
+    score gradients of its product, one of the probabilities that o, and so the row sums, are made of.  They are
+    independent, so their squares add; a tenth on top."""
+    for got, name in zip(grads, ("gq", "gk", "gv")):
+        assert torch.isfinite(got).all(), name
+        one = relative(want[name].half(), want[name])
+        assert relative(got, want[name]) <= 1.1 * math.sqrt(one ** 2 + 2 * ROUND16 ** 2), (name, relative(got, want[name]) / one)
+
+
+@pytest.mark.parametrize("size", [1.0, 1e-2, 1e-3, 3e-4, 1e-4, 3e-5])
+@pytest.mark.parametrize("Hq,Hk,D,lens", [(4, 2, 128, [1500, 37]), (2, 2, 64, [2100]), (3, 1, 80, [700, 1, 900])])
+def test_attention_fp16_gradients_of_any_size(size, Hq, Hk, D, lens):
+    q, k, v, go = qkv(sum(lens), Hq, Hk, D, F16)
+    go = (size * go.float()).half()
+    b, cu = offsets(lens)
+    o, lse = nf4.attention_fwd(q, k, v, cu)
+    grads = nf4.attention_bwd(go, q, k, v, o, lse, cu)
+    check_relative(grads, ref.attention(q, k, v, b, D ** -0.5, go)[0])
+
+
+def test_attention_fp16_large_score_gradients():
+    """Score gradients beyond fp16's largest value whose sums, times small queries and keys, fit."""
+    q, k, v, go = qkv(300, 2, 1, 128, F16)
+    q, k, v, go = ((f * x.float()).half() for f, x in ((1e-3, q), (1e-3, k), (40, v), (4e3, go)))
+    o, lse = nf4.attention_fwd(q, k, v)
+    check_relative(nf4.attention_bwd(go, q, k, v, o, lse), ref.attention(q, k, v, [0, 300], 128 ** -0.5, go)[0])
+
+
+def test_attention_fp16_rows_of_different_size():
+    """Output gradients from 1e-5 to 10 in neighbouring rows: each row's gq is as good as on its own."""
+    T = 1200
+    q, k, v, go = qkv(T, 2, 2, 128, F16)
+    size = 10.0 ** (torch.arange(T, device=DEV) * 0.37 % 6 - 5)
+    go = (size[:, None, None] * go.float()).half()
+    o, lse = nf4.attention_fwd(q, k, v)
+    gq = nf4.attention_bwd(go, q, k, v, o, lse)[0].double()[1:]  # row 0 sees one key: its gradient is 0
+    want = ref.attention(q, k, v, [0, T], 128 ** -0.5, go)[0]["gq"][1:]
+
+    def mean_square(x):
+        return ((x - want).square().sum(-1) / want.square().sum(-1)).mean().item()
+
+    assert mean_square(gq) <= 1.21 * (mean_square(want.half().double()) + 2 * ROUND16 ** 2)
+
+
+@pytest.mark.parametrize("at", [3, 127, 128, 200])
+def test_attention_fp16_masked_values_leave_no_trace(at):
+    """The scale that fp16 score gradients are held at comes from what a row sees: a large value or output gradient
+    behind the mask, or in another sequence, changes no bit."""
+    lens = [300, 150]
+    b, cu = offsets(lens)
+    q, k, v, go = qkv(sum(lens), 4, 2, 64, F16)
+    go = (1e-4 * go.float()).half()
+
+    def both():
+        o, lse = nf4.attention_fwd(q, k, v, cu)
+        return nf4.attention_bwd(go, q, k, v, o, lse, cu)
+
+    base = both()
+    v[at] *= 4096
+    gq = both()[0]
+    assert torch.equal(gq[:at], base[0][:at]) and torch.equal(gq[300:], base[0][300:])
+    v[at] /= 4096
+    go[at] *= 4096
+    gq, gk, gv = both()
+    assert torch.equal(gk[at + 1:], base[1][at + 1:]) and torch.equal(gv[at + 1:], base[2][at + 1:])
+    rows = torch.arange(450, device=DEV) != at
+    assert torch.equal(gq[rows], base[0][rows])
+
+
+def test_attention_fp16_zero_and_nonfinite_gradients():
+    """go of zero gives zero gradients; a NaN in go reaches the keys that its row sees and no others."""
+    b, cu = offsets([300, 60])
+    q, k, v, go = qkv(360, 2, 2, 64, F16)
+    o, lse = nf4.attention_fwd(q, k, v, cu)
+    for g in nf4.attention_bwd(torch.zeros_like(go), q, k, v, o, lse, cu):
+        assert (g == 0).all()
+    base = nf4.attention_bwd(go, q, k, v, o, lse, cu)
+    for bad in (math.nan, math.inf):
+        x = go.clone()
+        x[140, 1, 9] = bad
+        gq, gk, gv = nf4.attention_bwd(x, q, k, v, o, lse, cu)
+        assert torch.equal(gk[141:], base[1][141:]) and torch.equal(gv[141:], base[2][141:])
+        assert not torch.isfinite(gk[:141, 1]).any() and not torch.isfinite(gv[:141, 1, 9]).any()
+        rows = torch.arange(360, device=DEV) != 140
+        assert torch.equal(gq[rows], base[0][rows]) and not torch.isfinite(gq[140, 1]).any()
