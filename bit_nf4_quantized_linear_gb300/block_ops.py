@@ -284,7 +284,8 @@ class AdamWState:
 
     Tensor i occupies `slices[i]` of `exp_avg` and `exp_avg_sq` (fp32 values, or uint8 codes), starting at
     a multiple of 256; with 8 bits, every 256 values share a scale in `exp_avg_absmax` and
-    `exp_avg_sq_absmax`.  `step` is the number of steps taken."""
+    `exp_avg_sq_absmax`.  `step` is the number of steps taken, and `missed` says in how many of them a tensor
+    had no gradient (index: count; tensors that missed none are not in it)."""
 
     def __init__(self, params: Sequence[torch.Tensor], bits: int = 8):
         name = "adamw_state"
@@ -294,7 +295,7 @@ class AdamWState:
         if not params:
             raise ValueError(f"{name}: no tensors")
         _one_device(name, *params)
-        self.bits, self.step, self.device = bits, 0, params[0].device
+        self.bits, self.step, self.missed, self.device = bits, 0, {}, params[0].device
         self.shapes = [p.size() for p in params]
         self._rows, self._held = struct.Struct("@" + "6Pq" * len(params)), None  # nf4_adamw_tensor
         self.numels = [p.numel() for p in params]
@@ -345,10 +346,13 @@ def adamw_state(params: Sequence[torch.Tensor], bits: int = 8) -> AdamWState:
 
 def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[Optional[torch.Tensor]], state: AdamWState, *, lr: float,
                betas: tuple = (0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01,
-               grad_scale: Optional[torch.Tensor] = None) -> None:
+               grad_scale: Optional[torch.Tensor] = None, per_tensor: bool = False) -> None:
     """nf4_adamw_step: one AdamW step over all tensors in place (params, state; state.step advances).
     Parameters and gradients are contiguous and of one dtype; a gradient of None leaves its tensor and
-    states alone.  `grad_scale`, a device fp32 scalar, multiplies the gradients (a clipping factor)."""
+    states alone.  The step is number state.step + 1 for every tensor; with `per_tensor` a tensor's number
+    counts its own gradients only (a launch for each number), so that moments which start late get the bias
+    correction of their start.  `grad_scale`, a device fp32 scalar, multiplies the gradients (a clipping
+    factor)."""
     name = "adamw_step"
     n = len(state.numels)
     if len(params) != n or len(grads) != n:
@@ -367,12 +371,23 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[Optional[torch.Te
     if not full:
         it = iter(ptrs)
         ptrs = [0 if g is None else next(it) for g in grads]
-    tab = state._table(map(T.data_ptr, params), ptrs)
-    rc = _fn("nf4_adamw_step")(tab, n, _DTYPES[dtype], state.bits, _ptr(state.levels[0]), _ptr(state.levels[1]), lr, betas[0],
-                               betas[1], eps, weight_decay, state.step + 1, _ptr(grad_scale), _raw_stream(dev))
-    if rc:
-        _lib.check(rc, "nf4_adamw_step")
+    steps = [(state.step + 1, ptrs)]
+    if per_tensor and state.missed:
+        number = [state.step + 1 - state.missed.get(i, 0) for i in range(n)]
+        steps = [(s, [p if s == m else 0 for p, m in zip(ptrs, number)])
+                 for s in sorted({m for m, g in zip(number, grads) if g is not None})]
+    addresses = list(map(T.data_ptr, params))
+    for step, ptrs in steps:
+        rc = _fn("nf4_adamw_step")(state._table(addresses, ptrs), n, _DTYPES[dtype], state.bits, _ptr(state.levels[0]),
+                                   _ptr(state.levels[1]), lr, betas[0], betas[1], eps, weight_decay, step, _ptr(grad_scale),
+                                   _raw_stream(dev))
+        if rc:
+            _lib.check(rc, "nf4_adamw_step")
     state.step += 1
+    if not full:
+        for i, g in enumerate(grads):
+            if g is None:
+                state.missed[i] = state.missed.get(i, 0) + 1
 
 
 def _explain_adamw(name, params, grads, state):

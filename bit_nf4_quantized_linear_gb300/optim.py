@@ -10,7 +10,8 @@ from . import block_ops
 
 class NF4AdamW(torch.optim.Optimizer):
     """AdamW whose step is one launch per parameter group and dtype (nf4_adamw_step), with the two moments
-    in 8 bits (256-value blocks of the dynamic map) or in fp32.
+    in 8 bits (256-value blocks of the dynamic map) or in fp32.  A parameter's steps count its own gradients;
+    where the counts of a group differ, each count is a launch.
 
     Options per group as in torch.optim.AdamW: lr, betas, eps, weight_decay; `state_bits` is 8 or 32.  A
     group's parameters are contiguous CUDA tensors on one device, of fp32, bf16 or fp16.  The state of a group
@@ -52,12 +53,12 @@ class NF4AdamW(torch.optim.Optimizer):
                 continue
             block_ops.adamw_step([p.detach() for p in ps], grads, self._state(key, group, ps), lr=group["lr"],
                                  betas=group["betas"], eps=group["eps"], weight_decay=group["weight_decay"],
-                                 grad_scale=grad_scale)
+                                 grad_scale=grad_scale, per_tensor=True)
         return loss
 
     def state_dict(self):
         d = super().state_dict()
-        d["group_state"] = {key: dict(bits=st.bits, step=st.step, buffers=list(st._buffers()))
+        d["group_state"] = {key: dict(bits=st.bits, step=st.step, missed=dict(st.missed), buffers=list(st._buffers()))
                             for key, st in self.group_state.items()}
         return d
 
@@ -73,7 +74,7 @@ class NF4AdamW(torch.optim.Optimizer):
             if rec["bits"] != st.bits or any((a is None) != (b is None) or (a is not None and a.shape != b.shape)
                                              for a, b in zip(rec["buffers"], st._buffers())):
                 raise ValueError("NF4AdamW: the saved state belongs to other parameters or another state_bits")
-            st.step = int(rec["step"])
+            st.step, st.missed = int(rec["step"]), dict(rec.get("missed", {}))
             for saved, own in zip(rec["buffers"], st._buffers()):
                 if own is not None:
                     own.copy_(saved)
