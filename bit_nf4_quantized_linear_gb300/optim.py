@@ -5,7 +5,7 @@ from typing import Optional
 
 import torch
 
-from . import block_ops
+from . import _lib, block_ops
 
 
 class NF4AdamW(torch.optim.Optimizer):
@@ -58,22 +58,30 @@ class NF4AdamW(torch.optim.Optimizer):
 
     def state_dict(self):
         d = super().state_dict()
-        d["group_state"] = {key: dict(bits=st.bits, step=st.step, missed=dict(st.missed), buffers=list(st._buffers()))
+        d["group_state"] = {key: dict(bits=st.bits, step=st.step, missed=dict(st.missed),
+                                      shapes=[tuple(s) for s in st.shapes], buffers=list(st._buffers()))
                             for key, st in self.group_state.items()}
         return d
 
     def load_state_dict(self, state_dict):
+        """Takes over a state_dict's options and moments.  Every saved state has to belong to a group and dtype of
+        this optimiser, with tensors of the saved shapes; a group that had not stepped when it was saved has none and
+        starts anew.  A refusal changes nothing."""
         state_dict = dict(state_dict)
         held = state_dict.pop("group_state")
+        sets = {key: ps for key, _, ps in self._sets()}
+        for key, rec in held.items():
+            shapes = [tuple(p.shape) for p in sets.get(key, ())]
+            size = sum(-(-p.numel() // _lib.ADAMW_BLOCK) * _lib.ADAMW_BLOCK for p in sets.get(key, ()))
+            scales = size // _lib.ADAMW_BLOCK if rec["bits"] == 8 else None
+            # records from before the shapes were kept: the buffers' lengths are all there is
+            if (key not in sets or list(map(tuple, rec.get("shapes", shapes))) != shapes
+                    or [None if b is None else b.numel() for b in rec["buffers"]] != [size, size, scales, scales]):
+                raise ValueError(f"NF4AdamW: the saved state of group {key[0]}, {key[1]} belongs to other parameters")
         super().load_state_dict(state_dict)
         self.group_state = {}
-        for key, group, ps in self._sets():
-            if key not in held:
-                continue
-            rec, st = held[key], self._state(key, group, ps)
-            if rec["bits"] != st.bits or any((a is None) != (b is None) or (a is not None and a.shape != b.shape)
-                                             for a, b in zip(rec["buffers"], st._buffers())):
-                raise ValueError("NF4AdamW: the saved state belongs to other parameters or another state_bits")
+        for key, rec in held.items():
+            st = self.group_state[key] = block_ops.adamw_state([p.detach() for p in sets[key]], bits=rec["bits"])
             st.step, st.missed = int(rec["step"]), dict(rec.get("missed", {}))
             for saved, own in zip(rec["buffers"], st._buffers()):
                 if own is not None:

@@ -1,5 +1,6 @@
 """NF4AdamW beside torch.optim.AdamW, and what a program does to an optimiser between steps: late gradients, saved
 and loaded states, copies, graphs."""
+import copy
 import io
 
 import pytest
@@ -102,3 +103,45 @@ def test_raw_step_counts():
         nf4.adamw_step(shared, [g[0], None], state, **hyper)
     nf4.adamw_step(shared, g, state, **hyper)
     assert state.step == 5 and torch.equal(shared[0], ps[0]) and not torch.equal(shared[1], ps[1])
+
+
+def stepped(ps, **kw):
+    opt = nf4.NF4AdamW(ps, **kw)
+    n = gen(4)
+    for p in opt.param_groups[0]["params"]:
+        p.grad = n(*p.shape).to(p.dtype)
+    opt.step()
+    return opt
+
+
+def test_a_saved_state_that_fits_no_parameters_is_refused():
+    """Of parameters of another dtype, or of other shapes in buffers of the same size; the refusal changes nothing."""
+    saved = stepped(params()).state_dict()
+    other = stepped(params(BF16))
+    before = copy.deepcopy(other.state_dict())
+    with pytest.raises(ValueError, match="state"):
+        other.load_state_dict(saved)
+    after = other.state_dict()
+    assert before["param_groups"] == after["param_groups"] and before["group_state"].keys() == after["group_state"].keys()
+    for key, rec in before["group_state"].items():
+        assert rec["step"] == after["group_state"][key]["step"]
+        for x, y in zip(rec["buffers"], after["group_state"][key]["buffers"]):
+            assert (x is None and y is None) or torch.equal(x, y)
+    swapped = params()
+    swapped = [swapped[i] for i in (3, 2, 1, 0)]  # 77, 5, 1000, 300: as many blocks in all
+    with pytest.raises(ValueError, match="state"):
+        nf4.NF4AdamW(swapped).load_state_dict(saved)
+
+
+def test_a_group_that_never_stepped_loads_without_a_state():
+    ps, qs = params(), params()
+    opt = nf4.NF4AdamW([dict(params=ps[:2]), dict(params=ps[2:])])
+    for p in ps[:2]:
+        p.grad = torch.ones_like(p)
+    opt.step()
+    second = nf4.NF4AdamW([dict(params=qs[:2]), dict(params=qs[2:])])
+    second.load_state_dict(opt.state_dict())
+    assert list(second.group_state) == list(opt.group_state)
+    for q in qs:
+        q.grad = torch.ones_like(q)
+    second.step()
