@@ -351,8 +351,9 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[Optional[torch.Te
     Parameters and gradients are contiguous and of one dtype; a gradient of None leaves its tensor and
     states alone.  The step is number state.step + 1 for every tensor; with `per_tensor` a tensor's number
     counts its own gradients only (a launch for each number), so that moments which start late get the bias
-    correction of their start.  `grad_scale`, a device fp32 scalar, multiplies the gradients (a clipping
-    factor)."""
+    correction of their start.  The number is fixed at the launch: a replayed CUDA graph repeats it, and
+    `state` does not count replays.  `grad_scale`, a device fp32 scalar, multiplies the gradients (a
+    clipping factor)."""
     name = "adamw_step"
     n = len(state.numels)
     if len(params) != n or len(grads) != n:

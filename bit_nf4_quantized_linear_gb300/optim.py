@@ -42,7 +42,10 @@ class NF4AdamW(torch.optim.Optimizer):
     @torch.no_grad()
     def step(self, closure=None, grad_scale: Optional[torch.Tensor] = None):
         """One step; `grad_scale`, a device fp32 scalar, multiplies every gradient (a clipping factor).  A
-        parameter without a gradient is left alone."""
+        parameter without a gradient is left alone.  Not to be captured in a CUDA graph: the number of the step,
+        and with it the bias correction, is fixed at the launch, and a replay would repeat it."""
+        if torch.cuda.is_available() and torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("NF4AdamW: a step cannot be captured in a CUDA graph (its number is fixed at the launch)")
         loss = None
         if closure is not None:
             with torch.enable_grad():

@@ -450,7 +450,8 @@ nf4_status nf4_attention_bwd(const nf4_attention* d, const void* o, int64_t o_to
  *   levels_m, levels_v  DEVICE fp32 [256], ascending: the signed and the unsigned
  *               dynamic map (bits 8; NULL otherwise).  New codes are the nearest level
  *               of x / max|x| of the block, ties to the lower index.
- *   step        the number of this step, from 1.
+ *   step        the number of this step, from 1; like lr it is fixed at the launch (a
+ *               replayed CUDA graph repeats it).
  *   grad_scale  DEVICE fp32 [1] or NULL (1): for instance a clipping factor.
  * A block of a tensor is 256 consecutive values from its start; the last may be
  * short.  nf4_adamw_state_values writes levels[code] * scale of both states (n

@@ -145,3 +145,19 @@ def test_a_group_that_never_stepped_loads_without_a_state():
     for q in qs:
         q.grad = torch.ones_like(q)
     second.step()
+
+
+def test_a_captured_step_is_refused():
+    """The step's number is fixed when it is launched: a replayed graph would repeat one bias correction."""
+    ps = params()
+    opt = nf4.NF4AdamW(ps)
+    for p in ps:
+        p.grad = torch.ones_like(p)
+    opt.step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(RuntimeError, match="captur"):
+            opt.step()
+    opt.step()
+    assert [st.step for st in opt.group_state.values()] == [2]
