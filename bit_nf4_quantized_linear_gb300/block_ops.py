@@ -123,6 +123,8 @@ def attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens:
     rc = _fn("nf4_attention_fwd")(d, o.data_ptr(), ot, oh, lse.data_ptr(), _raw_stream(q.device))
     if rc:
         _lib.check(rc, "nf4_attention_fwd")
+    if out is not None:
+        torch.autograd.graph.increment_version(out)
     lse.o_rest = rest
     return o, lse
 
@@ -384,6 +386,8 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[Optional[torch.Te
                                    _raw_stream(dev))
         if rc:
             _lib.check(rc, "nf4_adamw_step")
+    # autograd's record of writes that it did not see
+    torch.autograd.graph.increment_version(params if full else [p for p, g in zip(params, grads) if g is not None])
     state.step += 1
     if not full:
         for i, g in enumerate(grads):

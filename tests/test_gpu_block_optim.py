@@ -161,3 +161,26 @@ def test_a_captured_step_is_refused():
             opt.step()
     opt.step()
     assert [st.step for st in opt.group_state.values()] == [2]
+
+
+def test_a_step_moves_the_version_counters_of_what_it_writes():
+    """A backward through a graph kept from before the step is an error, as with torch's optimisers."""
+    ps = params()
+    opt = nf4.NF4AdamW(ps)
+    loss = sum(p.square().sum() for p in ps)
+    loss.backward(retain_graph=True)
+    ps[2].grad = None
+    seen = [p._version for p in ps]
+    opt.step()
+    assert [p._version > s for p, s in zip(ps, seen)] == [True, True, False, True]
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    x = torch.zeros(9, 2, 64, dtype=BF16, device=DEV)
+    out = torch.zeros_like(x)
+    before = out._version
+    nf4.attention_fwd(x, x, x, out=out)
+    assert out._version > before
+    with torch.inference_mode():
+        p, g = torch.ones(10, device=DEV), torch.ones(10, device=DEV)
+        nf4.adamw_step([p], [g], nf4.adamw_state([p]), lr=0.1)
+        assert (p < 1).all()
