@@ -152,6 +152,11 @@ def attention_bwd(go: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.T
     ws = torch.empty(need, dtype=torch.uint8, device=dev)
     ot, oh, _ = o.stride()
     gt, gh, _ = go.stride()
+    # A gradient that no bulk copy can load (broadcast over tokens or heads, off 16 bytes) is copied: two passes over
+    # it, where the kernels for any layout would take some hundred times the products' time.
+    if dt is not torch.float32 and D <= 128 and D % 8 == 0 and (gt < 1 or gh < 1 or (gt | gh) & 7 or go.data_ptr() & 15):
+        go = go.clone(memory_format=torch.contiguous_format)
+        gt, gh, _ = go.stride()
     rc = _fn("nf4_attention_bwd")(d, o.data_ptr(), ot, oh, lse.data_ptr(), go.data_ptr(), gt, gh, gq.data_ptr(), Hq * D, D,
                                   gk.data_ptr(), Hk * D, D, gv.data_ptr(), Hk * D, D, ws.data_ptr(), need, _raw_stream(dev))
     if rc:

@@ -189,3 +189,27 @@ def test_attention_fp16_zero_and_nonfinite_gradients():
         assert not torch.isfinite(gk[:141, 1]).any() and not torch.isfinite(gv[:141, 1, 9]).any()
         rows = torch.arange(360, device=DEV) != 140
         assert torch.equal(gq[rows], base[0][rows]) and not torch.isfinite(gq[140, 1]).any()
+
+
+@pytest.mark.parametrize("kind", ["tokens", "heads", "both", "misaligned", "odd pitch"])
+def test_attention_output_gradient_of_any_layout_stays_on_the_tensor_cores(kind):
+    """A gradient broadcast over tokens or heads (of a mean, for instance), or that no bulk copy can load, is copied:
+    the backward does not leave the tensor-core kernels for it."""
+    T, H, D = 200, 4, 64
+    q, k, v, go = qkv(T, H, 2, D, BF16)
+    if kind in ("misaligned", "odd pitch"):
+        pitch = H * D + (8 if kind == "misaligned" else 3)
+        store = torch.zeros(T * pitch + 1, dtype=BF16, device=DEV)
+        go = store[1 if kind == "misaligned" else 0:].as_strided((T, H, D), (pitch, D, 1)).copy_(go)
+    else:
+        go = go[:1 if kind != "heads" else T, :1 if kind != "tokens" else H].expand(T, H, D)
+    o, lse = nf4.attention_fwd(q, k, v)
+    want = nf4.attention_bwd(go.contiguous(), q, k, v, o, lse)
+    nf4.reset_path_counters()
+    got = nf4.attention_bwd(go, q, k, v, o, lse)
+    leaves = [t.clone().requires_grad_() for t in (q, k, v)]
+    nf4.nf4_attention(*leaves).backward(go)
+    counts = nf4.path_counters()
+    assert counts["attention_any"] == 0 and counts["attention"] == 3
+    for a, b, leaf in zip(got, want, leaves):
+        assert torch.equal(a, b) and torch.equal(leaf.grad, b)
