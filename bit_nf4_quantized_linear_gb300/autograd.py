@@ -185,10 +185,33 @@ def nf4_combine(rows: torch.Tensor, token_rows: torch.Tensor) -> torch.Tensor:
     return NF4MoECombineFn.apply(rows, token_rows)
 
 
+class _FirstOrderFn(torch.autograd.Function):
+    """Hands gradients on; going back through them is an error."""
+
+    @staticmethod
+    def forward(ctx, name, n, *tensors):
+        ctx.name = name
+        return tuple(t.view_as(t) for t in tensors[:n])
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError(f"{ctx.name}: the second derivative is not implemented")
+
+
+def _first_order(name: str, grads: tuple, inputs: tuple) -> tuple:
+    """`grads` as a backward pass returns them.  With create_graph they depend on `inputs` in a way that autograd did
+    not see, so they are tied to them by a node that refuses the second derivative."""
+    if not torch.is_grad_enabled():
+        return grads
+    given = [g for g in grads if g is not None]
+    made = iter(_FirstOrderFn.apply(name, len(given), *given, *(t for t in inputs if t is not None and t.requires_grad)))
+    return tuple(None if g is None else next(made) for g in grads)
+
+
 class NF4AttentionFn(torch.autograd.Function):
     """Causal attention over packed sequences (nf4_attention_fwd) and its gradients
     (nf4_attention_bwd).  Inputs, output and row statistics go through
-    save_for_backward; ctx holds the scale."""
+    save_for_backward; ctx holds the scale.  First derivatives only."""
 
     @staticmethod
     def forward(ctx, q, k, v, cu_seqlens, scale):
@@ -202,8 +225,8 @@ class NF4AttentionFn(torch.autograd.Function):
         q, k, v, o, lse, rest, cu_seqlens = ctx.saved_tensors
         if go.stride(2) != 1:
             go = go.contiguous()
-        gq, gk, gv = block_ops.attention_bwd(go, q, k, v, o, lse, cu_seqlens, ctx.scale, rest)
-        return gq, gk, gv, None, None
+        grads = block_ops.attention_bwd(go, q, k, v, o, lse, cu_seqlens, ctx.scale, rest)
+        return (*_first_order("nf4_attention", grads, (q, k, v)), None, None)
 
 
 def nf4_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor = None,
@@ -216,7 +239,7 @@ def nf4_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens:
 
 class NF4NormResidualFn(torch.autograd.Function):
     """The gated residual norm (nf4_norm_residual_fwd / _bwd).  The inputs and the rows' statistics are
-    saved; z is recomputed from them in the backward."""
+    saved; z is recomputed from them in the backward.  First derivatives only."""
 
     @staticmethod
     def forward(ctx, y, residual, w_post, gate, w_pre, scale, eps):
@@ -233,10 +256,11 @@ class NF4NormResidualFn(torch.autograd.Function):
             return (None,) * 7
         gz, gh = (g if g is None or g.stride(1) == 1 else g.contiguous() for g in (gz, gh))
         need = ctx.needs_input_grad
-        gy, gr, gw_post, ggate, gw_pre = block_ops.norm_residual_bwd(
+        grads = block_ops.norm_residual_bwd(
             gz, gh, y, residual, stats, w_post=w_post, gate=gate, scale=ctx.scale, w_pre=w_pre, eps=ctx.eps, need_y=need[0],
             need_residual=need[1], need_vectors=need[2] or need[3] or need[4])
-        return tuple(g if n else None for g, n in zip((gy, gr, gw_post, ggate, gw_pre), need)) + (None, None)
+        grads = tuple(g if n else None for g, n in zip(grads, need))
+        return _first_order("nf4_norm_residual", grads, (y, residual, w_post, gate, w_pre)) + (None, None)
 
 
 def nf4_norm_residual(y: torch.Tensor, residual: torch.Tensor = None, *, w_post: torch.Tensor = None,
