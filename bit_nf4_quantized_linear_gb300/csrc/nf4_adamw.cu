@@ -27,6 +27,7 @@
 
 #include "elem.cuh"
 #include "internal.h"
+#include "smem_limit.h"
 
 namespace nf4 {
 namespace {
@@ -574,11 +575,9 @@ bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % 
 template <typename T, int BITS>
 cudaError_t launch_one(const AdamTable& tab, const AdamArgs& a, int sms, cudaStream_t s) {
   constexpr int kSmem = smem_bytes<T, BITS>(), kWarps = threads(BITS) / 32;
-  static bool configured = false;
-  if (!configured && kSmem > 0) {
-    if (cudaError_t e = cudaFuncSetAttribute(adamw_kernel<T, BITS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem))
-      return e;
-    configured = true;
+  if constexpr (kSmem > 0) {
+    static SmemLimit limit;
+    if (cudaError_t e = limit.allow(adamw_kernel<T, BITS>, kSmem)) return e;
   }
   const int64_t want = (tab.blk0[tab.count] + kWarps - 1) / kWarps, most = (BITS == 8 ? 1 : 2) * static_cast<int64_t>(sms);
   adamw_kernel<T, BITS><<<static_cast<unsigned>(want < most ? want : most), threads(BITS), kSmem, s>>>(tab, a);

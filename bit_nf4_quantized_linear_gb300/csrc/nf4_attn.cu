@@ -42,6 +42,7 @@
 
 #include "attn_mma.cuh"
 #include "elem.cuh"
+#include "smem_limit.h"
 
 namespace nf4 {
 namespace {
@@ -395,13 +396,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <bool F16, int PANELS, bool FULL>
 cudaError_t launch_one(const AttnMaps& m, const AttnArgs& a, cudaStream_t s) {
-  static bool configured = false;
+  static SmemLimit limit;
   auto kern = attn_fwd_kernel<F16, PANELS, FULL>;
-  if (!configured) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<PANELS>::kSmem);
-    if (e != cudaSuccess) return e;
-    configured = true;
-  }
+  if (cudaError_t e = limit.allow(kern, Geo<PANELS>::kSmem)) return e;
   const int64_t grid = attn_tiles(a, 2 * kAttnTile) * a.Hq;
   kern<<<static_cast<unsigned>(grid), kThreads, Geo<PANELS>::kSmem, s>>>(m.q, m.k, m.v, a);
   return cudaGetLastError();

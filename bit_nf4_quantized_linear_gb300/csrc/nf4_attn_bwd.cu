@@ -52,6 +52,7 @@
 
 #include "attn_mma.cuh"
 #include "elem.cuh"
+#include "smem_limit.h"
 
 namespace nf4 {
 namespace {
@@ -726,14 +727,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <bool F16, int PANELS, bool FULL>
 cudaError_t launch_one(const AttnMaps& m, const AttnArgs& a, int sms, cudaStream_t s) {
-  static bool configured = false;
+  static SmemLimit limit;
   using T = typename std::conditional<F16, __half, __nv_bfloat16>::type;
   auto kern = attn_bwd_kernel<F16, PANELS, FULL>;
-  if (!configured) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<PANELS>::kSmem);
-    if (e != cudaSuccess) return e;
-    configured = true;
-  }
+  if (cudaError_t e = limit.allow(kern, Geo<PANELS>::kSmem)) return e;
   const int width = a.D <= 64 ? 8 : 16;
   const int64_t want = (a.T * (a.Hq + (F16 ? a.Hk : 0)) * width + 255) / 256, most = 32 * static_cast<int64_t>(sms);
   attn_delta_kernel<T><<<static_cast<unsigned>(want < most ? want : most), 256, 0, s>>>(a);

@@ -42,6 +42,7 @@
 #include "internal.h"
 #include "decode.cuh"
 #include "sm100_ptx.cuh"
+#include "smem_limit.h"
 
 // Code width and operand type of the kernel instances this translation unit
 // launches: 4-bit codes with bf16 operands here, 8-bit codes when nf4_gemm8.cu
@@ -1421,14 +1422,9 @@ template <int MODE, int BT, int BITS, bool F16>
 cudaError_t launch_one(const GemmArgs& a, const CUtensorMap& ta, const CUtensorMap& tp,
                        const CUtensorMap& to, int grid,
                        cudaStream_t s) {
-  static bool configured = false;
+  static SmemLimit limit;
   auto kern = nf4_gemm_kernel<MODE, BT, BITS, F16>;
-  if (!configured) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         Geo<BT, BITS>::kSmem);
-    if (e != cudaSuccess) return e;
-    configured = true;
-  }
+  if (cudaError_t e = limit.allow(kern, Geo<BT, BITS>::kSmem)) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
@@ -1456,14 +1452,9 @@ cudaError_t launch_one(const GemmArgs& a, const CUtensorMap& ta, const CUtensorM
 // A multi-product launch (classic schedule, no clusters).
 template <int MODE, int BT>
 cudaError_t launch_multi_one(const GemmArgs& a, const MapSet<kMaxProds>& maps, int grid, cudaStream_t s) {
-  static bool configured = false;
+  static SmemLimit limit;
   auto kern = nf4_gemm_kernel<MODE, BT, 4, false, true>;
-  if (!configured) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         Geo<BT, 4>::kSmem);
-    if (e != cudaSuccess) return e;
-    configured = true;
-  }
+  if (cudaError_t e = limit.allow(kern, Geo<BT, 4>::kSmem)) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);

@@ -18,6 +18,7 @@
 
 #include "decode.cuh"
 #include "internal.h"
+#include "smem_limit.h"
 
 namespace nf4 {
 namespace {
@@ -288,13 +289,8 @@ cudaError_t launch_fwd_mg(const GemvArgs& a, cudaStream_t s) {
 template <int MG>
 cudaError_t launch_dgrad_mg(const GemvArgs& a, int64_t rgroups, cudaStream_t s) {
   const int smem = 8 * MG * kChunk * 33 * static_cast<int>(sizeof(float));
-  static bool configured = false;
-  if (!configured) {
-    cudaError_t e = cudaFuncSetAttribute(gemv_dgrad_kernel<MG>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    configured = true;
-  }
+  static SmemLimit limit;
+  if (cudaError_t e = limit.allow(gemv_dgrad_kernel<MG>, smem)) return e;
   const int64_t kgroups = (a.K + kStepK - 1) / kStepK;
   gemv_dgrad_kernel<MG><<<static_cast<unsigned>(kgroups * rgroups), kGemvThreads, smem, s>>>(a);
   return cudaGetLastError();

@@ -27,13 +27,13 @@
 // partials in order.
 #include <cuda_runtime.h>
 
-#include <atomic>
 #include <cstdint>
 #include <type_traits>
 
 #include "elem.cuh"
 #include "internal.h"
 #include "sm100_ptx.cuh"
+#include "smem_limit.h"
 
 namespace nf4 {
 namespace {
@@ -827,14 +827,11 @@ int ring_smem(const NormArgs& a, size_t elem, bool backward, int* stages) {
   return static_cast<int>(gains + *stages * stage);
 }
 
-// KERN's own, so that the attribute is set once and not with every launch.
+// KERN's own, so that the limit is not set with every launch.
 template <auto KERN>
 cudaError_t ring_launch(unsigned grid, int n, int smem, const NormArgs& a, int stages, cudaStream_t s) {
-  static std::atomic<bool> configured{false};
-  if (!configured.load(std::memory_order_relaxed)) {
-    if (cudaError_t e = cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024)) return e;
-    configured.store(true, std::memory_order_relaxed);
-  }
+  static SmemLimit limit;
+  if (cudaError_t e = limit.allow(KERN, 220 * 1024)) return e;
   KERN<<<grid, n, smem, s>>>(a, stages);
   return cudaGetLastError();
 }

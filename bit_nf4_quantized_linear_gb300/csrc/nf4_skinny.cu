@@ -51,6 +51,7 @@
 
 #include "internal.h"
 #include "sm100_ptx.cuh"
+#include "smem_limit.h"
 
 namespace nf4 {
 namespace {
@@ -901,14 +902,8 @@ using SkinnyKernel = void (*)(CUtensorMap, SkinnyArgs);
 template <int MODE, int MT, bool F16>
 cudaError_t configure(SkinnyKernel& kern) {
   kern = MODE == 0 ? skinny_fwd_kernel<MT, F16> : skinny_dgrad_kernel<MT, F16>;
-  static bool configured = false;
-  if (!configured) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(kMaxSmem));
-    if (e != cudaSuccess) return e;
-    configured = true;
-  }
-  return cudaSuccess;
+  static SmemLimit limit;
+  return limit.allow(kern, static_cast<int>(kMaxSmem));
 }
 
 // Clusters of S CTAs (with `smem` bytes each) that can be resident at once.
