@@ -6,6 +6,7 @@ the computation runs in the library's kernels, and there is no CPU path.
 """
 from __future__ import annotations
 
+import contextlib
 import functools
 import itertools
 import struct
@@ -34,8 +35,16 @@ def _fn(name: str):
 
 
 def _raw_stream(device: torch.device) -> int:
-    """The current stream of `device` (which has to be the current device, as for every launch)."""
+    """The current stream of `device`."""
     return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+_current_device, _guard, _HERE = torch._C._cuda_getDevice, torch.cuda.device, contextlib.nullcontext()
+
+
+def _on(device: torch.device):
+    """A context in which `device` is the current one, as the library's launches and size queries need it."""
+    return _HERE if _current_device() == device.index else _guard(device)
 
 
 @functools.lru_cache(maxsize=4096)
@@ -120,7 +129,8 @@ def attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens:
     o = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device) if out is None else out
     lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
     ot, oh, _ = o.stride()
-    rc = _fn("nf4_attention_fwd")(d, o.data_ptr(), ot, oh, lse.data_ptr(), _raw_stream(q.device))
+    with _on(q.device):
+        rc = _fn("nf4_attention_fwd")(d, o.data_ptr(), ot, oh, lse.data_ptr(), _raw_stream(q.device))
     if rc:
         _lib.check(rc, "nf4_attention_fwd")
     if out is not None:
@@ -148,8 +158,6 @@ def attention_bwd(go: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.T
     gq = torch.empty((T, Hq, D), dtype=dt, device=dev)
     gk = torch.empty((T, Hk, D), dtype=dt, device=dev)
     gv = torch.empty((T, Hk, D), dtype=dt, device=dev)
-    need = _workspace(_lib.OP_ATTENTION_BWD, T, Hq, dev)
-    ws = torch.empty(need, dtype=torch.uint8, device=dev)
     ot, oh, _ = o.stride()
     gt, gh, _ = go.stride()
     # A gradient that no bulk copy can load (broadcast over tokens or heads, off 16 bytes) is copied: two passes over
@@ -157,8 +165,11 @@ def attention_bwd(go: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.T
     if dt is not torch.float32 and D <= 128 and D % 8 == 0 and (gt < 1 or gh < 1 or (gt | gh) & 7 or go.data_ptr() & 15):
         go = go.clone(memory_format=torch.contiguous_format)
         gt, gh, _ = go.stride()
-    rc = _fn("nf4_attention_bwd")(d, o.data_ptr(), ot, oh, lse.data_ptr(), go.data_ptr(), gt, gh, gq.data_ptr(), Hq * D, D,
-                                  gk.data_ptr(), Hk * D, D, gv.data_ptr(), Hk * D, D, ws.data_ptr(), need, _raw_stream(dev))
+    with _on(dev):
+        need = _workspace(_lib.OP_ATTENTION_BWD, T, Hq, dev)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        rc = _fn("nf4_attention_bwd")(d, o.data_ptr(), ot, oh, lse.data_ptr(), go.data_ptr(), gt, gh, gq.data_ptr(), Hq * D, D,
+                                      gk.data_ptr(), Hk * D, D, gv.data_ptr(), Hk * D, D, ws.data_ptr(), need, _raw_stream(dev))
     if rc:
         _lib.check(rc, "nf4_attention_bwd")
     return gq, gk, gv
@@ -243,7 +254,8 @@ def norm_residual_fwd(y: torch.Tensor, residual: Optional[torch.Tensor] = None, 
     z = y if same else torch.empty((T, H), dtype=dt, device=dev)
     h = None if w_pre is None else torch.empty((T, H), dtype=dt, device=dev)
     stats = torch.empty((2, T), dtype=torch.float32, device=dev)
-    rc = _fn("nf4_norm_residual_fwd")(d, None if same else z.data_ptr(), H, _ptr(h), H, stats.data_ptr(), _raw_stream(dev))
+    with _on(dev):
+        rc = _fn("nf4_norm_residual_fwd")(d, None if same else z.data_ptr(), H, _ptr(h), H, stats.data_ptr(), _raw_stream(dev))
     if rc:
         _lib.check(rc, "nf4_norm_residual_fwd")
     return z, h, stats
@@ -274,11 +286,13 @@ def norm_residual_bwd(gz: Optional[torch.Tensor], gh: Optional[torch.Tensor], y:
     if need_vectors and kind != _lib.GATE_NONE:
         ggate = torch.empty((T, H), dtype=dt, device=dev) if kind == _lib.GATE_TOKEN else torch.empty(H, dtype=f32, device=dev)
     ws, need = None, 0
-    if gw_post is not None or gw_pre is not None or (ggate is not None and kind == _lib.GATE_CHANNEL):
-        need = _workspace(_lib.OP_NORM_RESIDUAL_BWD, T, H, dev)
-        ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    rc = _fn("nf4_norm_residual_bwd")(d, stats.data_ptr(), _ptr(held[1]), pitch_z, _ptr(held[2]), pitch_h, _ptr(gy), H, _ptr(gr), H,
-                                      _ptr(gw_post), _ptr(ggate), H, _ptr(gw_pre), _ptr(ws), need, _raw_stream(dev))
+    with _on(dev):
+        if gw_post is not None or gw_pre is not None or (ggate is not None and kind == _lib.GATE_CHANNEL):
+            need = _workspace(_lib.OP_NORM_RESIDUAL_BWD, T, H, dev)
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        rc = _fn("nf4_norm_residual_bwd")(d, stats.data_ptr(), _ptr(held[1]), pitch_z, _ptr(held[2]), pitch_h, _ptr(gy), H,
+                                          _ptr(gr), H, _ptr(gw_post), _ptr(ggate), H, _ptr(gw_pre), _ptr(ws), need,
+                                          _raw_stream(dev))
     if rc:
         _lib.check(rc, "nf4_norm_residual_bwd")
     return gy, gr, gw_post, ggate, gw_pre
@@ -386,9 +400,10 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[Optional[torch.Te
                  for s in sorted({m for m, g in zip(number, grads) if g is not None})]
     addresses = list(map(T.data_ptr, params))
     for step, ptrs in steps:
-        rc = _fn("nf4_adamw_step")(state._table(addresses, ptrs), n, _DTYPES[dtype], state.bits, _ptr(state.levels[0]),
-                                   _ptr(state.levels[1]), lr, betas[0], betas[1], eps, weight_decay, step, _ptr(grad_scale),
-                                   _raw_stream(dev))
+        with _on(dev):
+            rc = _fn("nf4_adamw_step")(state._table(addresses, ptrs), n, _DTYPES[dtype], state.bits, _ptr(state.levels[0]),
+                                       _ptr(state.levels[1]), lr, betas[0], betas[1], eps, weight_decay, step, _ptr(grad_scale),
+                                       _raw_stream(dev))
         if rc:
             _lib.check(rc, "nf4_adamw_step")
     # autograd's record of writes that it did not see
@@ -417,8 +432,9 @@ def adamw_state_values(state: AdamWState):
     if state.bits == 32:
         return state.exp_avg, state.exp_avg_sq
     m, v = (torch.empty(state.exp_avg.numel(), dtype=torch.float32, device=state.device) for _ in range(2))
-    _lib.check(_fn("nf4_adamw_state_values")(
-        _ptr(state.exp_avg), _ptr(state.exp_avg_sq), _ptr(state.exp_avg_absmax), _ptr(state.exp_avg_sq_absmax),
-        _ptr(state.levels[0]), _ptr(state.levels[1]), m.numel(), m.data_ptr(), v.data_ptr(), _raw_stream(state.device)),
-        "nf4_adamw_state_values")
+    with _on(state.device):
+        rc = _fn("nf4_adamw_state_values")(
+            _ptr(state.exp_avg), _ptr(state.exp_avg_sq), _ptr(state.exp_avg_absmax), _ptr(state.exp_avg_sq_absmax),
+            _ptr(state.levels[0]), _ptr(state.levels[1]), m.numel(), m.data_ptr(), v.data_ptr(), _raw_stream(state.device))
+    _lib.check(rc, "nf4_adamw_state_values")
     return m, v

@@ -55,6 +55,7 @@ def calls(monkeypatch):
     monkeypatch.setattr(block_ops, "torch", OnCpu())
     monkeypatch.setattr(block_ops, "_raw_stream", lambda device: 0)
     monkeypatch.setattr(block_ops, "_workspace", lambda *a: 16)
+    monkeypatch.setattr(block_ops, "_current_device", lambda: 0, raising=False)
     return seen
 
 

@@ -1,8 +1,9 @@
-"""Second derivatives of the training-block operators."""
+"""Second derivatives of the training-block operators, and the device that their calls run on."""
 import pytest
 import torch
 
 import bit_nf4_quantized_linear_gb300 as nf4
+from bit_nf4_quantized_linear_gb300 import block_ops
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -42,3 +43,48 @@ def test_second_derivatives_are_refused(op):
             assert torch.equal(a, b) and b.requires_grad
         with pytest.raises(RuntimeError, match="second derivative"):
             torch.autograd.grad(sum(g.float().square().sum() for g in grads), leaves)
+
+
+def test_calls_run_on_the_device_of_their_tensors(monkeypatch):
+    """With another device current, every call makes its tensors' device current around its launches and queries."""
+    entered = []
+
+    class Guard:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            entered.append(self.device)
+
+        def __exit__(self, *a):
+            entered.pop()
+
+    seen = []
+    library, workspace = block_ops._fn, block_ops._workspace
+
+    def fn(name):
+        def call(*args):
+            seen.append((name, list(entered)))
+            return library(name)(*args)
+        return call
+
+    monkeypatch.setattr(block_ops, "_fn", fn)
+    monkeypatch.setattr(block_ops, "_workspace", lambda *a: (seen.append(("workspace", list(entered))), workspace(*a))[1])
+    monkeypatch.setattr(block_ops, "_guard", Guard)
+    n = gen(9)
+    q = n(20, 2, 64).to(BF16)
+    y, w = n(20, 64).to(BF16), torch.ones(64, device=DEV)
+    p, g = torch.ones(300, device=DEV), torch.ones(300, device=DEV)
+    for current in (0, 1):
+        monkeypatch.setattr(block_ops, "_current_device", lambda: current)
+        seen.clear()
+        o, lse = block_ops.attention_fwd(q, q, q)
+        block_ops.attention_bwd(q, q, q, q, o, lse)
+        _, _, stats = block_ops.norm_residual_fwd(y, w_pre=w)
+        block_ops.norm_residual_bwd(y, y, y, None, stats, w_pre=w)
+        state = block_ops.adamw_state([p])
+        block_ops.adamw_step([p], [g], state, lr=0.1)
+        block_ops.adamw_state_values(state)
+        assert len(seen) == 8
+        for name, devices in seen:
+            assert devices == ([torch.device(DEV)] if current else []), name
