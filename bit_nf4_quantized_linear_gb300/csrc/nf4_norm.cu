@@ -697,8 +697,9 @@ __global__ void __launch_bounds__(kMaxThreadsBwd) norm_bwd_ring_kernel(const __g
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
     const bool more = t + gridDim.x < a.T;
     const float rstd_y1 = more ? a.stats[t + gridDim.x] : 0.0f, rstd_z1 = more ? a.stats[a.T + t + gridDim.x] : 0.0f;
-    // dz = gz + rstd_z gh w_pre - z rstd_z^3 mean(z gh w_pre)
-    const float pull = rstd_z * rstd_z * rstd_z * dot * inv_h;
+    // dz = gz + rstd_z gh w_pre - z rstd_z^3 mean(z gh w_pre), without forming the power alone:
+    // with a small eps it leaves fp32 long before the product does
+    const float pull = rstd_z * dot * inv_h * rstd_z * rstd_z;
     F y;
     float2 b[kPairs], s = both(0.0f);
     {
@@ -744,10 +745,10 @@ __global__ void __launch_bounds__(kMaxThreadsBwd) norm_bwd_ring_kernel(const __g
       rr.issue(st, t + static_cast<int64_t>(stages) * gridDim.x);
     if (a.gy) {
       // without w_post, n is y itself: no norm to go back through
-      const float back = a.w_post ? rstd_y * rstd_y * sums.x * inv_h : 0.0f;
+      const float back = a.w_post ? rstd_y * (sums.x * inv_h) : 0.0f;
       F gy;
 #pragma unroll
-      for (int i = 0; i < kPairs; ++i) gy.set_pair(i, fma2(both(-back), y.pair(i), mul2(both(rstd_y), b[i])));
+      for (int i = 0; i < kPairs; ++i) gy.set_pair(i, mul2(both(rstd_y), fma2(both(-back), y.pair(i), b[i])));
       rr.put(gy, row_of<T>(a.gy, t, a.ld_gy));
     }
     dot = sums.y;

@@ -213,3 +213,23 @@ def test_attention_output_gradient_of_any_layout_stays_on_the_tensor_cores(kind)
     assert counts["attention_any"] == 0 and counts["attention"] == 3
     for a, b, leaf in zip(got, want, leaves):
         assert torch.equal(a, b) and torch.equal(leaf.grad, b)
+
+
+@pytest.mark.parametrize("gate", ["channel", "token", None])
+@pytest.mark.parametrize("T", [5, 400])
+@pytest.mark.parametrize("y,r,w,gz", [(1e-14, 1e-14, 1e-14, 1.0), (1e-18, 1.0, 1.0, 1e5)])
+def test_norm_rows_of_tiny_values(y, r, w, gz, gate, T):
+    """Tiny rows with eps = 0: the powers of a row's 1 / rms leave fp32, the gradients do not."""
+    n, H = gen(3), 512
+    c = dict(y=y * n(T, H), residual=r * n(T, H), gz=gz * n(T, H), gh=n(T, H), w_post=w * (1 + 0.2 * n(H)), w_pre=1 + 0.2 * n(H))
+    g = n(H) if gate == "channel" else n(T, H) if gate == "token" else None
+    kw = dict(w_post=c["w_post"], gate=g, scale=0.5, w_pre=c["w_pre"], eps=0.0)
+    z, h, stats = nf4.norm_residual_fwd(c["y"], c["residual"], **kw)
+    gy, gr, gw_post, ggate, gw_pre = nf4.norm_residual_bwd(c["gz"], c["gh"], c["y"], c["residual"], stats, **kw)
+    want, mag = ref.norm_residual(c["y"], c["residual"], c["w_post"], g, 0.5, c["w_pre"], 0.0, c["gz"], c["gh"])
+    for name, x in dict(z=z, h=h, gy=gy, gr=gr, gw_post=gw_post, ggate=ggate, gw_pre=gw_pre).items():
+        if x is None:
+            continue
+        bound = ref.norm_bound(want[name], mag[name], F32, T, H, x.dim() == 1)
+        assert torch.isfinite(x).all(), name
+        assert ((x.double() - want[name]).abs() <= bound).all(), name
