@@ -336,6 +336,12 @@ class AdamWState:
             self.exp_avg_absmax, self.exp_avg_sq_absmax = (
                 torch.zeros(at // _lib.ADAMW_BLOCK, dtype=torch.float32, device=self.device) for _ in range(2))
 
+    def __getstate__(self):  # a Struct cannot be pickled, and the addresses are those of this state's buffers
+        return {k: v for k, v in self.__dict__.items() if k not in ("_rows", "_held")}
+
+    def __setstate__(self, state):
+        self.__dict__.update(state, _rows=struct.Struct("@" + "6Pq" * len(state["numels"])), _held=None)
+
     def nbytes(self) -> int:
         return sum(t.numel() * t.element_size() for t in self._buffers() if t is not None)
 

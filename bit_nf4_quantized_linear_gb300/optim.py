@@ -59,6 +59,13 @@ class NF4AdamW(torch.optim.Optimizer):
                                  grad_scale=grad_scale, per_tensor=True)
         return loss
 
+    def __getstate__(self):
+        return dict(super().__getstate__(), group_state=self.group_state)
+
+    def __setstate__(self, state):
+        super().__setstate__(state)
+        self.__dict__.setdefault("group_state", {})  # a copy made without one
+
     def state_dict(self):
         d = super().state_dict()
         d["group_state"] = {key: dict(bits=st.bits, step=st.step, missed=dict(st.missed),

@@ -184,3 +184,30 @@ def test_a_step_moves_the_version_counters_of_what_it_writes():
         p, g = torch.ones(10, device=DEV), torch.ones(10, device=DEV)
         nf4.adamw_step([p], [g], nf4.adamw_state([p]), lr=0.1)
         assert (p < 1).all()
+
+
+@pytest.mark.parametrize("how", ["deepcopy", "pickle"])
+def test_copies_of_an_optimiser_step_like_it(how):
+    n = gen(6)
+    ps = params()
+    opt = nf4.NF4AdamW(ps, lr=1e-2)
+    grads = [[n(p.numel()) for p in ps] for _ in range(3)]
+
+    def step(o, t):
+        for p, g in zip(o.param_groups[0]["params"], grads[t]):
+            p.grad = g.clone()
+        o.step()
+
+    step(opt, 0)
+    step(opt, 1)
+    if how == "deepcopy":
+        twin = copy.deepcopy(opt)
+    else:
+        held = io.BytesIO()
+        torch.save(opt, held)
+        held.seek(0)
+        twin = torch.load(held, weights_only=False)
+    step(opt, 2)
+    step(twin, 2)
+    for p, q in zip(ps, twin.param_groups[0]["params"]):
+        assert p is not q and torch.equal(p, q)
