@@ -43,7 +43,10 @@
 // infinity or a NaN as a factor -- rows of another sequence in a ragged tile, and rows
 // of the diagonal tile -- the tile is cleaned in shared memory first.  A row whose lse
 // is not finite has P = NaN wherever it is seen, and non-finite values of dO taken out
-// of a diagonal tile are added to dV at the end.
+// of a diagonal tile are added to dV at the end.  The queries' diagonal tile of K is
+// cleaned for dQ only, after its scores (a key of -inf scores has P = 0, not what its
+// other columns give); a query that sees a non-finite value of it gets NaN there, as its
+// dS is 0 or NaN.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -84,7 +87,7 @@ struct Shared {
   uint32_t tmem;
   int abort_flag;
   int dirty;
-  uint64_t own_full, full[3], vfull[2], empty[3], vempty[2], ready[2], gready[2], diag, clean;
+  uint64_t own_full, full[3], vfull[2], empty[3], vempty[2], ready[2], gready[2], diag, scored, clean;
   uint64_t s_full[2], dp_full, dp_free, p_full, ds_full, out_full, drain;
 };
 
@@ -517,7 +520,7 @@ __device__ __forceinline__ void queries_cta(const Ctx<F16, PANELS, FULL>& x, con
     bool diag = false;
     for (int j = 0; j < n; ++j) {
       if (!x.wait(sh.empty[j % 3], ((j / 3) & 1) ^ 1)) break;
-      const uint64_t& b = j + 1 == n ? sh.diag : sh.full[j % 3];  // the last one is cleaned first
+      const uint64_t& b = j + 1 == n ? sh.diag : sh.full[j % 3];  // the last one is cleaned
       x.expect(b, x.bytes());
       x.load(mk, 2 + j % 3, b, hk, row0 + j * kAttnTile);
       if (j + 1 == n) diag = true; else nk = j + 1;
@@ -532,19 +535,23 @@ __device__ __forceinline__ void queries_cta(const Ctx<F16, PANELS, FULL>& x, con
     for (int j = nv < 2 ? 0 : nv - 2; j < nv; ++j) attn_drain(x.bar(sh.vfull[j & 1]), (j >> 1) & 1, x.guard);
     __syncwarp();
   } else if (warp >= kWarpPrep) {
-    if (x.wait(sh.diag, 0)) {
-      clean_tile<F16, PANELS>(x.smem + (2 + it % 3) * Geo<PANELS>::kTileBytes, min(kAttnTile, w.len - it * kAttnTile), true,
-                              warp - kWarpPrep, 2);
+    // the diagonal's K, between its scores and dQ
+    if (x.wait(sh.diag, 0) && x.wait(sh.scored, 0)) {
+      if (clean_tile<F16, PANELS>(x.smem + (2 + it % 3) * Geo<PANELS>::kTileBytes, min(kAttnTile, w.len - it * kAttnTile), true,
+                                  warp - kWarpPrep, 2) &&
+          lane == 0)
+        sh.dirty = 1;
       mbar_arrive(x.bar(sh.clean));
     }
   } else if (warp == kWarpMma) {
     const uint32_t id_s = F16 ? idesc_f16_f32(128, 128, false, false) : idesc_bf16_f32(128, 128, false, false);
     const uint32_t id_o = F16 ? idesc_f16_f32(128, x.ksteps * 16, false, true) : idesc_bf16_f32(128, x.ksteps * 16, false, true);
     const uint32_t S = x.tmem, P = x.tmem + 256, DQ = x.tmem + 384;
-    auto key = [&](int j) { return j + 1 == n ? x.wait(sh.clean, 0) : x.wait(sh.full[j % 3], (j / 3) & 1); };
+    auto key = [&](int j) { return j + 1 == n ? x.wait(sh.diag, 0) : x.wait(sh.full[j % 3], (j / 3) & 1); };
     auto scores = [&](int j) {
       x.over_columns(S + (j & 1) * 128, 0, 2 + j % 3, id_s);
       x.commit(sh.s_full[j & 1]);
+      if (j + 1 == n) x.commit(sh.scored);
     };
     auto grads = [&](int j) {
       x.over_columns(P, 1, 5 + (j & 1), id_s);
@@ -563,7 +570,7 @@ __device__ __forceinline__ void queries_cta(const Ctx<F16, PANELS, FULL>& x, con
         tc_fence_after();
         grads(j + 1);
       }
-      if (!(ok = x.wait(sh.ds_full, j & 1))) break;
+      if (!(ok = x.wait(sh.ds_full, j & 1) && (j + 1 < n || x.wait(sh.clean, 0)))) break;
       tc_fence_after();
       x.over_rows(DQ, S + (j & 1) * 128, 2 + j % 3, id_o, j > 0);
       x.commit(sh.empty[j % 3]);
@@ -629,6 +636,14 @@ __device__ __forceinline__ void queries_cta(const Ctx<F16, PANELS, FULL>& x, con
         uint32_t o[32];
         tmem_ld<32>(x.tmem + lanes + 384 + q, o);
         tmem_wait_ld<32>(o);
+        if (sh.dirty && live) {
+          const T* k = static_cast<const T*>(a.k) + hk * a.k_h + q;
+#pragma unroll 1
+          for (int t = it * kAttnTile; t <= i; ++t)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (q + e < a.D && !(fabsf(to_f32(k[(w.row0 + t) * a.k_t + e])) < INFINITY)) o[e] = 0x7fffffffu;
+        }
         if (live) store32<F16>(out, o, a.scale * pow2(-shift()), q, a.D);
         __syncwarp();
       }
@@ -683,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       sh.abort_flag = 0;
       sh.dirty = 0;
       uint64_t* one[] = {&sh.full[0], &sh.full[1], &sh.full[2], &sh.vfull[0], &sh.vfull[1], &sh.empty[0], &sh.empty[1],
-                         &sh.empty[2], &sh.vempty[0], &sh.vempty[1], &sh.diag, &sh.s_full[0], &sh.s_full[1], &sh.dp_full,
+                         &sh.empty[2], &sh.vempty[0], &sh.vempty[1], &sh.diag, &sh.scored, &sh.s_full[0], &sh.s_full[1], &sh.dp_full,
                          &sh.out_full, &sh.drain};
       for (uint64_t* b : one) mbar_init(smem_addr(b), 1);
       uint64_t* prep[] = {&sh.ready[0], &sh.ready[1], &sh.gready[0], &sh.gready[1], &sh.clean};

@@ -233,3 +233,24 @@ def test_norm_rows_of_tiny_values(y, r, w, gz, gate, T):
         bound = ref.norm_bound(want[name], mag[name], F32, T, H, x.dim() == 1)
         assert torch.isfinite(x).all(), name
         assert ((x.double() - want[name]).abs() <= bound).all(), name
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("at", [5, 127, 128, 200, 299])
+def test_attention_key_of_minus_infinity(at, dtype):
+    """A key whose scores are -inf takes no part: outputs and gradients are those without it, but for gq in the
+    channel where 0 meets the infinity."""
+    q, k, v, go = qkv(300, 4, 2, 128, dtype)
+    q[..., 3] = q[..., 3].abs() + 0.5
+    k[at, 1, 3] = -6e4  # as good as -inf: every weight underflows to 0 in 64 bits
+    smax = 128 ** -0.5 * (q.double().norm(dim=2).max() * k[torch.arange(300, device=DEV) != at].double().norm(dim=2).max()).item()
+    want, mag = ref.attention(q, k, v, [0, 300], 128 ** -0.5, go)
+    k[at, 1, 3] = -math.inf
+    o, lse = nf4.attention_fwd(q, k, v)
+    got = dict(zip(("gq", "gk", "gv"), nf4.attention_bwd(go, q, k, v, o, lse)), o=o)
+    assert torch.isnan(got["gq"][at:, 2:, 3]).all()
+    got["gq"][at:, 2:, 3] = want["gq"][at:, 2:, 3].to(dtype)
+    for name, x in got.items():
+        assert torch.isfinite(x).all(), name
+        bound = ref.attention_bound(name, want[name], mag[name], dtype, smax)
+        assert ((x.double() - want[name]).abs() <= bound).all(), name
