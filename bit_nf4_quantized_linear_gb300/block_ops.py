@@ -114,17 +114,35 @@ def _attention(name, q, k, v, cu_seqlens, scale, rest, like_q=()):
                            0 if rest is None else rest.data_ptr())
 
 
+def _share_storage(t: torch.Tensor) -> bool:
+    """Whether two rows of a [T, heads, D] tensor meet in memory."""
+    (T, H, D), (st, sh, _) = t.shape, t.stride()
+    reach = D
+    for stride, n in sorted((s, n) for s, n in ((st, T), (sh, H)) if n > 1):
+        if stride < reach and T > 0:
+            break
+        reach += stride * (n - 1)
+    else:
+        return False  # one dimension inside the other's steps
+    # interleaved: heads dh apart meet tokens dt apart where dh sh - dt st is less than a row
+    return (T > 1 and st < D) or any(abs(dh * sh - dt * st) < D for dh in range(1, H) for dt in
+                                     ({min(T - 1, dh * sh // st), min(T - 1, dh * sh // st + 1)} if st else {0}))
+
+
 def attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None,
                   scale: Optional[float] = None, out: Optional[torch.Tensor] = None, for_backward: bool = True):
     """nf4_attention_fwd: causal attention of packed sequences, q [T, Hq, D] over k, v [T, Hk, D]
     (any token and head strides).  `cu_seqlens` int32 [sequences + 1] holds the row offsets (None:
     one sequence); rows outside them give zeros.  Returns (o [T, Hq, D], lse fp32 [Hq, T]).  With
     `for_backward` and a 16-bit dtype, `lse.o_rest` is a tensor of o's shape with what o's rounding
-    left over, for attention_bwd; a caller that wants no gradients saves its memory with False."""
+    left over, for attention_bwd; a caller that wants no gradients saves its memory with False.  `out` takes o
+    in place of a new tensor: any token and head strides whose rows do not share storage."""
     rest = None
     if for_backward and q.dtype is not torch.float32 and q.dim() == 3 and q.is_cuda:
         rest = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     d = _attention("attention_fwd", q, k, v, cu_seqlens, scale, rest, () if out is None else (("out", out),))
+    if out is not None and _share_storage(out):
+        raise ValueError("attention_fwd: rows of out share storage")
     T, Hq, D = q.shape
     o = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device) if out is None else out
     lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)

@@ -90,3 +90,13 @@ def test_norm_pitches_stay_inside_the_tensors(calls, which, kind, T, H):
             assert pitch >= H and (T - 1) * pitch + H <= left, (name, pitch, left)
             assert T == 1 or pitch == own.stride(0), name
     assert len(calls) == 2
+
+
+def test_rows_that_share_storage_are_recognised():
+    """Against every element's address, over all small strides."""
+    for T, H, D in ((1, 1, 2), (3, 1, 2), (1, 3, 2), (3, 2, 2), (2, 3, 1), (4, 3, 3), (0, 2, 2)):
+        for st in range(0, 14):
+            for sh in range(0, 14):
+                t = torch.zeros(200).as_strided((T, H, D), (st, sh, 1))
+                at = [i * st + h * sh + d for i in range(T) for h in range(H) for d in range(D)]
+                assert block_ops._share_storage(t) == (len(set(at)) < len(at)), (T, H, D, st, sh)

@@ -254,3 +254,19 @@ def test_attention_key_of_minus_infinity(at, dtype):
         assert torch.isfinite(x).all(), name
         bound = ref.attention_bound(name, want[name], mag[name], dtype, smax)
         assert ((x.double() - want[name]).abs() <= bound).all(), name
+
+
+def test_attention_out_must_not_share_storage():
+    """Rows of `out` that share storage would be written by several blocks at once: refused; any other view is filled."""
+    q, k, v, _ = qkv(50, 4, 2, 64, BF16)
+    o, _ = nf4.attention_fwd(q, k, v)
+    row = torch.zeros(1, 4, 64, dtype=BF16, device=DEV)
+    for out in (row.expand(50, 4, 64), torch.zeros(50, 1, 64, dtype=BF16, device=DEV).expand(50, 4, 64),
+                torch.zeros(50 * 128 + 128, dtype=BF16, device=DEV).as_strided((50, 4, 64), (128, 64, 1))):
+        with pytest.raises(ValueError, match="out"):
+            nf4.attention_fwd(q, k, v, out=out)
+    wide = torch.zeros(50, 6, 72, dtype=BF16, device=DEV)
+    for out in (wide[:, 1:5, :64], torch.zeros(4, 50, 64, dtype=BF16, device=DEV).transpose(0, 1)):
+        assert nf4.attention_fwd(q, k, v, out=out)[0] is out and torch.equal(out, o)
+    one = torch.zeros(1, 1, 64, dtype=BF16, device=DEV).expand(1, 4, 64).contiguous()[:, :1].expand(1, 1, 64)
+    nf4.attention_fwd(q[:1, :1], k[:1, :1], v[:1, :1], out=one)
