@@ -177,6 +177,7 @@ def lib() -> ctypes.CDLL:
             "nf4_set_cluster_split": [I32],
             "nf4_set_token_tile": [I32],
             "nf4_inject_stream_k_timeout": [],
+            "nf4_inject_norm_timeout": [],
             "nf4_plan_query": [I32, I64, I64, I64, I32, I32, I32, ctypes.POINTER(nf4_plan_info)],
         }
         for name, args in sig.items():
@@ -194,6 +195,7 @@ def lib() -> ctypes.CDLL:
         L.nf4_set_cluster_split.restype = None
         L.nf4_set_token_tile.restype = None
         L.nf4_inject_stream_k_timeout.restype = None
+        L.nf4_inject_norm_timeout.restype = None
         L.nf4_inject_bounds_failure.restype = None
         _lib = L
         return _lib
@@ -274,6 +276,12 @@ def inject_stream_k_timeout():
     """Failure-path test hook: the next stream-K launch's bounded waits run out
     (NF4_ERR_TIMEOUT in the device status word); see nf4_inject_stream_k_timeout."""
     lib().nf4_inject_stream_k_timeout()
+
+
+def inject_norm_timeout():
+    """Failure-path test hook: the next streamed norm launch's bounded waits run out
+    (NF4_ERR_TIMEOUT in the device status word); see nf4_inject_norm_timeout."""
+    lib().nf4_inject_norm_timeout()
 
 
 def set_weight_prefetch(enabled: bool):

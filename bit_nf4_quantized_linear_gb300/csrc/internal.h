@@ -76,6 +76,7 @@ struct NormArgs {
   int gate_kind;
   float scale, eps;
   int* status;
+  int starve;  // failure-path test hook: row 0's copies never complete
 };
 // CTAs of the backward, each with its own partial sums.
 int norm_bwd_ctas(int64_t T, int64_t H, int sms);

@@ -226,8 +226,9 @@ std::atomic<int> g_weight_prefetch{0};
 std::atomic<int> g_small_m_path{NF4_SMALL_M_AUTO};
 
 // One-shot failure-path test hooks (nf4_inject_stream_k_timeout,
-// nf4_inject_bounds_failure).
+// nf4_inject_norm_timeout, nf4_inject_bounds_failure).
 std::atomic<int> g_inject_sk_timeout{0};
+std::atomic<int> g_inject_norm_timeout{0};
 std::atomic<int> g_inject_bounds{0};
 
 // Stream-K schedule of the fused kernel (nf4_set_stream_k).
@@ -1043,6 +1044,7 @@ nf4_status nf4_norm_residual_fwd(const nf4_norm_residual* d, void* z, int64_t ld
   DevInfo dev;
   if (!current_device(&dev)) return cuda_fail(cudaGetLastError(), "device query");
   a.status = dev.status;
+  a.starve = g_inject_norm_timeout.exchange(0, std::memory_order_relaxed);
   cudaError_t le = nf4::launch_norm(false, d->dtype, a, dev.sms, static_cast<cudaStream_t>(stream));
   if (le != cudaSuccess) return cuda_fail(le, "kernel launch");
   count(NF4_PATH_NORM_RESIDUAL);
@@ -1097,6 +1099,7 @@ nf4_status nf4_norm_residual_bwd(const nf4_norm_residual* d, const float* stats,
   a.gw_post = gw_post;
   a.gw_pre = gw_pre;
   a.status = dev.status;
+  a.starve = g_inject_norm_timeout.exchange(0, std::memory_order_relaxed);
   cudaError_t le = nf4::launch_norm(true, d->dtype, a, dev.sms, st);
   if (le != cudaSuccess) return cuda_fail(le, "kernel launch");
   count(NF4_PATH_NORM_RESIDUAL);
@@ -1527,6 +1530,8 @@ void nf4_set_token_tile(int32_t tokens) {
 }
 
 void nf4_inject_stream_k_timeout(void) { g_inject_sk_timeout.store(1, std::memory_order_relaxed); }
+
+void nf4_inject_norm_timeout(void) { g_inject_norm_timeout.store(1, std::memory_order_relaxed); }
 
 void nf4_inject_bounds_failure(void) { g_inject_bounds.store(1, std::memory_order_relaxed); }
 

@@ -433,26 +433,32 @@ __global__ void __launch_bounds__(kMaxThreadsBwd) norm_bwd_kernel(const __grid_c
 // never wait for a row's two sums; the gains stay in shared memory for all rows.
 
 constexpr int kMaxStages = 4;
-constexpr uint64_t kTimeoutNs = 2000000000;
-
 struct Ring {
   uint64_t full[kMaxStages];
-  int gave_up;
+  volatile int gave_up;
 };
 
-// Bounded: after a timeout (recorded) every later wait returns at once, and the kernel
-// runs out on whatever the buffers hold.
-static __device__ __noinline__ void ring_wait_slow(Ring& r, uint32_t bar, uint32_t parity, int* status) {
-  volatile int* gave_up = &r.gave_up;
+// Bounded: after a timeout (recorded) every later wait returns at once, no further copy is
+// issued, and the kernel runs out on whatever the buffers hold.
+static __device__ __noinline__ void ring_wait_slow(Ring& r, uint32_t bar, uint32_t parity, uint64_t limit_ns, int* status) {
   const uint64_t t0 = nf4ptx::globaltimer_ns();
   while (!nf4ptx::mbar_try_wait_sleep(bar, parity, 20000)) {
-    if (*gave_up) return;
-    if (nf4ptx::globaltimer_ns() - t0 > kTimeoutNs) {
-      *gave_up = 1;
+    if (r.gave_up) return;
+    if (nf4ptx::globaltimer_ns() - t0 > limit_ns) {
+      r.gave_up = 1;
       if (status) atomicCAS(status, 0, kStatusTimeout);
       return;
     }
   }
+}
+
+// Thread 0, once a wait ran out: the copies in flight land, or are given up too, before the
+// CTA's shared memory can be another's.  Bit i of `last`: parity of stage i's last copy.
+static __device__ __noinline__ void ring_drain(Ring& r, int used, uint32_t last, uint64_t limit_ns) {
+  const uint64_t t0 = nf4ptx::globaltimer_ns();
+  for (int i = 0; i < used; ++i)
+    while (!nf4ptx::mbar_try_wait_sleep(nf4ptx::smem_addr(&r.full[i]), (last >> i) & 1u, 20000))
+      if (nf4ptx::globaltimer_ns() - t0 > limit_ns) break;
 }
 
 constexpr int kPairs = kHold / 2;
@@ -496,7 +502,8 @@ struct RowRing {
   // Thread 0: the copies of row t into a stage.
   __device__ __forceinline__ void issue(int st, int64_t t) const {
     const uint32_t bar = nf4ptx::smem_addr(&ring.full[st]);
-    nf4ptx::mbar_arrive_expect_tx(bar, stage_bytes);
+    // the injected failure: 16 bytes that no copy brings
+    nf4ptx::mbar_arrive_expect_tx(bar, stage_bytes + (a.starve && t == 0 ? 16 : 0));
     uint32_t to = nf4ptx::smem_addr(stage0) + st * stage_bytes;
     auto copy = [&](const void* p, int64_t ld) {
       nf4ptx::bulk_load_g2s(to, row_of<T>(p, t, ld), row_bytes, bar);
@@ -510,7 +517,18 @@ struct RowRing {
   }
   __device__ __forceinline__ void wait(int st, uint32_t parity, int* status) const {
     const uint32_t bar = nf4ptx::smem_addr(&ring.full[st]);
-    if (!nf4ptx::mbar_test_wait(bar, parity)) ring_wait_slow(ring, bar, parity, status);
+    if (!nf4ptx::mbar_test_wait(bar, parity)) ring_wait_slow(ring, bar, parity, limit_ns(), status);
+  }
+  __device__ __forceinline__ uint64_t limit_ns() const { return a.starve ? 100000000 : 2000000000; }
+  __device__ __forceinline__ int used() const {  // stages that ever held a row
+    return static_cast<int>(min(static_cast<int64_t>(stages), (a.T - 1 - blockIdx.x) / gridDim.x + 1));
+  }
+  // Thread 0: row t, where there is one, into the stage whose last copy had parity `ph`.  A
+  // barrier whose wait ran out is not armed again.
+  __device__ __forceinline__ void refill(int st, uint32_t ph, int64_t t, uint32_t& last) const {
+    if (t >= a.T || ring.gave_up) return;
+    issue(st, t);
+    last = (last & ~(1u << st)) | ((ph ^ 1u) << st);
   }
   __device__ __forceinline__ void take(F& f, bool have, const uint8_t* row) const {
     f.clear();
@@ -580,7 +598,7 @@ __global__ void __launch_bounds__(kMaxThreadsFwd) norm_fwd_ring_kernel(const __g
   const bool token = a.gate_kind == NF4_GATE_TOKEN;
   const float inv_h = 1.0f / static_cast<float>(a.H);
   int st = 0, buf = 0;
-  uint32_t ph = 0;
+  uint32_t ph = 0, last = 0;
   auto squares = [&](int stage) {  // of this thread's part of y
     float2 s = both(0.0f);
     if (a.w_post) {
@@ -623,8 +641,7 @@ __global__ void __launch_bounds__(kMaxThreadsFwd) norm_fwd_ring_kernel(const __g
     ss_y = sums.y;
     const float rstd_z = rsqrtf(sums.x * inv_h + a.eps);
     // every thread has read its part of row t
-    if (threadIdx.x == 0 && t + static_cast<int64_t>(stages) * gridDim.x < a.T)
-      rr.issue(st, t + static_cast<int64_t>(stages) * gridDim.x);
+    if (threadIdx.x == 0) rr.refill(st, ph, t + static_cast<int64_t>(stages) * gridDim.x, last);
     if (a.h) {
       rr.gain(g, 2);
 #pragma unroll
@@ -638,6 +655,7 @@ __global__ void __launch_bounds__(kMaxThreadsFwd) norm_fwd_ring_kernel(const __g
     st = st1;
     ph = ph1;
   }
+  if (threadIdx.x == 0 && ring.gave_up) ring_drain(ring, rr.used(), last, rr.limit_ns());
 }
 
 // As in the forward, row t's second sum and row t + 1's first share a barrier.  What a row
@@ -690,7 +708,7 @@ __global__ void __launch_bounds__(kMaxThreadsBwd) norm_bwd_ring_kernel(const __g
 #pragma unroll
   for (int i = 0; i < kPairs; ++i) sum_pre[i] = sum_post[i] = sum_gate[i] = both(0.0f);
   int st = 0, buf = 0;
-  uint32_t ph = 0;
+  uint32_t ph = 0, last = 0;
   float rstd_y = a.stats[blockIdx.x], rstd_z = a.stats[a.T + blockIdx.x];
   rr.wait(0, 0, a.status);
   float dot = block_sum2(make_float2(first_sum(0, rstd_y), 0.0f), red[1]).x;
@@ -741,8 +759,7 @@ __global__ void __launch_bounds__(kMaxThreadsBwd) norm_bwd_ring_kernel(const __g
     const float2 sums = block_sum2(make_float2(s.x + s.y, s1), red[buf]);
     buf ^= 1;
     // every thread has read its part of row t
-    if (threadIdx.x == 0 && t + static_cast<int64_t>(stages) * gridDim.x < a.T)
-      rr.issue(st, t + static_cast<int64_t>(stages) * gridDim.x);
+    if (threadIdx.x == 0) rr.refill(st, ph, t + static_cast<int64_t>(stages) * gridDim.x, last);
     if (a.gy) {
       // without w_post, n is y itself: no norm to go back through
       const float back = a.w_post ? rstd_y * (sums.x * inv_h) : 0.0f;
@@ -757,6 +774,7 @@ __global__ void __launch_bounds__(kMaxThreadsBwd) norm_bwd_ring_kernel(const __g
     st = st1;
     ph = ph1;
   }
+  if (threadIdx.x == 0 && ring.gave_up) ring_drain(ring, rr.used(), last, rr.limit_ns());
   Sums sum;
 #pragma unroll
   for (int i = 0; i < kPairs; ++i) {

@@ -630,6 +630,14 @@ nf4_status nf4_plan_query(int32_t op, int64_t M, int64_t N, int64_t K, int32_t s
  * unaffected.  The affected call's output is unspecified. */
 void nf4_inject_stream_k_timeout(void);
 
+/* Failure-path test hook (host-side injection; no fault of any kind): arms a
+ * one-shot for this process's next gated-residual-norm launch.  Where that streams
+ * its rows through shared memory, row 0 waits for 16 bytes that no copy brings: the
+ * bounded wait runs out (0.1 s), NF4_ERR_TIMEOUT is recorded in the device status
+ * word, and the kernel lets its copies land and exits normally; later launches are
+ * unaffected.  The affected call's output is unspecified. */
+void nf4_inject_norm_timeout(void);
+
 /* Failure-path test hook of the checked build (nf4_checked_build): one-shot for
  * the next product launched on the fused tcgen05 kernel (nf4_linear_* at an M
  * that takes it) by this process, whose statistics-load index checks then fail.
