@@ -418,6 +418,12 @@ __device__ __forceinline__ void keys_cta(const Ctx<F16, PANELS, FULL>& x, const 
         for (int q = 0; q < 64; ++q)
           if (wg * 64 + q < kv) s[q] = 0u;  // queries before this key
       }
+      if (const int rows = w.len - i * kAttnTile - wg * 64; rows < 64) {
+        // queries past the sequence: a key of infinite values and their cleared rows make NaN, not a weight of 0
+#pragma unroll
+        for (int q = 0; q < 64; ++q)
+          if (q >= rows) s[q] = 0u;
+      }
 #pragma unroll
       for (int q = 0; q < 64; q += 32) {
         uint32_t p[16];
