@@ -436,6 +436,7 @@ constexpr int kMaxStages = 4;
 struct Ring {
   uint64_t full[kMaxStages];
   volatile int gave_up;
+  int64_t unissued;  // the first row that was not copied after that, or T
 };
 
 // Bounded: after a timeout (recorded) every later wait returns at once, no further copy is
@@ -453,11 +454,12 @@ static __device__ __noinline__ void ring_wait_slow(Ring& r, uint32_t bar, uint32
 }
 
 // Thread 0, once a wait ran out: the copies in flight land, or are given up too, before the
-// CTA's shared memory can be another's.  Bit i of `last`: parity of stage i's last copy.
-static __device__ __noinline__ void ring_drain(Ring& r, int used, uint32_t last, uint64_t limit_ns) {
+// CTA's shared memory can be another's.
+static __device__ __noinline__ void ring_drain(Ring& r, int stages, uint64_t limit_ns) {
+  const int64_t rows = (r.unissued - blockIdx.x + gridDim.x - 1) / gridDim.x;  // copied ones, in turn to the stages
   const uint64_t t0 = nf4ptx::globaltimer_ns();
-  for (int i = 0; i < used; ++i)
-    while (!nf4ptx::mbar_try_wait_sleep(nf4ptx::smem_addr(&r.full[i]), (last >> i) & 1u, 20000))
+  for (int64_t k = rows < stages ? 0 : rows - stages; k < rows; ++k)
+    while (!nf4ptx::mbar_try_wait_sleep(nf4ptx::smem_addr(&r.full[k % stages]), (k / stages) & 1, 20000))
       if (nf4ptx::globaltimer_ns() - t0 > limit_ns) break;
 }
 
@@ -499,11 +501,10 @@ struct RowRing {
     stage_bytes = row_bytes * (1 + (a.residual != nullptr) + (a.gate_kind == NF4_GATE_TOKEN) + (BWD && a.gz) + (BWD && a.gh));
     stage0 = smem + 3 * a.H * sizeof(float);
   }
-  // Thread 0: the copies of row t into a stage.
-  __device__ __forceinline__ void issue(int st, int64_t t) const {
+  // Thread 0: the copies of row t into a stage, which waits for `missing` bytes more than they are.
+  __device__ __forceinline__ void issue(int st, int64_t t, uint32_t missing) const {
     const uint32_t bar = nf4ptx::smem_addr(&ring.full[st]);
-    // the injected failure: 16 bytes that no copy brings
-    nf4ptx::mbar_arrive_expect_tx(bar, stage_bytes + (a.starve && t == 0 ? 16 : 0));
+    nf4ptx::mbar_arrive_expect_tx(bar, stage_bytes + missing);
     uint32_t to = nf4ptx::smem_addr(stage0) + st * stage_bytes;
     auto copy = [&](const void* p, int64_t ld) {
       nf4ptx::bulk_load_g2s(to, row_of<T>(p, t, ld), row_bytes, bar);
@@ -520,15 +521,14 @@ struct RowRing {
     if (!nf4ptx::mbar_test_wait(bar, parity)) ring_wait_slow(ring, bar, parity, limit_ns(), status);
   }
   __device__ __forceinline__ uint64_t limit_ns() const { return a.starve ? 100000000 : 2000000000; }
-  __device__ __forceinline__ int used() const {  // stages that ever held a row
-    return static_cast<int>(min(static_cast<int64_t>(stages), (a.T - 1 - blockIdx.x) / gridDim.x + 1));
-  }
-  // Thread 0: row t, where there is one, into the stage whose last copy had parity `ph`.  A
-  // barrier whose wait ran out is not armed again.
-  __device__ __forceinline__ void refill(int st, uint32_t ph, int64_t t, uint32_t& last) const {
-    if (t >= a.T || ring.gave_up) return;
-    issue(st, t);
-    last = (last & ~(1u << st)) | ((ph ^ 1u) << st);
+  // Thread 0: row t, where there is one, into a stage that has been read.  A barrier whose
+  // wait ran out is not armed again.
+  __device__ __forceinline__ void refill(int st, int64_t t) const {
+    if (t >= a.T) return;
+    if (!ring.gave_up)
+      issue(st, t, 0);
+    else if (t < ring.unissued)
+      ring.unissued = t;
   }
   __device__ __forceinline__ void take(F& f, bool have, const uint8_t* row) const {
     f.clear();
@@ -561,11 +561,12 @@ struct RowRing {
   __device__ __forceinline__ void start(int n) const {
     if (threadIdx.x == 0) {
       ring.gave_up = 0;
+      ring.unissued = a.T;
       for (int i = 0; i < stages; ++i) nf4ptx::mbar_init(nf4ptx::smem_addr(&ring.full[i]), 1);
       nf4ptx::fence_mbar_init();
       for (int i = 0; i < stages; ++i) {
         const int64_t t = blockIdx.x + static_cast<int64_t>(i) * gridDim.x;
-        if (t < a.T) issue(i, t);
+        if (t < a.T) issue(i, t, a.starve && t == 0 ? 16 : 0);
       }
     }
     const float* src[3] = {a.w_post, a.gate_kind == NF4_GATE_CHANNEL ? static_cast<const float*>(a.gate) : nullptr, a.w_pre};
@@ -598,7 +599,7 @@ __global__ void __launch_bounds__(kMaxThreadsFwd) norm_fwd_ring_kernel(const __g
   const bool token = a.gate_kind == NF4_GATE_TOKEN;
   const float inv_h = 1.0f / static_cast<float>(a.H);
   int st = 0, buf = 0;
-  uint32_t ph = 0, last = 0;
+  uint32_t ph = 0;
   auto squares = [&](int stage) {  // of this thread's part of y
     float2 s = both(0.0f);
     if (a.w_post) {
@@ -641,7 +642,7 @@ __global__ void __launch_bounds__(kMaxThreadsFwd) norm_fwd_ring_kernel(const __g
     ss_y = sums.y;
     const float rstd_z = rsqrtf(sums.x * inv_h + a.eps);
     // every thread has read its part of row t
-    if (threadIdx.x == 0) rr.refill(st, ph, t + static_cast<int64_t>(stages) * gridDim.x, last);
+    if (threadIdx.x == 0) rr.refill(st, t + static_cast<int64_t>(stages) * gridDim.x);
     if (a.h) {
       rr.gain(g, 2);
 #pragma unroll
@@ -655,7 +656,7 @@ __global__ void __launch_bounds__(kMaxThreadsFwd) norm_fwd_ring_kernel(const __g
     st = st1;
     ph = ph1;
   }
-  if (threadIdx.x == 0 && ring.gave_up) ring_drain(ring, rr.used(), last, rr.limit_ns());
+  if (threadIdx.x == 0 && ring.gave_up) ring_drain(ring, stages, rr.limit_ns());
 }
 
 // As in the forward, row t's second sum and row t + 1's first share a barrier.  What a row
@@ -708,7 +709,7 @@ __global__ void __launch_bounds__(kMaxThreadsBwd) norm_bwd_ring_kernel(const __g
 #pragma unroll
   for (int i = 0; i < kPairs; ++i) sum_pre[i] = sum_post[i] = sum_gate[i] = both(0.0f);
   int st = 0, buf = 0;
-  uint32_t ph = 0, last = 0;
+  uint32_t ph = 0;
   float rstd_y = a.stats[blockIdx.x], rstd_z = a.stats[a.T + blockIdx.x];
   rr.wait(0, 0, a.status);
   float dot = block_sum2(make_float2(first_sum(0, rstd_y), 0.0f), red[1]).x;
@@ -759,7 +760,7 @@ __global__ void __launch_bounds__(kMaxThreadsBwd) norm_bwd_ring_kernel(const __g
     const float2 sums = block_sum2(make_float2(s.x + s.y, s1), red[buf]);
     buf ^= 1;
     // every thread has read its part of row t
-    if (threadIdx.x == 0) rr.refill(st, ph, t + static_cast<int64_t>(stages) * gridDim.x, last);
+    if (threadIdx.x == 0) rr.refill(st, t + static_cast<int64_t>(stages) * gridDim.x);
     if (a.gy) {
       // without w_post, n is y itself: no norm to go back through
       const float back = a.w_post ? rstd_y * (sums.x * inv_h) : 0.0f;
@@ -774,7 +775,7 @@ __global__ void __launch_bounds__(kMaxThreadsBwd) norm_bwd_ring_kernel(const __g
     st = st1;
     ph = ph1;
   }
-  if (threadIdx.x == 0 && ring.gave_up) ring_drain(ring, rr.used(), last, rr.limit_ns());
+  if (threadIdx.x == 0 && ring.gave_up) ring_drain(ring, stages, rr.limit_ns());
   Sums sum;
 #pragma unroll
   for (int i = 0; i < kPairs; ++i) {
