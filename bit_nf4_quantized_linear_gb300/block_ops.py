@@ -39,6 +39,7 @@ def _raw_stream(device: torch.device) -> int:
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
+_written = torch._C._increment_version  # torch.autograd.graph.increment_version of a list
 _current_device, _guard, _HERE = torch._C._cuda_getDevice, torch.cuda.device, contextlib.nullcontext()
 
 
@@ -152,7 +153,7 @@ def attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens:
     if rc:
         _lib.check(rc, "nf4_attention_fwd")
     if out is not None:
-        torch.autograd.graph.increment_version(out)
+        _written((out,))
     lse.o_rest = rest
     return o, lse
 
@@ -417,21 +418,20 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[Optional[torch.Te
     if not full:
         it = iter(ptrs)
         ptrs = [0 if g is None else next(it) for g in grads]
-    steps = [(state.step + 1, ptrs)]
+    numbers = {state.step + 1: ptrs}
     if per_tensor and state.missed:
-        number = [state.step + 1 - state.missed.get(i, 0) for i in range(n)]
-        steps = [(s, [p if s == m else 0 for p, m in zip(ptrs, number)])
-                 for s in sorted({m for m, g in zip(number, grads) if g is not None})]
-    addresses = list(map(T.data_ptr, params))
-    for step, ptrs in steps:
-        with _on(dev):
-            rc = _fn("nf4_adamw_step")(state._table(addresses, ptrs), n, _DTYPES[dtype], state.bits, _ptr(state.levels[0]),
+        own = [state.step + 1 - state.missed.get(i, 0) for i in range(n)]
+        numbers = {s: [p if s == m else 0 for p, m in zip(ptrs, own)] for s in {m for m, g in zip(own, grads) if g is not None}}
+    at = list(map(T.data_ptr, params))
+    with _on(dev):
+        for step, ptrs in numbers.items():
+            rc = _fn("nf4_adamw_step")(state._table(at, ptrs), n, _DTYPES[dtype], state.bits, _ptr(state.levels[0]),
                                        _ptr(state.levels[1]), lr, betas[0], betas[1], eps, weight_decay, step, _ptr(grad_scale),
                                        _raw_stream(dev))
-        if rc:
-            _lib.check(rc, "nf4_adamw_step")
+            if rc:
+                _lib.check(rc, "nf4_adamw_step")
     # autograd's record of writes that it did not see
-    torch.autograd.graph.increment_version(params if full else [p for p, g in zip(params, grads) if g is not None])
+    _written(params if full else [p for p, g in zip(params, grads) if g is not None])
     state.step += 1
     if not full:
         for i, g in enumerate(grads):
