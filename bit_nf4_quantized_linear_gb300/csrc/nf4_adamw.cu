@@ -541,7 +541,7 @@ __global__ void __launch_bounds__(threads(BITS), BITS == 8 ? 1 : 2) adamw_kernel
 }
 
 // out[i] = levels[codes[i]] * absmax[i / 256] for both states, eight values a thread
-// where the pointers allow (18 bytes a value in and out: bound by HBM).
+// where the pointers allow (10 bytes a value, two in and eight out: bound by HBM).
 __global__ void __launch_bounds__(kThreads) adamw_values_kernel(const __grid_constant__ AdamValuesArgs a) {
   __shared__ float lev[2][256];
   for (int i = threadIdx.x; i < 512; i += kThreads) lev[i >> 8][i & 255] = (i < 256 ? a.levels_m : a.levels_v)[i & 255];

@@ -18,16 +18,18 @@
 // warp alternates between the tiles (P V of one, then its next S), so the tensor cores
 // work on one tile while the other's softmax runs.
 //
-// What bounds it (12289 rows, 40 heads over 8 of width 128, fp16: 1.17 ms, 1320 TFLOP/s):
-// the MMAs and the clock, which falls under them: S has both operands in shared memory,
-// which its 128 x 128 products read at the full 128 bytes a clock.  Issued under a lane test
-// instead of an elected lane the MMAs took 1.37 ms.  256 rows a CTA halve the key and value
-// traffic against 128; two tiles fill tensor memory.  Splitting a row between two threads
-// (twice the softmax warps) was slower (1.63 against 1.34 ms): the warps' latency is hidden
-// already, their meetings are not.  So was forming a quarter of the exponentials by a
-// polynomial (1.56 against 1.37 ms).  Ragged batches pay about 4 us a CTA for its start and
-// end on top (8192 rows in sequences of 1 to 3001: 163 us, 830 TFLOP/s).  With heads of 64
-// the products halve and the softmax bounds (4095 rows, 32 heads: 71 us, 480 TFLOP/s).
+// What bounds it: for a long prompt the products at the clock that the power limit leaves
+// (12289 rows, 40 heads over 8 of width 128, fp16: 1.18 ms, 1310 TFLOP/s of 1702 that a
+// library product sustains; 1957 MHz of 2070 at 1370 W); S has both operands in shared
+// memory, which its 128 x 128 products read at the full 128 bytes a clock.  Shorter ones
+// wait for tensor memory on either side of the softmax (two sequences of 4096: the tensor
+// pipe is active 44% of the cycles).  Issued under a lane test instead of an elected lane the
+// MMAs took 1.37 ms.  256 rows a CTA halve the key and value traffic against 128; two tiles
+// fill tensor memory.  While the MMAs were still issued under a lane test, splitting a row
+// between two threads (1.63 against 1.34 ms) and forming a quarter of the exponentials by a
+// polynomial (1.56 against 1.37 ms) were slower; neither was tried since.  Ragged batches pay
+// about 4 us a CTA for its start and end on top (8192 rows in sequences of 1 to 3001: 163 us,
+// 830 TFLOP/s).  With heads of 64 the products halve (4095 rows, 32 heads: 71 us, 480 TFLOP/s).
 //
 // Masked pairs: S is replaced before the exponential, so nothing of a masked key enters
 // P.  In P V the weight 0 of a masked row would still turn an infinite or NaN value into

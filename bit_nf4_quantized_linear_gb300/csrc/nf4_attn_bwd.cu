@@ -29,15 +29,17 @@
 // the queries' CTAs dQ and the scores after next run while dS is formed.
 //
 // What bounds it: the products, 7/5 of the definition's (12289 rows, 40 heads over 8 of
-// width 128: 3.6 to 3.7 ms, 1050 TFLOP/s of the definition's, 1470 executed), two of four
+// width 128, fp16: 3.7 to 3.9 ms with the passes before it, 1000 TFLOP/s of the definition's,
+// 1400 executed, at 1905 MHz under the power limit), two of four
 // (three) of them with both operands in shared memory at its full read rate.  A step of the
 // keys' CTAs spends 2250 of 3070 cycles issuing MMAs at the tensor cores' rate; with the
 // loads of Q and dO in two joint stages instead of three and two of their own it waited 730
 // cycles more for them.  Four compute groups of 32 columns instead of two of 64 were slower
-// (4.6 against 4.4 ms).  Short tiles pay for a CTA's start and end: about 4000 cycles before
+// (4.6 against 4.4 ms) while an MMA still took 100 cycles to issue; not tried since.  Short tiles pay for a CTA's start and end: about 4000 cycles before
 // its first step and as many after the last, of 28000 (8192 rows in 9 sequences).  Short
-// sequences are bound by the longest chain of steps of a key tile: 512 rows take 29 us with
-// the row sums.
+// sequences are bound by the longest chain of steps of a key tile: 512 rows take 30 us with
+// the row sums.  The scale of dS costs fp16 a multiplication a pair in the keys' CTAs and the
+// shift kernel: 8192 rows 503 us against 473 in bf16, 512 rows 38 against 32.
 //
 // Masked pairs: P and dS are set to 0 by index.  Where that 0 would still meet an
 // infinity or a NaN as a factor -- rows of another sequence in a ragged tile, and rows

@@ -16,8 +16,8 @@
 //   channel gate).
 // Three forms, by what the rows allow:
 //  - rows streamed through shared memory (16-byte rows, more rows than CTAs): 8192 x 5120
-//    bf16 with a gate per token 73 us forward (5.8 TB/s of 6.8 measured by a copy) and 134 us
-//    backward with the token sums (5.0 TB/s); bound by HBM with the issue slots at 65%
+//    bf16 with a gate per token 74 us forward (5.7 TB/s of 6.8 measured by a copy) and 134 us
+//    backward with the token sums (5.0 TB/s); bound by HBM with the issue slots at 55 to 60%
 //  - a row in a CTA's registers (any alignment; few rows): one token of 4096 in 4 us, mostly
 //    the latency of one load and two sums; 1023 x 2047 fp16 10 us
 //  - rows wider than a CTA's registers (8192 forward, 5120 backward): three passes over the

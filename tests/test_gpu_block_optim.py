@@ -157,6 +157,7 @@ def test_a_captured_step_is_refused():
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
+        ps[0].grad.mul_(1)  # a graph with something in it
         with pytest.raises(RuntimeError, match="captur"):
             opt.step()
     opt.step()
