@@ -103,14 +103,14 @@ def relative(got, want):
     return ((got.double() - want).norm() / want.norm()).item()
 
 
-def check_relative(grads, want):
+def check_relative(grads, want, unit=ROUND16):
     """Relative error of each whole gradient: one rounding of the result (subnormal where it is), one of the weights or
     score gradients of its product, one of the probabilities that o, and so the row sums, are made of.  They are
     independent, so their squares add; a tenth on top."""
     for got, name in zip(grads, ("gq", "gk", "gv")):
         assert torch.isfinite(got).all(), name
-        one = relative(want[name].half(), want[name])
-        assert relative(got, want[name]) <= 1.1 * math.sqrt(one ** 2 + 2 * ROUND16 ** 2), (name, relative(got, want[name]) / one)
+        one = relative(want[name].to(got.dtype), want[name])
+        assert relative(got, want[name]) <= 1.1 * math.sqrt(one ** 2 + 2 * unit ** 2), (name, relative(got, want[name]) / one)
 
 
 @pytest.mark.parametrize("size", [1.0, 1e-2, 1e-3, 3e-4, 1e-4, 3e-5])
@@ -122,6 +122,16 @@ def test_attention_fp16_gradients_of_any_size(size, Hq, Hk, D, lens):
     o, lse = nf4.attention_fwd(q, k, v, cu)
     grads = nf4.attention_bwd(go, q, k, v, o, lse, cu)
     check_relative(grads, ref.attention(q, k, v, b, D ** -0.5, go)[0])
+
+
+@pytest.mark.parametrize("Hq,Hk,D,lens", [(2, 1, 64, [2500]), (2, 2, 128, [2500]), (4, 1, 96, [1, 700, 0, 33, 1200])])
+def test_attention_bf16_error_of_whole_gradients(Hq, Hk, D, lens):
+    """Beside the bounds of single elements, which grow with the sum of their terms' sizes, one for each gradient."""
+    q, k, v, go = qkv(sum(lens), Hq, Hk, D, BF16)
+    b, cu = offsets(lens)
+    o, lse = nf4.attention_fwd(q, k, v, cu)
+    grads = nf4.attention_bwd(go, q, k, v, o, lse, cu)
+    check_relative(grads, ref.attention(q, k, v, b, D ** -0.5, go)[0], 8 * ROUND16)
 
 
 def test_attention_fp16_large_score_gradients():
