@@ -40,7 +40,8 @@ def _raw_stream(device: torch.device) -> int:
 
 
 _written = torch._C._increment_version  # torch.autograd.graph.increment_version of a list
-_current_device, _guard, _HERE = torch._C._cuda_getDevice, torch.cuda.device, contextlib.nullcontext()
+_current_device = getattr(torch._C, "_cuda_getDevice", None)  # None: a torch without CUDA, which gets no further
+_guard, _HERE = torch.cuda.device, contextlib.nullcontext()
 
 
 def _on(device: torch.device):
