@@ -24,13 +24,14 @@ STATUS_NAMES = {
 }
 DTYPE_F32, DTYPE_BF16, DTYPE_F16 = 0, 1, 2
 (OP_QUANTIZE, OP_LINEAR_FWD, OP_LINEAR_DGRAD, OP_GROUPED_FWD, OP_GROUPED_DGRAD, OP_GROUPED_SWIGLU_BWD,
- OP_NORM_RESIDUAL_BWD, OP_ATTENTION_BWD) = range(8)
+ OP_NORM_RESIDUAL_BWD, OP_ATTENTION_BWD, OP_PAGED_ATTENTION, OP_ROUTE) = range(10)
 GATE_NONE, GATE_CHANNEL, GATE_TOKEN = range(3)
+SCORE_SOFTMAX, SCORE_SIGMOID = range(2)
 ADAMW_BLOCK = 256  # NF4_ADAMW_BLOCK of include/nf4.h
 PATHS = ["linear_fwd", "linear_dgrad", "splitk_reduce", "grouped_fwd", "grouped_dgrad",
          "dequantize", "quantize", "total", "gemv_fwd", "gemv_dgrad", "skinny_fwd",
          "skinny_dgrad", "stream_k", "cluster_split", "multi", "moe_combine", "attention", "attention_any",
-         "norm_residual", "adamw"]
+         "norm_residual", "adamw", "paged_append", "paged_attention", "paged_attention_any", "route"]
 
 
 class NF4Error(RuntimeError):
@@ -93,6 +94,28 @@ class nf4_adamw_tensor(ctypes.Structure):
     _fields_ = [
         ("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
         ("m_absmax", ctypes.c_void_p), ("v_absmax", ctypes.c_void_p), ("n", ctypes.c_int64),
+    ]
+
+
+class nf4_paged_cache(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("k_page", ctypes.c_int64), ("k_token", ctypes.c_int64), ("k_head", ctypes.c_int64),
+        ("v_page", ctypes.c_int64), ("v_token", ctypes.c_int64), ("v_head", ctypes.c_int64),
+        ("table", ctypes.c_void_p), ("ld_table", ctypes.c_int64), ("lengths", ctypes.c_void_p),
+        ("nseq", ctypes.c_int64), ("pages", ctypes.c_int64),
+        ("max_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("Hk", ctypes.c_int32), ("D", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+    ]
+
+
+class nf4_route(ctypes.Structure):
+    _fields_ = [
+        ("logits", ctypes.c_void_p), ("ld", ctypes.c_int64), ("T", ctypes.c_int64),
+        ("bias", ctypes.c_void_p), ("live", ctypes.c_void_p),
+        ("E", ctypes.c_int32), ("k", ctypes.c_int32), ("dtype", ctypes.c_int32), ("score", ctypes.c_int32),
+        ("groups", ctypes.c_int32), ("top_groups", ctypes.c_int32), ("group_top", ctypes.c_int32),
+        ("renormalise", ctypes.c_int32), ("scale", ctypes.c_float),
     ]
 
 
@@ -161,6 +184,10 @@ def lib() -> ctypes.CDLL:
             "nf4_attention_bwd": [AT, P, I64, I64, P, P, I64, I64, P, I64, I64, P, I64, I64, P, I64, I64, P, SZ, P],
             "nf4_adamw_step": [P, I32, I32, I32, P, P, F64, F64, F64, F64, F64, I64, P, P],
             "nf4_adamw_state_values": [P, P, P, P, P, P, I64, P, P, P],
+            "nf4_paged_append": [P, P, I64, I64, P, I64, I64, P, I64, P],
+            "nf4_paged_attention": [P, P, I64, I64, I32, ctypes.c_float, P, I64, I64, P, P, SZ, P],
+            "nf4_route_fwd": [P, P, P, P, P, P, P, P, SZ, P],
+            "nf4_route_bwd": [P, P, P, P, P, P, I64, P],
             "nf4_workspace_size": [I32, I64, I64, I64, I32],
             "nf4_status_string": [I32],
             "nf4_checked_build": [],

@@ -17,7 +17,7 @@ from __future__ import annotations
 
 import torch
 
-from . import block_ops, ops
+from . import block_ops, ops, route_ops
 
 
 class NF4LinearFn(torch.autograd.Function):
@@ -185,6 +185,27 @@ def nf4_combine(rows: torch.Tensor, token_rows: torch.Tensor) -> torch.Tensor:
     return NF4MoECombineFn.apply(rows, token_rows)
 
 
+class NF4DispatchFn(torch.autograd.Function):
+    """Each token's activations copied to the rows of its routes (the copy that is the combine's
+    backward), with the combine as its own backward: the reverse of NF4MoECombineFn."""
+
+    @staticmethod
+    def forward(ctx, x, token_rows):
+        ctx.save_for_backward(token_rows)
+        return ops.moe_combine_bwd(x.contiguous(), token_rows, token_rows.numel())
+
+    @staticmethod
+    def backward(ctx, grows):
+        (token_rows,) = ctx.saved_tensors
+        return ops.moe_combine(grows.contiguous(), token_rows) if ctx.needs_input_grad[0] else None, None
+
+
+def nf4_dispatch(x: torch.Tensor, token_rows: torch.Tensor) -> torch.Tensor:
+    """The rows of the grouped experts from the tokens' activations (bf16 [tokens, H] -> [tokens * k, H]): row
+    token_rows[t, j] is token t (-1: no row; rows that no route names are zero).  See nf4_route."""
+    return NF4DispatchFn.apply(x, token_rows)
+
+
 class _FirstOrderFn(torch.autograd.Function):
     """Hands gradients on; going back through them is an error."""
 
@@ -271,6 +292,43 @@ def nf4_norm_residual(y: torch.Tensor, residual: torch.Tensor = None, *, w_post:
     fp32 [H]; the gate is fp32 [H] or [T, H] in y's dtype.  Every part but y may be left out (w_pre None:
     h is None; y with w_pre alone is a plain norm before the first block).  Returns (z, h)."""
     return NF4NormResidualFn.apply(y, residual, w_post, gate, w_pre, float(scale), float(eps))
+
+
+class NF4RouteFn(torch.autograd.Function):
+    """The router of the experts (nf4_route_fwd) and the gradient of its logits (nf4_route_bwd) from those of the
+    weights, by token or by row.  Logits and tables go through save_for_backward.  First derivatives only."""
+
+    @staticmethod
+    def forward(ctx, logits, k, bias, live, how):
+        r = route_ops.route_experts(logits, k, bias=bias, live=live, **how)
+        ctx.mark_non_differentiable(*(t for t in (r.experts, r.offsets, r.row_token, r.token_rows) if t is not None))
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(logits, r.experts, r.token_rows)
+        ctx.how = {n: how[n] for n in ("score", "renormalise", "scale")}
+        return tuple(r)
+
+    @staticmethod
+    def backward(ctx, _experts, g_weights, _offsets, _row_token, _token_rows, g_rows):
+        logits, experts, token_rows = ctx.saved_tensors
+        if g_weights is None and g_rows is None:
+            return (None,) * 5
+        routes = route_ops.Routes(experts, None, None, None, token_rows, None)
+        g = route_ops.route_experts_bwd(logits, routes, grad_weights=g_weights, grad_row_weight=g_rows, **ctx.how)
+        return (*_first_order("nf4_route", (g,), (logits,)), None, None, None, None)
+
+
+def nf4_route(logits: torch.Tensor, k: int, *, score: str = "softmax", bias: torch.Tensor = None, groups: int = 1,
+              top_groups: int = None, group_top: int = 1, renormalise: bool = False, scale: float = 1.0, live: torch.Tensor = None,
+              tables: bool = True) -> route_ops.Routes:
+    """The k experts of each token, their weights and the grouped experts' tables (see route_ops.route_experts), with
+    gradients of the logits through `weights` and `row_weight`.  (A backward pass that is captured in a CUDA graph needs what
+    autograd asks of all of them: no eager graph of the same leaves may be alive.)  A mixture-of-experts layer over grouped weights:
+
+        r = nf4_route(x @ gate.T, k)
+        h = nf4_grouped_swiglu(nf4_dispatch(x, r.token_rows), r.offsets, w_gate_up, E, r.row_weight)
+        y = nf4_combine(nf4_grouped(h, r.offsets, w_down, E), r.token_rows)"""
+    how = dict(score=score, groups=groups, top_groups=top_groups, group_top=group_top, renormalise=renormalise, scale=float(scale), tables=tables)
+    return route_ops.Routes(*NF4RouteFn.apply(logits, k, bias, live, how))
 
 
 def nf4_linear(x: torch.Tensor, w: ops.NF4Weight) -> torch.Tensor:

@@ -54,6 +54,11 @@ def _workspace(op: int, M: int, N: int, device: torch.device) -> int:
     return workspace_size(op, M, N, 0)
 
 
+@functools.lru_cache(maxsize=64)
+def _workspace3(op: int, M: int, N: int, K: int, device: torch.device) -> int:
+    return workspace_size(op, M, N, K)
+
+
 def _one_device(name: str, *ts):
     _need_cuda(name, *ts)
     devs = {t.device for t in ts if t is not None}

@@ -148,6 +148,60 @@ cudaError_t launch_attn_fwd(bool f16, const AttnMaps& m, const AttnArgs& a, cuda
 cudaError_t launch_attn_bwd(bool f16, const AttnMaps& m, const AttnArgs& a, int sms, cudaStream_t s);
 cudaError_t launch_attn_any(bool backward, int dtype, const AttnArgs& a, int sms, cudaStream_t s);
 
+// The paged key-value cache: writing new tokens into it (nf4_paged_append) and attention of
+// one query token a sequence over it (nf4_paged_attention).
+struct PagedArgs {
+  const void *q, *k_new, *v_new;
+  void *k, *v, *o;  // pages; outputs
+  float* lse;       // [nseq][Hq] or null
+  int64_t k_page, k_token, k_head, v_page, v_token, v_head;  // strides of the pages in elements
+  int64_t q_s, q_h, o_s, o_h, kn_t, kn_h, vn_t, vn_h;
+  int64_t pages, nseq, ld_table, T;
+  const int32_t *table, *lengths, *cu_seqlens;
+  int max_pages, page_size, Hq, Hk, D;
+  float scale;
+  float* part;  // partial results [CTAs][2][heads of a unit][paged_part_stride(D)]
+  struct PagedRec* rec;  // [CTAs]
+  int* status;
+};
+// What a CTA left in the partial results: slot 1 holds a unit run that begins a (sequence,
+// head group) and goes on in a later CTA, slot 0 one that began in an earlier CTA.
+struct PagedRec {
+  int64_t seq;
+  int32_t head;   // of slot 1: key head x groups of query heads + group
+  int32_t flags;  // 1: slot 1 is in use; 2: slot 0 is; 4: slot 0 ends its (sequence, head group)
+};
+// floats of one head's partial result: D sums, maximum (base 2), sum of weights
+inline __host__ __device__ int paged_part_stride(int D) { return (D + 3) / 4 * 4 + 4; }
+constexpr int kPagedSlots = 64;  // partial results of single heads a SM at most
+constexpr int kPagedCtas = 4;    // CTAs a SM at most
+inline size_t paged_ws_bytes(int D, int sms) {
+  return static_cast<size_t>(sms) * (kPagedSlots * paged_part_stride(D) * sizeof(float) + kPagedCtas * sizeof(PagedRec));
+}
+cudaError_t launch_paged_append(int dtype, const PagedArgs& a, int sms, cudaStream_t s);
+cudaError_t launch_paged_any(int dtype, const PagedArgs& a, int sms, cudaStream_t s);
+
+// The router of the experts (nf4_route_fwd / nf4_route_bwd).
+struct RouteArgs {
+  const void* logits;  // [T][E], pitch ld
+  int64_t ld, T;
+  const float* bias;     // [E] or null
+  const uint8_t* live;   // [T] or null
+  int E, k, sigmoid, groups, top_groups, group_top, renorm;
+  float scale;
+  int32_t *experts, *offsets, *row_token, *token_rows;  // [T][k], [E + 1], [T k], [T][k]; tables null: not wanted
+  float *weights, *row_weight;                          // [T][k], [T k]
+  int32_t* counts;  // [CTAs][E], workspace
+  // backward
+  const float *g_weights, *g_rows;  // [T][k], [T k]; either may be null
+  void* g_logits;
+  int64_t ld_g;
+  int* status;
+};
+constexpr int kRouteMaxK = 32;
+int route_ctas(int64_t T, int sms);
+cudaError_t launch_route(bool backward, int dtype, const RouteArgs& a, int sms, cudaStream_t s);
+
 // Multi-product launches (nf4_linear_fwd_multi / nf4_linear_dgrad_multi): up to
 // kMaxProds independent products with the same M and in-features K, each with its
 // own weight, activation and output, whose work items share one grid.

@@ -1024,9 +1024,193 @@ bool attn_maps(const nf4_attention* d, nf4::AttnMaps* m) {  // go, of the backwa
          encode_heads(&m->v, f16, d->v, d->T, d->Hk, d->D, d->v_token, d->v_head);
 }
 
+// Checks and arguments common to the calls on a paged cache.
+nf4_status paged_args(const nf4_paged_cache* c, nf4::PagedArgs* a) {
+  if (!c || !known_dtype(c->dtype)) return NF4_ERR_INVALID_ARG;
+  if (c->nseq < 0 || c->pages < 0 || c->max_pages < 0 || c->page_size < 1 || c->Hk < 1 || c->D < 1 || c->ld_table < 0)
+    return NF4_ERR_INVALID_ARG;
+  if (c->nseq > INT32_MAX || c->pages > INT32_MAX || c->Hk > 65535 || c->D > 256) return NF4_ERR_UNSUPPORTED_SHAPE;
+  if (static_cast<int64_t>(c->max_pages) * c->page_size > INT32_MAX) return NF4_ERR_UNSUPPORTED_SHAPE;
+  if (c->nseq > 0) {
+    if (!c->lengths || (c->max_pages > 0 && !c->table) || (c->pages > 0 && (!c->k || !c->v))) return NF4_ERR_INVALID_ARG;
+    const size_t e = dtype_bytes(c->dtype);
+    if (!aligned_to(c->k, e) || !aligned_to(c->v, e) || !aligned_to(c->table, 4) || !aligned_to(c->lengths, 4))
+      return NF4_ERR_ALIGNMENT;
+  }
+  *a = {};
+  a->k = c->k;
+  a->v = c->v;
+  a->k_page = c->k_page;
+  a->k_token = c->k_token;
+  a->k_head = c->k_head;
+  a->v_page = c->v_page;
+  a->v_token = c->v_token;
+  a->v_head = c->v_head;
+  a->table = c->table;
+  a->ld_table = c->ld_table;
+  a->lengths = c->lengths;
+  a->nseq = c->nseq;
+  a->pages = c->pages;
+  a->max_pages = c->max_pages;
+  a->page_size = c->page_size;
+  a->Hk = c->Hk;
+  a->D = c->D;
+  return NF4_OK;
+}
+
+// Checks and arguments common to the router's two directions.
+nf4_status route_args(const nf4_route* d, nf4::RouteArgs* a) {
+  if (!d || !known_dtype(d->dtype)) return NF4_ERR_INVALID_ARG;
+  if (d->T < 0 || d->E < 1 || d->k < 1 || d->ld < d->E) return NF4_ERR_INVALID_ARG;
+  if (d->score != NF4_SCORE_SOFTMAX && d->score != NF4_SCORE_SIGMOID) return NF4_ERR_INVALID_ARG;
+  if (d->groups < 1 || d->E % d->groups != 0 || d->top_groups < 1 || d->top_groups > d->groups || d->group_top < 1 ||
+      d->group_top > 2 || d->k > static_cast<int64_t>(d->top_groups) * (d->E / d->groups))
+    return NF4_ERR_INVALID_ARG;
+  if (d->E > nf4::kMaxExperts || d->k > nf4::kRouteMaxK || d->groups > 32 || d->T > INT32_MAX / d->k) return NF4_ERR_UNSUPPORTED_SHAPE;
+  if (d->T > 0 && !d->logits) return NF4_ERR_INVALID_ARG;
+  if (!aligned_to(d->logits, dtype_bytes(d->dtype)) || !aligned_to(d->bias, 4)) return NF4_ERR_ALIGNMENT;
+  *a = {};
+  a->logits = d->logits;
+  a->ld = d->ld;
+  a->T = d->T;
+  a->bias = d->bias;
+  a->live = d->live;
+  a->E = d->E;
+  a->k = d->k;
+  a->sigmoid = d->score == NF4_SCORE_SIGMOID;
+  a->groups = d->groups;
+  a->top_groups = d->top_groups;
+  a->group_top = d->group_top;
+  a->renorm = d->renormalise != 0;
+  a->scale = d->scale;
+  return NF4_OK;
+}
+
 }  // namespace
 
 extern "C" {
+
+nf4_status nf4_paged_append(const nf4_paged_cache* c, const void* k, int64_t k_token, int64_t k_head, const void* v,
+                            int64_t v_token, int64_t v_head, const int32_t* cu_seqlens, int64_t T, void* stream) {
+  nf4::PagedArgs a;
+  if (nf4_status s = paged_args(c, &a)) return s;
+  if (T < 0 || (!cu_seqlens && T != a.nseq)) return NF4_ERR_INVALID_ARG;
+  if (T > INT32_MAX) return NF4_ERR_UNSUPPORTED_SHAPE;
+  if (T == 0 || a.nseq == 0) return NF4_OK;
+  if (!k || !v) return NF4_ERR_INVALID_ARG;
+  const size_t e = dtype_bytes(c->dtype);
+  if (!aligned_to(k, e) || !aligned_to(v, e) || !aligned_to(cu_seqlens, 4)) return NF4_ERR_ALIGNMENT;
+  a.k_new = k;
+  a.v_new = v;
+  a.kn_t = k_token;
+  a.kn_h = k_head;
+  a.vn_t = v_token;
+  a.vn_h = v_head;
+  a.cu_seqlens = cu_seqlens;
+  a.T = T;
+  DevInfo dev;
+  if (!current_device(&dev)) return cuda_fail(cudaGetLastError(), "device query");
+  a.status = dev.status;
+  cudaError_t le = nf4::launch_paged_append(c->dtype, a, dev.sms, static_cast<cudaStream_t>(stream));
+  if (le != cudaSuccess) return cuda_fail(le, "kernel launch");
+  count(NF4_PATH_PAGED_APPEND);
+  return NF4_OK;
+}
+
+nf4_status nf4_paged_attention(const nf4_paged_cache* c, const void* q, int64_t q_seq, int64_t q_head, int32_t Hq,
+                               float scale, void* o, int64_t o_seq, int64_t o_head, float* lse, void* ws,
+                               size_t ws_bytes, void* stream) {
+  nf4::PagedArgs a;
+  if (nf4_status s = paged_args(c, &a)) return s;
+  if (Hq < 1 || Hq % a.Hk != 0) return NF4_ERR_INVALID_ARG;
+  if (Hq > 65535) return NF4_ERR_UNSUPPORTED_SHAPE;
+  if (a.nseq == 0) return NF4_OK;
+  if (!q || !o) return NF4_ERR_INVALID_ARG;
+  const size_t e = dtype_bytes(c->dtype);
+  if (!aligned_to(q, e) || !aligned_to(o, e) || !aligned_to(lse, 4)) return NF4_ERR_ALIGNMENT;
+  DevInfo dev;
+  if (!current_device(&dev)) return cuda_fail(cudaGetLastError(), "device query");
+  if (!ws || ws_bytes < nf4::paged_ws_bytes(a.D, dev.sms)) return NF4_ERR_WORKSPACE;
+  if (!aligned_to(ws, 16)) return NF4_ERR_ALIGNMENT;
+  a.q = q;
+  a.q_s = q_seq;
+  a.q_h = q_head;
+  a.o = o;
+  a.o_s = o_seq;
+  a.o_h = o_head;
+  a.lse = lse;
+  a.Hq = Hq;
+  a.scale = scale;
+  a.rec = static_cast<nf4::PagedRec*>(ws);
+  a.part = reinterpret_cast<float*>(a.rec + nf4::kPagedCtas * dev.sms);
+  a.status = dev.status;
+  cudaError_t le = nf4::launch_paged_any(c->dtype, a, dev.sms, static_cast<cudaStream_t>(stream));
+  if (le != cudaSuccess) return cuda_fail(le, "kernel launch");
+  count(NF4_PATH_PAGED_ATTENTION_ANY);
+  return NF4_OK;
+}
+
+nf4_status nf4_route_fwd(const nf4_route* d, int32_t* experts, float* weights, int32_t* offsets, int32_t* row_token,
+                         int32_t* token_rows, float* row_weight, void* ws, size_t ws_bytes, void* stream) {
+  nf4::RouteArgs a;
+  if (nf4_status s = route_args(d, &a)) return s;
+  const bool tables = offsets != nullptr;
+  if (a.T > 0 && (!experts || !weights || tables != (row_token != nullptr) || tables != (token_rows != nullptr) ||
+                  tables != (row_weight != nullptr)))
+    return NF4_ERR_INVALID_ARG;
+  for (const void* p : {static_cast<const void*>(experts), static_cast<const void*>(weights), static_cast<const void*>(offsets),
+                        static_cast<const void*>(row_token), static_cast<const void*>(token_rows), static_cast<const void*>(row_weight)})
+    if (!aligned_to(p, 4)) return NF4_ERR_ALIGNMENT;
+  DevInfo dev;
+  if (!current_device(&dev)) return cuda_fail(cudaGetLastError(), "device query");
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (a.T == 0) {
+    if (tables)
+      if (cudaError_t ce = cudaMemsetAsync(offsets, 0, (static_cast<size_t>(a.E) + 1) * 4, st)) return cuda_fail(ce, "memset");
+    return NF4_OK;
+  }
+  if (tables && nf4::route_ctas(a.T, dev.sms) > 1) {
+    if (!ws || ws_bytes < static_cast<size_t>(nf4::route_ctas(a.T, dev.sms)) * a.E * 4) return NF4_ERR_WORKSPACE;
+    if (!aligned_to(ws, 4)) return NF4_ERR_ALIGNMENT;
+    a.counts = static_cast<int32_t*>(ws);
+  }
+  a.experts = experts;
+  a.weights = weights;
+  a.offsets = offsets;
+  a.row_token = row_token;
+  a.token_rows = token_rows;
+  a.row_weight = row_weight;
+  a.status = dev.status;
+  cudaError_t le = nf4::launch_route(false, d->dtype, a, dev.sms, st);
+  if (le != cudaSuccess) return cuda_fail(le, "kernel launch");
+  count(NF4_PATH_ROUTE);
+  return NF4_OK;
+}
+
+nf4_status nf4_route_bwd(const nf4_route* d, const int32_t* experts, const int32_t* token_rows, const float* g_weights,
+                         const float* g_rows, void* g_logits, int64_t ld_g, void* stream) {
+  nf4::RouteArgs a;
+  if (nf4_status s = route_args(d, &a)) return s;
+  if (ld_g < a.E || (g_rows && !token_rows)) return NF4_ERR_INVALID_ARG;
+  if (a.T == 0) return NF4_OK;
+  if (!experts || !g_logits) return NF4_ERR_INVALID_ARG;
+  if (!aligned_to(experts, 4) || !aligned_to(token_rows, 4) || !aligned_to(g_weights, 4) || !aligned_to(g_rows, 4) ||
+      !aligned_to(g_logits, dtype_bytes(d->dtype)))
+    return NF4_ERR_ALIGNMENT;
+  a.experts = const_cast<int32_t*>(experts);
+  a.token_rows = const_cast<int32_t*>(token_rows);
+  a.g_weights = g_weights;
+  a.g_rows = g_rows;
+  a.g_logits = g_logits;
+  a.ld_g = ld_g;
+  DevInfo dev;
+  if (!current_device(&dev)) return cuda_fail(cudaGetLastError(), "device query");
+  a.status = dev.status;
+  cudaError_t le = nf4::launch_route(true, d->dtype, a, dev.sms, static_cast<cudaStream_t>(stream));
+  if (le != cudaSuccess) return cuda_fail(le, "kernel launch");
+  count(NF4_PATH_ROUTE);
+  return NF4_OK;
+}
 
 nf4_status nf4_norm_residual_fwd(const nf4_norm_residual* d, void* z, int64_t ld_z, void* h, int64_t ld_h,
                                  float* stats, void* stream) {
@@ -1421,6 +1605,12 @@ size_t nf4_workspace_size(int32_t op, int64_t M, int64_t N, int64_t K, int32_t E
     if (M <= 0 || N <= 0) return 0;
     // delta and shift_q [Hq][T], v_norm and shift_k [Hk][T] with Hk <= Hq
     return static_cast<size_t>(M) * N * 4 * sizeof(float);
+  }
+  if (op == NF4_OP_PAGED_ATTENTION || op == NF4_OP_ROUTE) {
+    DevInfo dev;
+    if (!current_device(&dev)) return 0;
+    if (op == NF4_OP_PAGED_ATTENTION) return K < 1 || K > 256 ? 0 : nf4::paged_ws_bytes(static_cast<int>(K), dev.sms);
+    return M <= 0 || N <= 0 ? 0 : static_cast<size_t>(nf4::route_ctas(M, dev.sms)) * N * 4;
   }
   if (op == NF4_OP_QUANTIZE) {
     const int64_t nblocks = (N * K + 63) / 64;

@@ -1,0 +1,331 @@
+// nf4_paged.cu -- the paged key-value cache: new tokens written into their pages
+// (nf4_paged_append), and attention of one query token a sequence for every type, width and
+// alignment (nf4_paged_attention; 16-bit types of whole 16-byte rows run on the tensor cores).
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "elem.cuh"
+#include "internal.h"
+#include "paged_common.cuh"
+#include "smem_limit.h"
+
+namespace nf4 {
+namespace {
+
+// ---------------------------------------------------------------------- append --
+
+constexpr int kAppendThreads = 256;
+
+// The place of new row r: its page and slot, or page -1 for none.  Row r of sequence i, the
+// last with cu[i] <= r, goes to position lengths[i] - cu[i + 1] + r; without cu_seqlens row r
+// is the newest token of sequence r.
+__device__ __forceinline__ int append_place(const PagedArgs& a, int64_t r, int* slot) {
+  int64_t seq = r, end = r + 1;
+  if (a.cu_seqlens) {
+    int64_t lo = 0, hi = a.nseq;  // cu[lo] <= r < cu[hi], as far as the offsets ascend
+    if (r < a.cu_seqlens[0] || r >= a.cu_seqlens[a.nseq]) return -1;
+    while (hi - lo > 1) {
+      const int64_t mid = (lo + hi) >> 1;
+      if (a.cu_seqlens[mid] <= r) lo = mid; else hi = mid;
+    }
+    seq = lo;
+    end = a.cu_seqlens[lo + 1];
+  }
+  const int len = paged_len(a, seq);
+  if (len == 0) return -1;  // an idle sequence
+  const int64_t pos = len - end + r;
+  if (pos < 0 || pos >= len) {
+    if (a.status) atomicCAS(a.status, 0, kStatusBadOffsets);
+    return -1;
+  }
+  return paged_slot(a, seq, static_cast<int>(pos), slot);
+}
+
+// Copies `V`-wide pieces of `rows` new rows a CTA.  Bound by HBM: each value is read and
+// written once.
+template <typename V>
+__global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(PagedArgs a, int rows, int per_head, int elems) {
+  __shared__ int64_t s_k[32], s_v[32];
+  if (a.cu_seqlens && blockIdx.x == 0 && a.status) {
+    bool bad = threadIdx.x == 0 && (a.cu_seqlens[0] < 0 || a.cu_seqlens[a.nseq] > a.T);
+    for (int64_t i = threadIdx.x; i < a.nseq; i += kAppendThreads) bad |= a.cu_seqlens[i + 1] < a.cu_seqlens[i];
+    if (bad) atomicCAS(a.status, 0, kStatusBadOffsets);
+  }
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * rows;
+  if (threadIdx.x < rows) {
+    int slot = 0;
+    const int64_t r = r0 + threadIdx.x;
+    const int64_t page = r < a.T ? append_place(a, r, &slot) : -1;
+    s_k[threadIdx.x] = page < 0 ? -1 : page * a.k_page + slot * a.k_token;
+    s_v[threadIdx.x] = page < 0 ? -1 : page * a.v_page + slot * a.v_token;
+  }
+  __syncthreads();
+  const int row = 2 * a.Hk * per_head;  // pieces of a row: keys, then values
+  for (int i = threadIdx.x; i < rows * row; i += kAppendThreads) {
+    const int t = i / row, j = i % row, h = j / per_head, hk = h < a.Hk ? h : h - a.Hk;
+    const int64_t d = static_cast<int64_t>(j % per_head) * elems, at = h < a.Hk ? s_k[t] : s_v[t];
+    if (at < 0) continue;
+    constexpr int64_t e = sizeof(V);
+    const int64_t r = r0 + t;
+    if (h < a.Hk)
+      *reinterpret_cast<V*>(static_cast<char*>(a.k) + (at + hk * a.k_head + d) * e / elems) =
+          *reinterpret_cast<const V*>(static_cast<const char*>(a.k_new) + (r * a.kn_t + hk * a.kn_h + d) * e / elems);
+    else
+      *reinterpret_cast<V*>(static_cast<char*>(a.v) + (at + hk * a.v_head + d) * e / elems) =
+          *reinterpret_cast<const V*>(static_cast<const char*>(a.v_new) + (r * a.vn_t + hk * a.vn_h + d) * e / elems);
+  }
+}
+
+// ------------------------------------------------------- attention, any layout --
+
+// fp32 arithmetic throughout.  A warp takes 32 / HC tokens at a time: its lanes hold the
+// tokens' rows 32 columns apart, form the partial products with HC query heads, and reduce the
+// 32 sums of (token, head) so that lane i ends with sum i, in 31 shuffles.
+constexpr int kAnyWarps = 8;
+
+template <typename T, int HC, int DV>
+__global__ void __launch_bounds__(kAnyWarps * 32) paged_any_kernel(PagedArgs a, int groups) {
+  constexpr int NT = 32 / HC;
+  extern __shared__ float dyn[];
+  float* s_q = dyn;                     // [HC][DV * 32]
+  float* s_acc = dyn + HC * DV * 32;    // [4][HC][DV * 32]
+  __shared__ int64_t s_red[34];
+  __shared__ float s_ml[kAnyWarps][HC][2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  paged_allow_join();
+  paged_empty<T>(a);
+  const int heads = a.Hk * groups, G = a.Hq / a.Hk;
+  PagedRun run = paged_run(a, heads, s_red);
+  PagedRec rec{0, 0, 0};
+  const T* kp = static_cast<const T*>(a.k);
+  const T* vp = static_cast<const T*>(a.v);
+
+  int64_t u = run.u0, seq = run.seq, before = run.before;
+  while (u < run.u1 && seq < a.nseq) {
+    const int len = paged_len(a, seq), n = paged_tiles(len);
+    if (n == 0) {
+      ++seq;
+      continue;
+    }
+    const int64_t r = u - before * heads;
+    const int head = static_cast<int>(r / n), t0 = static_cast<int>(r % n);
+    const int t1 = n - t0 < run.u1 - u ? n : t0 + static_cast<int>(run.u1 - u);
+    const int hk = head / groups, g0 = head % groups * HC, nh = G - g0 < HC ? G - g0 : HC;
+    const int64_t hq = static_cast<int64_t>(hk) * G + g0;
+
+    __syncthreads();  // the last run's readers are done
+    for (int i = threadIdx.x; i < HC * DV * 32; i += kAnyWarps * 32) {
+      const int h = i / (DV * 32), d = i % (DV * 32);
+      s_q[i] = h < nh && d < a.D ? to_f32(static_cast<const T*>(a.q)[seq * a.q_s + (hq + h) * a.q_h + d]) : 0.0f;
+    }
+    __syncthreads();
+
+    float m = -INFINITY, l = 0.0f, acc[HC][DV];
+#pragma unroll
+    for (int h = 0; h < HC; ++h)
+#pragma unroll
+      for (int i = 0; i < DV; ++i) acc[h][i] = 0.0f;
+    const int64_t end = static_cast<int64_t>(t1) * kPagedTile < len ? static_cast<int64_t>(t1) * kPagedTile : len;
+    for (int64_t tb = static_cast<int64_t>(t0) * kPagedTile + warp * NT; tb < end; tb += kAnyWarps * NT) {
+      int64_t at_k = -1, at_v = -1;
+      if (lane < NT && tb + lane < end) {
+        int slot;
+        const int64_t page = paged_slot(a, seq, static_cast<int>(tb + lane), &slot);
+        if (page >= 0) {
+          at_k = page * a.k_page + slot * a.k_token + hk * a.k_head;
+          at_v = page * a.v_page + slot * a.v_token + hk * a.v_head;
+        }
+      }
+      float kr[NT][DV], vr[NT][DV];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const int64_t ok = __shfl_sync(0xffffffffu, at_k, j), ov = __shfl_sync(0xffffffffu, at_v, j);
+#pragma unroll
+        for (int i = 0; i < DV; ++i) {
+          const bool in = ok >= 0 && lane + 32 * i < a.D;
+          kr[j][i] = in ? to_f32(kp[ok + lane + 32 * i]) : 0.0f;
+          vr[j][i] = in ? to_f32(vp[ov + lane + 32 * i]) : 0.0f;
+        }
+      }
+      float s[32];
+#pragma unroll
+      for (int h = 0; h < HC; ++h) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) s[j * HC + h] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < DV; ++i) {
+          const float qv = s_q[(h * DV + i) * 32 + lane];
+#pragma unroll
+          for (int j = 0; j < NT; ++j) s[j * HC + h] = fmaf(kr[j][i], qv, s[j * HC + h]);
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < o; ++i) {
+          const bool up = lane & o;
+          const float send = up ? s[i] : s[i + o], keep = up ? s[i + o] : s[i];
+          s[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+        }
+      const bool live = __shfl_sync(0xffffffffu, at_k, lane / HC) >= 0;
+      const float x = live ? s[0] * (a.scale * kLog2e) : -INFINITY;
+      float top = x;
+#pragma unroll
+      for (int o = HC; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      top = fmaxf(top, m);
+      const float mm = top == -INFINITY ? 0.0f : top;
+      const float p = exp2f(x - mm), down = exp2f(m - mm);
+      if (__any_sync(0xffffffffu, down != 1.0f)) {
+#pragma unroll
+        for (int h = 0; h < HC; ++h) {
+          const float f = __shfl_sync(0xffffffffu, down, h);
+#pragma unroll
+          for (int i = 0; i < DV; ++i) acc[h][i] *= f;
+        }
+      }
+      m = top;
+      l = l * down + p;
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int h = 0; h < HC; ++h) {
+          const float w = __shfl_sync(0xffffffffu, p, j * HC + h);
+#pragma unroll
+          for (int i = 0; i < DV; ++i) acc[h][i] = fmaf(w, vr[j][i], acc[h][i]);
+        }
+    }
+#pragma unroll
+    for (int o = HC; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (lane < HC) {
+      s_ml[warp][lane][0] = m;
+      s_ml[warp][lane][1] = l;
+    }
+    __syncthreads();
+    float top = -INFINITY, sum = 0.0f;
+    const int mine = lane % HC;
+#pragma unroll
+    for (int w = 0; w < kAnyWarps; ++w) top = fmaxf(top, s_ml[w][mine][0]);
+    const float mm = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+    for (int w = 0; w < kAnyWarps; ++w) sum += s_ml[w][mine][1] * exp2f(s_ml[w][mine][0] - mm);
+    const float f = exp2f(m - mm);
+#pragma unroll
+    for (int h = 0; h < HC; ++h) {
+      const float fh = __shfl_sync(0xffffffffu, f, h);
+#pragma unroll
+      for (int i = 0; i < DV; ++i) acc[h][i] *= fh;
+    }
+    // the warps' sums in a tree
+#pragma unroll
+    for (int half = kAnyWarps / 2; half > 0; half >>= 1) {
+      if (warp >= half && warp < 2 * half)
+#pragma unroll
+        for (int h = 0; h < HC; ++h)
+#pragma unroll
+          for (int i = 0; i < DV; ++i) s_acc[(((warp - half) * HC + h) * DV + i) * 32 + lane] = acc[h][i];
+      __syncthreads();
+      if (warp < half)
+#pragma unroll
+        for (int h = 0; h < HC; ++h)
+#pragma unroll
+          for (int i = 0; i < DV; ++i) acc[h][i] += s_acc[((warp * HC + h) * DV + i) * 32 + lane];
+      __syncthreads();
+    }
+    if (warp == 0) {
+      const bool whole = t0 == 0 && t1 == n;
+      const int st = paged_part_stride(a.D);
+      float* part = a.part + static_cast<int64_t>(blockIdx.x * 2 + (t0 == 0)) * HC * st;
+#pragma unroll
+      for (int h = 0; h < HC; ++h) {
+        const float lh = __shfl_sync(0xffffffffu, sum, h), th = __shfl_sync(0xffffffffu, top, h);
+        if (h < nh) {
+          T* o = static_cast<T*>(a.o) + seq * a.o_s + (hq + h) * a.o_h;
+#pragma unroll
+          for (int i = 0; i < DV; ++i)
+            if (lane + 32 * i < a.D) {
+              if (whole) o[lane + 32 * i] = from_f32<T>(acc[h][i] / lh);
+              else part[h * st + lane + 32 * i] = acc[h][i];
+            }
+          if (lane == 0) {
+            if (whole) {
+              if (a.lse) a.lse[seq * a.Hq + hq + h] = th * kLn2 + logf(lh);
+            } else {
+              part[h * st + st - 4] = th;
+              part[h * st + st - 3] = lh;
+            }
+          }
+        }
+      }
+    }
+    if (t0 > 0) rec.flags |= t1 == n ? 6 : 2;
+    if (t0 == 0 && t1 < n) {
+      rec.flags |= 1;
+      rec.seq = seq;
+      rec.head = head;
+    }
+    u += t1 - t0;
+    if (t1 == n && head == heads - 1) {
+      before += n;
+      ++seq;
+    }
+  }
+  if (threadIdx.x == 0) a.rec[blockIdx.x] = rec;
+}
+
+constexpr int kAnyCtas = 4;  // a SM
+
+template <typename T, int HC, int DV>
+cudaError_t launch_any(const PagedArgs& a, int sms, cudaStream_t s) {
+  static SmemLimit limit;
+  static_assert(kAnyCtas * 2 * HC <= kPagedSlots && kAnyCtas <= kPagedCtas, "workspace");
+  auto kern = paged_any_kernel<T, HC, DV>;
+  const int smem = 5 * HC * DV * 32 * static_cast<int>(sizeof(float));
+  if (cudaError_t e = limit.allow(kern, smem)) return e;
+  const int groups = (a.Hq / a.Hk + HC - 1) / HC;
+  kern<<<kAnyCtas * sms, kAnyWarps * 32, smem, s>>>(a, groups);
+  if (cudaError_t e = cudaGetLastError()) return e;
+  return launch_paged_join<T>(a, kAnyCtas * sms, HC, groups, s);
+}
+
+template <typename T, int HC>
+cudaError_t launch_any_width(const PagedArgs& a, int sms, cudaStream_t s) {
+  if (a.D <= 64) return launch_any<T, HC, 2>(a, sms, s);
+  if (a.D <= 128) return launch_any<T, HC, 4>(a, sms, s);
+  return launch_any<T, HC, 8>(a, sms, s);
+}
+
+template <typename T>
+cudaError_t launch_any_heads(const PagedArgs& a, int sms, cudaStream_t s) {
+  return a.Hq / a.Hk <= 4 ? launch_any_width<T, 4>(a, sms, s) : launch_any_width<T, 8>(a, sms, s);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_any(int dtype, const PagedArgs& a, int sms, cudaStream_t s) {
+  if (dtype == NF4_DTYPE_F32) return launch_any_heads<float>(a, sms, s);
+  if (dtype == NF4_DTYPE_F16) return launch_any_heads<__half>(a, sms, s);
+  return launch_any_heads<__nv_bfloat16>(a, sms, s);
+}
+
+cudaError_t launch_paged_append(int dtype, const PagedArgs& a, int sms, cudaStream_t s) {
+  const int e = dtype == NF4_DTYPE_F32 ? 4 : 2, wide = 16 / e;
+  const int64_t ld[] = {a.k_page, a.k_token, a.k_head, a.v_page, a.v_token, a.v_head, a.kn_t, a.kn_h, a.vn_t, a.vn_h, a.D};
+  const void* p[] = {a.k, a.v, a.k_new, a.v_new};
+  bool vec = true;
+  for (int64_t x : ld) vec = vec && x % wide == 0;
+  for (const void* x : p) vec = vec && reinterpret_cast<uintptr_t>(x) % 16 == 0;
+  const int rows = a.T >= 32 * static_cast<int64_t>(sms) ? 8 : 1;
+  const unsigned grid = static_cast<unsigned>((a.T + rows - 1) / rows);
+  if (vec)
+    paged_append_kernel<uint4><<<grid, kAppendThreads, 0, s>>>(a, rows, a.D / wide, wide);
+  else if (e == 4)
+    paged_append_kernel<uint32_t><<<grid, kAppendThreads, 0, s>>>(a, rows, a.D, 1);
+  else
+    paged_append_kernel<uint16_t><<<grid, kAppendThreads, 0, s>>>(a, rows, a.D, 1);
+  return cudaGetLastError();
+}
+
+}  // namespace nf4

@@ -1,0 +1,132 @@
+"""Torch-facing wrappers of the paged key-value cache of ``include/nf4.h``: new tokens written into
+their pages, and attention of one new token a sequence over them.
+
+As in ``ops``: PyTorch supplies device memory and the current stream, every step of the
+computation runs in the library's kernels, and there is no CPU path.
+"""
+from __future__ import annotations
+
+import functools
+import struct
+from typing import Optional
+
+import torch
+
+from . import _lib
+from .block_ops import _DTYPES, _dtype, _fn, _on, _one_device, _raw_stream, _share_storage, _workspace3, _written
+
+_CACHE = struct.Struct("@2P6qPqP2q5i4x")  # nf4_paged_cache
+
+
+def _explain_cache(name, k_pages, v_pages, page_table, lengths, rows):
+    """Why these are no cache with rows of its heads; rows: (what, tensor, heads or None)."""
+    _one_device(name, k_pages, v_pages, page_table, lengths, *(t for _, t, _ in rows))
+    _dtype(name, k_pages)
+    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype or 0 in k_pages.shape[1:]:
+        raise ValueError(f"{name}: k_pages and v_pages must be [pages, slots, heads, D] of one shape and dtype, got "
+                         f"{tuple(k_pages.shape)} {k_pages.dtype} and {tuple(v_pages.shape)} {v_pages.dtype}")
+    D = k_pages.shape[3]
+    for what, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        if D > 1 and t.stride(3) != 1:
+            raise ValueError(f"{name}: {what} must have unit stride within a head")
+    if lengths.dtype != torch.int32 or lengths.dim() != 1 or not lengths.is_contiguous():
+        raise ValueError(f"{name}: lengths must be a contiguous int32 [sequences] tensor")
+    if (page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != lengths.shape[0]
+            or (page_table.shape[1] > 1 and page_table.stride(1) != 1)):
+        raise ValueError(f"{name}: page_table must be an int32 [{lengths.shape[0]}, pages of a sequence] tensor with unit column stride")
+    for what, t, heads in rows:
+        if t.dim() != 3 or t.dtype != k_pages.dtype or t.shape[2] != D or (heads is not None and t.shape[1] != heads):
+            raise ValueError(f"{name}: {what} must be a {k_pages.dtype} [rows, {'heads' if heads is None else heads}, {D}] tensor, got "
+                             f"{t.dtype} {tuple(t.shape)}")
+        if D > 1 and t.stride(2) != 1:
+            raise ValueError(f"{name}: {what} must have unit stride within a head")
+
+
+def _cache(name, k_pages, v_pages, page_table, lengths, rows):
+    """The packed nf4_paged_cache of checked arguments."""
+    dt, dev, ks, kt, vt = k_pages.dtype, k_pages.device, k_pages.shape, k_pages.stride(), v_pages.stride()
+    n = lengths.shape[0] if lengths.dim() == 1 else -1
+    ok = (dt in _DTYPES and dev.type == "cuda" and len(ks) == 4 and v_pages.shape == ks and v_pages.dtype is dt and 0 not in ks[1:]
+          and v_pages.device == page_table.device == lengths.device == dev and (ks[3] == 1 or kt[3] == vt[3] == 1)
+          and lengths.dtype is torch.int32 and lengths.is_contiguous() and page_table.dtype is torch.int32 and page_table.dim() == 2
+          and page_table.shape[0] == n and (page_table.shape[1] < 2 or page_table.stride(1) == 1))
+    for _, t, heads in rows if ok else ():
+        ok = (ok and t.dtype is dt and t.device == dev and t.dim() == 3 and t.shape[2] == ks[3] and (heads is None or t.shape[1] == heads)
+              and (ks[3] == 1 or t.stride(2) == 1))
+    if not ok:
+        _explain_cache(name, k_pages, v_pages, page_table, lengths, rows)
+        raise ValueError(f"{name}: arguments do not make a paged cache")
+    return _CACHE.pack(k_pages.data_ptr(), v_pages.data_ptr(), kt[0], kt[1], kt[2], vt[0], vt[1], vt[2], page_table.data_ptr(),
+                       page_table.stride(0), lengths.data_ptr(), n, ks[0], page_table.shape[1], ks[1], ks[2], ks[3], _DTYPES[dt])
+
+
+@functools.lru_cache(maxsize=1024)
+def _slots_share(shape: tuple, stride: tuple) -> bool:
+    """Whether slots of pages [pages, slots, heads, D] may meet in memory (one dimension not inside another's steps)."""
+    reach = shape[3]
+    for step, n in sorted((s, n) for s, n in zip(stride[:3], shape[:3]) if n > 1):
+        if step < reach:
+            return True
+        reach += step * (n - 1)
+    return False
+
+
+def paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,
+                 lengths: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None) -> None:
+    """nf4_paged_append: writes new tokens' rows k, v [T, Hk, D] into the pages [pages, slots, Hk, D] (any strides whose
+    slots do not share storage: a transposed view of [pages, Hk, slots, D] will do).  Token t of sequence i lies in page
+    page_table[i, t // slots], slot t % slots.  `lengths` int32 [sequences] counts the new tokens already: rows
+    cu_seqlens[i] .. cu_seqlens[i + 1] - 1 are the last tokens of sequence i (a prompt or a chunk of one); without
+    cu_seqlens row i is the newest token of sequence i.  Rows of sequences of length 0, and rows whose page is missing
+    from the table (recorded in the device status), are not written."""
+    name = "paged_append"
+    Hk = k_pages.shape[2] if k_pages.dim() == 4 else -1
+    d = _cache(name, k_pages, v_pages, page_table, lengths, (("k", k, Hk), ("v", v, Hk)))
+    T, n, dev = k.shape[0], lengths.shape[0], k_pages.device
+    if v.shape[0] != T or (cu_seqlens is None and T != n):
+        raise ValueError(f"{name}: {T} and {v.shape[0]} rows of keys and values for {n} sequences")
+    cu = None
+    if cu_seqlens is not None:
+        cu = cu_seqlens.data_ptr()
+        if (cu_seqlens.dtype is not torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] != n + 1 or not cu_seqlens.is_contiguous()
+                or cu_seqlens.device != dev):
+            raise ValueError(f"{name}: cu_seqlens must be a contiguous int32 [{n + 1}] tensor on {dev}")
+    if _slots_share(k_pages.shape, k_pages.stride()) or _slots_share(v_pages.shape, v_pages.stride()):
+        raise ValueError(f"{name}: slots of the pages share storage")
+    kt, vt = k.stride(), v.stride()
+    with _on(dev):
+        rc = _fn("nf4_paged_append")(d, k.data_ptr(), kt[0], kt[1], v.data_ptr(), vt[0], vt[1], cu, T, _raw_stream(dev))
+    if rc:
+        _lib.check(rc, "nf4_paged_append")
+    _written((k_pages, v_pages))
+
+
+def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor, lengths: torch.Tensor,
+                    scale: Optional[float] = None, out: Optional[torch.Tensor] = None):
+    """nf4_paged_attention: attention of one query token a sequence, q [sequences, Hq, D] (any sequence and head strides),
+    over the lengths[i] tokens that page_table names for it (pages and table as in paged_append; the new token's own
+    keys and values are appended first).  Query head h reads key head h // (Hq // Hk); `scale` defaults to D ** -0.5.
+    Returns (o [sequences, Hq, D], lse fp32 [sequences, Hq]); a sequence of length 0 gives zeros and -inf.  `out` takes o in
+    place of a new tensor: any strides whose rows do not share storage.  Tables and lengths are read on the device, so a
+    captured graph follows them.  No gradients."""
+    name = "paged_attention"
+    d = _cache(name, k_pages, v_pages, page_table, lengths, (("q", q, None),) if out is None else (("q", q, None), ("out", out, None)))
+    n, Hq, D = q.shape
+    Hk, dev = k_pages.shape[2], q.device
+    if n != lengths.shape[0] or Hq == 0 or Hq % Hk:
+        raise ValueError(f"{name}: q {tuple(q.shape)} does not fit {lengths.shape[0]} sequences of {Hk} key heads")
+    if out is not None and (out.shape != q.shape or _share_storage(out)):
+        raise ValueError(f"{name}: out must have q's shape, and rows that do not share storage")
+    o = torch.empty((n, Hq, D), dtype=q.dtype, device=dev) if out is None else out
+    lse = torch.empty((n, Hq), dtype=torch.float32, device=dev)
+    qt, ot = q.stride(), o.stride()
+    with _on(dev):
+        need = _workspace3(_lib.OP_PAGED_ATTENTION, 0, 0, D, dev)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        rc = _fn("nf4_paged_attention")(d, q.data_ptr(), qt[0], qt[1], Hq, D ** -0.5 if scale is None else scale, o.data_ptr(), ot[0],
+                                        ot[1], lse.data_ptr(), ws.data_ptr(), need, _raw_stream(dev))
+    if rc:
+        _lib.check(rc, "nf4_paged_attention")
+    if out is not None:
+        _written((out,))
+    return o, lse

@@ -61,7 +61,7 @@ typedef enum {
   NF4_ERR_BOUNDS = 9             /* checked build: an in-kernel index check failed   */
 } nf4_status;
 
-enum { NF4_DTYPE_F32 = 0, NF4_DTYPE_BF16 = 1, NF4_DTYPE_F16 = 2 /* attention, norms, optimiser */ };
+enum { NF4_DTYPE_F32 = 0, NF4_DTYPE_BF16 = 1, NF4_DTYPE_F16 = 2 /* attention, norms, optimiser, cache, router */ };
 
 enum {
   NF4_OP_QUANTIZE = 0,
@@ -71,7 +71,9 @@ enum {
   NF4_OP_GROUPED_DGRAD = 4,
   NF4_OP_GROUPED_SWIGLU_BWD = 5, /* M = T rows, N = N_e, K; E experts */
   NF4_OP_NORM_RESIDUAL_BWD = 6,  /* M = T rows, N = H; K and E unused */
-  NF4_OP_ATTENTION_BWD = 7       /* M = T rows, N = Hq query heads; K and E unused */
+  NF4_OP_ATTENTION_BWD = 7,      /* M = T rows, N = Hq query heads; K and E unused */
+  NF4_OP_PAGED_ATTENTION = 8,    /* K = D; M, N and E unused */
+  NF4_OP_ROUTE = 9               /* M = T tokens, N = E experts; K and E unused */
 };
 
 /* Path counters (nf4_get_path_counters): how many launches each kernel got.
@@ -98,7 +100,11 @@ enum {
   NF4_PATH_ATTENTION_ANY = 17,/* the same for layouts the tensor-core kernels do not take */
   NF4_PATH_NORM_RESIDUAL = 18,/* gated residual norm, or its backward       */
   NF4_PATH_ADAMW = 19,       /* AdamW step, or the read-out of 8-bit states */
-  NF4_NUM_PATHS = 20
+  NF4_PATH_PAGED_APPEND = 20,/* new tokens written into the paged cache     */
+  NF4_PATH_PAGED_ATTENTION = 21,/* attention over the paged cache, tensor-core kernel */
+  NF4_PATH_PAGED_ATTENTION_ANY = 22,/* the same for what that kernel does not take */
+  NF4_PATH_ROUTE = 23,       /* router of the experts, or its backward     */
+  NF4_NUM_PATHS = 24
 };
 
 /* A quantised weight: the tensors of the pages' QuantState as plain device
@@ -472,6 +478,111 @@ nf4_status nf4_adamw_step(const nf4_adamw_tensor* tensors, int32_t count, int32_
 nf4_status nf4_adamw_state_values(const uint8_t* m, const uint8_t* v, const float* m_absmax, const float* v_absmax,
                                   const float* levels_m, const float* levels_v, int64_t n, float* out_m, float* out_v,
                                   void* stream);
+
+/* nf4_paged_append / nf4_paged_attention -- the key-value cache of decoding, in pages, and
+ * attention of one new token a sequence over it (the product calls at M <= 16 are the rest of
+ * such a step).
+ *   k, v        pages of `dtype`: slot t of page p holds head h's row of D values at
+ *               p * page + t * token + h * head (strides in elements, each tensor its own;
+ *               unit stride within a row), so that pages may hold whole tokens
+ *               ([pages][slots][Hk][D]), a head's tokens together ([pages][Hk][slots][D]),
+ *               or keys and values side by side.
+ *   table       DEVICE int32, row i (pitch ld_table) names the pages of sequence i in
+ *               order: its token t lies in page table[i][t / page_size], slot t % page_size.
+ *               Entries past a sequence's last page are not read.
+ *   lengths     DEVICE int32 [nseq], tokens of each sequence in the cache, the new ones
+ *               among them; 0 for an idle row of the batch.
+ * A length outside [0, max_pages * page_size] is clamped, a page outside [0, pages) is passed
+ * over (its tokens are not written, and have no weight); both are recorded as
+ * NF4_ERR_BAD_OFFSETS in the device status word.  Everything is read on the device when the
+ * kernels run, so a captured graph follows the tables and lengths of its replays.
+ *
+ * nf4_paged_append: rows cu_seqlens[i] .. cu_seqlens[i + 1] - 1 of k, v [T, Hk, D] (token and
+ * head strides) are the LAST tokens of sequence i: row r goes to position lengths[i] -
+ * cu_seqlens[i + 1] + r.  cu_seqlens DEVICE int32 [nseq + 1] ascending, or NULL: row i is the
+ * newest token of sequence i (T == nseq).  Rows of idle sequences and outside the offsets are
+ * not written; rows before a sequence's first token (more new rows than its length) are
+ * neither, and are recorded.  Nothing but the named slots is written; two rows must not share one.
+ *
+ * nf4_paged_attention: o_i = sum_t p_t v_t with p = softmax(scale q_i . k_t) over the
+ * lengths[i] tokens of sequence i; query head h reads key head h / (Hq / Hk).
+ *   q, o        [nseq, Hq, D] of `dtype`, sequence and head strides in elements.
+ *   lse         fp32 [nseq][Hq], natural log of the sum of exponentials, or NULL.
+ *   Idle rows: zeros, and lse -inf.  Slots past a sequence's length are never read.
+ *   ws: nf4_workspace_size(NF4_OP_PAGED_ATTENTION, 0, 0, D, 0) bytes, 16-byte aligned, of a
+ *   call's own (calls on two streams, or two graphs whose replays overlap, must not share it).
+ * Hq a multiple of Hk, 1 <= D <= 256.  fp32 sums and statistics; partial results over the
+ * length are added in a fixed order (deterministic for given lengths and device).  16-bit
+ * types with D a multiple of 8, 16-byte aligned pointers and strides of a multiple of 8
+ * elements run on the tensor cores, everything else in fp32 arithmetic. */
+typedef struct {
+  void* k;
+  void* v;
+  int64_t k_page, k_token, k_head, v_page, v_token, v_head;
+  const int32_t* table;
+  int64_t ld_table;
+  const int32_t* lengths;
+  int64_t nseq;
+  int64_t pages;
+  int32_t max_pages; /* entries of a table row */
+  int32_t page_size; /* slots of a page */
+  int32_t Hk, D;
+  int32_t dtype;
+} nf4_paged_cache;
+nf4_status nf4_paged_append(const nf4_paged_cache* c, const void* k, int64_t k_token, int64_t k_head, const void* v,
+                            int64_t v_token, int64_t v_head, const int32_t* cu_seqlens, int64_t T, void* stream);
+nf4_status nf4_paged_attention(const nf4_paged_cache* c, const void* q, int64_t q_seq, int64_t q_head, int32_t Hq,
+                               float scale, void* o, int64_t o_seq, int64_t o_head, float* lse, void* ws,
+                               size_t ws_bytes, void* stream);
+
+/* nf4_route_fwd / nf4_route_bwd -- the router before the grouped experts: the k experts of
+ * each token, their weights, and the tables that nf4_grouped_* and nf4_moe_combine take.
+ * Per token, with logits x [E]:
+ *   s = softmax(x) (NF4_SCORE_SOFTMAX) or 1 / (1 + exp(-x)) (NF4_SCORE_SIGMOID);
+ *   c = s + bias (bias fp32 [E], it moves the choice alone), or without bias x itself; an
+ *   expert of logit -inf comes after all others;
+ *   groups > 1: the experts form `groups` runs of E / groups; a run is worth its largest c
+ *   (group_top 1) or the sum of its two largest s + bias (group_top 2; -inf counts nothing
+ *   beside another); the top_groups best are kept;
+ *   the k largest c of the kept experts are chosen.  Everywhere equal ones go by the lower
+ *   index, and the order is that of the numbers themselves (candidates too near for fp32 are
+ *   compared in fp64).  NaN comes before all else.
+ *   weight = scale * s, or with renormalise scale * s / (sum of the chosen s).  A token
+ *   whose chosen logits are all -inf has weights 0.
+ *   logits   [T, E] of `dtype`, row pitch ld; live: uint8 [T] or NULL: tokens of live[t] ==
+ *            0 (padding of a batch) get no experts.
+ *   experts  int32 [T][k], ascending; -1 for a token that is not live.  weights fp32 [T][k].
+ * Tables (all or none of them NULL), for the (token, expert) pairs sorted by expert, then token:
+ *   offsets    int32 [E + 1]: rows offsets[e] .. offsets[e + 1] - 1 belong to expert e;
+ *   row_token  int32 [T k], row_weight fp32 [T k]: the token and the weight of each row; -1
+ *              and 0 from offsets[E] on;
+ *   token_rows int32 [T][k]: the row of each route, -1 for none.
+ * ws: nf4_workspace_size(NF4_OP_ROUTE, T, E, 0, 0) bytes, needed with tables.
+ * 1 <= E <= 512, 1 <= k <= 32 and k <= top_groups * (E / groups), groups <= 32.
+ *
+ * nf4_route_bwd: g_logits [T, E] (pitch ld_g, of `dtype`) from g_weights [T][k] and / or
+ * g_rows [T k] (the gradient of row_weight, through token_rows), either NULL.  The choice has
+ * no gradient, nor has bias.  d, experts and token_rows are the forward's (of d it reads
+ * logits, T, E, k, dtype, score, renormalise and scale).  Deterministic: no atomics whose
+ * order shows. */
+enum { NF4_SCORE_SOFTMAX = 0, NF4_SCORE_SIGMOID = 1 };
+typedef struct {
+  const void* logits;
+  int64_t ld;
+  int64_t T;
+  const float* bias;
+  const uint8_t* live;
+  int32_t E, k;
+  int32_t dtype;
+  int32_t score;
+  int32_t groups, top_groups, group_top;
+  int32_t renormalise;
+  float scale;
+} nf4_route;
+nf4_status nf4_route_fwd(const nf4_route* d, int32_t* experts, float* weights, int32_t* offsets, int32_t* row_token,
+                         int32_t* token_rows, float* row_weight, void* ws, size_t ws_bytes, void* stream);
+nf4_status nf4_route_bwd(const nf4_route* d, const int32_t* experts, const int32_t* token_rows, const float* g_weights,
+                         const float* g_rows, void* g_logits, int64_t ld_g, void* stream);
 
 /* nf4_linear_fwd_noalloc -- the forward of nf4_linear_fwd without a workspace
  * argument, for callers that cannot allocate device memory themselves (for

@@ -1,0 +1,188 @@
+"""The router and the paged cache together with the operators that they stand beside: a trained mixture-of-experts layer,
+and a decoding step of a whole block, against plain torch over the same dequantised weights."""
+import math
+
+import pytest
+import torch
+
+import bit_nf4_quantized_linear_gb300 as nf4
+from tests.helpers import ELEM, REL_FRO
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF16 = torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    import __graft_entry__
+    __graft_entry__.build()
+    nf4.device_status(clear=True)
+    yield
+    assert nf4.device_status() == 0
+
+
+def gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return lambda *shape: torch.randn(*shape, generator=g, device=DEV)
+
+
+def near(got, want, what, stages):
+    """Each stage of bf16 products is held to the products' own bounds, REL_FRO in all and ELEM by element."""
+    got, want = got.double(), want.double()
+    assert torch.isfinite(got).all(), what
+    assert (got - want).norm() <= stages * REL_FRO * want.norm(), (what, ((got - want).norm() / want.norm()).item())
+    assert ((got - want).abs() <= stages * ELEM * (want.abs() + want.square().mean().sqrt())).all(), what
+
+
+class Experts:
+    """E experts of hidden H and intermediate I, quantised; and their dense values."""
+
+    def __init__(self, E, H, I, seed):
+        n = gen(seed)
+        gate, up, down = 0.05 * n(E * I, H), 0.05 * n(E * I, H), 0.05 * n(E * H, I)
+        self.E, self.I = E, I
+        self.gate_up = nf4.quantize(nf4.interleave_gate_up(gate, up, E))
+        self.down = nf4.quantize(down)
+        gu = nf4.dequantize(self.gate_up).view(E, I // 64, 2, 64, H)
+        self.dense = [gu[:, :, i].reshape(E, I, H).double() for i in range(2)] + [nf4.dequantize(self.down).view(E, H, I).double()]
+
+    def layer(self, x, r):
+        """The layer as nf4_route's documentation gives it."""
+        h = nf4.nf4_grouped_swiglu(nf4.nf4_dispatch(x, r.token_rows), r.offsets, self.gate_up, self.E, r.row_weight)
+        return nf4.nf4_combine(nf4.nf4_grouped(h, r.offsets, self.down, self.E), r.token_rows)
+
+    def plain(self, x, experts, weights):
+        """In float64, with the routes given; -1 for none."""
+        gate, up, down = self.dense
+        y = torch.zeros_like(x)
+        for e in range(self.E):
+            t, j = (experts == e).nonzero(as_tuple=True)
+            if t.numel():
+                h = torch.nn.functional.silu(x[t] @ gate[e].T) * (x[t] @ up[e].T) * weights[t, j][:, None]
+                y = y.index_add(0, t, h @ down[e].T)
+        return y
+
+
+@pytest.mark.parametrize("T,pad", [(1, 0), (48, 0), (300, 37)])
+@pytest.mark.parametrize("renormalise", [False, True])
+def test_moe_layer_with_gradients(T, pad, renormalise):
+    """Router, dispatch, grouped experts and combine: output and the gradients of activations and router weights."""
+    E, H, I, k = 16, 256, 128, 4
+    ex = Experts(E, H, I, T)
+    n = gen(T + 1)
+    x, wr = n(T, H).to(BF16).requires_grad_(), (0.1 * n(E, H)).requires_grad_()
+    live = torch.arange(T, device=DEV) < T - pad
+    gy = n(T, H).to(BF16) * live[:, None]
+    r = nf4.nf4_route(x.float() @ wr.T, k, renormalise=renormalise, live=live)
+    y = ex.layer(x, r)
+    gx, gw = torch.autograd.grad(y, (x, wr), gy)
+    xd, wd = x.detach().double().requires_grad_(), wr.detach().double().requires_grad_()
+    logits = xd @ wd.T
+    held = r.experts.clamp(min=0).long()
+    w = torch.softmax(logits, 1).gather(1, held)
+    w = (w / w.sum(1, keepdim=True) if renormalise else w) * live[:, None]
+    want = ex.plain(xd, r.experts, w)
+    wx, ww = torch.autograd.grad(want, (xd, wd), gy.double())
+    assert (y[~live] == 0).all() and (gx[~live] == 0).all()
+    near(y, want, "y", 3)
+    near(gx, wx, "gx", 5)
+    near(gw, ww, "gw", 5)
+
+
+def test_moe_route_tables_are_those_of_route_rows():
+    x = gen(3)(130, 32)
+    r = nf4.route_experts(x, 4)
+    assert torch.equal(r.token_rows, nf4.route_rows(r.row_token, 130, 4))
+
+
+def test_decoding_steps_of_a_block():
+    """A prompt through the prompt attention with its keys appended, then steps of one token for three sequences and an idle
+    one, captured in a graph: norm, fused q, k, v, append, paged attention, output projection, norm, experts."""
+    H, heads, kv, D, E, I, k, B, page = 256, 8, 2, 64, 8, 128, 2, 4, 16
+    n = gen(0)
+    ex = Experts(E, H, I, 1)
+    dense = [0.06 * n(r, H) for r in (heads * D, kv * D, kv * D)] + [0.05 * n(H, heads * D)]
+    ws = [nf4.quantize(w) for w in dense]
+    wd = [nf4.dequantize(w).double() for w in ws]
+    gain1, gain2, wr = 1 + 0.1 * n(H), 1 + 0.1 * n(H), 0.1 * n(E, H)
+    prompts, steps = [37, 0, 5, 64], 20
+    lens = [m + (steps if m else 0) for m in prompts]
+    need = [-(-m // page) for m in lens]
+    table = torch.full((B, max(need)), -1, dtype=torch.int32)
+    ids = torch.randperm(sum(need), generator=torch.Generator().manual_seed(1)).int()
+    at = 0
+    for i, m in enumerate(need):
+        table[i, :m], at = ids[at:at + m], at + m
+    table = table.to(DEV)
+    kp, vp = (torch.full((sum(need), page, kv, D), math.nan, dtype=BF16, device=DEV) for _ in range(2))
+    lengths = torch.tensor(prompts, dtype=torch.int32, device=DEV)
+    live = lengths > 0
+
+    def block(x, attend):
+        stream, h = nf4.nf4_norm_residual(x, w_pre=gain1)
+        q, key, val = (t.view(x.shape[0], -1, D) for t in nf4.linear_fwd_multi([h] * 3, ws[:3]))
+        stream, h = nf4.nf4_norm_residual(nf4.linear_fwd(attend(q, key, val).flatten(1), ws[3]), stream, w_pre=gain2)
+        return stream, h
+
+    def experts(stream, h, live=None):
+        r = nf4.route_experts(h.float() @ wr.T, k, renormalise=True, live=live)
+        return stream + ex.layer(h, r), r
+
+    # the prompts, packed
+    cu = torch.tensor([sum(prompts[:i]) for i in range(B + 1)], dtype=torch.int32, device=DEV)
+    xp = n(sum(prompts), H).to(BF16)
+    kept = {}
+
+    def attend_prompt(q, key, val):
+        nf4.paged_append(key, val, kp, vp, table, lengths, cu)
+        return nf4.nf4_attention(q, key, val, cu)
+
+    yp, _ = experts(*block(xp, attend_prompt))
+    assert torch.isfinite(yp).all()
+
+    x = torch.zeros(B, H, dtype=BF16, device=DEV)
+
+    def attend_token(q, key, val):
+        nf4.paged_append(key, val, kp, vp, table, lengths)
+        kept["q"] = q
+        return nf4.paged_attention(q, kp, vp, table, lengths)[0]
+
+    def step():
+        stream, h = block(x, attend_token)
+        y, r = experts(stream, h, live)
+        return y, r
+
+    lengths += live.int()
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, r = step()
+    lengths -= live.int()
+
+    history = [xp[cu[i]:cu[i + 1]].double() for i in range(B)]
+
+    def norm(t, gain):
+        return t * torch.rsqrt(t.square().mean(-1, keepdim=True) + 1e-6) * gain.double()
+
+    for s in range(steps):
+        lengths += live.int()
+        x.copy_(gen(100 + s)(B, H))
+        graph.replay()
+        for i in range(B):
+            if not live[i]:
+                continue
+            history[i] = torch.cat([history[i], x[i:i + 1].double()])
+            if s % 7:
+                continue
+            h = norm(history[i], gain1)
+            q, key, val = (h @ w.T for w in wd[:3])
+            q, key, val = q[-1].view(heads, D), *(t.view(-1, kv, D).repeat_interleave(heads // kv, 1) for t in (key, val))
+            p = torch.softmax(torch.einsum("hd,lhd->hl", q, key) / math.sqrt(D), 1)
+            stream = x[i].double() + torch.einsum("hl,lhd->hd", p, val).flatten() @ wd[3].T
+            want = stream + ex.plain(norm(stream, gain2)[None], r.experts[i:i + 1], r.weights[i:i + 1].double())[0]
+            near(y[i], want, f"step {s}, sequence {i}", 4)
+        assert torch.equal(r.experts[1], torch.full_like(r.experts[1], -1)) and torch.isfinite(y).all()
+    assert lengths.tolist() == lens
