@@ -179,6 +179,7 @@ inline size_t paged_ws_bytes(int D, int sms) {
   return static_cast<size_t>(sms) * (kPagedSlots * paged_part_stride(D) * sizeof(float) + kPagedCtas * sizeof(PagedRec));
 }
 cudaError_t launch_paged_append(int dtype, const PagedArgs& a, int sms, cudaStream_t s);
+cudaError_t launch_paged_mma(bool f16, const PagedArgs& a, int sms, cudaStream_t s);
 cudaError_t launch_paged_any(int dtype, const PagedArgs& a, int sms, cudaStream_t s);
 
 // The router of the experts (nf4_route_fwd / nf4_route_bwd).

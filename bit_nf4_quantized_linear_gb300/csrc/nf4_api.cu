@@ -1144,6 +1144,14 @@ nf4_status nf4_paged_attention(const nf4_paged_cache* c, const void* q, int64_t 
   a.rec = static_cast<nf4::PagedRec*>(ws);
   a.part = reinterpret_cast<float*>(a.rec + nf4::kPagedCtas * dev.sms);
   a.status = dev.status;
+  const auto vec = [](int64_t page, int64_t token, int64_t head) { return page % 8 == 0 && token % 8 == 0 && head % 8 == 0; };
+  if (dev.supported && c->dtype != NF4_DTYPE_F32 && a.D % 8 == 0 && aligned16(a.k) && aligned16(a.v) && vec_heads(q, q_seq, q_head) &&
+      vec_heads(o, o_seq, o_head) && vec(a.k_page, a.k_token, a.k_head) && vec(a.v_page, a.v_token, a.v_head)) {
+    cudaError_t le = nf4::launch_paged_mma(c->dtype == NF4_DTYPE_F16, a, dev.sms, static_cast<cudaStream_t>(stream));
+    if (le != cudaSuccess) return cuda_fail(le, "kernel launch");
+    count(NF4_PATH_PAGED_ATTENTION);
+    return NF4_OK;
+  }
   cudaError_t le = nf4::launch_paged_any(c->dtype, a, dev.sms, static_cast<cudaStream_t>(stream));
   if (le != cudaSuccess) return cuda_fail(le, "kernel launch");
   count(NF4_PATH_PAGED_ATTENTION_ANY);

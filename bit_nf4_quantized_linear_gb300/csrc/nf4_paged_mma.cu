@@ -1,0 +1,411 @@
+// nf4_paged_mma.cu -- attention of one query token a sequence over the paged cache, 16-bit
+// types, on the tensor cores (nf4_paged_attention).
+//
+// The query heads of one key head are the narrow side of two products: S' = K Q' (16 tokens x
+// 8 heads an MMA) and O' += V' P' (16 columns x 8 heads), so a group of up to 8 heads wastes
+// nothing of the key and value rows, which are read once.  Bound by HBM: 2 D values a token
+// and key head against 4 D operations a query head; mma.sync's rate is some ten times what
+// that needs, and its operands come from shared memory as the copies left them.
+//
+// A CTA of four warps takes its run of units (paged_common.cuh) 64 tokens at a time, 16 a
+// warp.  Each warp streams its tokens' rows through a ring of its own with 16-byte
+// asynchronous copies (a table look-up a token, so any page size and order), over the borders
+// of sequences and heads, with no barrier in the loop: the warps meet only where a (sequence,
+// head group) ends, to add their sums.  Rows past a length are zeros that no copy reads.
+// S is fp32; P is held as two values of the operands' type, p and what its rounding left (a
+// second MMA that costs nothing here), so the result sees one rounding, its own.  fp16 weights
+// are held times 2^7, out of the subnormal range.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <type_traits>
+
+#include "elem.cuh"
+#include "internal.h"
+#include "paged_common.cuh"
+#include "sm100_ptx.cuh"
+#include "smem_limit.h"
+
+namespace nf4 {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kRows = kPagedTile / kWarps;  // tokens of a warp's tile
+static_assert(kRows == 16, "the MMA's rows");
+
+template <int DM>
+struct Geo {
+  static constexpr int kStages = DM == 64 ? 6 : 3;
+  static constexpr int kCtas = DM <= 128 ? 2 : 1;   // a SM
+  static constexpr int kHalf = kRows * DM * 2;      // bytes of a tile's keys
+  static constexpr int kStage = 2 * kHalf;
+  static constexpr int kPitch = DM + 4;             // floats between heads of a warp's sums
+  static constexpr int kRing = kWarps * kStages * kStage;
+  static constexpr int kSums = kWarps * 8 * kPitch * 4;
+  static constexpr int kSmem = kRing + kSums + kWarps * 8 * 8 + kWarps * kStages * 4;
+};
+
+// Columns of 8 values stored XOR-swizzled by row, so that the eight rows of an 8 x 8 matrix
+// lie in different banks.
+template <int DM>
+__device__ __forceinline__ uint32_t at_chunk(int row, int chunk) {
+  return static_cast<uint32_t>(row * DM * 2 + ((chunk ^ (row & 7)) << 4));
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+template <bool F16>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (F16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Weights a and b as two values each of the operands' type: what the type holds of them (cut,
+// not rounded), and the rest, never negative and never 0 beside a first part, so that an
+// infinite value times the weight is that infinity and not 0 x inf.
+template <bool F16>
+__device__ __forceinline__ void split2(float a, float b, uint32_t* hi, uint32_t* lo) {
+  if constexpr (F16) {
+    constexpr float least = 5.9604645e-8f;  // 2^-24, of weights up to 2^7
+    asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(*hi) : "f"(b), "f"(a));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(hi));
+    const float ra = f.x > 0.0f ? fmaxf(a - f.x, least) : a - f.x, rb = f.y > 0.0f ? fmaxf(b - f.y, least) : b - f.y;
+    const __half2 l = __floats2half2_rn(ra, rb);
+    *lo = *reinterpret_cast<const uint32_t*>(&l);
+  } else {
+    constexpr float least = 1.1754944e-38f;
+    const uint32_t ua = __float_as_uint(a) & 0xffff0000u, ub = __float_as_uint(b) & 0xffff0000u;
+    *hi = ua >> 16 | ub;
+    const __nv_bfloat162 l = __floats2bfloat162_rn(fmaxf(a - __uint_as_float(ua), least), fmaxf(b - __uint_as_float(ub), least));
+    *lo = *reinterpret_cast<const uint32_t*>(&l);
+  }
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// The units of a run, one after another.
+struct Walk {
+  int64_t seq, left;  // sequence; units left in the run, this one among them
+  int len, tiles, head, tile;
+
+  // The next unit with tokens; `heads` a tile.
+  __device__ __forceinline__ void next(const PagedArgs& a, int heads) {
+    --left;
+    if (++tile < tiles) return;
+    tile = 0;
+    if (++head < heads || left <= 0) return;
+    head = 0;
+    do {
+      ++seq;
+      len = seq < a.nseq ? paged_len(a, seq) : 1;
+      tiles = paged_tiles(len);
+    } while (tiles == 0);
+  }
+};
+
+template <bool F16, int DM, int NT>
+__global__ void __launch_bounds__(kThreads, Geo<DM>::kCtas) paged_mma_kernel(PagedArgs a, int groups) {
+  using G = Geo<DM>;
+  using T = typename std::conditional<F16, __half, __nv_bfloat16>::type;
+  constexpr int HC = 8 * NT, KS = DM / 16, CH = DM / 8;
+  constexpr float kShift = F16 ? 7.0f : 0.0f;
+  extern __shared__ __align__(128) unsigned char dyn[];
+  float* s_sum = reinterpret_cast<float*>(dyn + G::kRing);                          // [kWarps][8][kPitch]
+  float2* s_ml = reinterpret_cast<float2*>(dyn + G::kRing + G::kSums);              // [kWarps][8]
+  uint32_t* s_valid = reinterpret_cast<uint32_t*>(s_ml + kWarps * 8);              // [kWarps][kStages]
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t ring = nf4ptx::smem_addr(dyn) + warp * G::kStages * G::kStage;
+  s_valid += warp * G::kStages;
+  paged_allow_join();
+  paged_empty<T>(a);
+  const int heads = a.Hk * groups, GQ = a.Hq / a.Hk;
+  const PagedRun run = paged_run(a, heads, reinterpret_cast<int64_t*>(s_sum));
+  PagedRec rec{0, 0, 0};
+
+  if (run.u0 < run.u1) {
+    Walk load;
+    load.seq = run.seq;
+    load.left = run.u1 - run.u0;
+    load.len = paged_len(a, run.seq);
+    load.tiles = paged_tiles(load.len);
+    const int64_t r0 = run.u0 - run.before * heads;
+    load.head = static_cast<int>(r0 / load.tiles);
+    load.tile = static_cast<int>(r0 % load.tiles);
+    Walk use = load;
+
+    // Starts the copies of this warp's tokens of the unit `load` into ring slot `st`.
+    auto start_copies = [&](int st) {
+      const int tok0 = load.tile * kPagedTile + warp * kRows;
+      if (load.left > 0 && tok0 < load.len) {
+        // lane i < 16 looks up the key row of token i, lane 16 + i its value row
+        const int tok = tok0 + (lane & 15), hk = load.head / groups;
+        int64_t at = 0;
+        bool ok = false;
+        if (tok < load.len) {
+          int slot;
+          const int64_t page = paged_slot(a, load.seq, tok, &slot);
+          ok = page >= 0;
+          if (ok)
+            at = lane < 16 ? page * a.k_page + slot * a.k_token + hk * a.k_head
+                           : page * a.v_page + slot * a.v_token + hk * a.v_head;
+        }
+        const unsigned valid = __ballot_sync(0xffffffffu, ok) & 0xffffu;
+        if (lane == 0) s_valid[st] = valid;
+        const uint32_t to = ring + st * G::kStage;
+        constexpr int kPer = 32 / CH;  // rows of one copy instruction of the warp
+#pragma unroll
+        for (int i = 0; i < kRows / kPer; ++i) {
+          const int r = i * kPer + lane / CH, c = lane % CH;
+          const int64_t ak = __shfl_sync(0xffffffffu, at, r), av = __shfl_sync(0xffffffffu, at, r + 16);
+          const int bytes = (valid >> r & 1) && c * 8 < a.D ? 16 : 0;
+          const T* kp = bytes ? static_cast<const T*>(a.k) + ak + c * 8 : static_cast<const T*>(a.q);
+          const T* vp = bytes ? static_cast<const T*>(a.v) + av + c * 8 : static_cast<const T*>(a.q);
+          copy16(to + at_chunk<DM>(r, c), kp, bytes);
+          copy16(to + G::kHalf + at_chunk<DM>(r, c), vp, bytes);
+        }
+      }
+      copies_commit();
+    };
+
+    uint32_t qf[NT][KS][2];
+    float acc[NT][KS][4], m[NT][2], l[NT][2];
+    const float c = a.scale * kLog2e;
+    int tile0 = use.tile;  // where the part of this (sequence, head group) begins
+    bool fresh = true;
+#pragma unroll
+    for (int i = 0; i < G::kStages; ++i) {
+      start_copies(i);
+      if (load.left > 0) load.next(a, heads);
+    }
+    int st = 0;
+    while (use.left > 0) {
+      const int hk = use.head / groups, g0 = use.head % groups * HC;
+      const int64_t hq = static_cast<int64_t>(hk) * GQ + g0;
+      if (fresh) {  // queries of a new (sequence, head group) as the right operand, 16 columns a step
+        fresh = false;
+        tile0 = use.tile;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const int h = n * 8 + lane / 4;
+          const T* q = static_cast<const T*>(a.q) + use.seq * a.q_s + (hq + h) * a.q_h;
+#pragma unroll
+          for (int s = 0; s < KS; ++s)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int d = s * 16 + j * 8 + (lane & 3) * 2;
+              qf[n][s][j] = g0 + h < GQ && d < a.D ? *reinterpret_cast<const uint32_t*>(q + d) : 0u;
+            }
+          m[n][0] = m[n][1] = -INFINITY;
+          l[n][0] = l[n][1] = 0.0f;
+#pragma unroll
+          for (int s = 0; s < KS; ++s)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[n][s][j] = 0.0f;
+        }
+      }
+      copies_wait<G::kStages - 1>();
+      __syncwarp();
+      if (use.tile * kPagedTile + warp * kRows < use.len) {
+        const uint32_t from = ring + st * G::kStage;
+        const unsigned valid = s_valid[st];
+        float x[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) x[n][0] = x[n][1] = x[n][2] = x[n][3] = 0.0f;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          uint32_t kf[4];
+          ldsm(kf, from + at_chunk<DM>(lane & 15, 2 * s + (lane >> 4)));
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma<F16>(x[n], kf, qf[n][s][0], qf[n][s][1]);
+        }
+        uint32_t hi[NT][2], lo[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          // x: tokens lane / 4 and lane / 4 + 8, heads 2 (lane % 4) and the next
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            x[n][j] *= c;
+            if (!(valid >> (lane / 4 + (j & 2) * 4) & 1)) x[n][j] = -INFINITY;
+          }
+          float t0 = fmaxf(x[n][0], x[n][2]), t1 = fmaxf(x[n][1], x[n][3]);
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) {
+            t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, o));
+            t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, o));
+          }
+          if (__any_sync(0xffffffffu, t0 > m[n][0] || t1 > m[n][1])) {
+            t0 = fmaxf(t0, m[n][0]);
+            t1 = fmaxf(t1, m[n][1]);
+            const float f0 = t0 == -INFINITY ? 1.0f : exp2_fast(m[n][0] - t0), f1 = t1 == -INFINITY ? 1.0f : exp2_fast(m[n][1] - t1);
+            m[n][0] = t0;
+            m[n][1] = t1;
+            l[n][0] *= f0;
+            l[n][1] *= f1;
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+              acc[n][s][0] *= f0;
+              acc[n][s][1] *= f1;
+              acc[n][s][2] *= f0;
+              acc[n][s][3] *= f1;
+            }
+          }
+          const float b0 = m[n][0] == -INFINITY ? 0.0f : m[n][0] - kShift, b1 = m[n][1] == -INFINITY ? 0.0f : m[n][1] - kShift;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[n][j] = exp2_fast(x[n][j] - (j & 1 ? b1 : b0));
+          l[n][0] += x[n][0] + x[n][2];
+          l[n][1] += x[n][1] + x[n][3];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            split2<F16>(x[n][2 * j], x[n][2 * j + 1], &hi[n][j], &lo[n][j]);
+            hi[n][j] = transpose8(hi[n][j]);
+            lo[n][j] = transpose8(lo[n][j]);
+          }
+        }
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          uint32_t vf[4];
+          ldsm_t(vf, from + G::kHalf + at_chunk<DM>((lane & 7) + (lane >> 4 << 3), 2 * s + (lane >> 3 & 1)));
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma<F16>(acc[n][s], vf, hi[n][0], hi[n][1]);
+            mma<F16>(acc[n][s], vf, lo[n][0], lo[n][1]);
+          }
+        }
+      }
+      __syncwarp();
+      start_copies(st);
+      if (load.left > 0) load.next(a, heads);
+      st = st + 1 == G::kStages ? 0 : st + 1;
+
+      const bool ends = use.tile + 1 == use.tiles;
+      if (ends || use.left == 1) {  // add the warps' sums
+        const bool whole = ends && tile0 == 0;
+        const int stride = paged_part_stride(a.D);
+        float* part = a.part + static_cast<int64_t>(blockIdx.x * 2 + (tile0 == 0)) * HC * stride;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) {
+            l[n][0] += __shfl_xor_sync(0xffffffffu, l[n][0], o);
+            l[n][1] += __shfl_xor_sync(0xffffffffu, l[n][1], o);
+          }
+          if (lane < 4)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) s_ml[warp * 8 + lane * 2 + j] = make_float2(m[n][j] - kShift, l[n][j]);
+          float* own = s_sum + warp * 8 * G::kPitch + (lane & 3) * 2 * G::kPitch + lane / 4;
+#pragma unroll
+          for (int s = 0; s < KS; ++s)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) own[(j & 1) * G::kPitch + s * 16 + (j & 2) * 4] = acc[n][s][j];
+          __syncthreads();
+#pragma unroll 1
+          for (int i = threadIdx.x; i < 8 * DM; i += kThreads) {
+            const int h = i / DM, d = i % DM, hn = n * 8 + h;
+            if (g0 + hn >= GQ) break;
+            float top = -INFINITY, sum = 0.0f, v = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w * 8 + h].x);
+            const float mm = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+              const float2 ml = s_ml[w * 8 + h];
+              const float f = exp2f(ml.x - mm);
+              sum += ml.y * f;
+              v += s_sum[(w * 8 + h) * G::kPitch + d] * f;
+            }
+            if (d < a.D) {
+              if (whole) static_cast<T*>(a.o)[use.seq * a.o_s + (hq + hn) * a.o_h + d] = from_f32<T>(v / sum);
+              else part[hn * stride + d] = v;
+            }
+            if (d == 0) {
+              if (whole) {
+                if (a.lse) a.lse[use.seq * a.Hq + hq + hn] = top * kLn2 + logf(sum);
+              } else {
+                part[hn * stride + stride - 4] = top;
+                part[hn * stride + stride - 3] = sum;
+              }
+            }
+          }
+          __syncthreads();
+        }
+        if (tile0 > 0) rec.flags |= ends ? 6 : 2;
+        if (tile0 == 0 && !ends) {
+          rec.flags |= 1;
+          rec.seq = use.seq;
+          rec.head = use.head;
+        }
+        fresh = true;
+      }
+      use.next(a, heads);
+    }
+    copies_wait<0>();
+  }
+  if (threadIdx.x == 0) a.rec[blockIdx.x] = rec;
+}
+
+template <bool F16, int DM, int NT>
+cudaError_t launch(const PagedArgs& a, int sms, cudaStream_t s) {
+  using G = Geo<DM>;
+  static SmemLimit limit;
+  static_assert(G::kCtas * 2 * 8 * NT <= kPagedSlots && G::kCtas <= kPagedCtas, "workspace");
+  auto kern = paged_mma_kernel<F16, DM, NT>;
+  if (cudaError_t e = limit.allow(kern, G::kSmem)) return e;
+  const int groups = (a.Hq / a.Hk + 8 * NT - 1) / (8 * NT), ctas = G::kCtas * sms;
+  kern<<<ctas, kThreads, G::kSmem, s>>>(a, groups);
+  if (cudaError_t e = cudaGetLastError()) return e;
+  return launch_paged_join<typename std::conditional<F16, __half, __nv_bfloat16>::type>(a, ctas, 8 * NT, groups, s);
+}
+
+template <bool F16>
+cudaError_t launch_width(const PagedArgs& a, int sms, cudaStream_t s) {
+  const bool wide = a.Hq / a.Hk > 8;  // 16 heads a group: the rows are read half as often
+  if (a.D <= 64) return wide ? launch<F16, 64, 2>(a, sms, s) : launch<F16, 64, 1>(a, sms, s);
+  if (a.D <= 128) return wide ? launch<F16, 128, 2>(a, sms, s) : launch<F16, 128, 1>(a, sms, s);
+  return launch<F16, 256, 1>(a, sms, s);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_mma(bool f16, const PagedArgs& a, int sms, cudaStream_t s) {
+  return f16 ? launch_width<true>(a, sms, s) : launch_width<false>(a, sms, s);
+}
+
+}  // namespace nf4
