@@ -159,6 +159,7 @@ struct PagedArgs {
   int64_t pages, nseq, ld_table, T;
   const int32_t *table, *lengths, *cu_seqlens;
   int max_pages, page_size, Hq, Hk, D;
+  unsigned page_mul, page_shift;  // p / page_size = p * page_mul >> page_shift for p < 2^31
   float scale;
   float* part;  // partial results [CTAs][2][heads of a unit][paged_part_stride(D)]
   struct PagedRec* rec;  // [CTAs]

@@ -1053,6 +1053,12 @@ nf4_status paged_args(const nf4_paged_cache* c, nf4::PagedArgs* a) {
   a->pages = c->pages;
   a->max_pages = c->max_pages;
   a->page_size = c->page_size;
+  // with 2^s >= page_size and mul = ceil(2^(31 + s) / page_size), p mul / 2^(31 + s) exceeds p / page_size by
+  // less than p / 2^31 / page_size < 1 / page_size
+  unsigned s = 0;
+  while ((int64_t{1} << s) < c->page_size) ++s;
+  a->page_shift = 31 + s;
+  a->page_mul = static_cast<unsigned>(((uint64_t{1} << (31 + s)) + static_cast<unsigned>(c->page_size) - 1) / static_cast<unsigned>(c->page_size));
   a->Hk = c->Hk;
   a->D = c->D;
   return NF4_OK;

@@ -49,6 +49,8 @@ __device__ __forceinline__ int append_place(const PagedArgs& a, int64_t r, int* 
 template <typename V>
 __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(PagedArgs a, int rows, int per_head, int elems) {
   __shared__ int64_t s_k[32], s_v[32];
+  grid_allow();
+  grid_wait();
   if (a.cu_seqlens && blockIdx.x == 0 && a.status) {
     bool bad = threadIdx.x == 0 && (a.cu_seqlens[0] < 0 || a.cu_seqlens[a.nseq] > a.T);
     for (int64_t i = threadIdx.x; i < a.nseq; i += kAppendThreads) bad |= a.cu_seqlens[i + 1] < a.cu_seqlens[i];
@@ -92,10 +94,11 @@ __global__ void __launch_bounds__(kAnyWarps * 32) paged_any_kernel(PagedArgs a, 
   extern __shared__ float dyn[];
   float* s_q = dyn;                     // [HC][DV * 32]
   float* s_acc = dyn + HC * DV * 32;    // [4][HC][DV * 32]
-  __shared__ int64_t s_red[34];
+  __shared__ int64_t s_red[68];
   __shared__ float s_ml[kAnyWarps][HC][2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  paged_allow_join();
+  grid_allow();
+  grid_wait();
   paged_empty<T>(a);
   const int heads = a.Hk * groups, G = a.Hq / a.Hk;
   PagedRun run = paged_run(a, heads, s_red);
@@ -111,7 +114,7 @@ __global__ void __launch_bounds__(kAnyWarps * 32) paged_any_kernel(PagedArgs a, 
       continue;
     }
     const int64_t r = u - before * heads;
-    const int head = static_cast<int>(r / n), t0 = static_cast<int>(r % n);
+    const int head = static_cast<int>(divide(r, n)), t0 = static_cast<int>(r - static_cast<int64_t>(head) * n);
     const int t1 = n - t0 < run.u1 - u ? n : t0 + static_cast<int>(run.u1 - u);
     const int hk = head / groups, g0 = head % groups * HC, nh = G - g0 < HC ? G - g0 : HC;
     const int64_t hq = static_cast<int64_t>(hk) * G + g0;
@@ -275,7 +278,7 @@ __global__ void __launch_bounds__(kAnyWarps * 32) paged_any_kernel(PagedArgs a, 
   if (threadIdx.x == 0) a.rec[blockIdx.x] = rec;
 }
 
-constexpr int kAnyCtas = 4;  // a SM
+constexpr int kAnyCtas = 2;  // a SM: what the registers leave room for
 
 template <typename T, int HC, int DV>
 cudaError_t launch_any(const PagedArgs& a, int sms, cudaStream_t s) {
@@ -285,8 +288,7 @@ cudaError_t launch_any(const PagedArgs& a, int sms, cudaStream_t s) {
   const int smem = 5 * HC * DV * 32 * static_cast<int>(sizeof(float));
   if (cudaError_t e = limit.allow(kern, smem)) return e;
   const int groups = (a.Hq / a.Hk + HC - 1) / HC;
-  kern<<<kAnyCtas * sms, kAnyWarps * 32, smem, s>>>(a, groups);
-  if (cudaError_t e = cudaGetLastError()) return e;
+  if (cudaError_t e = launch_early(kern, dim3(static_cast<unsigned>(kAnyCtas * sms)), kAnyWarps * 32, smem, s, a, groups)) return e;
   return launch_paged_join<T>(a, kAnyCtas * sms, HC, groups, s);
 }
 
@@ -319,13 +321,9 @@ cudaError_t launch_paged_append(int dtype, const PagedArgs& a, int sms, cudaStre
   for (const void* x : p) vec = vec && reinterpret_cast<uintptr_t>(x) % 16 == 0;
   const int rows = a.T >= 32 * static_cast<int64_t>(sms) ? 8 : 1;
   const unsigned grid = static_cast<unsigned>((a.T + rows - 1) / rows);
-  if (vec)
-    paged_append_kernel<uint4><<<grid, kAppendThreads, 0, s>>>(a, rows, a.D / wide, wide);
-  else if (e == 4)
-    paged_append_kernel<uint32_t><<<grid, kAppendThreads, 0, s>>>(a, rows, a.D, 1);
-  else
-    paged_append_kernel<uint16_t><<<grid, kAppendThreads, 0, s>>>(a, rows, a.D, 1);
-  return cudaGetLastError();
+  if (vec) return launch_early(paged_append_kernel<uint4>, dim3(grid), kAppendThreads, 0, s, a, rows, a.D / wide, wide);
+  if (e == 4) return launch_early(paged_append_kernel<uint32_t>, dim3(grid), kAppendThreads, 0, s, a, rows, a.D, 1);
+  return launch_early(paged_append_kernel<uint16_t>, dim3(grid), kAppendThreads, 0, s, a, rows, a.D, 1);
 }
 
 }  // namespace nf4

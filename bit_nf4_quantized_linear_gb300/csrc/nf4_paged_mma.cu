@@ -123,7 +123,8 @@ __device__ __forceinline__ float exp2_fast(float x) {
 
 // The units of a run, one after another.
 struct Walk {
-  int64_t seq, left;  // sequence; units left in the run, this one among them
+  int64_t seq;
+  int left;  // units left in the run, this one among them (2^31 would be days of work)
   int len, tiles, head, tile;
 
   // The next unit with tokens; `heads` a tile.
@@ -154,7 +155,8 @@ __global__ void __launch_bounds__(kThreads, Geo<DM>::kCtas) paged_mma_kernel(Pag
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t ring = nf4ptx::smem_addr(dyn) + warp * G::kStages * G::kStage;
   s_valid += warp * G::kStages;
-  paged_allow_join();
+  grid_allow();
+  grid_wait();
   paged_empty<T>(a);
   const int heads = a.Hk * groups, GQ = a.Hq / a.Hk;
   const PagedRun run = paged_run(a, heads, reinterpret_cast<int64_t*>(s_sum));
@@ -163,44 +165,87 @@ __global__ void __launch_bounds__(kThreads, Geo<DM>::kCtas) paged_mma_kernel(Pag
   if (run.u0 < run.u1) {
     Walk load;
     load.seq = run.seq;
-    load.left = run.u1 - run.u0;
+    load.left = static_cast<int>(run.u1 - run.u0 < INT32_MAX ? run.u1 - run.u0 : INT32_MAX);
     load.len = paged_len(a, run.seq);
     load.tiles = paged_tiles(load.len);
     const int64_t r0 = run.u0 - run.before * heads;
-    load.head = static_cast<int>(r0 / load.tiles);
-    load.tile = static_cast<int>(r0 % load.tiles);
+    load.head = static_cast<int>(divide(r0, load.tiles));
+    load.tile = static_cast<int>(r0 - static_cast<int64_t>(load.head) * load.tiles);
     Walk use = load;
 
-    // Starts the copies of this warp's tokens of the unit `load` into ring slot `st`.
+    // Starts the copies of this warp's tokens of the unit `load` into ring slot `st`.  Lane i
+    // copies column group i % CH of rows i / CH and every kPer-th after it.
+    constexpr int kPer = 32 / CH;
+    const int row0 = lane / CH, col = lane % CH * 8;
+    const bool in = col < a.D;
+    const bool whole_pages = a.page_size % kRows == 0;  // a tile lies in one page
+    const uint32_t dst0 = ring + at_chunk<DM>(row0, lane % CH);
     auto start_copies = [&](int st) {
-      const int tok0 = load.tile * kPagedTile + warp * kRows;
-      if (load.left > 0 && tok0 < load.len) {
-        // lane i < 16 looks up the key row of token i, lane 16 + i its value row
-        const int tok = tok0 + (lane & 15), hk = load.head / groups;
-        int64_t at = 0;
-        bool ok = false;
-        if (tok < load.len) {
+      const int tok0 = load.tile * kPagedTile + warp * kRows, rows = load.len - tok0, hk = groups == 1 ? load.head : load.head / groups;
+      if (load.left > 0 && rows > 0) {
+        const uint32_t to = dst0 + st * G::kStage;
+        // a row's swizzle repeats after eight rows
+        auto dst = [&](int i) {
+          return kPer >= 8 || (i * kPer) % 8 == 0 ? to + i * kPer * DM * 2 : (to ^ ((i * kPer) % 8 << 4)) + i * kPer * DM * 2;
+        };
+        unsigned valid;
+        if (whole_pages) {
           int slot;
-          const int64_t page = paged_slot(a, load.seq, tok, &slot);
-          ok = page >= 0;
-          if (ok)
-            at = lane < 16 ? page * a.k_page + slot * a.k_token + hk * a.k_head
-                           : page * a.v_page + slot * a.v_token + hk * a.v_head;
-        }
-        const unsigned valid = __ballot_sync(0xffffffffu, ok) & 0xffffu;
-        if (lane == 0) s_valid[st] = valid;
-        const uint32_t to = ring + st * G::kStage;
-        constexpr int kPer = 32 / CH;  // rows of one copy instruction of the warp
+          const int64_t page = paged_slot(a, load.seq, tok0, &slot);
+          const int n = page < 0 ? 0 : rows;
+          valid = n >= kRows ? 0xffffu : (1u << n) - 1u;
+          const T* kp = static_cast<const T*>(a.q);
+          const T* vp = kp;
+          int64_t ks = 0, vs = 0;
+          if (in && page >= 0) {
+            kp = static_cast<const T*>(a.k) + (page * a.k_page + (slot + row0) * a.k_token + hk * a.k_head + col);
+            vp = static_cast<const T*>(a.v) + (page * a.v_page + (slot + row0) * a.v_token + hk * a.v_head + col);
+            ks = kPer * a.k_token;
+            vs = kPer * a.v_token;
+          }
+          if (n >= kRows) {
+            const int bytes = in ? 16 : 0;
 #pragma unroll
-        for (int i = 0; i < kRows / kPer; ++i) {
-          const int r = i * kPer + lane / CH, c = lane % CH;
-          const int64_t ak = __shfl_sync(0xffffffffu, at, r), av = __shfl_sync(0xffffffffu, at, r + 16);
-          const int bytes = (valid >> r & 1) && c * 8 < a.D ? 16 : 0;
-          const T* kp = bytes ? static_cast<const T*>(a.k) + ak + c * 8 : static_cast<const T*>(a.q);
-          const T* vp = bytes ? static_cast<const T*>(a.v) + av + c * 8 : static_cast<const T*>(a.q);
-          copy16(to + at_chunk<DM>(r, c), kp, bytes);
-          copy16(to + G::kHalf + at_chunk<DM>(r, c), vp, bytes);
+            for (int i = 0; i < kRows / kPer; ++i) {
+              copy16(dst(i), kp, bytes);
+              copy16(dst(i) + G::kHalf, vp, bytes);
+              kp += ks;
+              vp += vs;
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < kRows / kPer; ++i) {
+              const bool row = in && i * kPer + row0 < n;
+              copy16(dst(i), row ? kp : static_cast<const T*>(a.q), row ? 16 : 0);
+              copy16(dst(i) + G::kHalf, row ? vp : static_cast<const T*>(a.q), row ? 16 : 0);
+              kp += ks;
+              vp += vs;
+            }
+          }
+        } else {
+          // lane i < 16 looks up the key row of token i, lane 16 + i its value row
+          const int tok = tok0 + (lane & 15);
+          int64_t at = 0;
+          bool ok = false;
+          if (tok < load.len) {
+            int slot;
+            const int64_t page = paged_slot(a, load.seq, tok, &slot);
+            ok = page >= 0;
+            if (ok)
+              at = lane < 16 ? page * a.k_page + slot * a.k_token + hk * a.k_head
+                             : page * a.v_page + slot * a.v_token + hk * a.v_head;
+          }
+          valid = __ballot_sync(0xffffffffu, ok) & 0xffffu;
+#pragma unroll
+          for (int i = 0; i < kRows / kPer; ++i) {
+            const int r = i * kPer + row0;
+            const int64_t ak = __shfl_sync(0xffffffffu, at, r), av = __shfl_sync(0xffffffffu, at, r + 16);
+            const int bytes = (valid >> r & 1) && in ? 16 : 0;
+            copy16(dst(i), bytes ? static_cast<const T*>(a.k) + ak + col : static_cast<const T*>(a.q), bytes);
+            copy16(dst(i) + G::kHalf, bytes ? static_cast<const T*>(a.v) + av + col : static_cast<const T*>(a.q), bytes);
+          }
         }
+        if (lane == 0) s_valid[st] = valid;
       }
       copies_commit();
     };
@@ -208,63 +253,76 @@ __global__ void __launch_bounds__(kThreads, Geo<DM>::kCtas) paged_mma_kernel(Pag
     uint32_t qf[NT][KS][2];
     float acc[NT][KS][4], m[NT][2], l[NT][2];
     const float c = a.scale * kLog2e;
+    // Offsets of the ldmatrix rows in a tile: the swizzle repeats after four steps of two chunks.
+    constexpr int KO = KS < 4 ? KS : 4;
+    uint32_t k_off[KO], v_off[KO];
+#pragma unroll
+    for (int s = 0; s < KO; ++s) {
+      k_off[s] = ring + at_chunk<DM>(lane & 15, 2 * s + (lane >> 4));
+      v_off[s] = ring + G::kHalf + at_chunk<DM>((lane & 7) + (lane >> 4 << 3), 2 * s + (lane >> 3 & 1));
+    }
     int tile0 = use.tile;  // where the part of this (sequence, head group) begins
-    bool fresh = true;
+    // The queries of the unit `use` as the right operand, 16 columns a step.
+    auto fetch_queries = [&]() {
+      const int hk = groups == 1 ? use.head : use.head / groups, g0 = (use.head - hk * groups) * HC;
+      const T* q = static_cast<const T*>(a.q) + use.seq * a.q_s + (static_cast<int64_t>(hk) * GQ + g0 + lane / 4) * a.q_h + (lane & 3) * 2;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int d = s * 16 + j * 8;
+            qf[n][s][j] = g0 + n * 8 + lane / 4 < GQ && d < a.D ? *reinterpret_cast<const uint32_t*>(q + n * 8 * a.q_h + d) : 0u;
+          }
+    };
+    auto clear_sums = [&]() {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        m[n][0] = m[n][1] = -INFINITY;
+        l[n][0] = l[n][1] = 0.0f;
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[n][s][j] = 0.0f;
+      }
+    };
 #pragma unroll
     for (int i = 0; i < G::kStages; ++i) {
       start_copies(i);
       if (load.left > 0) load.next(a, heads);
     }
+    fetch_queries();
+    clear_sums();
     int st = 0;
     while (use.left > 0) {
-      const int hk = use.head / groups, g0 = use.head % groups * HC;
-      const int64_t hq = static_cast<int64_t>(hk) * GQ + g0;
-      if (fresh) {  // queries of a new (sequence, head group) as the right operand, 16 columns a step
-        fresh = false;
-        tile0 = use.tile;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const int h = n * 8 + lane / 4;
-          const T* q = static_cast<const T*>(a.q) + use.seq * a.q_s + (hq + h) * a.q_h;
-#pragma unroll
-          for (int s = 0; s < KS; ++s)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const int d = s * 16 + j * 8 + (lane & 3) * 2;
-              qf[n][s][j] = g0 + h < GQ && d < a.D ? *reinterpret_cast<const uint32_t*>(q + d) : 0u;
-            }
-          m[n][0] = m[n][1] = -INFINITY;
-          l[n][0] = l[n][1] = 0.0f;
-#pragma unroll
-          for (int s = 0; s < KS; ++s)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[n][s][j] = 0.0f;
-        }
-      }
       copies_wait<G::kStages - 1>();
       __syncwarp();
       if (use.tile * kPagedTile + warp * kRows < use.len) {
-        const uint32_t from = ring + st * G::kStage;
+        const uint32_t from = st * G::kStage;
         const unsigned valid = s_valid[st];
-        float x[NT][4];
+        float x[NT][4], x2[NT][4];  // two chains of MMAs
 #pragma unroll
-        for (int n = 0; n < NT; ++n) x[n][0] = x[n][1] = x[n][2] = x[n][3] = 0.0f;
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[n][j] = x2[n][j] = 0.0f;
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
           uint32_t kf[4];
-          ldsm(kf, from + at_chunk<DM>(lane & 15, 2 * s + (lane >> 4)));
+          ldsm(kf, k_off[s % KO] + from + s / KO * 128);
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma<F16>(x[n], kf, qf[n][s][0], qf[n][s][1]);
+          for (int n = 0; n < NT; ++n) mma<F16>(s & 1 ? x2[n] : x[n], kf, qf[n][s][0], qf[n][s][1]);
         }
         uint32_t hi[NT][2], lo[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           // x: tokens lane / 4 and lane / 4 + 8, heads 2 (lane % 4) and the next
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            x[n][j] *= c;
-            if (!(valid >> (lane / 4 + (j & 2) * 4) & 1)) x[n][j] = -INFINITY;
-          }
+          for (int j = 0; j < 4; ++j) x[n][j] = (x[n][j] + x2[n][j]) * c;
+          if (valid != 0xffffu)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (!(valid >> (lane / 4 + (j & 2) * 4) & 1)) x[n][j] = -INFINITY;
           float t0 = fmaxf(x[n][0], x[n][2]), t1 = fmaxf(x[n][1], x[n][3]);
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) {
@@ -302,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, Geo<DM>::kCtas) paged_mma_kernel(Pag
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
           uint32_t vf[4];
-          ldsm_t(vf, from + G::kHalf + at_chunk<DM>((lane & 7) + (lane >> 4 << 3), 2 * s + (lane >> 3 & 1)));
+          ldsm_t(vf, v_off[s % KO] + from + s / KO * 128);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             mma<F16>(acc[n][s], vf, hi[n][0], hi[n][1]);
@@ -316,65 +374,92 @@ __global__ void __launch_bounds__(kThreads, Geo<DM>::kCtas) paged_mma_kernel(Pag
       st = st + 1 == G::kStages ? 0 : st + 1;
 
       const bool ends = use.tile + 1 == use.tiles;
-      if (ends || use.left == 1) {  // add the warps' sums
-        const bool whole = ends && tile0 == 0;
-        const int stride = paged_part_stride(a.D);
-        float* part = a.part + static_cast<int64_t>(blockIdx.x * 2 + (tile0 == 0)) * HC * stride;
+      if (!ends && use.left > 1) {
+        use.next(a, heads);
+        continue;
+      }
+      // The part of this (sequence, head group) is done: add the warps' sums.  The next one's
+      // queries are fetched meanwhile.
+      const Walk was = use;
+      use.next(a, heads);
+      if (use.left > 0) fetch_queries();
+      const int hk = groups == 1 ? was.head : was.head / groups, g0 = (was.head - hk * groups) * HC;
+      const bool whole = ends && tile0 == 0;
+      const int stride = paged_part_stride(a.D);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+      for (int n = 0; n < NT; ++n) {
 #pragma unroll
-          for (int o = 4; o < 32; o <<= 1) {
-            l[n][0] += __shfl_xor_sync(0xffffffffu, l[n][0], o);
-            l[n][1] += __shfl_xor_sync(0xffffffffu, l[n][1], o);
+        for (int o = 4; o < 32; o <<= 1) {
+          l[n][0] += __shfl_xor_sync(0xffffffffu, l[n][0], o);
+          l[n][1] += __shfl_xor_sync(0xffffffffu, l[n][1], o);
+        }
+        if (lane < 4)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) s_ml[warp * 8 + lane * 2 + j] = make_float2(m[n][j] - kShift, l[n][j]);
+        float* own = s_sum + warp * 8 * G::kPitch + (lane & 3) * 2 * G::kPitch + lane / 4;
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) own[(j & 1) * G::kPitch + s * 16 + (j & 2) * 4] = acc[n][s][j];
+        __syncthreads();
+        // 16 threads a head, four columns at a time
+        const int h = threadIdx.x >> 4, hn = n * 8 + h;
+        if (g0 + hn < GQ) {
+          float top = -INFINITY, sum = 0.0f, f[kWarps];
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w * 8 + h].x);
+          const float mm = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) {
+            const float2 ml = s_ml[w * 8 + h];
+            f[w] = exp2_fast(ml.x - mm);
+            sum += ml.y * f[w];
           }
-          if (lane < 4)
+          const float inv = whole ? 1.0f / sum : 1.0f;
+          const int64_t hq = static_cast<int64_t>(hk) * GQ + g0 + hn;
+          T* o = static_cast<T*>(a.o) + was.seq * a.o_s + hq * a.o_h;
+          float* part = a.part + (static_cast<int64_t>(blockIdx.x * 2 + (tile0 == 0)) * HC + hn) * stride;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) s_ml[warp * 8 + lane * 2 + j] = make_float2(m[n][j] - kShift, l[n][j]);
-          float* own = s_sum + warp * 8 * G::kPitch + (lane & 3) * 2 * G::kPitch + lane / 4;
-#pragma unroll
-          for (int s = 0; s < KS; ++s)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) own[(j & 1) * G::kPitch + s * 16 + (j & 2) * 4] = acc[n][s][j];
-          __syncthreads();
-#pragma unroll 1
-          for (int i = threadIdx.x; i < 8 * DM; i += kThreads) {
-            const int h = i / DM, d = i % DM, hn = n * 8 + h;
-            if (g0 + hn >= GQ) break;
-            float top = -INFINITY, sum = 0.0f, v = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w * 8 + h].x);
-            const float mm = top == -INFINITY ? 0.0f : top;
+          for (int i = 0; i < DM / 64; ++i) {
+            const int d = i * 64 + (threadIdx.x & 15) * 4;
+            float v[4] = {};
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-              const float2 ml = s_ml[w * 8 + h];
-              const float f = exp2f(ml.x - mm);
-              sum += ml.y * f;
-              v += s_sum[(w * 8 + h) * G::kPitch + d] * f;
+              const float4 x = *reinterpret_cast<const float4*>(s_sum + (w * 8 + h) * G::kPitch + d);
+              v[0] += x.x * f[w];
+              v[1] += x.y * f[w];
+              v[2] += x.z * f[w];
+              v[3] += x.w * f[w];
             }
-            if (d < a.D) {
-              if (whole) static_cast<T*>(a.o)[use.seq * a.o_s + (hq + hn) * a.o_h + d] = from_f32<T>(v / sum);
-              else part[hn * stride + d] = v;
-            }
-            if (d == 0) {
-              if (whole) {
-                if (a.lse) a.lse[use.seq * a.Hq + hq + hn] = top * kLn2 + logf(sum);
-              } else {
-                part[hn * stride + stride - 4] = top;
-                part[hn * stride + stride - 3] = sum;
-              }
+            if (d >= a.D) break;  // D is a multiple of 8
+            if (whole) {
+              __align__(8) T r[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) r[j] = from_f32<T>(v[j] * inv);
+              *reinterpret_cast<uint2*>(o + d) = *reinterpret_cast<const uint2*>(r);
+            } else {
+              *reinterpret_cast<float4*>(part + d) = make_float4(v[0], v[1], v[2], v[3]);
             }
           }
-          __syncthreads();
+          if ((threadIdx.x & 15) == 0) {
+            if (whole) {
+              if (a.lse) a.lse[was.seq * a.Hq + hq] = top * kLn2 + logf(sum);
+            } else {
+              part[stride - 4] = top;
+              part[stride - 3] = sum;
+            }
+          }
         }
-        if (tile0 > 0) rec.flags |= ends ? 6 : 2;
-        if (tile0 == 0 && !ends) {
-          rec.flags |= 1;
-          rec.seq = use.seq;
-          rec.head = use.head;
-        }
-        fresh = true;
+        __syncthreads();
       }
-      use.next(a, heads);
+      if (tile0 > 0) rec.flags |= ends ? 6 : 2;
+      if (tile0 == 0 && !ends) {
+        rec.flags |= 1;
+        rec.seq = was.seq;
+        rec.head = was.head;
+      }
+      tile0 = use.tile;
+      clear_sums();
     }
     copies_wait<0>();
   }
@@ -389,8 +474,7 @@ cudaError_t launch(const PagedArgs& a, int sms, cudaStream_t s) {
   auto kern = paged_mma_kernel<F16, DM, NT>;
   if (cudaError_t e = limit.allow(kern, G::kSmem)) return e;
   const int groups = (a.Hq / a.Hk + 8 * NT - 1) / (8 * NT), ctas = G::kCtas * sms;
-  kern<<<ctas, kThreads, G::kSmem, s>>>(a, groups);
-  if (cudaError_t e = cudaGetLastError()) return e;
+  if (cudaError_t e = launch_early(kern, dim3(static_cast<unsigned>(ctas)), kThreads, G::kSmem, s, a, groups)) return e;
   return launch_paged_join<typename std::conditional<F16, __half, __nv_bfloat16>::type>(a, ctas, 8 * NT, groups, s);
 }
 

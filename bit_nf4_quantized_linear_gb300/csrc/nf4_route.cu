@@ -98,7 +98,7 @@ __device__ __forceinline__ int group_of(int e, float inv) { return static_cast<i
 // The largest, or the sum of the two largest, of a group's `size` values; -inf counts nothing
 // beside another.  Lanes start at different values of their groups (bank conflicts).
 template <typename F>
-__device__ __forceinline__ F group_worth(const F* v, int size, int top, int lane) {
+__device__ __forceinline__ F group_worth(const F* v, int size, int top, int lane, F* least) {
   F a = -INFINITY, b = -INFINITY;
   bool nan = false;
   int j = lane % size;
@@ -109,8 +109,33 @@ __device__ __forceinline__ F group_worth(const F* v, int size, int top, int lane
     a = x > a ? x : a;
     j = j + 1 == size ? 0 : j + 1;
   }
+  *least = top == 2 ? b : a;  // the smallest that counts
   if (nan) return static_cast<F>(NAN);
   return top == 2 && b > -INFINITY ? a + b : a;
+}
+
+// fp64 values, in row[e], of the experts whose bit i (expert i * 32 + lane) is set: s + bias
+// for sigmoid scores; for softmax without bias exp(x - top), in the order of s and of sums of s.
+// Their indices are listed in `list`; returns how many they are.
+template <typename T, int V>
+__device__ __noinline__ int evaluate(const RouteArgs& a, int64_t t, unsigned mask, float top, double* row, uint16_t* list) {
+  const int lane = threadIdx.x & 31;
+  int n = 0;
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const unsigned all = __ballot_sync(kAll, mask >> i & 1);
+    if (mask >> i & 1) list[n + __popc(all & ((1u << lane) - 1u))] = static_cast<uint16_t>(i * 32 + lane);
+    n += __popc(all);
+  }
+  __syncwarp();
+  for (int i = lane; i < n; i += 32) {
+    const int e = list[i];
+    const double x = to_f32(static_cast<const T*>(a.logits)[t * a.ld + e]);
+    row[e] = a.sigmoid ? 1.0 / (1.0 + exp(-x)) + (a.bias ? static_cast<double>(a.bias[e]) : 0.0) : exp(x - static_cast<double>(top));
+  }
+  __syncwarp();
+  return n;
 }
 
 // The choice of token t in fp64.
@@ -128,30 +153,27 @@ __device__ __noinline__ unsigned choose_exactly(const RouteArgs& a, int64_t t, d
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmax(top, __shfl_xor_sync(kAll, top, o));
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = i * 32 + lane;
-      if (e < a.E) sum += exp(static_cast<double>(to_f32(x[e])) - top);
-    }
-    sum = warp_sum64(sum);
   }
   uint64_t key[V];
   __syncwarp();
-#pragma unroll 1
-  for (int i = 0; i < V; ++i) {
-    const int e = i * 32 + lane;
-    if (e >= a.E) continue;
+  for (int e = lane; e < a.E; e += 32) {
     const double xe = to_f32(x[e]);
-    double c = xe;
-    if (scores && xe > -INFINITY)
-      c = (a.sigmoid ? 1.0 / (1.0 + exp(-xe)) : exp(xe - top) / sum) + (a.bias ? static_cast<double>(a.bias[e]) : 0.0);
-    row[e] = c;
+    row[e] = !scores ? xe : a.sigmoid ? 1.0 / (1.0 + exp(-xe)) : exp(xe - top);
+    sum += row[e];
+  }
+  if (scores) {
+    sum = warp_sum64(sum);
+    for (int e = lane; e < a.E; e += 32) {
+      const double c = (a.sigmoid ? row[e] : row[e] / sum) + (a.bias ? static_cast<double>(a.bias[e]) : 0.0);
+      row[e] = to_f32(x[e]) == -INFINITY ? -INFINITY : c;
+    }
   }
   __syncwarp();
   unsigned kept = kAll;
   const int size = a.E / a.groups;
   if (a.groups > 1) {
-    uint64_t best[1] = {lane < a.groups ? key_of(group_worth(row + lane * size, size, a.group_top, lane)) : 0};
+    double least;
+    uint64_t best[1] = {lane < a.groups ? key_of(group_worth(row + lane * size, size, a.group_top, lane, &least)) : 0};
     uint64_t last;
     kept = __ballot_sync(kAll, take_largest(best, a.top_groups, &last));
   }
@@ -169,7 +191,7 @@ __device__ __noinline__ unsigned choose_exactly(const RouteArgs& a, int64_t t, d
 // Routes token t: bit i of the result is set where this lane's expert i * 32 + lane is chosen,
 // and w[i] is its weight.
 template <typename T, int V>
-__device__ __forceinline__ unsigned route_token(const RouteArgs& a, int64_t t, double* row, float (&w)[V]) {
+__device__ __forceinline__ unsigned route_token(const RouteArgs& a, int64_t t, double* row, uint16_t* list, float (&w)[V]) {
   const int lane = threadIdx.x & 31;
   const T* xr = static_cast<const T*>(a.logits) + t * a.ld;
   float x[V], s[V];
@@ -220,12 +242,12 @@ __device__ __forceinline__ unsigned route_token(const RouteArgs& a, int64_t t, d
       }
     }
     unsure = __any_sync(kAll, nan);
-    // Bounds on the error of c.  Sigmoid: exponential, sum and quotient, 8 units of 2^-24 of a
-    // value below 1.  Softmax: the rounding of x - top (as d exp(-d) <= 0.4 units), and 24
+    // Bounds on the error of c.  Sigmoid: with an exponential of two roundings' error, a sum and
+    // a quotient, (4 s (1 - s) + 2 s) units of 2^-24, less than 4.  Softmax: the rounding of x - top (as d exp(-d) <= 0.4 units), and 24
     // units of s for exponential, row sum and quotient; s is at most 1 / sum.  And c's own
     // rounding.
     constexpr float u = 5.9604645e-8f;
-    const float off = (a.sigmoid ? 8.0f * u : u * (1.0f + 24.0f * norm)) + u * __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(cmax)));
+    const float off = (a.sigmoid ? 4.0f * u : u * (1.0f + 24.0f * norm)) + u * __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(cmax)));
     const int size = a.E / a.groups;
     if (grouped && !unsure) {
       float* r32 = reinterpret_cast<float*>(row);
@@ -234,12 +256,39 @@ __device__ __forceinline__ unsigned route_token(const RouteArgs& a, int64_t t, d
       for (int i = 0; i < V; ++i)
         if (i * 32 + lane < a.E) r32[i * 32 + lane] = c[i];
       __syncwarp();
-      const float f = lane < a.groups ? group_worth(r32 + lane * size, size, a.group_top, lane) : -INFINITY;
+      float least = -INFINITY;
+      const float f = lane < a.groups ? group_worth(r32 + lane * size, size, a.group_top, lane, &least) : -INFINITY;
       uint32_t best[1] = {lane < a.groups ? key_of(f) : 0}, last;
-      const unsigned kept = __ballot_sync(kAll, take_largest(best, a.top_groups, &last));
+      unsigned kept = __ballot_sync(kAll, take_largest(best, a.top_groups, &last));
       if (inexact) {  // two values a group: twice the bound each way, and the roundings of the sum and of low - far
         const float low = value_of(last), far = 10.0f * off;
-        unsure = __popc(__ballot_sync(kAll, lane < a.groups && !(f < low - far))) != a.top_groups;
+        const bool sure = lane < a.groups && f > low + far;
+        const unsigned near = __ballot_sync(kAll, lane < a.groups && !sure && !(f < low - far)), safe = __ballot_sync(kAll, sure);
+        if (__popc(near) + __popc(safe) != a.top_groups) {
+          if (!a.sigmoid && a.bias) {
+            unsure = true;
+          } else {  // the values that can count in the groups near the border
+            const float inv = 1.0f / size;
+            unsigned mask = 0;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+              const int g = group_of(min(i * 32 + lane, a.E - 1), inv);
+              const float from = __shfl_sync(kAll, least, g) - 4.0f * off;
+              mask |= (i * 32 + lane < a.E && x[i] > -INFINITY && (near >> g & 1) && !(c[i] < from)) << i;
+            }
+            const int n = evaluate<T, V>(a, t, mask, top, row, list);
+            double one = -INFINITY, two = -INFINITY;
+            for (int j = 0; j < n; ++j) {
+              const double v = row[list[j]];
+              if (group_of(list[j], inv) != lane) continue;
+              two = v > one ? one : (v > two ? v : two);
+              one = v > one ? v : one;
+            }
+            const double worth = a.group_top == 2 && two > -INFINITY ? one + two : one;
+            uint64_t wide[1] = {near >> lane & 1 ? key_of(worth) : 0}, border;
+            kept = safe | __ballot_sync(kAll, take_largest(wide, a.top_groups - __popc(safe), &border));
+          }
+        }
       }
       const float inv = 1.0f / size;
 #pragma unroll
@@ -258,10 +307,25 @@ __device__ __forceinline__ unsigned route_token(const RouteArgs& a, int64_t t, d
       chosen = take_largest(key, a.k, &last);
       if (a.bias) {
         const float low = value_of(last), far = 3.0f * off;  // the bound each way, and the rounding of low - far
-        int near = 0;
+        unsigned near = 0, safe = 0;
 #pragma unroll
-        for (int i = 0; i < V; ++i) near += (open >> i & 1) && !(c[i] < low - far);
-        unsure = __reduce_add_sync(kAll, near) != a.k;
+        for (int i = 0; i < V; ++i) {
+          const bool sure = c[i] > low + far;
+          safe |= ((open >> i & 1) && sure) << i;
+          near |= ((open >> i & 1) && !sure && !(c[i] < low - far)) << i;
+        }
+        const int fixed = __reduce_add_sync(kAll, __popc(safe));
+        if (fixed + __reduce_add_sync(kAll, __popc(near)) != a.k) {
+          // experts of logit -inf are equal to each other and below all else, as their keys are
+          unsure = !a.sigmoid || low == -INFINITY;
+          if (!unsure) {
+            evaluate<T, V>(a, t, near, top, row, list);
+            uint64_t wide[V], border;
+#pragma unroll
+            for (int i = 0; i < V; ++i) wide[i] = near >> i & 1 ? key_of(row[i * 32 + lane]) : 0;
+            chosen = safe | take_largest(wide, a.k - fixed, &border);
+          }
+        }
       }
     }
   }
@@ -363,7 +427,8 @@ __device__ __forceinline__ void write_rest(const RouteArgs& a, int64_t rows, int
 
 template <typename T, int V>
 __global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs a, int per) {
-  extern __shared__ double s_rows[];  // [kRouteWarps][E]
+  extern __shared__ double s_rows[];  // [kRouteWarps][E], then the lists [kRouteWarps][E]
+  uint16_t* s_list = reinterpret_cast<uint16_t*>(s_rows + kRouteWarps * a.E);
   __shared__ int s_base[kMaxExperts];
   __shared__ unsigned s_mask[kMaxExperts];
   __shared__ int s_red[kRouteWarps];
@@ -381,7 +446,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs a, int p
       continue;
     }
     float w[V];
-    const unsigned chosen = route_token<T, V>(a, t, s_rows + warp * a.E, w);
+    const unsigned chosen = route_token<T, V>(a, t, s_rows + warp * a.E, s_list + warp * a.E, w);
     int at = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -524,8 +589,8 @@ cudaError_t launch_fwd(const RouteArgs& a, int sms, cudaStream_t s) {
   static SmemLimit limit;
   auto kern = route_kernel<T, V>;
   const int ctas = route_ctas(a.T, sms), per = static_cast<int>((a.T + ctas - 1) / ctas);
-  if (cudaError_t e = limit.allow(kern, kRouteWarps * kMaxExperts * 8)) return e;
-  kern<<<ctas, kRouteThreads, kRouteWarps * a.E * 8, s>>>(a, per);
+  if (cudaError_t e = limit.allow(kern, kRouteWarps * kMaxExperts * 10)) return e;
+  kern<<<ctas, kRouteThreads, kRouteWarps * a.E * 10, s>>>(a, per);
   if (cudaError_t e = cudaGetLastError()) return e;
   if (!a.offsets || ctas == 1) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};

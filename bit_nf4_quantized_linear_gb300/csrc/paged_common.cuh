@@ -31,9 +31,13 @@ __device__ __forceinline__ int paged_len(const PagedArgs& a, int64_t s) {
 
 __device__ __forceinline__ int paged_tiles(int len) { return static_cast<int>((static_cast<int64_t>(len) + kPagedTile - 1) / kPagedTile); }
 
+__device__ __forceinline__ unsigned paged_index(const PagedArgs& a, int pos) {
+  return static_cast<unsigned>(static_cast<uint64_t>(static_cast<unsigned>(pos)) * a.page_mul >> a.page_shift);
+}
+
 // The page and slot of token `pos` of sequence s, or page -1 where the table names none.
 __device__ __forceinline__ int paged_slot(const PagedArgs& a, int64_t s, int pos, int* slot) {
-  const unsigned p = static_cast<unsigned>(pos) / static_cast<unsigned>(a.page_size);
+  const unsigned p = paged_index(a, pos);
   *slot = pos - static_cast<int>(p) * a.page_size;
   const int id = a.table[s * a.ld_table + p];
   if (id >= 0 && id < a.pages) return id;
@@ -47,44 +51,93 @@ struct PagedRun {
   int64_t before;  // tiles of the sequences before it
 };
 
-// This CTA's run of the units, `heads` a tile.  Called by all threads of the CTA; `red` holds
-// 34 values and is free again when the call returns.
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {  // of values >= 0; most fit 32 bits, where it is quick
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
+// This CTA's run of the units, `heads` a tile.  Equal shares of time, not of units: what a
+// (sequence, head group) costs beside its tiles (queries, and the warps' sums at its end) is
+// about half a tile's, so one of n tiles counts 2 n + 1.  Called by all threads of the CTA;
+// `red` holds 68 values and is free again when the call returns.
 __device__ __forceinline__ PagedRun paged_run(const PagedArgs& a, int heads, int64_t* red) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  const int64_t each = (a.nseq + blockDim.x - 1) / blockDim.x;
+  const int64_t each = a.nseq <= blockDim.x ? 1 : (a.nseq + blockDim.x - 1) / blockDim.x;
   const int64_t s0 = threadIdx.x * each, s1 = s0 + each < a.nseq ? s0 + each : a.nseq;
-  int64_t own = 0;
-  for (int64_t s = s0; s < s1; ++s) own += paged_tiles(paged_len(a, s));
-  int64_t incl = own;
+  int64_t own = 0, live = 0;  // tiles, and sequences that have some
+  for (int64_t s = s0; s < s1; ++s) {
+    const int n = paged_tiles(paged_len(a, s));
+    own += n;
+    live += n > 0;
+  }
+  int64_t tiles = own, seqs = live;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += up;
-  }
-  if (lane == 31) red[warp] = incl;
-  __syncthreads();
-  int64_t base = 0, total = 0;
-  for (int w = 0; w < nw; ++w) {
-    if (w == warp) base = total;
-    total += red[w];
-  }
-  base += incl - own;
-  PagedRun r;
-  r.u0 = blockIdx.x * (total * heads) / gridDim.x;
-  r.u1 = (blockIdx.x + 1) * (total * heads) / gridDim.x;
-  if (r.u0 < r.u1 && r.u0 >= base * heads && r.u0 < (base + own) * heads) {
-    int64_t s = s0, at = base;
-    for (;; ++s) {
-      const int n = paged_tiles(paged_len(a, s));
-      if (r.u0 < (at + n) * heads || s + 1 >= s1) break;
-      at += n;
+    const int64_t t = __shfl_up_sync(0xffffffffu, tiles, o), q = __shfl_up_sync(0xffffffffu, seqs, o);
+    if (lane >= o) {
+      tiles += t;
+      seqs += q;
     }
-    red[32] = s;
-    red[33] = at;
+  }
+  if (lane == 31) {
+    red[warp] = tiles;
+    red[32 + warp] = seqs;
   }
   __syncthreads();
-  r.seq = red[32];
-  r.before = red[33];
+  int64_t tiles0 = 0, seqs0 = 0, all_tiles = 0, all_seqs = 0;
+  for (int w = 0; w < nw; ++w) {
+    if (w == warp) {
+      tiles0 = all_tiles;
+      seqs0 = all_seqs;
+    }
+    all_tiles += red[w];
+    all_seqs += red[32 + w];
+  }
+  tiles0 += tiles - own;
+  seqs0 += seqs - live;
+  // shares of the whole, in halves of a tile
+  const int64_t total = (2 * all_tiles + all_seqs) * heads, share = divide(total, gridDim.x), rest = total - share * gridDim.x;
+  const int64_t c = blockIdx.x, v0 = c * share + (c < rest ? c : rest), v1 = v0 + share + (c < rest);
+  const int64_t first = (2 * tiles0 + seqs0) * heads, past = first + (2 * own + live) * heads;
+  __syncthreads();
+  if (threadIdx.x == 0) {  // where no thread's sequences hold an end of the run
+    red[0] = red[1] = all_tiles * heads;
+    red[2] = a.nseq;
+  }
+  __syncthreads();
+  for (int end = 0; end < 2; ++end) {
+    const int64_t v = end ? v1 : v0;
+    if (v < first || v >= past) continue;
+    int64_t s = s0, before = tiles0, at = first;
+    for (; s < s1; ++s) {
+      const int n = paged_tiles(paged_len(a, s));
+      if (n == 0) continue;
+      const int64_t span = static_cast<int64_t>(2 * static_cast<int64_t>(n) + 1) * heads;
+      if (v >= at + span) {
+        at += span;
+        before += n;
+        continue;
+      }
+      const int64_t head = divide(v - at, 2 * static_cast<int64_t>(n) + 1), tile = (v - at - head * (2 * static_cast<int64_t>(n) + 1)) >> 1;
+      red[end] = before * heads + head * n + tile;
+      if (end == 0) {
+        if (head * n + tile == static_cast<int64_t>(heads) * n) {  // the half behind its last tile: the run begins with the next
+          before += n;
+          do ++s;
+          while (s < a.nseq && paged_len(a, s) == 0);
+        }
+        red[2] = s;
+        red[3] = before;
+      }
+      break;
+    }
+  }
+  __syncthreads();
+  PagedRun r;
+  r.u0 = red[0];
+  r.u1 = red[1];
+  r.seq = red[2];
+  r.before = red[3];
   __syncthreads();
   return r;
 }
@@ -100,7 +153,25 @@ __device__ __forceinline__ void paged_empty(const PagedArgs& a) {
   }
 }
 
-__device__ __forceinline__ void paged_allow_join() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// Programmatic launches: the next kernel of the stream starts its CTAs while this one runs
+// and waits (grid_wait) before it reads or writes anything.
+__device__ __forceinline__ void grid_allow() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kern)(P...), dim3 grid, int threads, int smem, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
 
 // Adds the partial results of each (sequence, head group) that was cut, in CTA order.  A CTA
 // for each CTA of the attention kernel whose run may begin one (blockIdx.x) and each head of
@@ -109,7 +180,7 @@ template <typename T>
 __global__ void __launch_bounds__(128) paged_join_kernel(PagedArgs a, int heads, int groups) {
   __shared__ float s_acc[4][256], s_ml[4][2];
   __shared__ int s_n;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  grid_wait();
   const int c = blockIdx.x, n = gridDim.x, h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const PagedRec me = a.rec[c];
   if (!(me.flags & 1)) return;
@@ -173,16 +244,7 @@ __global__ void __launch_bounds__(128) paged_join_kernel(PagedArgs a, int heads,
 
 template <typename T>
 cudaError_t launch_paged_join(const PagedArgs& a, int ctas, int heads, int groups, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(heads), 1);
-  cfg.blockDim = dim3(128, 1, 1);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_join_kernel<T>, a, heads, groups);
+  return launch_early(paged_join_kernel<T>, dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(heads), 1), 128, 0, s, a, heads, groups);
 }
 
 }  // namespace nf4
