@@ -193,7 +193,7 @@ struct RouteArgs {
   float scale;
   int32_t *experts, *offsets, *row_token, *token_rows;  // [T][k], [E + 1], [T k], [T][k]; tables null: not wanted
   float *weights, *row_weight;                          // [T][k], [T k]
-  int32_t* counts;  // [CTAs][E], workspace
+  int32_t* counts;  // [CTAs][route_pitch(E)] values, or bytes where a CTA has few tokens; workspace
   // backward
   const float *g_weights, *g_rows;  // [T][k], [T k]; either may be null
   void* g_logits;
@@ -201,7 +201,13 @@ struct RouteArgs {
   int* status;
 };
 constexpr int kRouteMaxK = 32;
+inline __host__ __device__ int route_pitch(int E) { return (E + 15) / 16 * 16; }
 int route_ctas(int64_t T, int sms);
+// workspace of the forward with tables
+inline size_t route_ws_bytes(int64_t T, int E, int sms) {
+  const int n = route_ctas(T, sms);
+  return n > 1 ? static_cast<size_t>(n) * route_pitch(E) * sizeof(int32_t) : 0;
+}
 cudaError_t launch_route(bool backward, int dtype, const RouteArgs& a, int sms, cudaStream_t s);
 
 // Multi-product launches (nf4_linear_fwd_multi / nf4_linear_dgrad_multi): up to

@@ -1183,9 +1183,9 @@ nf4_status nf4_route_fwd(const nf4_route* d, int32_t* experts, float* weights, i
       if (cudaError_t ce = cudaMemsetAsync(offsets, 0, (static_cast<size_t>(a.E) + 1) * 4, st)) return cuda_fail(ce, "memset");
     return NF4_OK;
   }
-  if (tables && nf4::route_ctas(a.T, dev.sms) > 1) {
-    if (!ws || ws_bytes < static_cast<size_t>(nf4::route_ctas(a.T, dev.sms)) * a.E * 4) return NF4_ERR_WORKSPACE;
-    if (!aligned_to(ws, 4)) return NF4_ERR_ALIGNMENT;
+  if (const size_t need = tables ? nf4::route_ws_bytes(a.T, a.E, dev.sms) : 0) {
+    if (!ws || ws_bytes < need) return NF4_ERR_WORKSPACE;
+    if (!aligned_to(ws, 16)) return NF4_ERR_ALIGNMENT;
     a.counts = static_cast<int32_t*>(ws);
   }
   a.experts = experts;
@@ -1624,7 +1624,7 @@ size_t nf4_workspace_size(int32_t op, int64_t M, int64_t N, int64_t K, int32_t E
     DevInfo dev;
     if (!current_device(&dev)) return 0;
     if (op == NF4_OP_PAGED_ATTENTION) return K < 1 || K > 256 ? 0 : nf4::paged_ws_bytes(static_cast<int>(K), dev.sms);
-    return M <= 0 || N <= 0 ? 0 : static_cast<size_t>(nf4::route_ctas(M, dev.sms)) * N * 4;
+    return M <= 0 || N <= 0 || N > nf4::kMaxExperts ? 0 : nf4::route_ws_bytes(M, static_cast<int>(N), dev.sms);
   }
   if (op == NF4_OP_QUANTIZE) {
     const int64_t nblocks = (N * K + 63) / 64;

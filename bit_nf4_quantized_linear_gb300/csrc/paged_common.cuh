@@ -13,6 +13,7 @@
 
 #include <cstdint>
 
+#include "early_launch.cuh"
 #include "elem.cuh"
 #include "internal.h"
 
@@ -151,26 +152,6 @@ __device__ __forceinline__ void paged_empty(const PagedArgs& a) {
       static_cast<T*>(a.o)[s * a.o_s + static_cast<int64_t>(i / a.D) * a.o_h + i % a.D] = T(0.0f);
     for (int h = threadIdx.x; a.lse && h < a.Hq; h += blockDim.x) a.lse[s * a.Hq + h] = -INFINITY;
   }
-}
-
-// Programmatic launches: the next kernel of the stream starts its CTAs while this one runs
-// and waits (grid_wait) before it reads or writes anything.
-__device__ __forceinline__ void grid_allow() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
-template <typename... P, typename... A>
-cudaError_t launch_early(void (*kern)(P...), dim3 grid, int threads, int smem, cudaStream_t s, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
-  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 // Adds the partial results of each (sequence, head group) that was cut, in CTA order.  A CTA

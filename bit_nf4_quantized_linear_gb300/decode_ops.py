@@ -43,21 +43,24 @@ def _explain_cache(name, k_pages, v_pages, page_table, lengths, rows):
 
 
 def _cache(name, k_pages, v_pages, page_table, lengths, rows):
-    """The packed nf4_paged_cache of checked arguments."""
-    dt, dev, ks, kt, vt = k_pages.dtype, k_pages.device, k_pages.shape, k_pages.stride(), v_pages.stride()
-    n = lengths.shape[0] if lengths.dim() == 1 else -1
-    ok = (dt in _DTYPES and dev.type == "cuda" and len(ks) == 4 and v_pages.shape == ks and v_pages.dtype is dt and 0 not in ks[1:]
-          and v_pages.device == page_table.device == lengths.device == dev and (ks[3] == 1 or kt[3] == vt[3] == 1)
-          and lengths.dtype is torch.int32 and lengths.is_contiguous() and page_table.dtype is torch.int32 and page_table.dim() == 2
-          and page_table.shape[0] == n and (page_table.shape[1] < 2 or page_table.stride(1) == 1))
+    """The packed nf4_paged_cache of checked arguments, and the cache's shape."""
+    dt, dev, ks, kt, vt, ts, tt, ls = (k_pages.dtype, k_pages.device, k_pages.shape, k_pages.stride(), v_pages.stride(), page_table.shape,
+                                       page_table.stride(), lengths.shape)
+    at = k_pages.get_device()
+    ok = (dt in _DTYPES and at >= 0 and len(ks) == 4 and v_pages.shape == ks and v_pages.dtype is dt and 0 not in ks[1:]
+          and v_pages.get_device() == at and page_table.get_device() == at and lengths.get_device() == at
+          and (kt[3] == 1 == vt[3] or ks[3] == 1) and lengths.dtype is torch.int32 and lengths.is_contiguous() and len(ls) == 1
+          and page_table.dtype is torch.int32 and len(ts) == 2 and ts[0] == ls[0] and (tt[1] == 1 or ts[1] < 2))
     for _, t, heads in rows if ok else ():
-        ok = (ok and t.dtype is dt and t.device == dev and t.dim() == 3 and t.shape[2] == ks[3] and (heads is None or t.shape[1] == heads)
-              and (ks[3] == 1 or t.stride(2) == 1))
+        s = t.shape
+        ok = (ok and t.dtype is dt and t.get_device() == at and len(s) == 3 and s[2] == ks[3] and (heads is None or s[1] == heads)
+              and (t.stride(2) == 1 or s[2] == 1))
     if not ok:
         _explain_cache(name, k_pages, v_pages, page_table, lengths, rows)
         raise ValueError(f"{name}: arguments do not make a paged cache")
-    return _CACHE.pack(k_pages.data_ptr(), v_pages.data_ptr(), kt[0], kt[1], kt[2], vt[0], vt[1], vt[2], page_table.data_ptr(),
-                       page_table.stride(0), lengths.data_ptr(), n, ks[0], page_table.shape[1], ks[1], ks[2], ks[3], _DTYPES[dt])
+    pages, slots, Hk, D = ks
+    return _CACHE.pack(k_pages.data_ptr(), v_pages.data_ptr(), kt[0], kt[1], kt[2], vt[0], vt[1], vt[2], page_table.data_ptr(), tt[0],
+                       lengths.data_ptr(), ls[0], pages, ts[1], slots, Hk, D, _DTYPES[dt]), dev, ls[0], Hk, D
 
 
 @functools.lru_cache(maxsize=1024)
@@ -81,14 +84,13 @@ def paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
     from the table (recorded in the device status), are not written."""
     name = "paged_append"
     Hk = k_pages.shape[2] if k_pages.dim() == 4 else -1
-    d = _cache(name, k_pages, v_pages, page_table, lengths, (("k", k, Hk), ("v", v, Hk)))
-    T, n, dev = k.shape[0], lengths.shape[0], k_pages.device
+    d, dev, n, _, _ = _cache(name, k_pages, v_pages, page_table, lengths, (("k", k, Hk), ("v", v, Hk)))
+    T, cu = k.shape[0], None
     if v.shape[0] != T or (cu_seqlens is None and T != n):
         raise ValueError(f"{name}: {T} and {v.shape[0]} rows of keys and values for {n} sequences")
-    cu = None
     if cu_seqlens is not None:
         cu = cu_seqlens.data_ptr()
-        if (cu_seqlens.dtype is not torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] != n + 1 or not cu_seqlens.is_contiguous()
+        if (cu_seqlens.dtype is not torch.int32 or cu_seqlens.shape != (n + 1,) or not cu_seqlens.is_contiguous()
                 or cu_seqlens.device != dev):
             raise ValueError(f"{name}: cu_seqlens must be a contiguous int32 [{n + 1}] tensor on {dev}")
     if _slots_share(k_pages.shape, k_pages.stride()) or _slots_share(v_pages.shape, v_pages.stride()):
@@ -110,11 +112,10 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     place of a new tensor: any strides whose rows do not share storage.  Tables and lengths are read on the device, so a
     captured graph follows them.  No gradients."""
     name = "paged_attention"
-    d = _cache(name, k_pages, v_pages, page_table, lengths, (("q", q, None),) if out is None else (("q", q, None), ("out", out, None)))
-    n, Hq, D = q.shape
-    Hk, dev = k_pages.shape[2], q.device
-    if n != lengths.shape[0] or Hq == 0 or Hq % Hk:
-        raise ValueError(f"{name}: q {tuple(q.shape)} does not fit {lengths.shape[0]} sequences of {Hk} key heads")
+    d, dev, n, Hk, D = _cache(name, k_pages, v_pages, page_table, lengths, (("q", q, None),) if out is None else (("q", q, None), ("out", out, None)))
+    Hq = q.shape[1]
+    if q.shape[0] != n or Hq == 0 or Hq % Hk:
+        raise ValueError(f"{name}: q {tuple(q.shape)} does not fit {n} sequences of {Hk} key heads")
     if out is not None and (out.shape != q.shape or _share_storage(out)):
         raise ValueError(f"{name}: out must have q's shape, and rows that do not share storage")
     o = torch.empty((n, Hq, D), dtype=q.dtype, device=dev) if out is None else out

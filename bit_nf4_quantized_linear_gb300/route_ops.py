@@ -28,10 +28,9 @@ class Routes(NamedTuple):
     row_weight: Optional[torch.Tensor]    # fp32 [R]: the weight of each row
 
 
-def _route(name, logits, k, score, bias, groups, top_groups, group_top, renormalise, scale, live):
-    """The packed nf4_route of checked arguments, and the tensor that the logits' pointer lies in."""
+def _explain_route(name, logits, k, score, bias, groups, top_groups, group_top, live):
     _one_device(name, logits, bias, live)
-    dt = _dtype(name, logits)
+    _dtype(name, logits)
     if logits.dim() != 2 or logits.shape[1] < 1 or (logits.shape[1] > 1 and logits.stride(1) != 1):
         raise ValueError(f"{name}: logits must be [tokens, experts] with unit column stride")
     T, E = logits.shape
@@ -43,12 +42,30 @@ def _route(name, logits, k, score, bias, groups, top_groups, group_top, renormal
         raise ValueError(f"{name}: {k} experts of the {top_groups * (E // groups)} that are kept")
     if bias is not None and (bias.dtype is not torch.float32 or bias.shape != (E,) or not bias.is_contiguous()):
         raise ValueError(f"{name}: bias must be a contiguous fp32 [{E}] tensor")
-    if live is not None and (live.dtype not in (torch.bool, torch.uint8) or live.shape != (T,) or not live.is_contiguous()):
-        raise ValueError(f"{name}: live must be a contiguous bool or uint8 [{T}] tensor")
-    if T > 1 and logits.stride(0) < E:  # rows that share storage
-        logits = logits.contiguous()
-    d = _ROUTE.pack(logits.data_ptr(), logits.stride(0) if T > 1 else E, T, 0 if bias is None else bias.data_ptr(),
-                    0 if live is None else live.data_ptr(), E, k, dt, _SCORES[score], groups, top_groups, group_top, bool(renormalise), scale)
+    raise ValueError(f"{name}: live must be a contiguous bool or uint8 [{T}] tensor")
+
+
+def _route(name, logits, k, score, bias, groups, top_groups, group_top, renormalise, scale, live):
+    """The packed nf4_route of checked arguments, and the tensor that the logits' pointer lies in."""
+    dt, shape, stride, at = logits.dtype, logits.shape, logits.stride(), logits.get_device()
+    T, E = shape if len(shape) == 2 else (0, 0)
+    ok = (dt in _DTYPES and at >= 0 and E > 0 and (stride[1] == 1 or E == 1) and score in _SCORES and groups > 0 and E % groups == 0
+          and 1 <= top_groups <= groups and (group_top == 1 or group_top == 2) and 1 <= k <= top_groups * (E // groups))
+    bp = lp = 0
+    if bias is not None:
+        bp = bias.data_ptr()
+        ok = ok and bias.dtype is torch.float32 and bias.shape == (E,) and bias.is_contiguous() and bias.get_device() == at
+    if live is not None:
+        lp = live.data_ptr()
+        ok = (ok and (live.dtype is torch.bool or live.dtype is torch.uint8) and live.shape == (T,) and live.is_contiguous()
+              and live.get_device() == at)
+    if not ok:
+        _explain_route(name, logits, k, score, bias, groups, top_groups, group_top, live)
+    ld = stride[0] if T > 1 else E
+    if ld < E:  # rows that share storage
+        logits, ld = logits.contiguous(), E
+    d = _ROUTE.pack(logits.data_ptr(), ld, T, bp, lp, E, k, _DTYPES[dt], _SCORES[score], groups, top_groups, group_top, bool(renormalise),
+                    scale)
     return d, logits
 
 
@@ -75,9 +92,11 @@ def route_experts(logits: torch.Tensor, k: int, *, score: str = "softmax", bias:
             token_rows = torch.empty((T, k), dtype=i32, device=dev)
             row_weight = torch.empty(T * k, dtype=f32, device=dev)
             need = _workspace(_lib.OP_ROUTE, T, E, dev)
-            ws = torch.empty(need, dtype=torch.uint8, device=dev)
+            if need:
+                ws = torch.empty(need, dtype=torch.uint8, device=dev)
             rc = _fn("nf4_route_fwd")(d, experts.data_ptr(), weights.data_ptr(), offsets.data_ptr(), row_token.data_ptr(),
-                                      token_rows.data_ptr(), row_weight.data_ptr(), ws.data_ptr(), need, _raw_stream(dev))
+                                      token_rows.data_ptr(), row_weight.data_ptr(), ws.data_ptr() if need else None, need,
+                                      _raw_stream(dev))
         else:
             rc = _fn("nf4_route_fwd")(d, experts.data_ptr(), weights.data_ptr(), None, None, None, None, None, 0, _raw_stream(dev))
     if rc:
@@ -92,8 +111,10 @@ def route_experts_bwd(logits: torch.Tensor, routes: Routes, *, grad_weights: Opt
     and of `row_weight` (fp32 [R], as grouped_swiglu_bwd returns it), either None.  `routes` is the forward's; score,
     renormalise and scale as there.  The choice of the experts has no gradient."""
     name = "route_experts_bwd"
-    experts, token_rows = routes.experts, routes.token_rows
-    _one_device(name, logits, experts, token_rows, grad_weights, grad_row_weight)
+    experts, token_rows, at = routes.experts, routes.token_rows, logits.get_device()
+    for t in (experts, token_rows, grad_weights, grad_row_weight):
+        if t is not None and t.get_device() != at:
+            _one_device(name, logits, experts, token_rows, grad_weights, grad_row_weight)
     if experts.dtype is not torch.int32 or experts.dim() != 2 or experts.shape[0] != logits.shape[0] or not experts.is_contiguous():
         raise ValueError(f"{name}: routes.experts must be the contiguous int32 [tokens, k] of the forward")
     T, k = experts.shape

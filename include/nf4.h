@@ -557,7 +557,8 @@ nf4_status nf4_paged_attention(const nf4_paged_cache* c, const void* q, int64_t 
  *   row_token  int32 [T k], row_weight fp32 [T k]: the token and the weight of each row; -1
  *              and 0 from offsets[E] on;
  *   token_rows int32 [T][k]: the row of each route, -1 for none.
- * ws: nf4_workspace_size(NF4_OP_ROUTE, T, E, 0, 0) bytes, needed with tables.
+ * ws: nf4_workspace_size(NF4_OP_ROUTE, T, E, 0, 0) bytes, 16-byte aligned, for the tables (NULL where
+ *   that is 0).
  * 1 <= E <= 512, 1 <= k <= 32 and k <= top_groups * (E / groups), groups <= 32.
  *
  * nf4_route_bwd: g_logits [T, E] (pitch ld_g, of `dtype`) from g_weights [T][k] and / or
