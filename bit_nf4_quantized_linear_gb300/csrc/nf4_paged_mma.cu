@@ -157,7 +157,6 @@ __global__ void __launch_bounds__(kThreads, Geo<DM>::kCtas) paged_mma_kernel(Pag
   s_valid += warp * G::kStages;
   grid_allow();
   grid_wait();
-  paged_empty<T>(a);
   const int heads = a.Hk * groups, GQ = a.Hq / a.Hk;
   const PagedRun run = paged_run(a, heads, reinterpret_cast<int64_t*>(s_sum));
   PagedRec rec{0, 0, 0};
@@ -294,6 +293,7 @@ __global__ void __launch_bounds__(kThreads, Geo<DM>::kCtas) paged_mma_kernel(Pag
     }
     fetch_queries();
     clear_sums();
+    paged_empty<T>(a);
     int st = 0;
     while (use.left > 0) {
       copies_wait<G::kStages - 1>();
@@ -462,6 +462,8 @@ __global__ void __launch_bounds__(kThreads, Geo<DM>::kCtas) paged_mma_kernel(Pag
       clear_sums();
     }
     copies_wait<0>();
+  } else {
+    paged_empty<T>(a);
   }
   if (threadIdx.x == 0) a.rec[blockIdx.x] = rec;
 }

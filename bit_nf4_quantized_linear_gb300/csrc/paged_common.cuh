@@ -156,47 +156,58 @@ __device__ __forceinline__ void paged_empty(const PagedArgs& a) {
 
 // Adds the partial results of each (sequence, head group) that was cut, in CTA order.  A CTA
 // for each CTA of the attention kernel whose run may begin one (blockIdx.x) and each head of
-// a group (blockIdx.y); `heads` a group.
-template <typename T>
+// a group (blockIdx.y); `heads` a group.  Its time is that of a few dependent loads, so what a
+// load needs not wait for it does not: flags and sums of all parts are read at once, and those
+// of no use are dropped.
+template <typename T, int DV>
 __global__ void __launch_bounds__(128) paged_join_kernel(PagedArgs a, int heads, int groups) {
-  __shared__ float s_acc[4][256], s_ml[4][2];
-  __shared__ int s_n;
-  grid_wait();
+  constexpr int kAtOnce = DV <= 4 ? 4 : 2;
+  __shared__ float s_acc[4][DV * 32], s_ml[4][2];
+  __shared__ int s_last[4];
   const int c = blockIdx.x, n = gridDim.x, h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  grid_wait();
   const PagedRec me = a.rec[c];
+  // the CTA that ends it: the first after c with that flag
+  int last = n;
+  for (int p = n - 1 - threadIdx.x; p > c; p -= 128) last = a.rec[p].flags & 4 ? p : last;
   if (!(me.flags & 1)) return;
-  const int G = a.Hq / a.Hk, hk = me.head / groups, g = me.head % groups * heads + h;
+  const int G = a.Hq / a.Hk, hk = me.head / groups, g = (me.head - hk * groups) * heads + h;
   if (g >= G) return;
-  if (warp == 0) {  // the CTA that ends it
-    int last = n - 1;
-    for (int c0 = c + 1; c0 < n; c0 += 32) {
-      const int f = c0 + lane < n ? a.rec[c0 + lane].flags : 0;
-      const unsigned hit = __ballot_sync(0xffffffffu, (f & 4) != 0);
-      if (hit) {
-        last = c0 + __ffs(hit) - 1;
-        break;
+  last = static_cast<int>(__reduce_min_sync(0xffffffffu, static_cast<unsigned>(last)));
+  if (lane == 0) s_last[warp] = last;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 4; ++w) last = min(last, s_last[w]);
+  const int st = paged_part_stride(a.D);
+  float m = -INFINITY, l = 0.0f, acc[DV] = {};
+  for (int p0 = c + warp; p0 <= last; p0 += 4 * kAtOnce) {
+    float pm[kAtOnce], pl[kAtOnce], pv[kAtOnce][DV];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int p = min(p0 + 4 * i, n - 1);
+      const float* part = a.part + (static_cast<int64_t>(p * 2 + (p == c)) * heads + h) * st;
+      const bool in = p0 + 4 * i <= last && (p == c || (a.rec[p].flags & 2));
+      const float m0 = part[st - 4], l0 = part[st - 3];
+      pm[i] = in ? m0 : -INFINITY;
+      pl[i] = in ? l0 : 0.0f;
+#pragma unroll
+      for (int j = 0; j < DV; ++j) {
+        const float v = lane + 32 * j < a.D ? part[lane + 32 * j] : 0.0f;
+        pv[i][j] = in ? v : 0.0f;
       }
     }
-    if (lane == 0) s_n = last;
-  }
-  __syncthreads();
-  const int last = s_n, st = paged_part_stride(a.D);
-  float m = -INFINITY, l = 0.0f, acc[8] = {};
-  for (int p = c + warp; p <= last; p += 4) {
-    if (p > c && !(a.rec[p].flags & 2)) continue;
-    const float* part = a.part + (static_cast<int64_t>(p * 2 + (p == c)) * heads + h) * st;
-    const float pm = part[st - 4], pl = part[st - 3];
-    const float top = fmaxf(m, pm), mm = top == -INFINITY ? 0.0f : top;
-    const float f0 = exp2f(m - mm), f1 = exp2f(pm - mm);
-    m = top;
-    l = l * f0 + pl * f1;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (lane + 32 * i < a.D) acc[i] = acc[i] * f0 + part[lane + 32 * i] * f1;
+    for (int i = 0; i < kAtOnce; ++i) {
+      const float top = fmaxf(m, pm[i]), mm = top == -INFINITY ? 0.0f : top;
+      const float f0 = exp2f(m - mm), f1 = exp2f(pm[i] - mm);
+      m = top;
+      l = l * f0 + pl[i] * f1;
+#pragma unroll
+      for (int j = 0; j < DV; ++j) acc[j] = acc[j] * f0 + pv[i][j] * f1;
+    }
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (lane + 32 * i < a.D) s_acc[warp][lane + 32 * i] = acc[i];
+  for (int i = 0; i < DV; ++i) s_acc[warp][lane + 32 * i] = acc[i];
   if (lane == 0) {
     s_ml[warp][0] = m;
     s_ml[warp][1] = l;
@@ -225,7 +236,11 @@ __global__ void __launch_bounds__(128) paged_join_kernel(PagedArgs a, int heads,
 
 template <typename T>
 cudaError_t launch_paged_join(const PagedArgs& a, int ctas, int heads, int groups, cudaStream_t s) {
-  return launch_early(paged_join_kernel<T>, dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(heads), 1), 128, 0, s, a, heads, groups);
+  const int G = a.Hq / a.Hk;
+  const dim3 grid(static_cast<unsigned>(ctas), static_cast<unsigned>(G < heads ? G : heads), 1);
+  if (a.D <= 64) return launch_early(paged_join_kernel<T, 2>, grid, 128, 0, s, a, heads, groups);
+  if (a.D <= 128) return launch_early(paged_join_kernel<T, 4>, grid, 128, 0, s, a, heads, groups);
+  return launch_early(paged_join_kernel<T, 8>, grid, 128, 0, s, a, heads, groups);
 }
 
 }  // namespace nf4
