@@ -181,6 +181,7 @@ inline size_t paged_ws_bytes(int D, int sms) {
 }
 cudaError_t launch_paged_append(int dtype, const PagedArgs& a, int sms, cudaStream_t s);
 cudaError_t launch_paged_mma(bool f16, const PagedArgs& a, int sms, cudaStream_t s);
+cudaError_t launch_paged_f32(const PagedArgs& a, int sms, cudaStream_t s);
 cudaError_t launch_paged_any(int dtype, const PagedArgs& a, int sms, cudaStream_t s);
 
 // The router of the experts (nf4_route_fwd / nf4_route_bwd).

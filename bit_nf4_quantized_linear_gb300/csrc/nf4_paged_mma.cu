@@ -25,6 +25,7 @@
 #include "elem.cuh"
 #include "internal.h"
 #include "paged_common.cuh"
+#include "paged_ring.cuh"
 #include "sm100_ptx.cuh"
 #include "smem_limit.h"
 
@@ -47,22 +48,6 @@ struct Geo {
   static constexpr int kSums = kWarps * 8 * kPitch * 4;
   static constexpr int kSmem = kRing + kSums + kWarps * 8 * 8 + kWarps * kStages * 4;
 };
-
-// Columns of 8 values stored XOR-swizzled by row, so that the eight rows of an 8 x 8 matrix
-// lie in different banks.
-template <int DM>
-__device__ __forceinline__ uint32_t at_chunk(int row, int chunk) {
-  return static_cast<uint32_t>(row * DM * 2 + ((chunk ^ (row & 7)) << 4));
-}
-
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 
 __device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -115,38 +100,11 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t* hi, uint32_t*
   }
 }
 
-__device__ __forceinline__ float exp2_fast(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
-// The units of a run, one after another.
-struct Walk {
-  int64_t seq;
-  int left;  // units left in the run, this one among them (2^31 would be days of work)
-  int len, tiles, head, tile;
-
-  // The next unit with tokens; `heads` a tile.
-  __device__ __forceinline__ void next(const PagedArgs& a, int heads) {
-    --left;
-    if (++tile < tiles) return;
-    tile = 0;
-    if (++head < heads || left <= 0) return;
-    head = 0;
-    do {
-      ++seq;
-      len = seq < a.nseq ? paged_len(a, seq) : 1;
-      tiles = paged_tiles(len);
-    } while (tiles == 0);
-  }
-};
-
 template <bool F16, int DM, int NT>
 __global__ void __launch_bounds__(kThreads, Geo<DM>::kCtas) paged_mma_kernel(PagedArgs a, int groups) {
   using G = Geo<DM>;
   using T = typename std::conditional<F16, __half, __nv_bfloat16>::type;
-  constexpr int HC = 8 * NT, KS = DM / 16, CH = DM / 8;
+  constexpr int HC = 8 * NT, KS = DM / 16;
   constexpr float kShift = F16 ? 7.0f : 0.0f;
   extern __shared__ __align__(128) unsigned char dyn[];
   float* s_sum = reinterpret_cast<float*>(dyn + G::kRing);                          // [kWarps][8][kPitch]
@@ -162,93 +120,10 @@ __global__ void __launch_bounds__(kThreads, Geo<DM>::kCtas) paged_mma_kernel(Pag
   PagedRec rec{0, 0, 0};
 
   if (run.u0 < run.u1) {
-    Walk load;
-    load.seq = run.seq;
-    load.left = static_cast<int>(run.u1 - run.u0 < INT32_MAX ? run.u1 - run.u0 : INT32_MAX);
-    load.len = paged_len(a, run.seq);
-    load.tiles = paged_tiles(load.len);
-    const int64_t r0 = run.u0 - run.before * heads;
-    load.head = static_cast<int>(divide(r0, load.tiles));
-    load.tile = static_cast<int>(r0 - static_cast<int64_t>(load.head) * load.tiles);
+    Walk load(a, run, heads);
     Walk use = load;
 
-    // Starts the copies of this warp's tokens of the unit `load` into ring slot `st`.  Lane i
-    // copies column group i % CH of rows i / CH and every kPer-th after it.
-    constexpr int kPer = 32 / CH;
-    const int row0 = lane / CH, col = lane % CH * 8;
-    const bool in = col < a.D;
-    const bool whole_pages = a.page_size % kRows == 0;  // a tile lies in one page
-    const uint32_t dst0 = ring + at_chunk<DM>(row0, lane % CH);
-    auto start_copies = [&](int st) {
-      const int tok0 = load.tile * kPagedTile + warp * kRows, rows = load.len - tok0, hk = groups == 1 ? load.head : load.head / groups;
-      if (load.left > 0 && rows > 0) {
-        const uint32_t to = dst0 + st * G::kStage;
-        // a row's swizzle repeats after eight rows
-        auto dst = [&](int i) {
-          return kPer >= 8 || (i * kPer) % 8 == 0 ? to + i * kPer * DM * 2 : (to ^ ((i * kPer) % 8 << 4)) + i * kPer * DM * 2;
-        };
-        unsigned valid;
-        if (whole_pages) {
-          int slot;
-          const int64_t page = paged_slot(a, load.seq, tok0, &slot);
-          const int n = page < 0 ? 0 : rows;
-          valid = n >= kRows ? 0xffffu : (1u << n) - 1u;
-          const T* kp = static_cast<const T*>(a.q);
-          const T* vp = kp;
-          int64_t ks = 0, vs = 0;
-          if (in && page >= 0) {
-            kp = static_cast<const T*>(a.k) + (page * a.k_page + (slot + row0) * a.k_token + hk * a.k_head + col);
-            vp = static_cast<const T*>(a.v) + (page * a.v_page + (slot + row0) * a.v_token + hk * a.v_head + col);
-            ks = kPer * a.k_token;
-            vs = kPer * a.v_token;
-          }
-          if (n >= kRows) {
-            const int bytes = in ? 16 : 0;
-#pragma unroll
-            for (int i = 0; i < kRows / kPer; ++i) {
-              copy16(dst(i), kp, bytes);
-              copy16(dst(i) + G::kHalf, vp, bytes);
-              kp += ks;
-              vp += vs;
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < kRows / kPer; ++i) {
-              const bool row = in && i * kPer + row0 < n;
-              copy16(dst(i), row ? kp : static_cast<const T*>(a.q), row ? 16 : 0);
-              copy16(dst(i) + G::kHalf, row ? vp : static_cast<const T*>(a.q), row ? 16 : 0);
-              kp += ks;
-              vp += vs;
-            }
-          }
-        } else {
-          // lane i < 16 looks up the key row of token i, lane 16 + i its value row
-          const int tok = tok0 + (lane & 15);
-          int64_t at = 0;
-          bool ok = false;
-          if (tok < load.len) {
-            int slot;
-            const int64_t page = paged_slot(a, load.seq, tok, &slot);
-            ok = page >= 0;
-            if (ok)
-              at = lane < 16 ? page * a.k_page + slot * a.k_token + hk * a.k_head
-                             : page * a.v_page + slot * a.v_token + hk * a.v_head;
-          }
-          valid = __ballot_sync(0xffffffffu, ok) & 0xffffu;
-#pragma unroll
-          for (int i = 0; i < kRows / kPer; ++i) {
-            const int r = i * kPer + row0;
-            const int64_t ak = __shfl_sync(0xffffffffu, at, r), av = __shfl_sync(0xffffffffu, at, r + 16);
-            const int bytes = (valid >> r & 1) && in ? 16 : 0;
-            copy16(dst(i), bytes ? static_cast<const T*>(a.k) + ak + col : static_cast<const T*>(a.q), bytes);
-            copy16(dst(i) + G::kHalf, bytes ? static_cast<const T*>(a.v) + av + col : static_cast<const T*>(a.q), bytes);
-          }
-        }
-        if (lane == 0) s_valid[st] = valid;
-      }
-      copies_commit();
-    };
-
+    const TileCopies<T, DM, kRows> copies(a, ring, s_valid, groups);
     uint32_t qf[NT][KS][2];
     float acc[NT][KS][4], m[NT][2], l[NT][2];
     const float c = a.scale * kLog2e;
@@ -257,8 +132,8 @@ __global__ void __launch_bounds__(kThreads, Geo<DM>::kCtas) paged_mma_kernel(Pag
     uint32_t k_off[KO], v_off[KO];
 #pragma unroll
     for (int s = 0; s < KO; ++s) {
-      k_off[s] = ring + at_chunk<DM>(lane & 15, 2 * s + (lane >> 4));
-      v_off[s] = ring + G::kHalf + at_chunk<DM>((lane & 7) + (lane >> 4 << 3), 2 * s + (lane >> 3 & 1));
+      k_off[s] = ring + at_chunk<DM * 2>(lane & 15, 2 * s + (lane >> 4));
+      v_off[s] = ring + G::kHalf + at_chunk<DM * 2>((lane & 7) + (lane >> 4 << 3), 2 * s + (lane >> 3 & 1));
     }
     int tile0 = use.tile;  // where the part of this (sequence, head group) begins
     // The queries of the unit `use` as the right operand, 16 columns a step.
@@ -288,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, Geo<DM>::kCtas) paged_mma_kernel(Pag
     };
 #pragma unroll
     for (int i = 0; i < G::kStages; ++i) {
-      start_copies(i);
+      copies.start(a, load, load.tile * kPagedTile + warp * kRows, i);
       if (load.left > 0) load.next(a, heads);
     }
     fetch_queries();
@@ -369,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, Geo<DM>::kCtas) paged_mma_kernel(Pag
         }
       }
       __syncwarp();
-      start_copies(st);
+      copies.start(a, load, load.tile * kPagedTile + warp * kRows, st);
       if (load.left > 0) load.next(a, heads);
       st = st + 1 == G::kStages ? 0 : st + 1;
 

@@ -1,0 +1,163 @@
+// paged_ring.cuh -- a warp's stream of cache rows through shared memory: 16-byte asynchronous
+// copies of one tile of tokens after another, over the borders of sequences and heads, some
+// tiles ahead of their use.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "paged_common.cuh"
+
+namespace nf4 {
+
+// Pieces of 16 bytes lie XOR-swizzled by row, so that eight rows' pieces of one column lie in
+// different banks.
+template <int ROW_BYTES>
+__device__ __forceinline__ uint32_t at_chunk(int row, int chunk) {
+  return static_cast<uint32_t>(row * ROW_BYTES + ((chunk ^ (row & 7)) << 4));
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {  // zeros past `bytes`
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// The units of a run, one after another.
+struct Walk {
+  int64_t seq;
+  int left;  // units left in the run, this one among them (2^31 would be days of work)
+  int len, tiles, head, tile;
+
+  __device__ __forceinline__ Walk(const PagedArgs& a, const PagedRun& run, int heads) {
+    seq = run.seq;
+    left = static_cast<int>(run.u1 - run.u0 < INT32_MAX ? run.u1 - run.u0 : INT32_MAX);
+    len = paged_len(a, run.seq);
+    tiles = paged_tiles(len);
+    const int64_t r0 = run.u0 - run.before * heads;
+    head = static_cast<int>(divide(r0, tiles));
+    tile = static_cast<int>(r0 - static_cast<int64_t>(head) * tiles);
+  }
+
+  // The next unit with tokens; `heads` a tile.
+  __device__ __forceinline__ void next(const PagedArgs& a, int heads) {
+    --left;
+    if (++tile < tiles) return;
+    tile = 0;
+    if (++head < heads || left <= 0) return;
+    head = 0;
+    do {
+      ++seq;
+      len = seq < a.nseq ? paged_len(a, seq) : 1;
+      tiles = paged_tiles(len);
+    } while (tiles == 0);
+  }
+};
+
+// The copies of a tile of ROWS tokens, keys and then values, rows of W values; columns past D
+// and rows past a length or without a page are zeros that nothing reads.  Lane i copies column
+// piece i % kPieces of rows i / kPieces and every kPer-th after it.
+template <typename T, int W, int ROWS>
+struct TileCopies {
+  static constexpr int kRowBytes = W * static_cast<int>(sizeof(T)), kPieces = kRowBytes / 16, kPer = 32 / kPieces;
+  static constexpr int kHalf = ROWS * kRowBytes, kStage = 2 * kHalf;
+  static_assert(kPieces >= 1 && kPer >= 1 && ROWS % 8 == 0 && ROWS <= 16, "a row a warp's copy at least");
+
+  uint32_t dst0;
+  uint32_t* s_valid;  // [ring slots]: which rows of a tile are tokens
+  int row0, col, groups;
+  bool in, one_page;
+
+  __device__ __forceinline__ TileCopies(const PagedArgs& a, uint32_t ring, uint32_t* valid, int groups_) {
+    const int lane = threadIdx.x & 31;
+    row0 = lane / kPieces;
+    col = lane % kPieces * (16 / static_cast<int>(sizeof(T)));
+    in = col < a.D;
+    one_page = a.page_size % ROWS == 0;  // a tile lies in one page
+    dst0 = ring + at_chunk<kRowBytes>(row0, lane % kPieces);
+    s_valid = valid;
+    groups = groups_;
+  }
+
+  // Starts the copies of the tokens from tok0 on of the unit `load` into ring slot `st`.
+  __device__ __forceinline__ void start(const PagedArgs& a, const Walk& load, int tok0, int st) const {
+    const int lane = threadIdx.x & 31, rows = load.len - tok0, hk = groups == 1 ? load.head : load.head / groups;
+    if (load.left > 0 && rows > 0) {
+      const uint32_t to = dst0 + st * kStage;
+      // a row's swizzle repeats after eight rows
+      auto dst = [&](int i) { return (i * kPer % 8 == 0 ? to : to ^ (i * kPer % 8 << 4)) + i * kPer * kRowBytes; };
+      const T* none = static_cast<const T*>(a.q);
+      constexpr unsigned kFull = (1u << ROWS) - 1u;
+      unsigned valid;
+      if (one_page) {
+        int slot;
+        const int64_t page = paged_slot(a, load.seq, tok0, &slot);
+        const int n = page < 0 ? 0 : rows;
+        valid = n >= ROWS ? kFull : (1u << n) - 1u;
+        const T *kp = none, *vp = none;
+        int64_t ks = 0, vs = 0;
+        if (in && page >= 0) {
+          kp = static_cast<const T*>(a.k) + (page * a.k_page + (slot + row0) * a.k_token + hk * a.k_head + col);
+          vp = static_cast<const T*>(a.v) + (page * a.v_page + (slot + row0) * a.v_token + hk * a.v_head + col);
+          ks = kPer * a.k_token;
+          vs = kPer * a.v_token;
+        }
+        if (n >= ROWS) {
+          const int bytes = in ? 16 : 0;
+#pragma unroll
+          for (int i = 0; i < ROWS / kPer; ++i) {
+            copy16(dst(i), kp, bytes);
+            copy16(dst(i) + kHalf, vp, bytes);
+            kp += ks;
+            vp += vs;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < ROWS / kPer; ++i) {
+            const bool row = in && i * kPer + row0 < n;
+            copy16(dst(i), row ? kp : none, row ? 16 : 0);
+            copy16(dst(i) + kHalf, row ? vp : none, row ? 16 : 0);
+            kp += ks;
+            vp += vs;
+          }
+        }
+      } else {
+        // lane i < 16 looks up the key row of token i, lane 16 + i its value row
+        const int tok = tok0 + (lane & (ROWS - 1));
+        int64_t at = 0;
+        bool ok = false;
+        if (tok < load.len) {
+          int slot;
+          const int64_t page = paged_slot(a, load.seq, tok, &slot);
+          ok = page >= 0;
+          if (ok)
+            at = lane < 16 ? page * a.k_page + slot * a.k_token + hk * a.k_head
+                           : page * a.v_page + slot * a.v_token + hk * a.v_head;
+        }
+        valid = __ballot_sync(0xffffffffu, ok) & kFull;
+#pragma unroll
+        for (int i = 0; i < ROWS / kPer; ++i) {
+          const int r = i * kPer + row0;
+          const int64_t ak = __shfl_sync(0xffffffffu, at, r), av = __shfl_sync(0xffffffffu, at, r + 16);
+          const int bytes = (valid >> r & 1) && in ? 16 : 0;
+          copy16(dst(i), bytes ? static_cast<const T*>(a.k) + ak + col : none, bytes);
+          copy16(dst(i) + kHalf, bytes ? static_cast<const T*>(a.v) + av + col : none, bytes);
+        }
+      }
+      if (lane == 0) s_valid[st] = valid;
+    }
+    copies_commit();
+  }
+};
+
+}  // namespace nf4

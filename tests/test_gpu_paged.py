@@ -103,6 +103,22 @@ def test_attention_fp32(Hq, Hk, D):
 def test_attention_pages(page, order):
     kp, vp, table, lengths = cache([700, 99, 1, 0, 333], 2, 64, BF16, page=page, order=order, seed=page)
     check(queries(5, 8, 64, BF16), kp, vp, table, lengths, path="paged_attention")
+    for D in (64, 100, 128):
+        kp, vp, table, lengths = cache([700, 99, 1, 0, 333], 2, D, F32, page=page, order=order, seed=page)
+        check(queries(5, 8, D, F32), kp, vp, table, lengths, path="paged_attention_any")
+
+
+@pytest.mark.parametrize("Hq,Hk", [(1, 1), (4, 4), (8, 2), (5, 1), (16, 2), (9, 1), (20, 1)])
+@pytest.mark.parametrize("D", [4, 20, 64, 68, 128])
+def test_attention_fp32_heads(Hq, Hk, D):
+    """Groups of one to twenty heads, widths that fill a row of the ring and do not; rows that no 16-byte copy can take."""
+    lens = [331, 7, 64, 0, 1500]
+    kp, vp, table, lengths = cache(lens, Hk, D, F32, seed=D)
+    q = queries(5, Hq, D, F32)
+    check(q, kp, vp, table, lengths)
+    odd = torch.zeros(kp.numel() + 1, device=DEV)[1:].view(kp.shape)
+    odd.copy_(kp)
+    check(q, odd, vp, table, lengths)
 
 
 @pytest.mark.parametrize("n", [33, 300, 1500])
