@@ -55,8 +55,8 @@ def _workspace(op: int, M: int, N: int, device: torch.device) -> int:
 
 
 @functools.lru_cache(maxsize=64)
-def _workspace3(op: int, M: int, N: int, K: int, device: torch.device) -> int:
-    return workspace_size(op, M, N, K)
+def _workspace5(op: int, M: int, N: int, K: int, E: int, device: torch.device) -> int:
+    return workspace_size(op, M, N, K, E)
 
 
 def _one_device(name: str, *ts):

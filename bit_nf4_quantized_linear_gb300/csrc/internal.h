@@ -161,23 +161,45 @@ struct PagedArgs {
   int max_pages, page_size, Hq, Hk, D;
   unsigned page_mul, page_shift;  // p / page_size = p * page_mul >> page_shift for p < 2^31
   float scale;
-  float* part;  // partial results [CTAs][2][heads of a unit][paged_part_stride(D)]
+  float* part;  // partial results [CTAs][2][query heads of a set][paged_part_stride(D)]
   struct PagedRec* rec;  // [CTAs]
   int* status;
 };
-// What a CTA left in the partial results: slot 1 holds a unit run that begins a (sequence,
-// head group) and goes on in a later CTA, slot 0 one that began in an earlier CTA.
+// What a CTA left in the partial results: slot 1 holds a run of units that begins a (sequence,
+// head set) and goes on in a later CTA, slot 0 one that began in an earlier CTA.
 struct PagedRec {
   int64_t seq;
-  int32_t head;   // of slot 1: key head x groups of query heads + group
-  int32_t flags;  // 1: slot 1 is in use; 2: slot 0 is; 4: slot 0 ends its (sequence, head group)
+  int32_t set;    // of slot 1
+  int32_t flags;  // 1: slot 1 is in use; 2: slot 0 is; 4: slot 0 ends its (sequence, head set)
 };
 // floats of one head's partial result: D sums, maximum (base 2), sum of weights
 inline __host__ __device__ int paged_part_stride(int D) { return (D + 3) / 4 * 4 + 4; }
-constexpr int kPagedSlots = 64;  // partial results of single heads a SM at most
-constexpr int kPagedCtas = 4;    // CTAs a SM at most
-inline size_t paged_ws_bytes(int D, int sms) {
-  return static_cast<size_t>(sms) * (kPagedSlots * paged_part_stride(D) * sizeof(float) + kPagedCtas * sizeof(PagedRec));
+// How a kernel shares out the heads: groups of `group` query heads, `wh` of them a CTA.
+struct PagedShape {
+  int group, groups, wh, ctas;  // ctas: a SM
+};
+// Several heads a CTA where a token's heads lie together (`together`; ragged batch of 463,000
+// tokens, 8 heads of 128: 275 us against 297 with all warps on one head), else one, whose tokens do (24
+// sequences, 32 heads of 64: 76 us against 67).
+inline PagedShape paged_shape(int G, int Hk, int group, int warps, int ctas, bool together) {
+  PagedShape s{group, (G + group - 1) / group, 1, ctas};
+  while (together && s.wh < warps && Hk * s.groups % (2 * s.wh) == 0) s.wh *= 2;
+  return s;
+}
+inline size_t paged_part_bytes(const PagedShape& s, int D) {  // of a SM
+  return static_cast<size_t>(s.ctas) * (2 * s.wh * s.group * paged_part_stride(D) * sizeof(float) + sizeof(PagedRec));
+}
+PagedShape paged_shape_mma(int G, int Hk, int D, bool together);
+PagedShape paged_shape_f32(int G, int Hk, int D, bool together);
+PagedShape paged_shape_any(int G, int Hk);
+constexpr int kPagedCtas = 4;  // CTAs a SM at most
+// enough for whichever kernel takes the call
+inline size_t paged_ws_bytes(int Hq, int Hk, int D, int sms) {
+  const int G = Hq / Hk;
+  size_t most = paged_part_bytes(paged_shape_any(G, Hk), D);
+  for (const PagedShape& s : {paged_shape_mma(G, Hk, D, true), paged_shape_f32(G, Hk, D, true)})
+    if (paged_part_bytes(s, D) > most) most = paged_part_bytes(s, D);
+  return static_cast<size_t>(sms) * (most + kPagedCtas * sizeof(PagedRec));
 }
 cudaError_t launch_paged_append(int dtype, const PagedArgs& a, int sms, cudaStream_t s);
 cudaError_t launch_paged_mma(bool f16, const PagedArgs& a, int sms, cudaStream_t s);

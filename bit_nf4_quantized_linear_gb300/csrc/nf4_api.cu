@@ -1136,7 +1136,7 @@ nf4_status nf4_paged_attention(const nf4_paged_cache* c, const void* q, int64_t 
   if (!aligned_to(q, e) || !aligned_to(o, e) || !aligned_to(lse, 4)) return NF4_ERR_ALIGNMENT;
   DevInfo dev;
   if (!current_device(&dev)) return cuda_fail(cudaGetLastError(), "device query");
-  if (!ws || ws_bytes < nf4::paged_ws_bytes(a.D, dev.sms)) return NF4_ERR_WORKSPACE;
+  if (!ws || ws_bytes < nf4::paged_ws_bytes(Hq, a.Hk, a.D, dev.sms)) return NF4_ERR_WORKSPACE;
   if (!aligned_to(ws, 16)) return NF4_ERR_ALIGNMENT;
   a.q = q;
   a.q_s = q_seq;
@@ -1610,7 +1610,6 @@ nf4_status nf4_grouped_swiglu_bwd(const void* x, const int32_t* offsets, int32_t
 }
 
 size_t nf4_workspace_size(int32_t op, int64_t M, int64_t N, int64_t K, int32_t E) {
-  (void)E;
   if (op == NF4_OP_GROUPED_SWIGLU_BWD) {
     if (M <= 0 || N <= 0) return 0;
     return swiglu_bwd_dgu_bytes(M, N) + static_cast<size_t>(N / 64) * M * sizeof(float);
@@ -1628,7 +1627,7 @@ size_t nf4_workspace_size(int32_t op, int64_t M, int64_t N, int64_t K, int32_t E
   if (op == NF4_OP_PAGED_ATTENTION || op == NF4_OP_ROUTE) {
     DevInfo dev;
     if (!current_device(&dev)) return 0;
-    if (op == NF4_OP_PAGED_ATTENTION) return K < 1 || K > 256 ? 0 : nf4::paged_ws_bytes(static_cast<int>(K), dev.sms);
+    if (op == NF4_OP_PAGED_ATTENTION) return K < 1 || K > 256 || E < 1 || N < E || N > 65535 || N % E != 0 ? 0 : nf4::paged_ws_bytes(static_cast<int>(N), E, static_cast<int>(K), dev.sms);
     return M <= 0 || N <= 0 || N > nf4::kMaxExperts ? 0 : nf4::route_ws_bytes(M, static_cast<int>(N), dev.sms);
   }
   if (op == NF4_OP_QUANTIZE) {

@@ -87,6 +87,7 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(PagedArgs 
 // tokens' rows 32 columns apart, form the partial products with HC query heads, and reduce the
 // 32 sums of (token, head) so that lane i ends with sum i, in 31 shuffles.
 constexpr int kAnyWarps = 8;
+constexpr int kAnyTile = 6;  // log2 of the tokens of a unit, all warps on one head
 
 template <typename T, int HC, int DV>
 __global__ void __launch_bounds__(kAnyWarps * 32) paged_any_kernel(PagedArgs a, int groups) {
@@ -100,23 +101,16 @@ __global__ void __launch_bounds__(kAnyWarps * 32) paged_any_kernel(PagedArgs a, 
   grid_allow();
   grid_wait();
   paged_empty<T>(a);
-  const int heads = a.Hk * groups, G = a.Hq / a.Hk;
-  PagedRun run = paged_run(a, heads, s_red);
+  const int G = a.Hq / a.Hk;
+  Walk use = paged_run(a, a.Hk * groups, kAnyTile, s_red);
   PagedRec rec{0, 0, 0};
   const T* kp = static_cast<const T*>(a.k);
   const T* vp = static_cast<const T*>(a.v);
 
-  int64_t u = run.u0, seq = run.seq, before = run.before;
-  while (u < run.u1 && seq < a.nseq) {
-    const int len = paged_len(a, seq), n = paged_tiles(len);
-    if (n == 0) {
-      ++seq;
-      continue;
-    }
-    const int64_t r = u - before * heads;
-    const int head = static_cast<int>(divide(r, n)), t0 = static_cast<int>(r - static_cast<int64_t>(head) * n);
-    const int t1 = n - t0 < run.u1 - u ? n : t0 + static_cast<int>(run.u1 - u);
-    const int hk = head / groups, g0 = head % groups * HC, nh = G - g0 < HC ? G - g0 : HC;
+  while (use.left > 0) {
+    const int64_t seq = use.seq;
+    const int len = use.len, n = use.tiles, t0 = use.tile, t1 = n - t0 < use.left ? n : t0 + use.left;
+    const int hk = use.set / groups, g0 = use.set % groups * HC, nh = G - g0 < HC ? G - g0 : HC;
     const int64_t hq = static_cast<int64_t>(hk) * G + g0;
 
     __syncthreads();  // the last run's readers are done
@@ -131,8 +125,8 @@ __global__ void __launch_bounds__(kAnyWarps * 32) paged_any_kernel(PagedArgs a, 
     for (int h = 0; h < HC; ++h)
 #pragma unroll
       for (int i = 0; i < DV; ++i) acc[h][i] = 0.0f;
-    const int64_t end = static_cast<int64_t>(t1) * kPagedTile < len ? static_cast<int64_t>(t1) * kPagedTile : len;
-    for (int64_t tb = static_cast<int64_t>(t0) * kPagedTile + warp * NT; tb < end; tb += kAnyWarps * NT) {
+    const int64_t end = (static_cast<int64_t>(t1) << kAnyTile) < len ? static_cast<int64_t>(t1) << kAnyTile : len;
+    for (int64_t tb = (static_cast<int64_t>(t0) << kAnyTile) + warp * NT; tb < end; tb += kAnyWarps * NT) {
       int64_t at_k = -1, at_v = -1;
       if (lane < NT && tb + lane < end) {
         int slot;
@@ -267,13 +261,11 @@ __global__ void __launch_bounds__(kAnyWarps * 32) paged_any_kernel(PagedArgs a, 
     if (t0 == 0 && t1 < n) {
       rec.flags |= 1;
       rec.seq = seq;
-      rec.head = head;
+      rec.set = use.set;
     }
-    u += t1 - t0;
-    if (t1 == n && head == heads - 1) {
-      before += n;
-      ++seq;
-    }
+    use.left -= t1 - t0 - 1;
+    use.tile = t1 - 1;
+    use.next(a);
   }
   if (threadIdx.x == 0) a.rec[blockIdx.x] = rec;
 }
@@ -283,13 +275,12 @@ constexpr int kAnyCtas = 2;  // a SM: what the registers leave room for
 template <typename T, int HC, int DV>
 cudaError_t launch_any(const PagedArgs& a, int sms, cudaStream_t s) {
   static SmemLimit limit;
-  static_assert(kAnyCtas * 2 * HC <= kPagedSlots && kAnyCtas <= kPagedCtas, "workspace");
   auto kern = paged_any_kernel<T, HC, DV>;
   const int smem = 5 * HC * DV * 32 * static_cast<int>(sizeof(float));
   if (cudaError_t e = limit.allow(kern, smem)) return e;
   const int groups = (a.Hq / a.Hk + HC - 1) / HC;
   if (cudaError_t e = launch_early(kern, dim3(static_cast<unsigned>(kAnyCtas * sms)), kAnyWarps * 32, smem, s, a, groups)) return e;
-  return launch_paged_join<T>(a, kAnyCtas * sms, HC, groups, s);
+  return launch_paged_join<T>(a, kAnyCtas * sms, HC, groups, 1, s);
 }
 
 template <typename T, int HC>
@@ -305,6 +296,8 @@ cudaError_t launch_any_heads(const PagedArgs& a, int sms, cudaStream_t s) {
 }
 
 }  // namespace
+
+PagedShape paged_shape_any(int G, int Hk) { return paged_shape(G, Hk, G <= 4 ? 4 : 8, 1, kAnyCtas, false); }
 
 cudaError_t launch_paged_any(int dtype, const PagedArgs& a, int sms, cudaStream_t s) {
   if (dtype == NF4_DTYPE_F32) return launch_any_heads<float>(a, sms, s);

@@ -23,26 +23,28 @@
 namespace nf4 {
 namespace {
 
+#ifndef F32S
+#define F32S 2
+#endif
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kRows = kPagedTile / kWarps;  // tokens of a warp's tile
-static_assert(kRows == 8, "a lane a token and quarter");
+constexpr int kRows = 8;  // tokens of a warp's tile: a lane a token and quarter of its columns
 
 template <int DM, int HC>
 struct Geo {
-  static constexpr int kStages = 3;
+  static constexpr int kStages = F32S;
   static constexpr int kCtas = DM == 64 ? 2 : 1;  // a SM
   static constexpr int kPitch = DM + 4;           // floats between heads of a warp's sums
   static constexpr int kRing = kWarps * kStages * TileCopies<float, DM, kRows>::kStage;
   static constexpr int kSums = kWarps * 4 * kPitch * 4;  // four heads at a time
-  static constexpr int kQ = HC * DM * 4;
+  static constexpr int kQ = kWarps * HC * DM * 4;
   static constexpr int kP = kWarps * kRows * HC * 4;
   static constexpr int kMl = kWarps * HC * 8;
   static constexpr int kSmem = kRing + kSums + kQ + kP + kMl + kWarps * kStages * 4;
 };
 
 template <int DM, int HC>
-__global__ void __launch_bounds__(kThreads, Geo<DM, HC>::kCtas) paged_f32_kernel(PagedArgs a, int groups) {
+__global__ void __launch_bounds__(kThreads, Geo<DM, HC>::kCtas) paged_f32_kernel(PagedArgs a, int groups, int log2_wh) {
   using G = Geo<DM, HC>;
   using Copies = TileCopies<float, DM, kRows>;
   constexpr int HL = HC / 4;          // heads of a quarter's lanes
@@ -50,35 +52,45 @@ __global__ void __launch_bounds__(kThreads, Geo<DM, HC>::kCtas) paged_f32_kernel
   constexpr int TP = 128 / DM;        // tokens that a warp's read of one piece a lane covers
   extern __shared__ __align__(128) unsigned char dyn[];
   float* s_sum = reinterpret_cast<float*>(dyn + G::kRing);          // [kWarps][4][kPitch]
-  float* s_q = reinterpret_cast<float*>(dyn + G::kRing + G::kSums); // [HC][DM]
-  float* s_p = s_q + HC * DM;                                       // [kWarps][kRows][HC]
+  float* s_q = reinterpret_cast<float*>(dyn + G::kRing + G::kSums); // [kWarps][HC][DM]
+  float* s_p = s_q + kWarps * HC * DM;                              // [kWarps][kRows][HC]
   float2* s_ml = reinterpret_cast<float2*>(s_p + kWarps * kRows * HC);  // [kWarps][HC]
   uint32_t* s_valid = reinterpret_cast<uint32_t*>(s_ml + kWarps * HC);  // [kWarps][kStages]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int wh = 1 << log2_wh, wt = kWarps >> log2_wh, my_head = warp & (wh - 1), my_tile = warp >> log2_wh;
   const unsigned char* ring = dyn + warp * G::kStages * Copies::kStage;
+  s_q += warp * HC * DM;
   s_p += warp * kRows * HC;
   s_valid += warp * G::kStages;
   grid_allow();
   grid_wait();
-  const int heads = a.Hk * groups, GQ = a.Hq / a.Hk;
-  const PagedRun run = paged_run(a, heads, reinterpret_cast<int64_t*>(s_sum));
+  const int GQ = a.Hq / a.Hk;
+  Walk load = paged_run(a, a.Hk * groups >> log2_wh, 6 - log2_wh, reinterpret_cast<int64_t*>(s_sum));  // 8 wt tokens a unit
+  Walk use = load;
   PagedRec rec{0, 0, 0};
 
-  if (run.u0 < run.u1) {
-    Walk load(a, run, heads);
-    Walk use = load;
-    const Copies copies(a, nf4ptx::smem_addr(ring), s_valid, groups);
-#pragma unroll
-    for (int i = 0; i < G::kStages; ++i) {
-      copies.start(a, load, load.tile * kPagedTile + warp * kRows, i);
-      if (load.left > 0) load.next(a, heads);
-    }
+  if (use.left > 0) {
+    const Copies copies(a, nf4ptx::smem_addr(ring), s_valid);
+    // The key head of this warp in a head set, and its first query head's place in the group.
+    auto place = [&](int set, int* g0) {
+      const int head = (set << log2_wh) + my_head, hk = groups == 1 ? head : head / groups;
+      *g0 = (head - hk * groups) * HC;
+      return hk;
+    };
+    auto first_token = [&](const Walk& w) { return (w.tile << w.log2_tile) + my_tile * kRows; };
+    auto start_copies = [&](int st) {
+      int g0;
+      copies.start(a, load, first_token(load), place(load.set, &g0), st);
+      if (load.left > 0) load.next(a);
+    };
     auto fetch_queries = [&]() {
-      const int hk = groups == 1 ? use.head : use.head / groups, g0 = (use.head - hk * groups) * HC;
+      int g0;
+      const int hk = place(use.set, &g0);
       const float* q = static_cast<const float*>(a.q) + use.seq * a.q_s + (static_cast<int64_t>(hk) * GQ + g0) * a.q_h;
-      for (int i = threadIdx.x; i < HC * DM; i += kThreads) {
-        const int h = i / DM, d = i % DM;
-        s_q[i] = g0 + h < GQ && d < a.D ? q[h * a.q_h + d] : 0.0f;
+#pragma unroll
+      for (int i = 0; i < HC * DM / 32; ++i) {
+        const int h = i * 32 / DM, d = (i * 32 + lane) % DM;
+        s_q[i * 32 + lane] = g0 + h < GQ && d < a.D ? q[h * a.q_h + d] : 0.0f;
       }
     };
     // lane (t, r): token t = lane % 8; as quarter r = lane / 8 it keeps heads r HL .. r HL + HL - 1
@@ -95,15 +107,16 @@ __global__ void __launch_bounds__(kThreads, Geo<DM, HC>::kCtas) paged_f32_kernel
       }
     };
     const float c = a.scale * kLog2e;
+#pragma unroll
+    for (int i = 0; i < G::kStages; ++i) start_copies(i);
     fetch_queries();
     clear_sums();
     paged_empty<float>(a);
-    __syncthreads();
-    int st = 0, tile0 = use.tile;  // where the part of this (sequence, head group) begins
+    int st = 0, tile0 = use.tile;  // where the part of this (sequence, head set) begins
     while (use.left > 0) {
       copies_wait<G::kStages - 1>();
       __syncwarp();
-      if (use.tile * kPagedTile + warp * kRows < use.len) {
+      if (first_token(use) < use.len) {
         const unsigned char* keys = ring + st * Copies::kStage;
         const unsigned char* values = keys + Copies::kHalf;
         float2 s2[HC];
@@ -180,21 +193,29 @@ __global__ void __launch_bounds__(kThreads, Geo<DM, HC>::kCtas) paged_f32_kernel
         }
       }
       __syncwarp();
-      copies.start(a, load, load.tile * kPagedTile + warp * kRows, st);
-      if (load.left > 0) load.next(a, heads);
+      start_copies(st);
       st = st + 1 == G::kStages ? 0 : st + 1;
 
       const bool ends = use.tile + 1 == use.tiles;
       if (!ends && use.left > 1) {
-        use.next(a, heads);
+        use.next(a);
         continue;
       }
-      // The part of this (sequence, head group) is done: add the warps' sums, four heads at a time.
-      const Walk was = use;
-      use.next(a, heads);
-      const int hk = groups == 1 ? was.head : was.head / groups, g0 = (was.head - hk * groups) * HC;
+      // The part of this (sequence, head set) is done: its outputs, or its sums.
+      int g0;
+      const int hk = place(use.set, &g0);
+      const int64_t seq = use.seq;
       const bool whole = ends && tile0 == 0;
       const int stride = paged_part_stride(a.D);
+      if (tile0 > 0) rec.flags |= ends ? 6 : 2;
+      if (tile0 == 0 && !ends) {
+        rec.flags |= 1;
+        rec.seq = seq;
+        rec.set = use.set;
+      }
+      float* part = a.part + (static_cast<int64_t>(blockIdx.x * 2 + (tile0 == 0)) * (HC << log2_wh) + my_head * HC) * stride;
+      use.next(a);
+      if (use.left > 0) fetch_queries();
 #pragma unroll
       for (int j = 0; j < HL; ++j) {
 #pragma unroll
@@ -211,52 +232,43 @@ __global__ void __launch_bounds__(kThreads, Geo<DM, HC>::kCtas) paged_f32_kernel
           }
       }
 #pragma unroll
-      for (int n = 0; n < HC; n += 4) {
+      for (int n = 0; n < HC; n += 4) {  // four heads at a time
         if (lane < DM / 4)
 #pragma unroll
           for (int h = 0; h < 4; ++h)
             *reinterpret_cast<float4*>(s_sum + (warp * 4 + h) * G::kPitch + lane * 4) =
                 make_float4(acc[n + h][0].x, acc[n + h][0].y, acc[n + h][1].x, acc[n + h][1].y);
-        __syncthreads();
-        if (n == 0 && use.left > 0) fetch_queries();
-        const int h = threadIdx.x >> 6, hn = n + h;  // 64 threads a head
-        if (g0 + hn < GQ) {
-          float top = -INFINITY, sum = 0.0f, f[kWarps];
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w * HC + hn].x);
+        if (wt > 1) __syncthreads();
+        else __syncwarp();
+        // the warps of a head take its four query heads' columns in turn
+        for (int i = my_tile * 32 + lane; i < 4 * DM; i += wt * 32) {
+          const int h = i / DM, d = i % DM, hn = n + h;
+          if (g0 + hn >= GQ) break;
+          float top = -INFINITY, sum = 0.0f, v = 0.0f;
+          for (int w = my_head; w < kWarps; w += wh) top = fmaxf(top, s_ml[w * HC + hn].x);
           const float mm = top == -INFINITY ? 0.0f : top;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
+          for (int w = my_head; w < kWarps; w += wh) {
             const float2 ml = s_ml[w * HC + hn];
-            f[w] = exp2_fast(ml.x - mm);
-            sum += ml.y * f[w];
+            const float f = exp2_fast(ml.x - mm);
+            sum += ml.y * f;
+            v += s_sum[(w * 4 + h) * G::kPitch + d] * f;
           }
           const int64_t hq = static_cast<int64_t>(hk) * GQ + g0 + hn;
-          float* o = static_cast<float*>(a.o) + was.seq * a.o_s + hq * a.o_h;
-          float* part = a.part + (static_cast<int64_t>(blockIdx.x * 2 + (tile0 == 0)) * HC + hn) * stride;
-          for (int d = threadIdx.x & 63; d < a.D; d += 64) {
-            float v = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) v += s_sum[(w * 4 + h) * G::kPitch + d] * f[w];
-            if (whole) o[d] = v / sum;
-            else part[d] = v;
+          if (d < a.D) {
+            if (whole) static_cast<float*>(a.o)[seq * a.o_s + hq * a.o_h + d] = v / sum;
+            else part[hn * stride + d] = v;
           }
-          if ((threadIdx.x & 63) == 0) {
-            if (whole) {
-              if (a.lse) a.lse[was.seq * a.Hq + hq] = top * kLn2 + logf(sum);
-            } else {
-              part[stride - 4] = top;
-              part[stride - 3] = sum;
+          if (d == 0) {
+            if (!whole) {
+              part[hn * stride + stride - 4] = top;
+              part[hn * stride + stride - 3] = sum;
+            } else if (a.lse) {
+              a.lse[seq * a.Hq + hq] = top * kLn2 + logf(sum);
             }
           }
         }
-        __syncthreads();
-      }
-      if (tile0 > 0) rec.flags |= ends ? 6 : 2;
-      if (tile0 == 0 && !ends) {
-        rec.flags |= 1;
-        rec.seq = was.seq;
-        rec.head = was.head;
+        if (wt > 1) __syncthreads();
+        else __syncwarp();
       }
       tile0 = use.tile;
       clear_sums();
@@ -268,20 +280,28 @@ __global__ void __launch_bounds__(kThreads, Geo<DM, HC>::kCtas) paged_f32_kernel
   if (threadIdx.x == 0) a.rec[blockIdx.x] = rec;
 }
 
+inline int log2_of(int n) {
+  int l = 0;
+  while (n >> (l + 1)) ++l;
+  return l;
+}
+
 template <int DM, int HC>
 cudaError_t launch(const PagedArgs& a, int sms, cudaStream_t s) {
   using G = Geo<DM, HC>;
   static SmemLimit limit;
-  static_assert(G::kCtas * 2 * HC <= kPagedSlots && G::kCtas <= kPagedCtas, "workspace");
   static_assert(G::kSmem <= (G::kCtas == 1 ? 227 : 113) * 1024, "shared memory");
   auto kern = paged_f32_kernel<DM, HC>;
   if (cudaError_t e = limit.allow(kern, G::kSmem)) return e;
-  const int groups = (a.Hq / a.Hk + HC - 1) / HC, ctas = G::kCtas * sms;
-  if (cudaError_t e = launch_early(kern, dim3(static_cast<unsigned>(ctas)), kThreads, G::kSmem, s, a, groups)) return e;
-  return launch_paged_join<float>(a, ctas, HC, groups, s);
+  const PagedShape p = paged_shape_f32(a.Hq / a.Hk, a.Hk, a.D, a.k_head < a.k_token);
+  const int ctas = p.ctas * sms;
+  if (cudaError_t e = launch_early(kern, dim3(static_cast<unsigned>(ctas)), kThreads, G::kSmem, s, a, p.groups, log2_of(p.wh))) return e;
+  return launch_paged_join<float>(a, ctas, HC, p.groups, p.wh, s);
 }
 
 }  // namespace
+
+PagedShape paged_shape_f32(int G, int Hk, int D, bool together) { return paged_shape(G, Hk, G > 4 ? 8 : 4, kWarps, D <= 64 ? 2 : 1, together); }
 
 // D a multiple of 4 up to 128, all rows 16-byte aligned.
 cudaError_t launch_paged_f32(const PagedArgs& a, int sms, cudaStream_t s) {

@@ -7,11 +7,10 @@
 // and key head against 4 D operations a query head; mma.sync's rate is some ten times what
 // that needs, and its operands come from shared memory as the copies left them.
 //
-// A CTA of four warps takes its run of units (paged_common.cuh) 64 tokens at a time, 16 a
-// warp.  Each warp streams its tokens' rows through a ring of its own with 16-byte
-// asynchronous copies (a table look-up a token, so any page size and order), over the borders
-// of sequences and heads, with no barrier in the loop: the warps meet only where a (sequence,
-// head group) ends, to add their sums.  Rows past a length are zeros that no copy reads.
+// A CTA's four warps share out heads or tokens (paged_common.cuh), 16 tokens a warp's tile.  Each
+// warp streams its tokens' rows through a ring of its own (paged_ring.cuh), over the borders of
+// sequences and head sets, with no barrier in the loop; where several warps share a head they meet
+// as it ends, to add their sums.
 // S is fp32; P is held as two values of the operands' type, p and what its rounding left (a
 // second MMA that costs nothing here), so the result sees one rounding, its own.  fp16 weights
 // are held times 2^7, out of the subnormal range.
@@ -34,13 +33,18 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kRows = kPagedTile / kWarps;  // tokens of a warp's tile
-static_assert(kRows == 16, "the MMA's rows");
+constexpr int kRows = 16;  // tokens of a warp's tile: the MMA's rows
 
+#ifndef V64S
+#define V64S 4
+#define V64C 2
+#define V128S 2
+#define V128C 2
+#endif
 template <int DM>
 struct Geo {
-  static constexpr int kStages = DM == 64 ? 6 : 3;
-  static constexpr int kCtas = DM <= 128 ? 2 : 1;   // a SM
+  static constexpr int kStages = DM == 64 ? V64S : DM == 128 ? V128S : 3;
+  static constexpr int kCtas = DM == 64 ? V64C : DM == 128 ? V128C : 1;  // a SM
   static constexpr int kHalf = kRows * DM * 2;      // bytes of a tile's keys
   static constexpr int kStage = 2 * kHalf;
   static constexpr int kPitch = DM + 4;             // floats between heads of a warp's sums
@@ -101,7 +105,7 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t* hi, uint32_t*
 }
 
 template <bool F16, int DM, int NT>
-__global__ void __launch_bounds__(kThreads, Geo<DM>::kCtas) paged_mma_kernel(PagedArgs a, int groups) {
+__global__ void __launch_bounds__(kThreads, Geo<DM>::kCtas) paged_mma_kernel(PagedArgs a, int groups, int log2_wh) {
   using G = Geo<DM>;
   using T = typename std::conditional<F16, __half, __nv_bfloat16>::type;
   constexpr int HC = 8 * NT, KS = DM / 16;
@@ -109,21 +113,33 @@ __global__ void __launch_bounds__(kThreads, Geo<DM>::kCtas) paged_mma_kernel(Pag
   extern __shared__ __align__(128) unsigned char dyn[];
   float* s_sum = reinterpret_cast<float*>(dyn + G::kRing);                          // [kWarps][8][kPitch]
   float2* s_ml = reinterpret_cast<float2*>(dyn + G::kRing + G::kSums);              // [kWarps][8]
-  uint32_t* s_valid = reinterpret_cast<uint32_t*>(s_ml + kWarps * 8);              // [kWarps][kStages]
+  uint32_t* s_valid = reinterpret_cast<uint32_t*>(s_ml + kWarps * 8);               // [kWarps][kStages]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int wh = 1 << log2_wh, wt = kWarps >> log2_wh, my_head = warp & (wh - 1), my_tile = warp >> log2_wh;
   const uint32_t ring = nf4ptx::smem_addr(dyn) + warp * G::kStages * G::kStage;
   s_valid += warp * G::kStages;
   grid_allow();
   grid_wait();
-  const int heads = a.Hk * groups, GQ = a.Hq / a.Hk;
-  const PagedRun run = paged_run(a, heads, reinterpret_cast<int64_t*>(s_sum));
+  const int GQ = a.Hq / a.Hk;
+  Walk load = paged_run(a, a.Hk * groups >> log2_wh, 6 - log2_wh, reinterpret_cast<int64_t*>(s_sum));  // 16 wt tokens a unit
+  Walk use = load;
   PagedRec rec{0, 0, 0};
 
-  if (run.u0 < run.u1) {
-    Walk load(a, run, heads);
-    Walk use = load;
+  if (use.left > 0) {
+    const TileCopies<T, DM, kRows> copies(a, ring, s_valid);
+    // The key head of this warp in a head set, and its first query head's place in the group.
+    auto place = [&](int set, int* g0) {
+      const int head = (set << log2_wh) + my_head, hk = groups == 1 ? head : head / groups;
+      *g0 = (head - hk * groups) * HC;
+      return hk;
+    };
+    auto first_token = [&](const Walk& w) { return (w.tile << w.log2_tile) + my_tile * kRows; };
+    auto start_copies = [&](int st) {
+      int g0;
+      copies.start(a, load, first_token(load), place(load.set, &g0), st);
+      if (load.left > 0) load.next(a);
+    };
 
-    const TileCopies<T, DM, kRows> copies(a, ring, s_valid, groups);
     uint32_t qf[NT][KS][2];
     float acc[NT][KS][4], m[NT][2], l[NT][2];
     const float c = a.scale * kLog2e;
@@ -135,10 +151,11 @@ __global__ void __launch_bounds__(kThreads, Geo<DM>::kCtas) paged_mma_kernel(Pag
       k_off[s] = ring + at_chunk<DM * 2>(lane & 15, 2 * s + (lane >> 4));
       v_off[s] = ring + G::kHalf + at_chunk<DM * 2>((lane & 7) + (lane >> 4 << 3), 2 * s + (lane >> 3 & 1));
     }
-    int tile0 = use.tile;  // where the part of this (sequence, head group) begins
+    int tile0 = use.tile;  // where the part of this (sequence, head set) begins
     // The queries of the unit `use` as the right operand, 16 columns a step.
     auto fetch_queries = [&]() {
-      const int hk = groups == 1 ? use.head : use.head / groups, g0 = (use.head - hk * groups) * HC;
+      int g0;
+      const int hk = place(use.set, &g0);
       const T* q = static_cast<const T*>(a.q) + use.seq * a.q_s + (static_cast<int64_t>(hk) * GQ + g0 + lane / 4) * a.q_h + (lane & 3) * 2;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -162,10 +179,7 @@ __global__ void __launch_bounds__(kThreads, Geo<DM>::kCtas) paged_mma_kernel(Pag
       }
     };
 #pragma unroll
-    for (int i = 0; i < G::kStages; ++i) {
-      copies.start(a, load, load.tile * kPagedTile + warp * kRows, i);
-      if (load.left > 0) load.next(a, heads);
-    }
+    for (int i = 0; i < G::kStages; ++i) start_copies(i);
     fetch_queries();
     clear_sums();
     paged_empty<T>(a);
@@ -173,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, Geo<DM>::kCtas) paged_mma_kernel(Pag
     while (use.left > 0) {
       copies_wait<G::kStages - 1>();
       __syncwarp();
-      if (use.tile * kPagedTile + warp * kRows < use.len) {
+      if (first_token(use) < use.len) {
         const uint32_t from = st * G::kStage;
         const unsigned valid = s_valid[st];
         float x[NT][4], x2[NT][4];  // two chains of MMAs
@@ -244,23 +258,30 @@ __global__ void __launch_bounds__(kThreads, Geo<DM>::kCtas) paged_mma_kernel(Pag
         }
       }
       __syncwarp();
-      copies.start(a, load, load.tile * kPagedTile + warp * kRows, st);
-      if (load.left > 0) load.next(a, heads);
+      start_copies(st);
       st = st + 1 == G::kStages ? 0 : st + 1;
 
       const bool ends = use.tile + 1 == use.tiles;
       if (!ends && use.left > 1) {
-        use.next(a, heads);
+        use.next(a);
         continue;
       }
-      // The part of this (sequence, head group) is done: add the warps' sums.  The next one's
+      // The part of this (sequence, head set) is done: its outputs, or its sums.  The next one's
       // queries are fetched meanwhile.
-      const Walk was = use;
-      use.next(a, heads);
-      if (use.left > 0) fetch_queries();
-      const int hk = groups == 1 ? was.head : was.head / groups, g0 = (was.head - hk * groups) * HC;
+      int g0;
+      const int hk = place(use.set, &g0);
+      const int64_t seq = use.seq;
       const bool whole = ends && tile0 == 0;
       const int stride = paged_part_stride(a.D);
+      if (tile0 > 0) rec.flags |= ends ? 6 : 2;
+      if (tile0 == 0 && !ends) {
+        rec.flags |= 1;
+        rec.seq = seq;
+        rec.set = use.set;
+      }
+      float* part = a.part + (static_cast<int64_t>(blockIdx.x * 2 + (tile0 == 0)) * (HC << log2_wh) + my_head * HC) * stride;
+      use.next(a);
+      if (use.left > 0) fetch_queries();
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -276,62 +297,55 @@ __global__ void __launch_bounds__(kThreads, Geo<DM>::kCtas) paged_mma_kernel(Pag
         for (int s = 0; s < KS; ++s)
 #pragma unroll
           for (int j = 0; j < 4; ++j) own[(j & 1) * G::kPitch + s * 16 + (j & 2) * 4] = acc[n][s][j];
-        __syncthreads();
-        // 16 threads a head, four columns at a time
-        const int h = threadIdx.x >> 4, hn = n * 8 + h;
-        if (g0 + hn < GQ) {
-          float top = -INFINITY, sum = 0.0f, f[kWarps];
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w * 8 + h].x);
-          const float mm = top == -INFINITY ? 0.0f : top;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            const float2 ml = s_ml[w * 8 + h];
-            f[w] = exp2_fast(ml.x - mm);
-            sum += ml.y * f[w];
-          }
-          const float inv = whole ? 1.0f / sum : 1.0f;
-          const int64_t hq = static_cast<int64_t>(hk) * GQ + g0 + hn;
-          T* o = static_cast<T*>(a.o) + was.seq * a.o_s + hq * a.o_h;
-          float* part = a.part + (static_cast<int64_t>(blockIdx.x * 2 + (tile0 == 0)) * HC + hn) * stride;
-#pragma unroll
-          for (int i = 0; i < DM / 64; ++i) {
-            const int d = i * 64 + (threadIdx.x & 15) * 4;
-            float v[4] = {};
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
+        if (wt > 1) __syncthreads();
+        else __syncwarp();
+        // the warps of a head take its query heads in turn, a lane four columns
+#pragma unroll 2
+        for (int i = lane; i < (8 / wt) * (DM / 4); i += 32) {
+          const int h = my_tile + wt * (i / (DM / 4)), d = i % (DM / 4) * 4, hn = n * 8 + h;
+          if (g0 + hn >= GQ) break;
+          float top = -INFINITY, sum = 0.0f;
+          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (wt == 1) {
+            const float2 ml = s_ml[warp * 8 + h];
+            top = ml.x;
+            sum = ml.y;
+            v = *reinterpret_cast<const float4*>(s_sum + (warp * 8 + h) * G::kPitch + d);
+          } else {
+            for (int w = my_head; w < kWarps; w += wh) top = fmaxf(top, s_ml[w * 8 + h].x);
+            const float mm = top == -INFINITY ? 0.0f : top;
+            for (int w = my_head; w < kWarps; w += wh) {
+              const float2 ml = s_ml[w * 8 + h];
+              const float f = exp2_fast(ml.x - mm);
               const float4 x = *reinterpret_cast<const float4*>(s_sum + (w * 8 + h) * G::kPitch + d);
-              v[0] += x.x * f[w];
-              v[1] += x.y * f[w];
-              v[2] += x.z * f[w];
-              v[3] += x.w * f[w];
-            }
-            if (d >= a.D) break;  // D is a multiple of 8
-            if (whole) {
-              __align__(8) T r[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) r[j] = from_f32<T>(v[j] * inv);
-              *reinterpret_cast<uint2*>(o + d) = *reinterpret_cast<const uint2*>(r);
-            } else {
-              *reinterpret_cast<float4*>(part + d) = make_float4(v[0], v[1], v[2], v[3]);
+              sum += ml.y * f;
+              v.x += x.x * f;
+              v.y += x.y * f;
+              v.z += x.z * f;
+              v.w += x.w * f;
             }
           }
-          if ((threadIdx.x & 15) == 0) {
+          const int64_t hq = static_cast<int64_t>(hk) * GQ + g0 + hn;
+          if (d < a.D) {  // D is a multiple of 8
             if (whole) {
-              if (a.lse) a.lse[was.seq * a.Hq + hq] = top * kLn2 + logf(sum);
+              const float inv = 1.0f / sum;
+              __align__(8) T r[4] = {from_f32<T>(v.x * inv), from_f32<T>(v.y * inv), from_f32<T>(v.z * inv), from_f32<T>(v.w * inv)};
+              *reinterpret_cast<uint2*>(static_cast<T*>(a.o) + seq * a.o_s + hq * a.o_h + d) = *reinterpret_cast<const uint2*>(r);
             } else {
-              part[stride - 4] = top;
-              part[stride - 3] = sum;
+              *reinterpret_cast<float4*>(part + hn * stride + d) = v;
+            }
+          }
+          if (d == 0) {
+            if (!whole) {
+              part[hn * stride + stride - 4] = top;
+              part[hn * stride + stride - 3] = sum;
+            } else if (a.lse) {
+              a.lse[seq * a.Hq + hq] = top * kLn2 + logf(sum);
             }
           }
         }
-        __syncthreads();
-      }
-      if (tile0 > 0) rec.flags |= ends ? 6 : 2;
-      if (tile0 == 0 && !ends) {
-        rec.flags |= 1;
-        rec.seq = was.seq;
-        rec.head = was.head;
+        if (wt > 1) __syncthreads();
+        else __syncwarp();
       }
       tile0 = use.tile;
       clear_sums();
@@ -343,27 +357,39 @@ __global__ void __launch_bounds__(kThreads, Geo<DM>::kCtas) paged_mma_kernel(Pag
   if (threadIdx.x == 0) a.rec[blockIdx.x] = rec;
 }
 
+inline int log2_of(int n) {
+  int l = 0;
+  while (n >> (l + 1)) ++l;
+  return l;
+}
+
 template <bool F16, int DM, int NT>
 cudaError_t launch(const PagedArgs& a, int sms, cudaStream_t s) {
   using G = Geo<DM>;
   static SmemLimit limit;
-  static_assert(G::kCtas * 2 * 8 * NT <= kPagedSlots && G::kCtas <= kPagedCtas, "workspace");
   auto kern = paged_mma_kernel<F16, DM, NT>;
   if (cudaError_t e = limit.allow(kern, G::kSmem)) return e;
-  const int groups = (a.Hq / a.Hk + 8 * NT - 1) / (8 * NT), ctas = G::kCtas * sms;
-  if (cudaError_t e = launch_early(kern, dim3(static_cast<unsigned>(ctas)), kThreads, G::kSmem, s, a, groups)) return e;
-  return launch_paged_join<typename std::conditional<F16, __half, __nv_bfloat16>::type>(a, ctas, 8 * NT, groups, s);
+  const PagedShape p = paged_shape_mma(a.Hq / a.Hk, a.Hk, a.D, a.k_head < a.k_token);
+  const int ctas = p.ctas * sms;
+  if (cudaError_t e = launch_early(kern, dim3(static_cast<unsigned>(ctas)), kThreads, G::kSmem, s, a, p.groups, log2_of(p.wh))) return e;
+  return launch_paged_join<typename std::conditional<F16, __half, __nv_bfloat16>::type>(a, ctas, p.group, p.groups, p.wh, s);
 }
 
 template <bool F16>
 cudaError_t launch_width(const PagedArgs& a, int sms, cudaStream_t s) {
-  const bool wide = a.Hq / a.Hk > 8;  // 16 heads a group: the rows are read half as often
+  const bool wide = paged_shape_mma(a.Hq / a.Hk, a.Hk, a.D, a.k_head < a.k_token).group == 16;
   if (a.D <= 64) return wide ? launch<F16, 64, 2>(a, sms, s) : launch<F16, 64, 1>(a, sms, s);
   if (a.D <= 128) return wide ? launch<F16, 128, 2>(a, sms, s) : launch<F16, 128, 1>(a, sms, s);
   return launch<F16, 256, 1>(a, sms, s);
 }
 
 }  // namespace
+
+// Groups of 16 query heads from 9 on, so that the rows are read half as often (not beside the
+// registers that 256 columns take).
+PagedShape paged_shape_mma(int G, int Hk, int D, bool together) {
+  return paged_shape(G, Hk, G > 8 && D <= 128 ? 16 : 8, kWarps, D <= 64 ? Geo<64>::kCtas : D <= 128 ? Geo<128>::kCtas : Geo<256>::kCtas, together);
+}
 
 cudaError_t launch_paged_mma(bool f16, const PagedArgs& a, int sms, cudaStream_t s) {
   return f16 ? launch_width<true>(a, sms, s) : launch_width<false>(a, sms, s);

@@ -1,12 +1,16 @@
 // paged_common.cuh -- what the kernels of attention over a paged cache share: the cut of
 // all sequences' work into equal runs, one a CTA, and the partial results that a cut leaves.
 //
-// A unit is kPagedTile tokens of one sequence for one key head (and one group of its query
-// heads).  Units in the order (sequence, key head and group, tile) are dealt in contiguous
-// runs of equal length, from the lengths on the device, so that ragged batches load every SM
-// alike and a captured graph follows its lengths.  A run that covers a (sequence, head group)
-// whole writes its outputs; of the others each CTA leaves at most two, its first and its
-// last, and paged_join adds them in CTA order: no atomics, the same bits in every run.
+// A CTA's warps share out `wh` heads (a head: a key head, or one group of its query heads) and
+// kWarps / wh token tiles; a unit is such a tile of tokens of one sequence for one set of wh
+// heads.  Neighbouring key heads lie beside each other in a token's row, so a CTA reads longer
+// pieces of memory, and a warp that has a head to itself ends it without the others.  Units in
+// the order (head set, sequence, tile) are dealt in contiguous runs of equal cost, from the
+// lengths on the device, so that ragged batches load every SM alike, a captured graph follows
+// its lengths, and the sets of one token are read at about the same time.  A run that covers a
+// (sequence, head set) whole writes its outputs; of the others each CTA leaves at most two, its
+// first and its last, and paged_join adds them in CTA order: no atomics, the same bits in every
+// run.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -19,7 +23,6 @@
 
 namespace nf4 {
 
-constexpr int kPagedTile = 64;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // Tokens of sequence s, forced into what its table row can hold; a length outside is recorded.
@@ -30,7 +33,9 @@ __device__ __forceinline__ int paged_len(const PagedArgs& a, int64_t s) {
   return n < 0 ? 0 : (n > most ? static_cast<int>(most) : n);
 }
 
-__device__ __forceinline__ int paged_tiles(int len) { return static_cast<int>((static_cast<int64_t>(len) + kPagedTile - 1) / kPagedTile); }
+__device__ __forceinline__ int paged_tiles(int len, int log2_tile) {
+  return static_cast<int>((static_cast<unsigned>(len) + (1u << log2_tile) - 1u) >> log2_tile);
+}
 
 __device__ __forceinline__ unsigned paged_index(const PagedArgs& a, int pos) {
   return static_cast<unsigned>(static_cast<uint64_t>(static_cast<unsigned>(pos)) * a.page_mul >> a.page_shift);
@@ -46,28 +51,51 @@ __device__ __forceinline__ int paged_slot(const PagedArgs& a, int64_t s, int pos
   return -1;
 }
 
-struct PagedRun {
-  int64_t u0, u1;  // units of this CTA
-  int64_t seq;     // sequence of u0
-  int64_t before;  // tiles of the sequences before it
-};
-
 __device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {  // of values >= 0; most fit 32 bits, where it is quick
   if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
   return a / b;
 }
 
-// This CTA's run of the units, `heads` a tile.  Equal shares of time, not of units: what a
-// (sequence, head group) costs beside its tiles (queries, and the warps' sums at its end) is
-// about half a tile's, so one of n tiles counts 2 n + 1.  Called by all threads of the CTA;
-// `red` holds 68 values and is free again when the call returns.
-__device__ __forceinline__ PagedRun paged_run(const PagedArgs& a, int heads, int64_t* red) {
+// A CTA's run of units, one after another.
+struct Walk {
+  int64_t seq;
+  int left;  // units left in the run, this one among them (2^31 would be days of work)
+  int len, tiles, set, tile, log2_tile;
+
+  // To a sequence with tokens, from `seq` on.
+  __device__ __forceinline__ void settle(const PagedArgs& a) {
+    for (int64_t i = 0; i <= a.nseq; ++i, ++seq) {
+      if (seq >= a.nseq) {
+        seq = 0;
+        ++set;
+      }
+      len = paged_len(a, seq);
+      tiles = paged_tiles(len, log2_tile);
+      if (tiles > 0) return;
+    }
+    left = 0;
+  }
+
+  __device__ __forceinline__ void next(const PagedArgs& a) {
+    --left;
+    if (++tile < tiles || left <= 0) return;
+    tile = 0;
+    ++seq;
+    settle(a);
+  }
+};
+
+// This CTA's run of the units of `sets` head sets.  Equal shares of cost: what a (sequence,
+// head set) takes beside its tiles (queries, its end) is about half a tile's, so one of n tiles
+// counts 2 n + 1.  Called by all threads of the CTA; `red` holds 68 values and is free again
+// when the call returns.
+__device__ __forceinline__ Walk paged_run(const PagedArgs& a, int sets, int log2_tile, int64_t* red) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
   const int64_t each = a.nseq <= blockDim.x ? 1 : (a.nseq + blockDim.x - 1) / blockDim.x;
   const int64_t s0 = threadIdx.x * each, s1 = s0 + each < a.nseq ? s0 + each : a.nseq;
   int64_t own = 0, live = 0;  // tiles, and sequences that have some
   for (int64_t s = s0; s < s1; ++s) {
-    const int n = paged_tiles(paged_len(a, s));
+    const int n = paged_tiles(paged_len(a, s), log2_tile);
     own += n;
     live += n > 0;
   }
@@ -97,50 +125,47 @@ __device__ __forceinline__ PagedRun paged_run(const PagedArgs& a, int heads, int
   tiles0 += tiles - own;
   seqs0 += seqs - live;
   // shares of the whole, in halves of a tile
-  const int64_t total = (2 * all_tiles + all_seqs) * heads, share = divide(total, gridDim.x), rest = total - share * gridDim.x;
+  const int64_t span = 2 * all_tiles + all_seqs, total = span * sets, share = divide(total, gridDim.x), rest = total - share * gridDim.x;
   const int64_t c = blockIdx.x, v0 = c * share + (c < rest ? c : rest), v1 = v0 + share + (c < rest);
-  const int64_t first = (2 * tiles0 + seqs0) * heads, past = first + (2 * own + live) * heads;
+  const int64_t first = 2 * tiles0 + seqs0, past = first + 2 * own + live;
   __syncthreads();
-  if (threadIdx.x == 0) {  // where no thread's sequences hold an end of the run
-    red[0] = red[1] = all_tiles * heads;
-    red[2] = a.nseq;
-  }
+  if (threadIdx.x == 0) red[0] = red[1] = all_tiles * sets;  // the end of all units, which no thread's sequences hold
   __syncthreads();
   for (int end = 0; end < 2; ++end) {
     const int64_t v = end ? v1 : v0;
-    if (v < first || v >= past) continue;
-    int64_t s = s0, before = tiles0, at = first;
-    for (; s < s1; ++s) {
-      const int n = paged_tiles(paged_len(a, s));
+    if (v >= total) continue;
+    const int64_t set = divide(v, span), in = v - set * span;
+    if (in < first || in >= past) continue;
+    int64_t before = tiles0, at = first;
+    for (int64_t s = s0; s < s1; ++s) {
+      const int n = paged_tiles(paged_len(a, s), log2_tile);
       if (n == 0) continue;
-      const int64_t span = static_cast<int64_t>(2 * static_cast<int64_t>(n) + 1) * heads;
-      if (v >= at + span) {
-        at += span;
+      if (in >= at + 2 * static_cast<int64_t>(n) + 1) {
+        at += 2 * static_cast<int64_t>(n) + 1;
         before += n;
         continue;
       }
-      const int64_t head = divide(v - at, 2 * static_cast<int64_t>(n) + 1), tile = (v - at - head * (2 * static_cast<int64_t>(n) + 1)) >> 1;
-      red[end] = before * heads + head * n + tile;
+      const int64_t tile = (in - at) >> 1;  // n: the half behind its last tile, so the next sequence's first
+      red[end] = set * all_tiles + before + tile;
       if (end == 0) {
-        if (head * n + tile == static_cast<int64_t>(heads) * n) {  // the half behind its last tile: the run begins with the next
-          before += n;
-          do ++s;
-          while (s < a.nseq && paged_len(a, s) == 0);
-        }
-        red[2] = s;
-        red[3] = before;
+        red[2] = tile < n ? s : s + 1;
+        red[3] = tile < n ? tile : 0;
+        red[4] = set;
       }
       break;
     }
   }
   __syncthreads();
-  PagedRun r;
-  r.u0 = red[0];
-  r.u1 = red[1];
-  r.seq = red[2];
-  r.before = red[3];
+  Walk w;
+  const int64_t units = red[1] - red[0];
+  w.left = static_cast<int>(units < INT32_MAX ? units : INT32_MAX);
+  w.seq = red[2];
+  w.tile = static_cast<int>(red[3]);
+  w.set = static_cast<int>(red[4]);
+  w.log2_tile = log2_tile;
+  if (w.left > 0) w.settle(a);
   __syncthreads();
-  return r;
+  return w;
 }
 
 // Sequences of no tokens: zeros, and -inf for the logarithm of their sum.
@@ -154,93 +179,146 @@ __device__ __forceinline__ void paged_empty(const PagedArgs& a) {
   }
 }
 
-// Adds the partial results of each (sequence, head group) that was cut, in CTA order.  A CTA
-// for each CTA of the attention kernel whose run may begin one (blockIdx.x) and each head of
-// a group (blockIdx.y); `heads` a group.  Its time is that of a few dependent loads, so what a
-// load needs not wait for it does not: flags and sums of all parts are read at once, and those
-// of no use are dropped.
-template <typename T, int DV>
-__global__ void __launch_bounds__(128) paged_join_kernel(PagedArgs a, int heads, int groups) {
+// Adds the partial results of each (sequence, head set) that was cut, in CTA order; `heads` query
+// heads a group, `wh` groups a set.  WIDE: a CTA for each such pair that there can be (blockIdx.x,
+// which finds the pair's first CTA) and query head, the warps sharing the parts out: for few
+// pairs, which are cut into many.  Else a CTA for each CTA of the attention kernel, which may
+// begin one, a warp for each query head.  The time is that of a few dependent loads, so what a
+// load needs not wait for it does not: flags and sums of several parts are read at once, and
+// those of no use are dropped.
+constexpr int kJoinWarps = 16;
+constexpr int kJoinCtas = 1024;  // of the attention kernel at most
+
+template <typename T, int DV, bool WIDE>
+__global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(PagedArgs a, int ctas, int heads, int groups, int wh) {
   constexpr int kAtOnce = DV <= 4 ? 4 : 2;
-  __shared__ float s_acc[4][DV * 32], s_ml[4][2];
-  __shared__ int s_last[4];
-  const int c = blockIdx.x, n = gridDim.x, h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __shared__ float s_acc[WIDE ? kJoinWarps : 1][DV * 32], s_ml[WIDE ? kJoinWarps : 1][2];
+  constexpr int kMost = kJoinCtas;
+  __shared__ unsigned s_begin[kMost / 32], s_end[kMost / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = ctas;
   grid_wait();
-  const PagedRec me = a.rec[c];
-  // the CTA that ends it: the first after c with that flag
-  int last = n;
-  for (int p = n - 1 - threadIdx.x; p > c; p -= 128) last = a.rec[p].flags & 4 ? p : last;
-  if (!(me.flags & 1)) return;
-  const int G = a.Hq / a.Hk, hk = me.head / groups, g = (me.head - hk * groups) * heads + h;
-  if (g >= G) return;
-  last = static_cast<int>(__reduce_min_sync(0xffffffffu, static_cast<unsigned>(last)));
-  if (lane == 0) s_last[warp] = last;
+  // which CTAs begin a cut pair, and which end one
+#pragma unroll
+  for (int i = 0; i < kMost / (kJoinWarps * 32); ++i) {
+    const int p = (i * kJoinWarps + warp) * 32 + lane, f = p < n ? a.rec[p].flags : 0;
+    const unsigned begin = __ballot_sync(0xffffffffu, f & 1), end = __ballot_sync(0xffffffffu, f & 4);
+    if (lane == 0) {
+      s_begin[i * kJoinWarps + warp] = begin;
+      s_end[i * kJoinWarps + warp] = end;
+    }
+  }
   __syncthreads();
+  int c = blockIdx.x;
+  if (WIDE) {  // the (c + 1)-th that begins one
+    const unsigned begin = s_begin[lane];
+    int upto = __popc(begin);
 #pragma unroll
-  for (int w = 0; w < 4; ++w) last = min(last, s_last[w]);
-  const int st = paged_part_stride(a.D);
-  float m = -INFINITY, l = 0.0f, acc[DV] = {};
-  for (int p0 = c + warp; p0 <= last; p0 += 4 * kAtOnce) {
-    float pm[kAtOnce], pl[kAtOnce], pv[kAtOnce][DV];
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += up;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, upto > c);
+    if (past == 0) return;
+    const int word = __ffs(past) - 1;
+    unsigned rest = __shfl_sync(0xffffffffu, begin, word);
+    for (int i = c - (__shfl_sync(0xffffffffu, upto, word) - __popc(rest)); i > 0; --i) rest &= rest - 1;
+    c = word * 32 + __ffs(rest) - 1;
+  } else if (!(s_begin[c >> 5] >> (c & 31) & 1)) {
+    return;
+  }
+  const PagedRec me = a.rec[c];
+  int last;  // the first after c that ends one ends this one
+  {
+    const int word = c >> 5;
+    const unsigned after = (c & 31) == 31 ? 0u : ~0u << ((c & 31) + 1);
+    const unsigned end = lane < word ? 0 : lane > word ? s_end[lane] : s_end[lane] & after;
+    const unsigned some = __ballot_sync(0xffffffffu, end != 0);
+    if (some == 0) return;
+    const int at = __ffs(some) - 1;
+    last = at * 32 + __ffs(__shfl_sync(0xffffffffu, end, at)) - 1;
+  }
+  const int st = paged_part_stride(a.D), G = a.Hq / a.Hk, each = G < heads ? G : heads;
+  for (int y = WIDE ? blockIdx.y : warp; y < wh * each; y += WIDE ? wh * each : kJoinWarps) {
+    const int sub = y / each, h = sub * heads + y - sub * each, head = me.set * wh + sub, hk = head / groups;
+    const int g = (head - hk * groups) * heads + y - sub * each;
+    if (g >= G) continue;
+    const int step = WIDE ? kJoinWarps : 1;
+    float m = -INFINITY, l = 0.0f, acc[DV] = {};
+    for (int p0 = c + (WIDE ? warp : 0); p0 <= last; p0 += step * kAtOnce) {
+      float pm[kAtOnce], pl[kAtOnce], pv[kAtOnce][DV];
 #pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-      const int p = min(p0 + 4 * i, n - 1);
-      const float* part = a.part + (static_cast<int64_t>(p * 2 + (p == c)) * heads + h) * st;
-      const bool in = p0 + 4 * i <= last && (p == c || (a.rec[p].flags & 2));
-      const float m0 = part[st - 4], l0 = part[st - 3];
-      pm[i] = in ? m0 : -INFINITY;
-      pl[i] = in ? l0 : 0.0f;
+      for (int i = 0; i < kAtOnce; ++i) {
+        const int p = min(p0 + step * i, n - 1);
+        const float* part = a.part + (static_cast<int64_t>(p * 2 + (p == c)) * (wh * heads) + h) * st;
+        const bool in = p0 + step * i <= last && (p == c || (a.rec[p].flags & 2));
+        const float m0 = part[st - 4], l0 = part[st - 3];
+        pm[i] = in ? m0 : -INFINITY;
+        pl[i] = in ? l0 : 0.0f;
 #pragma unroll
-      for (int j = 0; j < DV; ++j) {
-        const float v = lane + 32 * j < a.D ? part[lane + 32 * j] : 0.0f;
-        pv[i][j] = in ? v : 0.0f;
+        for (int j = 0; j < DV; ++j) {
+          const float v = lane + 32 * j < a.D ? part[lane + 32 * j] : 0.0f;
+          pv[i][j] = in ? v : 0.0f;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        const float top = fmaxf(m, pm[i]), mm = top == -INFINITY ? 0.0f : top;
+        const float f0 = exp2f(m - mm), f1 = exp2f(pm[i] - mm);
+        m = top;
+        l = l * f0 + pl[i] * f1;
+#pragma unroll
+        for (int j = 0; j < DV; ++j) acc[j] = acc[j] * f0 + pv[i][j] * f1;
       }
     }
+    const int hq = hk * G + g;
+    T* o = static_cast<T*>(a.o) + me.seq * a.o_s + hq * a.o_h;
+    if constexpr (!WIDE) {
 #pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-      const float top = fmaxf(m, pm[i]), mm = top == -INFINITY ? 0.0f : top;
-      const float f0 = exp2f(m - mm), f1 = exp2f(pm[i] - mm);
-      m = top;
-      l = l * f0 + pl[i] * f1;
+      for (int j = 0; j < DV; ++j)
+        if (lane + 32 * j < a.D) o[lane + 32 * j] = from_f32<T>(acc[j] / l);
+      if (lane == 0 && a.lse) a.lse[me.seq * a.Hq + hq] = m * kLn2 + logf(l);
+    } else {
 #pragma unroll
-      for (int j = 0; j < DV; ++j) acc[j] = acc[j] * f0 + pv[i][j] * f1;
+    for (int i = 0; i < DV; ++i) s_acc[warp][lane + 32 * i] = acc[i];
+    if (lane == 0) {
+      s_ml[warp][0] = m;
+      s_ml[warp][1] = l;
+    }
+    __syncthreads();
+    float top = -INFINITY;
+    for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, s_ml[w][0]);
+    const float mm = top == -INFINITY ? 0.0f : top;
+    for (int d = threadIdx.x; d < a.D; d += kJoinWarps * 32) {
+      float v = 0.0f, sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kJoinWarps; ++w) {
+        const float f = exp2f(s_ml[w][0] - mm);
+        sum += s_ml[w][1] * f;
+        v += s_acc[w][d] * f;
+      }
+      o[d] = from_f32<T>(v / sum);
+      if (d == 0 && a.lse) a.lse[me.seq * a.Hq + hq] = top * kLn2 + logf(sum);
+    }
     }
   }
-#pragma unroll
-  for (int i = 0; i < DV; ++i) s_acc[warp][lane + 32 * i] = acc[i];
-  if (lane == 0) {
-    s_ml[warp][0] = m;
-    s_ml[warp][1] = l;
-  }
-  __syncthreads();
-  float top = -INFINITY;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) top = fmaxf(top, s_ml[w][0]);
-  const float mm = top == -INFINITY ? 0.0f : top;
-  float f[4], sum = 0.0f;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    f[w] = exp2f(s_ml[w][0] - mm);
-    sum += s_ml[w][1] * f[w];
-  }
-  const int hq = hk * G + g;
-  T* o = static_cast<T*>(a.o) + me.seq * a.o_s + hq * a.o_h;
-  for (int d = threadIdx.x; d < a.D; d += 128) {
-    float v = 0.0f;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) v += s_acc[w][d] * f[w];
-    o[d] = from_f32<T>(v / sum);
-  }
-  if (threadIdx.x == 0 && a.lse) a.lse[me.seq * a.Hq + hq] = top * kLn2 + logf(sum);
+}
+
+template <typename T, int DV>
+cudaError_t launch_paged_join_width(const PagedArgs& a, int ctas, int heads, int groups, int wh, cudaStream_t s) {
+  if (ctas > kJoinCtas) return cudaErrorInvalidConfiguration;
+  const int G = a.Hq / a.Hk;
+  const int64_t pairs = a.nseq * (static_cast<int64_t>(a.Hk) * groups / wh);
+  if (pairs <= ctas / 4)
+    return launch_early(paged_join_kernel<T, DV, true>, dim3(static_cast<unsigned>(pairs), static_cast<unsigned>(wh * (G < heads ? G : heads))),
+                        kJoinWarps * 32, 0, s, a, ctas, heads, groups, wh);
+  return launch_early(paged_join_kernel<T, DV, false>, dim3(static_cast<unsigned>(ctas)), kJoinWarps * 32, 0, s, a, ctas, heads, groups, wh);
 }
 
 template <typename T>
-cudaError_t launch_paged_join(const PagedArgs& a, int ctas, int heads, int groups, cudaStream_t s) {
-  const int G = a.Hq / a.Hk;
-  const dim3 grid(static_cast<unsigned>(ctas), static_cast<unsigned>(G < heads ? G : heads), 1);
-  if (a.D <= 64) return launch_early(paged_join_kernel<T, 2>, grid, 128, 0, s, a, heads, groups);
-  if (a.D <= 128) return launch_early(paged_join_kernel<T, 4>, grid, 128, 0, s, a, heads, groups);
-  return launch_early(paged_join_kernel<T, 8>, grid, 128, 0, s, a, heads, groups);
+cudaError_t launch_paged_join(const PagedArgs& a, int ctas, int heads, int groups, int wh, cudaStream_t s) {
+  if (a.D <= 64) return launch_paged_join_width<T, 2>(a, ctas, heads, groups, wh, s);
+  if (a.D <= 128) return launch_paged_join_width<T, 4>(a, ctas, heads, groups, wh, s);
+  return launch_paged_join_width<T, 8>(a, ctas, heads, groups, wh, s);
 }
 
 }  // namespace nf4

@@ -33,37 +33,6 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return r;
 }
 
-// The units of a run, one after another.
-struct Walk {
-  int64_t seq;
-  int left;  // units left in the run, this one among them (2^31 would be days of work)
-  int len, tiles, head, tile;
-
-  __device__ __forceinline__ Walk(const PagedArgs& a, const PagedRun& run, int heads) {
-    seq = run.seq;
-    left = static_cast<int>(run.u1 - run.u0 < INT32_MAX ? run.u1 - run.u0 : INT32_MAX);
-    len = paged_len(a, run.seq);
-    tiles = paged_tiles(len);
-    const int64_t r0 = run.u0 - run.before * heads;
-    head = static_cast<int>(divide(r0, tiles));
-    tile = static_cast<int>(r0 - static_cast<int64_t>(head) * tiles);
-  }
-
-  // The next unit with tokens; `heads` a tile.
-  __device__ __forceinline__ void next(const PagedArgs& a, int heads) {
-    --left;
-    if (++tile < tiles) return;
-    tile = 0;
-    if (++head < heads || left <= 0) return;
-    head = 0;
-    do {
-      ++seq;
-      len = seq < a.nseq ? paged_len(a, seq) : 1;
-      tiles = paged_tiles(len);
-    } while (tiles == 0);
-  }
-};
-
 // The copies of a tile of ROWS tokens, keys and then values, rows of W values; columns past D
 // and rows past a length or without a page are zeros that nothing reads.  Lane i copies column
 // piece i % kPieces of rows i / kPieces and every kPer-th after it.
@@ -75,10 +44,10 @@ struct TileCopies {
 
   uint32_t dst0;
   uint32_t* s_valid;  // [ring slots]: which rows of a tile are tokens
-  int row0, col, groups;
+  int row0, col;
   bool in, one_page;
 
-  __device__ __forceinline__ TileCopies(const PagedArgs& a, uint32_t ring, uint32_t* valid, int groups_) {
+  __device__ __forceinline__ TileCopies(const PagedArgs& a, uint32_t ring, uint32_t* valid) {
     const int lane = threadIdx.x & 31;
     row0 = lane / kPieces;
     col = lane % kPieces * (16 / static_cast<int>(sizeof(T)));
@@ -86,12 +55,11 @@ struct TileCopies {
     one_page = a.page_size % ROWS == 0;  // a tile lies in one page
     dst0 = ring + at_chunk<kRowBytes>(row0, lane % kPieces);
     s_valid = valid;
-    groups = groups_;
   }
 
-  // Starts the copies of the tokens from tok0 on of the unit `load` into ring slot `st`.
-  __device__ __forceinline__ void start(const PagedArgs& a, const Walk& load, int tok0, int st) const {
-    const int lane = threadIdx.x & 31, rows = load.len - tok0, hk = groups == 1 ? load.head : load.head / groups;
+  // Starts the copies of the tokens from tok0 on of the unit `load`, key head hk, into ring slot `st`.
+  __device__ __forceinline__ void start(const PagedArgs& a, const Walk& load, int tok0, int hk, int st) const {
+    const int lane = threadIdx.x & 31, rows = load.len - tok0;
     if (load.left > 0 && rows > 0) {
       const uint32_t to = dst0 + st * kStage;
       // a row's swizzle repeats after eight rows

@@ -13,7 +13,7 @@ from typing import Optional
 import torch
 
 from . import _lib
-from .block_ops import _DTYPES, _dtype, _fn, _on, _one_device, _raw_stream, _share_storage, _workspace3, _written
+from .block_ops import _DTYPES, _dtype, _fn, _on, _one_device, _raw_stream, _share_storage, _workspace5, _written
 
 _CACHE = struct.Struct("@2P6qPqP2q5i4x")  # nf4_paged_cache
 
@@ -122,7 +122,7 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     lse = torch.empty((n, Hq), dtype=torch.float32, device=dev)
     qt, ot = q.stride(), o.stride()
     with _on(dev):
-        need = _workspace3(_lib.OP_PAGED_ATTENTION, 0, 0, D, dev)
+        need = _workspace5(_lib.OP_PAGED_ATTENTION, 0, Hq, D, Hk, dev)
         ws = torch.empty(need, dtype=torch.uint8, device=dev)
         rc = _fn("nf4_paged_attention")(d, q.data_ptr(), qt[0], qt[1], Hq, D ** -0.5 if scale is None else scale, o.data_ptr(), ot[0],
                                         ot[1], lse.data_ptr(), ws.data_ptr(), need, _raw_stream(dev))

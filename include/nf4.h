@@ -72,7 +72,7 @@ enum {
   NF4_OP_GROUPED_SWIGLU_BWD = 5, /* M = T rows, N = N_e, K; E experts */
   NF4_OP_NORM_RESIDUAL_BWD = 6,  /* M = T rows, N = H; K and E unused */
   NF4_OP_ATTENTION_BWD = 7,      /* M = T rows, N = Hq query heads; K and E unused */
-  NF4_OP_PAGED_ATTENTION = 8,    /* K = D; M, N and E unused */
+  NF4_OP_PAGED_ATTENTION = 8,    /* N = Hq, K = D, E = Hk; M unused */
   NF4_OP_ROUTE = 9               /* M = T tokens, N = E experts; K and E unused */
 };
 
@@ -509,7 +509,7 @@ nf4_status nf4_adamw_state_values(const uint8_t* m, const uint8_t* v, const floa
  *   q, o        [nseq, Hq, D] of `dtype`, sequence and head strides in elements.
  *   lse         fp32 [nseq][Hq], natural log of the sum of exponentials, or NULL.
  *   Idle rows: zeros, and lse -inf.  Slots past a sequence's length are never read.
- *   ws: nf4_workspace_size(NF4_OP_PAGED_ATTENTION, 0, 0, D, 0) bytes, 16-byte aligned, of a
+ *   ws: nf4_workspace_size(NF4_OP_PAGED_ATTENTION, 0, Hq, D, Hk) bytes, 16-byte aligned, of a
  *   call's own (calls on two streams, or two graphs whose replays overlap, must not share it).
  * Hq a multiple of Hk, 1 <= D <= 256.  fp32 sums and statistics; partial results over the
  * length are added in a fixed order (deterministic for given lengths and device).  16-bit
