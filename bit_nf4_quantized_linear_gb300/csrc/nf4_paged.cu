@@ -44,11 +44,11 @@ __device__ __forceinline__ int append_place(const PagedArgs& a, int64_t r, int* 
   return paged_slot(a, seq, static_cast<int>(pos), slot);
 }
 
-// Copies `V`-wide pieces of `rows` new rows a CTA.  Bound by HBM: each value is read and
+// Copies `V`-wide pieces of ROWS new rows a CTA.  Bound by HBM: each value is read and
 // written once.
-template <typename V>
-__global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(PagedArgs a, int rows, int per_head, int elems) {
-  __shared__ int64_t s_k[32], s_v[32];
+template <typename V, int ROWS>
+__global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(PagedArgs a, int per_head, int elems) {
+  __shared__ int64_t s_k[ROWS], s_v[ROWS];
   grid_allow();
   grid_wait();
   if (a.cu_seqlens && blockIdx.x == 0 && a.status) {
@@ -56,8 +56,8 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(PagedArgs 
     for (int64_t i = threadIdx.x; i < a.nseq; i += kAppendThreads) bad |= a.cu_seqlens[i + 1] < a.cu_seqlens[i];
     if (bad) atomicCAS(a.status, 0, kStatusBadOffsets);
   }
-  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * rows;
-  if (threadIdx.x < rows) {
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * ROWS;
+  if (threadIdx.x < ROWS) {
     int slot = 0;
     const int64_t r = r0 + threadIdx.x;
     const int64_t page = r < a.T ? append_place(a, r, &slot) : -1;
@@ -65,19 +65,23 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(PagedArgs 
     s_v[threadIdx.x] = page < 0 ? -1 : page * a.v_page + slot * a.v_token;
   }
   __syncthreads();
-  const int row = 2 * a.Hk * per_head;  // pieces of a row: keys, then values
-  for (int i = threadIdx.x; i < rows * row; i += kAppendThreads) {
-    const int t = i / row, j = i % row, h = j / per_head, hk = h < a.Hk ? h : h - a.Hk;
-    const int64_t d = static_cast<int64_t>(j % per_head) * elems, at = h < a.Hk ? s_k[t] : s_v[t];
-    if (at < 0) continue;
-    constexpr int64_t e = sizeof(V);
-    const int64_t r = r0 + t;
-    if (h < a.Hk)
-      *reinterpret_cast<V*>(static_cast<char*>(a.k) + (at + hk * a.k_head + d) * e / elems) =
-          *reinterpret_cast<const V*>(static_cast<const char*>(a.k_new) + (r * a.kn_t + hk * a.kn_h + d) * e / elems);
-    else
-      *reinterpret_cast<V*>(static_cast<char*>(a.v) + (at + hk * a.v_head + d) * e / elems) =
-          *reinterpret_cast<const V*>(static_cast<const char*>(a.v_new) + (r * a.vn_t + hk * a.vn_h + d) * e / elems);
+  // A thread copies one piece of a row's keys or values, of all rows.
+  constexpr int64_t e = sizeof(V);
+  const int row = 2 * a.Hk * per_head;
+  for (int j = threadIdx.x; j < row; j += kAppendThreads) {
+    const int h = j / per_head, hk = h < a.Hk ? h : h - a.Hk;
+    const int64_t d = static_cast<int64_t>(j - h * per_head) * elems;
+    const bool keys = h < a.Hk;
+    const int64_t *at = keys ? s_k : s_v, step = (keys ? a.kn_t : a.vn_t) * e / elems;
+    char* to = static_cast<char*>(keys ? a.k : a.v) + (hk * (keys ? a.k_head : a.v_head) + d) * e / elems;
+    const char* from = static_cast<const char*>(keys ? a.k_new : a.v_new) + (r0 * (keys ? a.kn_t : a.vn_t) + hk * (keys ? a.kn_h : a.vn_h) + d) * e / elems;
+    V v[ROWS];
+#pragma unroll
+    for (int t = 0; t < ROWS; ++t)
+      if (at[t] >= 0) v[t] = *reinterpret_cast<const V*>(from + t * step);
+#pragma unroll
+    for (int t = 0; t < ROWS; ++t)
+      if (at[t] >= 0) *reinterpret_cast<V*>(to + at[t] * e / elems) = v[t];
   }
 }
 
@@ -305,6 +309,17 @@ cudaError_t launch_paged_any(int dtype, const PagedArgs& a, int sms, cudaStream_
   return launch_any_heads<__nv_bfloat16>(a, sms, s);
 }
 
+namespace {
+
+template <typename V>
+cudaError_t launch_append(const PagedArgs& a, int per_head, int elems, int sms, cudaStream_t s) {
+  if (a.T < 32 * static_cast<int64_t>(sms))  // few rows: a CTA each
+    return launch_early(paged_append_kernel<V, 1>, dim3(static_cast<unsigned>(a.T)), kAppendThreads, 0, s, a, per_head, elems);
+  return launch_early(paged_append_kernel<V, 8>, dim3(static_cast<unsigned>((a.T + 7) / 8)), kAppendThreads, 0, s, a, per_head, elems);
+}
+
+}  // namespace
+
 cudaError_t launch_paged_append(int dtype, const PagedArgs& a, int sms, cudaStream_t s) {
   const int e = dtype == NF4_DTYPE_F32 ? 4 : 2, wide = 16 / e;
   const int64_t ld[] = {a.k_page, a.k_token, a.k_head, a.v_page, a.v_token, a.v_head, a.kn_t, a.kn_h, a.vn_t, a.vn_h, a.D};
@@ -312,11 +327,9 @@ cudaError_t launch_paged_append(int dtype, const PagedArgs& a, int sms, cudaStre
   bool vec = true;
   for (int64_t x : ld) vec = vec && x % wide == 0;
   for (const void* x : p) vec = vec && reinterpret_cast<uintptr_t>(x) % 16 == 0;
-  const int rows = a.T >= 32 * static_cast<int64_t>(sms) ? 8 : 1;
-  const unsigned grid = static_cast<unsigned>((a.T + rows - 1) / rows);
-  if (vec) return launch_early(paged_append_kernel<uint4>, dim3(grid), kAppendThreads, 0, s, a, rows, a.D / wide, wide);
-  if (e == 4) return launch_early(paged_append_kernel<uint32_t>, dim3(grid), kAppendThreads, 0, s, a, rows, a.D, 1);
-  return launch_early(paged_append_kernel<uint16_t>, dim3(grid), kAppendThreads, 0, s, a, rows, a.D, 1);
+  if (vec) return launch_append<uint4>(a, a.D / wide, wide, sms, s);
+  if (e == 4) return launch_append<uint32_t>(a, a.D, 1, sms, s);
+  return launch_append<uint16_t>(a, a.D, 1, sms, s);
 }
 
 }  // namespace nf4

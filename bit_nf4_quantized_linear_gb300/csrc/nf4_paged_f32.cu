@@ -23,16 +23,13 @@
 namespace nf4 {
 namespace {
 
-#ifndef F32S
-#define F32S 2
-#endif
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kRows = 8;  // tokens of a warp's tile: a lane a token and quarter of its columns
 
 template <int DM, int HC>
 struct Geo {
-  static constexpr int kStages = F32S;
+  static constexpr int kStages = 2;
   static constexpr int kCtas = DM == 64 ? 2 : 1;  // a SM
   static constexpr int kPitch = DM + 4;           // floats between heads of a warp's sums
   static constexpr int kRing = kWarps * kStages * TileCopies<float, DM, kRows>::kStage;
@@ -70,7 +67,7 @@ __global__ void __launch_bounds__(kThreads, Geo<DM, HC>::kCtas) paged_f32_kernel
   PagedRec rec{0, 0, 0};
 
   if (use.left > 0) {
-    const Copies copies(a, nf4ptx::smem_addr(ring), s_valid);
+    Copies copies(a, nf4ptx::smem_addr(ring), s_valid);
     // The key head of this warp in a head set, and its first query head's place in the group.
     auto place = [&](int set, int* g0) {
       const int head = (set << log2_wh) + my_head, hk = groups == 1 ? head : head / groups;
@@ -82,6 +79,7 @@ __global__ void __launch_bounds__(kThreads, Geo<DM, HC>::kCtas) paged_f32_kernel
       int g0;
       copies.start(a, load, first_token(load), place(load.set, &g0), st);
       if (load.left > 0) load.next(a);
+      copies.look_up(a, load, first_token(load));
     };
     auto fetch_queries = [&]() {
       int g0;
@@ -107,6 +105,7 @@ __global__ void __launch_bounds__(kThreads, Geo<DM, HC>::kCtas) paged_f32_kernel
       }
     };
     const float c = a.scale * kLog2e;
+    copies.look_up(a, load, first_token(load));
 #pragma unroll
     for (int i = 0; i < G::kStages; ++i) start_copies(i);
     fetch_queries();

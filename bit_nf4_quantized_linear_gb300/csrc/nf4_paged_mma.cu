@@ -35,21 +35,14 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kRows = 16;  // tokens of a warp's tile: the MMA's rows
 
-#ifndef V64S
-#define V64S 4
-#define V64C 2
-#define V128S 2
-#define V128C 2
-#endif
 template <int DM>
 struct Geo {
-  static constexpr int kStages = DM == 64 ? V64S : DM == 128 ? V128S : 3;
-  static constexpr int kCtas = DM == 64 ? V64C : DM == 128 ? V128C : 1;  // a SM
+  static constexpr int kStages = DM == 128 ? 2 : 3;
   static constexpr int kHalf = kRows * DM * 2;      // bytes of a tile's keys
   static constexpr int kStage = 2 * kHalf;
   static constexpr int kPitch = DM + 4;             // floats between heads of a warp's sums
   static constexpr int kRing = kWarps * kStages * kStage;
-  static constexpr int kSums = kWarps * 8 * kPitch * 4;
+  static constexpr int kSums = kWarps * 4 * kPitch * 4;  // four heads at a time
   static constexpr int kSmem = kRing + kSums + kWarps * 8 * 8 + kWarps * kStages * 4;
 };
 
@@ -104,14 +97,14 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t* hi, uint32_t*
   }
 }
 
-template <bool F16, int DM, int NT>
-__global__ void __launch_bounds__(kThreads, Geo<DM>::kCtas) paged_mma_kernel(PagedArgs a, int groups, int log2_wh) {
+template <bool F16, int DM, int NT, int CTAS>
+__global__ void __launch_bounds__(kThreads, CTAS) paged_mma_kernel(PagedArgs a, int groups, int log2_wh) {
   using G = Geo<DM>;
   using T = typename std::conditional<F16, __half, __nv_bfloat16>::type;
   constexpr int HC = 8 * NT, KS = DM / 16;
   constexpr float kShift = F16 ? 7.0f : 0.0f;
   extern __shared__ __align__(128) unsigned char dyn[];
-  float* s_sum = reinterpret_cast<float*>(dyn + G::kRing);                          // [kWarps][8][kPitch]
+  float* s_sum = reinterpret_cast<float*>(dyn + G::kRing);                          // [kWarps][4][kPitch]
   float2* s_ml = reinterpret_cast<float2*>(dyn + G::kRing + G::kSums);              // [kWarps][8]
   uint32_t* s_valid = reinterpret_cast<uint32_t*>(s_ml + kWarps * 8);               // [kWarps][kStages]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -126,7 +119,7 @@ __global__ void __launch_bounds__(kThreads, Geo<DM>::kCtas) paged_mma_kernel(Pag
   PagedRec rec{0, 0, 0};
 
   if (use.left > 0) {
-    const TileCopies<T, DM, kRows> copies(a, ring, s_valid);
+    TileCopies<T, DM, kRows> copies(a, ring, s_valid);
     // The key head of this warp in a head set, and its first query head's place in the group.
     auto place = [&](int set, int* g0) {
       const int head = (set << log2_wh) + my_head, hk = groups == 1 ? head : head / groups;
@@ -138,6 +131,7 @@ __global__ void __launch_bounds__(kThreads, Geo<DM>::kCtas) paged_mma_kernel(Pag
       int g0;
       copies.start(a, load, first_token(load), place(load.set, &g0), st);
       if (load.left > 0) load.next(a);
+      copies.look_up(a, load, first_token(load));
     };
 
     uint32_t qf[NT][KS][2];
@@ -178,6 +172,7 @@ __global__ void __launch_bounds__(kThreads, Geo<DM>::kCtas) paged_mma_kernel(Pag
           for (int j = 0; j < 4; ++j) acc[n][s][j] = 0.0f;
       }
     };
+    copies.look_up(a, load, first_token(load));
 #pragma unroll
     for (int i = 0; i < G::kStages; ++i) start_copies(i);
     fetch_queries();
@@ -292,60 +287,65 @@ __global__ void __launch_bounds__(kThreads, Geo<DM>::kCtas) paged_mma_kernel(Pag
         if (lane < 4)
 #pragma unroll
           for (int j = 0; j < 2; ++j) s_ml[warp * 8 + lane * 2 + j] = make_float2(m[n][j] - kShift, l[n][j]);
-        float* own = s_sum + warp * 8 * G::kPitch + (lane & 3) * 2 * G::kPitch + lane / 4;
 #pragma unroll
-        for (int s = 0; s < KS; ++s)
+        for (int half = 0; half < 2; ++half) {  // four heads at a time, which lie in lanes 0, 1 or 2, 3 of four
+          if ((lane >> 1 & 1) == half) {
+            float* own = s_sum + (warp * 4 + (lane & 1) * 2) * G::kPitch + lane / 4;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) own[(j & 1) * G::kPitch + s * 16 + (j & 2) * 4] = acc[n][s][j];
-        if (wt > 1) __syncthreads();
-        else __syncwarp();
-        // the warps of a head take its query heads in turn, a lane four columns
+            for (int s = 0; s < KS; ++s)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) own[(j & 1) * G::kPitch + s * 16 + (j & 2) * 4] = acc[n][s][j];
+          }
+          if (wt > 1) __syncthreads();
+          else __syncwarp();
+          // the warps of a head take its query heads in turn, a lane four columns
 #pragma unroll 2
-        for (int i = lane; i < (8 / wt) * (DM / 4); i += 32) {
-          const int h = my_tile + wt * (i / (DM / 4)), d = i % (DM / 4) * 4, hn = n * 8 + h;
-          if (g0 + hn >= GQ) break;
-          float top = -INFINITY, sum = 0.0f;
-          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          if (wt == 1) {
-            const float2 ml = s_ml[warp * 8 + h];
-            top = ml.x;
-            sum = ml.y;
-            v = *reinterpret_cast<const float4*>(s_sum + (warp * 8 + h) * G::kPitch + d);
-          } else {
-            for (int w = my_head; w < kWarps; w += wh) top = fmaxf(top, s_ml[w * 8 + h].x);
-            const float mm = top == -INFINITY ? 0.0f : top;
-            for (int w = my_head; w < kWarps; w += wh) {
-              const float2 ml = s_ml[w * 8 + h];
-              const float f = exp2_fast(ml.x - mm);
-              const float4 x = *reinterpret_cast<const float4*>(s_sum + (w * 8 + h) * G::kPitch + d);
-              sum += ml.y * f;
-              v.x += x.x * f;
-              v.y += x.y * f;
-              v.z += x.z * f;
-              v.w += x.w * f;
-            }
-          }
-          const int64_t hq = static_cast<int64_t>(hk) * GQ + g0 + hn;
-          if (d < a.D) {  // D is a multiple of 8
-            if (whole) {
-              const float inv = 1.0f / sum;
-              __align__(8) T r[4] = {from_f32<T>(v.x * inv), from_f32<T>(v.y * inv), from_f32<T>(v.z * inv), from_f32<T>(v.w * inv)};
-              *reinterpret_cast<uint2*>(static_cast<T*>(a.o) + seq * a.o_s + hq * a.o_h + d) = *reinterpret_cast<const uint2*>(r);
+          for (int i = lane; i < (4 / wt) * (DM / 4); i += 32) {
+            const int h4 = my_tile + wt * (i / (DM / 4)), h = half * 4 + h4, d = i % (DM / 4) * 4, hn = n * 8 + h;
+            if (g0 + hn >= GQ) break;
+            float top = -INFINITY, sum = 0.0f;
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (wt == 1) {
+              const float2 ml = s_ml[warp * 8 + h];
+              top = ml.x;
+              sum = ml.y;
+              v = *reinterpret_cast<const float4*>(s_sum + (warp * 4 + h4) * G::kPitch + d);
             } else {
-              *reinterpret_cast<float4*>(part + hn * stride + d) = v;
+              for (int w = my_head; w < kWarps; w += wh) top = fmaxf(top, s_ml[w * 8 + h].x);
+              const float mm = top == -INFINITY ? 0.0f : top;
+              for (int w = my_head; w < kWarps; w += wh) {
+                const float2 ml = s_ml[w * 8 + h];
+                const float f = exp2_fast(ml.x - mm);
+                const float4 x = *reinterpret_cast<const float4*>(s_sum + (w * 4 + h4) * G::kPitch + d);
+                sum += ml.y * f;
+                v.x += x.x * f;
+                v.y += x.y * f;
+                v.z += x.z * f;
+                v.w += x.w * f;
+              }
+            }
+            const int64_t hq = static_cast<int64_t>(hk) * GQ + g0 + hn;
+            if (d < a.D) {  // D is a multiple of 8
+              if (whole) {
+                const float inv = 1.0f / sum;
+                __align__(8) T r[4] = {from_f32<T>(v.x * inv), from_f32<T>(v.y * inv), from_f32<T>(v.z * inv), from_f32<T>(v.w * inv)};
+                *reinterpret_cast<uint2*>(static_cast<T*>(a.o) + seq * a.o_s + hq * a.o_h + d) = *reinterpret_cast<const uint2*>(r);
+              } else {
+                *reinterpret_cast<float4*>(part + hn * stride + d) = v;
+              }
+            }
+            if (d == 0) {
+              if (!whole) {
+                part[hn * stride + stride - 4] = top;
+                part[hn * stride + stride - 3] = sum;
+              } else if (a.lse) {
+                a.lse[seq * a.Hq + hq] = top * kLn2 + logf(sum);
+              }
             }
           }
-          if (d == 0) {
-            if (!whole) {
-              part[hn * stride + stride - 4] = top;
-              part[hn * stride + stride - 3] = sum;
-            } else if (a.lse) {
-              a.lse[seq * a.Hq + hq] = top * kLn2 + logf(sum);
-            }
-          }
+          if (wt > 1) __syncthreads();
+          else __syncwarp();
         }
-        if (wt > 1) __syncthreads();
-        else __syncwarp();
       }
       tile0 = use.tile;
       clear_sums();
@@ -363,13 +363,12 @@ inline int log2_of(int n) {
   return l;
 }
 
-template <bool F16, int DM, int NT>
-cudaError_t launch(const PagedArgs& a, int sms, cudaStream_t s) {
+template <bool F16, int DM, int NT, int CTAS>
+cudaError_t launch(const PagedArgs& a, const PagedShape& p, int sms, cudaStream_t s) {
   using G = Geo<DM>;
   static SmemLimit limit;
-  auto kern = paged_mma_kernel<F16, DM, NT>;
+  auto kern = paged_mma_kernel<F16, DM, NT, CTAS>;
   if (cudaError_t e = limit.allow(kern, G::kSmem)) return e;
-  const PagedShape p = paged_shape_mma(a.Hq / a.Hk, a.Hk, a.D, a.k_head < a.k_token);
   const int ctas = p.ctas * sms;
   if (cudaError_t e = launch_early(kern, dim3(static_cast<unsigned>(ctas)), kThreads, G::kSmem, s, a, p.groups, log2_of(p.wh))) return e;
   return launch_paged_join<typename std::conditional<F16, __half, __nv_bfloat16>::type>(a, ctas, p.group, p.groups, p.wh, s);
@@ -377,18 +376,24 @@ cudaError_t launch(const PagedArgs& a, int sms, cudaStream_t s) {
 
 template <bool F16>
 cudaError_t launch_width(const PagedArgs& a, int sms, cudaStream_t s) {
-  const bool wide = paged_shape_mma(a.Hq / a.Hk, a.Hk, a.D, a.k_head < a.k_token).group == 16;
-  if (a.D <= 64) return wide ? launch<F16, 64, 2>(a, sms, s) : launch<F16, 64, 1>(a, sms, s);
-  if (a.D <= 128) return wide ? launch<F16, 128, 2>(a, sms, s) : launch<F16, 128, 1>(a, sms, s);
-  return launch<F16, 256, 1>(a, sms, s);
+  const PagedShape p = paged_shape_mma(a.Hq / a.Hk, a.Hk, a.D, a.k_head < a.k_token);
+  const bool wide = p.group == 16;
+  if (a.D <= 64) return wide ? launch<F16, 64, 2, 3>(a, p, sms, s) : launch<F16, 64, 1, 3>(a, p, sms, s);
+  if (a.D > 128) return launch<F16, 256, 1, 1>(a, p, sms, s);
+  if (wide) return launch<F16, 128, 2, 3>(a, p, sms, s);
+  return p.ctas == 3 ? launch<F16, 128, 1, 3>(a, p, sms, s) : launch<F16, 128, 1, 2>(a, p, sms, s);
 }
 
 }  // namespace
 
 // Groups of 16 query heads from 9 on, so that the rows are read half as often (not beside the
-// registers that 256 columns take).
+// registers that 256 columns take).  Three CTAs a SM where a tile's arithmetic takes longer than
+// its bytes (463,000 tokens over 8 heads of 80: 115 us against 123 with two, 121 against 146 in
+// pages that no tile fits), two where HBM is busy with fewer, whose order it minds (of 128: 274
+// us with two, 281 with three; with three stages a ring 285).
 PagedShape paged_shape_mma(int G, int Hk, int D, bool together) {
-  return paged_shape(G, Hk, G > 8 && D <= 128 ? 16 : 8, kWarps, D <= 64 ? Geo<64>::kCtas : D <= 128 ? Geo<128>::kCtas : Geo<256>::kCtas, together);
+  const int group = G > 8 && D <= 128 ? 16 : 8, ctas = D > 128 ? 1 : D > 112 && group == 8 ? 2 : 3;
+  return paged_shape(G, Hk, group, kWarps, ctas, together);
 }
 
 cudaError_t launch_paged_mma(bool f16, const PagedArgs& a, int sms, cudaStream_t s) {

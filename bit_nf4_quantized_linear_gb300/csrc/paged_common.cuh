@@ -195,12 +195,20 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(PagedArgs a
   __shared__ float s_acc[WIDE ? kJoinWarps : 1][DV * 32], s_ml[WIDE ? kJoinWarps : 1][2];
   constexpr int kMost = kJoinCtas;
   __shared__ unsigned s_begin[kMost / 32], s_end[kMost / 32];
+  __shared__ PagedRec s_me;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = ctas;
   grid_wait();
   // which CTAs begin a cut pair, and which end one
+  constexpr int kEach = kMost / (kJoinWarps * 32);
+  PagedRec rec[kEach];
 #pragma unroll
-  for (int i = 0; i < kMost / (kJoinWarps * 32); ++i) {
-    const int p = (i * kJoinWarps + warp) * 32 + lane, f = p < n ? a.rec[p].flags : 0;
+  for (int i = 0; i < kEach; ++i) {
+    const int p = (i * kJoinWarps + warp) * 32 + lane;
+    rec[i] = p < n ? a.rec[p] : PagedRec{0, 0, 0};
+  }
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int f = rec[i].flags;
     const unsigned begin = __ballot_sync(0xffffffffu, f & 1), end = __ballot_sync(0xffffffffu, f & 4);
     if (lane == 0) {
       s_begin[i * kJoinWarps + warp] = begin;
@@ -226,7 +234,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(PagedArgs a
   } else if (!(s_begin[c >> 5] >> (c & 31) & 1)) {
     return;
   }
-  const PagedRec me = a.rec[c];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i)
+    if ((i * kJoinWarps + warp) * 32 + lane == c) s_me = rec[i];
+  __syncthreads();
+  const PagedRec me = s_me;
   int last;  // the first after c that ends one ends this one
   {
     const int word = c >> 5;

@@ -46,6 +46,7 @@ struct TileCopies {
   uint32_t* s_valid;  // [ring slots]: which rows of a tile are tokens
   int row0, col;
   bool in, one_page;
+  int page, slot;  // of the tile that is copied next, where one page holds it: looked up a tile ahead
 
   __device__ __forceinline__ TileCopies(const PagedArgs& a, uint32_t ring, uint32_t* valid) {
     const int lane = threadIdx.x & 31;
@@ -55,6 +56,15 @@ struct TileCopies {
     one_page = a.page_size % ROWS == 0;  // a tile lies in one page
     dst0 = ring + at_chunk<kRowBytes>(row0, lane % kPieces);
     s_valid = valid;
+  }
+
+  // Looks up the page of the tokens from tok0 on of the unit `load`; before its start().
+  __device__ __forceinline__ void look_up(const PagedArgs& a, const Walk& load, int tok0) {
+    if (one_page && load.left > 0 && tok0 < load.len) {
+      const unsigned p = paged_index(a, tok0);
+      slot = tok0 - static_cast<int>(p) * a.page_size;
+      page = a.table[load.seq * a.ld_table + p];
+    }
   }
 
   // Starts the copies of the tokens from tok0 on of the unit `load`, key head hk, into ring slot `st`.
@@ -68,13 +78,13 @@ struct TileCopies {
       constexpr unsigned kFull = (1u << ROWS) - 1u;
       unsigned valid;
       if (one_page) {
-        int slot;
-        const int64_t page = paged_slot(a, load.seq, tok0, &slot);
-        const int n = page < 0 ? 0 : rows;
+        const bool known = page >= 0 && page < a.pages;
+        if (!known && a.status) atomicCAS(a.status, 0, kStatusBadOffsets);
+        const int n = known ? rows : 0;
         valid = n >= ROWS ? kFull : (1u << n) - 1u;
         const T *kp = none, *vp = none;
         int64_t ks = 0, vs = 0;
-        if (in && page >= 0) {
+        if (in && known) {
           kp = static_cast<const T*>(a.k) + (page * a.k_page + (slot + row0) * a.k_token + hk * a.k_head + col);
           vp = static_cast<const T*>(a.v) + (page * a.v_page + (slot + row0) * a.v_token + hk * a.v_head + col);
           ks = kPer * a.k_token;
