@@ -194,10 +194,26 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(PagedArgs a
   constexpr int kAtOnce = DV <= 4 ? 4 : 2;
   __shared__ float s_acc[WIDE ? kJoinWarps : 1][DV * 32], s_ml[WIDE ? kJoinWarps : 1][2];
   constexpr int kMost = kJoinCtas;
-  __shared__ unsigned s_begin[kMost / 32], s_end[kMost / 32];
+  __shared__ unsigned s_begin[kMost / 32], s_end[kMost / 32], s_used[kMost / 32];  // flags 1, 4 and 2
   __shared__ PagedRec s_me;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = ctas;
-  grid_wait();
+  const int st = paged_part_stride(a.D), G = a.Hq / a.Hk, each = G < heads ? G : heads, step = WIDE ? kJoinWarps : 1;
+  // kAtOnce parts from CTA p0 on of query head y of the set, that of CTA c in slot 1.
+  float pm[kAtOnce], pl[kAtOnce], pv[kAtOnce][DV];
+  auto read = [&](int y, int p0, int c) {
+    const int sub = y / each, h = sub * heads + y - sub * each;
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int p = min(p0 + step * i, n - 1);
+      const float* part = a.part + (static_cast<int64_t>(p * 2 + (p == c)) * (wh * heads) + h) * st;
+      pm[i] = part[st - 4];
+      pl[i] = part[st - 3];
+#pragma unroll
+      for (int j = 0; j < DV; ++j) pv[i][j] = lane + 32 * j < a.D ? part[lane + 32 * j] : 0.0f;
+    }
+  };
+  grid_wait();  // (no grid_allow: the attention of the next step would take the room of this one's last CTAs)
+  if (!WIDE && warp < wh * each) read(warp, blockIdx.x, blockIdx.x);  // before it is known what they are worth
   // which CTAs begin a cut pair, and which end one
   constexpr int kEach = kMost / (kJoinWarps * 32);
   PagedRec rec[kEach];
@@ -209,8 +225,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(PagedArgs a
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
     const int f = rec[i].flags;
-    const unsigned begin = __ballot_sync(0xffffffffu, f & 1), end = __ballot_sync(0xffffffffu, f & 4);
+    const unsigned begin = __ballot_sync(0xffffffffu, f & 1), end = __ballot_sync(0xffffffffu, f & 4), used = __ballot_sync(0xffffffffu, f & 2);
     if (lane == 0) {
+      s_used[i * kJoinWarps + warp] = used;
       s_begin[i * kJoinWarps + warp] = begin;
       s_end[i * kJoinWarps + warp] = end;
     }
@@ -249,28 +266,21 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(PagedArgs a
     const int at = __ffs(some) - 1;
     last = at * 32 + __ffs(__shfl_sync(0xffffffffu, end, at)) - 1;
   }
-  const int st = paged_part_stride(a.D), G = a.Hq / a.Hk, each = G < heads ? G : heads;
   for (int y = WIDE ? blockIdx.y : warp; y < wh * each; y += WIDE ? wh * each : kJoinWarps) {
-    const int sub = y / each, h = sub * heads + y - sub * each, head = me.set * wh + sub, hk = head / groups;
+    const int sub = y / each, head = me.set * wh + sub, hk = head / groups;
     const int g = (head - hk * groups) * heads + y - sub * each;
     if (g >= G) continue;
-    const int step = WIDE ? kJoinWarps : 1;
     float m = -INFINITY, l = 0.0f, acc[DV] = {};
     for (int p0 = c + (WIDE ? warp : 0); p0 <= last; p0 += step * kAtOnce) {
-      float pm[kAtOnce], pl[kAtOnce], pv[kAtOnce][DV];
+      if (WIDE || y != warp || p0 != c) read(y, p0, c);
 #pragma unroll
       for (int i = 0; i < kAtOnce; ++i) {
-        const int p = min(p0 + step * i, n - 1);
-        const float* part = a.part + (static_cast<int64_t>(p * 2 + (p == c)) * (wh * heads) + h) * st;
-        const bool in = p0 + step * i <= last && (p == c || (a.rec[p].flags & 2));
-        const float m0 = part[st - 4], l0 = part[st - 3];
-        pm[i] = in ? m0 : -INFINITY;
-        pl[i] = in ? l0 : 0.0f;
+        const int p = p0 + step * i;
+        const bool in = p <= last && (p == c || (s_used[p >> 5] >> (p & 31) & 1));
+        pm[i] = in ? pm[i] : -INFINITY;
+        pl[i] = in ? pl[i] : 0.0f;
 #pragma unroll
-        for (int j = 0; j < DV; ++j) {
-          const float v = lane + 32 * j < a.D ? part[lane + 32 * j] : 0.0f;
-          pv[i][j] = in ? v : 0.0f;
-        }
+        for (int j = 0; j < DV; ++j) pv[i][j] = in ? pv[i][j] : 0.0f;
       }
 #pragma unroll
       for (int i = 0; i < kAtOnce; ++i) {
@@ -291,26 +301,26 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(PagedArgs a
       if (lane == 0 && a.lse) a.lse[me.seq * a.Hq + hq] = m * kLn2 + logf(l);
     } else {
 #pragma unroll
-    for (int i = 0; i < DV; ++i) s_acc[warp][lane + 32 * i] = acc[i];
-    if (lane == 0) {
-      s_ml[warp][0] = m;
-      s_ml[warp][1] = l;
-    }
-    __syncthreads();
-    float top = -INFINITY;
-    for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, s_ml[w][0]);
-    const float mm = top == -INFINITY ? 0.0f : top;
-    for (int d = threadIdx.x; d < a.D; d += kJoinWarps * 32) {
-      float v = 0.0f, sum = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kJoinWarps; ++w) {
-        const float f = exp2f(s_ml[w][0] - mm);
-        sum += s_ml[w][1] * f;
-        v += s_acc[w][d] * f;
+      for (int i = 0; i < DV; ++i) s_acc[warp][lane + 32 * i] = acc[i];
+      if (lane == 0) {
+        s_ml[warp][0] = m;
+        s_ml[warp][1] = l;
       }
-      o[d] = from_f32<T>(v / sum);
-      if (d == 0 && a.lse) a.lse[me.seq * a.Hq + hq] = top * kLn2 + logf(sum);
-    }
+      __syncthreads();
+      float top = -INFINITY;
+      for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, s_ml[w][0]);
+      const float mm = top == -INFINITY ? 0.0f : top;
+      for (int d = threadIdx.x; d < a.D; d += kJoinWarps * 32) {
+        float v = 0.0f, sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) {
+          const float f = exp2f(s_ml[w][0] - mm);
+          sum += s_ml[w][1] * f;
+          v += s_acc[w][d] * f;
+        }
+        o[d] = from_f32<T>(v / sum);
+        if (d == 0 && a.lse) a.lse[me.seq * a.Hq + hq] = top * kLn2 + logf(sum);
+      }
     }
   }
 }
