@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(kAnyWarps * 32) paged_any_kernel(PagedArgs a, 
 #pragma unroll
           for (int i = 0; i < DV; ++i)
             if (lane + 32 * i < a.D) {
-              if (whole) o[lane + 32 * i] = from_f32<T>(acc[h][i] / lh);
+              if (whole) o[lane + 32 * i] = from_f32<T>(paged_mean(acc[h][i], lh));
               else part[h * st + lane + 32 * i] = acc[h][i];
             }
           if (lane == 0) {

@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, Geo<DM, HC>::kCtas) paged_f32_kernel
           }
           const int64_t hq = static_cast<int64_t>(hk) * GQ + g0 + hn;
           if (d < a.D) {
-            if (whole) static_cast<float*>(a.o)[seq * a.o_s + hq * a.o_h + d] = v / sum;
+            if (whole) static_cast<float*>(a.o)[seq * a.o_s + hq * a.o_h + d] = paged_mean(v, sum);
             else part[hn * stride + d] = v;
           }
           if (d == 0) {

@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) paged_mma_kernel(PagedArgs a, 
             const int64_t hq = static_cast<int64_t>(hk) * GQ + g0 + hn;
             if (d < a.D) {  // D is a multiple of 8
               if (whole) {
-                const float inv = 1.0f / sum;
+                const float inv = paged_mean(1.0f, sum);
                 __align__(8) T r[4] = {from_f32<T>(v.x * inv), from_f32<T>(v.y * inv), from_f32<T>(v.z * inv), from_f32<T>(v.w * inv)};
                 *reinterpret_cast<uint2*>(static_cast<T*>(a.o) + seq * a.o_s + hq * a.o_h + d) = *reinterpret_cast<const uint2*>(r);
               } else {

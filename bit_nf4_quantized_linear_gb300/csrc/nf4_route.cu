@@ -34,7 +34,8 @@ namespace nf4 {
 namespace {
 
 constexpr int kRouteSingle = 32;  // tokens that one CTA routes and sorts alone
-constexpr int kRouteBytes = 255;  // tokens of a CTA whose counts are held in bytes
+// Whether a CTA's counts fit bytes, and the sums of all CTAs' 16 bits.
+__host__ __device__ __forceinline__ bool route_bytes(int per, int ctas) { return per <= 255 && per * ctas <= 65535; }
 constexpr int kPlaceThreads = 512;
 constexpr unsigned kAll = 0xffffffffu;
 
@@ -596,7 +597,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a, int per
     for (int e = threadIdx.x; e < pitch; e += kThreads) {
       const int64_t at = static_cast<int64_t>(blockIdx.x) * pitch + e;
       const int n = e < a.E ? s_base[e] : 0;
-      if (per <= kRouteBytes) reinterpret_cast<uint8_t*>(a.counts)[at] = static_cast<uint8_t>(n);
+      if (route_bytes(per, gridDim.x)) reinterpret_cast<uint8_t*>(a.counts)[at] = static_cast<uint8_t>(n);
       else a.counts[at] = n;
     }
     return;
@@ -614,8 +615,8 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a, int per
 }
 
 // The second pass: a CTA for each CTA of the first, with the same tokens.  Each adds the counts
-// of all CTAs, and of those before it, 16 experts a thread.  BYTES: counts of at most
-// kRouteBytes a CTA, so that a sum fits 16 bits and two are added at once.
+// of all CTAs, and of those before it, 16 experts a thread.  BYTES: as route_bytes() says, so
+// that two sums are added at once.
 template <bool BYTES>
 __global__ void __launch_bounds__(kPlaceThreads) route_place_kernel(RouteArgs a, int per) {
   __shared__ int s_all[kMaxExperts], s_below[kMaxExperts], s_red[32];
@@ -786,7 +787,7 @@ cudaError_t launch_fwd(const RouteArgs& a, int ctas, int per, cudaStream_t s) {
   if (cudaError_t e = limit.allow(kern, kWarps * V * 32 * 10)) return e;
   if (cudaError_t e = launch_early(kern, dim3(static_cast<unsigned>(ctas)), kWarps * 32, kWarps * each, s, a, per)) return e;
   if (!a.offsets || ctas == 1) return cudaSuccess;
-  return launch_early(per <= kRouteBytes ? route_place_kernel<true> : route_place_kernel<false>, dim3(static_cast<unsigned>(ctas)),
+  return launch_early(route_bytes(per, ctas) ? route_place_kernel<true> : route_place_kernel<false>, dim3(static_cast<unsigned>(ctas)),
                       kPlaceThreads, 0, s, a, per);
 }
 

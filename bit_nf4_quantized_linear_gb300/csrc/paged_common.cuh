@@ -168,11 +168,14 @@ __device__ __forceinline__ Walk paged_run(const PagedArgs& a, int sets, int log2
   return w;
 }
 
+// A weighted mean; 0 where no token has a weight (all scores -inf, or no page in the table).
+__device__ __forceinline__ float paged_mean(float v, float sum) { return sum == 0.0f ? 0.0f : v / sum; }
+
 // Sequences of no tokens: zeros, and -inf for the logarithm of their sum.
 template <typename T>
 __device__ __forceinline__ void paged_empty(const PagedArgs& a) {
   for (int64_t s = blockIdx.x; s < a.nseq; s += gridDim.x) {
-    if (a.lengths[s] > 0) continue;
+    if (paged_len(a, s) > 0) continue;
     for (int i = threadIdx.x; i < a.Hq * a.D; i += blockDim.x)
       static_cast<T*>(a.o)[s * a.o_s + static_cast<int64_t>(i / a.D) * a.o_h + i % a.D] = T(0.0f);
     for (int h = threadIdx.x; a.lse && h < a.Hq; h += blockDim.x) a.lse[s * a.Hq + h] = -INFINITY;
@@ -297,7 +300,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(PagedArgs a
     if constexpr (!WIDE) {
 #pragma unroll
       for (int j = 0; j < DV; ++j)
-        if (lane + 32 * j < a.D) o[lane + 32 * j] = from_f32<T>(acc[j] / l);
+        if (lane + 32 * j < a.D) o[lane + 32 * j] = from_f32<T>(paged_mean(acc[j], l));
       if (lane == 0 && a.lse) a.lse[me.seq * a.Hq + hq] = m * kLn2 + logf(l);
     } else {
 #pragma unroll
@@ -318,7 +321,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(PagedArgs a
           sum += s_ml[w][1] * f;
           v += s_acc[w][d] * f;
         }
-        o[d] = from_f32<T>(v / sum);
+        o[d] = from_f32<T>(paged_mean(v, sum));
         if (d == 0 && a.lse) a.lse[me.seq * a.Hq + hq] = top * kLn2 + logf(sum);
       }
     }

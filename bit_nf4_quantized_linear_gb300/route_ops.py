@@ -115,7 +115,7 @@ def route_experts_bwd(logits: torch.Tensor, routes: Routes, *, grad_weights: Opt
     for t in (experts, token_rows, grad_weights, grad_row_weight):
         if t is not None and t.get_device() != at:
             _one_device(name, logits, experts, token_rows, grad_weights, grad_row_weight)
-    if experts.dtype is not torch.int32 or experts.dim() != 2 or experts.shape[0] != logits.shape[0] or not experts.is_contiguous():
+    if experts.dtype is not torch.int32 or experts.dim() != 2 or experts.shape[:1] != logits.shape[:1] or not experts.is_contiguous():
         raise ValueError(f"{name}: routes.experts must be the contiguous int32 [tokens, k] of the forward")
     T, k = experts.shape
     d, held = _route(name, logits, k, score, None, 1, 1, 1, renormalise, scale, None)

@@ -508,13 +508,15 @@ nf4_status nf4_adamw_state_values(const uint8_t* m, const uint8_t* v, const floa
  * lengths[i] tokens of sequence i; query head h reads key head h / (Hq / Hk).
  *   q, o        [nseq, Hq, D] of `dtype`, sequence and head strides in elements.
  *   lse         fp32 [nseq][Hq], natural log of the sum of exponentials, or NULL.
- *   Idle rows: zeros, and lse -inf.  Slots past a sequence's length are never read.
+ *   Idle rows, and rows no token of which has a weight: zeros, and lse -inf.  Slots past a
+ *   sequence's length are never read.
  *   ws: nf4_workspace_size(NF4_OP_PAGED_ATTENTION, 0, Hq, D, Hk) bytes, 16-byte aligned, of a
  *   call's own (calls on two streams, or two graphs whose replays overlap, must not share it).
  * Hq a multiple of Hk, 1 <= D <= 256.  fp32 sums and statistics; partial results over the
  * length are added in a fixed order (deterministic for given lengths and device).  16-bit
  * types with D a multiple of 8, 16-byte aligned pointers and strides of a multiple of 8
- * elements run on the tensor cores, everything else in fp32 arithmetic. */
+ * elements run on the tensor cores, everything else in fp32 arithmetic (quickest for fp32 with
+ * D a multiple of 4 up to 128, 16-byte aligned). */
 typedef struct {
   void* k;
   void* v;

@@ -290,6 +290,88 @@ def test_bad_pages_and_lengths_are_recorded_and_passed_over(dtype):
         assert ((o2[:2].double() - want).abs() <= bo).all() and ((lse2[:2].double() - wl).abs() <= bl).all()
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("D", [64, 37])
+def test_rows_without_a_weight_are_zero(dtype, D):
+    """All scores -inf, all pages missing, a table of no columns: zeros and -inf, beside rows that are as ever."""
+    kp, vp, table, lengths = cache([40, 70, 33], 2, D, dtype)
+    q = queries(3, 4, D, dtype).abs() + 0.1
+    o, lse = nf4.paged_attention(q, kp, vp, table, lengths)
+    k2 = kp.clone()
+    k2[table[1, :5].long()] = -math.inf
+    o2, lse2 = nf4.paged_attention(q, k2, vp, table, lengths)
+    assert (o2[1] == 0).all() and (lse2[1] == -math.inf).all() and torch.equal(o2[::2], o[::2]) and torch.equal(lse2[::2], lse[::2])
+    t = table.clone()
+    t[1] = -1
+    o2, lse2 = nf4.paged_attention(q, kp, vp, t, lengths)
+    assert nf4.device_status(clear=True) == BAD_OFFSETS
+    assert (o2[1] == 0).all() and (lse2[1] == -math.inf).all() and torch.equal(o2[::2], o[::2]) and torch.equal(lse2[::2], lse[::2])
+    o2, lse2 = nf4.paged_attention(q, kp, vp, table[:, :0], lengths)
+    assert nf4.device_status(clear=True) == BAD_OFFSETS
+    assert (o2 == 0).all() and (lse2 == -math.inf).all()
+    o2, lse2 = nf4.paged_attention(q[:0], kp, vp, table[:0], lengths[:0])
+    assert o2.shape == (0, 4, D) and lse2.shape == (0, 4)
+
+
+def test_decoding_under_inference_mode():
+    with torch.inference_mode():
+        kp, vp, table, lengths = cache([40, 17], 2, 64, BF16)
+        k, v = queries(2, 2, 64, BF16, 5), queries(2, 2, 64, BF16, 6)
+        nf4.paged_append(k, v, kp, vp, table, lengths)
+        check(queries(2, 4, 64, BF16), kp, vp, table, lengths)
+        last = ref.slots_of(table[0], 40, 16)
+        assert torch.equal(kp[last[0][-1], last[1][-1]], k[0])
+
+
+def test_refusals():
+    """Every argument that does not fit is refused with a message, before anything is launched."""
+    kp, vp, table, lengths = cache([20, 5], 2, 64, BF16)
+    q, k, v = queries(2, 4, 64, BF16), queries(2, 2, 64, BF16), queries(2, 2, 64, BF16)
+    cu = torch.tensor([0, 1, 2], dtype=torch.int32, device=DEV)
+    before = nf4.path_counters()["total"]
+
+    def attend(message, q=q, kp=kp, vp=vp, table=table, lengths=lengths, **kw):
+        with pytest.raises(ValueError, match=message):
+            nf4.paged_attention(q, kp, vp, table, lengths, **kw)
+
+    def append(message, k=k, v=v, kp=kp, vp=vp, table=table, lengths=lengths, cu=None):
+        with pytest.raises(ValueError, match=message):
+            nf4.paged_append(k, v, kp, vp, table, lengths, cu)
+
+    for f in (attend, append):
+        f("pages", kp=kp[0])
+        f("pages", vp=vp[:, :3])
+        f("pages", vp=vp.half())
+        f("fp32, bf16 or fp16", kp=kp.double(), vp=vp.double())
+        f("unit stride", kp=kp.transpose(2, 3).contiguous().transpose(2, 3))
+        f("lengths", lengths=lengths.long())
+        f("lengths", lengths=torch.zeros(4, dtype=torch.int32, device=DEV)[::2])
+        f("page_table", table=table[:1])
+        f("page_table", table=table.long())
+        f("page_table", table=table.T.contiguous().T)
+        f("CUDA", table=table.cpu())
+        f("CUDA", lengths=lengths.cpu())
+    attend("q must be", q=q.half())
+    attend("q must be", q=q[..., :32])
+    attend("does not fit", q=q[:1])
+    attend("does not fit", q=queries(2, 3, 64, BF16))
+    attend("does not fit", q=q[:, :0])
+    attend("unit stride", q=q.transpose(1, 2).contiguous().transpose(1, 2))
+    attend("out must", out=torch.zeros(2, 2, 64, dtype=BF16, device=DEV))
+    attend("out must be", out=torch.zeros(2, 4, 64, device=DEV))
+    attend("storage", out=torch.zeros(4, 64, dtype=BF16, device=DEV).expand(2, 4, 64))
+    append("k must be", k=queries(2, 4, 64, BF16))
+    append("v must be", v=v.half())
+    append("rows of keys", k=queries(3, 2, 64, BF16))
+    append("rows of keys", k=queries(3, 2, 64, BF16), v=queries(3, 2, 64, BF16))
+    append("cu_seqlens", cu=cu[:2])
+    append("cu_seqlens", cu=cu.long())
+    append("cu_seqlens", cu=cu.cpu())
+    append("share storage", kp=kp[:1].expand(kp.shape))
+    append("share storage", vp=vp[:, :1].expand(vp.shape))
+    assert nf4.path_counters()["total"] == before
+
+
 def test_repeats_bit_for_bit_and_on_another_stream():
     kp, vp, table, lengths = cache([5000, 17, 0, 900], 4, 128, BF16)
     q = queries(4, 16, 128, BF16)

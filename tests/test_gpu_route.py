@@ -275,6 +275,52 @@ def test_route_repeats_bit_for_bit_on_streams_and_in_graphs():
                 assert torch.equal(a, b)
 
 
+def test_route_refusals():
+    """Every argument that does not fit is refused with a message, before anything is launched."""
+    x = gen(19)(10, 24)
+    r = nf4.route_experts(x, 4)
+    before = nf4.path_counters()["total"]
+
+    def fwd(message, x=x, k=4, **kw):
+        with pytest.raises(ValueError, match=message):
+            nf4.route_experts(x, k, **kw)
+
+    fwd("logits", x=x[0])
+    fwd("logits", x=x[:, :0])
+    fwd("logits", x=x.T.contiguous().T)
+    fwd("fp32, bf16 or fp16", x=x.double())
+    fwd("CUDA", x=x.cpu())
+    fwd("score", score="relu")
+    for kw in (dict(groups=0), dict(groups=5), dict(groups=4, top_groups=0), dict(groups=4, top_groups=5), dict(group_top=3)):
+        fwd("groups", **kw)
+    fwd("experts of the", k=0)
+    fwd("experts of the", k=25)
+    fwd("experts of the", groups=6, top_groups=1, k=5)
+    fwd("bias", bias=torch.zeros(23, device=DEV))
+    fwd("bias", bias=torch.zeros(24, device=DEV, dtype=BF16))
+    fwd("CUDA", bias=torch.zeros(24))
+    fwd("live", live=torch.zeros(9, dtype=torch.bool, device=DEV))
+    fwd("live", live=torch.zeros(10, device=DEV))
+    for E, k, kw in ((513, 4, {}), (64, 33, {}), (64, 4, dict(groups=64))):
+        with pytest.raises(nf4._lib.NF4Error, match="UNSUPPORTED_SHAPE"):
+            nf4.route_experts(torch.zeros(2, E, device=DEV), k, **kw)
+
+    def bwd(message, x=x, r=r, **kw):
+        with pytest.raises(ValueError, match=message):
+            nf4.route_experts_bwd(x, r, **kw)
+
+    g = torch.zeros(10, 4, device=DEV)
+    bwd("routes.experts", r=r._replace(experts=r.experts.long()), grad_weights=g)
+    bwd("routes.experts", x=x[:5], grad_weights=g)
+    bwd("grad_weights", grad_weights=g[:, :3])
+    bwd("grad_weights", grad_weights=g.half())
+    bwd("grad_row_weight", grad_row_weight=g)
+    bwd("token_rows", r=r._replace(token_rows=None), grad_row_weight=g.flatten())
+    bwd("score", grad_weights=g, score="none")
+    bwd("CUDA", grad_weights=g.cpu())
+    assert nf4.path_counters()["total"] == before
+
+
 def test_route_autograd():
     """Through nf4_route: gradients by weight and by row, none asked for, second derivatives refused."""
     x = gen(16)(70, 24).requires_grad_()
