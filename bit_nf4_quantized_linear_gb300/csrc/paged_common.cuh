@@ -168,6 +168,12 @@ __device__ __forceinline__ Walk paged_run(const PagedArgs& a, int sets, int log2
   return w;
 }
 
+__device__ __forceinline__ float exp2_fast(float x) {  // relative error 2^-22
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // A weighted mean; 0 where no token has a weight (all scores -inf, or no page in the table).
 __device__ __forceinline__ float paged_mean(float v, float sum) { return sum == 0.0f ? 0.0f : v / sum; }
 
@@ -194,7 +200,7 @@ constexpr int kJoinCtas = 1024;  // of the attention kernel at most
 
 template <typename T, int DV, bool WIDE>
 __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(PagedArgs a, int ctas, int heads, int groups, int wh) {
-  constexpr int kAtOnce = DV <= 4 ? 4 : 2;
+  constexpr int kAtOnce = WIDE && DV <= 4 ? 4 : 2;  // a cut of many pairs leaves most of them two parts
   __shared__ float s_acc[WIDE ? kJoinWarps : 1][DV * 32], s_ml[WIDE ? kJoinWarps : 1][2];
   constexpr int kMost = kJoinCtas;
   __shared__ unsigned s_begin[kMost / 32], s_end[kMost / 32], s_used[kMost / 32];  // flags 1, 4 and 2
@@ -288,7 +294,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(PagedArgs a
 #pragma unroll
       for (int i = 0; i < kAtOnce; ++i) {
         const float top = fmaxf(m, pm[i]), mm = top == -INFINITY ? 0.0f : top;
-        const float f0 = exp2f(m - mm), f1 = exp2f(pm[i] - mm);
+        const float f0 = exp2_fast(m - mm), f1 = exp2_fast(pm[i] - mm);
         m = top;
         l = l * f0 + pl[i] * f1;
 #pragma unroll
@@ -317,7 +323,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(PagedArgs a
         float v = 0.0f, sum = 0.0f;
 #pragma unroll
         for (int w = 0; w < kJoinWarps; ++w) {
-          const float f = exp2f(s_ml[w][0] - mm);
+          const float f = exp2_fast(s_ml[w][0] - mm);
           sum += s_ml[w][1] * f;
           v += s_acc[w][d] * f;
         }

@@ -27,12 +27,6 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ float exp2_fast(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
 // The copies of a tile of ROWS tokens, keys and then values, rows of W values; columns past D
 // and rows past a length or without a page are zeros that nothing reads.  Lane i copies column
 // piece i % kPieces of rows i / kPieces and every kPer-th after it.
