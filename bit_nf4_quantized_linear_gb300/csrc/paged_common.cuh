@@ -194,7 +194,8 @@ __device__ __forceinline__ void paged_empty(const PagedArgs& a) {
 // pairs, which are cut into many.  Else a CTA for each CTA of the attention kernel, which may
 // begin one, a warp for each query head.  The time is that of a few dependent loads, so what a
 // load needs not wait for it does not: flags and sums of several parts are read at once, and
-// those of no use are dropped.
+// those of no use are dropped.  3 to 6 us of a call, most of it the wait for the attention
+// kernel's last write and the start of CTAs that found no room beside it.
 constexpr int kJoinWarps = 16;
 constexpr int kJoinCtas = 1024;  // of the attention kernel at most
 

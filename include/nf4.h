@@ -282,7 +282,8 @@ nf4_status nf4_linear_dgrad_f16(const void* gy, int64_t M, int64_t ldgy, const n
  *   w        the stacked weight: w->N == E * N_e rows, expert e owns rows
  *            [e*N_e, (e+1)*N_e); w->K = K.
  *   offsets  DEVICE int32 [E+1]: rows offsets[e] .. offsets[e+1]-1 of x belong to
- *            expert e; offsets[0] == 0, non-decreasing, offsets[E] == T.  Offsets
+ *            expert e; offsets[0] == 0, non-decreasing, offsets[E] <= T (rows from
+ *            offsets[E] on belong to none and are left as they were).  Offsets
  *            outside that contract are detected on the device: the bad expert's
  *            rows are skipped and NF4_ERR_BAD_OFFSETS is recorded in the device
  *            status word.
