@@ -280,6 +280,26 @@ __device__ __noinline__ unsigned choose_exactly(const RouteArgs& a, int64_t t, d
   return take_largest(key, a.k, &last);
 }
 
+// Whether all experts whose bit i (expert i * 32 + lane) is set, in any lane, have one logit and
+// one bias: then what fp32 finds equal is, and goes by the index.
+template <typename T, int V>
+__device__ __noinline__ bool all_alike(const RouteArgs& a, int64_t t, unsigned mask) {
+  const int lane = threadIdx.x & 31;
+  uint32_t lo[2] = {0xffffffffu, 0xffffffffu}, hi[2] = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (mask >> i & 1) {
+      const int e = i * 32 + lane;
+      const uint32_t k[2] = {key_of(to_f32(static_cast<const T*>(a.logits)[t * a.ld + e])), a.bias ? key_of(a.bias[e]) : 0u};
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        lo[j] = min(lo[j], k[j]);
+        hi[j] = max(hi[j], k[j]);
+      }
+    }
+  return __reduce_min_sync(kAll, lo[0]) == __reduce_max_sync(kAll, hi[0]) && __reduce_min_sync(kAll, lo[1]) == __reduce_max_sync(kAll, hi[1]);
+}
+
 __device__ __forceinline__ float ex2_fast(float x) {  // relative error 2^-22
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -370,16 +390,20 @@ __device__ __forceinline__ int route_token(const RouteArgs& a, int64_t t, double
         const bool sure = mine && f > low + far;
         const unsigned near = group_bits(mine && !sure && !(f < low - far), lanes), safe = group_bits(sure, lanes);
         if (__popc(near) + __popc(safe) != a.top_groups) {
-          if (!a.sigmoid && a.bias) {
-            unsure = true;
-          } else {  // the values that can count in the groups near the border
-            unsigned mask = 0;
+          // the values that can count in the groups near the border
+          unsigned mask = 0;
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-              const int g = group_of(min(i * 32 + lane, a.E - 1), inv);
-              const float from = __shfl_sync(kAll, least, g * lanes) - 4.0f * off;
-              mask |= (i * 32 + lane < a.E && c[i] > -INFINITY && (near >> g & 1) && !(c[i] < from)) << i;
-            }
+          for (int i = 0; i < V; ++i) {
+            const int g = group_of(min(i * 32 + lane, a.E - 1), inv);
+            const float from = __shfl_sync(kAll, least, g * lanes) - 4.0f * off;
+            mask |= (i * 32 + lane < a.E && c[i] > -INFINITY && (near >> g & 1) && !(c[i] < from)) << i;
+          }
+          const bool alike = low > -INFINITY && all_alike<T, V>(a, t, mask) && !__any_sync(kAll, mine && (near >> (lane / lanes) & 1) && f != low);
+          if (alike) {
+            // equal sums of equal values: the choice by fp32 stands
+          } else if (!a.sigmoid && a.bias) {
+            unsure = true;
+          } else {
             const int n = evaluate<T, V>(a, t, mask, top, row, list);
             double one = -INFINITY, two = -INFINITY;
             for (int j = 0; j < n; ++j) {
@@ -418,16 +442,20 @@ __device__ __forceinline__ int route_token(const RouteArgs& a, int64_t t, double
 #pragma unroll
         for (int i = 0; i < V; ++i) n += key[i] >= reach;
         if (__reduce_add_sync(kAll, n) != a.k) {
+          const bool was_picked = picked;
           picked = false;
-          unsure = !a.sigmoid || low == -INFINITY;
-          if (!unsure) {
-            const uint32_t above = key_of(low + far);
-            unsigned near = 0, safe = 0;
+          const uint32_t above = key_of(low + far);
+          unsigned near = 0, safe = 0;
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-              safe |= (key[i] > above) << i;
-              near |= (key[i] >= reach && key[i] <= above) << i;
-            }
+          for (int i = 0; i < V; ++i) {
+            safe |= (key[i] > above) << i;
+            near |= (key[i] >= reach && key[i] <= above) << i;
+          }
+          const bool alike = low > -INFINITY && all_alike<T, V>(a, t, near);
+          unsure = !alike && (!a.sigmoid || low == -INFINITY);
+          if (alike) {
+            picked = was_picked;
+          } else if (!unsure) {
             evaluate<T, V>(a, t, near, top, row, list);
             uint64_t wide[V], border;
 #pragma unroll
