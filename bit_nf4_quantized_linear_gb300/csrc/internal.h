@@ -186,6 +186,11 @@ inline PagedShape paged_shape(int G, int Hk, int group, int warps, int ctas, boo
   while (together && s.wh < warps && Hk * s.groups % (2 * s.wh) == 0) s.wh *= 2;
   return s;
 }
+inline int log2_of(int n) {
+  int l = 0;
+  while (n >> (l + 1)) ++l;
+  return l;
+}
 inline size_t paged_part_bytes(const PagedShape& s, int D) {  // of a SM
   return static_cast<size_t>(s.ctas) * (2 * s.wh * s.group * paged_part_stride(D) * sizeof(float) + sizeof(PagedRec));
 }

@@ -1160,7 +1160,7 @@ nf4_status nf4_paged_attention(const nf4_paged_cache* c, const void* q, int64_t 
   }
   // fp32 rows of whole 16-byte pieces have a kernel of their own
   const auto quads = [](int64_t page, int64_t token, int64_t head) { return page % 4 == 0 && token % 4 == 0 && head % 4 == 0; };
-  const bool rows = c->dtype == NF4_DTYPE_F32 && a.D % 4 == 0 && a.D <= 128 && aligned16(a.k) && aligned16(a.v) && aligned16(q) &&
+  const bool rows = c->dtype == NF4_DTYPE_F32 && a.D % 4 == 0 && aligned16(a.k) && aligned16(a.v) && aligned16(q) &&
                     quads(a.k_page, a.k_token, a.k_head) && quads(a.v_page, a.v_token, a.v_head);
   cudaError_t le = rows ? nf4::launch_paged_f32(a, dev.sms, static_cast<cudaStream_t>(stream))
                         : nf4::launch_paged_any(c->dtype, a, dev.sms, static_cast<cudaStream_t>(stream));

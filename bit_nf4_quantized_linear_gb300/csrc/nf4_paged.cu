@@ -88,9 +88,9 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(PagedArgs 
 
 // ------------------------------------------------------- attention, any layout --
 
-// fp32 arithmetic throughout, for rows that no 16-byte copy can take and fp32 past 128 columns:
-// right for everything, at an eighth of the others' rate (64 sequences of up to 4096 tokens, 8 heads
-// of 127, bf16: 570 us, 0.9 TB/s; 32, 8 heads of 200, fp32: 1060 us).  A warp takes 32 / HC tokens at a time: its lanes hold the
+// fp32 arithmetic throughout, for rows that no 16-byte copy can take: right for everything, at
+// an eighth of the others' rate (64 sequences of up to 4096 tokens, 8 heads of 127, bf16: 570 us,
+// 0.9 TB/s).  A warp takes 32 / HC tokens at a time: its lanes hold the
 // tokens' rows 32 columns apart, form the partial products with HC query heads, and reduce the
 // 32 sums of (token, head) so that lane i ends with sum i, in 31 shuffles.
 constexpr int kAnyWarps = 8;

@@ -1,5 +1,5 @@
 // nf4_paged_f32.cu -- attention of one query token a sequence over the paged cache in fp32
-// (nf4_paged_attention): rows of whole 16-byte pieces, up to 128 values.
+// (nf4_paged_attention): rows of whole 16-byte pieces.
 //
 // The arithmetic is fp32 on the ordinary cores, 4 D operations a query head and token against
 // 8 D bytes a key head and token: up to a group of some eight heads HBM bounds it, if the rows
@@ -11,8 +11,9 @@
 // Packed fp32 pairs halve the multiply-adds.
 //
 // Measured: 32 sequences of up to 16384 tokens, 32 heads over 8 of 128, 329 us, 6.7 TB/s; 64 of
-// up to 3000, 64 heads over 8 of 64, 112 us, 4.4 TB/s (there the arithmetic bounds it); seven of
-// up to 2000, 12 heads over 4 of 80, 16 us (launches, cut and join).
+// up to 3000, 64 heads over 8 of 64, 112 us, 4.4 TB/s (there the arithmetic bounds it); 32 of up
+// to 4096, 32 over 8 of 200, 179 us, 4.6 TB/s; seven of up to 2000, 12 heads over 4 of 80, 16 us
+// (launches, cut and join).
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -27,12 +28,11 @@
 namespace nf4 {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
 constexpr int kRows = 8;  // tokens of a warp's tile: a lane a token and quarter of its columns
 
 template <int DM, int HC>
 struct Geo {
+  static constexpr int kWarps = DM <= 128 ? 8 : 4, kThreads = kWarps * 32;
   static constexpr int kStages = 2;
   static constexpr int kCtas = DM == 64 ? 2 : 1;  // a SM
   static constexpr int kPitch = DM + 4;           // floats between heads of a warp's sums
@@ -45,12 +45,14 @@ struct Geo {
 };
 
 template <int DM, int HC>
-__global__ void __launch_bounds__(kThreads, Geo<DM, HC>::kCtas) paged_f32_kernel(PagedArgs a, int groups, int log2_wh) {
+__global__ void __launch_bounds__(Geo<DM, HC>::kThreads, Geo<DM, HC>::kCtas) paged_f32_kernel(PagedArgs a, int groups, int log2_wh) {
   using G = Geo<DM, HC>;
   using Copies = TileCopies<float, DM, kRows>;
-  constexpr int HL = HC / 4;          // heads of a quarter's lanes
-  constexpr int PQ = DM / 16;         // 16-byte pieces of a quarter row
-  constexpr int TP = 128 / DM;        // tokens that a warp's read of one piece a lane covers
+  constexpr int kWarps = G::kWarps;
+  constexpr int HL = HC / 4;                    // heads of a quarter's lanes
+  constexpr int PQ = DM / 16;                   // 16-byte pieces of a quarter row
+  constexpr int TP = DM == 64 ? 2 : 1;          // tokens that a warp's read of one piece a lane covers
+  constexpr int PL = DM <= 128 ? 1 : DM / 128;  // pieces of a row that a lane sums
   extern __shared__ __align__(128) unsigned char dyn[];
   float* s_sum = reinterpret_cast<float*>(dyn + G::kRing);          // [kWarps][4][kPitch]
   float* s_q = reinterpret_cast<float*>(dyn + G::kRing + G::kSums); // [kWarps][HC][DM]
@@ -66,7 +68,7 @@ __global__ void __launch_bounds__(kThreads, Geo<DM, HC>::kCtas) paged_f32_kernel
   grid_allow();
   grid_wait();
   const int GQ = a.Hq / a.Hk;
-  Walk load = paged_run(a, a.Hk * groups >> log2_wh, 6 - log2_wh, reinterpret_cast<int64_t*>(s_sum));  // 8 wt tokens a unit
+  Walk load = paged_run(a, a.Hk * groups >> log2_wh, (kWarps == 8 ? 6 : 5) - log2_wh, reinterpret_cast<int64_t*>(s_sum));  // 8 wt tokens a unit
   Walk use = load;
   PagedRec rec{0, 0, 0};
 
@@ -97,11 +99,13 @@ __global__ void __launch_bounds__(kThreads, Geo<DM, HC>::kCtas) paged_f32_kernel
     };
     // lane (t, r): token t = lane % 8; as quarter r = lane / 8 it keeps heads r HL .. r HL + HL - 1
     const int t = lane & 7, r = lane >> 3;
-    float2 acc[HC][2];
+    float2 acc[HC][2 * PL];
     float m[HL], l[HL];
     auto clear_sums = [&]() {
 #pragma unroll
-      for (int h = 0; h < HC; ++h) acc[h][0] = acc[h][1] = make_float2(0.0f, 0.0f);
+      for (int h = 0; h < HC; ++h)
+#pragma unroll
+        for (int i = 0; i < 2 * PL; ++i) acc[h][i] = make_float2(0.0f, 0.0f);
 #pragma unroll
       for (int j = 0; j < HL; ++j) {
         m[j] = -INFINITY;
@@ -174,24 +178,28 @@ __global__ void __launch_bounds__(kThreads, Geo<DM, HC>::kCtas) paged_f32_kernel
           for (int h = 0; h < HC; ++h) {
             const float f = __shfl_sync(0xffffffffu, down[h % HL], h / HL * 8);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) acc[h][i] = mul2(acc[h][i], make_float2(f, f));
+            for (int i = 0; i < 2 * PL; ++i) acc[h][i] = mul2(acc[h][i], make_float2(f, f));
           }
         }
         __syncwarp();
-        const int piece = lane % (DM / 4), sub = lane / (DM / 4);
+        const int piece = TP == 2 ? lane & 15 : lane, sub = TP == 2 ? lane >> 4 : 0;
 #pragma unroll
         for (int i = 0; i < kRows / TP; ++i) {
           const int tok = i * TP + sub;
-          const float4 v = *reinterpret_cast<const float4*>(values + at_chunk<DM * 4>(tok, piece));
+          float4 v[PL];
+#pragma unroll
+          for (int j = 0; j < PL; ++j) v[j] = *reinterpret_cast<const float4*>(values + at_chunk<DM * 4>(tok, piece + 32 * j));
 #pragma unroll
           for (int h = 0; h < HC; h += 4) {
             const float4 p = *reinterpret_cast<const float4*>(s_p + tok * HC + h);
             const float w[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              acc[h + j][0] = fma2(make_float2(w[j], w[j]), make_float2(v.x, v.y), acc[h + j][0]);
-              acc[h + j][1] = fma2(make_float2(w[j], w[j]), make_float2(v.z, v.w), acc[h + j][1]);
-            }
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+              for (int j = 0; j < PL; ++j) {
+                acc[h + k][2 * j] = fma2(make_float2(w[k], w[k]), make_float2(v[j].x, v[j].y), acc[h + k][2 * j]);
+                acc[h + k][2 * j + 1] = fma2(make_float2(w[k], w[k]), make_float2(v[j].z, v[j].w), acc[h + k][2 * j + 1]);
+              }
           }
         }
       }
@@ -236,11 +244,13 @@ __global__ void __launch_bounds__(kThreads, Geo<DM, HC>::kCtas) paged_f32_kernel
       }
 #pragma unroll
       for (int n = 0; n < HC; n += 4) {  // four heads at a time
-        if (lane < DM / 4)
+        if (TP == 1 || lane < 16)
 #pragma unroll
           for (int h = 0; h < 4; ++h)
-            *reinterpret_cast<float4*>(s_sum + (warp * 4 + h) * G::kPitch + lane * 4) =
-                make_float4(acc[n + h][0].x, acc[n + h][0].y, acc[n + h][1].x, acc[n + h][1].y);
+#pragma unroll
+            for (int j = 0; j < PL; ++j)
+              *reinterpret_cast<float4*>(s_sum + (warp * 4 + h) * G::kPitch + (lane + 32 * j) * 4) =
+                  make_float4(acc[n + h][2 * j].x, acc[n + h][2 * j].y, acc[n + h][2 * j + 1].x, acc[n + h][2 * j + 1].y);
         if (wt > 1) __syncthreads();
         else __syncwarp();
         // the warps of a head take its four query heads' columns in turn
@@ -283,12 +293,6 @@ __global__ void __launch_bounds__(kThreads, Geo<DM, HC>::kCtas) paged_f32_kernel
   if (threadIdx.x == 0) a.rec[blockIdx.x] = rec;
 }
 
-inline int log2_of(int n) {
-  int l = 0;
-  while (n >> (l + 1)) ++l;
-  return l;
-}
-
 template <int DM, int HC>
 cudaError_t launch(const PagedArgs& a, int sms, cudaStream_t s) {
   using G = Geo<DM, HC>;
@@ -298,19 +302,22 @@ cudaError_t launch(const PagedArgs& a, int sms, cudaStream_t s) {
   if (cudaError_t e = limit.allow(kern, G::kSmem)) return e;
   const PagedShape p = paged_shape_f32(a.Hq / a.Hk, a.Hk, a.D, a.k_head < a.k_token);
   const int ctas = p.ctas * sms;
-  if (cudaError_t e = launch_early(kern, dim3(static_cast<unsigned>(ctas)), kThreads, G::kSmem, s, a, p.groups, log2_of(p.wh))) return e;
+  if (cudaError_t e = launch_early(kern, dim3(static_cast<unsigned>(ctas)), G::kThreads, G::kSmem, s, a, p.groups, log2_of(p.wh))) return e;
   return launch_paged_join<float>(a, ctas, HC, p.groups, p.wh, s);
 }
 
 }  // namespace
 
-PagedShape paged_shape_f32(int G, int Hk, int D, bool together) { return paged_shape(G, Hk, G > 4 ? 8 : 4, kWarps, D <= 64 ? 2 : 1, together); }
+PagedShape paged_shape_f32(int G, int Hk, int D, bool together) {
+  return paged_shape(G, Hk, G > 4 ? 8 : 4, D <= 128 ? 8 : 4, D <= 64 ? 2 : 1, together);
+}
 
-// D a multiple of 4 up to 128, all rows 16-byte aligned.
+// D a multiple of 4, all rows 16-byte aligned.
 cudaError_t launch_paged_f32(const PagedArgs& a, int sms, cudaStream_t s) {
   const bool wide = a.Hq / a.Hk > 4;
   if (a.D <= 64) return wide ? launch<64, 8>(a, sms, s) : launch<64, 4>(a, sms, s);
-  return wide ? launch<128, 8>(a, sms, s) : launch<128, 4>(a, sms, s);
+  if (a.D <= 128) return wide ? launch<128, 8>(a, sms, s) : launch<128, 4>(a, sms, s);
+  return wide ? launch<256, 8>(a, sms, s) : launch<256, 4>(a, sms, s);
 }
 
 }  // namespace nf4

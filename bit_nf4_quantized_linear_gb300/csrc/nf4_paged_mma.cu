@@ -366,12 +366,6 @@ __global__ void __launch_bounds__(kThreads, CTAS) paged_mma_kernel(PagedArgs a, 
   if (threadIdx.x == 0) a.rec[blockIdx.x] = rec;
 }
 
-inline int log2_of(int n) {
-  int l = 0;
-  while (n >> (l + 1)) ++l;
-  return l;
-}
-
 template <bool F16, int DM, int NT, int CTAS>
 cudaError_t launch(const PagedArgs& a, const PagedShape& p, int sms, cudaStream_t s) {
   using G = Geo<DM>;

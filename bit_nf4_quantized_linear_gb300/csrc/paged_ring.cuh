@@ -29,10 +29,13 @@ __device__ __forceinline__ void copies_wait() {
 
 // The copies of a tile of ROWS tokens, keys and then values, rows of W values; columns past D
 // and rows past a length or without a page are zeros that nothing reads.  Lane i copies column
-// piece i % kPieces of rows i / kPieces and every kPer-th after it.
+// piece i % kPieces (and the 32nd after it, of rows that long) of rows i / kPieces and every
+// kPer-th after it.
 template <typename T, int W, int ROWS>
 struct TileCopies {
-  static constexpr int kRowBytes = W * static_cast<int>(sizeof(T)), kPieces = kRowBytes / 16, kPer = 32 / kPieces;
+  static constexpr int kRowBytes = W * static_cast<int>(sizeof(T)), kAll = kRowBytes / 16;
+  static constexpr int kPieces = kAll < 32 ? kAll : 32, kPer = 32 / kPieces, kTurns = kAll / kPieces;  // turns of a warp a row
+  static constexpr int kTurn = 512 / static_cast<int>(sizeof(T));  // columns between turns
   static constexpr int kHalf = ROWS * kRowBytes, kStage = 2 * kHalf;
   static_assert(kPieces >= 1 && kPer >= 1 && ROWS % 8 == 0 && ROWS <= 16, "a row a warp's copy at least");
 
@@ -84,7 +87,7 @@ struct TileCopies {
           ks = kPer * a.k_token;
           vs = kPer * a.v_token;
         }
-        if (n >= ROWS) {
+        if (n >= ROWS && kTurns == 1) {
           const int bytes = in ? 16 : 0;
 #pragma unroll
           for (int i = 0; i < ROWS / kPer; ++i) {
@@ -96,9 +99,12 @@ struct TileCopies {
         } else {
 #pragma unroll
           for (int i = 0; i < ROWS / kPer; ++i) {
-            const bool row = in && i * kPer + row0 < n;
-            copy16(dst(i), row ? kp : none, row ? 16 : 0);
-            copy16(dst(i) + kHalf, row ? vp : none, row ? 16 : 0);
+#pragma unroll
+            for (int t = 0; t < kTurns; ++t) {
+              const bool row = col + t * kTurn < a.D && i * kPer + row0 < n;
+              copy16(dst(i) + t * 512, row ? kp + t * kTurn : none, row ? 16 : 0);
+              copy16(dst(i) + kHalf + t * 512, row ? vp + t * kTurn : none, row ? 16 : 0);
+            }
             kp += ks;
             vp += vs;
           }
@@ -121,9 +127,12 @@ struct TileCopies {
         for (int i = 0; i < ROWS / kPer; ++i) {
           const int r = i * kPer + row0;
           const int64_t ak = __shfl_sync(0xffffffffu, at, r), av = __shfl_sync(0xffffffffu, at, r + 16);
-          const int bytes = (valid >> r & 1) && in ? 16 : 0;
-          copy16(dst(i), bytes ? static_cast<const T*>(a.k) + ak + col : none, bytes);
-          copy16(dst(i) + kHalf, bytes ? static_cast<const T*>(a.v) + av + col : none, bytes);
+#pragma unroll
+          for (int t = 0; t < kTurns; ++t) {
+            const int c = col + t * kTurn, bytes = (valid >> r & 1) && c < a.D ? 16 : 0;
+            copy16(dst(i) + t * 512, bytes ? static_cast<const T*>(a.k) + ak + c : none, bytes);
+            copy16(dst(i) + kHalf + t * 512, bytes ? static_cast<const T*>(a.v) + av + c : none, bytes);
+          }
         }
       }
       if (lane == 0) s_valid[st] = valid;

@@ -516,8 +516,8 @@ nf4_status nf4_adamw_state_values(const uint8_t* m, const uint8_t* v, const floa
  * Hq a multiple of Hk, 1 <= D <= 256.  fp32 sums and statistics; partial results over the
  * length are added in a fixed order (deterministic for given lengths and device).  16-bit
  * types with D a multiple of 8, 16-byte aligned pointers and strides of a multiple of 8
- * elements run on the tensor cores, everything else in fp32 arithmetic (quickest for fp32 with
- * D a multiple of 4 up to 128, 16-byte aligned). */
+ * elements run on the tensor cores, everything else in fp32 arithmetic (fp32 with D a multiple
+ * of 4 and 16-byte aligned rows streams its rows as those do; the rest is slower). */
 typedef struct {
   void* k;
   void* v;

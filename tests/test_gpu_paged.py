@@ -109,7 +109,7 @@ def test_attention_pages(page, order):
 
 
 @pytest.mark.parametrize("Hq,Hk", [(1, 1), (4, 4), (8, 2), (5, 1), (16, 2), (9, 1), (20, 1)])
-@pytest.mark.parametrize("D", [4, 20, 64, 68, 128])
+@pytest.mark.parametrize("D", [4, 20, 64, 68, 128, 132, 200, 256])
 def test_attention_fp32_heads(Hq, Hk, D):
     """Groups of one to twenty heads, widths that fill a row of the ring and do not; rows that no 16-byte copy can take."""
     lens = [331, 7, 64, 0, 1500]
