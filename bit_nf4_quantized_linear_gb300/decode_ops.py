@@ -109,8 +109,8 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     over the lengths[i] tokens that page_table names for it (pages and table as in paged_append; the new token's own
     keys and values are appended first).  Query head h reads key head h // (Hq // Hk); `scale` defaults to D ** -0.5.
     Returns (o [sequences, Hq, D], lse fp32 [sequences, Hq]); a sequence of length 0 gives zeros and -inf.  `out` takes o in
-    place of a new tensor: any strides whose rows do not share storage.  Tables and lengths are read on the device, so a
-    captured graph follows them.  No gradients."""
+    place of a new tensor (q itself will do): any strides whose rows do not share storage.  Tables and lengths are read on
+    the device, so a captured graph follows them.  No gradients."""
     name = "paged_attention"
     d, dev, n, Hk, D = _cache(name, k_pages, v_pages, page_table, lengths, (("q", q, None),) if out is None else (("q", q, None), ("out", out, None)))
     Hq = q.shape[1]

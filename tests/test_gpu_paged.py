@@ -309,8 +309,21 @@ def test_rows_without_a_weight_are_zero(dtype, D):
     o2, lse2 = nf4.paged_attention(q, kp, vp, table[:, :0], lengths)
     assert nf4.device_status(clear=True) == BAD_OFFSETS
     assert (o2 == 0).all() and (lse2 == -math.inf).all()
+    o2, lse2 = nf4.paged_attention(q, kp[:0], vp[:0], table, lengths)
+    nf4.paged_append(kp[0, :3], vp[0, :3], kp[:0], vp[:0], table, lengths)
+    assert nf4.device_status(clear=True) == BAD_OFFSETS
+    assert (o2 == 0).all() and (lse2 == -math.inf).all()
     o2, lse2 = nf4.paged_attention(q[:0], kp, vp, table[:0], lengths[:0])
     assert o2.shape == (0, 4, D) and lse2.shape == (0, 4)
+
+
+def test_out_may_be_the_queries():
+    kp, vp, table, lengths = cache([300, 17, 0, 64], 2, 64, BF16)
+    q = queries(4, 8, 64, BF16)
+    o, lse = nf4.paged_attention(q, kp, vp, table, lengths)
+    version = q._version
+    o2, lse2 = nf4.paged_attention(q, kp, vp, table, lengths, out=q)
+    assert o2 is q and q._version > version and torch.equal(o, q) and torch.equal(lse, lse2)
 
 
 def test_decoding_under_inference_mode():

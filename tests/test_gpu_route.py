@@ -116,6 +116,12 @@ def test_route_groups(E, groups, top_groups, k, group_top, score):
 def test_route_large_batch():
     x = gen(0)(20011, 64)
     check(x, 8, grads=True, score="sigmoid", bias=0.1 * gen(1)(64), renormalise=True)
+    # more tokens than fit the counts' bytes, none of them, or all, with one expert
+    x = gen(2)(40001, 48)
+    x[:, 7] += 20
+    x[:, 9] -= 20
+    r = check(x, 2, grads=False)
+    assert r.offsets[8] - r.offsets[7] == 40001 and r.offsets[10] == r.offsets[9]
 
 
 @pytest.mark.parametrize("biased", [False, True])
