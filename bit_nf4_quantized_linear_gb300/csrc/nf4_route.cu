@@ -358,7 +358,7 @@ __device__ __forceinline__ int route_token(const RouteArgs& a, int64_t t, double
         const int e = i * 32 + lane;
         const float s = a.sigmoid ? rcp_fast(1.0f + ex2_fast(-c[i] * kLog2e)) : ex2_fast((c[i] - top) * kLog2e) * norm;
         if (c[i] > -INFINITY) c[i] = s + (a.bias ? a.bias[e] : 0.0f);
-        if (c[i] > -INFINITY) cmax = fmaxf(cmax, fabsf(c[i]));
+        if (fabsf(c[i]) < INFINITY) cmax = fmaxf(cmax, fabsf(c[i]));  // an infinite bias is exact
         nan |= c[i] != c[i];
       }
       unsure = __any_sync(kAll, nan);

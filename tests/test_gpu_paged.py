@@ -317,9 +317,10 @@ def test_rows_without_a_weight_are_zero(dtype, D):
     assert o2.shape == (0, 4, D) and lse2.shape == (0, 4)
 
 
-def test_out_may_be_the_queries():
-    kp, vp, table, lengths = cache([300, 17, 0, 64], 2, 64, BF16)
-    q = queries(4, 8, 64, BF16)
+@pytest.mark.parametrize("dtype,D", [(BF16, 64), (F16, 128), (F32, 64), (F16, 31)])
+def test_out_may_be_the_queries(dtype, D):
+    kp, vp, table, lengths = cache([300, 17, 0, 64, 5000], 2, D, dtype)
+    q = queries(5, 24, D, dtype)
     o, lse = nf4.paged_attention(q, kp, vp, table, lengths)
     version = q._version
     o2, lse2 = nf4.paged_attention(q, kp, vp, table, lengths, out=q)

@@ -202,6 +202,29 @@ def test_route_nan_rows_stay_in_range():
     assert 5 in r.experts[3].tolist() and 7 in r.experts[5].tolist()
 
 
+@pytest.mark.parametrize("E", [24, 200, 512])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_extreme_biases(score, E):
+    """Experts of an infinite bias come first, or last but for those of logit -inf; equal ones by the lower index."""
+    x = gen(11)(120, E)
+    x[torch.rand(120, E, device=DEV) < 0.2] = -math.inf
+    some = torch.randperm(E, device=DEV)
+    for high in (1, 4, 6, 12, E):
+        for value in (math.inf, 3e38, 1e30):
+            bias = gen(E + high)(E)
+            bias[some[:high]] = value
+            bias[some[-3:]] = -value
+            for kw in ({}, dict(groups=4, top_groups=2), dict(groups=8, top_groups=3)):
+                check(x, 5, score=score, bias=bias, grads=False, **kw)
+            if value != 3e38:  # twice that is no fp32 number
+                check(x, 5, score=score, bias=bias, groups=4, top_groups=2, group_top=2, grads=False)
+    bias = gen(12)(E)
+    bias[3] = math.nan
+    for kw in ({}, dict(groups=4, top_groups=2, group_top=2)):
+        r = nf4.route_experts(x, 5, score=score, bias=bias, **kw)
+        assert ((r.experts >= 0) & (r.experts < E)).all() and (r.experts[:, 1:] > r.experts[:, :-1]).all()
+
+
 def test_route_extreme_logits():
     """Sigmoid scores that leave fp32's range, and softmax rows with one giant: weights stay those of the definition."""
     x = torch.linspace(-300, 60, 37 * 20, device=DEV).view(20, 37)
