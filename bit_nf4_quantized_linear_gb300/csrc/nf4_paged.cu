@@ -21,7 +21,8 @@ constexpr int kAppendThreads = 256;
 
 // The place of new row r: its page and slot, or page -1 for none.  Row r of sequence i, the
 // last with cu[i] <= r, goes to position lengths[i] - cu[i + 1] + r; without cu_seqlens row r
-// is the newest token of sequence r.
+// is the newest token of sequence r.  The length is taken as it is given: a position that the
+// table's row cannot name has no page, and no other token makes room for it.
 __device__ __forceinline__ int append_place(const PagedArgs& a, int64_t r, int* slot) {
   int64_t seq = r, end = r + 1;
   if (a.cu_seqlens) {
@@ -34,10 +35,9 @@ __device__ __forceinline__ int append_place(const PagedArgs& a, int64_t r, int* 
     seq = lo;
     end = a.cu_seqlens[lo + 1];
   }
-  const int len = paged_len(a, seq);
+  const int64_t len = a.lengths[seq], pos = len - end + r;
   if (len == 0) return -1;  // an idle sequence
-  const int64_t pos = len - end + r;
-  if (pos < 0 || pos >= len) {
+  if (pos < 0 || pos >= len || pos >= static_cast<int64_t>(a.max_pages) * a.page_size) {
     if (a.status) atomicCAS(a.status, 0, kStatusBadOffsets);
     return -1;
   }

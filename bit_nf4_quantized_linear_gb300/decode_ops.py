@@ -81,7 +81,7 @@ def paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
     page_table[i, t // slots], slot t % slots.  `lengths` int32 [sequences] counts the new tokens already: rows
     cu_seqlens[i] .. cu_seqlens[i + 1] - 1 are the last tokens of sequence i (a prompt or a chunk of one); without
     cu_seqlens row i is the newest token of sequence i.  Rows of sequences of length 0, and rows whose page is missing
-    from the table (recorded in the device status), are not written."""
+    from the table or lies past its last column (recorded in the device status), are not written."""
     name = "paged_append"
     Hk = k_pages.shape[2] if k_pages.dim() == 4 else -1
     d, dev, n, _, _ = _cache(name, k_pages, v_pages, page_table, lengths, (("k", k, Hk), ("v", v, Hk)))

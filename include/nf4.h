@@ -493,17 +493,19 @@ nf4_status nf4_adamw_state_values(const uint8_t* m, const uint8_t* v, const floa
  *               Entries past a sequence's last page are not read.
  *   lengths     DEVICE int32 [nseq], tokens of each sequence in the cache, the new ones
  *               among them; 0 for an idle row of the batch.
- * A length outside [0, max_pages * page_size] is clamped, a page outside [0, pages) is passed
- * over (its tokens are not written, and have no weight); both are recorded as
- * NF4_ERR_BAD_OFFSETS in the device status word.  Everything is read on the device when the
- * kernels run, so a captured graph follows the tables and lengths of its replays.
+ * Tokens past max_pages * page_size (of a longer length) and those whose page lies outside
+ * [0, pages) have no slot: they are not written, and have no weight; a negative length is that
+ * of an idle row.  All are recorded as NF4_ERR_BAD_OFFSETS in the device status word.
+ * Everything is read on the device when the kernels run, so a captured graph follows the tables
+ * and lengths of its replays.
  *
  * nf4_paged_append: rows cu_seqlens[i] .. cu_seqlens[i + 1] - 1 of k, v [T, Hk, D] (token and
  * head strides) are the LAST tokens of sequence i: row r goes to position lengths[i] -
  * cu_seqlens[i + 1] + r.  cu_seqlens DEVICE int32 [nseq + 1] ascending, or NULL: row i is the
  * newest token of sequence i (T == nseq).  Rows of idle sequences and outside the offsets are
- * not written; rows before a sequence's first token (more new rows than its length) are
- * neither, and are recorded.  Nothing but the named slots is written; two rows must not share one.
+ * not written; rows before a sequence's first token (more new rows than its length) and past
+ * its table's last page are neither, and are recorded.  Nothing but the named slots is written;
+ * two rows must not share one.
  *
  * nf4_paged_attention: o_i = sum_t p_t v_t with p = softmax(scale q_i . k_t) over the
  * lengths[i] tokens of sequence i; query head h reads key head h / (Hq / Hk).

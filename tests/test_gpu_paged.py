@@ -504,3 +504,27 @@ def test_append_then_attend_equals_the_attention_of_a_prompt():
         o, _ = nf4.paged_attention(q[t:t + 1], kp, vp, table, lengths)
         # each side is one rounding of the result and of the weights from it
         assert ((o[0].double() - want[t].double()).abs() <= 2 * 2.0 ** -8 * want[t].double().abs() + 2.0 ** -8 * v[:t + 1].abs().amax().double()).all()
+
+
+@pytest.mark.parametrize("dtype,D,order", [(BF16, 64, "token"), (F16, 72, "head"), (F32, 3, "token")])
+def test_append_past_the_table_overwrites_nothing(dtype, D, order):
+    """A length of more tokens than the table's row names: a row whose position has no page is not written, the others go
+    to their own positions, and no older token is lost.  A negative length has no new rows."""
+    kp, vp, table, _ = cache([32, 32, 32, 32], 2, D, dtype, order=order, extra_pages=0)  # two pages of 16 a sequence, all in use
+    for new, lens in ((None, [33, 20, 2 ** 31 - 1, 32]), ([6, 1, 0, 32], [35, 33, 40, 32]), ([3, 40, 5, 2], [-1, 50, 32, -2 ** 31]),
+                      ([1, 1, 1, 1], [32, 33, 1, 48])):
+        cu = [sum(new[:i]) for i in range(5)] if new else None
+        k, v = (queries(cu[-1] if new else 4, 2, D, dtype, s) for s in (5, 6))
+        wk, wv = kp.clone(), vp.clone()
+        for i, m in enumerate(lens):
+            rows = list(range(cu[i], cu[i + 1])) if new else [i]
+            for j, r in enumerate(rows):
+                pos = m - len(rows) + j
+                if 0 <= pos < 32:
+                    page = table[i, pos // 16]
+                    wk[page, pos % 16], wv[page, pos % 16] = k[r], v[r]
+        gk, gv = kp.clone(), vp.clone()
+        nf4.paged_append(k, v, gk, gv, table, torch.tensor(lens, dtype=torch.int32, device=DEV),
+                         None if cu is None else torch.tensor(cu, dtype=torch.int32, device=DEV))
+        assert nf4.device_status(clear=True) == BAD_OFFSETS
+        assert torch.equal(gk, wk) and torch.equal(gv, wv), lens
