@@ -87,7 +87,8 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
 
 // Weights a and b as two values each of the operands' type: what the type holds of them (cut,
 // not rounded), and the rest, never negative and never 0 beside a first part, so that an
-// infinite value times the weight is that infinity and not 0 x inf.
+// infinite value times the weight is that infinity and not 0 x inf.  Both parts of a weight of 0
+// are 0: its token adds nothing, however large its finite value.
 template <bool F16>
 __device__ __forceinline__ void split2(float a, float b, uint32_t* hi, uint32_t* lo) {
   if constexpr (F16) {
@@ -101,7 +102,8 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t* hi, uint32_t*
     constexpr float least = 1.1754944e-38f;
     const uint32_t ua = __float_as_uint(a) & 0xffff0000u, ub = __float_as_uint(b) & 0xffff0000u;
     *hi = ua >> 16 | ub;
-    const __nv_bfloat162 l = __floats2bfloat162_rn(fmaxf(a - __uint_as_float(ua), least), fmaxf(b - __uint_as_float(ub), least));
+    const float ra = a - __uint_as_float(ua), rb = b - __uint_as_float(ub);
+    const __nv_bfloat162 l = __floats2bfloat162_rn(ua ? fmaxf(ra, least) : ra, ub ? fmaxf(rb, least) : rb);
     *lo = *reinterpret_cast<const uint32_t*>(&l);
   }
 }

@@ -528,3 +528,23 @@ def test_append_past_the_table_overwrites_nothing(dtype, D, order):
                          None if cu is None else torch.tensor(cu, dtype=torch.int32, device=DEV))
         assert nf4.device_status(clear=True) == BAD_OFFSETS
         assert torch.equal(gk, wk) and torch.equal(gv, wv), lens
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+def test_attention_values_without_a_weight_count_nothing(dtype):
+    """Tokens of score -inf: the largest finite values there add nothing to the answer of the others."""
+    D = 64
+    kp, vp, table, lengths = cache([200], 1, D, dtype, seed=5)
+    q = queries(1, 4, D, dtype).abs() + 0.1
+    dead = torch.zeros(200, dtype=torch.bool, device=DEV)
+    dead[:70] = dead[130:150] = True
+    page, slot = ref.slots_of(table[0], 200, 16)
+    kp[page[dead], slot[dead], 0] = -math.inf
+    vp[page[dead], slot[dead], 0] = torch.finfo(dtype).max
+    o, lse = nf4.paged_attention(q, kp, vp, table, lengths)
+    live = (~dead).nonzero().flatten()
+    one = torch.zeros(1, 1, dtype=torch.int32, device=DEV)
+    want, wl, mag, smag = ref.paged_attention(q, kp[page[live], slot[live]][None], vp[page[live], slot[live]][None], one, [live.numel()],
+                                              D ** -0.5)
+    bo, bl = ref.paged_bounds(want, wl, mag, smag, [200], D, dtype)
+    assert ((o.double() - want).abs() <= bo).all() and ((lse.double() - wl).abs() <= bl).all()
