@@ -192,11 +192,12 @@ __global__ void __launch_bounds__(kAnyWarps * 32) paged_any_kernel(PagedArgs a, 
       }
       m = top;
       l = l * down + p;
+      const float pv = p * PagedSums<T>::kDown;
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int h = 0; h < HC; ++h) {
-          const float w = __shfl_sync(0xffffffffu, p, j * HC + h);
+          const float w = __shfl_sync(0xffffffffu, pv, j * HC + h);
 #pragma unroll
           for (int i = 0; i < DV; ++i) acc[h][i] = fmaf(w, vr[j][i], acc[h][i]);
         }
@@ -250,7 +251,7 @@ __global__ void __launch_bounds__(kAnyWarps * 32) paged_any_kernel(PagedArgs a, 
 #pragma unroll
           for (int i = 0; i < DV; ++i)
             if (lane + 32 * i < a.D) {
-              if (whole) o[lane + 32 * i] = from_f32<T>(paged_mean(acc[h][i], lh));
+              if (whole) o[lane + 32 * i] = from_f32<T>(paged_mean<T>(acc[h][i], lh));
               else part[h * st + lane + 32 * i] = acc[h][i];
             }
           if (lane == 0) {

@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(Geo<DM, HC>::kThreads, Geo<DM, HC>::kCtas) pag
           m[j] = top;
           const float p = exp2_fast(s[j] - mm);
           l[j] = l[j] * down[j] + p;
-          s_p[t * HC + r * HL + j] = p;
+          s_p[t * HC + r * HL + j] = p * PagedSums<float>::kDown;
         }
         if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(Geo<DM, HC>::kThreads, Geo<DM, HC>::kCtas) pag
           }
           const int64_t hq = static_cast<int64_t>(hk) * GQ + g0 + hn;
           if (d < a.D) {
-            if (whole) static_cast<float*>(a.o)[seq * a.o_s + hq * a.o_h + d] = paged_mean(v, sum);
+            if (whole) static_cast<float*>(a.o)[seq * a.o_s + hq * a.o_h + d] = paged_mean<float>(v, sum);
             else part[hn * stride + d] = v;
           }
           if (d == 0) {

@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) paged_mma_kernel(PagedArgs a, 
           l[n][1] += x[n][1] + x[n][3];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            split2<F16>(x[n][2 * j], x[n][2 * j + 1], &hi[n][j], &lo[n][j]);
+            split2<F16>(x[n][2 * j] * PagedSums<T>::kDown, x[n][2 * j + 1] * PagedSums<T>::kDown, &hi[n][j], &lo[n][j]);
             hi[n][j] = transpose8(hi[n][j]);
             lo[n][j] = transpose8(lo[n][j]);
           }
@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) paged_mma_kernel(PagedArgs a, 
             const int64_t hq = static_cast<int64_t>(hk) * GQ + g0 + hn;
             if (d < a.D) {  // D is a multiple of 8
               if (whole) {
-                const float inv = paged_mean(1.0f, sum);
+                const float inv = paged_mean<T>(1.0f, sum);
                 __align__(8) T r[4] = {from_f32<T>(v.x * inv), from_f32<T>(v.y * inv), from_f32<T>(v.z * inv), from_f32<T>(v.w * inv)};
                 *reinterpret_cast<uint2*>(static_cast<T*>(a.o) + seq * a.o_s + hq * a.o_h + d) = *reinterpret_cast<const uint2*>(r);
               } else {

@@ -13,9 +13,11 @@
 // run.
 #pragma once
 
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "early_launch.cuh"
 #include "elem.cuh"
@@ -174,8 +176,19 @@ __device__ __forceinline__ float exp2_fast(float x) {  // relative error 2^-22
   return r;
 }
 
-// A weighted mean; 0 where no token has a weight (all scores -inf, or no page in the table).
-__device__ __forceinline__ float paged_mean(float v, float sum) { return sum == 0.0f ? 0.0f : v / sum; }
+// Types of fp32's range: the sums of weighted values are formed of weights times 2^-20, so that a
+// million tokens of the largest finite value do not overflow before they are divided (2^-20 is
+// exact, but for sums near the bottom of that range).  fp16's values cannot get there.
+template <typename T>
+struct PagedSums {
+  static constexpr bool kHalf = sizeof(T) == 2 && !std::is_same<T, __nv_bfloat16>::value;
+  static constexpr float kDown = kHalf ? 1.0f : 0x1p-20f, kUp = kHalf ? 1.0f : 0x1p20f;
+};
+
+// A weighted mean from such a sum and the sum of the weights themselves; 0 where no token has a
+// weight (all scores -inf, or no page in the table).
+template <typename T>
+__device__ __forceinline__ float paged_mean(float v, float sum) { return sum == 0.0f ? 0.0f : v / sum * PagedSums<T>::kUp; }
 
 // Sequences of no tokens: zeros, and -inf for the logarithm of their sum.
 template <typename T>
@@ -307,7 +320,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(PagedArgs a
     if constexpr (!WIDE) {
 #pragma unroll
       for (int j = 0; j < DV; ++j)
-        if (lane + 32 * j < a.D) o[lane + 32 * j] = from_f32<T>(paged_mean(acc[j], l));
+        if (lane + 32 * j < a.D) o[lane + 32 * j] = from_f32<T>(paged_mean<T>(acc[j], l));
       if (lane == 0 && a.lse) a.lse[me.seq * a.Hq + hq] = m * kLn2 + logf(l);
     } else {
 #pragma unroll
@@ -328,7 +341,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(PagedArgs a
           sum += s_ml[w][1] * f;
           v += s_acc[w][d] * f;
         }
-        o[d] = from_f32<T>(paged_mean(v, sum));
+        o[d] = from_f32<T>(paged_mean<T>(v, sum));
         if (d == 0 && a.lse) a.lse[me.seq * a.Hq + hq] = top * kLn2 + logf(sum);
       }
     }

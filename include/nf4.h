@@ -515,7 +515,8 @@ nf4_status nf4_adamw_state_values(const uint8_t* m, const uint8_t* v, const floa
  *   sequence's length are never read.
  *   ws: nf4_workspace_size(NF4_OP_PAGED_ATTENTION, 0, Hq, D, Hk) bytes, 16-byte aligned, of a
  *   call's own (calls on two streams, or two graphs whose replays overlap, must not share it).
- * Hq a multiple of Hk, 1 <= D <= 256.  fp32 sums and statistics; partial results over the
+ * Hq a multiple of Hk, 1 <= D <= 256.  fp32 sums and statistics (the sums of up to 2^20 tokens
+ * of any finite values stay in range); partial results over the
  * length are added in a fixed order (deterministic for given lengths and device).  16-bit
  * types with D a multiple of 8, 16-byte aligned pointers and strides of a multiple of 8
  * elements run on the tensor cores, everything else in fp32 arithmetic (fp32 with D a multiple

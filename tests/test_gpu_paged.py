@@ -548,3 +548,18 @@ def test_attention_values_without_a_weight_count_nothing(dtype):
                                               D ** -0.5)
     bo, bl = ref.paged_bounds(want, wl, mag, smag, [200], D, dtype)
     assert ((o.double() - want).abs() <= bo).all() and ((lse.double() - wl).abs() <= bl).all()
+
+
+@pytest.mark.parametrize("dtype,D", [(BF16, 64), (BF16, 128), (F16, 64), (F32, 64), (BF16, 37), (F32, 37)])
+def test_attention_sums_of_the_largest_values(dtype, D):
+    """Values near the type's largest, of which a few add up past fp32's range: their mean is a number.  And such values at
+    tokens that lose all their weight to later ones."""
+    kp, vp, table, lengths = cache([200, 3, 0, 3000], 2, D, dtype, seed=D)
+    q = queries(4, 8, D, dtype)
+    big = 0.9 * torch.finfo(dtype).max
+    check(q, kp, torch.full_like(vp, big), table, lengths)
+    check(0 * q, kp, torch.full_like(vp, -big), table, lengths)
+    check(q, kp, (vp.sign() * big).to(dtype), table, lengths)
+    page, slot = (torch.cat(t) for t in zip(*(ref.slots_of(table[i], 70, 16) for i in (0, 3))))
+    kp[page, slot], vp[page, slot] = -3e4, big
+    check(q.abs() + 0.1, kp, vp, table, lengths)
