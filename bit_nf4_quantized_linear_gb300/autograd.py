@@ -202,7 +202,8 @@ class NF4DispatchFn(torch.autograd.Function):
 
 def nf4_dispatch(x: torch.Tensor, token_rows: torch.Tensor) -> torch.Tensor:
     """The rows of the grouped experts from the tokens' activations (bf16 [tokens, H] -> [tokens * k, H]): row
-    token_rows[t, j] is token t (-1: no row; rows that no route names are zero).  See nf4_route."""
+    token_rows[t, j] is token t (-1: no row; rows that no route names are zero), token_rows int32 [tokens, k] as nf4_route
+    and route_rows give it.  See nf4_route."""
     return NF4DispatchFn.apply(x, token_rows)
 
 

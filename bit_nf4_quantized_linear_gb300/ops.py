@@ -242,13 +242,22 @@ def route_rows(row_token: torch.Tensor, tokens: int, k: int) -> torch.Tensor:
     return order.to(torch.int32).reshape(tokens, k).contiguous()
 
 
+def _check_token_rows(name: str, token_rows: torch.Tensor, like: torch.Tensor, tokens: Optional[int] = None):
+    """The route table beside its activations, which the kernels read as packed int32 rows."""
+    if token_rows.dtype != torch.int32 or token_rows.dim() != 2 or not token_rows.is_contiguous():
+        raise ValueError(f"{name}: token_rows must be a contiguous int32 [tokens, k] tensor")
+    if token_rows.device != like.device:
+        raise ValueError(f"{name}: token_rows on {token_rows.device}, the activations on {like.device}")
+    if tokens is not None and token_rows.shape[0] != tokens:
+        raise ValueError(f"{name}: token_rows of {token_rows.shape[0]} tokens for {tokens} rows of activations")
+
+
 def moe_combine(rows: torch.Tensor, token_rows: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """nf4_moe_combine: out[t] = sum over j of rows[token_rows[t, j]] (bf16 [R, H] ->
     [tokens, H]; fp32 sum in route order, rounded once)."""
     _check_act("moe_combine", rows, rows.shape[1] if rows.dim() == 2 else -1)
     _need_cuda("moe_combine", token_rows)
-    if token_rows.dtype != torch.int32 or token_rows.dim() != 2 or not token_rows.is_contiguous():
-        raise ValueError("moe_combine: token_rows must be a contiguous int32 [tokens, k] tensor")
+    _check_token_rows("moe_combine", token_rows, rows)
     tokens, k = token_rows.shape
     R, H = rows.shape
     y = torch.empty(tokens, H, dtype=torch.bfloat16, device=rows.device) if out is None else out
@@ -261,10 +270,11 @@ def moe_combine(rows: torch.Tensor, token_rows: torch.Tensor, out: Optional[torc
 def moe_combine_bwd(grad_out: torch.Tensor, token_rows: torch.Tensor, R: int,
                     out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """nf4_moe_combine_bwd: each routed row receives its token's gradient (bf16
-    [tokens, H] -> [R, H]).  Rows no route names are zero in a new tensor, and left
-    as they are in a given `out`."""
+    [tokens, H] -> [R, H], token_rows of as many tokens).  Rows no route names are zero in
+    a new tensor, and left as they are in a given `out`."""
     _check_act("moe_combine_bwd", grad_out, grad_out.shape[1] if grad_out.dim() == 2 else -1)
     _need_cuda("moe_combine_bwd", token_rows)
+    _check_token_rows("moe_combine_bwd", token_rows, grad_out, grad_out.shape[0])
     tokens, k = token_rows.shape
     H = grad_out.shape[1]
     g = torch.zeros(R, H, dtype=torch.bfloat16, device=grad_out.device) if out is None else out

@@ -129,3 +129,19 @@ def test_slots_that_share_storage_are_recognised():
                 for c in range(0, 9):
                     at = [i * a + j * b + h * c + d for i in range(shape[0]) for j in range(shape[1]) for h in range(shape[2]) for d in range(shape[3])]
                     assert share(shape, (a, b, c, 1)) or len(set(at)) == len(at), (shape, a, b, c)
+
+
+def test_route_tables_that_do_not_fit_the_activations_are_refused():
+    """What the dispatch and the combine would read past their inputs or as other types, before any pointer is taken."""
+    from bit_nf4_quantized_linear_gb300 import ops
+    x, t = torch.zeros(5, 64, dtype=torch.bfloat16), torch.zeros(5, 2, dtype=torch.int32)
+    ops._check_token_rows("op", t, x, 5)
+    ops._check_token_rows("op", t, x)
+    for bad in (t.long(), t.float(), t[:, 0], t[None], t.T.contiguous().T, torch.zeros(5, 4, dtype=torch.int32)[:, ::2]):
+        with pytest.raises(ValueError, match="op: token_rows must be"):
+            ops._check_token_rows("op", bad, x)
+    for tokens in (0, 4, 6):
+        with pytest.raises(ValueError, match="op: token_rows of 5 tokens"):
+            ops._check_token_rows("op", t, x, tokens)
+    with pytest.raises(ValueError, match="op: token_rows on meta"):
+        ops._check_token_rows("op", t.to("meta"), x)

@@ -186,3 +186,21 @@ def test_decoding_steps_of_a_block():
             near(y[i], want, f"step {s}, sequence {i}", 4)
         assert torch.equal(r.experts[1], torch.full_like(r.experts[1], -1)) and torch.isfinite(y).all()
     assert lengths.tolist() == lens
+
+
+def test_dispatch_refuses_tables_that_do_not_fit():
+    """Fewer or more tokens than the table, another type, layout or device: refused before anything is launched."""
+    x = gen(8)(6, 64).to(BF16)
+    t = nf4.route_experts(gen(9)(6, 8), 2).token_rows
+    before = nf4.path_counters()["total"]
+    for f in (lambda x, t: nf4.nf4_dispatch(x, t), lambda x, t: nf4.moe_combine_bwd(x, t, t.numel())):
+        for bad, message in ((x[:5], "6 tokens for 5 rows"), (x[:0], "6 tokens for 0 rows"), (torch.cat([x, x]), "6 tokens for 12 rows"),
+                             (x.half(), "bf16"), (x[0], "bf16"), (x.cpu(), "CUDA")):
+            with pytest.raises(ValueError, match=message):
+                f(bad, t)
+        for bad, message in ((t.long(), "int32"), (t.T.contiguous().T, "contiguous"), (t.flatten(), "int32"), (t.cpu(), "CUDA")):
+            with pytest.raises(ValueError, match=message):
+                f(x, bad)
+    assert nf4.path_counters()["total"] == before
+    rows = nf4.nf4_dispatch(x, t)
+    assert torch.equal(rows[t.long()], x[:, None].expand(6, 2, 64))
