@@ -163,8 +163,9 @@ def nf4_linear_multi(x: torch.Tensor, ws) -> tuple:
 
 class NF4MoECombineFn(torch.autograd.Function):
     """The top-k combine of the grouped experts (nf4_moe_combine): token t's output
-    is the sum of its routed rows; the backward (nf4_moe_combine_bwd) copies each
-    token's gradient to its rows.  The route table goes through save_for_backward."""
+    is the sum of its routed rows; the backward (NF4DispatchFn, nf4_moe_combine_bwd) copies
+    each token's gradient to its rows.  The route table goes through save_for_backward.
+    Linear, so derivatives of any order are those of the two maps in turn."""
 
     @staticmethod
     def forward(ctx, rows, token_rows):
@@ -176,8 +177,7 @@ class NF4MoECombineFn(torch.autograd.Function):
     @staticmethod
     def backward(ctx, gy):
         (token_rows,) = ctx.saved_tensors
-        g = ops.moe_combine_bwd(gy.contiguous(), token_rows, ctx.R) if ctx.needs_input_grad[0] else None
-        return g, None
+        return NF4DispatchFn.apply(gy, token_rows, ctx.R) if ctx.needs_input_grad[0] else None, None
 
 
 def nf4_combine(rows: torch.Tensor, token_rows: torch.Tensor) -> torch.Tensor:
@@ -187,17 +187,18 @@ def nf4_combine(rows: torch.Tensor, token_rows: torch.Tensor) -> torch.Tensor:
 
 class NF4DispatchFn(torch.autograd.Function):
     """Each token's activations copied to the rows of its routes (the copy that is the combine's
-    backward), with the combine as its own backward: the reverse of NF4MoECombineFn."""
+    backward), with the combine (NF4MoECombineFn) as its own backward.  `R` rows, tokens * k of them
+    unless it is given."""
 
     @staticmethod
-    def forward(ctx, x, token_rows):
+    def forward(ctx, x, token_rows, R: int = None):
         ctx.save_for_backward(token_rows)
-        return ops.moe_combine_bwd(x.contiguous(), token_rows, token_rows.numel())
+        return ops.moe_combine_bwd(x.contiguous(), token_rows, token_rows.numel() if R is None else R)
 
     @staticmethod
     def backward(ctx, grows):
         (token_rows,) = ctx.saved_tensors
-        return ops.moe_combine(grows.contiguous(), token_rows) if ctx.needs_input_grad[0] else None, None
+        return NF4MoECombineFn.apply(grows, token_rows) if ctx.needs_input_grad[0] else None, None, None
 
 
 def nf4_dispatch(x: torch.Tensor, token_rows: torch.Tensor) -> torch.Tensor:

@@ -181,3 +181,39 @@ def _weight_from(w32):
     t = lambda a: torch.from_numpy(np.ascontiguousarray(a))
     return ops.NF4Weight(t(st.packed), t(st.absmax), None, None, None, t(ocb.nf4_code4()), None,
                          w32.shape[0], w32.shape[1], False)
+
+
+@pytest.fixture
+def cpu_routes(monkeypatch):
+    """The dispatch's and the combine's calls in plain torch, in the type of their inputs and, as kernels, not seen by autograd."""
+    @torch.no_grad()
+    def combine(rows, token_rows, out=None):
+        held = rows[token_rows.clamp(min=0).long()]
+        return torch.where((token_rows >= 0)[..., None], held, 0.0).sum(1)
+
+    @torch.no_grad()
+    def spread(grad_out, token_rows, R, out=None):
+        t, j = (token_rows >= 0).nonzero(as_tuple=True)
+        return torch.zeros(R, grad_out.shape[1], dtype=grad_out.dtype).index_add_(0, token_rows[t, j].long(), grad_out[t])
+
+    monkeypatch.setattr(ops, "moe_combine", combine)
+    monkeypatch.setattr(ops, "moe_combine_bwd", spread)
+
+
+def test_dispatch_and_combine_second_derivatives(cpu_routes):
+    """Gradients of gradients of dispatch and combine, against their own closed form and against differences."""
+    t = torch.tensor([[0, 3], [1, -1], [5, 2], [-1, -1]], dtype=torch.int32)
+    present = (t >= 0).sum(1, keepdim=True).double()
+    x = torch.randn(4, 3, dtype=torch.float64, requires_grad=True)
+    g, = torch.autograd.grad(nf4.nf4_dispatch(x, t).pow(3).sum() + x.pow(3).sum(), x, create_graph=True)
+    torch.testing.assert_close(g, 3 * (present + 1) * x.square())
+    g2, = torch.autograd.grad(g.sum(), x)
+    torch.testing.assert_close(g2, 6 * (present + 1) * x)
+    rows = torch.randn(9, 3, dtype=torch.float64, requires_grad=True)
+    g, = torch.autograd.grad(nf4.nf4_combine(rows, t).pow(3).sum(), rows, create_graph=True)
+    g2, = torch.autograd.grad(g.sum(), rows)
+    want, = torch.autograd.grad((6 * nf4.nf4_combine(rows.detach(), t) * present * nf4.nf4_combine(rows, t)).sum(), rows)
+    torch.testing.assert_close(g2, want)
+    for f, a in ((nf4.nf4_dispatch, x), (nf4.nf4_combine, rows)):
+        assert torch.autograd.gradcheck(lambda a: f(a, t).pow(2), (a,)) and torch.autograd.gradgradcheck(lambda a: f(a, t).pow(3), (a,))
+    assert nf4.NF4DispatchFn.apply(x, t).shape == (8, 3) and torch.autograd.grad(nf4.NF4DispatchFn.apply(x, t).sum(), x)[0].shape == x.shape

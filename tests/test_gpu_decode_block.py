@@ -204,3 +204,16 @@ def test_dispatch_refuses_tables_that_do_not_fit():
     assert nf4.path_counters()["total"] == before
     rows = nf4.nf4_dispatch(x, t)
     assert torch.equal(rows[t.long()], x[:, None].expand(6, 2, 64))
+
+
+def test_dispatch_and_combine_second_derivatives():
+    """A penalty on the gradient of a squared path through dispatch and combine, on the kernels.  The values are small whole
+    numbers, so that every sum is exact in bf16."""
+    T, k, H = 9, 2, 64
+    t = nf4.route_experts(gen(10)(T, 6), k, live=torch.arange(T, device=DEV) < 7).token_rows
+    x = torch.randint(-2, 3, (T, H), generator=torch.Generator().manual_seed(1)).to(DEV, BF16).requires_grad_()
+    y = nf4.nf4_combine(nf4.nf4_dispatch(x, t).square(), t)  # k x^2 of the live tokens
+    g, = torch.autograd.grad(y.sum(), x, create_graph=True)
+    g2, = torch.autograd.grad(g.square().sum(), x)  # of (2 k x)^2
+    live = (t[:, :1] >= 0)
+    assert torch.equal(g, 2 * k * x.detach() * live) and torch.equal(g2, 8 * k * k * x.detach() * live)
