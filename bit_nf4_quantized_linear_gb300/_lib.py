@@ -63,6 +63,7 @@ class nf4_epilogue(ctypes.Structure):
         ("bias", ctypes.c_void_p),
         ("row_scale", ctypes.c_void_p),
         ("swiglu", ctypes.c_int32),
+        ("zero_rest", ctypes.c_int32),
     ]
 
 
@@ -175,6 +176,7 @@ def lib() -> ctypes.CDLL:
             "nf4_linear_dgrad_f16": [P, I64, I64, W, P, I64, P, SZ, P],
             "nf4_grouped_fwd": [P, P, I32, I64, I64, W, I64, P, I64, P],
             "nf4_grouped_dgrad": [P, P, I32, I64, I64, W, I64, P, I64, P],
+            "nf4_grouped_dgrad_ep": [P, P, I32, I64, I64, W, I64, ctypes.POINTER(nf4_epilogue), P, I64, P],
             "nf4_grouped_fwd_ep": [P, P, I32, I64, I64, W, I64, ctypes.POINTER(nf4_epilogue), P, I64, P],
             "nf4_grouped_swiglu_bwd": [P, P, I32, I64, I64, W, I64, ctypes.POINTER(nf4_epilogue), P, I64,
                                        P, I64, P, P, SZ, P],

@@ -110,7 +110,8 @@ class NF4GroupedSwiGLUFn(torch.autograd.Function):
 
 def nf4_grouped_swiglu(x: torch.Tensor, offsets: torch.Tensor, w: ops.NF4Weight, experts: int,
                        row_scale: torch.Tensor = None) -> torch.Tensor:
-    """Fused expert SwiGLU over an interleaved gate/up weight (bf16 activations)."""
+    """Fused expert SwiGLU over an interleaved gate/up weight (bf16 activations).  Rows behind the last expert's
+    (offsets[E] below the rows of x: padding) are zero, and so are their gradients."""
     return NF4GroupedSwiGLUFn.apply(x, offsets, row_scale, *w.tensors(), experts, w.N, w.K,
                                     w.double_quant)
 
@@ -328,7 +329,10 @@ def nf4_route(logits: torch.Tensor, k: int, *, score: str = "softmax", bias: tor
 
         r = nf4_route(x @ gate.T, k)
         h = nf4_grouped_swiglu(nf4_dispatch(x, r.token_rows), r.offsets, w_gate_up, E, r.row_weight)
-        y = nf4_combine(nf4_grouped(h, r.offsets, w_down, E), r.token_rows)"""
+        y = nf4_combine(nf4_grouped(h, r.offsets, w_down, E), r.token_rows)
+
+    With `live`, the rows from r.offsets[E] on are no token's: zeros in all of these tensors.  (r.row_token is -1 there: no
+    index.)"""
     how = dict(score=score, groups=groups, top_groups=top_groups, group_top=group_top, renormalise=renormalise, scale=float(scale), tables=tables)
     return route_ops.Routes(*NF4RouteFn.apply(logits, k, bias, live, how))
 
@@ -347,6 +351,8 @@ def nf4_linear(x: torch.Tensor, w: ops.NF4Weight) -> torch.Tensor:
 
 
 def nf4_grouped(x: torch.Tensor, offsets: torch.Tensor, w: ops.NF4Weight, experts: int) -> torch.Tensor:
+    """Grouped experts, rows offsets[e] .. offsets[e + 1] - 1 of x through expert e.  Rows behind the last expert's
+    (offsets[E] below the rows of x: padding) are zero, and so are their gradients."""
     dt = x.dtype
     xb = x if dt == torch.bfloat16 else x.to(torch.bfloat16)
     y = NF4GroupedFn.apply(xb, offsets, *w.tensors(), experts, w.N, w.K, w.double_quant)

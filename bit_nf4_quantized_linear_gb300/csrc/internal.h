@@ -306,6 +306,9 @@ struct GemmArgs {
   const float* ep_bias;
   const float* ep_scale;
   int ep_swiglu;
+  // Grouped: columns of `out` to set to zero in the rows behind the last expert's (0: those
+  // rows are left as they were).
+  int64_t rest_cols;
   // Backward of the SwiGLU epilogue (ep_swiglu and ep_bwd set): the recomputed
   // gate g and up u meet the upstream gradient dh [T, N_e / 2] (bf16, row pitch
   // ep_ld_dh) and, instead of h, the kernel writes dg = dh r u silu'(g) and

@@ -682,7 +682,7 @@ size_t swiglu_bwd_dgu_bytes(int64_t T, int64_t N_e) {
 
 nf4_status run_grouped(int mode, const void* act, const int32_t* offsets, int32_t E, int64_t T,
                        int64_t ld_act, const nf4_weight* w, int64_t N_e, void* out, int64_t ld_out,
-                       void* stream, const nf4_epilogue* ep = nullptr,
+                       void* stream, bool zero_rest, const nf4_epilogue* ep = nullptr,
                        const SwigluBwd* bwd = nullptr) {
   nf4_status st = check_weight(w);
   if (st != NF4_OK) return st;
@@ -747,6 +747,7 @@ nf4_status run_grouped(int mode, const void* act, const int32_t* offsets, int32_
     a.ep_scale = ep->row_scale;
     a.ep_swiglu = ep->swiglu;
   }
+  a.rest_cols = zero_rest ? out_width : 0;
   if (bwd) {
     a.ep_bwd = 1;
     a.ep_dh = static_cast<const __nv_bfloat16*>(bwd->dh);
@@ -1562,20 +1563,27 @@ nf4_status nf4_linear_dgrad_f16(const void* gy, int64_t M, int64_t ldgy, const n
 
 nf4_status nf4_grouped_fwd(const void* x, const int32_t* offsets, int32_t E, int64_t T, int64_t ldx,
                            const nf4_weight* w, int64_t N_e, void* y, int64_t ldy, void* stream) {
-  return run_grouped(0, x, offsets, E, T, ldx, w, N_e, y, ldy, stream);
+  return run_grouped(0, x, offsets, E, T, ldx, w, N_e, y, ldy, stream, false);
 }
 
 nf4_status nf4_grouped_fwd_ep(const void* x, const int32_t* offsets, int32_t E, int64_t T,
                               int64_t ldx, const nf4_weight* w, int64_t N_e, const nf4_epilogue* ep,
                               void* y, int64_t ldy, void* stream) {
   if (!ep) return NF4_ERR_INVALID_ARG;
-  return run_grouped(0, x, offsets, E, T, ldx, w, N_e, y, ldy, stream, ep);
+  return run_grouped(0, x, offsets, E, T, ldx, w, N_e, y, ldy, stream, ep && ep->zero_rest == 1, ep);
 }
 
 nf4_status nf4_grouped_dgrad(const void* gy, const int32_t* offsets, int32_t E, int64_t T,
                              int64_t ldgy, const nf4_weight* w, int64_t N_e, void* gx, int64_t ldgx,
                              void* stream) {
-  return run_grouped(1, gy, offsets, E, T, ldgy, w, N_e, gx, ldgx, stream);
+  return run_grouped(1, gy, offsets, E, T, ldgy, w, N_e, gx, ldgx, stream, false);
+}
+
+nf4_status nf4_grouped_dgrad_ep(const void* gy, const int32_t* offsets, int32_t E, int64_t T, int64_t ldgy,
+                                const nf4_weight* w, int64_t N_e, const nf4_epilogue* ep, void* gx, int64_t ldgx,
+                                void* stream) {
+  if (ep && (ep->bias || ep->row_scale || ep->swiglu)) return NF4_ERR_INVALID_ARG;
+  return run_grouped(1, gy, offsets, E, T, ldgy, w, N_e, gx, ldgx, stream, ep && ep->zero_rest == 1);
 }
 
 nf4_status nf4_grouped_swiglu_bwd(const void* x, const int32_t* offsets, int32_t E, int64_t T,
@@ -1596,9 +1604,9 @@ nf4_status nf4_grouped_swiglu_bwd(const void* x, const int32_t* offsets, int32_t
   void* dgu = base;  // bf16 [T, N_e]
   float* part = grad_row_scale ? reinterpret_cast<float*>(base + swiglu_bwd_dgu_bytes(T, N_e)) : nullptr;
   SwigluBwd b{gh, ldgh, part};
-  nf4_status st = run_grouped(0, x, offsets, E, T, ldx, w, N_e, dgu, N_e, stream, ep, &b);
+  nf4_status st = run_grouped(0, x, offsets, E, T, ldx, w, N_e, dgu, N_e, stream, false, ep, &b);
   if (st != NF4_OK) return st;
-  st = run_grouped(1, dgu, offsets, E, T, N_e, w, N_e, gx, ldgx, stream);
+  st = run_grouped(1, dgu, offsets, E, T, N_e, w, N_e, gx, ldgx, stream, ep->zero_rest == 1);
   if (st != NF4_OK) return st;
   if (grad_row_scale) {
     cudaError_t le = nf4::launch_row_partial_sum(part, static_cast<int>(N_e / 64), T, offsets, E,

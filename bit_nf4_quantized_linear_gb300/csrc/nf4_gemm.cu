@@ -580,6 +580,18 @@ __device__ __forceinline__ void cs_epilogue(const GemmArgs& a, const Shared& sh,
   }
 }
 
+// Zeros in rows [first, M) of a grouped product's output, the CTAs taking rows in turn.
+__device__ __forceinline__ void zero_rest(const GemmArgs& a, int first) {
+  const bool vec = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && a.ld_out % 8 == 0 && a.rest_cols % 8 == 0;
+  for (int64_t r = first + static_cast<int64_t>(blockIdx.x); r < a.M; r += gridDim.x) {
+    __nv_bfloat16* row = a.out + r * a.ld_out;
+    if (vec)
+      for (int64_t c = threadIdx.x; c < a.rest_cols / 8; c += kThreads) reinterpret_cast<uint4*>(row)[c] = make_uint4(0u, 0u, 0u, 0u);
+    else
+      for (int64_t c = threadIdx.x; c < a.rest_cols; c += kThreads) reinterpret_cast<uint16_t*>(row)[c] = 0;
+  }
+}
+
 // MULTI: a multi-product launch (tensor maps and statistics per product).
 template <int MODE, int BT, int BITS, bool F16, bool MULTI = false>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -679,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (a.grouped && threadIdx.x == kWarpEpi0 * 32) {
     // Per-expert token tiles and their prefix; offsets outside the contract are
     // reported and that expert is skipped.
-    int acc = 0;
+    int acc = 0, rest = 0;  // rest: the first row behind all experts'
     bool bad = false;
     sh.pref[0] = 0;
     for (int e = 0; e < a.E; ++e) {
@@ -688,13 +700,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       bad |= !ok;
       sh.starts[e] = ok ? s0 : 0;
       sh.ends[e] = ok ? s1 : 0;
+      rest = ok && s1 > rest ? s1 : rest;
       acc += ok ? (s1 - s0 + BT - 1) / BT : 0;
       sh.pref[e + 1] = acc;
     }
     *item_count = acc;
+    sh.ends[a.E] = rest;
     if (bad) record_error(a, kStatusBadOffsets);
   }
   __syncthreads();
+  // Grouped, where asked for: zeros in the rows of no expert (padding of a batch), by all threads,
+  // of which no role holds registers yet.
+  if (a.rest_cols) zero_rest(a, sh.ends[a.E]);
   if (a.cs > 1 || kPair) cluster_sync();  // every rank's barriers exist before any remote arrival
   tc_fence_after();
   const uint32_t tmem_base = *sh.tmem_slot;

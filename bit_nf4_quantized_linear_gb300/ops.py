@@ -307,7 +307,9 @@ def grouped_fwd(x: torch.Tensor, offsets: torch.Tensor, w: NF4Weight, experts: i
                 out: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
                 row_scale: Optional[torch.Tensor] = None, swiglu: bool = False) -> torch.Tensor:
     """nf4_grouped_fwd: rows offsets[e]..offsets[e+1] of x through expert e.
-    w is the stacked [E*N_e, K] weight; returns bf16 [T, N_e].
+    w is the stacked [E*N_e, K] weight; returns bf16 [T, N_e].  Rows behind the last
+    expert's (offsets[E] < T: padding) are zero in a new tensor, and left as they are
+    in a given `out`.
     With an epilogue (nf4_grouped_fwd_ep): `bias` fp32 [E*N_e] per weight row,
     `row_scale` fp32 [T] per output row (routing weights), `swiglu` for a weight whose
     expert rows interleave gate and up in groups of 64 (see `interleave_gate_up`):
@@ -321,14 +323,14 @@ def grouped_fwd(x: torch.Tensor, offsets: torch.Tensor, w: NF4Weight, experts: i
     width = N_e // 2 if swiglu else N_e
     y = torch.empty(T, width, dtype=torch.bfloat16, device=x.device) if out is None else out
     s = w.struct()
-    if bias is None and row_scale is None and not swiglu:
+    if bias is None and row_scale is None and not swiglu and out is not None:
         rc = _lib.lib().nf4_grouped_fwd(_ptr(x), _ptr(offsets), experts, T, x.stride(0),
                                         ctypes.byref(s), N_e, _ptr(y), y.stride(0), _stream())
     else:
         for name, t, n in (("bias", bias, w.N), ("row_scale", row_scale, T)):
             if t is not None and (t.dtype != torch.float32 or t.numel() != n or not t.is_contiguous()):
                 raise ValueError(f"grouped_fwd: {name} must be a contiguous fp32 tensor of {n} values")
-        ep = _lib.nf4_epilogue(_ptr(bias), _ptr(row_scale), 1 if swiglu else 0)
+        ep = _lib.nf4_epilogue(_ptr(bias), _ptr(row_scale), 1 if swiglu else 0, 1 if out is None else 0)
         rc = _lib.lib().nf4_grouped_fwd_ep(_ptr(x), _ptr(offsets), experts, T, x.stride(0),
                                            ctypes.byref(s), N_e, ctypes.byref(ep), _ptr(y),
                                            y.stride(0), _stream())
@@ -343,7 +345,8 @@ def grouped_swiglu_bwd(x: torch.Tensor, offsets: torch.Tensor, w: NF4Weight, exp
     """nf4_grouped_swiglu_bwd: the backward of grouped_fwd(..., swiglu=True) over an
     interleaved gate/up weight.  x bf16 [T, K] (the forward input), gh bf16
     [T, N_e / 2].  Returns (grad_x bf16 [T, K], grad_row_scale fp32 [T] or None);
-    the second needs `row_scale` and `need_row_scale_grad`."""
+    the second needs `row_scale` and `need_row_scale_grad`.  Rows behind the last
+    expert's have gradients of zero."""
     _check_act("grouped_swiglu_bwd", x, w.K)
     N_e = w.N // experts
     _check_act("grouped_swiglu_bwd", gh, N_e // 2)
@@ -360,7 +363,7 @@ def grouped_swiglu_bwd(x: torch.Tensor, offsets: torch.Tensor, w: NF4Weight, exp
     need = workspace_size(_lib.OP_GROUPED_SWIGLU_BWD, T, N_e, w.K, experts)
     if ws is None or ws.numel() * ws.element_size() < need:
         ws = torch.empty(max(need, 256), dtype=torch.uint8, device=x.device)
-    ep = _lib.nf4_epilogue(_ptr(bias), _ptr(row_scale), 1)
+    ep = _lib.nf4_epilogue(_ptr(bias), _ptr(row_scale), 1, 1)
     s = w.struct()
     rc = _lib.lib().nf4_grouped_swiglu_bwd(_ptr(x), _ptr(offsets), experts, T, x.stride(0),
                                            ctypes.byref(s), N_e, ctypes.byref(ep), _ptr(gh),
@@ -386,7 +389,8 @@ def interleave_gate_up(gate: torch.Tensor, up: torch.Tensor, experts: int) -> to
 
 def grouped_dgrad(gy: torch.Tensor, offsets: torch.Tensor, w: NF4Weight, experts: int,
                   out: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """nf4_grouped_dgrad: per-expert grad_x; gy bf16 [T, N_e] -> gx bf16 [T, K]."""
+    """nf4_grouped_dgrad: per-expert grad_x; gy bf16 [T, N_e] -> gx bf16 [T, K].  Rows behind
+    the last expert's are zero in a new tensor, and left as they are in a given `out`."""
     N_e = w.N // experts
     _check_act("grouped_dgrad", gy, N_e)
     _need_cuda("grouped_dgrad", offsets)
@@ -395,8 +399,9 @@ def grouped_dgrad(gy: torch.Tensor, offsets: torch.Tensor, w: NF4Weight, experts
     T = gy.shape[0]
     gx = torch.empty(T, w.K, dtype=torch.bfloat16, device=gy.device) if out is None else out
     s = w.struct()
-    rc = _lib.lib().nf4_grouped_dgrad(_ptr(gy), _ptr(offsets), experts, T, gy.stride(0),
-                                      ctypes.byref(s), N_e, _ptr(gx), gx.stride(0), _stream())
+    ep = _lib.nf4_epilogue(None, None, 0, 1 if out is None else 0)
+    rc = _lib.lib().nf4_grouped_dgrad_ep(_ptr(gy), _ptr(offsets), experts, T, gy.stride(0),
+                                         ctypes.byref(s), N_e, ctypes.byref(ep), _ptr(gx), gx.stride(0), _stream())
     _lib.check(rc, "nf4_grouped_dgrad")
     return gx
 

@@ -283,7 +283,8 @@ nf4_status nf4_linear_dgrad_f16(const void* gy, int64_t M, int64_t ldgy, const n
  *            [e*N_e, (e+1)*N_e); w->K = K.
  *   offsets  DEVICE int32 [E+1]: rows offsets[e] .. offsets[e+1]-1 of x belong to
  *            expert e; offsets[0] == 0, non-decreasing, offsets[E] <= T (rows from
- *            offsets[E] on belong to none and are left as they were).  Offsets
+ *            offsets[E] on belong to none: they are left as they were, or set to
+ *            zero where the calls below are given zero_rest).  Offsets
  *            outside that contract are detected on the device: the bad expert's
  *            rows are skipped and NF4_ERR_BAD_OFFSETS is recorded in the device
  *            status word.
@@ -301,22 +302,30 @@ nf4_status nf4_grouped_fwd(const void* x, const int32_t* offsets, int32_t E, int
  *              silu(g) = g / (1 + exp(-g)), g and u including their biases;
  *              0: y = a (+ bias), N_e columns;
  *   row_scale  [T] fp32 multiplying each output row last (the tokens' routing
- *              weights in the expert-sorted order; NULL: none).
+ *              weights in the expert-sorted order; NULL: none);
+ *   zero_rest  1: the output's rows behind the last expert's (padding of a batch) are
+ *              set to zero; 0: they are left as they were.
  * fp32 arithmetic, one bf16 rounding at the end; otherwise as nf4_grouped_fwd. */
 typedef struct {
   const float* bias;
   const float* row_scale;
   int32_t swiglu;
+  int32_t zero_rest;
 } nf4_epilogue;
 nf4_status nf4_grouped_fwd_ep(const void* x, const int32_t* offsets, int32_t E, int64_t T,
                               int64_t ldx, const nf4_weight* w, int64_t N_e, const nf4_epilogue* ep,
                               void* y, int64_t ldy, void* stream);
 
 /* nf4_grouped_dgrad -- per-expert input gradient gx[rows of e] = gy[rows of e] W_e.
- *   gy [T, N_e] bf16 (ldgy), gx [T, K] bf16 (ldgx); other arguments as above. */
+ *   gy [T, N_e] bf16 (ldgy), gx [T, K] bf16 (ldgx); other arguments as above.
+ * nf4_grouped_dgrad_ep -- the same with ep's zero_rest for gx (its other fields 0; ep
+ * may be NULL). */
 nf4_status nf4_grouped_dgrad(const void* gy, const int32_t* offsets, int32_t E, int64_t T,
                              int64_t ldgy, const nf4_weight* w, int64_t N_e, void* gx, int64_t ldgx,
                              void* stream);
+nf4_status nf4_grouped_dgrad_ep(const void* gy, const int32_t* offsets, int32_t E, int64_t T, int64_t ldgy,
+                                const nf4_weight* w, int64_t N_e, const nf4_epilogue* ep, void* gx,
+                                int64_t ldgx, void* stream);
 
 /* nf4_grouped_swiglu_bwd -- backward of nf4_grouped_fwd_ep with swiglu = 1 (fork
  * PR "Experts trainability ...", commit 2: the backward recomputes the expert
@@ -332,7 +341,8 @@ nf4_status nf4_grouped_dgrad(const void* gy, const int32_t* offsets, int32_t E, 
  *      the row's N_e/2 outputs of silu(g) u gh, as fp32 partials per 32 gate
  *      columns added in a fixed order (rows outside the expert ranges get 0).
  *   x [T, K] bf16 (ldx), the forward's input; w, offsets, E, N_e, ep (swiglu must
- *   be 1; bias and row_scale as in the forward) as in nf4_grouped_fwd_ep.
+ *   be 1; bias and row_scale as in the forward; zero_rest is that of gx) as in
+ *   nf4_grouped_fwd_ep.
  *   gh [T, N_e/2] bf16 (ldgh, a multiple of 8, 16-byte aligned); gx [T, K] bf16
  *   (ldgx); grad_row_scale DEVICE fp32 [T] or NULL.
  *   ws: device workspace of nf4_workspace_size(NF4_OP_GROUPED_SWIGLU_BWD, T, N_e,

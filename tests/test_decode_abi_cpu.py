@@ -145,3 +145,17 @@ def test_route_tables_that_do_not_fit_the_activations_are_refused():
             ops._check_token_rows("op", t, x, tokens)
     with pytest.raises(ValueError, match="op: token_rows on meta"):
         ops._check_token_rows("op", t.to("meta"), x)
+
+
+def test_grouped_epilogue_of_the_input_gradient(L):
+    """nf4_grouped_dgrad_ep takes zero_rest alone; the flag lies in what was padding of the struct."""
+    assert ctypes.sizeof(_lib.nf4_epilogue) == 24 and _lib.nf4_epilogue(None, None, 1).zero_rest == 0
+    w = _lib.nf4_weight(0x1000, 0x1000, None, None, None, 0x1000, None, 384, 256, 64, 256, 0, 4)
+
+    def dgrad(ep, T=10, offsets=X):
+        return L.nf4_grouped_dgrad_ep(X, offsets, 3, T, 128, ctypes.byref(w), 128, ep, X, 256, None)
+
+    for ep in (_lib.nf4_epilogue(0x1000, None, 0, 1), _lib.nf4_epilogue(None, 0x1000, 0, 1), _lib.nf4_epilogue(None, None, 1, 1)):
+        assert dgrad(ctypes.byref(ep)) == INVALID
+    assert dgrad(None, offsets=None) == INVALID and dgrad(ctypes.byref(_lib.nf4_epilogue(None, None, 0, 1)), T=-1) == INVALID
+    assert dgrad(ctypes.byref(_lib.nf4_epilogue(None, None, 0, 1)), T=0) == 0 and dgrad(None, T=0) == 0

@@ -217,3 +217,56 @@ def test_dispatch_and_combine_second_derivatives():
     g2, = torch.autograd.grad(g.square().sum(), x)  # of (2 k x)^2
     live = (t[:, :1] >= 0)
     assert torch.equal(g, 2 * k * x.detach() * live) and torch.equal(g2, 8 * k * k * x.detach() * live)
+
+
+@pytest.mark.parametrize("counts,pad", [((0, 0, 0), 3), ((0, 0, 0), 300), ((1, 0, 0), 1), ((5, 40, 0), 7), ((0, 200, 133), 260)])
+@pytest.mark.parametrize("bits", [4, 8])
+def test_rows_of_no_expert_are_zero_in_new_tensors(counts, pad, bits):
+    """Rows behind the last expert's, in memory that held NaN: zeros in what the calls return, left as they were in `out`."""
+    E, N_e, K = 3, 384, 256
+    n = gen(sum(counts) + pad)
+    wt = 0.05 * n(E * N_e, K)
+    w = nf4.quantize(wt, quant_type="int8" if bits == 8 else "nf4")
+    used = sum(counts)
+    T = used + pad
+    offsets = torch.tensor([sum(counts[:i]) for i in range(E + 1)], dtype=torch.int32, device=DEV)
+    x, gy, gh = n(T, K).to(BF16), n(T, N_e).to(BF16), n(T, N_e // 2).to(BF16)
+    scale = torch.rand(T, device=DEV)
+
+    def dirty(*shapes):
+        held = [torch.full(s, math.nan, dtype=dt, device=DEV) for s, dt in shapes]
+        del held
+
+    calls = {"fwd": (N_e, lambda **kw: nf4.grouped_fwd(x, offsets, w, E, **kw)),
+             "scaled": (N_e, lambda **kw: nf4.grouped_fwd(x, offsets, w, E, row_scale=scale, **kw)),
+             "swiglu": (N_e // 2, lambda **kw: nf4.grouped_fwd(x, offsets, w, E, row_scale=scale, swiglu=True, **kw)),
+             "dgrad": (K, lambda **kw: nf4.grouped_dgrad(gy, offsets, w, E, **kw))}
+    for name, (width, call) in calls.items():
+        held = torch.full((T, width), 7.0, dtype=BF16, device=DEV)
+        call(out=held)
+        assert (held[used:] == 7).all(), name
+        dirty(((T, width), BF16))
+        y = call()
+        assert torch.equal(y[:used], held[:used]) and (y[used:] == 0).all(), name
+    if bits == 4:
+        dirty(((T, K), BF16), ((T,), torch.float32))
+        gx, gs = nf4.grouped_swiglu_bwd(x, offsets, w, E, gh, row_scale=scale, need_row_scale_grad=True)
+        assert torch.isfinite(gx).all() and (gx[used:] == 0).all() and (gs[used:] == 0).all()
+
+
+def test_an_adapter_between_dispatch_and_combine_with_padding():
+    """A trained low-rank path beside the frozen experts, over all rows: its weights' gradients see no row of padding."""
+    E, H, I, k, T, pad = 8, 256, 128, 2, 60, 23
+    ex = Experts(E, H, I, 5)
+    n = gen(6)
+    x, wr = n(T, H).to(BF16), 0.1 * n(E, H)
+    live = torch.arange(T, device=DEV) < T - pad
+    r = nf4.nf4_route(x.float() @ wr.T, k, live=live)
+    down, up = (0.05 * n(I, 4)).requires_grad_(), (0.05 * n(4, H)).requires_grad_()
+    for shape in ((T * k, I), (T * k, H)):
+        held = torch.full(shape, math.nan, dtype=BF16, device=DEV)
+        del held
+    h = nf4.nf4_grouped_swiglu(nf4.nf4_dispatch(x, r.token_rows), r.offsets, ex.gate_up, E, r.row_weight)
+    y = nf4.nf4_combine(nf4.nf4_grouped(h, r.offsets, ex.down, E) + (h.float() @ down @ up).to(BF16), r.token_rows)
+    gd, gu = torch.autograd.grad(y.float().sum(), (down, up))
+    assert torch.isfinite(gd).all() and torch.isfinite(gu).all() and torch.isfinite(y).all() and (y[~live] == 0).all()
