@@ -63,6 +63,12 @@ def _cache(name, k_pages, v_pages, page_table, lengths, rows):
                        lengths.data_ptr(), ls[0], pages, ts[1], slots, Hk, D, _DTYPES[dt]), dev, ls[0], Hk, D
 
 
+def _refuse_grad(name, *ts):
+    """The calls are seen by no autograd: a gradient that is asked for through them would be lost without a word."""
+    if torch.is_grad_enabled() and any([t is not None and t.requires_grad for t in ts]):
+        raise ValueError(f"{name} has no gradients: call it under torch.no_grad() or on detached tensors")
+
+
 @functools.lru_cache(maxsize=1024)
 def _slots_share(shape: tuple, stride: tuple) -> bool:
     """Whether slots of pages [pages, slots, heads, D] may meet in memory (one dimension not inside another's steps)."""
@@ -81,10 +87,12 @@ def paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
     page_table[i, t // slots], slot t % slots.  `lengths` int32 [sequences] counts the new tokens already: rows
     cu_seqlens[i] .. cu_seqlens[i + 1] - 1 are the last tokens of sequence i (a prompt or a chunk of one); without
     cu_seqlens row i is the newest token of sequence i.  Rows of sequences of length 0, and rows whose page is missing
-    from the table or lies past its last column (recorded in the device status), are not written."""
+    from the table or lies past its last column (recorded in the device status), are not written.  No gradients, as in
+    paged_attention."""
     name = "paged_append"
     Hk = k_pages.shape[2] if k_pages.dim() == 4 else -1
     d, dev, n, _, _ = _cache(name, k_pages, v_pages, page_table, lengths, (("k", k, Hk), ("v", v, Hk)))
+    _refuse_grad(name, k, v, k_pages, v_pages)
     T, cu = k.shape[0], None
     if v.shape[0] != T or (cu_seqlens is None and T != n):
         raise ValueError(f"{name}: {T} and {v.shape[0]} rows of keys and values for {n} sequences")
@@ -110,9 +118,10 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     keys and values are appended first).  Query head h reads key head h // (Hq // Hk); `scale` defaults to D ** -0.5.
     Returns (o [sequences, Hq, D], lse fp32 [sequences, Hq]); a sequence of length 0 gives zeros and -inf.  `out` takes o in
     place of a new tensor (q itself will do): any strides whose rows do not share storage.  Tables and lengths are read on
-    the device, so a captured graph follows them.  No gradients."""
+    the device, so a captured graph follows them.  No gradients: with gradients enabled, tensors that require one are refused."""
     name = "paged_attention"
     d, dev, n, Hk, D = _cache(name, k_pages, v_pages, page_table, lengths, (("q", q, None),) if out is None else (("q", q, None), ("out", out, None)))
+    _refuse_grad(name, q, k_pages, v_pages, out)
     Hq = q.shape[1]
     if q.shape[0] != n or Hq == 0 or Hq % Hk:
         raise ValueError(f"{name}: q {tuple(q.shape)} does not fit {n} sequences of {Hk} key heads")

@@ -563,3 +563,30 @@ def test_attention_sums_of_the_largest_values(dtype, D):
     page, slot = (torch.cat(t) for t in zip(*(ref.slots_of(table[i], 70, 16) for i in (0, 3))))
     kp[page, slot], vp[page, slot] = -3e4, big
     check(q.abs() + 0.1, kp, vp, table, lengths)
+
+
+def test_tensors_that_require_a_gradient_are_refused():
+    """The calls have no gradients: under grad mode they refuse what asks for one, and take it under no_grad or detached."""
+    kp, vp, table, lengths = cache([20, 5], 2, 64, BF16)
+    q, k, v = queries(2, 4, 64, BF16), queries(2, 2, 64, BF16, 2), queries(2, 2, 64, BF16, 3)
+    before = nf4.path_counters()["total"]
+
+    def leaf(t):
+        return t.clone().requires_grad_()
+
+    for args in ((leaf(q), kp, vp), (q, leaf(kp), vp), (q, kp, leaf(vp)), (leaf(q) * 2, kp, vp)):
+        with pytest.raises(ValueError, match="no gradients"):
+            nf4.paged_attention(*args, table, lengths)
+    with pytest.raises(ValueError, match="no gradients"):
+        nf4.paged_attention(q, kp, vp, table, lengths, out=leaf(q))
+    for args in ((leaf(k), v, kp, vp), (k, leaf(v), kp, vp), (k, v, leaf(kp), vp), (k, v, kp, leaf(vp))):
+        with pytest.raises(ValueError, match="no gradients"):
+            nf4.paged_append(*args, table, lengths)
+    assert nf4.path_counters()["total"] == before
+    want = nf4.paged_attention(q, kp, vp, table, lengths)
+    with torch.no_grad():
+        nf4.paged_append(leaf(k), leaf(v), kp.clone(), vp.clone(), table, lengths)
+        got = nf4.paged_attention(leaf(q), kp, vp, table, lengths)
+    also = nf4.paged_attention(leaf(q).detach(), kp, vp, table, lengths)
+    for a, b, c in zip(want, got, also):
+        assert torch.equal(a, b) and torch.equal(a, c) and not b.requires_grad
