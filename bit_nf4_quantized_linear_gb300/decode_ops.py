@@ -71,19 +71,62 @@ def _refuse_grad(name, *ts):
 
 @functools.lru_cache(maxsize=1024)
 def _slots_share(shape: tuple, stride: tuple) -> bool:
-    """Whether slots of pages [pages, slots, heads, D] may meet in memory (one dimension not inside another's steps)."""
-    reach = shape[3]
-    for step, n in sorted((s, n) for s, n in zip(stride[:3], shape[:3]) if n > 1):
+    """Whether rows of a tensor [..., D] may meet in memory (one dimension not inside another's steps)."""
+    reach = shape[-1]
+    for step, n in sorted((s, n) for s, n in zip(stride[:-1], shape[:-1]) if n > 1):
         if step < reach:
             return True
         reach += step * (n - 1)
     return False
 
 
+@functools.lru_cache(maxsize=1024)
+def _meet(shape: tuple, one: tuple, other: tuple, apart: int) -> bool:
+    """Whether rows of two tensors [..., D] of one shape, the second's first value `apart` behind the first's, may meet in
+    memory."""
+    def reach(stride):
+        return shape[-1] + sum(s * (n - 1) for s, n in zip(stride[:-1], shape[:-1]))
+
+    if 0 in shape or apart >= reach(one) or -apart >= reach(other):
+        return False
+    steps = sorted(((s, t, n) for s, t, n in zip(one[:-1], other[:-1], shape[:-1]) if n > 1), reverse=True)
+    if any(s != t for s, t, _ in steps) or _slots_share(shape, one):
+        return True
+
+    def hit(rest, steps):  # inner dimensions reach less than a step, so two counts of it can meet `rest`
+        if not steps:
+            return abs(rest) < shape[-1]
+        s, _, n = steps[0]
+        return any(hit(rest - i * s, steps[1:]) for i in (rest // s, rest // s + 1) if abs(i) < n)
+
+    return hit(apart, steps)
+
+
+@functools.lru_cache(maxsize=1024)
+def _writable(shape: tuple, k: tuple, v: tuple, apart: int) -> bool:
+    """Whether every slot of key and value pages of these strides has memory of its own."""
+    return not (_slots_share(shape, k) or _slots_share(shape, v) or _meet(shape, k, v, apart))
+
+
+def _check_out(name, out, q, k_pages, v_pages):
+    """out: q itself, or memory of its own."""
+    def ends(t):
+        return t.data_ptr(), t.data_ptr() + t.element_size() * (1 + sum(s * (n - 1) for s, n in zip(t.stride(), t.shape)))
+
+    if out.shape != q.shape or _share_storage(out):
+        raise ValueError(f"{name}: out must have q's shape, and rows that do not share storage")
+    apart, at = (out.data_ptr() - q.data_ptr()) // q.element_size(), ends(out)
+    itself = apart == 0 and all(s == t for s, t, n in zip(out.stride(), q.stride(), q.shape) if n > 1)
+    if out.numel() and (not itself and _meet(q.shape, q.stride(), out.stride(), apart)
+                        or any(p.numel() and at[0] < ends(p)[1] and ends(p)[0] < at[1] for p in (k_pages, v_pages))):
+        raise ValueError(f"{name}: out must be q itself or share no storage with q and the pages")
+
+
 def paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,
                  lengths: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None) -> None:
     """nf4_paged_append: writes new tokens' rows k, v [T, Hk, D] into the pages [pages, slots, Hk, D] (any strides whose
-    slots do not share storage: a transposed view of [pages, Hk, slots, D] will do).  Token t of sequence i lies in page
+    slots share no storage, keys and values neither: a transposed view of [pages, Hk, slots, D] will do, and so will two halves
+    of one buffer).  k and v may not lie in slots that the call writes.  Token t of sequence i lies in page
     page_table[i, t // slots], slot t % slots.  `lengths` int32 [sequences] counts the new tokens already: rows
     cu_seqlens[i] .. cu_seqlens[i + 1] - 1 are the last tokens of sequence i (a prompt or a chunk of one); without
     cu_seqlens row i is the newest token of sequence i.  Rows of sequences of length 0, and rows whose page is missing
@@ -101,7 +144,7 @@ def paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
         if (cu_seqlens.dtype is not torch.int32 or cu_seqlens.shape != (n + 1,) or not cu_seqlens.is_contiguous()
                 or cu_seqlens.device != dev):
             raise ValueError(f"{name}: cu_seqlens must be a contiguous int32 [{n + 1}] tensor on {dev}")
-    if _slots_share(k_pages.shape, k_pages.stride()) or _slots_share(v_pages.shape, v_pages.stride()):
+    if not _writable(k_pages.shape, k_pages.stride(), v_pages.stride(), (v_pages.data_ptr() - k_pages.data_ptr()) // k_pages.element_size()):
         raise ValueError(f"{name}: slots of the pages share storage")
     kt, vt = k.stride(), v.stride()
     with _on(dev):
@@ -117,7 +160,7 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     over the lengths[i] tokens that page_table names for it (pages and table as in paged_append; the new token's own
     keys and values are appended first).  Query head h reads key head h // (Hq // Hk); `scale` defaults to D ** -0.5.
     Returns (o [sequences, Hq, D], lse fp32 [sequences, Hq]); a sequence of length 0 gives zeros and -inf.  `out` takes o in
-    place of a new tensor (q itself will do): any strides whose rows do not share storage.  Tables and lengths are read on
+    place of a new tensor: q itself, or any strides whose rows share no storage with each other, q or the pages.  Tables and lengths are read on
     the device, so a captured graph follows them.  No gradients: with gradients enabled, tensors that require one are refused."""
     name = "paged_attention"
     d, dev, n, Hk, D = _cache(name, k_pages, v_pages, page_table, lengths, (("q", q, None),) if out is None else (("q", q, None), ("out", out, None)))
@@ -125,8 +168,8 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     Hq = q.shape[1]
     if q.shape[0] != n or Hq == 0 or Hq % Hk:
         raise ValueError(f"{name}: q {tuple(q.shape)} does not fit {n} sequences of {Hk} key heads")
-    if out is not None and (out.shape != q.shape or _share_storage(out)):
-        raise ValueError(f"{name}: out must have q's shape, and rows that do not share storage")
+    if out is not None:
+        _check_out(name, out, q, k_pages, v_pages)
     o = torch.empty((n, Hq, D), dtype=q.dtype, device=dev) if out is None else out
     lse = torch.empty((n, Hq), dtype=torch.float32, device=dev)
     qt, ot = q.stride(), o.stride()

@@ -515,11 +515,13 @@ nf4_status nf4_adamw_state_values(const uint8_t* m, const uint8_t* v, const floa
  * newest token of sequence i (T == nseq).  Rows of idle sequences and outside the offsets are
  * not written; rows before a sequence's first token (more new rows than its length) and past
  * its table's last page are neither, and are recorded.  Nothing but the named slots is written;
- * two rows must not share one.
+ * two rows must not share one, keys and values must not share memory, and k and v must not lie
+ * in what is written.
  *
  * nf4_paged_attention: o_i = sum_t p_t v_t with p = softmax(scale q_i . k_t) over the
  * lengths[i] tokens of sequence i; query head h reads key head h / (Hq / Hk).
- *   q, o        [nseq, Hq, D] of `dtype`, sequence and head strides in elements.
+ *   q, o        [nseq, Hq, D] of `dtype`, sequence and head strides in elements; o may be q
+ *               with q's strides, and otherwise shares no memory with what is read.
  *   lse         fp32 [nseq][Hq], natural log of the sum of exponentials, or NULL.
  *   Idle rows, and rows no token of which has a weight: zeros, and lse -inf.  Slots past a
  *   sequence's length are never read.

@@ -1,5 +1,6 @@
 """Host checks of the paged cache and the router: wrong arguments are refused before any launch (no GPU needed)."""
 import ctypes
+import itertools
 
 import pytest
 import torch
@@ -159,3 +160,27 @@ def test_grouped_epilogue_of_the_input_gradient(L):
         assert dgrad(ctypes.byref(ep)) == INVALID
     assert dgrad(None, offsets=None) == INVALID and dgrad(ctypes.byref(_lib.nf4_epilogue(None, None, 0, 1)), T=-1) == INVALID
     assert dgrad(ctypes.byref(_lib.nf4_epilogue(None, None, 0, 1)), T=0) == 0 and dgrad(None, T=0) == 0
+
+
+def test_tensors_that_meet_in_memory_are_recognised():
+    """Exactly the common addresses, for tensors of one layout; never called free where two addresses are equal."""
+    meet = decode_ops._meet
+
+    def at(shape, stride, first=0):
+        return {first + sum(i * s for i, s in zip(index, stride)) for index in itertools.product(*map(range, shape))}
+
+    for shape, stride in (((2, 3, 2, 2), (12, 4, 2, 1)), ((2, 3, 2, 2), (24, 8, 2, 1)), ((2, 3, 2, 2), (24, 2, 12, 1)), ((3, 2, 4), (20, 4, 1)),
+                          ((3, 2, 4), (5, 30, 1)), ((1, 3, 2), (0, 7, 1)), ((4, 3), (6, 1))):
+        one = at(shape, stride)
+        for apart in range(-90, 91):
+            assert meet(shape, stride, stride, apart) == bool(one & at(shape, stride, apart)), (shape, stride, apart)
+    for one, other in (((12, 4, 2, 1), (24, 4, 2, 1)), ((12, 4, 2, 1), (12, 2, 6, 1)), ((0, 4, 2, 1), (12, 4, 2, 1)), ((4, 4, 2, 1), (4, 4, 2, 1))):
+        for apart in range(-70, 71):
+            assert meet((2, 3, 2, 2), one, other, apart) or not at((2, 3, 2, 2), one) & at((2, 3, 2, 2), other, apart)
+    assert not meet((0, 2, 4), (8, 4, 1), (8, 4, 1), 0)
+    w = decode_ops._writable
+    token, pages = (2048, 128, 64, 1), (5, 16, 2, 64)
+    assert w(pages, token, token, 5 * 2048) and w(pages, token, token, -5 * 2048) and not w(pages, token, token, 0)
+    assert not w(pages, token, token, 2048) and w(pages, (4096, 128, 64, 1), (4096, 128, 64, 1), 2048)  # whole pages in turn
+    assert w(pages, (4096, 256, 64, 1), (4096, 256, 64, 1), 128) and w(pages, (4096, 256, 128, 1), (4096, 256, 128, 1), 64)
+    assert not w(pages, (4096, 256, 128, 1), (4096, 256, 128, 1), 32) and not w(pages, token, (2048, 64, 1024, 1), 64)

@@ -590,3 +590,35 @@ def test_tensors_that_require_a_gradient_are_refused():
     also = nf4.paged_attention(leaf(q).detach(), kp, vp, table, lengths)
     for a, b, c in zip(want, got, also):
         assert torch.equal(a, b) and torch.equal(a, c) and not b.requires_grad
+
+
+def test_memory_that_a_call_both_reads_and_writes():
+    """out in memory that other CTAs read, and keys and values in one place, are refused; out and q, and keys and values,
+    side by side in one buffer are taken."""
+    Hq, Hk, D = 8, 2, 64
+    kp, vp, table, lengths = cache([131, 40, 70], Hk, D, BF16)
+    q, k, v = queries(3, Hq, D, BF16), queries(3, Hk, D, BF16, 2), queries(3, Hk, D, BF16, 3)
+    want = nf4.paged_attention(q, kp, vp, table, lengths)
+    before = nf4.path_counters()["total"]
+    rows, held = torch.zeros(4, Hq, D, dtype=BF16, device=DEV), torch.zeros(3 * Hq * D + 8, dtype=BF16, device=DEV)
+    for a, out in ((rows[:3], rows[1:]), (rows[1:], rows[:3]), (held[:-8].view(3, Hq, D), held[8:].view(3, Hq, D)),
+                   (q, q.view(Hq, 3, D).transpose(0, 1)), (q, kp.view(-1)[5 * D:][:q.numel()].view(q.shape)),
+                   (q, vp.view(-1)[:q.numel()].view(q.shape))):
+        with pytest.raises(ValueError, match="share no storage"):
+            nf4.paged_attention(a, kp, vp, table, lengths, out=out)
+    flat = torch.cat([kp.flatten(), kp.flatten()])
+    for apart in (0, 8, 64, kp.numel() - 8):
+        with pytest.raises(ValueError, match="share storage"):
+            nf4.paged_append(k, v, flat[:kp.numel()].view(kp.shape), flat[apart:apart + kp.numel()].view(kp.shape), table, lengths)
+    assert nf4.path_counters()["total"] == before
+    both = torch.zeros(3, 2, Hq, D, dtype=BF16, device=DEV)
+    both[:, 0] = q
+    got = nf4.paged_attention(both[:, 0], kp, vp, table, lengths, out=both[:, 1])
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(both[:, 0], q)
+    assert torch.equal(nf4.paged_attention(both[:, 0], kp, vp, table, lengths, out=both[:, 0])[0], want[0])
+    wk, wv = kp.clone(), vp.clone()
+    nf4.paged_append(k, v, wk, wv, table, lengths)
+    for dim in range(4):
+        gk, gv = torch.stack([kp, vp], dim).unbind(dim)
+        nf4.paged_append(k, v, gk, gv, table, lengths)
+        assert torch.equal(gk, wk) and torch.equal(gv, wv), dim
