@@ -31,7 +31,8 @@ ADAMW_BLOCK = 256  # NF4_ADAMW_BLOCK of include/nf4.h
 PATHS = ["linear_fwd", "linear_dgrad", "splitk_reduce", "grouped_fwd", "grouped_dgrad",
          "dequantize", "quantize", "total", "gemv_fwd", "gemv_dgrad", "skinny_fwd",
          "skinny_dgrad", "stream_k", "cluster_split", "multi", "moe_combine", "attention", "attention_any",
-         "norm_residual", "adamw", "paged_append", "paged_attention", "paged_attention_any", "route"]
+         "norm_residual", "adamw", "paged_append", "paged_attention", "paged_attention_any", "route",
+         "paged_attention_f32"]
 
 
 class NF4Error(RuntimeError):

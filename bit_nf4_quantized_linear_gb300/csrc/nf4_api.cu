@@ -1167,6 +1167,7 @@ nf4_status nf4_paged_attention(const nf4_paged_cache* c, const void* q, int64_t 
                         : nf4::launch_paged_any(c->dtype, a, dev.sms, static_cast<cudaStream_t>(stream));
   if (le != cudaSuccess) return cuda_fail(le, "kernel launch");
   count(NF4_PATH_PAGED_ATTENTION_ANY);
+  if (rows) g_counters[NF4_PATH_PAGED_ATTENTION_F32].fetch_add(1, std::memory_order_relaxed);  // the same call: not in the total again
   return NF4_OK;
 }
 

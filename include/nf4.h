@@ -104,7 +104,8 @@ enum {
   NF4_PATH_PAGED_ATTENTION = 21,/* attention over the paged cache, tensor-core kernel */
   NF4_PATH_PAGED_ATTENTION_ANY = 22,/* the same for what that kernel does not take */
   NF4_PATH_ROUTE = 23,       /* router of the experts, or its backward     */
-  NF4_NUM_PATHS = 24
+  NF4_PATH_PAGED_ATTENTION_F32 = 24,/* of NF4_PATH_PAGED_ATTENTION_ANY, those of the kernel for aligned fp32 rows */
+  NF4_NUM_PATHS = 25
 };
 
 /* A quantised weight: the tensors of the pages' QuantState as plain device

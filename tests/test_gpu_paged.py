@@ -622,3 +622,36 @@ def test_memory_that_a_call_both_reads_and_writes():
         gk, gv = torch.stack([kp, vp], dim).unbind(dim)
         nf4.paged_append(k, v, gk, gv, table, lengths)
         assert torch.equal(gk, wk) and torch.equal(gv, wv), dim
+
+
+@pytest.mark.parametrize("Hq,Hk,D", [(4, 4, 4), (8, 2, 64), (16, 2, 80), (5, 1, 128), (9, 1, 200), (8, 2, 256)])
+def test_attention_fp32_rows_and_their_kernel(Hq, Hk, D):
+    """Aligned fp32 rows go through the rings, everything else of fp32 to the kernel of any layout; one call counts once."""
+    kp, vp, table, lengths = cache([331, 7, 64, 0, 150], Hk, D, F32, seed=D)
+    q = queries(5, Hq, D, F32)
+
+    def path(call, rings):
+        before = nf4.path_counters()
+        call()
+        after = nf4.path_counters()
+        moved = {name: after[name] - before[name] for name in after if after[name] != before[name]}
+        assert moved == dict(paged_attention_any=1, total=1, **({"paged_attention_f32": 1} if rings else {}))
+
+    def shifted(t):
+        return torch.zeros(t.numel() + 1, device=DEV)[1:].view(t.shape).copy_(t)
+
+    path(lambda: check(q, kp, vp, table, lengths), True)
+    path(lambda: check(q, kp, vp, table, lengths, out=shifted(q)), True)  # only what is read in pieces has to be aligned
+    for args in ((shifted(q), kp, vp), (q, shifted(kp), vp), (q, kp, shifted(vp))):
+        path(lambda: check(*args, table, lengths), False)
+    if D > 4:
+        path(lambda: check(q[..., :-1], kp[..., :-1], vp[..., :-1], table, lengths), False)
+
+
+@pytest.mark.parametrize("page", [3, 24, 100])
+@pytest.mark.parametrize("order", ["token", "head"])
+@pytest.mark.parametrize("D,dtype", [(128, BF16), (136, F16), (256, BF16), (132, F32), (200, F32), (256, F32)])
+def test_attention_pages_of_wide_heads(page, order, D, dtype):
+    """Pages that no tile fits, for rows that take a warp's whole copy or two."""
+    kp, vp, table, lengths = cache([700, 99, 1, 0, 333], 2, D, dtype, page=page, order=order, seed=page)
+    check(queries(5, 8, D, dtype), kp, vp, table, lengths, path="paged_attention_f32" if dtype == F32 else "paged_attention")
