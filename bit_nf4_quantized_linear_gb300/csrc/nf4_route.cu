@@ -365,11 +365,13 @@ __device__ __forceinline__ int route_token(const RouteArgs& a, int64_t t, double
     }
     // Bounds on the error of c, in units of u = 2^-24.  Sigmoid: an exponential of relative error
     // 4 + 1.5 |x| in 1 / (1 + e), so (4 + 1.5 |x|) s (1 - s) < 1.4, and 3 s of the sum and the
-    // reciprocal: less than 4.5.  Softmax: the exponential's 1.5 (top - x) beside exp(x - top) is
-    // less than 1; 24 s for its own error, the row sum's and the product's, and s is at most
-    // 1 / sum.  And c's own rounding.
+    // reciprocal: less than 4.5.  Softmax: an argument d = top - x is off by 2.3 d (difference,
+    // constant, product), which beside exp(-d) / sum is less than 1.  Relative to s: 4 of its own
+    // exponential; of the sum 4 of its terms', 2.3 of their mean d (at most the root of w exp(w) =
+    // (E - 1) / e: 3.9 for 512 experts), V - 1 + 5 additions; a reciprocal and a product: less than
+    // V + 24, and s is at most 1 / sum.  And c's own rounding.
     const float off = a.sigmoid || !inexact ? 4.5f * u + u * __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(cmax)))
-                                            : u * (1.0f + 24.0f * norm) + u * __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(cmax)));
+                                            : u * (1.0f + (V + 24.0f) * norm) + u * __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(cmax)));
     const int size = a.E / a.groups;
     const float inv = 1.0f / size;
     if (grouped && !unsure) {

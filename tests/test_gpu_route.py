@@ -390,3 +390,17 @@ def test_route_backward_in_a_graph():
             x.copy_(gen(s)(64, 16))
         graph.replay()
         assert torch.equal(g, step())
+
+
+@pytest.mark.parametrize("E", [130, 300, 512])
+@pytest.mark.parametrize("spread_by", [0.3, 1.0, 5.0])
+def test_route_borders_nearer_than_fp32_of_many_experts(E, spread_by):
+    """Softmax scores whose sum is of many terms, levelled to within a rounding by the bias."""
+    x = spread_by * gen(E)(60, E)
+    s = ref.scores(x.double(), "softmax")
+    for row in range(0, 60, 10):
+        bias = (0.75 - s[row]).float()
+        assert (s[row] + bias.double()).sub(0.75).abs().max() < 6.1e-8
+        for k in (1, 7, 32):
+            check(x[row:row + 10], k, bias=bias, grads=False)
+        check(x[row:row + 10], 5, bias=bias, groups=10 if E % 10 == 0 else 8, top_groups=3, group_top=2, grads=False)
