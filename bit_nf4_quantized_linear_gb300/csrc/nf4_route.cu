@@ -3,7 +3,7 @@
 // expert for the grouped products, and the gradient of the logits.
 //
 // With s = softmax(x) or 1 / (1 + exp(-x)) of a token's logits x:
-//   c = x (no bias; the order of s), or s + bias; experts of logit -inf come after all others;
+//   c = x (no bias; the order of s), or s + bias; c = -inf where x is (hidden experts);
 //   a group's worth is its largest c, or the sum of its two largest s + bias;
 //   the best groups are kept, and of their experts the k of largest c are chosen, equal ones
 //   by the lower index;

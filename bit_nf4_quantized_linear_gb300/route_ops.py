@@ -74,7 +74,7 @@ def route_experts(logits: torch.Tensor, k: int, *, score: str = "softmax", bias:
                   live: Optional[torch.Tensor] = None, tables: bool = True) -> Routes:
     """nf4_route_fwd: the k experts of each token of logits [tokens, E] (fp32, bf16 or fp16) and their weights, by
     `score` "softmax" or "sigmoid" s: the k largest s + bias (`bias` fp32 [E] moves the choice alone), equal ones by the
-    lower index, of the `top_groups` (None: all) best of `groups` runs of experts, each worth its largest (`group_top` 1) or the sum
+    lower index (s + bias is -inf where the logit is: a hidden expert, like one whose bias is -inf), of the `top_groups` (None: all) best of `groups` runs of experts, each worth its largest (`group_top` 1) or the sum
     of its two largest (2).  The weight is scale * s, with `renormalise` over the sum of the chosen.  Tokens of
     live[t] == 0 get no experts.  With `tables`, the rows of the (token, expert) pairs sorted by expert and then by token:
     `offsets` and `row_weight` are what grouped_fwd takes, `token_rows` what moe_combine takes."""

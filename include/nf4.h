@@ -558,8 +558,8 @@ nf4_status nf4_paged_attention(const nf4_paged_cache* c, const void* q, int64_t 
  * each token, their weights, and the tables that nf4_grouped_* and nf4_moe_combine take.
  * Per token, with logits x [E]:
  *   s = softmax(x) (NF4_SCORE_SOFTMAX) or 1 / (1 + exp(-x)) (NF4_SCORE_SIGMOID);
- *   c = s + bias (bias fp32 [E], it moves the choice alone), or without bias x itself; an
- *   expert of logit -inf comes after all others;
+ *   c = s + bias (bias fp32 [E], it moves the choice alone), or without bias x itself; of a
+ *   logit of -inf c is -inf, as it is of a bias of -inf;
  *   groups > 1: the experts form `groups` runs of E / groups; a run is worth its largest c
  *   (group_top 1) or the sum of its two largest s + bias (group_top 2; -inf counts nothing
  *   beside another); the top_groups best are kept;

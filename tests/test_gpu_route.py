@@ -404,3 +404,18 @@ def test_route_borders_nearer_than_fp32_of_many_experts(E, spread_by):
         for k in (1, 7, 32):
             check(x[row:row + 10], k, bias=bias, grads=False)
         check(x[row:row + 10], 5, bias=bias, groups=10 if E % 10 == 0 else 8, top_groups=3, group_top=2, grads=False)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_hidden_experts_equal_those_of_an_infinite_bias(score):
+    """A logit of -inf and a bias of -inf give the same c, -inf: behind all others, and by the index among each other."""
+    x = gen(20)(1, 8)
+    x[0, [1, 6]] = -math.inf
+    bias = torch.zeros(8, device=DEV)
+    bias[[0, 2, 7]] = -math.inf
+    live = [3, 4, 5]
+    for k in range(1, 9):
+        r = check(x, k, score=score, bias=bias, grads=False)
+        if k >= 3:
+            assert r.experts[0].tolist() == sorted((live + [0, 1, 2, 6, 7])[:k])
+    assert r.weights[0, 1] == 0 and r.weights[0, 6] == 0 and (r.weights[0, [0, 2, 7]] > 0).all()
