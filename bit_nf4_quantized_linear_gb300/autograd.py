@@ -162,6 +162,12 @@ def nf4_linear_multi(x: torch.Tensor, ws) -> tuple:
     return ys if dt == torch.bfloat16 else tuple(y.to(dt) for y in ys)
 
 
+def _packed(t: torch.Tensor) -> torch.Tensor:
+    """t in its own packed strides.  (An empty tensor counts as contiguous whatever its strides are, those of an expanded
+    gradient among them.)"""
+    return t.contiguous() if t.numel() else t.new_empty(t.shape)
+
+
 class NF4MoECombineFn(torch.autograd.Function):
     """The top-k combine of the grouped experts (nf4_moe_combine): token t's output
     is the sum of its routed rows; the backward (NF4DispatchFn, nf4_moe_combine_bwd) copies
@@ -170,7 +176,7 @@ class NF4MoECombineFn(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, rows, token_rows):
-        y = ops.moe_combine(rows.contiguous(), token_rows)
+        y = ops.moe_combine(_packed(rows), token_rows)
         ctx.save_for_backward(token_rows)
         ctx.R = int(rows.shape[0])
         return y
@@ -194,7 +200,7 @@ class NF4DispatchFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, token_rows, R: int = None):
         ctx.save_for_backward(token_rows)
-        return ops.moe_combine_bwd(x.contiguous(), token_rows, token_rows.numel() if R is None else R)
+        return ops.moe_combine_bwd(_packed(x), token_rows, token_rows.numel() if R is None else R)
 
     @staticmethod
     def backward(ctx, grows):

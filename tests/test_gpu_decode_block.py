@@ -270,3 +270,16 @@ def test_an_adapter_between_dispatch_and_combine_with_padding():
     y = nf4.nf4_combine(nf4.nf4_grouped(h, r.offsets, ex.down, E) + (h.float() @ down @ up).to(BF16), r.token_rows)
     gd, gu = torch.autograd.grad(y.float().sum(), (down, up))
     assert torch.isfinite(gd).all() and torch.isfinite(gu).all() and torch.isfinite(y).all() and (y[~live] == 0).all()
+
+
+@pytest.mark.parametrize("T,pad", [(0, 0), (5, 5), (1, 1)])
+def test_moe_layer_of_no_tokens(T, pad):
+    """No tokens, or none that is live: an output and gradients of zeros, from an expanded gradient as sum() gives it."""
+    ex = Experts(8, 256, 128, 1)
+    n = gen(11)
+    x, wr = n(T, 256).to(BF16).requires_grad_(), n(8, 256).requires_grad_()
+    r = nf4.nf4_route(x.float() @ wr.T, 2, live=torch.arange(T, device=DEV) < T - pad)
+    y = ex.layer(x, r)
+    for total in (y.sum(), y.float().sum()):
+        gx, gw = torch.autograd.grad(total, (x, wr), retain_graph=True)
+        assert y.shape == gx.shape == (T, 256) and (y == 0).all() and (gx == 0).all() and (gw == 0).all()
