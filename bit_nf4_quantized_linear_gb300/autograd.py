@@ -184,7 +184,11 @@ class NF4MoECombineFn(torch.autograd.Function):
     @staticmethod
     def backward(ctx, gy):
         (token_rows,) = ctx.saved_tensors
-        return NF4DispatchFn.apply(gy, token_rows, ctx.R) if ctx.needs_input_grad[0] else None, None
+        if not ctx.needs_input_grad[0]:
+            return None, None
+        if torch.is_grad_enabled():  # create_graph
+            return NF4DispatchFn.apply(gy, token_rows, ctx.R), None
+        return ops.moe_combine_bwd(_packed(gy), token_rows, ctx.R), None
 
 
 def nf4_combine(rows: torch.Tensor, token_rows: torch.Tensor) -> torch.Tensor:
@@ -205,7 +209,11 @@ class NF4DispatchFn(torch.autograd.Function):
     @staticmethod
     def backward(ctx, grows):
         (token_rows,) = ctx.saved_tensors
-        return NF4MoECombineFn.apply(grows, token_rows) if ctx.needs_input_grad[0] else None, None, None
+        if not ctx.needs_input_grad[0]:
+            return None, None, None
+        if torch.is_grad_enabled():  # create_graph
+            return NF4MoECombineFn.apply(grows, token_rows), None, None
+        return ops.moe_combine(_packed(grows), token_rows), None, None
 
 
 def nf4_dispatch(x: torch.Tensor, token_rows: torch.Tensor) -> torch.Tensor:
