@@ -81,13 +81,16 @@ def _slots_share(shape: tuple, stride: tuple) -> bool:
 
 
 @functools.lru_cache(maxsize=1024)
+def _reach(shape: tuple, stride: tuple) -> int:
+    """Values from a tensor's first to behind its last."""
+    return 0 if 0 in shape else 1 + sum(s * (n - 1) for s, n in zip(stride, shape))
+
+
+@functools.lru_cache(maxsize=1024)
 def _meet(shape: tuple, one: tuple, other: tuple, apart: int) -> bool:
     """Whether rows of two tensors [..., D] of one shape, the second's first value `apart` behind the first's, may meet in
     memory."""
-    def reach(stride):
-        return shape[-1] + sum(s * (n - 1) for s, n in zip(stride[:-1], shape[:-1]))
-
-    if 0 in shape or apart >= reach(one) or -apart >= reach(other):
+    if 0 in shape or apart >= _reach(shape, one) or -apart >= _reach(shape, other):
         return False
     steps = sorted(((s, t, n) for s, t, n in zip(one[:-1], other[:-1], shape[:-1]) if n > 1), reverse=True)
     if any(s != t for s, t, _ in steps) or _slots_share(shape, one):
@@ -110,15 +113,17 @@ def _writable(shape: tuple, k: tuple, v: tuple, apart: int) -> bool:
 
 def _check_out(name, out, q, k_pages, v_pages):
     """out: q itself, or memory of its own."""
-    def ends(t):
-        return t.data_ptr(), t.data_ptr() + t.element_size() * (1 + sum(s * (n - 1) for s, n in zip(t.stride(), t.shape)))
-
-    if out.shape != q.shape or _share_storage(out):
+    shape, to, tq, e = q.shape, out.stride(), q.stride(), q.element_size()
+    if out.shape != shape or _share_storage(out):
         raise ValueError(f"{name}: out must have q's shape, and rows that do not share storage")
-    apart, at = (out.data_ptr() - q.data_ptr()) // q.element_size(), ends(out)
-    itself = apart == 0 and all(s == t for s, t, n in zip(out.stride(), q.stride(), q.shape) if n > 1)
-    if out.numel() and (not itself and _meet(q.shape, q.stride(), out.stride(), apart)
-                        or any(p.numel() and at[0] < ends(p)[1] and ends(p)[0] < at[1] for p in (k_pages, v_pages))):
+    at = out.data_ptr()
+    apart, end = (at - q.data_ptr()) // e, at + e * _reach(shape, to)
+    itself = apart == 0 and (to == tq or all(s == t for s, t, n in zip(to, tq, shape) if n > 1))
+    meets = not itself and _meet(shape, tq, to, apart)
+    for p in (k_pages, v_pages):
+        first = p.data_ptr()
+        meets = meets or (first < end and at < first + e * _reach(p.shape, p.stride()))
+    if meets:
         raise ValueError(f"{name}: out must be q itself or share no storage with q and the pages")
 
 
