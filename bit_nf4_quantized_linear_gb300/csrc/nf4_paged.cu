@@ -89,8 +89,8 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(PagedArgs 
 // ------------------------------------------------------- attention, any layout --
 
 // fp32 arithmetic throughout, for rows that no 16-byte copy can take: right for everything, at
-// an eighth of the others' rate (64 sequences of up to 4096 tokens, 8 heads of 127, bf16: 570 us,
-// 0.9 TB/s).  A warp takes 32 / HC tokens at a time: its lanes hold the
+// an eighth of the others' rate (64 sequences of 1 to 4096 tokens, 120,000 in all, 32 heads over 8
+// of 127, bf16: 570 us, 0.9 TB/s).  A warp takes 32 / HC tokens at a time: its lanes hold the
 // tokens' rows 32 columns apart, form the partial products with HC query heads, and reduce the
 // 32 sums of (token, head) so that lane i ends with sum i, in 31 shuffles.
 constexpr int kAnyWarps = 8;

@@ -2,18 +2,22 @@
 // (nf4_paged_attention): rows of whole 16-byte pieces.
 //
 // The arithmetic is fp32 on the ordinary cores, 4 D operations a query head and token against
-// 8 D bytes a key head and token: up to a group of some eight heads HBM bounds it, if the rows
-// come in time and few instructions move them about.  They stream through per-warp rings as in
+// 8 D bytes a key head and token: up to a group of some eight heads HBM would bound it, if the
+// rows come in time and few instructions move them about.  They stream through per-warp rings as in
 // the tensor-core kernel (paged_ring.cuh), 8 tokens a warp's tile.  Scores: a lane takes one
 // token and a quarter of its columns; every 16 bytes of a key meet 16 of each head's query
 // (a broadcast); the quarters are added so that a quarter's lanes end with its heads.  Sums: a
 // lane takes 16 bytes of columns of all tokens, the weights come back through shared memory.
 // Packed fp32 pairs halve the multiply-adds.
 //
-// Measured: 32 sequences of up to 16384 tokens, 32 heads over 8 of 128, 329 us, 6.7 TB/s; 64 of
-// up to 3000, 64 heads over 8 of 64, 112 us, 4.4 TB/s (there the arithmetic bounds it); 32 of up
-// to 4096, 32 over 8 of 200, 179 us, 4.6 TB/s; seven of up to 2000, 12 heads over 4 of 80, 16 us
-// (launches, cut and join).
+// Measured (device time with the join; bytes: keys and values once): 32 sequences of 1 to 16384
+// tokens (269,000 in all), 32 heads over 8 of 128, 329 us, 6.7 TB/s.  64 of 500 to 3000 (119,600),
+// 8 key heads of 64: 32 heads 84 us, 5.9 TB/s; 64 heads 112 us, 4.4 TB/s, where no unit is full
+// (issue slots 59%, shared memory's wavefronts 54%, HBM 56%): 16 warps an SM, each with one tile's
+// chain of shared-memory reads, multiply-adds and exponentials, and a 16-byte read of a query for
+// two packed multiply-adds.  32 of 1 to 4096 (64,600), 32 heads over 8 of 200, 178 us, 4.6 TB/s:
+// the same with four warps an SM (issue slots 26%, wavefronts 51%).  Seven of 1 to 2000, 12 heads
+// over 4 of 80, 16 us (launches, cut and join).
 #include <cuda_runtime.h>
 
 #include <cstdint>

@@ -17,11 +17,14 @@
 // range.
 //
 // Measured, bf16, 32 heads over 8 of 128 unless said (device time with the join; 6.70 TB/s is a
-// plain copy's rate): 64 sequences of up to 16384 tokens 274 to 279 us, 6.8 to 6.9 TB/s; one of
-// 131072 tokens 89 us, 6.0 TB/s; 200 of up to 1024 in fp16, 40 heads over 8, 82 us, 5.6 TB/s; 24 of
-// up to 3000, 32 unshared heads of 64, 66 us, 6.0 TB/s; one token sequence of 37, 9 us.  Of a
-// call some 9 us are fixed: launch and cut 3.5, a tile's chain of loads and products 2, the join
-// 3.5.  In a long run HBM's order counts: fewer bytes in flight (two ring stages instead of
+// plain copy's rate; bytes: keys and values once): 64 sequences of 1 to 16384 tokens (480,000 in
+// all) 286 us, 6.9 TB/s; one of 131072 tokens 89 us, 6.0 TB/s; 200 of 64 to 1024 (111,000) in
+// fp16, 40 heads over 8, 84 us, 5.4 TB/s; 24 of 500 to 3000 (48,000), 32 unshared heads of 64, 66
+// us, 5.9 TB/s; one sequence of 37 tokens, 9 us.  Other widths, 32 of 1 to 8192 (146,300): 136
+// columns 145 us, 4.4 TB/s, 192 153 us, 5.9, 256 187 us, 6.4.  Groups, 64 of 1 to 8192 (266,600;
+// 163 us of bytes): 4 heads 168 us, 8 177, 16 206; from there on the rows are read once for each
+// 16: 20 heads 280 us, 32 290, 40 408.  Of a call some 9 us are fixed: launch and cut 3.5, a
+// tile's chain of loads and products 2, the join 3.5.  In a long run HBM's order counts: fewer bytes in flight (two ring stages instead of
 // three: -4%) and longer pieces a CTA (its warps on neighbouring heads: -7%) beat more of them.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -392,10 +395,15 @@ cudaError_t launch_width(const PagedArgs& a, int sms, cudaStream_t s) {
 }  // namespace
 
 // Groups of 16 query heads from 9 on, so that the rows are read half as often (not beside the
-// registers that 256 columns take).  Three CTAs a SM where a tile's arithmetic takes longer than
-// its bytes (463,000 tokens over 8 heads of 80: 115 us against 123 with two, 121 against 146 in
-// pages that no tile fits), two where HBM is busy with fewer, whose order it minds (of 128: 274
-// us with two, 281 with three; with three stages a ring 285).
+// registers that 256 columns take: 64 heads over 8 of 256 run at the bytes' rate, 333 us for 326,
+// 128 over 8 at 499).  Three CTAs a SM where a tile's arithmetic takes longer than its bytes, two
+// where HBM is busy with fewer, whose order it minds.  64 sequences of 1 to 8192 tokens (266,600
+// in all), 32 heads over 8, us with two and with three, in pages of 16 and of 24 (which no tile
+// fits):
+//   columns   72        80        88        96        104       112       120       128
+//   of 16  125, 121  125, 120  138, 148  138, 138  161, 171  158, 160  180, 187  168, 172
+//   of 24  149, 124  148, 124  151, 149  149, 139  157, 168  160, 160  179, 186  172, 176
+// (The cut at 112 gives 104 columns, and 88 in pages of 16, 6 to 7% too much.)
 PagedShape paged_shape_mma(int G, int Hk, int D, bool together) {
   const int group = G > 8 && D <= 128 ? 16 : 8, ctas = D > 128 ? 1 : D > 112 && group == 8 ? 2 : 3;
   return paged_shape(G, Hk, group, kWarps, ctas, together);
